@@ -251,7 +251,7 @@ def _run_own(s):
     r = t * k
     if op == "route":
         gp.gemmpipe_route(t, k, e, s["ids"], s["offsets"], s["slots"], s["rows"])
-        gp.gemmpipe_dispatch(ty, t, k, c["width"], s["x"], c["width"], s["slots"], None, s["xs"], c["width"])
+        gp.gemmpipe_dispatch(ty, t, k, c["width"], s["x"], c["width"], s["rows"], None, s["xs"], c["width"])
         return {n: s[n] for n in ("offsets", "slots", "rows", "xs")}
     if op == "combine":
         gp.gemmpipe_combine(ty, t, k, c["width"], s["ys"], c["width"], s["rows"], s["weights"], s["y"], c["width"])
