@@ -242,6 +242,152 @@ GEMMPIPE_API gemmpipe_status_t gemm_f16f32_host(int64_t M, int64_t N, int64_t K,
 GEMMPIPE_API int64_t gemmpipe_host_panel_rows(int64_t M);
 
 /*
+ * ---------------------------------------------------------------- experts
+ *
+ * The expert layer around the GEMM: every token's row is multiplied by the
+ * weight matrices of a few experts that a router chose for it, and the
+ * results are summed with the router's weights.
+ *
+ *   gemmpipe_route         a row for every choice, sorted by expert
+ *   gemmpipe_dispatch      the tokens' rows to their choices' rows
+ *   gemm_grouped           each expert's rows times its matrix
+ *   gemmpipe_combine       the weighted sum back to the tokens
+ *   gemmpipe_combine_grad, gemm_grouped_dx, gemm_grouped_dw,
+ *   gemmpipe_combine without weights (of gemmpipe_dispatch)
+ *                          the gradients
+ *   gemmpipe_keep8, gemmpipe_restore8, gemm_grouped_dw8
+ *                          rows kept in 8 bits for the backward pass
+ *
+ * The pages have no counterpart of these operators; the products use their
+ * pipelined k-loop.
+ *
+ * Common to all of them:
+ *   - type is GEMMPIPE_F16 or GEMMPIPE_BF16, the 16-bit floating-point type
+ *     of the activations and weights; sums are held in fp32 and rounded once,
+ *     to nearest even, where the result is stored;
+ *   - T tokens with top_k choices each (1 <= top_k <= 64) make R = T * top_k
+ *     slots and rows; choice j of token t is slot t * top_k + j; R is at most
+ *     2^31 - 1; there are 1 <= E <= 1024 experts;
+ *   - a matrix with a pitch argument (ldx and the like, in elements, at least
+ *     the row length) is row-major with rows that far apart, anything else is
+ *     densely packed; any element alignment is taken (rows on 16-byte
+ *     boundaries are fastest: the products copy other operands to aligned
+ *     rows in the library workspace first);
+ *   - outputs must not overlap inputs or each other;
+ *   - calls are asynchronous on `stream`, on the current device; results
+ *     repeat bit for bit;
+ *   - a size, pitch or type outside its range, a null or misaligned pointer
+ *     that is needed, or one the CUDA runtime does not know as device or
+ *     managed memory           -> GEMMPIPE_ERR_INVALID_VALUE
+ *     (the other errors as for the GEMM calls);
+ *   - calls with an empty output launch nothing.
+ */
+#define GEMMPIPE_F16 0
+#define GEMMPIPE_BF16 1
+
+/*
+ * Sorts the choices by expert: a stable counting sort of experts[0 .. R).
+ *   offsets (E + 1): expert e has the rows [offsets[e], offsets[e + 1]);
+ *   rows (R):  the row of each slot;
+ *   slots (R): the slot of each row (its inverse).
+ * A choice outside [0, E) is dropped: it sorts behind all others, rows at or
+ * past offsets[E], and is marked by the complement in both tables (rows[s] =
+ * ~r, slots[r] = ~s), which the operators below treat as a row that no expert
+ * has.  Uses the library workspace above 2048 slots.  T == 0 sets offsets to
+ * zero.
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_route(int64_t T, int64_t top_k, int64_t E, const int32_t *experts,
+                                              int32_t *offsets, int32_t *slots, int32_t *rows,
+                                              gemmpipe_stream_t stream);
+
+/*
+ * Xs[rows[t * top_k + j]] = weight * X[t] for every choice (weight =
+ * weights[t * top_k + j], fp32, or 1 where weights is NULL); a dropped
+ * choice's row is set to zero.  X is T x C, Xs is R x C.  `rows` is a table
+ * made by gemmpipe_route (here and below an entry for a row outside [0, R)
+ * is passed over).  With the gradient of combine's
+ * output in the place of X this is the gradient to combine's rows.
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_dispatch(int type, int64_t T, int64_t top_k, int64_t C, const void *X,
+                                                 int64_t ldx, const int32_t *rows, const float *weights, void *Xs,
+                                                 int64_t ldxs, gemmpipe_stream_t stream);
+
+/*
+ * Y[t] = sum over the token's kept choices, in order, of weight *
+ * Ys[rows[t * top_k + j]]; zero where none is kept.  Rows of dropped choices
+ * are not read.  Ys is R x C, Y is T x C.  With weights NULL (1) and the
+ * gradient of dispatch's output in the place of Ys this is the gradient of
+ * an unweighted dispatch.
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_combine(int type, int64_t T, int64_t top_k, int64_t C, const void *Ys,
+                                                int64_t ldys, const int32_t *rows, const float *weights, void *Y,
+                                                int64_t ldy, gemmpipe_stream_t stream);
+
+/*
+ * Gradient of gemmpipe_combine, in one pass over dY and Ys:
+ *   dYs[rows[s]] = weight[s] * dY[t]         (R x C; dropped choices: zero)
+ *   dweights[s]  = sum over c of dY[t][c] * Ys[rows[s]][c]
+ *                                            (R, fp32; dropped choices: zero)
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_combine_grad(int type, int64_t T, int64_t top_k, int64_t C, const void *dY,
+                                                     int64_t lddy, const void *Ys, int64_t ldys,
+                                                     const int32_t *rows, const float *weights, void *dYs,
+                                                     int64_t lddys, float *dweights, gemmpipe_stream_t stream);
+
+/*
+ * Y[r] = X[r] . W[e] for r in [offsets[e], offsets[e + 1]): X is R x K, W is
+ * E x K x N (dense), Y is R x N.  offsets (E + 1, int32, non-decreasing) is
+ * read on the device, so no copy to the host orders the routing before the
+ * product; bounds outside [0, R] or out of order are clamped.  Rows that no
+ * expert has are set to zero and not read into any other row's result (they
+ * may hold NaN).  K == 0 sets Y to zero.
+ *
+ * Tiles hold 32, 64, 128 or (on CTA pairs) 256 rows of one expert, chosen by
+ * the mean R / E.
+ */
+GEMMPIPE_API gemmpipe_status_t gemm_grouped(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *X,
+                                            int64_t ldx, const int32_t *offsets, const void *W, void *Y, int64_t ldy,
+                                            gemmpipe_stream_t stream);
+
+/* Its gradient to the rows: dX[r] = dY[r] . W[e]^T (dY is R x N, dX is R x K;
+ * offsets, W and rows without an expert as above; N == 0 sets dX to zero). */
+GEMMPIPE_API gemmpipe_status_t gemm_grouped_dx(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *dY,
+                                               int64_t lddy, const int32_t *offsets, const void *W, void *dX,
+                                               int64_t lddx, gemmpipe_stream_t stream);
+
+/* Its gradient to the weights: dW[e] = sum over the expert's rows of
+ * X[r]^T . dY[r] (E x K x N, dense, overwritten; zero for an expert without
+ * rows).  Rows that no expert has are not read into any result. */
+GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *X,
+                                               int64_t ldx, const void *dY, int64_t lddy, const int32_t *offsets,
+                                               void *dW, gemmpipe_stream_t stream);
+
+/*
+ * Rows kept in 8 bits: 32 neighbouring values of a row (the last group of a
+ * row may have fewer) share a power of two.  With m the exponent of the
+ * group's largest magnitude, e = max(m - 6, least), least = -24 for F16 and
+ * -127 for BF16 (an all-zero group has e = least):
+ *   Q = x / 2^e rounded to nearest even and clamped to [-127, 127]
+ *                                                     (R x C int8, dense)
+ *   S = e + 127                        (R x ceil(C / 32) bytes, dense)
+ * so a value is off by at most half a step, or one step at a group's largest
+ * value.  A group that holds an infinity or a NaN has S = 255 and Q = 0 and
+ * comes back as NaN.  8.25 bits a value.
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_keep8(int type, int64_t R, int64_t C, const void *X, int64_t ldx, int8_t *Q,
+                                              uint8_t *S, gemmpipe_stream_t stream);
+
+/* X = Q * 2^(S - 127) (NaN where S = 255), exact for what gemmpipe_keep8 wrote. */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_restore8(int type, int64_t R, int64_t C, const int8_t *Q, const uint8_t *S,
+                                                 void *X, int64_t ldx, gemmpipe_stream_t stream);
+
+/* gemm_grouped_dw with X in 8 bits (Q, S of gemmpipe_keep8, R x K): the same
+ * result as gemm_grouped_dw of the restored rows. */
+GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, int64_t K, int64_t E,
+                                                const int8_t *Q, const uint8_t *S, const void *dY, int64_t lddy,
+                                                const int32_t *offsets, void *dW, gemmpipe_stream_t stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the current device's error
  * word.  Returns GEMMPIPE_ERR_TIMEOUT if a kernel of this library gave up on
  * a pipeline wait (every wait is bounded; the kernel then stops issuing

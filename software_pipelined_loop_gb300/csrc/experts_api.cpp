@@ -1,0 +1,520 @@
+// experts_api.cpp -- the expert-layer entry points of include/gemmpipe.h:
+// argument checks, choice of the kernel variant, tensor maps and workspaces.
+#include "gemmpipe.h"
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+#include <initializer_list>
+#include <utility>
+
+#include "api_internal.h"
+#include "experts.h"
+#include "variants.h"
+
+namespace {
+
+using gp::ApiDevice;
+using gp::GroupedParams;
+using gp::GroupedVariant;
+
+constexpr int64_t kMaxDim = 2147483647;
+constexpr int64_t kMaxElems = int64_t(1) << 56;
+constexpr int kMaxTopK = 64;
+
+bool misaligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+
+bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
+
+// A matrix of `rows` rows of `width` elements, `ld` apart.
+bool bad_matrix(int64_t rows, int64_t width, int64_t ld)
+{
+    return bad_dim(rows) || bad_dim(width) || ld < width || ld > kMaxDim || (ld > 0 && rows > kMaxElems / ld);
+}
+
+bool bad_type(int type) { return type != GEMMPIPE_F16 && type != GEMMPIPE_BF16; }
+
+// Null or misaligned where something is to be read or written.
+bool bad_pointer(const void *p, int bytes) { return !p || misaligned(p, bytes); }
+
+// ----------------------------------------------------------- routing, rows
+
+struct Tokens {
+    int64_t T, k, R;
+};
+
+bool bad_tokens(int64_t T, int64_t top_k, Tokens *t)
+{
+    if (bad_dim(T) || top_k < 1 || top_k > kMaxTopK || T > kMaxDim / top_k) return true;
+    *t = Tokens{T, top_k, T * top_k};
+    return false;
+}
+
+gemmpipe_status_t check_all(std::initializer_list<std::pair<const void *, int>> ps)
+{
+    for (const auto &p : ps) {
+        if (!p.first) continue;  // optional
+        const gemmpipe_status_t st = gp::api_check_pointer(p.first, p.second);
+        if (st != GEMMPIPE_OK) return st;
+    }
+    return GEMMPIPE_OK;
+}
+
+// --------------------------------------------------------- grouped products
+
+struct Rows {         // a 16-bit row operand
+    const uint16_t *p;
+    int64_t width, ld;
+};
+
+bool tma_ok(const void *p, int64_t ld) { return !misaligned(p, 16) && ld % 8 == 0; }
+int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// Copy of `rows` rows of an operand that TMA cannot describe, in the
+// workspace at `to` with the pitch rounded up to 16 bytes.
+gemmpipe_status_t pad_rows(Rows *r, int64_t rows, uint16_t *to, const ApiDevice &d, cudaStream_t s)
+{
+    const Rows from = *r;
+    r->p = to;
+    r->ld = round8(from.width);
+    return gp::api_launch(false, s, 1, [&] {
+        if (from.ld == from.width)
+            return gp::launch_pad_f16(from.p, rows, from.width, to, r->ld, from.p, 0, 0, to, 8, d.sms, s);
+        return gp::launch_repitch(from.p, rows, from.width, from.ld, to, r->ld, d.sms, s);
+    });
+}
+
+// 64 elements x box_rows rows of a row operand.
+bool encode_rows(CUtensorMap *m, bool bf16, const Rows &r, int64_t rows, uint32_t box_rows)
+{
+    const uint64_t dims[2] = {static_cast<uint64_t>(r.width), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(r.ld) * 2};
+    const uint32_t box[2] = {64, box_rows};
+    return gp::api_encode_16bit(m, bf16, 2, r.p, dims, strides, box);
+}
+
+// The same as 64-element groups, `groups` of them in one copy (width a
+// multiple of 64).
+bool encode_row_groups(CUtensorMap *m, bool bf16, const Rows &r, int64_t rows, uint32_t groups)
+{
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(r.width / 64)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(r.ld) * 2, 128};
+    const uint32_t box[3] = {64, 64, groups};
+    return gp::api_encode_16bit(m, bf16, 3, r.p, dims, strides, box);
+}
+
+// Weights experts x rows x width: boxes of 64 elements x box_rows rows of
+// one expert, or (grouped) 2 x 64 elements x 64 rows in one copy.
+bool encode_weights(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t experts, int64_t rows, int64_t width,
+                    int64_t ld, uint32_t box_rows)
+{
+    const uint64_t dims[3] = {static_cast<uint64_t>(width), static_cast<uint64_t>(rows),
+                              static_cast<uint64_t>(experts)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(rows * ld) * 2};
+    const uint32_t box[3] = {64, box_rows, 1};
+    return gp::api_encode_16bit(m, bf16, 3, w, dims, strides, box);
+}
+
+bool encode_weight_groups(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t experts, int64_t rows, int64_t width,
+                          int64_t ld)
+{
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(width / 64),
+                              static_cast<uint64_t>(experts)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(ld) * 2, 128, static_cast<uint64_t>(rows * ld) * 2};
+    const uint32_t box[4] = {64, 64, 2, 1};
+    return gp::api_encode_16bit(m, bf16, 4, w, dims, strides, box);
+}
+
+// Rows per tile, by the mean number of rows of an expert.
+int rows_per_tile(int64_t R, int64_t E)
+{
+    const int64_t mean = (R + E - 1) / E;
+    return mean <= 16 ? 32 : (mean <= 32 ? 64 : (mean <= 96 ? 128 : 256));
+}
+
+struct Product {
+    int mode;
+    int type;
+    int64_t R, N, K, E;  // weights: K x N per expert
+    Rows rows;           // X (K wide) or dY (N wide); weight gradient: X
+    Rows grad;           // weight gradient: dY
+    const uint16_t *W;
+    const int32_t *offsets;
+    uint16_t *out;
+    int64_t ldo;
+    // Weight gradient from 8-bit rows: restored into the workspace first.
+    const int8_t *Q = nullptr;
+    const uint8_t *S = nullptr;
+};
+
+gemmpipe_status_t zero_rows(uint16_t *out, int64_t rows, int64_t width, int64_t ld, cudaStream_t s)
+{
+    const cudaError_t e = cudaMemset2DAsync(out, static_cast<size_t>(ld) * 2, 0, static_cast<size_t>(width) * 2,
+                                            static_cast<size_t>(rows), s);
+    if (e == cudaSuccess) return GEMMPIPE_OK;
+    cudaGetLastError();
+    return GEMMPIPE_ERR_LAUNCH;
+}
+
+gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
+{
+    const bool weights = q.mode == gp::kWeights, bf16 = q.type == GEMMPIPE_BF16;
+    const int64_t features = q.mode == gp::kRowsT ? q.K : q.N;
+    // An empty sum leaves zeros.
+    if (weights && q.R == 0) return zero_rows(q.out, q.E * q.K, q.N, q.ldo, s);
+    if (!weights && (q.mode == gp::kRows ? q.K : q.N) == 0) return zero_rows(q.out, q.R, features, q.ldo, s);
+
+    const int bn = weights ? 256 : rows_per_tile(q.R, q.E);
+    const GroupedVariant *v = gp::grouped_variant(q.mode, bn);
+    if (!v) return GEMMPIPE_ERR_INTERNAL;
+    if (v->smem_bytes > d.smem_optin) return GEMMPIPE_ERR_UNSUPPORTED_DEVICE;
+    const int64_t tile_f = v->pair ? 256 : 128;
+    const int64_t f_tiles = (features + tile_f - 1) / tile_f;
+    // Tiles of all experts, at most (the bounds are on the device).
+    const int64_t row_tiles = weights ? q.E * ((q.K + bn - 1) / bn) : q.R / bn + (q.R < q.E ? q.R : q.E);
+    if (row_tiles > kMaxDim / f_tiles) return GEMMPIPE_ERR_INVALID_VALUE;
+
+    // Operands that TMA cannot describe are copied to aligned rows.
+    const bool pad_x = q.Q == nullptr && !tma_ok(q.rows.p, q.rows.ld);
+    const bool pad_g = weights && !tma_ok(q.grad.p, q.grad.ld);
+    const bool pad_w = !weights && !tma_ok(q.W, q.N);
+    const int64_t wld = pad_w ? round8(q.N) : q.N;
+    const int64_t need_x = pad_x || q.Q ? align256(2 * q.R * round8(q.rows.width)) : 0;
+    const int64_t need_g = pad_g ? align256(2 * q.R * round8(q.grad.width)) : 0;
+    const int64_t need_w = pad_w ? align256(2 * q.E * q.K * wld) : 0;
+    gemmpipe_status_t st = GEMMPIPE_OK;
+    const uint16_t *W = q.W;
+    if (need_x + need_g + need_w > 0) {
+        void *ws = nullptr;
+        if ((st = gp::api_workspace(d.dev, s, need_x + need_g + need_w, &ws)) != GEMMPIPE_OK) return st;
+        uint16_t *to = static_cast<uint16_t *>(ws);
+        if (q.Q) {
+            q.rows.p = to;
+            q.rows.ld = round8(q.rows.width);
+            st = gp::api_launch(false, s, 1, [&] {
+                return gp::launch_restore8(bf16, q.R, q.K, q.Q, q.S, to, q.rows.ld, d.sms, s);
+            });
+            if (st != GEMMPIPE_OK) return st;
+        } else if (pad_x && (st = pad_rows(&q.rows, q.R, to, d, s)) != GEMMPIPE_OK) {
+            return st;
+        }
+        to += need_x / 2;
+        if (pad_g && (st = pad_rows(&q.grad, q.R, to, d, s)) != GEMMPIPE_OK) return st;
+        to += need_g / 2;
+        if (pad_w) {
+            Rows w{q.W, q.N, q.N};
+            if ((st = pad_rows(&w, q.E * q.K, to, d, s)) != GEMMPIPE_OK) return st;
+            W = to;
+        }
+    }
+
+    GroupedParams p;
+    std::memset(&p, 0, sizeof(p));
+    CUtensorMap ta, tb;
+    std::memset(&ta, 0, sizeof(ta));
+    std::memset(&tb, 0, sizeof(tb));
+    bool ok = true;
+    if (q.mode == gp::kRows) {
+        p.a_groups = q.N % 64 == 0;
+        ok = (p.a_groups ? encode_weight_groups(&ta, bf16, W, q.E, q.K, q.N, wld)
+                         : encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 64)) &&
+             encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn);
+        p.depth = q.K;
+    } else if (q.mode == gp::kRowsT) {
+        ok = encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 128) && encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn);
+        p.depth = q.N;
+    } else {
+        p.a_groups = q.grad.width % 64 == 0;
+        p.b_groups = q.rows.width % 64 == 0;
+        ok = (p.a_groups ? encode_row_groups(&ta, bf16, q.grad, q.R, 2) : encode_rows(&ta, bf16, q.grad, q.R, 64)) &&
+             (p.b_groups ? encode_row_groups(&tb, bf16, q.rows, q.R, v->cta_bn / 64)
+                         : encode_rows(&tb, bf16, q.rows, q.R, 64));
+        p.out_rows = q.K;
+    }
+    if (!ok) return GEMMPIPE_ERR_INTERNAL;
+    p.offsets = q.offsets;
+    p.experts = static_cast<int>(q.E);
+    p.rows = q.R;
+    p.features = features;
+    p.out = q.out;
+    p.ldo = q.ldo;
+    p.bf16 = bf16 ? 1 : 0;
+    p.stall_kb = -1;
+    p.timeout_ns = 2000000000ull + static_cast<uint64_t>((weights ? q.R : p.depth) / 64 + 1) * 10000ull;
+    if (gp::status_word(&p.status) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMMPIPE_ERR_LAUNCH;
+    }
+    const int64_t units = v->max_units(), tiles = row_tiles * f_tiles;
+    if (units < 1) return GEMMPIPE_ERR_LAUNCH;
+    const int grid = static_cast<int>((v->pair ? 2 : 1) * (tiles < units ? tiles : units));
+    return gp::api_launch(true, s, 1, [&] { return v->launch(ta, tb, p, grid, s); });
+}
+
+// Sizes common to the grouped products.
+bool bad_product(int type, int64_t R, int64_t N, int64_t K, int64_t E)
+{
+    return bad_type(type) || bad_dim(R) || bad_dim(N) || bad_dim(K) || E < 1 || E > gp::kMaxExperts ||
+           (N > 0 && K > kMaxElems / (E * (N + 8)));
+}
+
+cudaStream_t stream_of(gemmpipe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Nothing thrown (allocation of the library's own tables) leaves an entry point.
+template <class F>
+gemmpipe_status_t guarded(F f)
+{
+    try {
+        return f();
+    } catch (...) {
+        return GEMMPIPE_ERR_INTERNAL;
+    }
+}
+
+gemmpipe_status_t rows_product(int mode, int type, int64_t R, int64_t N, int64_t K, int64_t E, const uint16_t *in,
+                               int64_t ldi, const int32_t *offsets, const uint16_t *W, uint16_t *out, int64_t ldo,
+                               gemmpipe_stream_t stream)
+{
+    const int64_t wi = mode == gp::kRows ? K : N, wo = mode == gp::kRows ? N : K;
+    if (bad_product(type, R, N, K, E) || bad_matrix(R, wi, ldi) || bad_matrix(R, wo, ldo))
+        return GEMMPIPE_ERR_INVALID_VALUE;
+    if (R == 0 || wo == 0) return GEMMPIPE_OK;
+    if (bad_pointer(out, 2) || bad_pointer(offsets, 4) || (wi > 0 && (bad_pointer(in, 2) || bad_pointer(W, 2))))
+        return GEMMPIPE_ERR_INVALID_VALUE;
+    ApiDevice d;
+    gemmpipe_status_t st = gp::api_device(&d);
+    if (st != GEMMPIPE_OK) return st;
+    if ((st = check_all({{out, 2}, {offsets, 4}})) != GEMMPIPE_OK) return st;
+    if (wi > 0 && (st = check_all({{in, 2}, {W, 2}})) != GEMMPIPE_OK) return st;
+    Product q{};
+    q.mode = mode;
+    q.type = type;
+    q.R = R;
+    q.N = N;
+    q.K = K;
+    q.E = E;
+    q.rows = Rows{in, wi, ldi};
+    q.W = W;
+    q.offsets = offsets;
+    q.out = out;
+    q.ldo = ldo;
+    return run_product(q, d, stream_of(stream));
+}
+
+gemmpipe_status_t weights_product(int type, int64_t R, int64_t N, int64_t K, int64_t E, const uint16_t *X,
+                                  int64_t ldx, const int8_t *Q, const uint8_t *S, bool kept, const uint16_t *dY,
+                                  int64_t lddy, const int32_t *offsets, uint16_t *dW, gemmpipe_stream_t stream)
+{
+    if (bad_product(type, R, N, K, E) || bad_matrix(R, K, ldx) || bad_matrix(R, N, lddy))
+        return GEMMPIPE_ERR_INVALID_VALUE;
+    if (N == 0 || K == 0) return GEMMPIPE_OK;
+    if (bad_pointer(dW, 2) || bad_pointer(offsets, 4)) return GEMMPIPE_ERR_INVALID_VALUE;
+    if (R > 0 && (bad_pointer(dY, 2) || (kept ? !Q || !S : bad_pointer(X, 2)))) return GEMMPIPE_ERR_INVALID_VALUE;
+    ApiDevice d;
+    gemmpipe_status_t st = gp::api_device(&d);
+    if (st != GEMMPIPE_OK) return st;
+    if ((st = check_all({{dW, 2}, {offsets, 4}})) != GEMMPIPE_OK) return st;
+    if (R > 0 && (st = kept ? check_all({{dY, 2}, {Q, 1}, {S, 1}}) : check_all({{dY, 2}, {X, 2}})) != GEMMPIPE_OK)
+        return st;
+    Product q{};
+    q.mode = gp::kWeights;
+    q.type = type;
+    q.R = R;
+    q.N = N;
+    q.K = K;
+    q.E = E;
+    q.rows = Rows{X, K, ldx};
+    q.grad = Rows{dY, N, lddy};
+    q.offsets = offsets;
+    q.out = dW;
+    q.ldo = N;
+    q.Q = kept ? Q : nullptr;
+    q.S = S;
+    return run_product(q, d, stream_of(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+gemmpipe_status_t gemmpipe_route(int64_t T, int64_t top_k, int64_t E, const int32_t *experts, int32_t *offsets,
+                                 int32_t *slots, int32_t *rows, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        Tokens t;
+        if (bad_tokens(T, top_k, &t) || E < 1 || E > gp::kMaxExperts || bad_pointer(offsets, 4))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (t.R > 0 && (bad_pointer(experts, 4) || bad_pointer(slots, 4) || bad_pointer(rows, 4)))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{offsets, 4}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        if (t.R == 0) return zero_rows(reinterpret_cast<uint16_t *>(offsets), 1, 2 * (E + 1), 2 * (E + 1), s);
+        if ((st = check_all({{experts, 4}, {slots, 4}, {rows, 4}})) != GEMMPIPE_OK) return st;
+        void *ws = nullptr;
+        const int64_t bytes = gp::route_scratch_bytes(t.R, static_cast<int>(E));
+        if (bytes > 0 && (st = gp::api_workspace(d.dev, s, bytes, &ws)) != GEMMPIPE_OK) return st;
+        return gp::api_launch(false, s, gp::route_kernels(t.R), [&] {
+            return gp::launch_route(t.R, static_cast<int>(E), experts, offsets, slots, rows,
+                                    static_cast<int32_t *>(ws), s);
+        });
+    });
+}
+
+gemmpipe_status_t gemmpipe_dispatch(int type, int64_t T, int64_t top_k, int64_t C, const void *X, int64_t ldx,
+                                    const int32_t *rows, const float *weights, void *Xs, int64_t ldxs,
+                                    gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        Tokens t;
+        if (bad_type(type) || bad_tokens(T, top_k, &t) || bad_matrix(T, C, ldx) || bad_matrix(t.R, C, ldxs))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (T == 0 || C == 0) return GEMMPIPE_OK;
+        if (bad_pointer(X, 2) || bad_pointer(Xs, 2) || bad_pointer(rows, 4) || misaligned(weights, 4))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{X, 2}, {Xs, 2}, {rows, 4}, {weights, 4}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_dispatch(type == GEMMPIPE_BF16, T, static_cast<int>(top_k), C,
+                                       static_cast<const uint16_t *>(X), ldx, rows, weights,
+                                       static_cast<uint16_t *>(Xs), ldxs, s);
+        });
+    });
+}
+
+gemmpipe_status_t gemmpipe_combine(int type, int64_t T, int64_t top_k, int64_t C, const void *Ys, int64_t ldys,
+                                   const int32_t *rows, const float *weights, void *Y, int64_t ldy,
+                                   gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        Tokens t;
+        if (bad_type(type) || bad_tokens(T, top_k, &t) || bad_matrix(t.R, C, ldys) || bad_matrix(T, C, ldy))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (T == 0 || C == 0) return GEMMPIPE_OK;
+        if (bad_pointer(Ys, 2) || bad_pointer(Y, 2) || bad_pointer(rows, 4) || misaligned(weights, 4))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{Ys, 2}, {Y, 2}, {rows, 4}, {weights, 4}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_combine(type == GEMMPIPE_BF16, T, static_cast<int>(top_k), C,
+                                      static_cast<const uint16_t *>(Ys), ldys, rows, weights,
+                                      static_cast<uint16_t *>(Y), ldy, s);
+        });
+    });
+}
+
+gemmpipe_status_t gemmpipe_combine_grad(int type, int64_t T, int64_t top_k, int64_t C, const void *dY, int64_t lddy,
+                                        const void *Ys, int64_t ldys, const int32_t *rows, const float *weights,
+                                        void *dYs, int64_t lddys, float *dweights, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        Tokens t;
+        if (bad_type(type) || bad_tokens(T, top_k, &t) || bad_matrix(T, C, lddy) || bad_matrix(t.R, C, ldys) ||
+            bad_matrix(t.R, C, lddys))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (T == 0) return GEMMPIPE_OK;
+        if (bad_pointer(rows, 4) || misaligned(weights, 4) || bad_pointer(dweights, 4))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (C > 0 && (bad_pointer(dY, 2) || bad_pointer(Ys, 2) || bad_pointer(dYs, 2)))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{rows, 4}, {weights, 4}, {dweights, 4}})) != GEMMPIPE_OK) return st;
+        if (C > 0 && (st = check_all({{dY, 2}, {Ys, 2}, {dYs, 2}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_combine_grad(type == GEMMPIPE_BF16, T, static_cast<int>(top_k), C,
+                                           static_cast<const uint16_t *>(dY), lddy, static_cast<const uint16_t *>(Ys),
+                                           ldys, rows, weights, static_cast<uint16_t *>(dYs), lddys, dweights, s);
+        });
+    });
+}
+
+gemmpipe_status_t gemm_grouped(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *X, int64_t ldx,
+                               const int32_t *offsets, const void *W, void *Y, int64_t ldy, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        return rows_product(gp::kRows, type, R, N, K, E, static_cast<const uint16_t *>(X), ldx, offsets,
+                            static_cast<const uint16_t *>(W), static_cast<uint16_t *>(Y), ldy, stream);
+    });
+}
+
+gemmpipe_status_t gemm_grouped_dx(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *dY, int64_t lddy,
+                                  const int32_t *offsets, const void *W, void *dX, int64_t lddx,
+                                  gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        return rows_product(gp::kRowsT, type, R, N, K, E, static_cast<const uint16_t *>(dY), lddy, offsets,
+                            static_cast<const uint16_t *>(W), static_cast<uint16_t *>(dX), lddx, stream);
+    });
+}
+
+gemmpipe_status_t gemm_grouped_dw(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *X, int64_t ldx,
+                                  const void *dY, int64_t lddy, const int32_t *offsets, void *dW,
+                                  gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        return weights_product(type, R, N, K, E, static_cast<const uint16_t *>(X), ldx, nullptr, nullptr, false,
+                               static_cast<const uint16_t *>(dY), lddy, offsets, static_cast<uint16_t *>(dW), stream);
+    });
+}
+
+gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, int64_t K, int64_t E, const int8_t *Q,
+                                   const uint8_t *S, const void *dY, int64_t lddy, const int32_t *offsets, void *dW,
+                                   gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        return weights_product(type, R, N, K, E, nullptr, K, Q, S, true, static_cast<const uint16_t *>(dY), lddy,
+                               offsets, static_cast<uint16_t *>(dW), stream);
+    });
+}
+
+gemmpipe_status_t gemmpipe_keep8(int type, int64_t R, int64_t C, const void *X, int64_t ldx, int8_t *Q, uint8_t *S,
+                                 gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        if (bad_type(type) || bad_matrix(R, C, ldx)) return GEMMPIPE_ERR_INVALID_VALUE;
+        if (R == 0 || C == 0) return GEMMPIPE_OK;
+        if (bad_pointer(X, 2) || !Q || !S) return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{X, 2}, {Q, 1}, {S, 1}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_keep8(type == GEMMPIPE_BF16, R, C, static_cast<const uint16_t *>(X), ldx, Q, S, d.sms,
+                                    s);
+        });
+    });
+}
+
+gemmpipe_status_t gemmpipe_restore8(int type, int64_t R, int64_t C, const int8_t *Q, const uint8_t *S, void *X,
+                                    int64_t ldx, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        if (bad_type(type) || bad_matrix(R, C, ldx)) return GEMMPIPE_ERR_INVALID_VALUE;
+        if (R == 0 || C == 0) return GEMMPIPE_OK;
+        if (bad_pointer(X, 2) || !Q || !S) return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{X, 2}, {Q, 1}, {S, 1}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_restore8(type == GEMMPIPE_BF16, R, C, Q, S, static_cast<uint16_t *>(X), ldx, d.sms, s);
+        });
+    });
+}
+
+}  // extern "C"

@@ -14,6 +14,7 @@
 #include <utility>
 #include <vector>
 
+#include "api_internal.h"
 #include "variants.h"
 
 namespace {
@@ -775,6 +776,64 @@ gemmpipe_status_t s8_with_fixed_scratch(int64_t M, int64_t N, int64_t K, const i
     if (pl.v->launch(ta, tb, tc, p, pl.grid, s) != cudaSuccess) return GEMMPIPE_ERR_LAUNCH;
     g_launches.fetch_add(1);
     return GEMMPIPE_OK;
+}
+
+}  // namespace gp
+
+namespace {
+
+// ----------------------------------------------------- shared with other files
+
+}  // namespace
+
+namespace gp {
+
+gemmpipe_status_t api_device(ApiDevice *out)
+{
+    DeviceInfo d;
+    const gemmpipe_status_t st = device_info(&d, &out->dev);
+    if (st != GEMMPIPE_OK) return st;
+    out->sms = d.sms;
+    out->smem_optin = d.smem_optin;
+    return GEMMPIPE_OK;
+}
+
+gemmpipe_status_t api_check_pointer(const void *p, int align) { return check_pointer(p, align); }
+
+gemmpipe_status_t api_workspace(int dev, cudaStream_t s, int64_t bytes, void **out)
+{
+    return workspace(dev, s, bytes, out);
+}
+
+gemmpipe_status_t api_timed_launch(bool gemm, cudaStream_t s, int kernels, cudaError_t (*fn)(void *), void *ctx)
+{
+    TimedRegion tr(gemm, s);
+    const cudaError_t e = fn(ctx);
+    tr.end();
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GEMMPIPE_ERR_LAUNCH;
+    }
+    g_launches.fetch_add(kernels);
+    return GEMMPIPE_OK;
+}
+
+bool api_encode_16bit(CUtensorMap *m, bool bf16, int rank, const void *base, const uint64_t *dims,
+                      const uint64_t *strides, const uint32_t *box)
+{
+    EncodeFn f = encode_fn();
+    if (!f || rank < 2 || rank > 4) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], es[4];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+             const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace gp

@@ -1,0 +1,605 @@
+// grouped_kernel.cuh -- the pipelined tiled product with one weight matrix
+// per group of rows ("expert"), for sm_103a.
+//
+//   rows times matrix      Y[r]  = X[r] . W[e]            (kRows)
+//   gradient to the rows   dX[r] = dY[r] . W[e]^T         (kRowsT)
+//   gradient to a matrix   dW[e] = sum over r of X[r]^T . dY[r]   (kWeights)
+//
+// for r in [offsets[e], offsets[e + 1]), the bounds read on the device.
+//
+// Every product is computed transposed: the 128 (or, over a CTA pair, 256)
+// lanes of tensor memory are consecutive elements of the output's rows, and
+// the accumulator's columns are output rows.  The ragged dimension -- an
+// expert's rows -- is then the MMA's N, which may be any multiple of 16: a
+// tile of 32 rows costs a quarter of a 128-row one, so a few rows per expert
+// (token generation) stream the weights at the memory's rate.  A tile's last
+// rows may belong to the next expert; they only make columns that are not
+// stored.
+//
+// The ring, barriers, warp roles and bounded waits are those of
+// gemm_kernel.cuh: a producer warp filling stages of 64 products by TMA, an
+// MMA warp, and two epilogue warpgroups on double-buffered accumulators.
+//
+// Weight gradient: the summed dimension is the expert's rows, so the last
+// 64-row stage of an expert holds rows of the next one (or unused ones,
+// which may be NaN).  MMAs run only over the 16-row steps that hold a row of
+// the expert, and a warp clears the rest of the last step's rows in both
+// operands before the MMA reads them.
+#pragma once
+
+#include "gemm_kernel.cuh"
+#include "grouped_params.h"
+
+#include <cuda_bf16.h>
+
+namespace gp {
+
+template <int MODE_, int BN_, bool PAIR_>
+struct GroupedCfg {
+    static constexpr int MODE = MODE_;
+    static constexpr int BN = BN_;        // output rows per tile
+    static constexpr bool PAIR = PAIR_;   // cluster of two CTAs, 256 features per tile
+    static constexpr int CLUSTER = PAIR ? 2 : 1;
+    static constexpr int BM = 128;        // features per CTA
+    static constexpr int TILE_F = BM * CLUSTER;
+    static constexpr int BK = 64;
+    static constexpr bool A_MN = MODE != kRowsT;    // W[k][n] and dY[r][n]: features contiguous
+    static constexpr bool B_MN = MODE == kWeights;  // X[r][k] of the weight gradient
+    static constexpr int CTA_BN = BN / CLUSTER;     // columns of B each CTA holds
+    static constexpr int A_BYTES = BM * BK * 2;
+    static constexpr int B_BYTES = CTA_BN * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int ATOM_BYTES = BK * 128;     // 64 features (columns) x 64 products
+    static constexpr int RING_BYTES = 196608;
+    static constexpr int STAGES = RING_BYTES / STAGE_BYTES < 10 ? RING_BYTES / STAGE_BYTES : 10;
+    static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
+    static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+    static constexpr int EPI_COLS = BN / 2;         // columns per epilogue warp
+    static constexpr int EPI_BLOCK = EPI_COLS < 32 ? EPI_COLS : 32;
+
+    static constexpr int TABLE_OFF = STAGES * STAGE_BYTES;
+    static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2);
+    static constexpr int CTL_OFF = TABLE_OFF + TABLE_BYTES;
+    static constexpr int CTL_BYTES = 8 * (4 * STAGES + 5) + 32;
+    static constexpr int SMEM_BYTES = 1024 + CTL_OFF + CTL_BYTES;
+
+    static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "MMA columns");
+    static_assert(!PAIR || BN == 256, "pairs take 256 x 256 tiles");
+    static_assert(B_BYTES % 1024 == 0 && TABLE_BYTES % 8 == 0, "alignment");
+    static_assert(!B_MN || CTA_BN % 64 == 0, "64-column atoms");
+    static_assert(SMEM_BYTES <= 232448, "over the per-CTA shared-memory limit");
+};
+
+template <int STAGES>
+struct GroupedCtl {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t raw[STAGES];    // weight gradient: an expert's last stage has landed in this CTA
+    uint64_t peer[STAGES];   // ... and is cleared in the pair's other CTA (on the leader)
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Row bounds and tile numbers of the experts, made by every CTA at its
+// start: start[e] (e <= E) and first[e], the number of tiles before expert e.
+struct GroupTable {
+    int32_t *start;
+    int32_t *first;
+    int E;
+};
+
+// All threads of the CTA.  The bounds are clamped to [0, rows] and made
+// non-decreasing, so that nothing they hold can send an access outside.
+template <class Cfg>
+__device__ void make_table(const GroupedParams &p, GroupTable t)
+{
+    for (int i = threadIdx.x; i <= t.E; i += Cfg::THREADS) {
+        const int64_t v = p.offsets[i];
+        t.start[i] = static_cast<int32_t>(v < 0 ? 0 : (v > p.rows ? p.rows : v));
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int32_t f_tiles = static_cast<int32_t>((p.features + Cfg::TILE_F - 1) / Cfg::TILE_F);
+        const int32_t w_tiles = static_cast<int32_t>((p.out_rows + Cfg::BN - 1) / Cfg::BN);
+        int32_t top = 0, sum = 0;
+        for (int b = 0; b <= t.E; b += 32) {
+            const int i = b + lane;
+            int32_t v = i <= t.E ? t.start[i] : 0;
+            if (v < top) v = top;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d && u > v) v = u;
+            }
+            // This expert's end, the next entry's bound: tiles need it, so
+            // entry i's tiles are counted from v(i) - v(i - 1).
+            int32_t prev = __shfl_up_sync(0xffffffffu, v, 1);
+            if (lane == 0) prev = top;
+            int32_t n = 0;
+            if (i >= 1 && i <= t.E)
+                n = f_tiles * (Cfg::MODE == kWeights ? w_tiles : (v - prev + Cfg::BN - 1) / Cfg::BN);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += u;
+            }
+            if (i <= t.E) {
+                t.start[i] = v;
+                t.first[i] = sum + n;  // tiles of the experts before i
+            }
+            top = __shfl_sync(0xffffffffu, v, 31);
+            sum += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+    __syncthreads();
+}
+
+struct GroupedTile {
+    int e;           // expert
+    int32_t row0;    // its first row
+    int32_t count;   // its rows
+    int32_t f0;      // first feature of the tile
+    int32_t c0;      // first output row of the tile, within the expert
+    int32_t kbs;     // k-blocks
+    int32_t last;    // products in the last k-block (1 .. 64)
+};
+
+// Tiles of a unit (CTA or pair): round-robin, experts in order, features
+// fastest, so that tiles in flight share rows and a few experts' weights.
+template <class Cfg>
+struct GroupedIter {
+    GroupTable t;
+    int32_t pos, step;
+    int e;
+    int32_t f_tiles;
+
+    __device__ __forceinline__ GroupedIter(const GroupedParams &p, GroupTable tab)
+        : t(tab), pos(blockIdx.x / Cfg::CLUSTER), step(gridDim.x / Cfg::CLUSTER), e(0),
+          f_tiles(static_cast<int32_t>((p.features + Cfg::TILE_F - 1) / Cfg::TILE_F))
+    {
+    }
+
+    __device__ __forceinline__ bool next(const GroupedParams &p, GroupedTile &w)
+    {
+        if (pos >= t.first[t.E]) return false;
+        while (pos >= t.first[e + 1]) ++e;
+        const int32_t in = pos - t.first[e];
+        pos += step;
+        const int32_t c = in / f_tiles;
+        w.e = e;
+        w.row0 = t.start[e];
+        w.count = t.start[e + 1] - w.row0;
+        w.f0 = (in - c * f_tiles) * Cfg::TILE_F;
+        w.c0 = c * Cfg::BN;
+        const int64_t depth = Cfg::MODE == kWeights ? w.count : p.depth;
+        w.kbs = static_cast<int32_t>((depth + Cfg::BK - 1) / Cfg::BK);
+        w.last = static_cast<int32_t>(depth - static_cast<int64_t>(w.kbs - 1) * Cfg::BK);
+        return true;
+    }
+};
+
+// An expert's last stage holds rows that are not its own within an MMA's 16.
+template <class Cfg>
+__device__ __forceinline__ bool has_stray_rows(const GroupedTile &w, int32_t kb)
+{
+    return Cfg::MODE == kWeights && kb == w.kbs - 1 && (w.last & 15) != 0;
+}
+
+// --------------------------------------------------------------- producer
+
+template <class Cfg>
+__device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, const CUtensorMap *tB,
+                                 uint32_t sbase, GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w,
+                                 uint32_t rank)
+{
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t armed = 0, armed_par = 0, raw_armed = 0, raw_par = 0;
+    int64_t kb_count = 0;
+    bool ok = true;
+    const uint32_t full0 = smem_u32(&ctl->full[0]);
+    const uint32_t full0_leader = Cfg::PAIR ? mapa_shared(full0, 0) : full0;
+    const uint32_t raw0 = smem_u32(&ctl->raw[0]);
+    const uint32_t raw0_self = Cfg::PAIR ? mapa_shared(raw0, rank) : raw0;
+    GroupedIter<Cfg> it(p, tab);
+    GroupedTile t;
+    while (ok && it.next(p, t)) {
+        const int32_t f0 = t.f0 + static_cast<int32_t>(rank) * Cfg::BM;
+        const int32_t c0 = t.c0 + static_cast<int32_t>(rank) * Cfg::CTA_BN;
+        for (int32_t kb = 0; kb < t.kbs; ++kb, ++kb_count) {
+            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->empty[stage]), phase ^ 1u))) {
+                ok = false;
+                break;
+            }
+            if (!(blockIdx.x == 0 && kb_count == p.stall_kb)) {
+                const bool stray = has_stray_rows<Cfg>(t, kb);
+                if (elect_one_sync()) {
+                    const uint32_t so = 8u * static_cast<uint32_t>(stage);
+                    const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::A_BYTES;
+                    const int32_t k0 = kb * Cfg::BK;
+                    uint32_t bar;
+                    if (stray) {
+                        mbar_arrive_expect_tx(raw0 + so, Cfg::STAGE_BYTES);
+                        bar = raw0_self + so;
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * Cfg::STAGE_BYTES);
+                        bar = full0_leader + so;
+                    }
+                    auto load4 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z, int32_t v) {
+                        if constexpr (Cfg::PAIR)
+                            tma_load_4d_pair(dst, m, bar, x, y, z, v);
+                        else
+                            tma_load_4d(dst, m, bar, x, y, z, v);
+                    };
+                    auto load3 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
+                        if constexpr (Cfg::PAIR)
+                            tma_load_3d_pair(dst, m, bar, x, y, z);
+                        else
+                            tma_load_3d(dst, m, bar, x, y, z);
+                    };
+                    auto load2 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y) {
+                        if constexpr (Cfg::PAIR)
+                            tma_load_2d_pair(dst, m, bar, x, y);
+                        else
+                            tma_load_2d(dst, m, bar, x, y);
+                    };
+                    if constexpr (Cfg::MODE == kRows) {
+                        // W[e]: 64 products x 128 features, two 64-feature atoms.
+                        if (p.a_groups) {
+                            load4(sa, tA, 0, k0, f0 / 64, t.e);
+                        } else {
+                            load3(sa, tA, f0, k0, t.e);
+                            load3(sa + Cfg::ATOM_BYTES, tA, f0 + 64, k0, t.e);
+                        }
+                        load2(sb, tB, k0, t.row0 + c0);
+                    } else if constexpr (Cfg::MODE == kRowsT) {
+                        load3(sa, tA, k0, f0, t.e);
+                        load2(sb, tB, k0, t.row0 + c0);
+                    } else {
+                        if (p.a_groups) {
+                            load3(sa, tA, 0, t.row0 + k0, f0 / 64);
+                        } else {
+                            load2(sa, tA, f0, t.row0 + k0);
+                            load2(sa + Cfg::ATOM_BYTES, tA, f0 + 64, t.row0 + k0);
+                        }
+                        if (p.b_groups) {
+                            load3(sb, tB, 0, t.row0 + k0, c0 / 64);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < Cfg::CTA_BN / 64; ++j)
+                                load2(sb + j * Cfg::ATOM_BYTES, tB, c0 + 64 * j, t.row0 + k0);
+                        }
+                    }
+                }
+                __syncwarp();
+                const uint32_t bit = 1u << stage;
+                if (stray) {
+                    raw_par ^= raw_armed & bit;  // parity of this stage's latest use of raw
+                    raw_armed |= bit;
+                } else {
+                    armed |= bit;
+                    armed_par = phase ? (armed_par | bit) : (armed_par & ~bit);
+                }
+            }
+            if (++stage == Cfg::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (ok && Cfg::PAIR) {
+        // The last MMA commits arrive on both CTAs' empty barriers: none may
+        // be in flight when a CTA leaves.
+        for (int s = 0; s < Cfg::STAGES && ok; ++s) {
+            const uint32_t ph = s < stage ? phase ^ 1u : phase;
+            ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->empty[s]), ph ^ 1u));
+        }
+    }
+    if (!ok) {
+        // Let the copies that were started land before the CTA leaves.
+        if (rank == 0) {
+            for (int s = 0; s < Cfg::STAGES; ++s)
+                if (armed & (1u << s)) w.wait_drain(smem_u32(&ctl->full[s]), (armed_par >> s) & 1u, kDrainNs);
+        } else if (armed) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000ull) {
+            }
+        }
+        for (int s = 0; s < Cfg::STAGES; ++s)
+            if (raw_armed & (1u << s)) w.wait_drain(smem_u32(&ctl->raw[s]), (raw_par >> s) & 1u, kDrainNs);
+    }
+}
+
+// ---------------------------------------------------- stray rows (weights)
+
+// One warp per CTA: clears the rows past an expert's last one within the
+// 16-row step that holds it, in both operands' atoms (a row is 128 bytes of
+// each atom, whatever the swizzle within it), and completes full[s].
+template <class Cfg>
+__device__ void clear_stray_rows(const GroupedParams &p, uint32_t sbase, GroupedCtl<Cfg::STAGES> *ctl,
+                                 GroupTable tab, const Waiter &w, uint32_t rank, int lane)
+{
+    int64_t kb_count = 0;
+    uint32_t raw_phase = 0, peer_phase = 0;  // per stage
+    GroupedIter<Cfg> it(p, tab);
+    GroupedTile t;
+    while (it.next(p, t)) {
+        if (t.kbs > 0 && has_stray_rows<Cfg>(t, t.kbs - 1)) {
+            const int s = static_cast<int>((kb_count + t.kbs - 1) % Cfg::STAGES);
+            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->raw[s]), (raw_phase >> s) & 1u))) return;
+            raw_phase ^= 1u << s;
+            const int from = t.last, rows = 16 - (t.last & 15);
+            constexpr int ATOMS = Cfg::STAGE_BYTES / Cfg::ATOM_BYTES;
+            const uint32_t base = sbase + s * Cfg::STAGE_BYTES + from * 128;
+            for (int i = lane; i < ATOMS * rows * 8; i += 32) {
+                const int a = i / (rows * 8), j = i - a * (rows * 8);
+                st_shared_v4(base + a * Cfg::ATOM_BYTES + j * 16, 0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (Cfg::PAIR && rank != 0) {
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->peer[s]), 0));
+                __syncwarp();
+            } else {
+                if constexpr (Cfg::PAIR) {
+                    if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->peer[s]), (peer_phase >> s) & 1u))) return;
+                    fence_acq_rel_cluster();
+                    peer_phase ^= 1u << s;
+                    fence_proxy_async_smem();
+                }
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->full[s]));
+                __syncwarp();
+            }
+        }
+        kb_count += t.kbs;
+    }
+}
+
+// -------------------------------------------------------------------- MMA
+
+template <class Cfg>
+__device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
+                            GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w)
+{
+    const uint32_t idesc = umma_idesc_16bit_f32(Cfg::TILE_F, Cfg::BN, p.bf16 != 0, Cfg::A_MN, Cfg::B_MN);
+    const uint64_t dA0 = Cfg::A_MN ? umma_desc_sw128(sbase, Cfg::ATOM_BYTES, 1024) : umma_desc_sw128(sbase, 16, 1024);
+    const uint64_t dB0 = Cfg::B_MN ? umma_desc_sw128(sbase + Cfg::A_BYTES, Cfg::ATOM_BYTES, 1024)
+                                   : umma_desc_sw128(sbase + Cfg::A_BYTES, 16, 1024);
+    constexpr uint32_t A_STEP = (Cfg::A_MN ? 2048 : 32) >> 4, B_STEP = (Cfg::B_MN ? 2048 : 32) >> 4;
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t acc = 0, acc_phase = 0;
+    bool issued = false, ok = true;
+    GroupedIter<Cfg> it(p, tab);
+    GroupedTile t;
+    while (ok && it.next(p, t)) {
+        if (t.kbs == 0) continue;  // the empty sum: the epilogue writes zeros
+        if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->tempty[acc]), acc_phase ^ 1u))) {
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem_base + acc * Cfg::BN;
+        for (int32_t kb = 0; kb < t.kbs; ++kb) {
+            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->full[stage]), phase))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint64_t so = static_cast<uint64_t>((stage * Cfg::STAGE_BYTES) >> 4);
+            const int steps = kb == t.kbs - 1 ? (t.last + 15) / 16 : Cfg::BK / 16;
+            if (elect_one_sync()) {
+#pragma unroll
+                for (int kk = 0; kk < Cfg::BK / 16; ++kk) {
+                    if (kk < steps) {
+                        const uint32_t add = (kb > 0 || kk > 0) ? 1u : 0u;
+                        if constexpr (Cfg::PAIR)
+                            umma_f16_pair(d, dA0 + so + kk * A_STEP, dB0 + so + kk * B_STEP, idesc, add);
+                        else
+                            umma_f16(d, dA0 + so + kk * A_STEP, dB0 + so + kk * B_STEP, idesc, add);
+                    }
+                }
+                if constexpr (Cfg::PAIR)
+                    umma_commit_pair(smem_u32(&ctl->empty[stage]), 3);
+                else
+                    umma_commit(smem_u32(&ctl->empty[stage]));
+            }
+            __syncwarp();
+            issued = true;
+            if (++stage == Cfg::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) break;
+        if (elect_one_sync()) {
+            if constexpr (Cfg::PAIR)
+                umma_commit_pair(smem_u32(&ctl->tfull[acc]), 3);
+            else
+                umma_commit(smem_u32(&ctl->tfull[acc]));
+        }
+        __syncwarp();
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+    }
+    if (ok && Cfg::PAIR) {
+        // The accumulators' last releases, the peer's among them, have landed.
+        ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->tempty[acc]), acc_phase ^ 1u));
+        ok = ok && __all_sync(0xffffffffu,
+                              w.wait(smem_u32(&ctl->tempty[acc ^ 1u]), acc == 0 ? acc_phase ^ 1u : acc_phase));
+    }
+    if (!ok && issued) {
+        if (elect_one_sync()) {
+            if constexpr (Cfg::PAIR)
+                umma_commit_pair(smem_u32(&ctl->drain), 1);
+            else
+                umma_commit(smem_u32(&ctl->drain));
+        }
+        __syncwarp();
+        w.wait_drain(smem_u32(&ctl->drain), 0, kDrainNs);
+    }
+}
+
+// --------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ uint16_t round_16bit(float v, bool bf16)
+{
+    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// Accumulator lane l of warp quarter q is feature f0 + 32 q + l, column c the
+// output row c0 + c; the fp32 sum is rounded once, to the operands' type.
+template <class Cfg>
+__device__ void grouped_epilogue(const GroupedParams &p, uint32_t tmem_base, GroupedCtl<Cfg::STAGES> *ctl,
+                                 GroupTable tab, const Waiter &w, int warp, int lane, uint32_t rank)
+{
+    const int e = warp - Cfg::EPI_WARP0;
+    const int q = warp & 3, h = e >> 2;
+    const bool bf16 = p.bf16 != 0;
+    uint32_t acc = 0, acc_phase = 0;
+    const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
+    uint16_t *out = static_cast<uint16_t *>(p.out);
+    GroupedIter<Cfg> it(p, tab);
+    GroupedTile t;
+    while (it.next(p, t)) {
+        const int64_t f = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * 32 + lane;
+        const int64_t rows = Cfg::MODE == kWeights ? p.out_rows : t.count;  // output rows of the expert
+        const int64_t base = Cfg::MODE == kWeights ? p.out_rows * t.e : t.row0;
+        const int64_t c0 = static_cast<int64_t>(t.c0) + h * Cfg::EPI_COLS;
+        const bool empty = t.kbs == 0;
+        if (!empty) {
+            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->tfull[acc]), acc_phase))) return;
+            tc_fence_after_sync();
+        }
+        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * Cfg::BN + h * Cfg::EPI_COLS;
+#pragma unroll 1
+        for (int j = 0; j < Cfg::EPI_COLS; j += Cfg::EPI_BLOCK) {
+            if (c0 + j >= rows) break;
+            uint32_t r[Cfg::EPI_BLOCK];
+            if (empty) {
+#pragma unroll
+                for (int i = 0; i < Cfg::EPI_BLOCK; ++i) r[i] = 0;
+            } else {
+                if constexpr (Cfg::EPI_BLOCK == 32)
+                    tmem_ld_32x32b_x32(tbase + j, r);
+                else
+                    tmem_ld_32x32b_x16(tbase + j, r);
+                tmem_wait_ld();
+            }
+            uint16_t *o = out + (base + c0 + j) * p.ldo + f;
+            const int n = rows - (c0 + j) < Cfg::EPI_BLOCK ? static_cast<int>(rows - (c0 + j)) : Cfg::EPI_BLOCK;
+            if (f < p.features) {
+#pragma unroll
+                for (int i = 0; i < Cfg::EPI_BLOCK; ++i)
+                    if (i < n) o[i * p.ldo] = round_16bit(__uint_as_float(r[i]), bf16);
+            }
+            __syncwarp();
+        }
+        if (!empty) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (Cfg::PAIR)
+                    mbar_arrive_cluster(tempty0 + 8 * acc);
+                else
+                    mbar_arrive(tempty0 + 8 * acc);
+            }
+            acc ^= 1u;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+    if constexpr (Cfg::MODE != kWeights) {
+        // Rows of no expert are written as zeros.
+        const int64_t head = tab.start[0], tail = tab.start[tab.E];
+        const int64_t none = head + p.rows - tail;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * Cfg::EPI_WARPS + e; i < none;
+             i += static_cast<int64_t>(gridDim.x) * Cfg::EPI_WARPS) {
+            uint16_t *o = out + (i < head ? i : tail + (i - head)) * p.ldo;
+            for (int64_t x = lane; x < p.features; x += 32) o[x] = 0;
+        }
+    }
+}
+
+// ----------------------------------------------------------------- kernel
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const GroupedParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    auto *ctl = reinterpret_cast<GroupedCtl<Cfg::STAGES> *>(smem + Cfg::CTL_OFF);
+    GroupTable tab;
+    tab.start = reinterpret_cast<int32_t *>(smem + Cfg::TABLE_OFF);
+    tab.first = tab.start + kMaxExperts + 2;
+    tab.E = p.experts;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+            mbar_init(smem_u32(&ctl->raw[s]), 1);
+            mbar_init(smem_u32(&ctl->peer[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctl->tfull[b]), 1);
+            mbar_init(smem_u32(&ctl->tempty[b]), Cfg::CLUSTER * Cfg::EPI_WARPS);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        if constexpr (Cfg::PAIR) {
+            tmem_alloc_pair(smem_u32(&ctl->tmem_base), Cfg::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(&ctl->tmem_base), Cfg::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    make_table<Cfg>(p, tab);
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (Cfg::PAIR) cluster_sync();  // the leader's barriers exist before the peer signals them
+    tc_fence_after_sync();
+    const uint32_t tmem_base = ctl->tmem_base;
+    const Waiter w{&ctl->abort, p.status, p.timeout_ns};
+    const uint32_t rank = Cfg::PAIR ? cluster_ctarank() : 0u;
+    if (warp == 0) {
+        grouped_producer<Cfg>(p, &tmA, &tmB, sbase, ctl, tab, w, rank);
+    } else if (warp == 1) {
+        if (rank == 0) grouped_mma<Cfg>(p, sbase, tmem_base, ctl, tab, w);
+    } else if (warp == 2) {
+        if constexpr (Cfg::MODE == kWeights) clear_stray_rows<Cfg>(p, sbase, ctl, tab, w, rank, lane);
+    } else if (warp >= Cfg::EPI_WARP0) {
+        grouped_epilogue<Cfg>(p, tmem_base, ctl, tab, w, warp, lane, rank);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (Cfg::PAIR) cluster_sync();  // no peer still signals or reads this CTA
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if constexpr (Cfg::PAIR)
+            tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+}  // namespace gp

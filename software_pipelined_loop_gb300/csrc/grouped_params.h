@@ -1,0 +1,32 @@
+// grouped_params.h -- kernel arguments of the grouped products, shared by
+// host and device code.
+#pragma once
+
+#include <cstdint>
+
+namespace gp {
+
+constexpr int kMaxExperts = 1024;
+
+enum GroupedMode { kRows = 0, kRowsT = 1, kWeights = 2 };
+
+// The product of every expert e over its rows [offsets[e], offsets[e + 1]).
+// The kernel computes it transposed, D[f][c]: f runs over `features`, the
+// contiguous dimension of the output, c over rows of the output.
+struct GroupedParams {
+    const int32_t *offsets;  // experts + 1 row bounds, in device memory
+    int experts;
+    int64_t rows;            // rows of the row operands; the bounds are clamped to [0, rows]
+    int64_t features;        // length of an output row
+    int64_t out_rows;        // weight gradient: output rows per expert; else unused
+    int64_t depth;           // products summed per value (weight gradient: the expert's rows instead)
+    void *out;
+    int64_t ldo;             // output row pitch in elements
+    int bf16;
+    int a_groups, b_groups;  // 1: the operand's tensor map is in 64-column groups (one copy per k-block)
+    uint64_t timeout_ns;
+    int64_t stall_kb;        // test hook: CTA 0 leaves this k-block unfilled (-1: none)
+    int *status;
+};
+
+}  // namespace gp

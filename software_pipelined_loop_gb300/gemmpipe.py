@@ -20,6 +20,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "gemmpipe.h")
 STATUS = {0: "GEMMPIPE_OK", 1: "GEMMPIPE_ERR_INVALID_VALUE", 2: "GEMMPIPE_ERR_UNSUPPORTED_DEVICE",
           3: "GEMMPIPE_ERR_LAUNCH", 4: "GEMMPIPE_ERR_TIMEOUT", 5: "GEMMPIPE_ERR_INTERNAL",
           6: "GEMMPIPE_ERR_OUT_OF_MEMORY"}
+F16, BF16 = 0, 1  # GEMMPIPE_F16, GEMMPIPE_BF16: the type argument of the expert-layer calls
 NOALLOC_SCRATCH_BYTES = 16 << 20  # GEMMPIPE_NOALLOC_SCRATCH_BYTES
 OK, ERR_INVALID_VALUE, ERR_UNSUPPORTED_DEVICE, ERR_LAUNCH, ERR_TIMEOUT, ERR_INTERNAL, ERR_OUT_OF_MEMORY = range(7)
 
@@ -58,6 +59,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gemm_s8s8s32_noalloc": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp]),
         "gemm_s8s8s32_host": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp]),
         "gemm_f16f32_host": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+        "gemmpipe_route": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+        "gemmpipe_dispatch": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+        "gemmpipe_combine": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+        "gemmpipe_combine_grad": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp,
+                                         _vp]),
+        "gemm_grouped": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+        "gemm_grouped_dx": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+        "gemm_grouped_dw": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+        "gemm_grouped_dw8": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+        "gemmpipe_keep8": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+        "gemmpipe_restore8": (_int, [_int, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
         "gemmpipe_host_panel_rows": (_i64, [_i64]),
         "gemmpipe_test_trace": (_int, [_vp, _i64]),
         "gemmpipe_get_device_status": (_int, [_vp]),
@@ -144,6 +156,68 @@ def gemm_s8s8s32_host(M, N, K, A, B, C, stream=None) -> None:
 def gemm_f16f32_host(M, N, K, A, B, C, stream=None) -> None:
     """gemm_f16f32 with A, B and C in host memory (see gemm_s8s8s32_host)."""
     _check(load().gemm_f16f32_host(M, N, K, _ptr(A), _ptr(B), _ptr(C), _stream(stream)), "gemm_f16f32_host")
+
+
+def gemmpipe_route(T, top_k, E, experts, offsets, slots, rows, stream=None) -> None:
+    """Sorts T * top_k expert ids (int32) by expert: offsets (E + 1), and the
+    tables between slots (choices) and rows, each the other's inverse; ids
+    outside [0, E) get the last rows, marked by the complement."""
+    _check(load().gemmpipe_route(T, top_k, E, _ptr(experts), _ptr(offsets), _ptr(slots), _ptr(rows),
+                                 _stream(stream)), "gemmpipe_route")
+
+
+def gemmpipe_dispatch(type, T, top_k, C, X, ldx, rows, weights, Xs, ldxs, stream=None) -> None:
+    """Xs[rows[t, j]] = weights[t, j] * X[t] (weights None: 1)."""
+    _check(load().gemmpipe_dispatch(type, T, top_k, C, _ptr(X), ldx, _ptr(rows), _ptr(weights), _ptr(Xs), ldxs,
+                                    _stream(stream)), "gemmpipe_dispatch")
+
+
+def gemmpipe_combine(type, T, top_k, C, Ys, ldys, rows, weights, Y, ldy, stream=None) -> None:
+    """Y[t] = sum over j of weights[t, j] * Ys[rows[t, j]] (weights None: 1)."""
+    _check(load().gemmpipe_combine(type, T, top_k, C, _ptr(Ys), ldys, _ptr(rows), _ptr(weights), _ptr(Y), ldy,
+                                   _stream(stream)), "gemmpipe_combine")
+
+
+def gemmpipe_combine_grad(type, T, top_k, C, dY, lddy, Ys, ldys, rows, weights, dYs, lddys, dweights,
+                          stream=None) -> None:
+    """Gradients of gemmpipe_combine to its rows (dYs) and weights (dweights, fp32)."""
+    _check(load().gemmpipe_combine_grad(type, T, top_k, C, _ptr(dY), lddy, _ptr(Ys), ldys, _ptr(rows), _ptr(weights),
+                                        _ptr(dYs), lddys, _ptr(dweights), _stream(stream)), "gemmpipe_combine_grad")
+
+
+def gemm_grouped(type, R, N, K, E, X, ldx, offsets, W, Y, ldy, stream=None) -> None:
+    """Y[r] = X[r] @ W[e] for the rows r of each expert e (W: E x K x N)."""
+    _check(load().gemm_grouped(type, R, N, K, E, _ptr(X), ldx, _ptr(offsets), _ptr(W), _ptr(Y), ldy,
+                               _stream(stream)), "gemm_grouped")
+
+
+def gemm_grouped_dx(type, R, N, K, E, dY, lddy, offsets, W, dX, lddx, stream=None) -> None:
+    """dX[r] = dY[r] @ W[e].T: the gradient of gemm_grouped to its rows."""
+    _check(load().gemm_grouped_dx(type, R, N, K, E, _ptr(dY), lddy, _ptr(offsets), _ptr(W), _ptr(dX), lddx,
+                                  _stream(stream)), "gemm_grouped_dx")
+
+
+def gemm_grouped_dw(type, R, N, K, E, X, ldx, dY, lddy, offsets, dW, stream=None) -> None:
+    """dW[e] = X[rows of e].T @ dY[rows of e]: its gradient to the weights."""
+    _check(load().gemm_grouped_dw(type, R, N, K, E, _ptr(X), ldx, _ptr(dY), lddy, _ptr(offsets), _ptr(dW),
+                                  _stream(stream)), "gemm_grouped_dw")
+
+
+def gemm_grouped_dw8(type, R, N, K, E, Q, S, dY, lddy, offsets, dW, stream=None) -> None:
+    """gemm_grouped_dw with the rows X as gemmpipe_keep8 left them."""
+    _check(load().gemm_grouped_dw8(type, R, N, K, E, _ptr(Q), _ptr(S), _ptr(dY), lddy, _ptr(offsets), _ptr(dW),
+                                   _stream(stream)), "gemm_grouped_dw8")
+
+
+def gemmpipe_keep8(type, R, C, X, ldx, Q, S, stream=None) -> None:
+    """Keeps the rows X in 8 bits: Q (R x C int8) and a step byte per 32 values, S."""
+    _check(load().gemmpipe_keep8(type, R, C, _ptr(X), ldx, _ptr(Q), _ptr(S), _stream(stream)), "gemmpipe_keep8")
+
+
+def gemmpipe_restore8(type, R, C, Q, S, X, ldx, stream=None) -> None:
+    """X = Q * 2**(S - 127), the values that gemmpipe_keep8 kept."""
+    _check(load().gemmpipe_restore8(type, R, C, _ptr(Q), _ptr(S), _ptr(X), ldx, _stream(stream)),
+           "gemmpipe_restore8")
 
 
 def gemmpipe_host_panel_rows(M: int) -> int:
