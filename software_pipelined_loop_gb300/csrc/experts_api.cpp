@@ -212,18 +212,20 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
 
     GroupedParams p;
     std::memset(&p, 0, sizeof(p));
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, tp;  // tp: the row operand in short copies
     std::memset(&ta, 0, sizeof(ta));
     std::memset(&tb, 0, sizeof(tb));
+    std::memset(&tp, 0, sizeof(tp));
     bool ok = true;
     if (q.mode == gp::kRows) {
         p.a_groups = q.N % 64 == 0;
         ok = (p.a_groups ? encode_weight_groups(&ta, bf16, W, q.E, q.K, q.N, wld)
                          : encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 64)) &&
-             encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn);
+             encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn) && encode_rows(&tp, bf16, q.rows, q.R, 32);
         p.depth = q.K;
     } else if (q.mode == gp::kRowsT) {
-        ok = encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 128) && encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn);
+        ok = encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 128) &&
+             encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn) && encode_rows(&tp, bf16, q.rows, q.R, 32);
         p.depth = q.N;
     } else {
         p.a_groups = q.grad.width % 64 == 0;
@@ -241,6 +243,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     p.out = q.out;
     p.ldo = q.ldo;
     p.bf16 = bf16 ? 1 : 0;
+    p.vec_store = tma_ok(q.out, q.ldo) ? 1 : 0;
     p.stall_kb = -1;
     p.timeout_ns = 2000000000ull + static_cast<uint64_t>((weights ? q.R : p.depth) / 64 + 1) * 10000ull;
     if (gp::status_word(&p.status) != cudaSuccess) {
@@ -250,7 +253,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     const int64_t units = v->max_units(), tiles = row_tiles * f_tiles;
     if (units < 1) return GEMMPIPE_ERR_LAUNCH;
     const int grid = static_cast<int>((v->pair ? 2 : 1) * (tiles < units ? tiles : units));
-    return gp::api_launch(true, s, 1, [&] { return v->launch(ta, tb, p, grid, s); });
+    return gp::api_launch(true, s, 1, [&] { return v->launch(ta, tb, tp, p, grid, s); });
 }
 
 // Sizes common to the grouped products.

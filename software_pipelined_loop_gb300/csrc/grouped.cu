@@ -43,7 +43,7 @@ void configure(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid
 }
 
 template <class Cfg>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const GroupedParams &p, int grid, cudaStream_t s)
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &bpart, const GroupedParams &p, int grid, cudaStream_t s)
 {
     int dev = 0;
     cudaError_t e = prepare<Cfg>(&dev);
@@ -51,7 +51,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const GroupedPara
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     configure<Cfg>(cfg, attr, grid, s);
-    e = cudaLaunchKernelEx(&cfg, grouped_kernel<Cfg>, a, b, p);
+    e = cudaLaunchKernelEx(&cfg, grouped_kernel<Cfg>, a, b, bpart, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -45,6 +45,7 @@ struct GroupedCfg {
     static constexpr int BK = 64;
     static constexpr bool A_MN = MODE != kRowsT;    // W[k][n] and dY[r][n]: features contiguous
     static constexpr bool B_MN = MODE == kWeights;  // X[r][k] of the weight gradient
+    static constexpr int N_UNIT = 16 * CLUSTER;     // the MMA's columns are a multiple of this
     static constexpr int CTA_BN = BN / CLUSTER;     // columns of B each CTA holds
     static constexpr int A_BYTES = BM * BK * 2;
     static constexpr int B_BYTES = CTA_BN * BK * 2;
@@ -58,7 +59,12 @@ struct GroupedCfg {
     static constexpr int EPI_COLS = BN / 2;         // columns per epilogue warp
     static constexpr int EPI_BLOCK = EPI_COLS < 32 ? EPI_COLS : 32;
 
-    static constexpr int TABLE_OFF = STAGES * STAGE_BYTES;
+    static constexpr int B_PART_ROWS = 32;          // rows of one short copy of the row operand
+    static constexpr int B_PART_BYTES = B_PART_ROWS * 128;
+
+    static constexpr int STAGING_OFF = STAGES * STAGE_BYTES;
+    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * 64;
+    static constexpr int TABLE_OFF = STAGING_OFF + STAGING_BYTES;
     static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2);
     static constexpr int CTL_OFF = TABLE_OFF + TABLE_BYTES;
     static constexpr int CTL_BYTES = 8 * (4 * STAGES + 5) + 32;
@@ -145,6 +151,7 @@ struct GroupedTile {
     int32_t count;   // its rows
     int32_t f0;      // first feature of the tile
     int32_t c0;      // first output row of the tile, within the expert
+    int32_t cols;    // the MMA's columns: the tile's output rows, rounded up
     int32_t kbs;     // k-blocks
     int32_t last;    // products in the last k-block (1 .. 64)
 };
@@ -175,7 +182,15 @@ struct GroupedIter {
         w.row0 = t.start[e];
         w.count = t.start[e + 1] - w.row0;
         w.f0 = (in - c * f_tiles) * Cfg::TILE_F;
-        w.c0 = c * Cfg::BN;
+        if constexpr (Cfg::MODE == kWeights) {
+            w.c0 = c * Cfg::BN;
+            w.cols = Cfg::BN;
+        } else {
+            // Whole tiles, and a last one of as many columns as it needs.
+            w.c0 = c * Cfg::BN;
+            const int32_t left = w.count - w.c0;
+            w.cols = left < Cfg::BN ? (left + Cfg::N_UNIT - 1) / Cfg::N_UNIT * Cfg::N_UNIT : Cfg::BN;
+        }
         const int64_t depth = Cfg::MODE == kWeights ? w.count : p.depth;
         w.kbs = static_cast<int32_t>((depth + Cfg::BK - 1) / Cfg::BK);
         w.last = static_cast<int32_t>(depth - static_cast<int64_t>(w.kbs - 1) * Cfg::BK);
@@ -194,7 +209,7 @@ __device__ __forceinline__ bool has_stray_rows(const GroupedTile &w, int32_t kb)
 
 template <class Cfg>
 __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, const CUtensorMap *tB,
-                                 uint32_t sbase, GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w,
+                                 const CUtensorMap *tBpart, uint32_t sbase, GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w,
                                  uint32_t rank)
 {
     int stage = 0;
@@ -210,7 +225,12 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
     GroupedTile t;
     while (ok && it.next(p, t)) {
         const int32_t f0 = t.f0 + static_cast<int32_t>(rank) * Cfg::BM;
-        const int32_t c0 = t.c0 + static_cast<int32_t>(rank) * Cfg::CTA_BN;
+        const int32_t c0 = t.c0 + static_cast<int32_t>(rank) * (t.cols / Cfg::CLUSTER);
+        // Copies of the row operand: one of all CTA_BN rows, or as many of 32
+        // rows as hold the tile's columns when that is a quarter less.
+        const int32_t parts = (t.cols / Cfg::CLUSTER + Cfg::B_PART_ROWS - 1) / Cfg::B_PART_ROWS;
+        const bool whole = Cfg::MODE == kWeights || parts * Cfg::B_PART_ROWS >= Cfg::CTA_BN;
+        const uint32_t bytes = Cfg::A_BYTES + (whole ? Cfg::B_BYTES : parts * Cfg::B_PART_BYTES);
         for (int32_t kb = 0; kb < t.kbs; ++kb, ++kb_count) {
             if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->empty[stage]), phase ^ 1u))) {
                 ok = false;
@@ -227,7 +247,7 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
                         mbar_arrive_expect_tx(raw0 + so, Cfg::STAGE_BYTES);
                         bar = raw0_self + so;
                     } else {
-                        if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * Cfg::STAGE_BYTES);
+                        if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * bytes);
                         bar = full0_leader + so;
                     }
                     auto load4 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z, int32_t v) {
@@ -256,10 +276,8 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
                             load3(sa, tA, f0, k0, t.e);
                             load3(sa + Cfg::ATOM_BYTES, tA, f0 + 64, k0, t.e);
                         }
-                        load2(sb, tB, k0, t.row0 + c0);
                     } else if constexpr (Cfg::MODE == kRowsT) {
                         load3(sa, tA, k0, f0, t.e);
-                        load2(sb, tB, k0, t.row0 + c0);
                     } else {
                         if (p.a_groups) {
                             load3(sa, tA, 0, t.row0 + k0, f0 / 64);
@@ -273,6 +291,14 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
 #pragma unroll
                             for (int j = 0; j < Cfg::CTA_BN / 64; ++j)
                                 load2(sb + j * Cfg::ATOM_BYTES, tB, c0 + 64 * j, t.row0 + k0);
+                        }
+                    }
+                    if constexpr (Cfg::MODE != kWeights) {
+                        if (whole) {
+                            load2(sb, tB, k0, t.row0 + c0);
+                        } else {
+                            for (int32_t j = 0; j < parts; ++j)
+                                load2(sb + j * Cfg::B_PART_BYTES, tBpart, k0, t.row0 + c0 + j * Cfg::B_PART_ROWS);
                         }
                     }
                 }
@@ -366,7 +392,7 @@ template <class Cfg>
 __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
                             GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w)
 {
-    const uint32_t idesc = umma_idesc_16bit_f32(Cfg::TILE_F, Cfg::BN, p.bf16 != 0, Cfg::A_MN, Cfg::B_MN);
+    const uint32_t idesc0 = umma_idesc_16bit_f32(Cfg::TILE_F, 0, p.bf16 != 0, Cfg::A_MN, Cfg::B_MN);
     const uint64_t dA0 = Cfg::A_MN ? umma_desc_sw128(sbase, Cfg::ATOM_BYTES, 1024) : umma_desc_sw128(sbase, 16, 1024);
     const uint64_t dB0 = Cfg::B_MN ? umma_desc_sw128(sbase + Cfg::A_BYTES, Cfg::ATOM_BYTES, 1024)
                                    : umma_desc_sw128(sbase + Cfg::A_BYTES, 16, 1024);
@@ -385,6 +411,7 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
         }
         tc_fence_after_sync();
         const uint32_t d = tmem_base + acc * Cfg::BN;
+        const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.cols >> 3) << 17);
         for (int32_t kb = 0; kb < t.kbs; ++kb) {
             if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->full[stage]), phase))) {
                 ok = false;
@@ -447,56 +474,94 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
 
 // --------------------------------------------------------------- epilogue
 
-__device__ __forceinline__ uint16_t round_16bit(float v, bool bf16)
+// Two fp32 sums rounded to 16 bits, `lo` in the low half.
+__device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi, bool bf16)
 {
-    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+    uint32_t r;
+    if (bf16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+    return r;
 }
 
 // Accumulator lane l of warp quarter q is feature f0 + 32 q + l, column c the
-// output row c0 + c; the fp32 sum is rounded once, to the operands' type.
+// output row c0 + c.  The sums are rounded once, to the operands' type, and
+// turned through a per-warp staging tile of EPI_BLOCK rows x 32 features
+// (16-byte chunks, XOR-swizzled by row: free of bank conflicts both ways), so
+// that a store instruction writes 64 contiguous bytes of 8 output rows.
 template <class Cfg>
-__device__ void grouped_epilogue(const GroupedParams &p, uint32_t tmem_base, GroupedCtl<Cfg::STAGES> *ctl,
-                                 GroupTable tab, const Waiter &w, int warp, int lane, uint32_t rank)
+__device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
+                                 GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, int warp, int lane,
+                                 uint32_t rank)
 {
     const int e = warp - Cfg::EPI_WARP0;
     const int q = warp & 3, h = e >> 2;
     const bool bf16 = p.bf16 != 0;
+    constexpr int NB = Cfg::EPI_BLOCK;
+    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * 64);
+    // This lane's row address in stmatrix (matrix lane / 8 = 8 features, row lane % 8) ...
+    const uint32_t put = stg + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    // ... and its chunk when reading 8 rows x 64 bytes.
+    const uint32_t get = stg + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
     uint16_t *out = static_cast<uint16_t *>(p.out);
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (it.next(p, t)) {
-        const int64_t f = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * 32 + lane;
-        const int64_t rows = Cfg::MODE == kWeights ? p.out_rows : t.count;  // output rows of the expert
+        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * 32;  // the warp's first feature
+        const int64_t all = Cfg::MODE == kWeights ? p.out_rows : t.count;  // output rows of the expert
         const int64_t base = Cfg::MODE == kWeights ? p.out_rows * t.e : t.row0;
-        const int64_t c0 = static_cast<int64_t>(t.c0) + h * Cfg::EPI_COLS;
+        // The tile's rows are its columns up to the expert's last row; this
+        // warp takes the first or the second half of them.
+        const int32_t half = ((t.cols / 2) + NB - 1) / NB * NB;
+        const int64_t end = all - t.c0 < t.cols ? all - t.c0 : t.cols;
+        const int32_t from = h ? half : 0;
+        const int64_t to = h ? end : (end < half ? end : half);
         const bool empty = t.kbs == 0;
         if (!empty) {
             if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->tfull[acc]), acc_phase))) return;
             tc_fence_after_sync();
         }
-        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * Cfg::BN + h * Cfg::EPI_COLS;
+        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * Cfg::BN;
 #pragma unroll 1
-        for (int j = 0; j < Cfg::EPI_COLS; j += Cfg::EPI_BLOCK) {
-            if (c0 + j >= rows) break;
-            uint32_t r[Cfg::EPI_BLOCK];
+        for (int32_t j = from; j < to; j += NB) {
+            uint32_t lo[NB / 2], hi[NB / 2];  // lanes 0-15 and 16-31 of the quarter
             if (empty) {
 #pragma unroll
-                for (int i = 0; i < Cfg::EPI_BLOCK; ++i) r[i] = 0;
+                for (int i = 0; i < NB / 2; ++i) lo[i] = hi[i] = 0;
             } else {
-                if constexpr (Cfg::EPI_BLOCK == 32)
-                    tmem_ld_32x32b_x32(tbase + j, r);
-                else
-                    tmem_ld_32x32b_x16(tbase + j, r);
+                if constexpr (NB == 32) {
+                    tmem_ld_16x256b_x4(tbase + j, lo);
+                    tmem_ld_16x256b_x4(tbase + j + (16u << 16), hi);
+                } else {
+                    tmem_ld_16x256b_x2(tbase + j, lo);
+                    tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
+                }
                 tmem_wait_ld();
             }
-            uint16_t *o = out + (base + c0 + j) * p.ldo + f;
-            const int n = rows - (c0 + j) < Cfg::EPI_BLOCK ? static_cast<int>(rows - (c0 + j)) : Cfg::EPI_BLOCK;
-            if (f < p.features) {
 #pragma unroll
-                for (int i = 0; i < Cfg::EPI_BLOCK; ++i)
-                    if (i < n) o[i * p.ldo] = round_16bit(__uint_as_float(r[i]), bf16);
+            for (int i = 0; i < NB / 8; ++i)
+                stmatrix_x4_trans(put + i * 512, round_pair(lo[4 * i], lo[4 * i + 1], bf16),
+                                  round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
+                                  round_pair(hi[4 * i], hi[4 * i + 1], bf16),
+                                  round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
+            __syncwarp();
+            const int n = to - j < NB ? static_cast<int>(to - j) : NB;
+            uint16_t *o = out + (base + t.c0 + j) * p.ldo + f0;
+            if (p.vec_store && f0 + 32 <= p.features) {
+                // 16-byte pieces, four lanes to a row.
+                o += (lane >> 2) * p.ldo + (lane & 3) * 8;
+#pragma unroll
+                for (int i = 0; i < NB / 8; ++i)
+                    if (8 * i + (lane >> 2) < n)
+                        *reinterpret_cast<uint4 *>(o + i * 8 * p.ldo) = ld_shared_v4(get + i * 512);
+            } else if (f0 + lane < p.features) {
+                // A feature per lane, row by row.
+#pragma unroll 8
+                for (int c = 0; c < n; ++c)
+                    o[c * p.ldo + lane] = ld_shared_u16(stg + c * 64 + ((((lane >> 3) ^ (c >> 1)) & 3) << 4) + (lane & 7) * 2);
             }
             __syncwarp();
         }
@@ -530,7 +595,7 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t tmem_base, Gro
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const GroupedParams p)
+                   const __grid_constant__ CUtensorMap tmBpart, const GroupedParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -581,13 +646,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const Waiter w{&ctl->abort, p.status, p.timeout_ns};
     const uint32_t rank = Cfg::PAIR ? cluster_ctarank() : 0u;
     if (warp == 0) {
-        grouped_producer<Cfg>(p, &tmA, &tmB, sbase, ctl, tab, w, rank);
+        grouped_producer<Cfg>(p, &tmA, &tmB, &tmBpart, sbase, ctl, tab, w, rank);
     } else if (warp == 1) {
         if (rank == 0) grouped_mma<Cfg>(p, sbase, tmem_base, ctl, tab, w);
     } else if (warp == 2) {
         if constexpr (Cfg::MODE == kWeights) clear_stray_rows<Cfg>(p, sbase, ctl, tab, w, rank, lane);
     } else if (warp >= Cfg::EPI_WARP0) {
-        grouped_epilogue<Cfg>(p, tmem_base, ctl, tab, w, warp, lane, rank);
+        grouped_epilogue<Cfg>(p, sbase, tmem_base, ctl, tab, w, warp, lane, rank);
     }
     __syncwarp();
     tc_fence_before_sync();

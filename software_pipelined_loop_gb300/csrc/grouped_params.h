@@ -23,6 +23,7 @@ struct GroupedParams {
     void *out;
     int64_t ldo;             // output row pitch in elements
     int bf16;
+    int vec_store;           // output base and pitch allow 16-byte stores
     int a_groups, b_groups;  // 1: the operand's tensor map is in 64-column groups (one copy per k-block)
     uint64_t timeout_ns;
     int64_t stall_kb;        // test hook: CTA 0 leaves this k-block unfilled (-1: none)
