@@ -40,6 +40,8 @@ bool bad_pointer(const void *p, int bytes) { return !p || misaligned(p, bytes); 
 
 // ----------------------------------------------------------- routing, rows
 
+constexpr int64_t kMaxWidth = int64_t(1) << 30;  // elements of a token's row (32-bit places)
+
 struct Tokens {
     int64_t T, k, R;
 };
@@ -374,7 +376,8 @@ gemmpipe_status_t gemmpipe_dispatch(int type, int64_t T, int64_t top_k, int64_t 
 {
     return guarded([&] {
         Tokens t;
-        if (bad_type(type) || bad_tokens(T, top_k, &t) || bad_matrix(T, C, ldx) || bad_matrix(t.R, C, ldxs))
+        if (bad_type(type) || bad_tokens(T, top_k, &t) || C > kMaxWidth || bad_matrix(T, C, ldx) ||
+            bad_matrix(t.R, C, ldxs))
             return GEMMPIPE_ERR_INVALID_VALUE;
         if (T == 0 || C == 0) return GEMMPIPE_OK;
         if (bad_pointer(X, 2) || bad_pointer(Xs, 2) || bad_pointer(rows, 4) || misaligned(weights, 4))
@@ -398,7 +401,8 @@ gemmpipe_status_t gemmpipe_combine(int type, int64_t T, int64_t top_k, int64_t C
 {
     return guarded([&] {
         Tokens t;
-        if (bad_type(type) || bad_tokens(T, top_k, &t) || bad_matrix(t.R, C, ldys) || bad_matrix(T, C, ldy))
+        if (bad_type(type) || bad_tokens(T, top_k, &t) || C > kMaxWidth || bad_matrix(t.R, C, ldys) ||
+            bad_matrix(T, C, ldy))
             return GEMMPIPE_ERR_INVALID_VALUE;
         if (T == 0 || C == 0) return GEMMPIPE_OK;
         if (bad_pointer(Ys, 2) || bad_pointer(Y, 2) || bad_pointer(rows, 4) || misaligned(weights, 4))
@@ -422,8 +426,8 @@ gemmpipe_status_t gemmpipe_combine_grad(int type, int64_t T, int64_t top_k, int6
 {
     return guarded([&] {
         Tokens t;
-        if (bad_type(type) || bad_tokens(T, top_k, &t) || bad_matrix(T, C, lddy) || bad_matrix(t.R, C, ldys) ||
-            bad_matrix(t.R, C, lddys))
+        if (bad_type(type) || bad_tokens(T, top_k, &t) || C > kMaxWidth || bad_matrix(T, C, lddy) ||
+            bad_matrix(t.R, C, ldys) || bad_matrix(t.R, C, lddys))
             return GEMMPIPE_ERR_INVALID_VALUE;
         if (T == 0) return GEMMPIPE_OK;
         if (bad_pointer(rows, 4) || misaligned(weights, 4) || bad_pointer(dweights, 4))

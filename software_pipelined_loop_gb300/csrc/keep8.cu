@@ -59,92 +59,199 @@ __device__ __forceinline__ float step_of(uint32_t byte)
     return byte == kNanStep ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t quantise(uint32_t bits, float inv)
+// min(|a|, b) with a's sign (b positive).
+__device__ __forceinline__ float clamp_abs(float a, float b)
 {
-    const float q = fminf(fmaxf(rintf(value_of<BF16>(bits) * inv), -127.f), 127.f);
-    return static_cast<uint32_t>(static_cast<int>(q)) & 255u;
+    float r;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// Four lanes hold a group, 8 values each.
+// The bits of 1.5 * 2^23 + q: adding rounds x / step to a whole number, to
+// nearest even, and leaves q's byte lowest.
+__device__ __forceinline__ uint32_t whole_bits(float x, float inv)
+{
+    return __float_as_uint(clamp_abs(x * inv, 127.f) + 12582912.f);
+}
+
+// Eight values (two to a word) of one group to their bytes.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads)
-    keep8_wide_kernel(const uint16_t *X, int64_t rows, int64_t pieces, int64_t ldx, int8_t *Q, uint8_t *S)
+__device__ __forceinline__ uint2 quantise8(const uint32_t (&w)[4], uint32_t byte)
+{
+    const float inv = per_step(byte & 255u);
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        b[2 * i] = whole_bits(value_of<BF16>(w[i] & 0xffffu), inv);
+        b[2 * i + 1] = whole_bits(BF16 ? __uint_as_float(w[i] & 0xffff0000u) : value_of<BF16>(w[i] >> 16), inv);
+    }
+    uint2 q;
+    q.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    q.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    if (byte == kNanStep) q = make_uint2(0, 0);
+    return q;
+}
+
+// The largest magnitude of 8 values, as bits (an infinity or NaN is above all others).
+__device__ __forceinline__ uint32_t top8(const uint32_t (&w)[4])
+{
+    const uint32_t a = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & a, w[1] & a), __vmaxu2(w[2] & a, w[3] & a));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// The largest over the 4 lanes of a group.
+__device__ __forceinline__ uint32_t top_of_group(uint32_t top)
+{
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+}
+
+// Dense rows of whole groups on 16-byte boundaries: one run of 8-value
+// pieces, four lanes to a group, FLIGHT pieces per thread in flight.
+constexpr int kFlight = 4;
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) keep8_dense_kernel(const uint16_t *X, int64_t n, int8_t *Q, uint8_t *S)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t n = rows * pieces;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i - threadIdx.x % 32 < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const bool has = i < n;
-        const int64_t r = has ? i / pieces : 0, c = has ? i - r * pieces : 0;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (has) x = ldg_nc_v4(X + r * ldx + 8 * c);
-        const uint32_t a = 0x7fff7fffu;
-        const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & a, x.y & a), __vmaxu2(x.z & a, x.w & a));
-        uint32_t top = (m2 & 0xffffu) > (m2 >> 16) ? (m2 & 0xffffu) : (m2 >> 16);
-        uint32_t o = __shfl_xor_sync(0xffffffffu, top, 1);
-        top = o > top ? o : top;
-        o = __shfl_xor_sync(0xffffffffu, top, 2);
-        top = o > top ? o : top;
-        const uint32_t byte = step_byte<BF16>(top);
-        const float inv = byte == kNanStep ? 0.f : per_step(byte);
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t q[2] = {0, 0};
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kFlight) + threadIdx.x;
+    uint4 x[kFlight];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const uint32_t b = (w[u >> 1] >> (16 * (u & 1))) & 0xffffu;
-            q[u >> 2] |= (byte == kNanStep ? 0u : quantise<BF16>(b, inv)) << (8 * (u & 3));
-        }
-        if (has) {
-            *reinterpret_cast<uint2 *>(Q + 8 * i) = make_uint2(q[0], q[1]);
+    for (int k = 0; k < kFlight; ++k) {
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (i0 + k * kThreads < n) x[k] = ldg_nc_v4(X + 8 * (i0 + k * kThreads));
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+        const int64_t i = i0 + k * kThreads;
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        const uint32_t byte = step_byte<BF16>(top_of_group(top8(w)));
+        const uint2 q = quantise8<BF16>(w, byte);
+        if (i < n) {
+            *reinterpret_cast<uint2 *>(Q + 8 * i) = q;
             if ((i & 3) == 0) S[i >> 2] = static_cast<uint8_t>(byte);
         }
     }
 }
 
-// Any width, pitch and alignment: a warp per group, a value per lane.
+template <bool BF16>
+__device__ __forceinline__ uint4 restore_piece(uint2 q, float s0, float s1, int first)
+{
+    // The piece's elements before `first` have step s0, the others s1.
+    uint32_t o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t w = u < 2 ? q.x : q.y;
+        const int lo = static_cast<int8_t>(w >> (16 * (u & 1))), hi = static_cast<int8_t>(w >> (16 * (u & 1) + 8));
+        o[u] = bits_of<BF16>(static_cast<float>(lo) * (2 * u < first ? s0 : s1)) |
+               (bits_of<BF16>(static_cast<float>(hi) * (2 * u + 1 < first ? s0 : s1)) << 16);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) restore8_dense_kernel(const int8_t *Q, const uint8_t *S, int64_t n, uint16_t *X)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kFlight) + threadIdx.x;
+    uint2 q[kFlight];
+    uint32_t s[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+        const int64_t i = i0 + k * kThreads;
+        q[k] = make_uint2(0, 0);
+        s[k] = 0;
+        if (i < n) {
+            q[k] = *reinterpret_cast<const uint2 *>(Q + 8 * i);
+            s[k] = S[i >> 2];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+        const int64_t i = i0 + k * kThreads;
+        const float step = step_of(s[k]);
+        if (i < n) *reinterpret_cast<uint4 *>(X + 8 * i) = restore_piece<BF16>(q[k], step, step, 8);
+    }
+}
+
+// ---- any width, pitch and alignment: a warp takes 256 values of a row
+
+// Eight 16-bit values at elements [e, e + 8) of a row of n, zeros outside.
+__device__ __forceinline__ void load_values(const uint16_t *row, int64_t n, int64_t e, uint32_t (&w)[4])
+{
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(row), end = begin + 2 * static_cast<uintptr_t>(n);
+    const uintptr_t at = begin + 2 * static_cast<uintptr_t>(e);
+    const uint32_t shift = static_cast<uint32_t>(at & 15u);
+    const uintptr_t a0 = at - shift, a1 = a0 + 16;
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (a0 < end) lo = ldg_nc_v4(reinterpret_cast<const void *>(a0));
+    if (shift && a1 < end) hi = ldg_nc_v4(reinterpret_cast<const void *>(a1));
+    realign16(lo, hi, shift, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] &= (e + 2 * i < n ? 0xffffu : 0u) | (e + 2 * i + 1 < n ? 0xffff0000u : 0u);
+}
+
+// Eight bytes at p; only aligned words that hold a byte of [begin, end) are read.
+__device__ __forceinline__ uint2 load_bytes(uintptr_t p, uintptr_t begin, uintptr_t end)
+{
+    const uint32_t shift = static_cast<uint32_t>(p & 7u);
+    const uintptr_t a0 = p - shift, a1 = a0 + 8;
+    unsigned long long lo = 0, hi = 0;
+    if (a0 < end && a0 + 8 > begin) lo = *reinterpret_cast<const unsigned long long *>(a0);
+    if (shift && a1 < end && a1 + 8 > begin) hi = *reinterpret_cast<const unsigned long long *>(a1);
+    const unsigned long long v = shift ? (lo >> (8 * shift)) | (hi << (64 - 8 * shift)) : lo;
+    return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+}
+
+constexpr int kSpan = 256;  // values a warp takes at once
+
+// The bytes of a span meet in shared memory and leave as the destination's
+// own 8-byte words (rows of bytes start anywhere).
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
     keep8_kernel(const uint16_t *X, int64_t rows, int64_t width, int64_t ldx, int8_t *Q, uint8_t *S)
 {
+    __shared__ __align__(16) uint8_t stage[kThreads / 32][kSpan + 16];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t groups = (width + 31) / 32, n = rows * groups;
+    uint8_t *mine = stage[threadIdx.x >> 5] + 8;
+    const int64_t groups = (width + 31) / 32, spans = (width + kSpan - 1) / kSpan, n = rows * spans;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     for (int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; g < n; g += warps) {
-        const int64_t r = g / groups, c = (g - r * groups) * 32 + lane;
-        const uint32_t b = c < width ? X[r * ldx + c] : 0u;
-        const uint32_t byte = step_byte<BF16>(__reduce_max_sync(0xffffffffu, b & 0x7fffu));
-        if (c < width) Q[r * width + c] = byte == kNanStep ? 0 : static_cast<int8_t>(quantise<BF16>(b, per_step(byte)));
-        if (lane == 0) S[g] = static_cast<uint8_t>(byte);
-    }
-}
-
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads)
-    restore8_wide_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int64_t pieces, uint16_t *X, int64_t ldx)
-{
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t n = rows * pieces;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t r = i / pieces, c = i - r * pieces;
-        const uint2 q = *reinterpret_cast<const uint2 *>(Q + 8 * i);
-        const float step = step_of(S[i >> 2]);
-        uint32_t o[4];
+        const int64_t r = g / spans, e0 = (g - r * spans) * kSpan, e = e0 + 8 * lane;
+        uint32_t w[4];
+        load_values(X + r * ldx, width, e, w);
+        const uint32_t byte = step_byte<BF16>(top_of_group(top8(w)));
+        *reinterpret_cast<uint2 *>(mine + 8 * lane) = quantise8<BF16>(w, byte);
+        if ((lane & 3) == 0 && e < width) S[r * groups + e / 32] = static_cast<uint8_t>(byte);
+        __syncwarp();
+        uint8_t *to = reinterpret_cast<uint8_t *>(Q) + r * width + e0;
+        const int have = static_cast<int>(width - e0 < kSpan ? width - e0 : kSpan);
+        const int head = static_cast<int>((8 - (reinterpret_cast<uintptr_t>(to) & 7u)) & 7u);  // bytes before a word
+        const int at = head + 8 * lane;
+        if (at + 8 <= have) {
+            uint32_t a = 0, b = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t w = u < 2 ? q.x : q.y;
-            const int lo = static_cast<int8_t>(w >> (16 * (u & 1))), hi = static_cast<int8_t>(w >> (16 * (u & 1) + 8));
-            o[u] = bits_of<BF16>(lo * step) | (bits_of<BF16>(hi * step) << 16);
+            for (int u = 0; u < 4; ++u) {
+                a |= static_cast<uint32_t>(mine[at + u]) << (8 * u);
+                b |= static_cast<uint32_t>(mine[at + 4 + u]) << (8 * u);
+            }
+            *reinterpret_cast<uint2 *>(to + at) = make_uint2(a, b);
+        } else {
+            for (int u = at; u < have; ++u) to[u] = mine[u];
         }
-        *reinterpret_cast<uint4 *>(X + r * ldx + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (lane < head && lane < have) to[lane] = mine[lane];
+        __syncwarp();
     }
 }
 
+// A thread restores the values of one of the destination's 16-byte words;
+// they may lie in two groups.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
     restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int64_t width, uint16_t *X, int64_t ldx)
@@ -152,12 +259,26 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t groups = (width + 31) / 32, n = rows * groups;
+    const int64_t groups = (width + 31) / 32, spans = (width + 7 + kSpan - 1) / kSpan, n = rows * spans;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(Q), end = begin + static_cast<uintptr_t>(rows * width);
     for (int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; g < n; g += warps) {
-        const int64_t r = g / groups, c = (g - r * groups) * 32 + lane;
-        const float step = step_of(S[g]);
-        if (c < width) X[r * ldx + c] = static_cast<uint16_t>(bits_of<BF16>(Q[r * width + c] * step));
+        const int64_t r = g / spans;
+        uint16_t *x = X + r * ldx;
+        const int64_t e = (g - r * spans) * kSpan + 8 * lane - static_cast<int64_t>((reinterpret_cast<uintptr_t>(x) & 15u) >> 1);
+        if (e >= width || e + 8 <= 0) continue;
+        const int64_t g0 = e > 0 ? e / 32 : 0, g1 = (e + 7 < width ? e + 7 : width - 1) / 32;
+        const float s0 = step_of(S[r * groups + g0]), s1 = step_of(S[r * groups + g1]);
+        const uint2 q = load_bytes(begin + static_cast<uintptr_t>(r * width + e), begin, end);
+        const uint4 v = restore_piece<BF16>(q, s0, s1, static_cast<int>(32 * (g0 + 1) - e));
+        if (e >= 0 && e + 8 <= width) {
+            *reinterpret_cast<uint4 *>(x + e) = v;
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (e + u >= 0 && e + u < width) x[e + u] = static_cast<uint16_t>(w[u >> 1] >> (16 * (u & 1)));
+        }
     }
 }
 
@@ -181,12 +302,13 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// `most`: blocks of a grid-stride kernel (0: one per kThreads of work).
 template <class... P, class... A>
-cudaError_t launch(void (*k)(P...), int64_t work, int sms, cudaStream_t s, A... args)
+cudaError_t launch(void (*k)(P...), int64_t work, int64_t most, cudaStream_t s, A... args)
 {
-    const int64_t blocks = (work + kThreads - 1) / kThreads, most = static_cast<int64_t>(sms) * 8;
+    const int64_t blocks = (work + kThreads - 1) / kThreads;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1);
+    c.gridDim = dim3(static_cast<unsigned>(most == 0 || blocks < most ? blocks : most), 1, 1);
     c.blockDim = dim3(kThreads, 1, 1);
     c.stream = s;
     cudaLaunchAttribute a[1];
@@ -197,10 +319,12 @@ cudaError_t launch(void (*k)(P...), int64_t work, int sms, cudaStream_t s, A... 
     return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
-bool wide(const void *X, int64_t ldx, const void *Q, int64_t width)
+// Rows that are one run of whole groups, on the accesses' boundaries, in at
+// most 2^31 - 1 blocks.
+bool dense(const void *X, int64_t ldx, const void *Q, int64_t rows, int64_t width)
 {
-    return width % 32 == 0 && ldx % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 &&
-           reinterpret_cast<uintptr_t>(Q) % 8 == 0;
+    return width % 32 == 0 && ldx == width && reinterpret_cast<uintptr_t>(X) % 16 == 0 &&
+           reinterpret_cast<uintptr_t>(Q) % 8 == 0 && rows * (width / 8) < (int64_t(1) << 40);
 }
 
 }  // namespace
@@ -208,27 +332,31 @@ bool wide(const void *X, int64_t ldx, const void *Q, int64_t width)
 cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t *X, int64_t ldx, int8_t *Q,
                          uint8_t *S, int sms, cudaStream_t s)
 {
-    if (wide(X, ldx, Q, width))
-        return launch(bf16 ? keep8_wide_kernel<true> : keep8_wide_kernel<false>, rows * (width / 8), sms, s, X, rows,
-                      width / 8, ldx, Q, S);
-    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * ((width + 31) / 32) * 32, sms, s, X, rows,
-                  width, ldx, Q, S);
+    if (dense(X, ldx, Q, rows, width)) {
+        const int64_t n = rows * (width / 8);
+        return launch(bf16 ? keep8_dense_kernel<true> : keep8_dense_kernel<false>, (n + kFlight - 1) / kFlight, 0, s, X, n,
+                      Q, S);
+    }
+    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * ((width + kSpan - 1) / kSpan) * 32, 8 * sms, s,
+                  X, rows, width, ldx, Q, S);
 }
 
 cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t *Q, const uint8_t *S, uint16_t *X,
                             int64_t ldx, int sms, cudaStream_t s)
 {
-    if (wide(X, ldx, Q, width))
-        return launch(bf16 ? restore8_wide_kernel<true> : restore8_wide_kernel<false>, rows * (width / 8), sms, s, Q,
-                      S, rows, width / 8, X, ldx);
-    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * ((width + 31) / 32) * 32, sms, s, Q,
-                  S, rows, width, X, ldx);
+    if (dense(X, ldx, Q, rows, width)) {
+        const int64_t n = rows * (width / 8);
+        return launch(bf16 ? restore8_dense_kernel<true> : restore8_dense_kernel<false>, (n + kFlight - 1) / kFlight, 0, s,
+                      Q, S, n, X);
+    }
+    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * ((width + 7 + kSpan - 1) / kSpan) * 32,
+                  8 * sms, s, Q, S, rows, width, X, ldx);
 }
 
 cudaError_t launch_repitch(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,
                            int sms, cudaStream_t s)
 {
-    return launch(repitch_kernel, rows * (ldd / 8), sms, s, src, rows, width, lds, dst, ldd);
+    return launch(repitch_kernel, rows * (ldd / 8), 8 * sms, s, src, rows, width, lds, dst, ldd);
 }
 
 }  // namespace gp
