@@ -13,6 +13,7 @@ namespace gp {
 struct GroupedVariant {
     int mode;      // GroupedMode
     int bn;        // output rows per tile
+    int tile_f;    // features per tile
     int pair;      // 1: CTA pairs, 256 features per tile; 0: single CTAs, 128
     int cta_bn;    // columns of the row operand per CTA
     int smem_bytes;
@@ -21,7 +22,7 @@ struct GroupedVariant {
     int (*max_units)();  // co-resident CTAs (or CTA pairs) on the current device
 };
 
-const GroupedVariant *grouped_variant(int mode, int bn);
+const GroupedVariant *grouped_variant(int mode, int bn, int tile_f);  // tile_f 0: any
 
 // ---- routing and rows (experts_rows.cu)
 
@@ -40,10 +41,11 @@ cudaError_t launch_combine_grad(bool bf16, int64_t tokens, int top_k, int64_t wi
 
 // ---- 8-bit copies (keep8.cu)
 
+// rows * ceil((width + 7) / 8192) must fit the grid (2^31 - 1 blocks).
 cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t *X, int64_t ldx, int8_t *Q,
-                         uint8_t *S, int sms, cudaStream_t s);
+                         uint8_t *S, cudaStream_t s);
 cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t *Q, const uint8_t *S, uint16_t *X,
-                            int64_t ldx, int sms, cudaStream_t s);
+                            int64_t ldx, cudaStream_t s);
 // Copy of a pitched 16-bit matrix to pitch ldd >= width (columns past width: zeros).
 cudaError_t launch_repitch(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,
                            int sms, cudaStream_t s);

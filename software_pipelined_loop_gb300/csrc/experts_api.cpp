@@ -21,7 +21,6 @@ using gp::GroupedVariant;
 
 constexpr int64_t kMaxDim = 2147483647;
 constexpr int64_t kMaxElems = int64_t(1) << 56;
-constexpr int kMaxTopK = 64;
 
 bool misaligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
@@ -38,6 +37,12 @@ bool bad_type(int type) { return type != GEMMPIPE_F16 && type != GEMMPIPE_BF16; 
 // Null or misaligned where something is to be read or written.
 bool bad_pointer(const void *p, int bytes) { return !p || misaligned(p, bytes); }
 
+// Rows in 8 bits: up to 2^44 values (the grid's blocks hold 8192 of a row, or 8192 of all).
+bool bad_kept(int64_t rows, int64_t width, int64_t ld)
+{
+    return bad_matrix(rows, width, ld) || (rows > 0 && (width + 7) / 8192 + 1 > kMaxDim / rows);
+}
+
 // ----------------------------------------------------------- routing, rows
 
 constexpr int64_t kMaxWidth = int64_t(1) << 30;  // elements of a token's row (32-bit places)
@@ -48,7 +53,7 @@ struct Tokens {
 
 bool bad_tokens(int64_t T, int64_t top_k, Tokens *t)
 {
-    if (bad_dim(T) || top_k < 1 || top_k > kMaxTopK || T > kMaxDim / top_k) return true;
+    if (bad_dim(T) || top_k < 1 || top_k > gp::kMaxTopK || T > kMaxDim / top_k) return true;
     *t = Tokens{T, top_k, T * top_k};
     return false;
 }
@@ -169,13 +174,15 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     if (!weights && (q.mode == gp::kRows ? q.K : q.N) == 0) return zero_rows(q.out, q.R, features, q.ldo, s);
 
     const int bn = weights ? 256 : rows_per_tile(q.R, q.E);
-    const GroupedVariant *v = gp::grouped_variant(q.mode, bn);
-    if (!v) return GEMMPIPE_ERR_INTERNAL;
-    if (v->smem_bytes > d.smem_optin) return GEMMPIPE_ERR_UNSUPPORTED_DEVICE;
-    const int64_t tile_f = v->pair ? 256 : 128;
-    const int64_t f_tiles = (features + tile_f - 1) / tile_f;
     // Tiles of all experts, at most (the bounds are on the device).
     const int64_t row_tiles = weights ? q.E * ((q.K + bn - 1) / bn) : q.R / bn + (q.R < q.E ? q.R : q.E);
+    // 64-feature tiles where 128-feature ones would leave SMs without one:
+    // the weights then stream through twice as many.
+    const bool narrow = q.mode == gp::kRows && bn == 32 && row_tiles * ((features + 127) / 128) < d.sms;
+    const GroupedVariant *v = gp::grouped_variant(q.mode, bn, bn == 256 ? 256 : (narrow ? 64 : 128));
+    if (!v) return GEMMPIPE_ERR_INTERNAL;
+    if (v->smem_bytes > d.smem_optin) return GEMMPIPE_ERR_UNSUPPORTED_DEVICE;
+    const int64_t f_tiles = (features + v->tile_f - 1) / v->tile_f;
     if (row_tiles > kMaxDim / f_tiles) return GEMMPIPE_ERR_INVALID_VALUE;
 
     // Operands that TMA cannot describe are copied to aligned rows.
@@ -196,7 +203,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
             q.rows.p = to;
             q.rows.ld = round8(q.rows.width);
             st = gp::api_launch(false, s, 1, [&] {
-                return gp::launch_restore8(bf16, q.R, q.K, q.Q, q.S, to, q.rows.ld, d.sms, s);
+                return gp::launch_restore8(bf16, q.R, q.K, q.Q, q.S, to, q.rows.ld, s);
             });
             if (st != GEMMPIPE_OK) return st;
         } else if (pad_x && (st = pad_rows(&q.rows, q.R, to, d, s)) != GEMMPIPE_OK) {
@@ -220,7 +227,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     std::memset(&tp, 0, sizeof(tp));
     bool ok = true;
     if (q.mode == gp::kRows) {
-        p.a_groups = q.N % 64 == 0;
+        p.a_groups = q.N % 64 == 0 && v->tile_f >= 128;
         ok = (p.a_groups ? encode_weight_groups(&ta, bf16, W, q.E, q.K, q.N, wld)
                          : encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 64)) &&
              encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn) && encode_rows(&tp, bf16, q.rows, q.R, 32);
@@ -312,7 +319,8 @@ gemmpipe_status_t weights_product(int type, int64_t R, int64_t N, int64_t K, int
                                   int64_t ldx, const int8_t *Q, const uint8_t *S, bool kept, const uint16_t *dY,
                                   int64_t lddy, const int32_t *offsets, uint16_t *dW, gemmpipe_stream_t stream)
 {
-    if (bad_product(type, R, N, K, E) || bad_matrix(R, K, ldx) || bad_matrix(R, N, lddy))
+    if (bad_product(type, R, N, K, E) || bad_matrix(R, K, ldx) || bad_matrix(R, N, lddy) ||
+        (kept && bad_kept(R, K, K)))
         return GEMMPIPE_ERR_INVALID_VALUE;
     if (N == 0 || K == 0) return GEMMPIPE_OK;
     if (bad_pointer(dW, 2) || bad_pointer(offsets, 4)) return GEMMPIPE_ERR_INVALID_VALUE;
@@ -491,7 +499,7 @@ gemmpipe_status_t gemmpipe_keep8(int type, int64_t R, int64_t C, const void *X, 
                                  gemmpipe_stream_t stream)
 {
     return guarded([&] {
-        if (bad_type(type) || bad_matrix(R, C, ldx)) return GEMMPIPE_ERR_INVALID_VALUE;
+        if (bad_type(type) || bad_kept(R, C, ldx)) return GEMMPIPE_ERR_INVALID_VALUE;
         if (R == 0 || C == 0) return GEMMPIPE_OK;
         if (bad_pointer(X, 2) || !Q || !S) return GEMMPIPE_ERR_INVALID_VALUE;
         ApiDevice d;
@@ -500,8 +508,7 @@ gemmpipe_status_t gemmpipe_keep8(int type, int64_t R, int64_t C, const void *X, 
         if ((st = check_all({{X, 2}, {Q, 1}, {S, 1}})) != GEMMPIPE_OK) return st;
         cudaStream_t s = stream_of(stream);
         return gp::api_launch(false, s, 1, [&] {
-            return gp::launch_keep8(type == GEMMPIPE_BF16, R, C, static_cast<const uint16_t *>(X), ldx, Q, S, d.sms,
-                                    s);
+            return gp::launch_keep8(type == GEMMPIPE_BF16, R, C, static_cast<const uint16_t *>(X), ldx, Q, S, s);
         });
     });
 }
@@ -510,7 +517,7 @@ gemmpipe_status_t gemmpipe_restore8(int type, int64_t R, int64_t C, const int8_t
                                     int64_t ldx, gemmpipe_stream_t stream)
 {
     return guarded([&] {
-        if (bad_type(type) || bad_matrix(R, C, ldx)) return GEMMPIPE_ERR_INVALID_VALUE;
+        if (bad_type(type) || bad_kept(R, C, ldx)) return GEMMPIPE_ERR_INVALID_VALUE;
         if (R == 0 || C == 0) return GEMMPIPE_OK;
         if (bad_pointer(X, 2) || !Q || !S) return GEMMPIPE_ERR_INVALID_VALUE;
         ApiDevice d;
@@ -519,7 +526,7 @@ gemmpipe_status_t gemmpipe_restore8(int type, int64_t R, int64_t C, const int8_t
         if ((st = check_all({{X, 2}, {Q, 1}, {S, 1}})) != GEMMPIPE_OK) return st;
         cudaStream_t s = stream_of(stream);
         return gp::api_launch(false, s, 1, [&] {
-            return gp::launch_restore8(type == GEMMPIPE_BF16, R, C, Q, S, static_cast<uint16_t *>(X), ldx, d.sms, s);
+            return gp::launch_restore8(type == GEMMPIPE_BF16, R, C, Q, S, static_cast<uint16_t *>(X), ldx, s);
         });
     });
 }

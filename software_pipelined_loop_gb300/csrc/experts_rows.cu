@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kSortThreads)
     for (int b = threadIdx.x; b < bins; b += kSortThreads) {
         int32_t all = 0, prior = 0;
         if (counts) {
+#pragma unroll 8
             for (unsigned k = 0; k < gridDim.x; ++k) {
                 const int32_t c = counts[static_cast<int64_t>(k) * bins + b];
                 all += c;
@@ -143,13 +144,10 @@ int sort_blocks(int64_t slots) { return static_cast<int>((slots + sort_chunk(slo
 // -------------------------------------------------------------- row pieces
 //
 // A thread moves 8 elements, 16 bytes, at a time.  Where every row of every
-// matrix starts on 16 bytes and holds whole pieces (WIDE), a piece is one
-// access.  Otherwise the pieces of a row are those of the output row's own
-// 16-byte words, so that all stores but a row's first and last are whole
-// words; an input piece is cut from the two aligned words that hold it (each
-// holds a byte of the row, so nothing outside the matrix is touched).  For
-// 4093 tokens x 4 rows of 3001 fp16 the sum takes 25 us so, 79 us with
-// 2-byte accesses.
+// matrix starts on 16 bytes and holds whole pieces, a piece is one access
+// (the kernels named *_wide).  Otherwise an output row is written in its own
+// 16-byte words -- up to 7 single elements before the first and after the
+// last -- and an input piece is cut from the two aligned words that hold it.
 
 struct Piece {
     uint32_t w[4];
@@ -188,54 +186,66 @@ __device__ __forceinline__ Piece narrow8(const float (&f)[8])
     return p;
 }
 
-// Elements [e, e + 8) of a row of n (zeros outside it; e may be negative).
-template <bool WIDE>
-__device__ __forceinline__ Piece load_piece(const uint16_t *row, int n, int e)
+__device__ __forceinline__ Piece load_wide(const uint16_t *p)
 {
-    Piece p;
-    if constexpr (WIDE) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(row + e);
-        p.w[0] = v.x;
-        p.w[1] = v.y;
-        p.w[2] = v.z;
-        p.w[3] = v.w;
-    } else {
-        const intptr_t begin = reinterpret_cast<intptr_t>(row), end = begin + 2 * static_cast<intptr_t>(n);
-        const intptr_t at = begin + 2 * static_cast<intptr_t>(e);
-        const uint32_t shift = static_cast<uint32_t>(at) & 15u;
-        const intptr_t a0 = at - shift, a1 = a0 + 16;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (a0 < end && a0 + 16 > begin) lo = *reinterpret_cast<const uint4 *>(a0);
-        if (shift && a1 < end && a1 + 16 > begin) hi = *reinterpret_cast<const uint4 *>(a1);
-        realign16(lo, hi, shift, p.w);
-        if (e < 0 || e + 8 > n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = e + 2 * i;
-                p.w[i] &= (k >= 0 && k < n ? 0xffffu : 0u) | (k + 1 >= 0 && k + 1 < n ? 0xffff0000u : 0u);
-            }
-        }
-    }
-    return p;
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    return Piece{{v.x, v.y, v.z, v.w}};
 }
 
-template <bool WIDE>
-__device__ __forceinline__ void store_piece(uint16_t *row, int n, int e, const Piece &p)
+__device__ __forceinline__ Piece load_any(const uint16_t *p)
 {
-    if (WIDE || (e >= 0 && e + 8 <= n)) {
-        *reinterpret_cast<uint4 *>(row + e) = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (e + i >= 0 && e + i < n) row[e + i] = static_cast<uint16_t>(p.w[i >> 1] >> (16 * (i & 1)));
-    }
+    Piece r;
+    load8_any(p, r.w);
+    return r;
 }
 
-// First element of piece 0 of an output row: its 16-byte words start there.
-template <bool WIDE>
-__device__ __forceinline__ int first_piece(const uint16_t *row)
+// p is on a 16-byte boundary.
+__device__ __forceinline__ void store_wide(uint16_t *p, const Piece &v)
 {
-    return WIDE ? 0 : -static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) >> 1);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+
+// An output row at any alignment: elements [0, head) and [head + 8 body, n)
+// are written one by one, the others as `body` aligned pieces.
+struct RowCut {
+    int head, body, n;
+    __device__ __forceinline__ RowCut(const uint16_t *row, int n_) : n(n_)
+    {
+        head = static_cast<int>(((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) >> 1);
+        if (head > n) head = n;
+        body = (n - head) >> 3;
+    }
+    // Element of single number i (i < singles()).
+    __device__ __forceinline__ int singles() const { return n - 8 * body; }
+    __device__ __forceinline__ int single(int i) const { return i < head ? i : i + 8 * body; }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float widen1(uint16_t v)
+{
+    if constexpr (BF16)
+        return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    else
+        return __half2float(__ushort_as_half(v));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t narrow1(float v)
+{
+    if constexpr (BF16)
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else
+        return __half_as_ushort(__float2half_rn(v));
+}
+
+template <bool BF16>
+__device__ __forceinline__ Piece scaled(const Piece &p, float w)
+{
+    float f[8];
+    widen8<BF16>(p, f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) f[u] *= w;
+    return narrow8<BF16>(f);
 }
 
 // A block's threads work in groups of `lanes` threads, one token per group.
@@ -247,61 +257,82 @@ struct RowShape {
     int64_t rows;  // tokens * top_k: entries of the row table outside [0, rows) are passed over
 };
 
-// Rows of X to the rows of their choices: a token's row is read once from
-// memory and written top_k times (times the choice's weight, if there are
-// weights).  Bound by memory: 16384 tokens x 8 rows of 2048 bf16 take 90 us,
-// 6.7 TB/s.
-template <bool BF16, bool WIDE>
+// Rows of X to the rows of their choices (times the choice's weight, if
+// there are weights): a token's row is read once from memory and written
+// top_k times.  Bound by memory: 16384 tokens x 8 rows of 2048 bf16 take
+// 90 us, 6.7 TB/s.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    dispatch_wide_kernel(RowShape g, const uint16_t *X, int64_t ldx, const int32_t *rows, const float *weights,
+                         uint16_t *Xs, int64_t ldxs)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int per_block = 256 / g.lanes, lane = threadIdx.x % g.lanes;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / g.lanes;
+    if (t >= g.tokens) return;
+    const int32_t *mine = rows + t * g.top_k;
+    for (int e = lane * 8; e < g.width; e += g.lanes * 8) {
+        const Piece x = load_wide(X + t * ldx + e);
+#pragma unroll 4
+        for (int j = 0; j < g.top_k; ++j) {
+            const int32_t r = mine[j];
+            const int64_t to = r < 0 ? ~r : r;
+            Piece p = x;
+            if (r < 0)
+                p = Piece{{0, 0, 0, 0}};
+            else if (weights)
+                p = scaled<BF16>(x, weights[t * g.top_k + j]);
+            if (to < g.rows) store_wide(Xs + to * ldxs + e, p);
+        }
+    }
+}
+
+// The same at any alignment, a warp per choice.
+template <bool BF16>
 __global__ void __launch_bounds__(256)
     dispatch_kernel(RowShape g, const uint16_t *X, int64_t ldx, const int32_t *rows, const float *weights,
                     uint16_t *Xs, int64_t ldxs)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int per_block = 256 / g.lanes, lane = threadIdx.x % g.lanes;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / g.lanes;
-    if (t >= g.tokens) return;
-    const int32_t *mine = rows + t * g.top_k;
-    const uint16_t *x = X + t * ldx;
-    auto put = [&](int j, int32_t r, int e, Piece p) {
-        const int64_t to = r < 0 ? ~r : r;
-        if (to >= g.rows) return;
-        if (r < 0) {
-            p = Piece{{0, 0, 0, 0}};
-        } else if (weights) {
-            const float w = weights[t * g.top_k + j];
-            float f[8];
-            widen8<BF16>(p, f);
+    const int lane = threadIdx.x & 31;
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (s >= g.rows) return;
+    const int32_t r = rows[s];
+    const int64_t to = r < 0 ? ~r : r;
+    if (to >= g.rows) return;
+    const uint16_t *x = X + s / g.top_k * ldx;
+    uint16_t *o = Xs + to * ldxs;
+    const RowCut cut(o, g.width);
+    const bool copied = r >= 0 && !weights;
+    const float w = r >= 0 && weights ? weights[s] : 1.f;
+    constexpr int FLIGHT = 4;
+    for (int i = lane; i < cut.body; i += 32 * FLIGHT) {
+        Piece p[FLIGHT];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] *= w;
-            p = narrow8<BF16>(f);
+        for (int u = 0; u < FLIGHT; ++u) {
+            p[u] = Piece{{0, 0, 0, 0}};
+            if (r >= 0 && i + 32 * u < cut.body) p[u] = load_any(x + cut.head + 8 * (i + 32 * u));
         }
-        store_piece<WIDE>(Xs + to * ldxs, g.width, e, p);
-    };
-    if constexpr (WIDE) {
-        for (int e = lane * 8; e < g.width; e += g.lanes * 8) {
-            const Piece p = load_piece<true>(x, g.width, e);
-#pragma unroll 4
-            for (int j = 0; j < g.top_k; ++j) put(j, mine[j], e, p);
-        }
-    } else {
-        for (int j = 0; j < g.top_k; ++j) {
-            const int32_t r = mine[j];
-            const int64_t to = r < 0 ? ~r : r;
-            if (to >= g.rows) continue;
-            for (int e = first_piece<false>(Xs + to * ldxs) + lane * 8; e < g.width; e += g.lanes * 8)
-                put(j, r, e, load_piece<false>(x, g.width, e));
-        }
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u)
+            if (i + 32 * u < cut.body)
+                store_wide(o + cut.head + 8 * (i + 32 * u), copied || r < 0 ? p[u] : scaled<BF16>(p[u], w));
+    }
+    if (lane < cut.singles()) {
+        const int e = cut.single(lane);
+        o[e] = r < 0 ? uint16_t(0) : (copied ? x[e] : narrow1<BF16>(widen1<BF16>(x[e]) * w));
     }
 }
 
 // y = sum over the token's kept choices of weight times the expert's row, in
 // fp32 in the order of the choices, rounded once.  Eight rows are in flight
 // per thread.
-template <bool BF16, bool WIDE>
+template <bool BF16>
 __global__ void __launch_bounds__(256)
-    combine_kernel(RowShape g, const uint16_t *Ys, int64_t ldys, const int32_t *rows, const float *weights,
-                   uint16_t *Y, int64_t ldy)
+    combine_wide_kernel(RowShape g, const uint16_t *Ys, int64_t ldys, const int32_t *rows, const float *weights,
+                        uint16_t *Y, int64_t ldy)
 {
     pdl_wait();
     pdl_launch_dependents();
@@ -309,9 +340,8 @@ __global__ void __launch_bounds__(256)
     const int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / g.lanes;
     if (t >= g.tokens) return;
     const int32_t *mine = rows + t * g.top_k;
-    uint16_t *y = Y + t * ldy;
-    constexpr int FLIGHT = WIDE ? 8 : 4;
-    for (int e = first_piece<WIDE>(y) + lane * 8; e < g.width; e += g.lanes * 8) {
+    constexpr int FLIGHT = 8;
+    for (int e = lane * 8; e < g.width; e += g.lanes * 8) {
         float acc[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) acc[u] = 0.f;
@@ -324,7 +354,7 @@ __global__ void __launch_bounds__(256)
                 w[j] = 0.f;
                 p[j] = Piece{{0, 0, 0, 0}};
                 if (r >= 0 && r < g.rows) {
-                    p[j] = load_piece<WIDE>(Ys + static_cast<int64_t>(r) * ldys, g.width, e);
+                    p[j] = load_wide(Ys + static_cast<int64_t>(r) * ldys + e);
                     w[j] = weights ? weights[t * g.top_k + j0 + j] : 1.f;
                 }
             }
@@ -336,7 +366,67 @@ __global__ void __launch_bounds__(256)
                 for (int u = 0; u < 8; ++u) acc[u] = fmaf(w[j], f[u], acc[u]);
             }
         }
-        store_piece<WIDE>(y, g.width, e, narrow8<BF16>(acc));
+        store_wide(Y + t * ldy + e, narrow8<BF16>(acc));
+    }
+}
+
+// The same at any alignment.  The kept choices' rows and weights are
+// listed once per token in shared memory.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    combine_kernel(RowShape g, const uint16_t *Ys, int64_t ldys, const int32_t *rows, const float *weights,
+                   uint16_t *Y, int64_t ldy)
+{
+    __shared__ const uint16_t *row_of[8][kMaxTopK];
+    __shared__ float weight_of[8][kMaxTopK];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int per_block = 256 / g.lanes, lane = threadIdx.x % g.lanes, slot = threadIdx.x / g.lanes;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + slot;
+    if (t < g.tokens) {
+        for (int j = lane; j < g.top_k; j += g.lanes) {
+            const int32_t r = rows[t * g.top_k + j];
+            const bool kept = r >= 0 && r < g.rows;
+            row_of[slot][j] = kept ? Ys + static_cast<int64_t>(r) * ldys : nullptr;
+            weight_of[slot][j] = kept && weights ? weights[t * g.top_k + j] : 1.f;
+        }
+    }
+    __syncthreads();
+    if (t >= g.tokens) return;
+    uint16_t *y = Y + t * ldy;
+    const RowCut cut(y, g.width);
+    constexpr int FLIGHT = 4;
+    for (int i = lane; i < cut.body; i += g.lanes) {
+        const int e = cut.head + 8 * i;
+        float acc[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc[u] = 0.f;
+        for (int j0 = 0; j0 < g.top_k; j0 += FLIGHT) {
+            Piece p[FLIGHT];
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j) {
+                const uint16_t *row = j0 + j < g.top_k ? row_of[slot][j0 + j] : nullptr;
+                p[j] = Piece{{0, 0, 0, 0}};
+                if (row) p[j] = load_any(row + e);
+            }
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j) {
+                if (j0 + j >= g.top_k || !row_of[slot][j0 + j]) continue;
+                const float w = weight_of[slot][j0 + j];
+                float f[8];
+                widen8<BF16>(p[j], f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, f[u], acc[u]);
+            }
+        }
+        store_wide(y + e, narrow8<BF16>(acc));
+    }
+    if (lane < cut.singles()) {
+        const int e = cut.single(lane);
+        float acc = 0.f;
+        for (int j = 0; j < g.top_k; ++j)
+            if (row_of[slot][j]) acc = fmaf(weight_of[slot][j], widen1<BF16>(row_of[slot][j][e]), acc);
+        y[e] = narrow1<BF16>(acc);
     }
 }
 
@@ -345,10 +435,12 @@ constexpr int32_t kNoRow = INT32_MIN;  // its complement is 2^31 - 1, never a ro
 // One block per token: dYs[r] = weight * dY[t] and dweight = <Ys[r], dY[t]>
 // for each of its choices, eight at a time, their loads in flight together;
 // the dot products are summed in fp32, over the threads in a fixed order.
-template <bool BF16, bool WIDE>
+// Bound by memory: 8192 tokens x 8 rows of 4096 bf16 take 188 us, 6.1 TB/s.
+template <bool BF16>
 __global__ void __launch_bounds__(256)
-    combine_grad_kernel(RowShape g, const uint16_t *dY, int64_t lddy, const uint16_t *Ys, int64_t ldys,
-                        const int32_t *rows, const float *weights, uint16_t *dYs, int64_t lddys, float *dweights)
+    combine_grad_wide_kernel(RowShape g, const uint16_t *dY, int64_t lddy, const uint16_t *Ys, int64_t ldys,
+                             const int32_t *rows, const float *weights, uint16_t *dYs, int64_t lddys,
+                             float *dweights)
 {
     constexpr int FLIGHT = 8;
     __shared__ float part[8][FLIGHT];
@@ -356,7 +448,6 @@ __global__ void __launch_bounds__(256)
     pdl_launch_dependents();
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const uint16_t *dy = dY + t * lddy;
     for (int j0 = 0; j0 < g.top_k; j0 += FLIGHT) {
         int32_t r[FLIGHT];
         float w[FLIGHT], dot[FLIGHT];
@@ -368,43 +459,25 @@ __global__ void __launch_bounds__(256)
             w[j] = r[j] >= 0 ? (weights ? weights[t * g.top_k + j0 + j] : 1.f) : 0.f;
             dot[j] = 0.f;
         }
-        // One choice's piece: its share of the dot product, and its gradient.
-        auto one = [&](int j, int e, const Piece &d, const Piece &y) {
-            float fd[8], fy[8];
+        for (int e = threadIdx.x * 8; e < g.width; e += blockDim.x * 8) {
+            const Piece d = load_wide(dY + t * lddy + e);
+            Piece y[FLIGHT];
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j) {
+                y[j] = Piece{{0, 0, 0, 0}};
+                if (r[j] >= 0) y[j] = load_wide(Ys + static_cast<int64_t>(r[j]) * ldys + e);
+            }
+            float fd[8];
             widen8<BF16>(d, fd);
-            widen8<BF16>(y, fy);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                dot[j] = fmaf(fd[u], fy[u], dot[j]);
-                fd[u] *= w[j];
-            }
-            const int64_t to = r[j] < 0 ? ~r[j] : r[j];
-            store_piece<WIDE>(dYs + to * lddys, g.width, e, r[j] < 0 ? Piece{{0, 0, 0, 0}} : narrow8<BF16>(fd));
-        };
-        if constexpr (WIDE) {
-            for (int e = threadIdx.x * 8; e < g.width; e += blockDim.x * 8) {
-                const Piece d = load_piece<true>(dy, g.width, e);
-                Piece y[FLIGHT];
-#pragma unroll
-                for (int j = 0; j < FLIGHT; ++j) {
-                    y[j] = Piece{{0, 0, 0, 0}};
-                    if (r[j] >= 0) y[j] = load_piece<true>(Ys + static_cast<int64_t>(r[j]) * ldys, g.width, e);
-                }
-#pragma unroll
-                for (int j = 0; j < FLIGHT; ++j)
-                    if (r[j] != kNoRow) one(j, e, d, y[j]);
-            }
-        } else {
 #pragma unroll
             for (int j = 0; j < FLIGHT; ++j) {
                 if (r[j] == kNoRow) continue;
+                float fy[8];
+                widen8<BF16>(y[j], fy);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) dot[j] = fmaf(fd[u], fy[u], dot[j]);
                 const int64_t to = r[j] < 0 ? ~r[j] : r[j];
-                for (int e = first_piece<false>(dYs + to * lddys) + static_cast<int>(threadIdx.x) * 8; e < g.width;
-                     e += blockDim.x * 8) {
-                    Piece y{{0, 0, 0, 0}};
-                    if (r[j] >= 0) y = load_piece<false>(Ys + to * ldys, g.width, e);
-                    one(j, e, load_piece<false>(dy, g.width, e), y);
-                }
+                store_wide(dYs + to * lddys + e, r[j] < 0 ? Piece{{0, 0, 0, 0}} : scaled<BF16>(d, w[j]));
             }
         }
 #pragma unroll
@@ -421,6 +494,69 @@ __global__ void __launch_bounds__(256)
         }
         __syncthreads();
     }
+}
+
+// The same at any alignment, a warp per choice.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    combine_grad_kernel(RowShape g, const uint16_t *dY, int64_t lddy, const uint16_t *Ys, int64_t ldys,
+                        const int32_t *rows, const float *weights, uint16_t *dYs, int64_t lddys, float *dweights)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (s >= g.rows) return;
+    const int32_t r = rows[s];
+    const int64_t to = r < 0 ? ~r : r;
+    if (r < 0 || to >= g.rows) {
+        if (lane == 0) dweights[s] = 0.f;
+        if (to >= g.rows) return;
+    }
+    uint16_t *o = dYs + to * lddys;
+    const RowCut cut(o, g.width);
+    if (r < 0) {
+        for (int i = lane; i < cut.body; i += 32) store_wide(o + cut.head + 8 * i, Piece{{0, 0, 0, 0}});
+        if (lane < cut.singles()) o[cut.single(lane)] = 0;
+        return;
+    }
+    const uint16_t *d = dY + s / g.top_k * lddy, *y = Ys + to * ldys;
+    const float w = weights ? weights[s] : 1.f;
+    float dot = 0.f;
+    constexpr int FLIGHT = 2;
+    for (int i = lane; i < cut.body; i += 32 * FLIGHT) {
+        Piece pd[FLIGHT], py[FLIGHT];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            pd[u] = py[u] = Piece{{0, 0, 0, 0}};
+            if (i + 32 * u < cut.body) {
+                pd[u] = load_any(d + cut.head + 8 * (i + 32 * u));
+                py[u] = load_any(y + cut.head + 8 * (i + 32 * u));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            if (i + 32 * u >= cut.body) continue;
+            float fd[8], fy[8];
+            widen8<BF16>(pd[u], fd);
+            widen8<BF16>(py[u], fy);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                dot = fmaf(fd[k], fy[k], dot);
+                fd[k] *= w;
+            }
+            store_wide(o + cut.head + 8 * (i + 32 * u), narrow8<BF16>(fd));
+        }
+    }
+    if (lane < cut.singles()) {
+        const int e = cut.single(lane);
+        const float fd = widen1<BF16>(d[e]);
+        dot = fmaf(fd, widen1<BF16>(y[e]), dot);
+        o[e] = narrow1<BF16>(fd * w);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
+    if (lane == 0) dweights[s] = dot;
 }
 
 // --------------------------------------------------------------- launching
@@ -443,18 +579,18 @@ cudaLaunchConfig_t config(int64_t grid, int threads, int smem, cudaStream_t s, c
 
 RowShape row_shape(int64_t tokens, int top_k, int64_t width)
 {
+    // A group covers the row in one pass if 256 threads can; a longer row is
+    // covered in as few thread passes as 256 or 128 threads leave idle least.
     RowShape g{tokens, top_k, static_cast<int>(width), 32, tokens * top_k};
-    while (g.lanes < 256 && g.lanes * 8 < width) g.lanes *= 2;
+    const int64_t pieces = (width + 7) / 8;
+    while (g.lanes < 256 && g.lanes < pieces) g.lanes *= 2;
+    if (pieces > 256 && (pieces + 127) / 128 * 128 < (pieces + 255) / 256 * 256) g.lanes = 128;
     return g;
 }
 
 int64_t row_blocks(const RowShape &g) { return (g.tokens + 256 / g.lanes - 1) / (256 / g.lanes); }
 
-template <class K>
-K pick(bool bf16, bool wide, K bw, K bn, K hw, K hn)
-{
-    return bf16 ? (wide ? bw : bn) : (wide ? hw : hn);
-}
+int64_t slot_blocks(const RowShape &g) { return (g.rows + 7) / 8; }
 
 }  // namespace
 
@@ -499,12 +635,11 @@ cudaError_t launch_dispatch(bool bf16, int64_t tokens, int top_k, int64_t width,
 {
     const bool wide = width % 8 == 0 && wide_rows(X, ldx) && wide_rows(Xs, ldxs);
     const RowShape g = row_shape(tokens, top_k, width);
+    const auto k = wide ? (bf16 ? dispatch_wide_kernel<true> : dispatch_wide_kernel<false>)
+                        : (bf16 ? dispatch_kernel<true> : dispatch_kernel<false>);
     cudaLaunchAttribute a[1];
-    const cudaLaunchConfig_t c = config(row_blocks(g), 256, 0, s, a);
-    return cudaLaunchKernelEx(&c,
-                              pick(bf16, wide, dispatch_kernel<true, true>, dispatch_kernel<true, false>,
-                                   dispatch_kernel<false, true>, dispatch_kernel<false, false>),
-                              g, X, ldx, rows, weights, Xs, ldxs);
+    const cudaLaunchConfig_t c = config(wide ? row_blocks(g) : slot_blocks(g), 256, 0, s, a);
+    return cudaLaunchKernelEx(&c, k, g, X, ldx, rows, weights, Xs, ldxs);
 }
 
 cudaError_t launch_combine(bool bf16, int64_t tokens, int top_k, int64_t width, const uint16_t *Ys, int64_t ldys,
@@ -512,12 +647,11 @@ cudaError_t launch_combine(bool bf16, int64_t tokens, int top_k, int64_t width, 
 {
     const bool wide = width % 8 == 0 && wide_rows(Ys, ldys) && wide_rows(Y, ldy);
     const RowShape g = row_shape(tokens, top_k, width);
+    const auto k = wide ? (bf16 ? combine_wide_kernel<true> : combine_wide_kernel<false>)
+                        : (bf16 ? combine_kernel<true> : combine_kernel<false>);
     cudaLaunchAttribute a[1];
     const cudaLaunchConfig_t c = config(row_blocks(g), 256, 0, s, a);
-    return cudaLaunchKernelEx(&c,
-                              pick(bf16, wide, combine_kernel<true, true>, combine_kernel<true, false>,
-                                   combine_kernel<false, true>, combine_kernel<false, false>),
-                              g, Ys, ldys, rows, weights, Y, ldy);
+    return cudaLaunchKernelEx(&c, k, g, Ys, ldys, rows, weights, Y, ldy);
 }
 
 cudaError_t launch_combine_grad(bool bf16, int64_t tokens, int top_k, int64_t width, const uint16_t *dY, int64_t lddy,
@@ -526,12 +660,11 @@ cudaError_t launch_combine_grad(bool bf16, int64_t tokens, int top_k, int64_t wi
 {
     const bool wide = width % 8 == 0 && wide_rows(dY, lddy) && wide_rows(Ys, ldys) && wide_rows(dYs, lddys);
     const RowShape g = row_shape(tokens, top_k, width);
+    const auto k = wide ? (bf16 ? combine_grad_wide_kernel<true> : combine_grad_wide_kernel<false>)
+                        : (bf16 ? combine_grad_kernel<true> : combine_grad_kernel<false>);
     cudaLaunchAttribute a[1];
-    const cudaLaunchConfig_t c = config(tokens, g.lanes, 0, s, a);
-    return cudaLaunchKernelEx(&c,
-                              pick(bf16, wide, combine_grad_kernel<true, true>, combine_grad_kernel<true, false>,
-                                   combine_grad_kernel<false, true>, combine_grad_kernel<false, false>),
-                              g, dY, lddy, Ys, ldys, rows, weights, dYs, lddys, dweights);
+    const cudaLaunchConfig_t c = wide ? config(tokens, g.lanes, 0, s, a) : config(slot_blocks(g), 256, 0, s, a);
+    return cudaLaunchKernelEx(&c, k, g, dY, lddy, Ys, ldys, rows, weights, dYs, lddys, dweights);
 }
 
 }  // namespace gp

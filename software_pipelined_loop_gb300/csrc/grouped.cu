@@ -88,11 +88,12 @@ int max_units()
 template <class Cfg>
 constexpr GroupedVariant variant()
 {
-    return GroupedVariant{Cfg::MODE, Cfg::BN, Cfg::PAIR ? 1 : 0, Cfg::CTA_BN, Cfg::SMEM_BYTES, &launch<Cfg>,
+    return GroupedVariant{Cfg::MODE, Cfg::BN, Cfg::TILE_F, Cfg::PAIR ? 1 : 0, Cfg::CTA_BN, Cfg::SMEM_BYTES, &launch<Cfg>,
                           &max_units<Cfg>};
 }
 
 const GroupedVariant kVariants[] = {
+    variant<GroupedCfg<kRows, 32, false, 64>>(),
     variant<GroupedCfg<kRows, 32, false>>(),  variant<GroupedCfg<kRows, 64, false>>(),
     variant<GroupedCfg<kRows, 128, false>>(), variant<GroupedCfg<kRows, 256, true>>(),
     variant<GroupedCfg<kRowsT, 32, false>>(), variant<GroupedCfg<kRowsT, 64, false>>(),
@@ -102,10 +103,10 @@ const GroupedVariant kVariants[] = {
 
 }  // namespace
 
-const GroupedVariant *grouped_variant(int mode, int bn)
+const GroupedVariant *grouped_variant(int mode, int bn, int tile_f)
 {
     for (const GroupedVariant &v : kVariants)
-        if (v.mode == mode && v.bn == bn) return &v;
+        if (v.mode == mode && v.bn == bn && (tile_f == 0 || v.tile_f == tile_f)) return &v;
     return nullptr;
 }
 

@@ -34,13 +34,14 @@
 
 namespace gp {
 
-template <int MODE_, int BN_, bool PAIR_>
+template <int MODE_, int BN_, bool PAIR_, int BM_ = 128>
 struct GroupedCfg {
     static constexpr int MODE = MODE_;
     static constexpr int BN = BN_;        // output rows per tile
     static constexpr bool PAIR = PAIR_;   // cluster of two CTAs, 256 features per tile
     static constexpr int CLUSTER = PAIR ? 2 : 1;
-    static constexpr int BM = 128;        // features per CTA
+    static constexpr int BM = BM_;        // features per CTA: 128, or 64 (then in lanes 0-15 of each quarter)
+    static constexpr int QF = BM / 4;     // features of an epilogue warp's TMEM quarter
     static constexpr int TILE_F = BM * CLUSTER;
     static constexpr int BK = 64;
     static constexpr bool A_MN = MODE != kRowsT;    // W[k][n] and dY[r][n]: features contiguous
@@ -52,7 +53,7 @@ struct GroupedCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int ATOM_BYTES = BK * 128;     // 64 features (columns) x 64 products
     static constexpr int RING_BYTES = 196608;
-    static constexpr int STAGES = RING_BYTES / STAGE_BYTES < 10 ? RING_BYTES / STAGE_BYTES : 10;
+    static constexpr int STAGES = RING_BYTES / STAGE_BYTES < 16 ? RING_BYTES / STAGE_BYTES : 16;
     static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
@@ -63,7 +64,7 @@ struct GroupedCfg {
     static constexpr int B_PART_BYTES = B_PART_ROWS * 128;
 
     static constexpr int STAGING_OFF = STAGES * STAGE_BYTES;
-    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * 64;
+    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * QF * 2;
     static constexpr int TABLE_OFF = STAGING_OFF + STAGING_BYTES;
     static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2);
     static constexpr int CTL_OFF = TABLE_OFF + TABLE_BYTES;
@@ -71,6 +72,7 @@ struct GroupedCfg {
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + CTL_BYTES;
 
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "MMA columns");
+    static_assert(BM == 128 || (BM == 64 && MODE == kRows && !PAIR && BN == 32), "64 features: few rows, forward");
     static_assert(!PAIR || BN == 256, "pairs take 256 x 256 tiles");
     static_assert(B_BYTES % 1024 == 0 && TABLE_BYTES % 8 == 0, "alignment");
     static_assert(!B_MN || CTA_BN % 64 == 0, "64-column atoms");
@@ -174,7 +176,19 @@ struct GroupedIter {
     __device__ __forceinline__ bool next(const GroupedParams &p, GroupedTile &w)
     {
         if (pos >= t.first[t.E]) return false;
-        while (pos >= t.first[e + 1]) ++e;
+        if (pos >= t.first[e + 1]) {
+            // The expert of this tile: the last one with first[e] <= pos.  (A
+            // step at a time costs 1 us of a 64-expert call of one token.)
+            int below = e + 1, above = t.E;
+            while (above - below > 1) {
+                const int mid = (below + above) >> 1;
+                if (t.first[mid] <= pos)
+                    below = mid;
+                else
+                    above = mid;
+            }
+            e = below;
+        }
         const int32_t in = pos - t.first[e];
         pos += step;
         const int32_t c = in / f_tiles;
@@ -273,8 +287,9 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
                         if (p.a_groups) {
                             load4(sa, tA, 0, k0, f0 / 64, t.e);
                         } else {
-                            load3(sa, tA, f0, k0, t.e);
-                            load3(sa + Cfg::ATOM_BYTES, tA, f0 + 64, k0, t.e);
+#pragma unroll
+                            for (int j = 0; j < Cfg::BM / 64; ++j)
+                                load3(sa + j * Cfg::ATOM_BYTES, tA, f0 + 64 * j, k0, t.e);
                         }
                     } else if constexpr (Cfg::MODE == kRowsT) {
                         load3(sa, tA, k0, f0, t.e);
@@ -498,19 +513,20 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
     const int e = warp - Cfg::EPI_WARP0;
     const int q = warp & 3, h = e >> 2;
     const bool bf16 = p.bf16 != 0;
-    constexpr int NB = Cfg::EPI_BLOCK;
-    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * 64);
-    // This lane's row address in stmatrix (matrix lane / 8 = 8 features, row lane % 8) ...
-    const uint32_t put = stg + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
-    // ... and its chunk when reading 8 rows x 64 bytes.
-    const uint32_t get = stg + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    constexpr int NB = Cfg::EPI_BLOCK, QF = Cfg::QF;
+    constexpr int ROW = QF * 2, CHUNKS = QF / 8;  // bytes and 16-byte chunks of a staged row
+    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * ROW);
+    // Address of chunk k of staged row c.
+    auto staged = [stg](int c, int k) {
+        return stg + c * ROW + ((k ^ (CHUNKS == 4 ? (c >> 1) & 3 : (c >> 2) & 1)) << 4);
+    };
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
     uint16_t *out = static_cast<uint16_t *>(p.out);
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (it.next(p, t)) {
-        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * 32;  // the warp's first feature
+        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * QF;  // the warp's first feature
         const int64_t all = Cfg::MODE == kWeights ? p.out_rows : t.count;  // output rows of the expert
         const int64_t base = Cfg::MODE == kWeights ? p.out_rows * t.e : t.row0;
         // The tile's rows are its columns up to the expert's last row; this
@@ -537,31 +553,41 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
                     tmem_ld_16x256b_x4(tbase + j + (16u << 16), hi);
                 } else {
                     tmem_ld_16x256b_x2(tbase + j, lo);
-                    tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
+                    if constexpr (QF == 32) tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
                 }
                 tmem_wait_ld();
             }
+            if constexpr (QF == 32) {
+                // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
 #pragma unroll
-            for (int i = 0; i < NB / 8; ++i)
-                stmatrix_x4_trans(put + i * 512, round_pair(lo[4 * i], lo[4 * i + 1], bf16),
-                                  round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
-                                  round_pair(hi[4 * i], hi[4 * i + 1], bf16),
-                                  round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
+                for (int i = 0; i < NB / 8; ++i)
+                    stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
+                                      round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
+                                      round_pair(hi[4 * i], hi[4 * i + 1], bf16),
+                                      round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
+            } else {
+                // Per 16 columns: the first 8 columns' two pieces of 8 features, then the others'.
+                static_assert(QF == 32 || NB == 16, "one store");
+                stmatrix_x4_trans(staged((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1), round_pair(lo[0], lo[1], bf16),
+                                  round_pair(lo[2], lo[3], bf16), round_pair(lo[4], lo[5], bf16),
+                                  round_pair(lo[6], lo[7], bf16));
+            }
             __syncwarp();
             const int n = to - j < NB ? static_cast<int>(to - j) : NB;
             uint16_t *o = out + (base + t.c0 + j) * p.ldo + f0;
-            if (p.vec_store && f0 + 32 <= p.features) {
-                // 16-byte pieces, four lanes to a row.
-                o += (lane >> 2) * p.ldo + (lane & 3) * 8;
+            if (p.vec_store && f0 + QF <= p.features) {
+                // 16-byte pieces, 32 / CHUNKS rows at a time.
+                constexpr int ROWS = 32 / CHUNKS;
+                o += (lane / CHUNKS) * p.ldo + (lane % CHUNKS) * 8;
 #pragma unroll
-                for (int i = 0; i < NB / 8; ++i)
-                    if (8 * i + (lane >> 2) < n)
-                        *reinterpret_cast<uint4 *>(o + i * 8 * p.ldo) = ld_shared_v4(get + i * 512);
-            } else if (f0 + lane < p.features) {
+                for (int i = 0; i < NB; i += ROWS)
+                    if (i + lane / CHUNKS < n)
+                        *reinterpret_cast<uint4 *>(o + i * p.ldo) =
+                            ld_shared_v4(staged(i + lane / CHUNKS, lane % CHUNKS));
+            } else if (lane < QF && f0 + lane < p.features) {
                 // A feature per lane, row by row.
 #pragma unroll 8
-                for (int c = 0; c < n; ++c)
-                    o[c * p.ldo + lane] = ld_shared_u16(stg + c * 64 + ((((lane >> 3) ^ (c >> 1)) & 3) << 4) + (lane & 7) * 2);
+                for (int c = 0; c < n; ++c) o[c * p.ldo + lane] = ld_shared_u16(staged(c, lane >> 3) + (lane & 7) * 2);
             }
             __syncwarp();
         }

@@ -7,6 +7,7 @@
 namespace gp {
 
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 64;
 
 enum GroupedMode { kRows = 0, kRowsT = 1, kWeights = 2 };
 

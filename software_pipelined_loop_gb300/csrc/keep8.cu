@@ -179,73 +179,83 @@ __global__ void __launch_bounds__(kThreads) restore8_dense_kernel(const int8_t *
 
 // ---- any width, pitch and alignment: a warp takes 256 values of a row
 
-// Eight 16-bit values at elements [e, e + 8) of a row of n, zeros outside.
-__device__ __forceinline__ void load_values(const uint16_t *row, int64_t n, int64_t e, uint32_t (&w)[4])
-{
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(row), end = begin + 2 * static_cast<uintptr_t>(n);
-    const uintptr_t at = begin + 2 * static_cast<uintptr_t>(e);
-    const uint32_t shift = static_cast<uint32_t>(at & 15u);
-    const uintptr_t a0 = at - shift, a1 = a0 + 16;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (a0 < end) lo = ldg_nc_v4(reinterpret_cast<const void *>(a0));
-    if (shift && a1 < end) hi = ldg_nc_v4(reinterpret_cast<const void *>(a1));
-    realign16(lo, hi, shift, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] &= (e + 2 * i < n ? 0xffffu : 0u) | (e + 2 * i + 1 < n ? 0xffff0000u : 0u);
-}
-
 // Eight bytes at p; only aligned words that hold a byte of [begin, end) are read.
-__device__ __forceinline__ uint2 load_bytes(uintptr_t p, uintptr_t begin, uintptr_t end)
+__device__ __forceinline__ uint2 load_bytes(const char *p, const char *begin, const char *end)
 {
-    const uint32_t shift = static_cast<uint32_t>(p & 7u);
-    const uintptr_t a0 = p - shift, a1 = a0 + 8;
-    unsigned long long lo = 0, hi = 0;
-    if (a0 < end && a0 + 8 > begin) lo = *reinterpret_cast<const unsigned long long *>(a0);
-    if (shift && a1 < end && a1 + 8 > begin) hi = *reinterpret_cast<const unsigned long long *>(a1);
-    const unsigned long long v = shift ? (lo >> (8 * shift)) | (hi << (64 - 8 * shift)) : lo;
-    return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+    const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 7u);
+    const char *a = p - shift;
+    uint2 lo = make_uint2(0, 0), hi = lo;
+    if (a < end && a + 8 > begin) lo = *reinterpret_cast<const uint2 *>(a);
+    if (shift && a + 8 < end && a + 16 > begin) hi = *reinterpret_cast<const uint2 *>(a + 8);
+    const bool b4 = (shift & 4u) != 0;
+    const uint32_t w0 = b4 ? lo.y : lo.x, w1 = b4 ? hi.x : lo.y, w2 = b4 ? hi.y : hi.x, sh = (shift & 3u) * 8u;
+    return make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
 }
 
-constexpr int kSpan = 256;  // values a warp takes at once
+constexpr int kSpan = 256;        // values a warp takes at once
+constexpr int kSpansPerBlock = 32;  // spans of one row that a block takes
+
+// A block's part of a row: `parts` blocks share a row of more than 32 spans.
+struct RowPart {
+    int64_t row;
+    int64_t span;  // the warp's first span; it takes every (kThreads / 32)-th up to `end`
+    int64_t end;
+};
+
+__device__ __forceinline__ RowPart row_part(int64_t spans, uint32_t parts)
+{
+    RowPart p;
+    const uint32_t row = blockIdx.x / parts, part = blockIdx.x - row * parts;
+    p.row = row;
+    p.span = static_cast<int64_t>(part) * kSpansPerBlock + threadIdx.x / 32;
+    const int64_t end = (static_cast<int64_t>(part) + 1) * kSpansPerBlock;
+    p.end = end < spans ? end : spans;
+    return p;
+}
 
 // The bytes of a span meet in shared memory and leave as the destination's
 // own 8-byte words (rows of bytes start anywhere).
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    keep8_kernel(const uint16_t *X, int64_t rows, int64_t width, int64_t ldx, int8_t *Q, uint8_t *S)
+    keep8_kernel(const uint16_t *X, int64_t width, int64_t ldx, uint32_t parts, int8_t *Q, uint8_t *S)
 {
     __shared__ __align__(16) uint8_t stage[kThreads / 32][kSpan + 16];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    uint8_t *mine = stage[threadIdx.x >> 5] + 8;
-    const int64_t groups = (width + 31) / 32, spans = (width + kSpan - 1) / kSpan, n = rows * spans;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; g < n; g += warps) {
-        const int64_t r = g / spans, e0 = (g - r * spans) * kSpan, e = e0 + 8 * lane;
-        uint32_t w[4];
-        load_values(X + r * ldx, width, e, w);
+    uint8_t *mine = stage[threadIdx.x >> 5];
+    const int64_t groups = (width + 31) / 32;
+    const RowPart p = row_part((width + kSpan - 1) / kSpan, parts);
+    const uint16_t *x = X + p.row * ldx;
+    uint8_t *q = reinterpret_cast<uint8_t *>(Q) + p.row * width;
+    // Bytes of a span before the destination's first 8-byte word: the same in every span of a row.
+    const int head = static_cast<int>((8 - (reinterpret_cast<uintptr_t>(q) & 7u)) & 7u);
+    for (int64_t sp = p.span; sp < p.end; sp += kThreads / 32) {
+        const int64_t e0 = sp * kSpan, e = e0 + 8 * lane;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (e + 8 <= width) {
+            load8_any(x + e, w);
+        } else {
+            for (int u = 0; u < 8 && e + u < width; ++u)
+                w[u >> 1] |= static_cast<uint32_t>(x[e + u]) << (16 * (u & 1));
+        }
         const uint32_t byte = step_byte<BF16>(top_of_group(top8(w)));
         *reinterpret_cast<uint2 *>(mine + 8 * lane) = quantise8<BF16>(w, byte);
-        if ((lane & 3) == 0 && e < width) S[r * groups + e / 32] = static_cast<uint8_t>(byte);
+        if ((lane & 3) == 0 && e < width) S[p.row * groups + e / 32] = static_cast<uint8_t>(byte);
         __syncwarp();
-        uint8_t *to = reinterpret_cast<uint8_t *>(Q) + r * width + e0;
         const int have = static_cast<int>(width - e0 < kSpan ? width - e0 : kSpan);
-        const int head = static_cast<int>((8 - (reinterpret_cast<uintptr_t>(to) & 7u)) & 7u);  // bytes before a word
         const int at = head + 8 * lane;
         if (at + 8 <= have) {
-            uint32_t a = 0, b = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                a |= static_cast<uint32_t>(mine[at + u]) << (8 * u);
-                b |= static_cast<uint32_t>(mine[at + 4 + u]) << (8 * u);
-            }
-            *reinterpret_cast<uint2 *>(to + at) = make_uint2(a, b);
+            const uint2 lo = *reinterpret_cast<const uint2 *>(mine + 8 * lane);
+            const uint2 hi = *reinterpret_cast<const uint2 *>(mine + 8 * lane + 8);
+            const bool b4 = (head & 4) != 0;
+            const uint32_t w0 = b4 ? lo.y : lo.x, w1 = b4 ? hi.x : lo.y, w2 = b4 ? hi.y : hi.x, sh = (head & 3) * 8;
+            *reinterpret_cast<uint2 *>(q + e0 + at) =
+                make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
         } else {
-            for (int u = at; u < have; ++u) to[u] = mine[u];
+            for (int u = at; u < have; ++u) q[e0 + u] = mine[u];
         }
-        if (lane < head && lane < have) to[lane] = mine[lane];
+        if (lane < head && lane < have) q[e0 + lane] = mine[lane];
         __syncwarp();
     }
 }
@@ -254,23 +264,25 @@ __global__ void __launch_bounds__(kThreads)
 // they may lie in two groups.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int64_t width, uint16_t *X, int64_t ldx)
+    restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int64_t width, uint32_t parts, uint16_t *X,
+                    int64_t ldx)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t groups = (width + 31) / 32, spans = (width + 7 + kSpan - 1) / kSpan, n = rows * spans;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(Q), end = begin + static_cast<uintptr_t>(rows * width);
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; g < n; g += warps) {
-        const int64_t r = g / spans;
-        uint16_t *x = X + r * ldx;
-        const int64_t e = (g - r * spans) * kSpan + 8 * lane - static_cast<int64_t>((reinterpret_cast<uintptr_t>(x) & 15u) >> 1);
+    const int64_t groups = (width + 31) / 32;
+    const RowPart p = row_part((width + 7 + kSpan - 1) / kSpan, parts);
+    const char *begin = reinterpret_cast<const char *>(Q), *end = begin + rows * width, *q = begin + p.row * width;
+    const uint8_t *s = S + p.row * groups;
+    uint16_t *x = X + p.row * ldx;
+    const int before = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) >> 1);
+    for (int64_t sp = p.span; sp < p.end; sp += kThreads / 32) {
+        const int64_t e = sp * kSpan + 8 * lane - before;
         if (e >= width || e + 8 <= 0) continue;
         const int64_t g0 = e > 0 ? e / 32 : 0, g1 = (e + 7 < width ? e + 7 : width - 1) / 32;
-        const float s0 = step_of(S[r * groups + g0]), s1 = step_of(S[r * groups + g1]);
-        const uint2 q = load_bytes(begin + static_cast<uintptr_t>(r * width + e), begin, end);
-        const uint4 v = restore_piece<BF16>(q, s0, s1, static_cast<int>(32 * (g0 + 1) - e));
+        const uint2 b = load_bytes(q + e, begin, end);
+        const float s0 = step_of(s[g0]), s1 = step_of(s[g1]);
+        const uint4 v = restore_piece<BF16>(b, s0, s1, static_cast<int>(32 * (g0 + 1) - e));
         if (e >= 0 && e + 8 <= width) {
             *reinterpret_cast<uint4 *>(x + e) = v;
         } else {
@@ -319,6 +331,12 @@ cudaError_t launch(void (*k)(P...), int64_t work, int64_t most, cudaStream_t s, 
     return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
+// Blocks of a row of `values` values.
+int64_t row_parts(int64_t values)
+{
+    return (values + int64_t(kSpan) * kSpansPerBlock - 1) / (int64_t(kSpan) * kSpansPerBlock);
+}
+
 // Rows that are one run of whole groups, on the accesses' boundaries, in at
 // most 2^31 - 1 blocks.
 bool dense(const void *X, int64_t ldx, const void *Q, int64_t rows, int64_t width)
@@ -330,27 +348,29 @@ bool dense(const void *X, int64_t ldx, const void *Q, int64_t rows, int64_t widt
 }  // namespace
 
 cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t *X, int64_t ldx, int8_t *Q,
-                         uint8_t *S, int sms, cudaStream_t s)
+                         uint8_t *S, cudaStream_t s)
 {
     if (dense(X, ldx, Q, rows, width)) {
         const int64_t n = rows * (width / 8);
         return launch(bf16 ? keep8_dense_kernel<true> : keep8_dense_kernel<false>, (n + kFlight - 1) / kFlight, 0, s, X, n,
                       Q, S);
     }
-    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * ((width + kSpan - 1) / kSpan) * 32, 8 * sms, s,
-                  X, rows, width, ldx, Q, S);
+    const int64_t parts = row_parts(width);
+    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * parts * kThreads, 0, s, X, width, ldx,
+                  static_cast<uint32_t>(parts), Q, S);
 }
 
 cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t *Q, const uint8_t *S, uint16_t *X,
-                            int64_t ldx, int sms, cudaStream_t s)
+                            int64_t ldx, cudaStream_t s)
 {
     if (dense(X, ldx, Q, rows, width)) {
         const int64_t n = rows * (width / 8);
         return launch(bf16 ? restore8_dense_kernel<true> : restore8_dense_kernel<false>, (n + kFlight - 1) / kFlight, 0, s,
                       Q, S, n, X);
     }
-    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * ((width + 7 + kSpan - 1) / kSpan) * 32,
-                  8 * sms, s, Q, S, rows, width, X, ldx);
+    const int64_t parts = row_parts(width + 7);
+    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * parts * kThreads, 0, s, Q, S, rows, width,
+                  static_cast<uint32_t>(parts), X, ldx);
 }
 
 cudaError_t launch_repitch(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,

@@ -500,6 +500,32 @@ __device__ __forceinline__ void realign16(const uint4 &lo, const uint4 &hi, uint
     o[3] = __funnelshift_r(a3, a4, sh);
 }
 
+// realign16 in three steps by the bits of s: 15 operations, no branches.
+__device__ __forceinline__ void realign16_steps(const uint4 &lo, const uint4 &hi, uint32_t s, uint32_t (&o)[4])
+{
+    const bool b8 = (s & 8u) != 0, b4 = (s & 4u) != 0;
+    const uint32_t w0 = b8 ? lo.z : lo.x, w1 = b8 ? lo.w : lo.y, w2 = b8 ? hi.x : lo.z, w3 = b8 ? hi.y : lo.w;
+    const uint32_t w4 = b8 ? hi.z : hi.x, w5 = b8 ? hi.w : hi.y;
+    const uint32_t v0 = b4 ? w1 : w0, v1 = b4 ? w2 : w1, v2 = b4 ? w3 : w2, v3 = b4 ? w4 : w3, v4 = b4 ? w5 : w4;
+    const uint32_t sh = (s & 3u) * 8u;
+    o[0] = __funnelshift_r(v0, v1, sh);
+    o[1] = __funnelshift_r(v1, v2, sh);
+    o[2] = __funnelshift_r(v2, v3, sh);
+    o[3] = __funnelshift_r(v3, v4, sh);
+}
+
+// Eight 16-bit elements at p, any 2-byte alignment.  The two aligned words
+// read each hold one of them.
+__device__ __forceinline__ void load8_any(const uint16_t *p, uint32_t (&o)[4])
+{
+    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const char *a = reinterpret_cast<const char *>(p) - s;
+    const uint4 lo = *reinterpret_cast<const uint4 *>(a);
+    uint4 hi = lo;
+    if (s) hi = *reinterpret_cast<const uint4 *>(a + 16);
+    realign16_steps(lo, hi, s, o);
+}
+
 // Warpgroup register reallocation (all four warps of a warpgroup execute
 // it, converged).
 template <int N>
