@@ -36,6 +36,10 @@ gemmpipe_status_t api_launch(bool gemm, cudaStream_t s, int kernels, F f)
         gemm, s, kernels, [](void *c) { return (*static_cast<F *>(c))(); }, &f);
 }
 
+// The k-block of the armed test stall (-1: none), whose time limit replaces
+// *timeout_ns; consumes the hook.
+int64_t api_take_stall(uint64_t *timeout_ns);
+
 // Tiled tensor map of 16-bit elements in the 128-byte swizzle: dims and box
 // from the innermost, strides (bytes) of dims 1 .. rank - 1, zero fill
 // outside.

@@ -79,17 +79,35 @@ bool tma_ok(const void *p, int64_t ld) { return !misaligned(p, 16) && ld % 8 == 
 int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Copy of `rows` rows of an operand that TMA cannot describe, in the
-// workspace at `to` with the pitch rounded up to 16 bytes.
-gemmpipe_status_t pad_rows(Rows *r, int64_t rows, uint16_t *to, const ApiDevice &d, cudaStream_t s)
+// An operand that TMA cannot describe, to be copied to `to` in the workspace
+// with its pitch rounded up to 16 bytes.
+struct Pad {
+    const uint16_t *from;
+    int64_t rows, width, ld;
+    uint16_t *to;
+};
+
+// Dense operands go two to a launch: 16372 rows and 24 x 4107 weight rows of
+// 1001 columns in 73 us, 82 us one by one.
+gemmpipe_status_t pad_operands(Pad *pads, int n, const ApiDevice &d, cudaStream_t s)
 {
-    const Rows from = *r;
-    r->p = to;
-    r->ld = round8(from.width);
+    gemmpipe_status_t st = GEMMPIPE_OK;
+    int dense = 0;
+    for (int i = 0; i < n && st == GEMMPIPE_OK; ++i) {
+        const Pad p = pads[i];
+        if (p.ld == p.width) {
+            pads[dense++] = p;
+        } else {
+            st = gp::api_launch(false, s, 1, [&] {
+                return gp::launch_repitch(p.from, p.rows, p.width, p.ld, p.to, round8(p.width), d.sms, s);
+            });
+        }
+    }
+    if (dense == 0 || st != GEMMPIPE_OK) return st;
+    const Pad a = pads[0], b = dense > 1 ? pads[1] : Pad{a.from, 0, 0, 0, a.to};
     return gp::api_launch(false, s, 1, [&] {
-        if (from.ld == from.width)
-            return gp::launch_pad_f16(from.p, rows, from.width, to, r->ld, from.p, 0, 0, to, 8, d.sms, s);
-        return gp::launch_repitch(from.p, rows, from.width, from.ld, to, r->ld, d.sms, s);
+        return gp::launch_pad_f16(a.from, a.rows, a.width, a.to, round8(a.width), b.from, b.rows, b.width, b.to,
+                                  dense > 1 ? round8(b.width) : 8, d.sms, s);
     });
 }
 
@@ -176,10 +194,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     const int bn = weights ? 256 : rows_per_tile(q.R, q.E);
     // Tiles of all experts, at most (the bounds are on the device).
     const int64_t row_tiles = weights ? q.E * ((q.K + bn - 1) / bn) : q.R / bn + (q.R < q.E ? q.R : q.E);
-    // 64-feature tiles where 128-feature ones would leave SMs without one:
-    // the weights then stream through twice as many.
-    const bool narrow = q.mode == gp::kRows && bn == 32 && row_tiles * ((features + 127) / 128) < d.sms;
-    const GroupedVariant *v = gp::grouped_variant(q.mode, bn, bn == 256 ? 256 : (narrow ? 64 : 128));
+    const GroupedVariant *v = gp::grouped_variant(q.mode, bn);
     if (!v) return GEMMPIPE_ERR_INTERNAL;
     if (v->smem_bytes > d.smem_optin) return GEMMPIPE_ERR_UNSUPPORTED_DEVICE;
     const int64_t f_tiles = (features + v->tile_f - 1) / v->tile_f;
@@ -198,51 +213,49 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     if (need_x + need_g + need_w > 0) {
         void *ws = nullptr;
         if ((st = gp::api_workspace(d.dev, s, need_x + need_g + need_w, &ws)) != GEMMPIPE_OK) return st;
-        uint16_t *to = static_cast<uint16_t *>(ws);
+        uint16_t *to_x = static_cast<uint16_t *>(ws), *to_g = to_x + need_x / 2, *to_w = to_g + need_g / 2;
+        Pad pads[2];  // of a rows product X or dY, and W; of a weight gradient X and dY
+        int n = 0;
+        if (pad_x) pads[n++] = Pad{q.rows.p, q.R, q.rows.width, q.rows.ld, to_x};
+        if (pad_g) pads[n++] = Pad{q.grad.p, q.R, q.grad.width, q.grad.ld, to_g};
+        if (pad_w) pads[n++] = Pad{q.W, q.E * q.K, q.N, q.N, to_w};
+        if ((st = pad_operands(pads, n, d, s)) != GEMMPIPE_OK) return st;
         if (q.Q) {
-            q.rows.p = to;
-            q.rows.ld = round8(q.rows.width);
             st = gp::api_launch(false, s, 1, [&] {
-                return gp::launch_restore8(bf16, q.R, q.K, q.Q, q.S, to, q.rows.ld, s);
+                return gp::launch_restore8(bf16, q.R, q.K, q.Q, q.S, to_x, round8(q.K), s);
             });
             if (st != GEMMPIPE_OK) return st;
-        } else if (pad_x && (st = pad_rows(&q.rows, q.R, to, d, s)) != GEMMPIPE_OK) {
-            return st;
         }
-        to += need_x / 2;
-        if (pad_g && (st = pad_rows(&q.grad, q.R, to, d, s)) != GEMMPIPE_OK) return st;
-        to += need_g / 2;
-        if (pad_w) {
-            Rows w{q.W, q.N, q.N};
-            if ((st = pad_rows(&w, q.E * q.K, to, d, s)) != GEMMPIPE_OK) return st;
-            W = to;
-        }
+        if (need_x) q.rows = Rows{to_x, q.rows.width, round8(q.rows.width)};
+        if (pad_g) q.grad = Rows{to_g, q.grad.width, round8(q.grad.width)};
+        if (pad_w) W = to_w;
     }
 
     GroupedParams p;
     std::memset(&p, 0, sizeof(p));
-    CUtensorMap ta, tb, tp;  // tp: the row operand in short copies
-    std::memset(&ta, 0, sizeof(ta));
-    std::memset(&tb, 0, sizeof(tb));
-    std::memset(&tp, 0, sizeof(tp));
+    gp::GroupedMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    CUtensorMap *m = maps.m;
     bool ok = true;
-    if (q.mode == gp::kRows) {
-        p.a_groups = q.N % 64 == 0 && v->tile_f >= 128;
-        ok = (p.a_groups ? encode_weight_groups(&ta, bf16, W, q.E, q.K, q.N, wld)
-                         : encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 64)) &&
-             encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn) && encode_rows(&tp, bf16, q.rows, q.R, 32);
-        p.depth = q.K;
-    } else if (q.mode == gp::kRowsT) {
-        ok = encode_weights(&ta, bf16, W, q.E, q.K, q.N, wld, 128) &&
-             encode_rows(&tb, bf16, q.rows, q.R, v->cta_bn) && encode_rows(&tp, bf16, q.rows, q.R, 32);
-        p.depth = q.N;
-    } else {
+    if (weights) {
         p.a_groups = q.grad.width % 64 == 0;
         p.b_groups = q.rows.width % 64 == 0;
-        ok = (p.a_groups ? encode_row_groups(&ta, bf16, q.grad, q.R, 2) : encode_rows(&ta, bf16, q.grad, q.R, 64)) &&
-             (p.b_groups ? encode_row_groups(&tb, bf16, q.rows, q.R, v->cta_bn / 64)
-                         : encode_rows(&tb, bf16, q.rows, q.R, 64));
+        ok = (p.a_groups ? encode_row_groups(&m[gp::kMapA], bf16, q.grad, q.R, 2)
+                         : encode_rows(&m[gp::kMapA], bf16, q.grad, q.R, 64)) &&
+             (p.b_groups ? encode_row_groups(&m[gp::kMapB], bf16, q.rows, q.R, v->cta_bn / 64)
+                         : encode_rows(&m[gp::kMapB], bf16, q.rows, q.R, 64));
+        const uint32_t last[2] = {4, 1};
+        for (int i = 0; i < 2 && ok; ++i)
+            ok = encode_rows(&m[gp::kMapALast + i], bf16, q.grad, q.R, last[i]) &&
+                 encode_rows(&m[gp::kMapBLast + i], bf16, q.rows, q.R, last[i]);
         p.out_rows = q.K;
+    } else {
+        p.a_groups = q.mode == gp::kRows && q.N % 64 == 0;
+        ok = (p.a_groups ? encode_weight_groups(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld)
+                         : encode_weights(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, q.mode == gp::kRows ? 64 : 128)) &&
+             encode_rows(&m[gp::kMapB], bf16, q.rows, q.R, v->cta_bn) &&
+             encode_rows(&m[gp::kMapBPart], bf16, q.rows, q.R, 32);
+        p.depth = q.mode == gp::kRows ? q.K : q.N;
     }
     if (!ok) return GEMMPIPE_ERR_INTERNAL;
     p.offsets = q.offsets;
@@ -253,8 +266,8 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     p.ldo = q.ldo;
     p.bf16 = bf16 ? 1 : 0;
     p.vec_store = tma_ok(q.out, q.ldo) ? 1 : 0;
-    p.stall_kb = -1;
     p.timeout_ns = 2000000000ull + static_cast<uint64_t>((weights ? q.R : p.depth) / 64 + 1) * 10000ull;
+    p.stall_kb = gp::api_take_stall(&p.timeout_ns);
     if (gp::status_word(&p.status) != cudaSuccess) {
         cudaGetLastError();
         return GEMMPIPE_ERR_LAUNCH;
@@ -262,7 +275,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     const int64_t units = v->max_units(), tiles = row_tiles * f_tiles;
     if (units < 1) return GEMMPIPE_ERR_LAUNCH;
     const int grid = static_cast<int>((v->pair ? 2 : 1) * (tiles < units ? tiles : units));
-    return gp::api_launch(true, s, 1, [&] { return v->launch(ta, tb, tp, p, grid, s); });
+    return gp::api_launch(true, s, 1, [&] { return v->launch(maps, p, grid, s); });
 }
 
 // Sizes common to the grouped products.

@@ -818,6 +818,15 @@ gemmpipe_status_t api_timed_launch(bool gemm, cudaStream_t s, int kernels, cudaE
     return GEMMPIPE_OK;
 }
 
+int64_t api_take_stall(uint64_t *timeout_ns)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    const StallHook h = g_stall;
+    if (h.kb >= 0) *timeout_ns = static_cast<uint64_t>(h.timeout_ms) * 1000000ull;
+    g_stall = StallHook();
+    return h.kb;
+}
+
 bool api_encode_16bit(CUtensorMap *m, bool bf16, int rank, const void *base, const uint64_t *dims,
                       const uint64_t *strides, const uint32_t *box)
 {

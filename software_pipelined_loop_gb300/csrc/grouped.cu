@@ -43,7 +43,7 @@ void configure(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid
 }
 
 template <class Cfg>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &bpart, const GroupedParams &p, int grid, cudaStream_t s)
+cudaError_t launch(const GroupedMaps &maps, const GroupedParams &p, int grid, cudaStream_t s)
 {
     int dev = 0;
     cudaError_t e = prepare<Cfg>(&dev);
@@ -51,7 +51,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     configure<Cfg>(cfg, attr, grid, s);
-    e = cudaLaunchKernelEx(&cfg, grouped_kernel<Cfg>, a, b, bpart, p);
+    e = cudaLaunchKernelEx(&cfg, grouped_kernel<Cfg>, maps, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -93,7 +93,6 @@ constexpr GroupedVariant variant()
 }
 
 const GroupedVariant kVariants[] = {
-    variant<GroupedCfg<kRows, 32, false, 64>>(),
     variant<GroupedCfg<kRows, 32, false>>(),  variant<GroupedCfg<kRows, 64, false>>(),
     variant<GroupedCfg<kRows, 128, false>>(), variant<GroupedCfg<kRows, 256, true>>(),
     variant<GroupedCfg<kRowsT, 32, false>>(), variant<GroupedCfg<kRowsT, 64, false>>(),
@@ -103,10 +102,10 @@ const GroupedVariant kVariants[] = {
 
 }  // namespace
 
-const GroupedVariant *grouped_variant(int mode, int bn, int tile_f)
+const GroupedVariant *grouped_variant(int mode, int bn)
 {
     for (const GroupedVariant &v : kVariants)
-        if (v.mode == mode && v.bn == bn && (tile_f == 0 || v.tile_f == tile_f)) return &v;
+        if (v.mode == mode && v.bn == bn) return &v;
     return nullptr;
 }
 

@@ -20,11 +20,15 @@
 // gemm_kernel.cuh: a producer warp filling stages of 64 products by TMA, an
 // MMA warp, and two epilogue warpgroups on double-buffered accumulators.
 //
-// Weight gradient: the summed dimension is the expert's rows, so the last
-// 64-row stage of an expert holds rows of the next one (or unused ones,
-// which may be NaN).  MMAs run only over the 16-row steps that hold a row of
-// the expert, and a warp clears the rest of the last step's rows in both
-// operands before the MMA reads them.
+// Weight gradient: the summed dimension is the expert's rows, and the 16 rows
+// of an MMA step must all be its own (the next expert's, or unused ones, may
+// be NaN).  The ring holds the expert's whole 16-row steps; its last 1 to 15
+// rows go to a 16-row buffer of their own, in pieces of 4 rows and 1 row, the
+// rows past the last one from outside the tensor, which reads as zeros.  A
+// warp of its own loads that buffer as soon as the previous tile has left it,
+// a whole tile ahead: these rows in the ring, whether cleared there by a warp
+// or loaded in pieces, held the MMAs up for 0.9 us a tile (8192 tokens x 4 on
+// 32 experts, 4096 x 1536: 309 us).
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -34,14 +38,13 @@
 
 namespace gp {
 
-template <int MODE_, int BN_, bool PAIR_, int BM_ = 128>
+template <int MODE_, int BN_, bool PAIR_>
 struct GroupedCfg {
     static constexpr int MODE = MODE_;
     static constexpr int BN = BN_;        // output rows per tile
     static constexpr bool PAIR = PAIR_;   // cluster of two CTAs, 256 features per tile
     static constexpr int CLUSTER = PAIR ? 2 : 1;
-    static constexpr int BM = BM_;        // features per CTA: 128, or 64 (then in lanes 0-15 of each quarter)
-    static constexpr int QF = BM / 4;     // features of an epilogue warp's TMEM quarter
+    static constexpr int BM = 128;        // features per CTA
     static constexpr int TILE_F = BM * CLUSTER;
     static constexpr int BK = 64;
     static constexpr bool A_MN = MODE != kRowsT;    // W[k][n] and dY[r][n]: features contiguous
@@ -63,16 +66,20 @@ struct GroupedCfg {
     static constexpr int B_PART_ROWS = 32;          // rows of one short copy of the row operand
     static constexpr int B_PART_BYTES = B_PART_ROWS * 128;
 
-    static constexpr int STAGING_OFF = STAGES * STAGE_BYTES;
-    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * QF * 2;
+    static constexpr int LAST_ROWS = 16;            // weight gradient: rows of an expert's last MMA step
+    static constexpr int LAST_ATOM_BYTES = LAST_ROWS * 128;
+    static constexpr int LAST_BYTES = MODE == kWeights ? STAGE_BYTES / BK * LAST_ROWS : 0;
+    static constexpr int LAST_OFF = STAGES * STAGE_BYTES;
+
+    static constexpr int STAGING_OFF = LAST_OFF + LAST_BYTES;
+    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * 64;
     static constexpr int TABLE_OFF = STAGING_OFF + STAGING_BYTES;
     static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2);
     static constexpr int CTL_OFF = TABLE_OFF + TABLE_BYTES;
-    static constexpr int CTL_BYTES = 8 * (4 * STAGES + 5) + 32;
+    static constexpr int CTL_BYTES = 8 * (2 * STAGES + 7) + 16;
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + CTL_BYTES;
 
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "MMA columns");
-    static_assert(BM == 128 || (BM == 64 && MODE == kRows && !PAIR && BN == 32), "64 features: few rows, forward");
     static_assert(!PAIR || BN == 256, "pairs take 256 x 256 tiles");
     static_assert(B_BYTES % 1024 == 0 && TABLE_BYTES % 8 == 0, "alignment");
     static_assert(!B_MN || CTA_BN % 64 == 0, "64-column atoms");
@@ -83,8 +90,8 @@ template <int STAGES>
 struct GroupedCtl {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
-    uint64_t raw[STAGES];    // weight gradient: an expert's last stage has landed in this CTA
-    uint64_t peer[STAGES];   // ... and is cleared in the pair's other CTA (on the leader)
+    uint64_t last_full;   // weight gradient: the buffer of an expert's last rows
+    uint64_t last_empty;
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
@@ -154,8 +161,9 @@ struct GroupedTile {
     int32_t f0;      // first feature of the tile
     int32_t c0;      // first output row of the tile, within the expert
     int32_t cols;    // the MMA's columns: the tile's output rows, rounded up
-    int32_t kbs;     // k-blocks
-    int32_t last;    // products in the last k-block (1 .. 64)
+    int32_t kbs;     // k-blocks in the ring
+    int32_t last;    // products in the last of them (1 .. 64)
+    int32_t extra;   // weight gradient: rows past the last whole 16 (0 .. 15)
 };
 
 // Tiles of a unit (CTA or pair): round-robin, experts in order, features
@@ -205,36 +213,72 @@ struct GroupedIter {
             const int32_t left = w.count - w.c0;
             w.cols = left < Cfg::BN ? (left + Cfg::N_UNIT - 1) / Cfg::N_UNIT * Cfg::N_UNIT : Cfg::BN;
         }
-        const int64_t depth = Cfg::MODE == kWeights ? w.count : p.depth;
+        w.extra = Cfg::MODE == kWeights ? w.count & (Cfg::LAST_ROWS - 1) : 0;
+        const int64_t depth = Cfg::MODE == kWeights ? w.count - w.extra : p.depth;
         w.kbs = static_cast<int32_t>((depth + Cfg::BK - 1) / Cfg::BK);
         w.last = static_cast<int32_t>(depth - static_cast<int64_t>(w.kbs - 1) * Cfg::BK);
         return true;
     }
 };
 
-// An expert's last stage holds rows that are not its own within an MMA's 16.
-template <class Cfg>
-__device__ __forceinline__ bool has_stray_rows(const GroupedTile &w, int32_t kb)
-{
-    return Cfg::MODE == kWeights && kb == w.kbs - 1 && (w.last & 15) != 0;
-}
-
 // --------------------------------------------------------------- producer
 
 template <class Cfg>
-__device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, const CUtensorMap *tB,
-                                 const CUtensorMap *tBpart, uint32_t sbase, GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w,
-                                 uint32_t rank)
+struct TileLoader {
+    uint32_t bar;  // shared::cluster address for pairs
+
+    __device__ __forceinline__ void load4(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z,
+                                          int32_t v) const
+    {
+        if constexpr (Cfg::PAIR)
+            tma_load_4d_pair(dst, m, bar, x, y, z, v);
+        else
+            tma_load_4d(dst, m, bar, x, y, z, v);
+    }
+    __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z) const
+    {
+        if constexpr (Cfg::PAIR)
+            tma_load_3d_pair(dst, m, bar, x, y, z);
+        else
+            tma_load_3d(dst, m, bar, x, y, z);
+    }
+    __device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y) const
+    {
+        if constexpr (Cfg::PAIR)
+            tma_load_2d_pair(dst, m, bar, x, y);
+        else
+            tma_load_2d(dst, m, bar, x, y);
+    }
+
+    // `rows` (1 .. 15) rows of 64 elements from (x, y) and zeros up to 16
+    // rows: maps of 4- and 1-row boxes, `outside` the first row past the
+    // tensor.  (The swizzle goes by the address, so pieces of any number of
+    // rows land where one box would put them.)
+    __device__ __forceinline__ void load_last_rows(uint32_t dst, const CUtensorMap *m4, const CUtensorMap *m1,
+                                                   int32_t x, int32_t y, int32_t rows, int32_t outside) const
+    {
+        for (int32_t r = 0; r < Cfg::LAST_ROWS; r += 4) {
+            if (r + 4 <= rows || r >= rows) {
+                load2(dst + r * 128, m4, x, r < rows ? y + r : outside);
+            } else {
+                for (int32_t i = r; i < r + 4; ++i) load2(dst + i * 128, m1, x, i < rows ? y + i : outside);
+            }
+        }
+    }
+};
+
+template <class Cfg>
+__device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps, uint32_t sbase,
+                                 GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, uint32_t rank)
 {
+    const CUtensorMap *tA = &maps.m[kMapA], *tB = &maps.m[kMapB];
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t armed = 0, armed_par = 0, raw_armed = 0, raw_par = 0;
+    uint32_t armed = 0, armed_par = 0;
     int64_t kb_count = 0;
     bool ok = true;
     const uint32_t full0 = smem_u32(&ctl->full[0]);
     const uint32_t full0_leader = Cfg::PAIR ? mapa_shared(full0, 0) : full0;
-    const uint32_t raw0 = smem_u32(&ctl->raw[0]);
-    const uint32_t raw0_self = Cfg::PAIR ? mapa_shared(raw0, rank) : raw0;
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (ok && it.next(p, t)) {
@@ -244,88 +288,58 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
         // rows as hold the tile's columns when that is a quarter less.
         const int32_t parts = (t.cols / Cfg::CLUSTER + Cfg::B_PART_ROWS - 1) / Cfg::B_PART_ROWS;
         const bool whole = Cfg::MODE == kWeights || parts * Cfg::B_PART_ROWS >= Cfg::CTA_BN;
-        const uint32_t bytes = Cfg::A_BYTES + (whole ? Cfg::B_BYTES : parts * Cfg::B_PART_BYTES);
         for (int32_t kb = 0; kb < t.kbs; ++kb, ++kb_count) {
             if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->empty[stage]), phase ^ 1u))) {
                 ok = false;
                 break;
             }
             if (!(blockIdx.x == 0 && kb_count == p.stall_kb)) {
-                const bool stray = has_stray_rows<Cfg>(t, kb);
+                const uint32_t so = 8u * static_cast<uint32_t>(stage);
+                const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::A_BYTES;
+                const int32_t k0 = kb * Cfg::BK;
+                const TileLoader<Cfg> ld{full0_leader + so};
                 if (elect_one_sync()) {
-                    const uint32_t so = 8u * static_cast<uint32_t>(stage);
-                    const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::A_BYTES;
-                    const int32_t k0 = kb * Cfg::BK;
-                    uint32_t bar;
-                    if (stray) {
-                        mbar_arrive_expect_tx(raw0 + so, Cfg::STAGE_BYTES);
-                        bar = raw0_self + so;
-                    } else {
-                        if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * bytes);
-                        bar = full0_leader + so;
-                    }
-                    auto load4 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z, int32_t v) {
-                        if constexpr (Cfg::PAIR)
-                            tma_load_4d_pair(dst, m, bar, x, y, z, v);
-                        else
-                            tma_load_4d(dst, m, bar, x, y, z, v);
-                    };
-                    auto load3 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
-                        if constexpr (Cfg::PAIR)
-                            tma_load_3d_pair(dst, m, bar, x, y, z);
-                        else
-                            tma_load_3d(dst, m, bar, x, y, z);
-                    };
-                    auto load2 = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y) {
-                        if constexpr (Cfg::PAIR)
-                            tma_load_2d_pair(dst, m, bar, x, y);
-                        else
-                            tma_load_2d(dst, m, bar, x, y);
-                    };
+                    const uint32_t bytes = Cfg::A_BYTES + (whole ? Cfg::B_BYTES : parts * Cfg::B_PART_BYTES);
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * bytes);
                     if constexpr (Cfg::MODE == kRows) {
                         // W[e]: 64 products x 128 features, two 64-feature atoms.
                         if (p.a_groups) {
-                            load4(sa, tA, 0, k0, f0 / 64, t.e);
+                            ld.load4(sa, tA, 0, k0, f0 / 64, t.e);
                         } else {
-#pragma unroll
-                            for (int j = 0; j < Cfg::BM / 64; ++j)
-                                load3(sa + j * Cfg::ATOM_BYTES, tA, f0 + 64 * j, k0, t.e);
+                            ld.load3(sa, tA, f0, k0, t.e);
+                            ld.load3(sa + Cfg::ATOM_BYTES, tA, f0 + 64, k0, t.e);
                         }
                     } else if constexpr (Cfg::MODE == kRowsT) {
-                        load3(sa, tA, k0, f0, t.e);
+                        ld.load3(sa, tA, k0, f0, t.e);
                     } else {
                         if (p.a_groups) {
-                            load3(sa, tA, 0, t.row0 + k0, f0 / 64);
+                            ld.load3(sa, tA, 0, t.row0 + k0, f0 / 64);
                         } else {
-                            load2(sa, tA, f0, t.row0 + k0);
-                            load2(sa + Cfg::ATOM_BYTES, tA, f0 + 64, t.row0 + k0);
+                            ld.load2(sa, tA, f0, t.row0 + k0);
+                            ld.load2(sa + Cfg::ATOM_BYTES, tA, f0 + 64, t.row0 + k0);
                         }
                         if (p.b_groups) {
-                            load3(sb, tB, 0, t.row0 + k0, c0 / 64);
+                            ld.load3(sb, tB, 0, t.row0 + k0, c0 / 64);
                         } else {
 #pragma unroll
                             for (int j = 0; j < Cfg::CTA_BN / 64; ++j)
-                                load2(sb + j * Cfg::ATOM_BYTES, tB, c0 + 64 * j, t.row0 + k0);
+                                ld.load2(sb + j * Cfg::ATOM_BYTES, tB, c0 + 64 * j, t.row0 + k0);
                         }
                     }
                     if constexpr (Cfg::MODE != kWeights) {
                         if (whole) {
-                            load2(sb, tB, k0, t.row0 + c0);
+                            ld.load2(sb, tB, k0, t.row0 + c0);
                         } else {
                             for (int32_t j = 0; j < parts; ++j)
-                                load2(sb + j * Cfg::B_PART_BYTES, tBpart, k0, t.row0 + c0 + j * Cfg::B_PART_ROWS);
+                                ld.load2(sb + j * Cfg::B_PART_BYTES, &maps.m[kMapBPart], k0,
+                                         t.row0 + c0 + j * Cfg::B_PART_ROWS);
                         }
                     }
                 }
                 __syncwarp();
                 const uint32_t bit = 1u << stage;
-                if (stray) {
-                    raw_par ^= raw_armed & bit;  // parity of this stage's latest use of raw
-                    raw_armed |= bit;
-                } else {
-                    armed |= bit;
-                    armed_par = phase ? (armed_par | bit) : (armed_par & ~bit);
-                }
+                armed |= bit;
+                armed_par = phase ? (armed_par | bit) : (armed_par & ~bit);
             }
             if (++stage == Cfg::STAGES) {
                 stage = 0;
@@ -351,53 +365,53 @@ __device__ void grouped_producer(const GroupedParams &p, const CUtensorMap *tA, 
             while (globaltimer_ns() - t0 < 2000000ull) {
             }
         }
-        for (int s = 0; s < Cfg::STAGES; ++s)
-            if (raw_armed & (1u << s)) w.wait_drain(smem_u32(&ctl->raw[s]), (raw_par >> s) & 1u, kDrainNs);
     }
 }
 
-// ---------------------------------------------------- stray rows (weights)
-
-// One warp per CTA: clears the rows past an expert's last one within the
-// 16-row step that holds it, in both operands' atoms (a row is 128 bytes of
-// each atom, whatever the swizzle within it), and completes full[s].
+// Weight gradient: one warp loads every tile's last rows (fewer than 16) into
+// their buffer, a lane per 64-element atom: two of A, then B's.
 template <class Cfg>
-__device__ void clear_stray_rows(const GroupedParams &p, uint32_t sbase, GroupedCtl<Cfg::STAGES> *ctl,
-                                 GroupTable tab, const Waiter &w, uint32_t rank, int lane)
+__device__ void last_rows_producer(const GroupedParams &p, const GroupedMaps &maps, uint32_t sbase,
+                                   GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, uint32_t rank,
+                                   int lane)
 {
+    constexpr int ATOMS = Cfg::LAST_BYTES / Cfg::LAST_ATOM_BYTES;
+    const uint32_t full = smem_u32(&ctl->last_full);
+    const TileLoader<Cfg> ld{Cfg::PAIR ? mapa_shared(full, 0) : full};
+    uint32_t phase = 0;
     int64_t kb_count = 0;
-    uint32_t raw_phase = 0, peer_phase = 0;  // per stage
+    bool used = false, ok = true;
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (it.next(p, t)) {
-        if (t.kbs > 0 && has_stray_rows<Cfg>(t, t.kbs - 1)) {
-            const int s = static_cast<int>((kb_count + t.kbs - 1) % Cfg::STAGES);
-            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->raw[s]), (raw_phase >> s) & 1u))) return;
-            raw_phase ^= 1u << s;
-            const int from = t.last, rows = 16 - (t.last & 15);
-            constexpr int ATOMS = Cfg::STAGE_BYTES / Cfg::ATOM_BYTES;
-            const uint32_t base = sbase + s * Cfg::STAGE_BYTES + from * 128;
-            for (int i = lane; i < ATOMS * rows * 8; i += 32) {
-                const int a = i / (rows * 8), j = i - a * (rows * 8);
-                st_shared_v4(base + a * Cfg::ATOM_BYTES + j * 16, 0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (Cfg::PAIR && rank != 0) {
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->peer[s]), 0));
-                __syncwarp();
-            } else {
-                if constexpr (Cfg::PAIR) {
-                    if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->peer[s]), (peer_phase >> s) & 1u))) return;
-                    fence_acq_rel_cluster();
-                    peer_phase ^= 1u << s;
-                    fence_proxy_async_smem();
-                }
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->full[s]));
-                __syncwarp();
-            }
-        }
+        // (Test hook: a tile without ring k-blocks stalls here.)
+        const bool stalled = blockIdx.x == 0 && t.kbs == 0 && kb_count == p.stall_kb;
         kb_count += t.kbs;
+        if (t.extra == 0) continue;
+        ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->last_empty), phase ^ 1u));
+        if (!ok) break;
+        if (stalled) {
+            phase ^= 1u;
+            continue;
+        }
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full, Cfg::CLUSTER * Cfg::LAST_BYTES);
+        __syncwarp();
+        if (lane < ATOMS) {
+            const bool a = lane < 2;
+            const int32_t x = a ? t.f0 + static_cast<int32_t>(rank) * Cfg::BM + 64 * lane
+                                : t.c0 + static_cast<int32_t>(rank) * Cfg::CTA_BN + 64 * (lane - 2);
+            const CUtensorMap *m = &maps.m[a ? kMapALast : kMapBLast];
+            ld.load_last_rows(sbase + Cfg::LAST_OFF + lane * Cfg::LAST_ATOM_BYTES, m, m + 1, x,
+                              t.row0 + t.count - t.extra, t.extra, static_cast<int32_t>(p.rows));
+        }
+        __syncwarp();
+        used = true;
+        phase ^= 1u;
+    }
+    if (used) {
+        // The copies have landed, and (unless giving up) the commit that frees the buffer has arrived.
+        if (ok) ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->last_empty), phase ^ 1u));
+        if (!ok && rank == 0) w.wait_drain(full, phase ^ 1u, kDrainNs);
     }
 }
 
@@ -412,14 +426,26 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
     const uint64_t dB0 = Cfg::B_MN ? umma_desc_sw128(sbase + Cfg::A_BYTES, Cfg::ATOM_BYTES, 1024)
                                    : umma_desc_sw128(sbase + Cfg::A_BYTES, 16, 1024);
     constexpr uint32_t A_STEP = (Cfg::A_MN ? 2048 : 32) >> 4, B_STEP = (Cfg::B_MN ? 2048 : 32) >> 4;
+    auto mma = [](uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t add) {
+        if constexpr (Cfg::PAIR)
+            umma_f16_pair(d, da, db, idesc, add);
+        else
+            umma_f16(d, da, db, idesc, add);
+    };
+    auto commit = [](uint64_t *bar) {
+        if constexpr (Cfg::PAIR)
+            umma_commit_pair(smem_u32(bar), 3);
+        else
+            umma_commit(smem_u32(bar));
+    };
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, last_phase = 0;
     uint32_t acc = 0, acc_phase = 0;
     bool issued = false, ok = true;
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (ok && it.next(p, t)) {
-        if (t.kbs == 0) continue;  // the empty sum: the epilogue writes zeros
+        if (t.kbs == 0 && t.extra == 0) continue;  // the empty sum: the epilogue writes zeros
         if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->tempty[acc]), acc_phase ^ 1u))) {
             ok = false;
             break;
@@ -437,19 +463,10 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
             const int steps = kb == t.kbs - 1 ? (t.last + 15) / 16 : Cfg::BK / 16;
             if (elect_one_sync()) {
 #pragma unroll
-                for (int kk = 0; kk < Cfg::BK / 16; ++kk) {
-                    if (kk < steps) {
-                        const uint32_t add = (kb > 0 || kk > 0) ? 1u : 0u;
-                        if constexpr (Cfg::PAIR)
-                            umma_f16_pair(d, dA0 + so + kk * A_STEP, dB0 + so + kk * B_STEP, idesc, add);
-                        else
-                            umma_f16(d, dA0 + so + kk * A_STEP, dB0 + so + kk * B_STEP, idesc, add);
-                    }
-                }
-                if constexpr (Cfg::PAIR)
-                    umma_commit_pair(smem_u32(&ctl->empty[stage]), 3);
-                else
-                    umma_commit(smem_u32(&ctl->empty[stage]));
+                for (int kk = 0; kk < Cfg::BK / 16; ++kk)
+                    if (kk < steps)
+                        mma(d, dA0 + so + kk * A_STEP, dB0 + so + kk * B_STEP, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+                commit(&ctl->empty[stage]);
             }
             __syncwarp();
             issued = true;
@@ -458,13 +475,26 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
                 phase ^= 1u;
             }
         }
-        if (!ok) break;
-        if (elect_one_sync()) {
-            if constexpr (Cfg::PAIR)
-                umma_commit_pair(smem_u32(&ctl->tfull[acc]), 3);
-            else
-                umma_commit(smem_u32(&ctl->tfull[acc]));
+        if constexpr (Cfg::MODE == kWeights) {
+            if (ok && t.extra > 0) {
+                ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->last_full), last_phase));
+                if (ok) {
+                    last_phase ^= 1u;
+                    tc_fence_after_sync();
+                    const uint32_t at = sbase + Cfg::LAST_OFF;
+                    if (elect_one_sync()) {
+                        mma(d, umma_desc_sw128(at, Cfg::LAST_ATOM_BYTES, 1024),
+                            umma_desc_sw128(at + 2 * Cfg::LAST_ATOM_BYTES, Cfg::LAST_ATOM_BYTES, 1024), idesc,
+                            t.kbs > 0 ? 1u : 0u);
+                        commit(&ctl->last_empty);
+                    }
+                    __syncwarp();
+                    issued = true;
+                }
+            }
         }
+        if (!ok) break;
+        if (elect_one_sync()) commit(&ctl->tfull[acc]);
         __syncwarp();
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
@@ -504,7 +534,12 @@ __device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi, bool bf
 // output row c0 + c.  The sums are rounded once, to the operands' type, and
 // turned through a per-warp staging tile of EPI_BLOCK rows x 32 features
 // (16-byte chunks, XOR-swizzled by row: free of bank conflicts both ways), so
-// that a store instruction writes 64 contiguous bytes of 8 output rows.
+// that a store instruction writes 64 contiguous bytes of 8 output rows.  (One
+// tile per warpgroup, 256 contiguous bytes of 2 rows, measured the same.)
+// The tile's way through shared memory is what the weight gradient pays for
+// the epilogue: the operands' copies and the MMA's reads already take 128
+// bytes a cycle, all that shared memory gives.  8192 tokens x 4 on 32
+// experts, 4096 x 1536: 272 us, 233 us with nothing stored.
 template <class Cfg>
 __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
                                  GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, int warp, int lane,
@@ -513,21 +548,18 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
     const int e = warp - Cfg::EPI_WARP0;
     const int q = warp & 3, h = e >> 2;
     const bool bf16 = p.bf16 != 0;
-    constexpr int NB = Cfg::EPI_BLOCK, QF = Cfg::QF;
-    constexpr int ROW = QF * 2, CHUNKS = QF / 8;  // bytes and 16-byte chunks of a staged row
-    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * ROW);
-    // Address of chunk k of staged row c.
-    auto staged = [stg](int c, int k) {
-        return stg + c * ROW + ((k ^ (CHUNKS == 4 ? (c >> 1) & 3 : (c >> 2) & 1)) << 4);
-    };
+    constexpr int NB = Cfg::EPI_BLOCK;
+    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * 64);
+    // Address of 16-byte chunk k of staged row c.
+    auto staged = [stg](int c, int k) { return stg + c * 64 + ((k ^ ((c >> 1) & 3)) << 4); };
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
     uint16_t *out = static_cast<uint16_t *>(p.out);
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (it.next(p, t)) {
-        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * QF;  // the warp's first feature
-        const int64_t all = Cfg::MODE == kWeights ? p.out_rows : t.count;  // output rows of the expert
+        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * 32;  // the warp's first feature
+        const int64_t all = Cfg::MODE == kWeights ? p.out_rows : t.count;          // output rows of the expert
         const int64_t base = Cfg::MODE == kWeights ? p.out_rows * t.e : t.row0;
         // The tile's rows are its columns up to the expert's last row; this
         // warp takes the first or the second half of them.
@@ -535,12 +567,23 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
         const int64_t end = all - t.c0 < t.cols ? all - t.c0 : t.cols;
         const int32_t from = h ? half : 0;
         const int64_t to = h ? end : (end < half ? end : half);
-        const bool empty = t.kbs == 0;
+        const bool empty = t.kbs == 0 && t.extra == 0;
         if (!empty) {
             if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->tfull[acc]), acc_phase))) return;
             tc_fence_after_sync();
         }
         const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * Cfg::BN;
+        auto release = [&] {  // this warp has read its part of the accumulator
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (Cfg::PAIR)
+                    mbar_arrive_cluster(tempty0 + 8 * acc);
+                else
+                    mbar_arrive(tempty0 + 8 * acc);
+            }
+        };
+        if (!empty && to <= from) release();
 #pragma unroll 1
         for (int32_t j = from; j < to; j += NB) {
             uint32_t lo[NB / 2], hi[NB / 2];  // lanes 0-15 and 16-31 of the quarter
@@ -553,53 +596,37 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
                     tmem_ld_16x256b_x4(tbase + j + (16u << 16), hi);
                 } else {
                     tmem_ld_16x256b_x2(tbase + j, lo);
-                    if constexpr (QF == 32) tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
+                    tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
                 }
                 tmem_wait_ld();
+                if (j + NB >= to) release();
             }
-            if constexpr (QF == 32) {
-                // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
+            // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
 #pragma unroll
-                for (int i = 0; i < NB / 8; ++i)
-                    stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
-                                      round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
-                                      round_pair(hi[4 * i], hi[4 * i + 1], bf16),
-                                      round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
-            } else {
-                // Per 16 columns: the first 8 columns' two pieces of 8 features, then the others'.
-                static_assert(QF == 32 || NB == 16, "one store");
-                stmatrix_x4_trans(staged((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1), round_pair(lo[0], lo[1], bf16),
-                                  round_pair(lo[2], lo[3], bf16), round_pair(lo[4], lo[5], bf16),
-                                  round_pair(lo[6], lo[7], bf16));
-            }
+            for (int i = 0; i < NB / 8; ++i)
+                stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
+                                  round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
+                                  round_pair(hi[4 * i], hi[4 * i + 1], bf16),
+                                  round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
             __syncwarp();
             const int n = to - j < NB ? static_cast<int>(to - j) : NB;
             uint16_t *o = out + (base + t.c0 + j) * p.ldo + f0;
-            if (p.vec_store && f0 + QF <= p.features) {
-                // 16-byte pieces, 32 / CHUNKS rows at a time.
-                constexpr int ROWS = 32 / CHUNKS;
-                o += (lane / CHUNKS) * p.ldo + (lane % CHUNKS) * 8;
+            if (p.vec_store && f0 + 32 <= p.features) {
+                // 16-byte pieces, four lanes to a row.
+                o += (lane >> 2) * p.ldo + (lane & 3) * 8;
 #pragma unroll
-                for (int i = 0; i < NB; i += ROWS)
-                    if (i + lane / CHUNKS < n)
-                        *reinterpret_cast<uint4 *>(o + i * p.ldo) =
-                            ld_shared_v4(staged(i + lane / CHUNKS, lane % CHUNKS));
-            } else if (lane < QF && f0 + lane < p.features) {
-                // A feature per lane, row by row.
+                for (int i = 0; i < NB; i += 8)
+                    if (i + (lane >> 2) < n)
+                        *reinterpret_cast<uint4 *>(o + i * p.ldo) = ld_shared_v4(staged(i + (lane >> 2), lane & 3));
+            } else if (f0 + lane < p.features) {
+                // A feature per lane, row by row.  (Two rows at a time in the
+                // row's own 4-byte words: 179 us where this takes 112.)
 #pragma unroll 8
                 for (int c = 0; c < n; ++c) o[c * p.ldo + lane] = ld_shared_u16(staged(c, lane >> 3) + (lane & 7) * 2);
             }
             __syncwarp();
         }
         if (!empty) {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (Cfg::PAIR)
-                    mbar_arrive_cluster(tempty0 + 8 * acc);
-                else
-                    mbar_arrive(tempty0 + 8 * acc);
-            }
             acc ^= 1u;
             if (acc == 0) acc_phase ^= 1u;
         }
@@ -620,8 +647,7 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmBpart, const GroupedParams p)
+    grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -639,9 +665,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int s = 0; s < Cfg::STAGES; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
-            mbar_init(smem_u32(&ctl->raw[s]), 1);
-            mbar_init(smem_u32(&ctl->peer[s]), 1);
         }
+        mbar_init(smem_u32(&ctl->last_full), 1);
+        mbar_init(smem_u32(&ctl->last_empty), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctl->tfull[b]), 1);
             mbar_init(smem_u32(&ctl->tempty[b]), Cfg::CLUSTER * Cfg::EPI_WARPS);
@@ -649,8 +675,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&maps.m[kMapA]);
+        tma_prefetch_desc(&maps.m[kMapB]);
     }
     if (warp == 1) {
         if constexpr (Cfg::PAIR) {
@@ -672,11 +698,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const Waiter w{&ctl->abort, p.status, p.timeout_ns};
     const uint32_t rank = Cfg::PAIR ? cluster_ctarank() : 0u;
     if (warp == 0) {
-        grouped_producer<Cfg>(p, &tmA, &tmB, &tmBpart, sbase, ctl, tab, w, rank);
+        grouped_producer<Cfg>(p, maps, sbase, ctl, tab, w, rank);
     } else if (warp == 1) {
         if (rank == 0) grouped_mma<Cfg>(p, sbase, tmem_base, ctl, tab, w);
     } else if (warp == 2) {
-        if constexpr (Cfg::MODE == kWeights) clear_stray_rows<Cfg>(p, sbase, ctl, tab, w, rank, lane);
+        if constexpr (Cfg::MODE == kWeights) last_rows_producer<Cfg>(p, maps, sbase, ctl, tab, w, rank, lane);
     } else if (warp >= Cfg::EPI_WARP0) {
         grouped_epilogue<Cfg>(p, sbase, tmem_base, ctl, tab, w, warp, lane, rank);
     }

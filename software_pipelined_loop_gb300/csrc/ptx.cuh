@@ -417,13 +417,6 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *tmap,
         : "memory");
 }
 
-// Orders what this thread observed from other CTAs of the cluster before
-// what it does next (acquire side of a cross-CTA mbarrier arrival).
-__device__ __forceinline__ void fence_acq_rel_cluster()
-{
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-}
-
 // True in exactly one lane of the calling (converged, full) warp.  Code
 // that the whole warp runs keeps its operands warp-uniform, and the one
 // elected lane issues the single-thread instructions (tcgen05.mma, commit).

@@ -104,10 +104,10 @@ def header_functions(path: str = HEADER) -> list[str]:
 def _ptr(x) -> int | None:
     if x is None:
         return None
+    if hasattr(x, "data_ptr"):
+        return x.data_ptr()
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
     if hasattr(x, "__array_interface__"):
         return int(x.__array_interface__["data"][0])
     raise TypeError(f"expected a tensor or an address, got {type(x)!r}")

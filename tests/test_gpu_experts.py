@@ -588,3 +588,24 @@ def test_host_memory_is_refused():
         with pytest.raises(gp.GemmpipeError) as e:
             gp.gemm_grouped(gp.F16, 64, 64, 64, 1, *args)
         assert e.value.status == gp.ERR_INVALID_VALUE
+
+
+@pytest.mark.parametrize("mean", [4, 300])
+def test_a_stalled_pipeline_times_out(mean):
+    # The wait for a k-block that never arrives ends the kernel, which reports it; the next call is unharmed.
+    K, N, E = 512, 256, 2
+    off, R, X, dY, W = setup([mean, mean], K, N, torch.float16, seed=21)
+    Y = torch.empty(R, N, dtype=torch.float16, device="cuda")
+    dW = torch.empty(E, K, N, dtype=torch.float16, device="cuda")
+    calls = [lambda: gp.gemm_grouped(gp.F16, R, N, K, E, X, K, off, W, Y, N),
+             lambda: gp.gemm_grouped_dw(gp.F16, R, N, K, E, X, K, dY, N, off, dW)]
+    for call in calls:
+        gp.gemmpipe_test_inject_stall(0, 50)
+        call()
+        assert gp.gemmpipe_get_device_status() == gp.ERR_TIMEOUT
+        call()
+        assert gp.gemmpipe_get_device_status() == gp.OK
+    exact, mag = rows_reference(off, X, W)
+    check_close(Y, exact, product_bound(2.0 ** -11, K, exact, mag))
+    exact, mag = weights_reference(off, X, dY)
+    check_close(dW, exact, product_bound(2.0 ** -11, mean, exact, mag))
