@@ -16,6 +16,7 @@ struct GroupedVariant {
     int tile_f;    // features per tile
     int pair;      // 1: CTA pairs, 256 features per tile; 0: single CTAs, 128
     int cta_bn;    // columns of the row operand per CTA
+    int bk;        // products per stage
     int smem_bytes;
     cudaError_t (*launch)(const GroupedMaps &, const GroupedParams &, int grid, cudaStream_t);
     int (*max_units)();  // co-resident CTAs (or CTA pairs) on the current device

@@ -131,7 +131,7 @@ bool encode_row_groups(CUtensorMap *m, bool bf16, const Rows &r, int64_t rows, u
 }
 
 // Weights experts x rows x width: boxes of 64 elements x box_rows rows of
-// one expert, or (grouped) 2 x 64 elements x 64 rows in one copy.
+// one expert, or (grouped) 2 x 64 elements x box_rows rows in one copy.
 bool encode_weights(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t experts, int64_t rows, int64_t width,
                     int64_t ld, uint32_t box_rows)
 {
@@ -143,12 +143,12 @@ bool encode_weights(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t expert
 }
 
 bool encode_weight_groups(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t experts, int64_t rows, int64_t width,
-                          int64_t ld)
+                          int64_t ld, uint32_t box_rows)
 {
     const uint64_t dims[4] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(width / 64),
                               static_cast<uint64_t>(experts)};
     const uint64_t strides[3] = {static_cast<uint64_t>(ld) * 2, 128, static_cast<uint64_t>(rows * ld) * 2};
-    const uint32_t box[4] = {64, 64, 2, 1};
+    const uint32_t box[4] = {64, box_rows, 2, 1};
     return gp::api_encode_16bit(m, bf16, 4, w, dims, strides, box);
 }
 
@@ -251,8 +251,8 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
         p.out_rows = q.K;
     } else {
         p.a_groups = q.mode == gp::kRows && q.N % 64 == 0;
-        ok = (p.a_groups ? encode_weight_groups(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld)
-                         : encode_weights(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, q.mode == gp::kRows ? 64 : 128)) &&
+        ok = (p.a_groups ? encode_weight_groups(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, v->bk)
+                         : encode_weights(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, q.mode == gp::kRows ? v->bk : 128)) &&
              encode_rows(&m[gp::kMapB], bf16, q.rows, q.R, v->cta_bn) &&
              encode_rows(&m[gp::kMapBPart], bf16, q.rows, q.R, 32);
         p.depth = q.mode == gp::kRows ? q.K : q.N;

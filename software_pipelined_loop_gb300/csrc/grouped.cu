@@ -88,14 +88,14 @@ int max_units()
 template <class Cfg>
 constexpr GroupedVariant variant()
 {
-    return GroupedVariant{Cfg::MODE, Cfg::BN, Cfg::TILE_F, Cfg::PAIR ? 1 : 0, Cfg::CTA_BN, Cfg::SMEM_BYTES, &launch<Cfg>,
+    return GroupedVariant{Cfg::MODE, Cfg::BN, Cfg::TILE_F, Cfg::PAIR ? 1 : 0, Cfg::CTA_BN, Cfg::BK, Cfg::SMEM_BYTES, &launch<Cfg>,
                           &max_units<Cfg>};
 }
 
 const GroupedVariant kVariants[] = {
-    variant<GroupedCfg<kRows, 32, false>>(),  variant<GroupedCfg<kRows, 64, false>>(),
+    variant<GroupedCfg<kRows, 32, false, 128>>(),  variant<GroupedCfg<kRows, 64, false, 128>>(),
     variant<GroupedCfg<kRows, 128, false>>(), variant<GroupedCfg<kRows, 256, true>>(),
-    variant<GroupedCfg<kRowsT, 32, false>>(), variant<GroupedCfg<kRowsT, 64, false>>(),
+    variant<GroupedCfg<kRowsT, 32, false, 128>>(), variant<GroupedCfg<kRowsT, 64, false, 128>>(),
     variant<GroupedCfg<kRowsT, 128, false>>(), variant<GroupedCfg<kRowsT, 256, true>>(),
     variant<GroupedCfg<kWeights, 256, true>>(),
 };

@@ -38,7 +38,7 @@
 
 namespace gp {
 
-template <int MODE_, int BN_, bool PAIR_>
+template <int MODE_, int BN_, bool PAIR_, int BK_ = 64>
 struct GroupedCfg {
     static constexpr int MODE = MODE_;
     static constexpr int BN = BN_;        // output rows per tile
@@ -46,7 +46,8 @@ struct GroupedCfg {
     static constexpr int CLUSTER = PAIR ? 2 : 1;
     static constexpr int BM = 128;        // features per CTA
     static constexpr int TILE_F = BM * CLUSTER;
-    static constexpr int BK = 64;
+    static constexpr int BK = BK_;        // products per stage
+    static constexpr int SUBS = BK / 64;  // 64-product sub-tiles of an operand with products contiguous
     static constexpr bool A_MN = MODE != kRowsT;    // W[k][n] and dY[r][n]: features contiguous
     static constexpr bool B_MN = MODE == kWeights;  // X[r][k] of the weight gradient
     static constexpr int N_UNIT = 16 * CLUSTER;     // the MMA's columns are a multiple of this
@@ -54,7 +55,8 @@ struct GroupedCfg {
     static constexpr int A_BYTES = BM * BK * 2;
     static constexpr int B_BYTES = CTA_BN * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int ATOM_BYTES = BK * 128;     // 64 features (columns) x 64 products
+    static constexpr int ATOM_BYTES = BK * 128;     // 64 features (columns) x BK products
+    static constexpr int A_SUB_BYTES = BM * 128, B_SUB_BYTES = CTA_BN * 128;
     static constexpr int RING_BYTES = 196608;
     static constexpr int STAGES = RING_BYTES / STAGE_BYTES < 16 ? RING_BYTES / STAGE_BYTES : 16;
     static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
@@ -82,7 +84,7 @@ struct GroupedCfg {
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "MMA columns");
     static_assert(!PAIR || BN == 256, "pairs take 256 x 256 tiles");
     static_assert(B_BYTES % 1024 == 0 && TABLE_BYTES % 8 == 0, "alignment");
-    static_assert(!B_MN || CTA_BN % 64 == 0, "64-column atoms");
+    static_assert(!B_MN || (CTA_BN % 64 == 0 && BK == 64), "64-column atoms, 64 rows a stage");
     static_assert(SMEM_BYTES <= 232448, "over the per-CTA shared-memory limit");
 };
 
@@ -267,17 +269,23 @@ struct TileLoader {
     }
 };
 
-template <class Cfg>
+// Two warps run this loop, one for each operand, the whole warp with one
+// elected lane issuing.  A stage costs a warp a few hundred cycles of issue
+// whatever it holds (a passed wait 120, a barrier armed and two copies 260 --
+// one warp for both operands kept a 64-feature tile and a 128-feature one to
+// the same 470 cycles per 64 products), so the operands have a warp each and
+// the next stage's barrier is looked at while this one's copies are issued.
+template <class Cfg, bool A_SIDE>
 __device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps, uint32_t sbase,
                                  GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, uint32_t rank)
 {
-    const CUtensorMap *tA = &maps.m[kMapA], *tB = &maps.m[kMapB];
+    const CUtensorMap *map = &maps.m[A_SIDE ? kMapA : kMapB];
     int stage = 0;
     uint32_t phase = 0;
     uint32_t armed = 0, armed_par = 0;
     int64_t kb_count = 0;
-    bool ok = true;
-    const uint32_t full0 = smem_u32(&ctl->full[0]);
+    bool ok = true, ready = false;
+    const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
     const uint32_t full0_leader = Cfg::PAIR ? mapa_shared(full0, 0) : full0;
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
@@ -285,82 +293,89 @@ __device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps
         const int32_t f0 = t.f0 + static_cast<int32_t>(rank) * Cfg::BM;
         const int32_t c0 = t.c0 + static_cast<int32_t>(rank) * (t.cols / Cfg::CLUSTER);
         // Copies of the row operand: one of all CTA_BN rows, or as many of 32
-        // rows as hold the tile's columns when that is a quarter less.
+        // rows as hold the tile's columns when that is fewer rows.
         const int32_t parts = (t.cols / Cfg::CLUSTER + Cfg::B_PART_ROWS - 1) / Cfg::B_PART_ROWS;
         const bool whole = Cfg::MODE == kWeights || parts * Cfg::B_PART_ROWS >= Cfg::CTA_BN;
+        const uint32_t bytes = Cfg::A_BYTES + (whole ? Cfg::B_BYTES : Cfg::SUBS * parts * Cfg::B_PART_BYTES);
         for (int32_t kb = 0; kb < t.kbs; ++kb, ++kb_count) {
-            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->empty[stage]), phase ^ 1u))) {
+            if (!ready && !__all_sync(0xffffffffu, w.wait(empty0 + 8u * stage, phase ^ 1u))) {
                 ok = false;
                 break;
             }
-            if (!(blockIdx.x == 0 && kb_count == p.stall_kb)) {
-                const uint32_t so = 8u * static_cast<uint32_t>(stage);
-                const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::A_BYTES;
-                const int32_t k0 = kb * Cfg::BK;
-                const TileLoader<Cfg> ld{full0_leader + so};
-                if (elect_one_sync()) {
-                    const uint32_t bytes = Cfg::A_BYTES + (whole ? Cfg::B_BYTES : parts * Cfg::B_PART_BYTES);
-                    if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * bytes);
-                    if constexpr (Cfg::MODE == kRows) {
-                        // W[e]: 64 products x 128 features, two 64-feature atoms.
-                        if (p.a_groups) {
-                            ld.load4(sa, tA, 0, k0, f0 / 64, t.e);
-                        } else {
-                            ld.load3(sa, tA, f0, k0, t.e);
-                            ld.load3(sa + Cfg::ATOM_BYTES, tA, f0 + 64, k0, t.e);
-                        }
-                    } else if constexpr (Cfg::MODE == kRowsT) {
-                        ld.load3(sa, tA, k0, f0, t.e);
-                    } else {
-                        if (p.a_groups) {
-                            ld.load3(sa, tA, 0, t.row0 + k0, f0 / 64);
-                        } else {
-                            ld.load2(sa, tA, f0, t.row0 + k0);
-                            ld.load2(sa + Cfg::ATOM_BYTES, tA, f0 + 64, t.row0 + k0);
-                        }
-                        if (p.b_groups) {
-                            ld.load3(sb, tB, 0, t.row0 + k0, c0 / 64);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < Cfg::CTA_BN / 64; ++j)
-                                ld.load2(sb + j * Cfg::ATOM_BYTES, tB, c0 + 64 * j, t.row0 + k0);
-                        }
-                    }
-                    if constexpr (Cfg::MODE != kWeights) {
-                        if (whole) {
-                            ld.load2(sb, tB, k0, t.row0 + c0);
-                        } else {
-                            for (int32_t j = 0; j < parts; ++j)
-                                ld.load2(sb + j * Cfg::B_PART_BYTES, &maps.m[kMapBPart], k0,
-                                         t.row0 + c0 + j * Cfg::B_PART_ROWS);
-                        }
-                    }
-                }
-                __syncwarp();
-                const uint32_t bit = 1u << stage;
-                armed |= bit;
-                armed_par = phase ? (armed_par | bit) : (armed_par & ~bit);
-            }
+            const uint32_t so = 8u * static_cast<uint32_t>(stage);
+            const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::A_BYTES;
+            const uint32_t bit = 1u << stage, this_phase = phase;
             if (++stage == Cfg::STAGES) {
                 stage = 0;
                 phase ^= 1u;
             }
+            ready = __all_sync(0xffffffffu, mbar_test_wait(empty0 + 8u * stage, phase ^ 1u));
+            if (blockIdx.x == 0 && kb_count == p.stall_kb) continue;
+            const int32_t k0 = kb * Cfg::BK;
+            const TileLoader<Cfg> ld{full0_leader + so};
+            if (elect_one_sync()) {
+                if constexpr (A_SIDE) {
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * bytes);
+                    if constexpr (Cfg::MODE == kRows) {
+                        // W[e]: BK products x 128 features, two 64-feature atoms.
+                        if (p.a_groups) {
+                            ld.load4(sa, map, 0, k0, f0 / 64, t.e);
+                        } else {
+                            ld.load3(sa, map, f0, k0, t.e);
+                            ld.load3(sa + Cfg::ATOM_BYTES, map, f0 + 64, k0, t.e);
+                        }
+                    } else if constexpr (Cfg::MODE == kRowsT) {
+#pragma unroll
+                        for (int u = 0; u < Cfg::SUBS; ++u)
+                            ld.load3(sa + u * Cfg::A_SUB_BYTES, map, k0 + 64 * u, f0, t.e);
+                    } else if (p.a_groups) {
+                        ld.load3(sa, map, 0, t.row0 + k0, f0 / 64);
+                    } else {
+                        ld.load2(sa, map, f0, t.row0 + k0);
+                        ld.load2(sa + Cfg::ATOM_BYTES, map, f0 + 64, t.row0 + k0);
+                    }
+                } else if constexpr (Cfg::MODE == kWeights) {
+                    if (p.b_groups) {
+                        ld.load3(sb, map, 0, t.row0 + k0, c0 / 64);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < Cfg::CTA_BN / 64; ++j)
+                            ld.load2(sb + j * Cfg::ATOM_BYTES, map, c0 + 64 * j, t.row0 + k0);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < Cfg::SUBS; ++u) {
+                        if (whole) {
+                            ld.load2(sb + u * Cfg::B_SUB_BYTES, map, k0 + 64 * u, t.row0 + c0);
+                        } else {
+                            for (int32_t j = 0; j < parts; ++j)
+                                ld.load2(sb + u * Cfg::B_SUB_BYTES + j * Cfg::B_PART_BYTES, &maps.m[kMapBPart],
+                                         k0 + 64 * u, t.row0 + c0 + j * Cfg::B_PART_ROWS);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            armed |= bit;
+            armed_par = this_phase ? (armed_par | bit) : (armed_par & ~bit);
         }
     }
-    if (ok && Cfg::PAIR) {
+    if (ok && Cfg::PAIR && A_SIDE) {
         // The last MMA commits arrive on both CTAs' empty barriers: none may
         // be in flight when a CTA leaves.
         for (int s = 0; s < Cfg::STAGES && ok; ++s) {
             const uint32_t ph = s < stage ? phase ^ 1u : phase;
-            ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->empty[s]), ph ^ 1u));
+            ok = __all_sync(0xffffffffu, w.wait(empty0 + 8u * s, ph ^ 1u));
         }
     }
-    if (!ok) {
-        // Let the copies that were started land before the CTA leaves.
-        if (rank == 0) {
+    if (!ok && armed) {
+        // Let the copies that were started land before the CTA leaves: the
+        // leader's first warp sees them on its barriers, the others give
+        // them a bounded time.
+        if (A_SIDE && rank == 0) {
             for (int s = 0; s < Cfg::STAGES; ++s)
-                if (armed & (1u << s)) w.wait_drain(smem_u32(&ctl->full[s]), (armed_par >> s) & 1u, kDrainNs);
-        } else if (armed) {
+                if (armed & (1u << s)) w.wait_drain(full0 + 8u * s, (armed_par >> s) & 1u, kDrainNs);
+        } else {
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 2000000ull) {
             }
@@ -425,7 +440,6 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
     const uint64_t dA0 = Cfg::A_MN ? umma_desc_sw128(sbase, Cfg::ATOM_BYTES, 1024) : umma_desc_sw128(sbase, 16, 1024);
     const uint64_t dB0 = Cfg::B_MN ? umma_desc_sw128(sbase + Cfg::A_BYTES, Cfg::ATOM_BYTES, 1024)
                                    : umma_desc_sw128(sbase + Cfg::A_BYTES, 16, 1024);
-    constexpr uint32_t A_STEP = (Cfg::A_MN ? 2048 : 32) >> 4, B_STEP = (Cfg::B_MN ? 2048 : 32) >> 4;
     auto mma = [](uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t add) {
         if constexpr (Cfg::PAIR)
             umma_f16_pair(d, da, db, idesc, add);
@@ -441,7 +455,8 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
     int stage = 0;
     uint32_t phase = 0, last_phase = 0;
     uint32_t acc = 0, acc_phase = 0;
-    bool issued = false, ok = true;
+    bool issued = false, ok = true, ready = false;
+    const uint32_t full0 = smem_u32(&ctl->full[0]);
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (ok && it.next(p, t)) {
@@ -454,26 +469,32 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
         const uint32_t d = tmem_base + acc * Cfg::BN;
         const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.cols >> 3) << 17);
         for (int32_t kb = 0; kb < t.kbs; ++kb) {
-            if (!__all_sync(0xffffffffu, w.wait(smem_u32(&ctl->full[stage]), phase))) {
+            if (!ready && !__all_sync(0xffffffffu, w.wait(full0 + 8u * stage, phase))) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
-            const uint64_t so = static_cast<uint64_t>((stage * Cfg::STAGE_BYTES) >> 4);
-            const int steps = kb == t.kbs - 1 ? (t.last + 15) / 16 : Cfg::BK / 16;
-            if (elect_one_sync()) {
-#pragma unroll
-                for (int kk = 0; kk < Cfg::BK / 16; ++kk)
-                    if (kk < steps)
-                        mma(d, dA0 + so + kk * A_STEP, dB0 + so + kk * B_STEP, idesc, kb > 0 || kk > 0 ? 1u : 0u);
-                commit(&ctl->empty[stage]);
-            }
-            __syncwarp();
-            issued = true;
+            const int at = stage;
             if (++stage == Cfg::STAGES) {
                 stage = 0;
                 phase ^= 1u;
             }
+            // The next stage's barrier, looked at while this one's MMAs are issued.
+            ready = __all_sync(0xffffffffu, mbar_test_wait(full0 + 8u * stage, phase));
+            const uint64_t so = static_cast<uint64_t>((at * Cfg::STAGE_BYTES) >> 4);
+            const int steps = kb == t.kbs - 1 ? (t.last + 15) / 16 : Cfg::BK / 16;
+            if (elect_one_sync()) {
+#pragma unroll
+                for (int kk = 0; kk < Cfg::BK / 16; ++kk) {
+                    // 16 products on: rows of an atom, or 32 bytes within a 64-product sub-tile.
+                    const uint32_t ak = (Cfg::A_MN ? kk * 2048 : (kk / 4) * Cfg::A_SUB_BYTES + (kk % 4) * 32) >> 4;
+                    const uint32_t bk = (Cfg::B_MN ? kk * 2048 : (kk / 4) * Cfg::B_SUB_BYTES + (kk % 4) * 32) >> 4;
+                    if (kk < steps) mma(d, dA0 + so + ak, dB0 + so + bk, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+                }
+                commit(&ctl->empty[at]);
+            }
+            __syncwarp();
+            issued = true;
         }
         if constexpr (Cfg::MODE == kWeights) {
             if (ok && t.extra > 0) {
@@ -698,7 +719,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const Waiter w{&ctl->abort, p.status, p.timeout_ns};
     const uint32_t rank = Cfg::PAIR ? cluster_ctarank() : 0u;
     if (warp == 0) {
-        grouped_producer<Cfg>(p, maps, sbase, ctl, tab, w, rank);
+        grouped_producer<Cfg, true>(p, maps, sbase, ctl, tab, w, rank);
+    } else if (warp == 3) {
+        grouped_producer<Cfg, false>(p, maps, sbase, ctl, tab, w, rank);
     } else if (warp == 1) {
         if (rank == 0) grouped_mma<Cfg>(p, sbase, tmem_base, ctl, tab, w);
     } else if (warp == 2) {
