@@ -309,8 +309,11 @@ __device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps
                 stage = 0;
                 phase ^= 1u;
             }
-            ready = __all_sync(0xffffffffu, mbar_test_wait(empty0 + 8u * stage, phase ^ 1u));
-            if (blockIdx.x == 0 && kb_count == p.stall_kb) continue;
+            const bool free = mbar_test_wait(empty0 + 8u * stage, phase ^ 1u);
+            if (blockIdx.x == 0 && kb_count == p.stall_kb) {
+                ready = false;
+                continue;
+            }
             const int32_t k0 = kb * Cfg::BK;
             const TileLoader<Cfg> ld{full0_leader + so};
             if (elect_one_sync()) {
@@ -355,7 +358,7 @@ __device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps
                     }
                 }
             }
-            __syncwarp();
+            ready = __all_sync(0xffffffffu, free);
             armed |= bit;
             armed_par = this_phase ? (armed_par | bit) : (armed_par & ~bit);
         }
@@ -432,6 +435,13 @@ __device__ void last_rows_producer(const GroupedParams &p, const GroupedMaps &ma
 
 // -------------------------------------------------------------------- MMA
 
+// A shared-memory descriptor `units` of 16 bytes on (the address field never
+// carries out of the low word).
+__device__ __forceinline__ uint64_t desc_plus(uint64_t desc, uint32_t units)
+{
+    return (desc & 0xffffffff00000000ull) | (static_cast<uint32_t>(desc) + units);
+}
+
 template <class Cfg>
 __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
                             GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w)
@@ -480,8 +490,8 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
                 phase ^= 1u;
             }
             // The next stage's barrier, looked at while this one's MMAs are issued.
-            ready = __all_sync(0xffffffffu, mbar_test_wait(full0 + 8u * stage, phase));
-            const uint64_t so = static_cast<uint64_t>((at * Cfg::STAGE_BYTES) >> 4);
+            const bool there = mbar_test_wait(full0 + 8u * stage, phase);
+            const uint32_t so = static_cast<uint32_t>(at * Cfg::STAGE_BYTES) >> 4;
             const int steps = kb == t.kbs - 1 ? (t.last + 15) / 16 : Cfg::BK / 16;
             if (elect_one_sync()) {
 #pragma unroll
@@ -489,11 +499,12 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
                     // 16 products on: rows of an atom, or 32 bytes within a 64-product sub-tile.
                     const uint32_t ak = (Cfg::A_MN ? kk * 2048 : (kk / 4) * Cfg::A_SUB_BYTES + (kk % 4) * 32) >> 4;
                     const uint32_t bk = (Cfg::B_MN ? kk * 2048 : (kk / 4) * Cfg::B_SUB_BYTES + (kk % 4) * 32) >> 4;
-                    if (kk < steps) mma(d, dA0 + so + ak, dB0 + so + bk, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+                    if (kk < steps)
+                        mma(d, desc_plus(dA0, so + ak), desc_plus(dB0, so + bk), idesc, kb > 0 || kk > 0 ? 1u : 0u);
                 }
                 commit(&ctl->empty[at]);
             }
-            __syncwarp();
+            ready = __all_sync(0xffffffffu, there);
             issued = true;
         }
         if constexpr (Cfg::MODE == kWeights) {
