@@ -17,12 +17,13 @@ struct GroupedVariant {
     int pair;      // 1: CTA pairs, 256 features per tile; 0: single CTAs, 128
     int cta_bn;    // columns of the row operand per CTA
     int bk;        // products per stage
+    int b_part;    // rows of a short copy of the row operand
     int smem_bytes;
     cudaError_t (*launch)(const GroupedMaps &, const GroupedParams &, int grid, cudaStream_t);
     int (*max_units)();  // co-resident CTAs (or CTA pairs) on the current device
 };
 
-const GroupedVariant *grouped_variant(int mode, int bn);
+const GroupedVariant *grouped_variant(int mode, int bn, int tile_f);
 
 // ---- routing and rows (experts_rows.cu)
 

@@ -131,7 +131,7 @@ bool encode_row_groups(CUtensorMap *m, bool bf16, const Rows &r, int64_t rows, u
 }
 
 // Weights experts x rows x width: boxes of 64 elements x box_rows rows of
-// one expert, or (grouped) 2 x 64 elements x box_rows rows in one copy.
+// one expert, or (grouped) `groups` x 64 elements x box_rows rows in one copy.
 bool encode_weights(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t experts, int64_t rows, int64_t width,
                     int64_t ld, uint32_t box_rows)
 {
@@ -143,12 +143,12 @@ bool encode_weights(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t expert
 }
 
 bool encode_weight_groups(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t experts, int64_t rows, int64_t width,
-                          int64_t ld, uint32_t box_rows)
+                          int64_t ld, uint32_t box_rows, uint32_t groups)
 {
     const uint64_t dims[4] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(width / 64),
                               static_cast<uint64_t>(experts)};
     const uint64_t strides[3] = {static_cast<uint64_t>(ld) * 2, 128, static_cast<uint64_t>(rows * ld) * 2};
-    const uint32_t box[4] = {64, box_rows, 2, 1};
+    const uint32_t box[4] = {64, box_rows, groups, 1};
     return gp::api_encode_16bit(m, bf16, 4, w, dims, strides, box);
 }
 
@@ -194,7 +194,12 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     const int bn = weights ? 256 : rows_per_tile(q.R, q.E);
     // Tiles of all experts, at most (the bounds are on the device).
     const int64_t row_tiles = weights ? q.E * ((q.K + bn - 1) / bn) : q.R / bn + (q.R < q.E ? q.R : q.E);
-    const GroupedVariant *v = gp::grouped_variant(q.mode, bn);
+    // 64-feature tiles where there is an SM for each of them: the rate at
+    // which a CTA streams weights is bound by its shared memory.  (Eight rows
+    // on 64 experts: 2048 x 1024 8.3 us, 8.6 with 128 features; 8192 x 1024
+    // 24.3 and 27.8; 2048 x 1536, 192 tiles of 64, 12.9 and 10.4.)
+    const bool narrow = q.mode == gp::kRows && bn == 32 && row_tiles * ((features + 63) / 64) <= d.sms;
+    const GroupedVariant *v = gp::grouped_variant(q.mode, bn, bn == 256 ? 256 : (narrow ? 64 : 128));
     if (!v) return GEMMPIPE_ERR_INTERNAL;
     if (v->smem_bytes > d.smem_optin) return GEMMPIPE_ERR_UNSUPPORTED_DEVICE;
     const int64_t f_tiles = (features + v->tile_f - 1) / v->tile_f;
@@ -251,10 +256,10 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
         p.out_rows = q.K;
     } else {
         p.a_groups = q.mode == gp::kRows && q.N % 64 == 0;
-        ok = (p.a_groups ? encode_weight_groups(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, v->bk)
+        ok = (p.a_groups ? encode_weight_groups(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, v->bk, v->tile_f / (v->pair ? 128 : 64))
                          : encode_weights(&m[gp::kMapA], bf16, W, q.E, q.K, q.N, wld, q.mode == gp::kRows ? v->bk : 128)) &&
              encode_rows(&m[gp::kMapB], bf16, q.rows, q.R, v->cta_bn) &&
-             encode_rows(&m[gp::kMapBPart], bf16, q.rows, q.R, 32);
+             encode_rows(&m[gp::kMapBPart], bf16, q.rows, q.R, v->b_part);
         p.depth = q.mode == gp::kRows ? q.K : q.N;
     }
     if (!ok) return GEMMPIPE_ERR_INTERNAL;

@@ -88,11 +88,12 @@ int max_units()
 template <class Cfg>
 constexpr GroupedVariant variant()
 {
-    return GroupedVariant{Cfg::MODE, Cfg::BN, Cfg::TILE_F, Cfg::PAIR ? 1 : 0, Cfg::CTA_BN, Cfg::BK, Cfg::SMEM_BYTES, &launch<Cfg>,
+    return GroupedVariant{Cfg::MODE, Cfg::BN, Cfg::TILE_F, Cfg::PAIR ? 1 : 0, Cfg::CTA_BN, Cfg::BK, Cfg::B_PART_ROWS, Cfg::SMEM_BYTES, &launch<Cfg>,
                           &max_units<Cfg>};
 }
 
 const GroupedVariant kVariants[] = {
+    variant<GroupedCfg<kRows, 32, false, 128, 64>>(),
     variant<GroupedCfg<kRows, 32, false, 128>>(),  variant<GroupedCfg<kRows, 64, false, 128>>(),
     variant<GroupedCfg<kRows, 128, false>>(), variant<GroupedCfg<kRows, 256, true>>(),
     variant<GroupedCfg<kRowsT, 32, false, 128>>(), variant<GroupedCfg<kRowsT, 64, false, 128>>(),
@@ -102,10 +103,10 @@ const GroupedVariant kVariants[] = {
 
 }  // namespace
 
-const GroupedVariant *grouped_variant(int mode, int bn)
+const GroupedVariant *grouped_variant(int mode, int bn, int tile_f)
 {
     for (const GroupedVariant &v : kVariants)
-        if (v.mode == mode && v.bn == bn) return &v;
+        if (v.mode == mode && v.bn == bn && v.tile_f == tile_f) return &v;
     return nullptr;
 }
 

@@ -38,13 +38,14 @@
 
 namespace gp {
 
-template <int MODE_, int BN_, bool PAIR_, int BK_ = 64>
+template <int MODE_, int BN_, bool PAIR_, int BK_ = 64, int BM_ = 128>
 struct GroupedCfg {
     static constexpr int MODE = MODE_;
     static constexpr int BN = BN_;        // output rows per tile
     static constexpr bool PAIR = PAIR_;   // cluster of two CTAs, 256 features per tile
     static constexpr int CLUSTER = PAIR ? 2 : 1;
-    static constexpr int BM = 128;        // features per CTA
+    static constexpr int BM = BM_;        // features per CTA: 128, or 64 (then in lanes 0-15 of each TMEM quarter)
+    static constexpr int QF = BM / 4;     // features of an epilogue warp's TMEM quarter
     static constexpr int TILE_F = BM * CLUSTER;
     static constexpr int BK = BK_;        // products per stage
     static constexpr int SUBS = BK / 64;  // 64-product sub-tiles of an operand with products contiguous
@@ -65,7 +66,7 @@ struct GroupedCfg {
     static constexpr int EPI_COLS = BN / 2;         // columns per epilogue warp
     static constexpr int EPI_BLOCK = EPI_COLS < 32 ? EPI_COLS : 32;
 
-    static constexpr int B_PART_ROWS = 32;          // rows of one short copy of the row operand
+    static constexpr int B_PART_ROWS = BN <= 32 ? 16 : 32;  // rows of one short copy of the row operand
     static constexpr int B_PART_BYTES = B_PART_ROWS * 128;
 
     static constexpr int LAST_ROWS = 16;            // weight gradient: rows of an expert's last MMA step
@@ -74,7 +75,7 @@ struct GroupedCfg {
     static constexpr int LAST_OFF = STAGES * STAGE_BYTES;
 
     static constexpr int STAGING_OFF = LAST_OFF + LAST_BYTES;
-    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * 64;
+    static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * QF * 2;
     static constexpr int TABLE_OFF = STAGING_OFF + STAGING_BYTES;
     static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2);
     static constexpr int CTL_OFF = TABLE_OFF + TABLE_BYTES;
@@ -82,6 +83,7 @@ struct GroupedCfg {
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + CTL_BYTES;
 
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "MMA columns");
+    static_assert(BM == 128 || (BM == 64 && MODE == kRows && !PAIR && BN == 32), "64 features: few rows, forward");
     static_assert(!PAIR || BN == 256, "pairs take 256 x 256 tiles");
     static_assert(B_BYTES % 1024 == 0 && TABLE_BYTES % 8 == 0, "alignment");
     static_assert(!B_MN || (CTA_BN % 64 == 0 && BK == 64), "64-column atoms, 64 rows a stage");
@@ -292,8 +294,8 @@ __device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps
     while (ok && it.next(p, t)) {
         const int32_t f0 = t.f0 + static_cast<int32_t>(rank) * Cfg::BM;
         const int32_t c0 = t.c0 + static_cast<int32_t>(rank) * (t.cols / Cfg::CLUSTER);
-        // Copies of the row operand: one of all CTA_BN rows, or as many of 32
-        // rows as hold the tile's columns when that is fewer rows.
+        // Copies of the row operand: one of all CTA_BN rows, or as many short
+        // ones as hold the tile's columns when that is fewer rows.
         const int32_t parts = (t.cols / Cfg::CLUSTER + Cfg::B_PART_ROWS - 1) / Cfg::B_PART_ROWS;
         const bool whole = Cfg::MODE == kWeights || parts * Cfg::B_PART_ROWS >= Cfg::CTA_BN;
         const uint32_t bytes = Cfg::A_BYTES + (whole ? Cfg::B_BYTES : Cfg::SUBS * parts * Cfg::B_PART_BYTES);
@@ -320,12 +322,13 @@ __device__ void grouped_producer(const GroupedParams &p, const GroupedMaps &maps
                 if constexpr (A_SIDE) {
                     if (rank == 0) mbar_arrive_expect_tx(full0 + so, Cfg::CLUSTER * bytes);
                     if constexpr (Cfg::MODE == kRows) {
-                        // W[e]: BK products x 128 features, two 64-feature atoms.
+                        // W[e]: BK products x BM features, atoms of 64 features.
                         if (p.a_groups) {
                             ld.load4(sa, map, 0, k0, f0 / 64, t.e);
                         } else {
-                            ld.load3(sa, map, f0, k0, t.e);
-                            ld.load3(sa + Cfg::ATOM_BYTES, map, f0 + 64, k0, t.e);
+#pragma unroll
+                            for (int j = 0; j < Cfg::BM / 64; ++j)
+                                ld.load3(sa + j * Cfg::ATOM_BYTES, map, f0 + 64 * j, k0, t.e);
                         }
                     } else if constexpr (Cfg::MODE == kRowsT) {
 #pragma unroll
@@ -580,17 +583,20 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
     const int e = warp - Cfg::EPI_WARP0;
     const int q = warp & 3, h = e >> 2;
     const bool bf16 = p.bf16 != 0;
-    constexpr int NB = Cfg::EPI_BLOCK;
-    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * 64);
-    // Address of 16-byte chunk k of staged row c.
-    auto staged = [stg](int c, int k) { return stg + c * 64 + ((k ^ ((c >> 1) & 3)) << 4); };
+    constexpr int NB = Cfg::EPI_BLOCK, QF = Cfg::QF;
+    constexpr int ROW = QF * 2, CHUNKS = QF / 8;  // bytes and 16-byte chunks of a staged row
+    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * ROW);
+    // Address of chunk k of staged row c.
+    auto staged = [stg](int c, int k) {
+        return stg + c * ROW + ((k ^ (CHUNKS == 4 ? (c >> 1) & 3 : (c >> 2) & 1)) << 4);
+    };
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
     uint16_t *out = static_cast<uint16_t *>(p.out);
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (it.next(p, t)) {
-        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * 32;  // the warp's first feature
+        const int64_t f0 = static_cast<int64_t>(t.f0) + rank * Cfg::BM + q * QF;  // the warp's first feature
         const int64_t all = Cfg::MODE == kWeights ? p.out_rows : t.count;          // output rows of the expert
         const int64_t base = Cfg::MODE == kWeights ? p.out_rows * t.e : t.row0;
         // The tile's rows are its columns up to the expert's last row; this
@@ -628,29 +634,39 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
                     tmem_ld_16x256b_x4(tbase + j + (16u << 16), hi);
                 } else {
                     tmem_ld_16x256b_x2(tbase + j, lo);
-                    tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
+                    if constexpr (QF == 32) tmem_ld_16x256b_x2(tbase + j + (16u << 16), hi);
                 }
                 tmem_wait_ld();
                 if (j + NB >= to) release();
             }
-            // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
+            if constexpr (QF == 32) {
+                // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
 #pragma unroll
-            for (int i = 0; i < NB / 8; ++i)
-                stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
-                                  round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
-                                  round_pair(hi[4 * i], hi[4 * i + 1], bf16),
-                                  round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
+                for (int i = 0; i < NB / 8; ++i)
+                    stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
+                                      round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
+                                      round_pair(hi[4 * i], hi[4 * i + 1], bf16),
+                                      round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
+            } else {
+                // Sixteen columns: the first 8 columns' two pieces of 8 features, then the others'.
+                static_assert(QF == 32 || NB == 16, "one store");
+                stmatrix_x4_trans(staged((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1), round_pair(lo[0], lo[1], bf16),
+                                  round_pair(lo[2], lo[3], bf16), round_pair(lo[4], lo[5], bf16),
+                                  round_pair(lo[6], lo[7], bf16));
+            }
             __syncwarp();
             const int n = to - j < NB ? static_cast<int>(to - j) : NB;
             uint16_t *o = out + (base + t.c0 + j) * p.ldo + f0;
-            if (p.vec_store && f0 + 32 <= p.features) {
-                // 16-byte pieces, four lanes to a row.
-                o += (lane >> 2) * p.ldo + (lane & 3) * 8;
+            if (p.vec_store && f0 + QF <= p.features) {
+                // 16-byte pieces, CHUNKS lanes to a row.
+                constexpr int ROWS = 32 / CHUNKS;
+                o += (lane / CHUNKS) * p.ldo + (lane % CHUNKS) * 8;
 #pragma unroll
-                for (int i = 0; i < NB; i += 8)
-                    if (i + (lane >> 2) < n)
-                        *reinterpret_cast<uint4 *>(o + i * p.ldo) = ld_shared_v4(staged(i + (lane >> 2), lane & 3));
-            } else if (f0 + lane < p.features) {
+                for (int i = 0; i < NB; i += ROWS)
+                    if (i + lane / CHUNKS < n)
+                        *reinterpret_cast<uint4 *>(o + i * p.ldo) =
+                            ld_shared_v4(staged(i + lane / CHUNKS, lane % CHUNKS));
+            } else if (lane < QF && f0 + lane < p.features) {
                 // A feature per lane, row by row.  (Two rows at a time in the
                 // row's own 4-byte words: 179 us where this takes 112.)
 #pragma unroll 8

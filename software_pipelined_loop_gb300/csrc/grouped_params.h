@@ -14,7 +14,7 @@ constexpr int kMaxTopK = 64;
 enum GroupedMode { kRows = 0, kRowsT = 1, kWeights = 2 };
 
 // Tensor maps of one launch.  Rows: A the weights, B the row operand, BPart
-// the same in 32-row boxes.  Weight gradient: A and B the two row operands,
+// the same in boxes of fewer rows.  Weight gradient: A and B the two row operands,
 // and each in boxes of 4 rows and of 1 row of 64 elements (from ALast, BLast).
 enum GroupedMap { kMapA = 0, kMapB = 1, kMapBPart = 2, kMapALast = 2, kMapBLast = 4, kMaps = 6 };
 struct GroupedMaps {

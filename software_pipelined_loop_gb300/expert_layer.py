@@ -1,0 +1,167 @@
+"""An expert layer for PyTorch on libgemmpipe's operators, forward and backward.
+
+    y[t] = sum over the chosen experts e of token t:
+               weight[t, e] * (silu(x[t] @ W1[e]) @ W2[e])
+
+`expert_layer` is differentiable in x, the router's weights, W1 and W2; with
+``keep8=True`` the rows that the weight gradients need (the inputs of both
+products) are kept in 8 bits between the passes.  All products, sorts and sums
+run in the CUDA library; torch supplies memory, autograd's bookkeeping and the
+activation function.
+
+    python -m software_pipelined_loop_gb300.expert_layer [--tokens N] [--keep8]
+
+runs a training step and a one-token step on the GPU and prints their times.
+"""
+from __future__ import annotations
+
+import argparse
+
+import torch
+
+from software_pipelined_loop_gb300 import gemmpipe as gp
+
+_CODE = {torch.float16: gp.F16, torch.bfloat16: gp.BF16}
+
+
+def _empty(like, *shape, dtype=None):
+    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+
+
+def route(ids: torch.Tensor, experts: int) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(offsets, slots, rows) of the choices `ids` (tokens x top_k, int32), sorted by expert."""
+    t, k = ids.shape
+    new = lambda n: torch.empty(n, dtype=torch.int32, device=ids.device)  # noqa: E731
+    offsets, slots, rows = new(experts + 1), new(t * k), new(t * k)
+    gp.gemmpipe_route(t, k, experts, ids.contiguous(), offsets, slots, rows)
+    return offsets, slots, rows
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rows, k):
+        t, c = x.shape
+        xs = _empty(x, t * k, c)
+        gp.gemmpipe_dispatch(_CODE[x.dtype], t, k, c, x, c, rows, None, xs, c)
+        ctx.save_for_backward(rows)
+        ctx.k = k
+        return xs
+
+    @staticmethod
+    def backward(ctx, dxs):
+        rows, = ctx.saved_tensors
+        dxs = dxs.contiguous()
+        t, c = dxs.shape[0] // ctx.k, dxs.shape[1]
+        dx = _empty(dxs, t, c)
+        gp.gemmpipe_combine(_CODE[dxs.dtype], t, ctx.k, c, dxs, c, rows, None, dx, c)
+        return dx, None, None
+
+
+class _Product(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets, keep8):
+        r, k = x.shape
+        e, _, n = w.shape
+        y = _empty(x, r, n)
+        gp.gemm_grouped(_CODE[x.dtype], r, n, k, e, x, k, offsets, w, y, n)
+        if keep8:
+            q, s = _empty(x, r, k, dtype=torch.int8), _empty(x, r, (k + 31) // 32, dtype=torch.uint8)
+            gp.gemmpipe_keep8(_CODE[x.dtype], r, k, x, k, q, s)
+            ctx.save_for_backward(q, s, w, offsets)
+        else:
+            ctx.save_for_backward(x, w, offsets)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        *kept, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        e, k, n = w.shape
+        r, ty = dy.shape[0], _CODE[dy.dtype]
+        dx, dw = _empty(dy, r, k), torch.empty_like(w)
+        gp.gemm_grouped_dx(ty, r, n, k, e, dy, n, offsets, w, dx, k)
+        if len(kept) == 2:
+            gp.gemm_grouped_dw8(ty, r, n, k, e, kept[0], kept[1], dy, n, offsets, dw)
+        else:
+            gp.gemm_grouped_dw(ty, r, n, k, e, kept[0], k, dy, n, offsets, dw)
+        return dx, dw, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, weights, rows):
+        t, k = weights.shape
+        c = ys.shape[1]
+        y = _empty(ys, t, c)
+        gp.gemmpipe_combine(_CODE[ys.dtype], t, k, c, ys, c, rows, weights, y, c)
+        ctx.save_for_backward(ys, weights, rows)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        ys, weights, rows = ctx.saved_tensors
+        dy = dy.contiguous()
+        t, k = weights.shape
+        c = ys.shape[1]
+        dys, dweights = torch.empty_like(ys), torch.empty_like(weights)
+        gp.gemmpipe_combine_grad(_CODE[ys.dtype], t, k, c, dy, c, ys, c, rows, weights, dys, c, dweights)
+        return dys, dweights, None
+
+
+def expert_layer(x, ids, weights, w1, w2, keep8: bool = False):
+    """x: tokens x c; ids: tokens x top_k int32 (outside [0, experts): dropped);
+    weights: tokens x top_k fp32; w1: experts x c x h; w2: experts x h x c."""
+    offsets, _, rows = route(ids, w1.shape[0])
+    xs = _Dispatch.apply(x.contiguous(), rows, ids.shape[1])
+    hidden = torch.nn.functional.silu(_Product.apply(xs, w1, offsets, keep8))
+    ys = _Product.apply(hidden, w2, offsets, keep8)
+    return _Combine.apply(ys, weights, rows)
+
+
+def main() -> None:
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--tokens", type=int, default=4096)
+    ap.add_argument("--keep8", action="store_true", help="keep the saved rows in 8 bits")
+    args = ap.parse_args()
+    top_k, experts, c, h = 4, 32, 2048, 1024
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    w1 = (rand(experts, c, h) * c ** -0.5).bfloat16().requires_grad_()
+    w2 = (rand(experts, h, c) * h ** -0.5).bfloat16().requires_grad_()
+
+    def inputs(tokens):
+        best, ids = rand(tokens, experts).topk(top_k, dim=1)
+        return rand(tokens, c).bfloat16().requires_grad_(), ids.int(), torch.softmax(best, 1).requires_grad_()
+
+    def timed(step, reps=10):
+        step()
+        start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        for _ in range(reps):
+            step()
+        stop.record()
+        torch.cuda.synchronize()
+        return start.elapsed_time(stop) / reps
+
+    x, ids, weights = inputs(args.tokens)
+    target = rand(args.tokens, c).bfloat16()
+
+    def train():
+        for leaf in (x, weights, w1, w2):
+            leaf.grad = None
+        expert_layer(x, ids, weights, w1, w2, args.keep8).backward(target)
+
+    ms = timed(train)
+    flops = 3 * 2 * 2 * args.tokens * top_k * c * h
+    print(f"training step, {args.tokens} tokens x {top_k} of {experts} experts, {c} x {h}: {ms:.3f} ms "
+          f"({flops / ms / 1e9:.0f} TFLOP/s)")
+    one = inputs(1)
+    with torch.no_grad():
+        print(f"one token: {timed(lambda: expert_layer(*one, w1, w2), 100) * 1e3:.1f} us")
+    status = gp.gemmpipe_get_device_status()
+    if status != gp.OK:
+        raise SystemExit(f"device status {gp.STATUS.get(status, status)}")
+
+
+if __name__ == "__main__":
+    main()
