@@ -265,7 +265,9 @@ GEMMPIPE_API int64_t gemmpipe_host_panel_rows(int64_t M);
  *   - type is GEMMPIPE_F16 or GEMMPIPE_BF16, the 16-bit floating-point type
  *     of the activations and weights; sums are held in fp32 and rounded once,
  *     to nearest even, where the result is stored;
- *   - C, the length of a token's row, is at most 2^30;
+ *   - C, the length of a row of the operators named gemmpipe_*, is at most
+ *     2^30 (as is K of gemm_grouped_dw8), and rows in 8 bits make at most
+ *     2^31 - 1 pieces of 8192 values of one row;
  *   - T tokens with top_k choices each (1 <= top_k <= 64) make R = T * top_k
  *     slots and rows; choice j of token t is slot t * top_k + j; R is at most
  *     2^31 - 1; there are 1 <= E <= 1024 experts;

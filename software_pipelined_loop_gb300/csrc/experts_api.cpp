@@ -37,15 +37,15 @@ bool bad_type(int type) { return type != GEMMPIPE_F16 && type != GEMMPIPE_BF16; 
 // Null or misaligned where something is to be read or written.
 bool bad_pointer(const void *p, int bytes) { return !p || misaligned(p, bytes); }
 
-// Rows in 8 bits: up to 2^44 values (the grid's blocks hold 8192 of a row, or 8192 of all).
+constexpr int64_t kMaxWidth = int64_t(1) << 30;  // elements of a row of the rows' operators (32-bit places)
+
+// Rows in 8 bits: a block holds 8192 values, of one row or of all.
 bool bad_kept(int64_t rows, int64_t width, int64_t ld)
 {
-    return bad_matrix(rows, width, ld) || (rows > 0 && (width + 7) / 8192 + 1 > kMaxDim / rows);
+    return width > kMaxWidth || bad_matrix(rows, width, ld) || (rows > 0 && (width + 7) / 8192 + 1 > kMaxDim / rows);
 }
 
 // ----------------------------------------------------------- routing, rows
-
-constexpr int64_t kMaxWidth = int64_t(1) << 30;  // elements of a token's row (32-bit places)
 
 struct Tokens {
     int64_t T, k, R;

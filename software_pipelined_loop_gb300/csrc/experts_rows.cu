@@ -192,10 +192,10 @@ __device__ __forceinline__ Piece load_wide(const uint16_t *p)
     return Piece{{v.x, v.y, v.z, v.w}};
 }
 
-__device__ __forceinline__ Piece load_any(const uint16_t *p)
+__device__ __forceinline__ Piece cut(const Words8 &w, const uint16_t *p)
 {
     Piece r;
-    load8_any(p, r.w);
+    cut_words8(w, p, r.w);
     return r;
 }
 
@@ -304,24 +304,24 @@ __global__ void __launch_bounds__(256)
     if (to >= g.rows) return;
     const uint16_t *x = X + s / g.top_k * ldx;
     uint16_t *o = Xs + to * ldxs;
-    const RowCut cut(o, g.width);
+    const RowCut row(o, g.width);
     const bool copied = r >= 0 && !weights;
     const float w = r >= 0 && weights ? weights[s] : 1.f;
     constexpr int FLIGHT = 4;
-    for (int i = lane; i < cut.body; i += 32 * FLIGHT) {
-        Piece p[FLIGHT];
-#pragma unroll
-        for (int u = 0; u < FLIGHT; ++u) {
-            p[u] = Piece{{0, 0, 0, 0}};
-            if (r >= 0 && i + 32 * u < cut.body) p[u] = load_any(x + cut.head + 8 * (i + 32 * u));
-        }
+    for (int i = lane; i < row.body; i += 32 * FLIGHT) {
+        Words8 v[FLIGHT];
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u)
-            if (i + 32 * u < cut.body)
-                store_wide(o + cut.head + 8 * (i + 32 * u), copied || r < 0 ? p[u] : scaled<BF16>(p[u], w));
+            v[u] = load_words8(x + row.head + 8 * (i + 32 * u), r >= 0 && i + 32 * u < row.body);
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int e = row.head + 8 * (i + 32 * u);
+            const Piece p = cut(v[u], x + e);
+            if (i + 32 * u < row.body) store_wide(o + e, copied || r < 0 ? p : scaled<BF16>(p, w));
+        }
     }
-    if (lane < cut.singles()) {
-        const int e = cut.single(lane);
+    if (lane < row.singles()) {
+        const int e = row.single(lane);
         o[e] = r < 0 ? uint16_t(0) : (copied ? x[e] : narrow1<BF16>(widen1<BF16>(x[e]) * w));
     }
 }
@@ -394,35 +394,34 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     if (t >= g.tokens) return;
     uint16_t *y = Y + t * ldy;
-    const RowCut cut(y, g.width);
+    const RowCut own(y, g.width);
     constexpr int FLIGHT = 4;
-    for (int i = lane; i < cut.body; i += g.lanes) {
-        const int e = cut.head + 8 * i;
+    for (int i = lane; i < own.body; i += g.lanes) {
+        const int e = own.head + 8 * i;
         float acc[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) acc[u] = 0.f;
         for (int j0 = 0; j0 < g.top_k; j0 += FLIGHT) {
-            Piece p[FLIGHT];
+            Words8 v[FLIGHT];
 #pragma unroll
             for (int j = 0; j < FLIGHT; ++j) {
                 const uint16_t *row = j0 + j < g.top_k ? row_of[slot][j0 + j] : nullptr;
-                p[j] = Piece{{0, 0, 0, 0}};
-                if (row) p[j] = load_any(row + e);
+                v[j] = load_words8(row + e, row != nullptr);
             }
 #pragma unroll
             for (int j = 0; j < FLIGHT; ++j) {
                 if (j0 + j >= g.top_k || !row_of[slot][j0 + j]) continue;
                 const float w = weight_of[slot][j0 + j];
                 float f[8];
-                widen8<BF16>(p[j], f);
+                widen8<BF16>(cut(v[j], row_of[slot][j0 + j] + e), f);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, f[u], acc[u]);
             }
         }
         store_wide(y + e, narrow8<BF16>(acc));
     }
-    if (lane < cut.singles()) {
-        const int e = cut.single(lane);
+    if (lane < own.singles()) {
+        const int e = own.single(lane);
         float acc = 0.f;
         for (int j = 0; j < g.top_k; ++j)
             if (row_of[slot][j]) acc = fmaf(weight_of[slot][j], widen1<BF16>(row_of[slot][j][e]), acc);
@@ -514,42 +513,41 @@ __global__ void __launch_bounds__(256)
         if (to >= g.rows) return;
     }
     uint16_t *o = dYs + to * lddys;
-    const RowCut cut(o, g.width);
+    const RowCut row(o, g.width);
     if (r < 0) {
-        for (int i = lane; i < cut.body; i += 32) store_wide(o + cut.head + 8 * i, Piece{{0, 0, 0, 0}});
-        if (lane < cut.singles()) o[cut.single(lane)] = 0;
+        for (int i = lane; i < row.body; i += 32) store_wide(o + row.head + 8 * i, Piece{{0, 0, 0, 0}});
+        if (lane < row.singles()) o[row.single(lane)] = 0;
         return;
     }
     const uint16_t *d = dY + s / g.top_k * lddy, *y = Ys + to * ldys;
     const float w = weights ? weights[s] : 1.f;
     float dot = 0.f;
     constexpr int FLIGHT = 2;
-    for (int i = lane; i < cut.body; i += 32 * FLIGHT) {
-        Piece pd[FLIGHT], py[FLIGHT];
+    for (int i = lane; i < row.body; i += 32 * FLIGHT) {
+        Words8 vd[FLIGHT], vy[FLIGHT];
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
-            pd[u] = py[u] = Piece{{0, 0, 0, 0}};
-            if (i + 32 * u < cut.body) {
-                pd[u] = load_any(d + cut.head + 8 * (i + 32 * u));
-                py[u] = load_any(y + cut.head + 8 * (i + 32 * u));
-            }
+            const int e = row.head + 8 * (i + 32 * u);
+            const bool on = i + 32 * u < row.body;
+            vy[u] = load_words8(y + e, on);
+            vd[u] = load_words8(d + e, on);
         }
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
-            if (i + 32 * u >= cut.body) continue;
+            const int e = row.head + 8 * (i + 32 * u);
             float fd[8], fy[8];
-            widen8<BF16>(pd[u], fd);
-            widen8<BF16>(py[u], fy);
+            widen8<BF16>(cut(vd[u], d + e), fd);
+            widen8<BF16>(cut(vy[u], y + e), fy);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 dot = fmaf(fd[k], fy[k], dot);
                 fd[k] *= w;
             }
-            store_wide(o + cut.head + 8 * (i + 32 * u), narrow8<BF16>(fd));
+            if (i + 32 * u < row.body) store_wide(o + e, narrow8<BF16>(fd));
         }
     }
-    if (lane < cut.singles()) {
-        const int e = cut.single(lane);
+    if (lane < row.singles()) {
+        const int e = row.single(lane);
         const float fd = widen1<BF16>(d[e]);
         dot = fmaf(fd, widen1<BF16>(y[e]), dot);
         o[e] = narrow1<BF16>(fd * w);

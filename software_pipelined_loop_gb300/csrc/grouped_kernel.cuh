@@ -570,11 +570,12 @@ __device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi, bool bf
 // turned through a per-warp staging tile of EPI_BLOCK rows x 32 features
 // (16-byte chunks, XOR-swizzled by row: free of bank conflicts both ways), so
 // that a store instruction writes 64 contiguous bytes of 8 output rows.  (One
-// tile per warpgroup, 256 contiguous bytes of 2 rows, measured the same.)
-// The tile's way through shared memory is what the weight gradient pays for
-// the epilogue: the operands' copies and the MMA's reads already take 128
-// bytes a cycle, all that shared memory gives.  8192 tokens x 4 on 32
-// experts, 4096 x 1536: 272 us, 233 us with nothing stored.
+// tile per warpgroup, 256 contiguous bytes of 2 rows, and bulk tensor copies
+// out of the staging tiles measured the same.)  While the output leaves, the
+// operands come in more slowly: the operands' copies and the MMA's reads
+// already take the 128 bytes a cycle that shared memory gives.  Weight
+// gradient of 8192 tokens x 4 on 32 experts, 4096 x 1536: 270 us, 233 us with
+// nothing stored.
 template <class Cfg>
 __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
                                  GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, int warp, int lane,

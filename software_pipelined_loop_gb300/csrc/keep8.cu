@@ -198,18 +198,18 @@ constexpr int kSpansPerBlock = 32;  // spans of one row that a block takes
 // A block's part of a row: `parts` blocks share a row of more than 32 spans.
 struct RowPart {
     int64_t row;
-    int64_t span;  // the warp's first span; it takes every (kThreads / 32)-th up to `end`
-    int64_t end;
+    int span;  // the warp's first span; it takes every (kThreads / 32)-th up to `end`
+    int end;
 };
 
-__device__ __forceinline__ RowPart row_part(int64_t spans, uint32_t parts)
+__device__ __forceinline__ RowPart row_part(int spans, uint32_t parts)
 {
     RowPart p;
-    const uint32_t row = blockIdx.x / parts, part = blockIdx.x - row * parts;
+    const uint32_t row = blockIdx.x / parts;
+    const int first = static_cast<int>(blockIdx.x - row * parts) * kSpansPerBlock;
     p.row = row;
-    p.span = static_cast<int64_t>(part) * kSpansPerBlock + threadIdx.x / 32;
-    const int64_t end = (static_cast<int64_t>(part) + 1) * kSpansPerBlock;
-    p.end = end < spans ? end : spans;
+    p.span = first + static_cast<int>(threadIdx.x / 32);
+    p.end = first + kSpansPerBlock < spans ? first + kSpansPerBlock : spans;
     return p;
 }
 
@@ -217,33 +217,33 @@ __device__ __forceinline__ RowPart row_part(int64_t spans, uint32_t parts)
 // own 8-byte words (rows of bytes start anywhere).
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    keep8_kernel(const uint16_t *X, int64_t width, int64_t ldx, uint32_t parts, int8_t *Q, uint8_t *S)
+    keep8_kernel(const uint16_t *X, int width, int64_t ldx, uint32_t parts, int8_t *Q, uint8_t *S)
 {
     __shared__ __align__(16) uint8_t stage[kThreads / 32][kSpan + 16];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     uint8_t *mine = stage[threadIdx.x >> 5];
-    const int64_t groups = (width + 31) / 32;
     const RowPart p = row_part((width + kSpan - 1) / kSpan, parts);
     const uint16_t *x = X + p.row * ldx;
+    uint8_t *steps = S + p.row * ((width + 31) / 32);
     uint8_t *q = reinterpret_cast<uint8_t *>(Q) + p.row * width;
     // Bytes of a span before the destination's first 8-byte word: the same in every span of a row.
     const int head = static_cast<int>((8 - (reinterpret_cast<uintptr_t>(q) & 7u)) & 7u);
-    for (int64_t sp = p.span; sp < p.end; sp += kThreads / 32) {
-        const int64_t e0 = sp * kSpan, e = e0 + 8 * lane;
+    for (int sp = p.span; sp < p.end; sp += kThreads / 32) {
+        const int e0 = sp * kSpan, e = e0 + 8 * lane;
         uint32_t w[4] = {0, 0, 0, 0};
         if (e + 8 <= width) {
-            load8_any(x + e, w);
+            cut_words8(load_words8(x + e, true), x + e, w);
         } else {
             for (int u = 0; u < 8 && e + u < width; ++u)
                 w[u >> 1] |= static_cast<uint32_t>(x[e + u]) << (16 * (u & 1));
         }
         const uint32_t byte = step_byte<BF16>(top_of_group(top8(w)));
         *reinterpret_cast<uint2 *>(mine + 8 * lane) = quantise8<BF16>(w, byte);
-        if ((lane & 3) == 0 && e < width) S[p.row * groups + e / 32] = static_cast<uint8_t>(byte);
+        if ((lane & 3) == 0 && e < width) steps[e >> 5] = static_cast<uint8_t>(byte);
         __syncwarp();
-        const int have = static_cast<int>(width - e0 < kSpan ? width - e0 : kSpan);
+        const int have = width - e0 < kSpan ? width - e0 : kSpan;
         const int at = head + 8 * lane;
         if (at + 8 <= have) {
             const uint2 lo = *reinterpret_cast<const uint2 *>(mine + 8 * lane);
@@ -264,25 +264,24 @@ __global__ void __launch_bounds__(kThreads)
 // they may lie in two groups.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int64_t width, uint32_t parts, uint16_t *X,
+    restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int width, uint32_t parts, uint16_t *X,
                     int64_t ldx)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t groups = (width + 31) / 32;
     const RowPart p = row_part((width + 7 + kSpan - 1) / kSpan, parts);
     const char *begin = reinterpret_cast<const char *>(Q), *end = begin + rows * width, *q = begin + p.row * width;
-    const uint8_t *s = S + p.row * groups;
+    const uint8_t *s = S + p.row * ((width + 31) / 32);
     uint16_t *x = X + p.row * ldx;
     const int before = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) >> 1);
-    for (int64_t sp = p.span; sp < p.end; sp += kThreads / 32) {
-        const int64_t e = sp * kSpan + 8 * lane - before;
+    for (int sp = p.span; sp < p.end; sp += kThreads / 32) {
+        const int e = sp * kSpan + 8 * lane - before;
         if (e >= width || e + 8 <= 0) continue;
-        const int64_t g0 = e > 0 ? e / 32 : 0, g1 = (e + 7 < width ? e + 7 : width - 1) / 32;
+        const int g0 = e > 0 ? e >> 5 : 0, g1 = (e + 7 < width ? e + 7 : width - 1) >> 5;
         const uint2 b = load_bytes(q + e, begin, end);
         const float s0 = step_of(s[g0]), s1 = step_of(s[g1]);
-        const uint4 v = restore_piece<BF16>(b, s0, s1, static_cast<int>(32 * (g0 + 1) - e));
+        const uint4 v = restore_piece<BF16>(b, s0, s1, 32 * (g0 + 1) - e);
         if (e >= 0 && e + 8 <= width) {
             *reinterpret_cast<uint4 *>(x + e) = v;
         } else {
@@ -331,7 +330,7 @@ cudaError_t launch(void (*k)(P...), int64_t work, int64_t most, cudaStream_t s, 
     return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
-// Blocks of a row of `values` values.
+// Blocks of a row of `values` values (at most 2^30 and a few: places within a row are 32-bit).
 int64_t row_parts(int64_t values)
 {
     return (values + int64_t(kSpan) * kSpansPerBlock - 1) / (int64_t(kSpan) * kSpansPerBlock);
@@ -356,7 +355,8 @@ cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t 
                       Q, S);
     }
     const int64_t parts = row_parts(width);
-    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * parts * kThreads, 0, s, X, width, ldx,
+    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * parts * kThreads, 0, s, X,
+                  static_cast<int>(width), ldx,
                   static_cast<uint32_t>(parts), Q, S);
 }
 
@@ -369,7 +369,8 @@ cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t
                       Q, S, n, X);
     }
     const int64_t parts = row_parts(width + 7);
-    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * parts * kThreads, 0, s, Q, S, rows, width,
+    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * parts * kThreads, 0, s, Q, S, rows,
+                  static_cast<int>(width),
                   static_cast<uint32_t>(parts), X, ldx);
 }
 

@@ -521,16 +521,39 @@ __device__ __forceinline__ void realign16_steps(const uint4 &lo, const uint4 &hi
     o[3] = __funnelshift_r(v3, v4, sh);
 }
 
-// Eight 16-bit elements at p, any 2-byte alignment.  The two aligned words
-// read each hold one of them.
-__device__ __forceinline__ void load8_any(const uint16_t *p, uint32_t (&o)[4])
+// 16 bytes at p if `on`, else zeros: a predicated load, so that several can
+// be in flight (a branch around each would wait for it).
+__device__ __forceinline__ uint4 ld_global_v4_if(const void *p, bool on)
+{
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(on ? 1u : 0u)
+        : "memory");
+    return v;
+}
+
+// The two aligned 16-byte words that hold the eight 16-bit elements at p, any
+// 2-byte alignment (each word holds one of them); zeros if not `on`.
+struct Words8 {
+    uint4 lo, hi;
+};
+
+__device__ __forceinline__ Words8 load_words8(const uint16_t *p, bool on)
 {
     const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
     const char *a = reinterpret_cast<const char *>(p) - s;
-    const uint4 lo = *reinterpret_cast<const uint4 *>(a);
-    uint4 hi = lo;
-    if (s) hi = *reinterpret_cast<const uint4 *>(a + 16);
-    realign16_steps(lo, hi, s, o);
+    return Words8{ld_global_v4_if(a, on), ld_global_v4_if(a + 16, on && s != 0)};
+}
+
+// The eight elements out of load_words8(p)'s words.
+__device__ __forceinline__ void cut_words8(const Words8 &w, const uint16_t *p, uint32_t (&o)[4])
+{
+    realign16_steps(w.lo, w.hi, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u, o);
 }
 
 // Warpgroup register reallocation (all four warps of a warpgroup execute
