@@ -47,8 +47,10 @@ cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t 
                          uint8_t *S, cudaStream_t s);
 cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t *Q, const uint8_t *S, uint16_t *X,
                             int64_t ldx, cudaStream_t s);
-// Copy of a pitched 16-bit matrix to pitch ldd >= width (columns past width: zeros).
+// Copy of a pitched 16-bit matrix to pitch ldd >= width (columns past width:
+// zeros); with `offsets`, only rows of experts (per_expert each) that have
+// rows of their own to multiply.
 cudaError_t launch_repitch(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,
-                           int sms, cudaStream_t s);
+                           const int32_t *offsets, int64_t per_expert, cudaStream_t s);
 
 }  // namespace gp

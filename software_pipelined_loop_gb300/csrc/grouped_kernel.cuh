@@ -430,9 +430,14 @@ __device__ void last_rows_producer(const GroupedParams &p, const GroupedMaps &ma
         phase ^= 1u;
     }
     if (used) {
-        // The copies have landed, and (unless giving up) the commit that frees the buffer has arrived.
+        // The commit that frees the buffer has arrived, or (giving up) the
+        // copies get a bounded time to land.
         if (ok) ok = __all_sync(0xffffffffu, w.wait(smem_u32(&ctl->last_empty), phase ^ 1u));
-        if (!ok && rank == 0) w.wait_drain(full, phase ^ 1u, kDrainNs);
+        if (!ok) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000ull) {
+            }
+        }
     }
 }
 
@@ -554,14 +559,15 @@ __device__ void grouped_mma(const GroupedParams &p, uint32_t sbase, uint32_t tme
 
 // --------------------------------------------------------------- epilogue
 
-// Two fp32 sums rounded to 16 bits, `lo` in the low half.
+// Two fp32 sums rounded to 16 bits, `lo` in the low half.  (Volatile, so that
+// it stays behind the wait for the tensor memory load it takes its inputs from.)
 __device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi, bool bf16)
 {
     uint32_t r;
     if (bf16)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+        asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
     else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+        asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
     return r;
 }
 

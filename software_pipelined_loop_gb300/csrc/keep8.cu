@@ -293,33 +293,46 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Rows to aligned rows, a warp per row.  With `offsets`, rows of an expert
+// (per_expert rows each) that has no row to multiply are left out: raw bounds
+// that do not rise from e to e + 1 give it none, however they are clamped.
 __global__ void __launch_bounds__(kThreads)
-    repitch_kernel(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd)
+    repitch_kernel(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,
+                   const int32_t *offsets, int64_t per_expert)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t pieces = ldd / 8, n = rows * pieces;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t r = i / pieces, c = (i - r * pieces) * 8;
-        uint32_t o[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t lo = c + 2 * u < width ? src[r * lds + c + 2 * u] : 0u;
-            const uint32_t hi = c + 2 * u + 1 < width ? src[r * lds + c + 2 * u + 1] : 0u;
-            o[u] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint4 *>(dst + r * ldd + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int lane = threadIdx.x & 31;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+    if (r >= rows) return;
+    if (offsets) {
+        const int64_t e = r / per_expert;
+        if (offsets[e + 1] <= offsets[e]) return;
     }
+    const uint16_t *x = src + r * lds;
+    uint16_t *o = dst + r * ldd;
+    const int64_t whole = width / 8;
+    constexpr int FLIGHT = 4;
+    for (int64_t i = lane; i < whole; i += 32 * FLIGHT) {
+        Words8 v[FLIGHT];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) v[u] = load_words8(x + 8 * (i + 32 * u), i + 32 * u < whole);
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            uint32_t w[4];
+            cut_words8(v[u], x + 8 * (i + 32 * u), w);
+            if (i + 32 * u < whole)
+                *reinterpret_cast<uint4 *>(o + 8 * (i + 32 * u)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (8 * whole < ldd && lane < 8) o[8 * whole + lane] = 8 * whole + lane < width ? x[8 * whole + lane] : uint16_t(0);
 }
 
-// `most`: blocks of a grid-stride kernel (0: one per kThreads of work).
 template <class... P, class... A>
-cudaError_t launch(void (*k)(P...), int64_t work, int64_t most, cudaStream_t s, A... args)
+cudaError_t launch(void (*k)(P...), int64_t work, cudaStream_t s, A... args)
 {
-    const int64_t blocks = (work + kThreads - 1) / kThreads;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(static_cast<unsigned>(most == 0 || blocks < most ? blocks : most), 1, 1);
+    c.gridDim = dim3(static_cast<unsigned>((work + kThreads - 1) / kThreads), 1, 1);
     c.blockDim = dim3(kThreads, 1, 1);
     c.stream = s;
     cudaLaunchAttribute a[1];
@@ -351,11 +364,11 @@ cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t 
 {
     if (dense(X, ldx, Q, rows, width)) {
         const int64_t n = rows * (width / 8);
-        return launch(bf16 ? keep8_dense_kernel<true> : keep8_dense_kernel<false>, (n + kFlight - 1) / kFlight, 0, s, X, n,
+        return launch(bf16 ? keep8_dense_kernel<true> : keep8_dense_kernel<false>, (n + kFlight - 1) / kFlight, s, X, n,
                       Q, S);
     }
     const int64_t parts = row_parts(width);
-    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * parts * kThreads, 0, s, X,
+    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * parts * kThreads, s, X,
                   static_cast<int>(width), ldx,
                   static_cast<uint32_t>(parts), Q, S);
 }
@@ -365,19 +378,19 @@ cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t
 {
     if (dense(X, ldx, Q, rows, width)) {
         const int64_t n = rows * (width / 8);
-        return launch(bf16 ? restore8_dense_kernel<true> : restore8_dense_kernel<false>, (n + kFlight - 1) / kFlight, 0, s,
+        return launch(bf16 ? restore8_dense_kernel<true> : restore8_dense_kernel<false>, (n + kFlight - 1) / kFlight, s,
                       Q, S, n, X);
     }
     const int64_t parts = row_parts(width + 7);
-    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * parts * kThreads, 0, s, Q, S, rows,
+    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * parts * kThreads, s, Q, S, rows,
                   static_cast<int>(width),
                   static_cast<uint32_t>(parts), X, ldx);
 }
 
 cudaError_t launch_repitch(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,
-                           int sms, cudaStream_t s)
+                           const int32_t *offsets, int64_t per_expert, cudaStream_t s)
 {
-    return launch(repitch_kernel, rows * (ldd / 8), 8 * sms, s, src, rows, width, lds, dst, ldd);
+    return launch(repitch_kernel, rows * 32, s, src, rows, width, lds, dst, ldd, offsets, per_expert);
 }
 
 }  // namespace gp
