@@ -265,6 +265,7 @@ GEMMPIPE_API int64_t gemmpipe_host_panel_rows(int64_t M);
  *   - type is GEMMPIPE_F16 or GEMMPIPE_BF16, the 16-bit floating-point type
  *     of the activations and weights; sums are held in fp32 and rounded once,
  *     to nearest even, where the result is stored;
+ *   - R, N and K of the products are at most 2^31 - 1024;
  *   - C, the length of a row of the operators named gemmpipe_*, is at most
  *     2^30 (as is K of gemm_grouped_dw8), and rows in 8 bits make at most
  *     2^31 - 1 pieces of 8192 values of one row;
@@ -278,7 +279,8 @@ GEMMPIPE_API int64_t gemmpipe_host_panel_rows(int64_t M);
  *     rows in the library workspace first);
  *   - outputs must not overlap inputs or each other;
  *   - calls are asynchronous on `stream`, on the current device; results
- *     repeat bit for bit;
+ *     repeat bit for bit; in kernel timing the products are main kernels, all
+ *     others auxiliary;
  *   - a size, pitch or type outside its range, a null or misaligned pointer
  *     that is needed, or one the CUDA runtime does not know as device or
  *     managed memory           -> GEMMPIPE_ERR_INVALID_VALUE

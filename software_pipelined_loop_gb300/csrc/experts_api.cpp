@@ -295,10 +295,12 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     return gp::api_launch(true, s, 1, [&] { return v->launch(maps, p, grid, s); });
 }
 
-// Sizes common to the grouped products.
+// Sizes common to the grouped products.  The kernel counts rows and features
+// in 32 bits, up to a tile past the last one.
 bool bad_product(int type, int64_t R, int64_t N, int64_t K, int64_t E)
 {
-    return bad_type(type) || bad_dim(R) || bad_dim(N) || bad_dim(K) || E < 1 || E > gp::kMaxExperts ||
+    constexpr int64_t kMost = kMaxDim - 1023;
+    return bad_type(type) || bad_dim(R) || bad_dim(N) || bad_dim(K) || R > kMost || N > kMost || K > kMost || E < 1 || E > gp::kMaxExperts ||
            (N > 0 && K > kMaxElems / (E * (N + 8)));
 }
 

@@ -79,6 +79,8 @@ def test_sizes_past_the_address_range(lib):
     assert lib.gemm_grouped(0, BIG, BIG, 8, 1, FAKE, 8, FAKE, FAKE, FAKE, BIG, None) == BAD      # 2^62 elements of Y
     assert lib.gemm_grouped(0, 8, BIG, BIG, 1, FAKE, BIG, FAKE, FAKE, FAKE, BIG, None) == BAD    # ... of W
     assert lib.gemm_grouped_dw(0, 8, 1 << 23, 1 << 23, 1024, FAKE, 1 << 23, FAKE, 1 << 23, FAKE, FAKE, None) == BAD
+    assert lib.gemm_grouped(0, BIG - 1022, 8, 8, 1, FAKE, 8, FAKE, FAKE, FAKE, 8, None) == BAD   # a tile past 2^31
+    assert lib.gemmpipe_dispatch(0, 1, 1, (1 << 30) + 1, FAKE, 1 << 31, FAKE, FAKE, FAKE, 1 << 31, None) == BAD
     assert lib.gemmpipe_keep8(0, BIG, BIG, FAKE, BIG, FAKE, FAKE, None) == BAD
 
 
