@@ -362,7 +362,10 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dx(int type, int64_t R, int64_t N, i
 
 /* Its gradient to the weights: dW[e] = sum over the expert's rows of
  * X[r]^T . dY[r] (E x K x N, dense, overwritten; zero for an expert without
- * rows).  Rows that no expert has are not read into any result. */
+ * rows).  Rows that no expert has are not read into any result.
+ * Where the matrices have fewer tiles than the machine has CTA pairs, the sum
+ * of an expert of many rows is split among pairs: fp32 partial sums in the
+ * library workspace, added in a fixed order. */
 GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw(int type, int64_t R, int64_t N, int64_t K, int64_t E, const void *X,
                                                int64_t ldx, const void *dY, int64_t lddy, const int32_t *offsets,
                                                void *dW, gemmpipe_stream_t stream);

@@ -76,6 +76,9 @@ struct Rows {         // a 16-bit row operand
 };
 
 bool tma_ok(const void *p, int64_t ld) { return !misaligned(p, 16) && ld % 8 == 0; }
+int64_t round64(int64_t x) { return (x + 63) / 64 * 64; }
+constexpr int64_t kLeastSplit = 2048;  // rows of a part, at least: a part costs about 4 us more than its products
+
 int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
@@ -212,7 +215,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     if (!v) return GEMMPIPE_ERR_INTERNAL;
     if (v->smem_bytes > d.smem_optin) return GEMMPIPE_ERR_UNSUPPORTED_DEVICE;
     const int64_t f_tiles = (features + v->tile_f - 1) / v->tile_f;
-    if (row_tiles > kMaxDim / f_tiles) return GEMMPIPE_ERR_INVALID_VALUE;
+    if (row_tiles > kMaxDim / 4 / f_tiles) return GEMMPIPE_ERR_INVALID_VALUE;
 
     // Operands that TMA cannot describe are copied to aligned rows.
     const bool pad_x = q.Q == nullptr && !tma_ok(q.rows.p, q.rows.ld);
@@ -222,10 +225,23 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     const int64_t need_x = pad_x || q.Q ? align256(2 * q.R * round8(q.rows.width)) : 0;
     const int64_t need_g = pad_g ? align256(2 * q.R * round8(q.grad.width)) : 0;
     const int64_t need_w = pad_w ? align256(2 * q.E * q.K * wld) : 0;
+    // Weight gradient of fewer tiles per matrix than CTA pairs: an expert of
+    // far more rows than the others would leave most pairs idle while a few
+    // sum them, so sums longer than 1.5 times a pair's even share are split.
+    const int64_t units = v->max_units();
+    if (units < 1) return GEMMPIPE_ERR_LAUNCH;
+    int64_t split_rows = 0, slots = 0;
+    const int64_t matrix_tiles = weights ? f_tiles * ((q.K + bn - 1) / bn) : 0;
+    if (weights && matrix_tiles < units) {
+        split_rows = round64(q.R * matrix_tiles / units + 1);
+        if (split_rows < kLeastSplit) split_rows = kLeastSplit;
+        slots = (2 * q.R / split_rows + 1) * matrix_tiles;
+        if (split_rows + split_rows / 2 >= q.R || slots > gp::kMaxPartSlots) split_rows = slots = 0;
+    }
     gemmpipe_status_t st = GEMMPIPE_OK;
     const uint16_t *W = q.W;
+    void *ws = nullptr;
     if (need_x + need_g + need_w > 0) {
-        void *ws = nullptr;
         if ((st = gp::api_workspace(d.dev, s, need_x + need_g + need_w, &ws)) != GEMMPIPE_OK) return st;
         uint16_t *to_x = static_cast<uint16_t *>(ws), *to_g = to_x + need_x / 2, *to_w = to_g + need_g / 2;
         Pad pads[2];  // of a rows product X or dY, and W; of a weight gradient X and dY
@@ -285,12 +301,23 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
     p.vec_store = tma_ok(q.out, q.ldo) ? 1 : 0;
     p.timeout_ns = 2000000000ull + static_cast<uint64_t>((weights ? q.R : p.depth) / 64 + 1) * 10000ull;
     p.stall_kb = gp::api_take_stall(&p.timeout_ns);
+    if (split_rows > 0) {
+        // A count per slot and epilogue warp of both CTAs, then 256 KiB a slot.
+        constexpr int64_t kCounts = gp::kMaxPartSlots * 16 * 8;
+        void *parts = nullptr;
+        if ((st = gp::api_parts_workspace(d.dev, s, kCounts, slots * 256 * 256 * 4, &parts)) != GEMMPIPE_OK) return st;
+        p.part_counts = static_cast<unsigned long long *>(parts);
+        p.parts = reinterpret_cast<float *>(static_cast<char *>(parts) + kCounts);
+        p.split_rows = static_cast<int32_t>(split_rows);
+        p.epoch = gp::api_epoch();
+    }
     if (gp::status_word(&p.status) != cudaSuccess) {
         cudaGetLastError();
         return GEMMPIPE_ERR_LAUNCH;
     }
-    const int64_t units = v->max_units(), tiles = row_tiles * f_tiles;
-    if (units < 1) return GEMMPIPE_ERR_LAUNCH;
+    // Tiles at most: whole sums, and the parts of split ones.
+    const int64_t tiles = row_tiles * f_tiles + slots;
+    p.sorted = weights && tiles > units && q.E > 1 && q.E <= gp::kMaxSorted ? 1 : 0;
     const int grid = static_cast<int>((v->pair ? 2 : 1) * (tiles < units ? tiles : units));
     return gp::api_launch(true, s, 1, [&] { return v->launch(maps, p, grid, s); });
 }

@@ -516,7 +516,7 @@ struct Workspace {
     int64_t bytes = 0;
 };
 // Kinds of workspace per (device, stream).
-enum WsKind { kWsOperands = 0, kWsSplit = 1, kWsHost = 2 };
+enum WsKind { kWsOperands = 0, kWsSplit = 1, kWsHost = 2, kWsParts = 3 };
 std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_ws;
 
 // The (device, stream) workspace of one kind, at least `bytes` long.  A new
@@ -803,6 +803,17 @@ gemmpipe_status_t api_check_pointer(const void *p, int align) { return check_poi
 gemmpipe_status_t api_workspace(int dev, cudaStream_t s, int64_t bytes, void **out)
 {
     return workspace(dev, s, bytes, out);
+}
+
+gemmpipe_status_t api_parts_workspace(int dev, cudaStream_t s, int64_t counts, int64_t bytes, void **out)
+{
+    return workspace(dev, s, counts + bytes, out, kWsParts, counts);
+}
+
+uint32_t api_epoch()
+{
+    uint32_t e = g_epoch.fetch_add(1) + 1;
+    return e != 0 ? e : g_epoch.fetch_add(1) + 1;
 }
 
 gemmpipe_status_t api_timed_launch(bool gemm, cudaStream_t s, int kernels, cudaError_t (*fn)(void *), void *ctx)

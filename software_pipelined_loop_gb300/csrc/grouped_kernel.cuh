@@ -77,7 +77,7 @@ struct GroupedCfg {
     static constexpr int STAGING_OFF = LAST_OFF + LAST_BYTES;
     static constexpr int STAGING_BYTES = EPI_WARPS * EPI_BLOCK * QF * 2;
     static constexpr int TABLE_OFF = STAGING_OFF + STAGING_BYTES;
-    static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2);
+    static constexpr int TABLE_BYTES = 2 * 4 * (kMaxExperts + 2) + (MODE == kWeights ? kMaxSorted : 0);
     static constexpr int CTL_OFF = TABLE_OFF + TABLE_BYTES;
     static constexpr int CTL_BYTES = 8 * (2 * STAGES + 7) + 16;
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + CTL_BYTES;
@@ -104,28 +104,60 @@ struct GroupedCtl {
 };
 
 // Row bounds and tile numbers of the experts, made by every CTA at its
-// start: start[e] (e <= E) and first[e], the number of tiles before expert e.
+// start: start[e] (e <= E) and first[i], the tiles before the i-th expert in
+// the order of work (their own order; weight gradient: order[i]).
 struct GroupTable {
     int32_t *start;
     int32_t *first;
+    uint8_t *order;  // null: their own order
     int E;
 };
+
+// Weight gradient: an expert's rows are summed in one part, or, where the
+// matrices have too few tiles for the machine (split_rows > 0) and the expert
+// has more than 1.5 split_rows rows, in parts of at most split_rows rows each
+// (a multiple of 64, but for the last one's).
+__device__ __forceinline__ int32_t rows_of_part(int32_t rows, int32_t split_rows)
+{
+    if (split_rows == 0 || rows - split_rows <= split_rows / 2) return rows;
+    const int32_t parts = (rows - 1) / split_rows + 1;
+    return ((rows - 1) / parts + 64) / 64 * 64;
+}
+
+__device__ __forceinline__ int32_t parts_of(int32_t rows, int32_t split_rows)
+{
+    const int32_t part = rows_of_part(rows, split_rows);
+    return part == rows ? 1 : (rows - 1) / part + 1;
+}
+
+// Slot of an expert's first part of the first tile, in units of one matrix's
+// tiles.  An expert of x = rows / split_rows > 1 has at most ceil(x) <=
+// floor(2 x) parts, so experts do not meet.
+__device__ __forceinline__ int32_t first_slot(int32_t start, int32_t split_rows)
+{
+    return static_cast<int32_t>(2 * static_cast<int64_t>(start) / split_rows);
+}
+
+// Expert of the i-th place in the order of work.
+template <int MODE>
+__device__ __forceinline__ int expert_at(const GroupTable &t, int i)
+{
+    return MODE == kWeights && t.order ? t.order[i] : i;
+}
 
 // All threads of the CTA.  The bounds are clamped to [0, rows] and made
 // non-decreasing, so that nothing they hold can send an access outside.
 template <class Cfg>
 __device__ void make_table(const GroupedParams &p, GroupTable t)
 {
+    const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i <= t.E; i += Cfg::THREADS) {
         const int64_t v = p.offsets[i];
         t.start[i] = static_cast<int32_t>(v < 0 ? 0 : (v > p.rows ? p.rows : v));
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        const int32_t f_tiles = static_cast<int32_t>((p.features + Cfg::TILE_F - 1) / Cfg::TILE_F);
-        const int32_t w_tiles = static_cast<int32_t>((p.out_rows + Cfg::BN - 1) / Cfg::BN);
-        int32_t top = 0, sum = 0;
+        int32_t top = 0;
         for (int b = 0; b <= t.E; b += 32) {
             const int i = b + lane;
             int32_t v = i <= t.E ? t.start[i] : 0;
@@ -135,52 +167,82 @@ __device__ void make_table(const GroupedParams &p, GroupTable t)
                 const int32_t u = __shfl_up_sync(0xffffffffu, v, d);
                 if (lane >= d && u > v) v = u;
             }
-            // This expert's end, the next entry's bound: tiles need it, so
-            // entry i's tiles are counted from v(i) - v(i - 1).
-            int32_t prev = __shfl_up_sync(0xffffffffu, v, 1);
-            if (lane == 0) prev = top;
+            if (i <= t.E) t.start[i] = v;
+            top = __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    if (Cfg::MODE == kWeights && t.order) {
+        // Longest sums first (first[] holds their lengths meanwhile).
+        for (int i = threadIdx.x; i < t.E; i += Cfg::THREADS)
+            t.first[i] = rows_of_part(t.start[i + 1] - t.start[i], p.split_rows);
+        __syncthreads();
+        for (int i = threadIdx.x; i < t.E; i += Cfg::THREADS) {
+            const int32_t mine = t.first[i];
+            int place = 0;
+#pragma unroll 8
+            for (int k = 0; k < t.E; ++k) {
+                const int32_t other = t.first[k];
+                place += other > mine || (other == mine && k < i);
+            }
+            t.order[place] = static_cast<uint8_t>(i);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x < 32) {
+        const int32_t f_tiles = static_cast<int32_t>((p.features + Cfg::TILE_F - 1) / Cfg::TILE_F);
+        const int32_t w_tiles = static_cast<int32_t>((p.out_rows + Cfg::BN - 1) / Cfg::BN);
+        int32_t sum = 0;
+        for (int b = 0; b < t.E; b += 32) {
             int32_t n = 0;
-            if (i >= 1 && i <= t.E)
-                n = f_tiles * (Cfg::MODE == kWeights ? w_tiles : (v - prev + Cfg::BN - 1) / Cfg::BN);
+            if (b + lane < t.E) {
+                const int e = expert_at<Cfg::MODE>(t, b + lane);
+                const int32_t rows = t.start[e + 1] - t.start[e];
+                n = f_tiles * (Cfg::MODE == kWeights ? w_tiles * parts_of(rows, p.split_rows)
+                                                     : (rows + Cfg::BN - 1) / Cfg::BN);
+            }
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int32_t u = __shfl_up_sync(0xffffffffu, n, d);
                 if (lane >= d) n += u;
             }
-            if (i <= t.E) {
-                t.start[i] = v;
-                t.first[i] = sum + n;  // tiles of the experts before i
-            }
-            top = __shfl_sync(0xffffffffu, v, 31);
+            if (b + lane < t.E) t.first[b + lane + 1] = sum + n;
             sum += __shfl_sync(0xffffffffu, n, 31);
         }
+        if (lane == 0) t.first[0] = 0;
     }
     __syncthreads();
 }
 
 struct GroupedTile {
     int e;           // expert
-    int32_t row0;    // its first row
-    int32_t count;   // its rows
+    int32_t row0;    // its first row (weight gradient: of the part)
+    int32_t count;   // its rows (of the part)
     int32_t f0;      // first feature of the tile
     int32_t c0;      // first output row of the tile, within the expert
     int32_t cols;    // the MMA's columns: the tile's output rows, rounded up
     int32_t kbs;     // k-blocks in the ring
     int32_t last;    // products in the last of them (1 .. 64)
     int32_t extra;   // weight gradient: rows past the last whole 16 (0 .. 15)
+    int32_t parts;   // weight gradient: parts of the expert's rows (1: the sums go to the output)
+    int32_t slot;    // ... where this part's sums go
+    int32_t slot0;   // ... and the first part's; `tiles` apart
+    int32_t tiles;
 };
 
-// Tiles of a unit (CTA or pair): round-robin, experts in order, features
-// fastest, so that tiles in flight share rows and a few experts' weights.
+// Tiles of a unit (CTA or pair).  Rows: round-robin, experts in order,
+// features fastest, so that tiles in flight share rows and a few experts'
+// weights.  Weight gradient: the tiles differ as the experts' rows do, so they
+// are dealt out longest first, in turns of alternating direction.
 template <class Cfg>
 struct GroupedIter {
     GroupTable t;
-    int32_t pos, step;
-    int e;
+    int32_t pos, unit, units, turn;
+    int at;  // place of the latest tile's expert in the order of work
     int32_t f_tiles;
 
     __device__ __forceinline__ GroupedIter(const GroupedParams &p, GroupTable tab)
-        : t(tab), pos(blockIdx.x / Cfg::CLUSTER), step(gridDim.x / Cfg::CLUSTER), e(0),
+        : t(tab), pos(blockIdx.x / Cfg::CLUSTER), unit(pos), units(gridDim.x / Cfg::CLUSTER), turn(0), at(0),
           f_tiles(static_cast<int32_t>((p.features + Cfg::TILE_F - 1) / Cfg::TILE_F))
     {
     }
@@ -188,10 +250,10 @@ struct GroupedIter {
     __device__ __forceinline__ bool next(const GroupedParams &p, GroupedTile &w)
     {
         if (pos >= t.first[t.E]) return false;
-        if (pos >= t.first[e + 1]) {
-            // The expert of this tile: the last one with first[e] <= pos.  (A
-            // step at a time costs 1 us of a 64-expert call of one token.)
-            int below = e + 1, above = t.E;
+        if (pos >= t.first[at + 1]) {
+            // The expert of this tile: the last place with first[i] <= pos.
+            // (A step at a time costs 1 us of a 64-expert call of one token.)
+            int below = at + 1, above = t.E;
             while (above - below > 1) {
                 const int mid = (below + above) >> 1;
                 if (t.first[mid] <= pos)
@@ -199,14 +261,33 @@ struct GroupedIter {
                 else
                     above = mid;
             }
-            e = below;
+            at = below;
         }
-        const int32_t in = pos - t.first[e];
-        pos += step;
+        int32_t in = pos - t.first[at];
+        if constexpr (Cfg::MODE == kWeights) {
+            ++turn;
+            pos = turn * units + ((turn & 1) ? units - 1 - unit : unit);
+        } else {
+            pos += units;
+        }
+        w.e = expert_at<Cfg::MODE>(t, at);
+        w.row0 = t.start[w.e];
+        w.count = t.start[w.e + 1] - w.row0;
+        w.parts = 1;
+        if constexpr (Cfg::MODE == kWeights) {
+            const int32_t rows = rows_of_part(w.count, p.split_rows);
+            if (rows < w.count) {
+                w.parts = (w.count - 1) / rows + 1;
+                w.tiles = f_tiles * static_cast<int32_t>((p.out_rows + Cfg::BN - 1) / Cfg::BN);
+                const int32_t part = in / w.tiles;
+                in -= part * w.tiles;
+                w.slot0 = first_slot(w.row0, p.split_rows) * w.tiles + in;
+                w.slot = w.slot0 + part * w.tiles;
+                w.row0 += part * rows;
+                w.count = w.count - part * rows < rows ? w.count - part * rows : rows;
+            }
+        }
         const int32_t c = in / f_tiles;
-        w.e = e;
-        w.row0 = t.start[e];
-        w.count = t.start[e + 1] - w.row0;
         w.f0 = (in - c * f_tiles) * Cfg::TILE_F;
         if constexpr (Cfg::MODE == kWeights) {
             w.c0 = c * Cfg::BN;
@@ -571,17 +652,91 @@ __device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi, bool bf
     return r;
 }
 
+// Stores a block of n (up to EPI_BLOCK) output rows x QF features whose fp32
+// sums a warp holds as tensor memory gives them (lanes 0-15 of its quarter in
+// lo, 16-31 in hi): rounded once to the output's type and turned through the
+// warp's staging tile (16-byte chunks, XOR-swizzled by row: free of bank
+// conflicts both ways), so that a store instruction writes 64 contiguous
+// bytes of 8 rows.  `o` is the block's first element, `left` the features
+// from there to the end of a row.
+template <class Cfg>
+__device__ __forceinline__ void store_block(const GroupedParams &p, uint32_t stg, int lane,
+                                            const uint32_t (&lo)[Cfg::EPI_BLOCK / 2],
+                                            const uint32_t (&hi)[Cfg::EPI_BLOCK / 2], uint16_t *o, int n, int64_t left)
+{
+    constexpr int NB = Cfg::EPI_BLOCK, QF = Cfg::QF;
+    constexpr int ROW = QF * 2, CHUNKS = QF / 8;  // bytes and 16-byte chunks of a staged row
+    const bool bf16 = p.bf16 != 0;
+    // Address of chunk k of staged row c.
+    auto staged = [stg](int c, int k) {
+        return stg + c * ROW + ((k ^ (CHUNKS == 4 ? (c >> 1) & 3 : (c >> 2) & 1)) << 4);
+    };
+    if constexpr (QF == 32) {
+        // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
+#pragma unroll
+        for (int i = 0; i < NB / 8; ++i)
+            stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
+                              round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
+                              round_pair(hi[4 * i], hi[4 * i + 1], bf16),
+                              round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
+    } else {
+        // Sixteen columns: the first 8 columns' two pieces of 8 features, then the others'.
+        static_assert(QF == 32 || NB == 16, "one store");
+        stmatrix_x4_trans(staged((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1), round_pair(lo[0], lo[1], bf16),
+                          round_pair(lo[2], lo[3], bf16), round_pair(lo[4], lo[5], bf16),
+                          round_pair(lo[6], lo[7], bf16));
+    }
+    __syncwarp();
+    if (p.vec_store && QF <= left) {
+        // 16-byte pieces, CHUNKS lanes to a row.
+        constexpr int ROWS = 32 / CHUNKS;
+        o += (lane / CHUNKS) * p.ldo + (lane % CHUNKS) * 8;
+#pragma unroll
+        for (int i = 0; i < NB; i += ROWS)
+            if (i + lane / CHUNKS < n)
+                *reinterpret_cast<uint4 *>(o + i * p.ldo) = ld_shared_v4(staged(i + lane / CHUNKS, lane % CHUNKS));
+    } else if (lane < QF && lane < left) {
+        // A feature per lane, row by row.  (Two rows at a time in the row's
+        // own 4-byte words: 179 us where this takes 112.)
+#pragma unroll 8
+        for (int c = 0; c < n; ++c) o[c * p.ldo + lane] = ld_shared_u16(staged(c, lane >> 3) + (lane & 7) * 2);
+    }
+    __syncwarp();
+}
+
+// Where a warp's block j of a slot's sums begins: 32 lanes of one register
+// after another, in the order of lo and hi.
+template <class Cfg>
+__device__ __forceinline__ float *part_of(const GroupedParams &p, int32_t slot, uint32_t rank, int e, int block)
+{
+    constexpr int BLOCKS = Cfg::EPI_COLS / Cfg::EPI_BLOCK;
+    const int64_t at = ((static_cast<int64_t>(slot) * Cfg::CLUSTER + rank) * Cfg::EPI_WARPS + e) * BLOCKS + block;
+    return p.parts + at * (Cfg::EPI_BLOCK * 32);
+}
+
+// Counts a finished part; true for the last of `parts`, which leaves the
+// counter at zero for the next launch.  A count is of one launch only (its
+// epoch is beside it), so that a launch that gave up leaves nothing behind.
+__device__ __forceinline__ bool last_part(unsigned long long *count, uint32_t epoch, int parts)
+{
+    unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(count), want;
+    for (;;) {  // at most as often as there are other parts
+        const uint32_t n = (seen >> 32) == epoch ? static_cast<uint32_t>(seen) + 1 : 1u;
+        const bool last = n == static_cast<uint32_t>(parts);
+        want = last ? 0ull : (static_cast<unsigned long long>(epoch) << 32) | n;
+        const unsigned long long was = atomicCAS(count, seen, want);
+        if (was == seen) return last;
+        seen = was;
+    }
+}
+
 // Accumulator lane l of warp quarter q is feature f0 + 32 q + l, column c the
-// output row c0 + c.  The sums are rounded once, to the operands' type, and
-// turned through a per-warp staging tile of EPI_BLOCK rows x 32 features
-// (16-byte chunks, XOR-swizzled by row: free of bank conflicts both ways), so
-// that a store instruction writes 64 contiguous bytes of 8 output rows.  (One
-// tile per warpgroup, 256 contiguous bytes of 2 rows, and bulk tensor copies
-// out of the staging tiles measured the same.)  While the output leaves, the
-// operands come in more slowly: the operands' copies and the MMA's reads
-// already take the 128 bytes a cycle that shared memory gives.  Weight
-// gradient of 8192 tokens x 4 on 32 experts, 4096 x 1536: 270 us, 233 us with
-// nothing stored.
+// output row c0 + c.  (One staging tile per warpgroup, 256 contiguous bytes of
+// 2 rows, and bulk tensor copies out of the staging tiles measured the same.)
+// While the output leaves, the operands come in more slowly: the operands'
+// copies and the MMA's reads already take the 128 bytes a cycle that shared
+// memory gives.  Weight gradient of 8192 tokens x 4 on 32 experts,
+// 4096 x 1536: 270 us, 233 us with nothing stored.
 template <class Cfg>
 __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
                                  GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, int warp, int lane,
@@ -589,14 +744,8 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
 {
     const int e = warp - Cfg::EPI_WARP0;
     const int q = warp & 3, h = e >> 2;
-    const bool bf16 = p.bf16 != 0;
     constexpr int NB = Cfg::EPI_BLOCK, QF = Cfg::QF;
-    constexpr int ROW = QF * 2, CHUNKS = QF / 8;  // bytes and 16-byte chunks of a staged row
-    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * ROW);
-    // Address of chunk k of staged row c.
-    auto staged = [stg](int c, int k) {
-        return stg + c * ROW + ((k ^ (CHUNKS == 4 ? (c >> 1) & 3 : (c >> 2) & 1)) << 4);
-    };
+    const uint32_t stg = sbase + Cfg::STAGING_OFF + e * (NB * QF * 2);
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
     uint16_t *out = static_cast<uint16_t *>(p.out);
@@ -646,40 +795,55 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
                 tmem_wait_ld();
                 if (j + NB >= to) release();
             }
-            if constexpr (QF == 32) {
-                // Per 8 columns: lane / 8 = 8 features, lane % 8 = column.
+            if (Cfg::MODE == kWeights && t.parts > 1) {
+                // A part of a sum: as it is, 128 contiguous bytes a register.
+                float *o = part_of<Cfg>(p, t.slot, rank, e, (j - from) / NB) + lane;
 #pragma unroll
-                for (int i = 0; i < NB / 8; ++i)
-                    stmatrix_x4_trans(staged(8 * i + (lane & 7), lane >> 3), round_pair(lo[4 * i], lo[4 * i + 1], bf16),
-                                      round_pair(lo[4 * i + 2], lo[4 * i + 3], bf16),
-                                      round_pair(hi[4 * i], hi[4 * i + 1], bf16),
-                                      round_pair(hi[4 * i + 2], hi[4 * i + 3], bf16));
-            } else {
-                // Sixteen columns: the first 8 columns' two pieces of 8 features, then the others'.
-                static_assert(QF == 32 || NB == 16, "one store");
-                stmatrix_x4_trans(staged((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1), round_pair(lo[0], lo[1], bf16),
-                                  round_pair(lo[2], lo[3], bf16), round_pair(lo[4], lo[5], bf16),
-                                  round_pair(lo[6], lo[7], bf16));
+                for (int i = 0; i < NB / 2; ++i) {
+                    o[32 * i] = __uint_as_float(lo[i]);
+                    o[32 * (NB / 2 + i)] = __uint_as_float(hi[i]);
+                }
+                continue;
             }
-            __syncwarp();
             const int n = to - j < NB ? static_cast<int>(to - j) : NB;
-            uint16_t *o = out + (base + t.c0 + j) * p.ldo + f0;
-            if (p.vec_store && f0 + QF <= p.features) {
-                // 16-byte pieces, CHUNKS lanes to a row.
-                constexpr int ROWS = 32 / CHUNKS;
-                o += (lane / CHUNKS) * p.ldo + (lane % CHUNKS) * 8;
+            store_block<Cfg>(p, stg, lane, lo, hi, out + (base + t.c0 + j) * p.ldo + f0, n, p.features - f0);
+        }
+        if constexpr (Cfg::MODE == kWeights) {
+            if (t.parts > 1 && from < to) {
+                // Whichever part of these sums comes last adds them all, in
+                // the parts' order, and stores them: no warp waits for another.
+                __threadfence();
+                __syncwarp();
+                bool last = false;
+                if (lane == 0)
+                    last = last_part(&p.part_counts[(t.slot0 * Cfg::CLUSTER + rank) * Cfg::EPI_WARPS + e], p.epoch,
+                                     t.parts);
+                if (__any_sync(0xffffffffu, last)) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int32_t j = from; j < to; j += NB) {
+                        float sum[NB];
 #pragma unroll
-                for (int i = 0; i < NB; i += ROWS)
-                    if (i + lane / CHUNKS < n)
-                        *reinterpret_cast<uint4 *>(o + i * p.ldo) =
-                            ld_shared_v4(staged(i + lane / CHUNKS, lane % CHUNKS));
-            } else if (lane < QF && f0 + lane < p.features) {
-                // A feature per lane, row by row.  (Two rows at a time in the
-                // row's own 4-byte words: 179 us where this takes 112.)
-#pragma unroll 8
-                for (int c = 0; c < n; ++c) o[c * p.ldo + lane] = ld_shared_u16(staged(c, lane >> 3) + (lane & 7) * 2);
+                        for (int i = 0; i < NB; ++i) sum[i] = 0.f;
+#pragma unroll 1
+                        for (int k = 0; k < t.parts; ++k) {
+                            const float *v =
+                                part_of<Cfg>(p, t.slot0 + k * t.tiles, rank, e, (j - from) / NB) + lane;
+#pragma unroll
+                            for (int i = 0; i < NB; ++i) sum[i] += __ldcg(v + 32 * i);
+                        }
+                        uint32_t lo[NB / 2], hi[NB / 2];
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) {
+                            lo[i] = __float_as_uint(sum[i]);
+                            hi[i] = __float_as_uint(sum[NB / 2 + i]);
+                        }
+                        const int n = to - j < NB ? static_cast<int>(to - j) : NB;
+                        store_block<Cfg>(p, stg, lane, lo, hi, out + (base + t.c0 + j) * p.ldo + f0, n,
+                                         p.features - f0);
+                    }
+                }
             }
-            __syncwarp();
         }
         if (!empty) {
             acc ^= 1u;
@@ -713,6 +877,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     GroupTable tab;
     tab.start = reinterpret_cast<int32_t *>(smem + Cfg::TABLE_OFF);
     tab.first = tab.start + kMaxExperts + 2;
+    tab.order = Cfg::MODE == kWeights && p.sorted ? reinterpret_cast<uint8_t *>(tab.first + kMaxExperts + 2) : nullptr;
     tab.E = p.experts;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

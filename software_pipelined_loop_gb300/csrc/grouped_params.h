@@ -10,6 +10,8 @@ namespace gp {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
+constexpr int kMaxSorted = 256;  // experts up to which the weight gradient sorts its work
+constexpr int kMaxPartSlots = 512;
 
 enum GroupedMode { kRows = 0, kRowsT = 1, kWeights = 2 };
 
@@ -33,6 +35,11 @@ struct GroupedParams {
     int64_t depth;           // products summed per value (weight gradient: the expert's rows instead)
     void *out;
     int64_t ldo;             // output row pitch in elements
+    float *parts;            // weight gradient: sums of parts of an expert's rows, a slot per tile
+    unsigned long long *part_counts;  // ... finished parts, one count per slot and epilogue warp of both CTAs
+    uint32_t epoch;          // ... of this launch
+    int32_t split_rows;      // ... an expert of more than 1.5 times as many is summed in parts (0: none is)
+    int sorted;              // ... the longest sums go first (up to kMaxSorted experts)
     int bf16;
     int vec_store;           // output base and pitch allow 16-byte stores
     int a_groups, b_groups;  // 1: the operand's tensor map is in 64-column groups (one copy per k-block)

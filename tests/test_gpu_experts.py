@@ -147,6 +147,23 @@ def test_gradient_to_weights(counts, size, ty):
     check_close(dW, exact, product_bound(u, max(c), exact, mag), "gradient to the weights")
 
 
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("size", [(64, 128), (300, 257), (1, 8), (512, 640)], ids=str)
+@pytest.mark.parametrize("counts", [[5000], [1025, 0, 7, 3333, 1024, 1], [40] * 300 + [2500, 0, 1500]], ids=len)
+def test_gradient_to_weights_in_parts(counts, size, ty):
+    # Matrices of few tiles and experts of many rows: their sums are split (300 experts: too many to sort).
+    code, dtype, u = TYPES[ty]
+    K, N = size
+    off, R, X, dY, W = setup(counts, K, N, dtype, seed=17, head=1, unused=33)
+    dW = torch.full((len(counts), K, N), 3.0, dtype=dtype, device="cuda")
+    gp.gemm_grouped_dw(code, R, N, K, len(counts), X, K, dY, N, off, dW)
+    exact, mag = weights_reference(off, X, dY)
+    check_close(dW, exact, product_bound(u, max(counts), exact, mag))
+    again = torch.empty_like(dW)
+    gp.gemm_grouped_dw(code, R, N, K, len(counts), X, K, dY, N, off, again)
+    assert torch.equal(dW, again)
+
+
 @pytest.mark.parametrize("size", [(64, 128), (200, 136), (129, 257)], ids=str)
 def test_rows_of_other_experts_are_not_mixed(size):
     # Every other expert's rows are infinite or NaN: the rest stay finite and right.
