@@ -28,7 +28,7 @@
 // warp of its own loads that buffer as soon as the previous tile has left it,
 // a whole tile ahead: these rows in the ring, whether cleared there by a warp
 // or loaded in pieces, held the MMAs up for 0.9 us a tile (8192 tokens x 4 on
-// 32 experts, 4096 x 1536: 309 us).
+// 32 experts, 4096 x 1536: 309 us against 275).
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -733,10 +733,11 @@ __device__ __forceinline__ bool last_part(unsigned long long *count, uint32_t ep
 // Accumulator lane l of warp quarter q is feature f0 + 32 q + l, column c the
 // output row c0 + c.  (One staging tile per warpgroup, 256 contiguous bytes of
 // 2 rows, and bulk tensor copies out of the staging tiles measured the same.)
-// While the output leaves, the operands come in more slowly: the operands'
-// copies and the MMA's reads already take the 128 bytes a cycle that shared
-// memory gives.  Weight gradient of 8192 tokens x 4 on 32 experts,
-// 4096 x 1536: 270 us, 233 us with nothing stored.
+// An accumulator is handed back with relaxed arrivals: a release at cluster
+// scope waits for the warp's stores of the tile before, and held the MMAs up
+// for it.  Weight gradient of 8192 tokens x 2 on 32 experts, 2048 x 1024:
+// 43 us, 60 with releases, 31 with nothing stored; of 8192 x 4 on 32 experts,
+// 4096 x 1536: 250, 261 and 233 us.
 template <class Cfg>
 __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,
                                  GroupedCtl<Cfg::STAGES> *ctl, GroupTable tab, const Waiter &w, int warp, int lane,
@@ -772,7 +773,7 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
             __syncwarp();
             if (lane == 0) {
                 if constexpr (Cfg::PAIR)
-                    mbar_arrive_cluster(tempty0 + 8 * acc);
+                    mbar_arrive_cluster_relaxed(tempty0 + 8 * acc);
                 else
                     mbar_arrive(tempty0 + 8 * acc);
             }
