@@ -253,6 +253,58 @@ struct RowShape {
     int64_t rows;  // tokens * top_k: entries of the row table outside [0, rows) are passed over
 };
 
+// The kernels of a warp per choice: small blocks, so that an SM refills as
+// soon as two rows are done (256 threads: 145 us where 64 take 129).
+constexpr int kSlotThreads = 64;
+
+// A warp writes 31 aligned 16-byte words of an output row at a time and reads
+// the input row in the input's own: lane l loads the word that holds the
+// first element of output word l, lane l + 1 has the rest.  Words off the row
+// are not read.
+constexpr int kWarpWords = 31;
+
+__device__ __forceinline__ int misalign8(const uint16_t *x, int e)
+{
+    return static_cast<int>(((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)) >> 1) + static_cast<uint32_t>(e)) & 7u);
+}
+
+__device__ __forceinline__ uint4 load_word(const uint16_t *x, int e, int width, bool on)
+{
+    const int at = e - misalign8(x, e);
+    return ld_global_v4_if(x + at, on && at > -8 && at < width);
+}
+
+// Elements [e, e + 8) of x out of the warp's words (all lanes call it).
+__device__ __forceinline__ Piece join_words(const uint4 &lo, const uint16_t *x, int e)
+{
+    uint4 hi;
+    hi.x = __shfl_down_sync(0xffffffffu, lo.x, 1);
+    hi.y = __shfl_down_sync(0xffffffffu, lo.y, 1);
+    hi.z = __shfl_down_sync(0xffffffffu, lo.z, 1);
+    hi.w = __shfl_down_sync(0xffffffffu, lo.w, 1);
+    Piece r;
+    realign16_steps(lo, hi, 2u * static_cast<uint32_t>(misalign8(x, e)), r.w);
+    return r;
+}
+
+// Element of the first aligned word of an output row, at or before 0.
+__device__ __forceinline__ int first_word(const uint16_t *row)
+{
+    return -static_cast<int>((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u) >> 1);
+}
+
+// Elements [e, e + 8) of the output row, those that it has.
+__device__ __forceinline__ void store_word(uint16_t *row, int e, int width, const Piece &p)
+{
+    if (e >= 0 && e + 8 <= width) {
+        store_wide(row + e, p);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (e + u >= 0 && e + u < width) row[e + u] = static_cast<uint16_t>(p.w[u >> 1] >> (16 * (u & 1)));
+    }
+}
+
 // Rows of X to the rows of their choices (times the choice's weight, if
 // there are weights): a token's row is read once from memory and written
 // top_k times.  Bound by memory: 16384 tokens x 8 rows of 2048 bf16 take
@@ -284,41 +336,37 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// The same at any alignment, a warp per choice.
+// The same at any alignment, a warp per choice: each word of the input row is
+// loaded once (two loads for each output word took 129 us instead of 119,
+// route included, for 16384 tokens x 8 rows of 2001 bf16).
 template <bool BF16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSlotThreads)
     dispatch_kernel(RowShape g, const uint16_t *X, int64_t ldx, const int32_t *rows, const float *weights,
                     uint16_t *Xs, int64_t ldxs)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * (kSlotThreads / 32) + (threadIdx.x >> 5);
     if (s >= g.rows) return;
     const int32_t r = rows[s];
     const int64_t to = r < 0 ? ~r : r;
     if (to >= g.rows) return;
     const uint16_t *x = X + s / g.top_k * ldx;
     uint16_t *o = Xs + to * ldxs;
-    const RowCut row(o, g.width);
-    const bool copied = r >= 0 && !weights;
-    const float w = r >= 0 && weights ? weights[s] : 1.f;
-    constexpr int FLIGHT = 4;
-    for (int i = lane; i < row.body; i += 32 * FLIGHT) {
-        Words8 v[FLIGHT];
+    const bool copied = r < 0 || !weights;
+    const float w = copied ? 1.f : weights[s];
+    constexpr int FLIGHT = 3;
+    for (int e0 = first_word(o); e0 < g.width; e0 += 8 * kWarpWords * FLIGHT) {
+        const int e = e0 + 8 * lane;
+        uint4 v[FLIGHT];
 #pragma unroll
-        for (int u = 0; u < FLIGHT; ++u)
-            v[u] = load_words8(x + row.head + 8 * (i + 32 * u), r >= 0 && i + 32 * u < row.body);
+        for (int u = 0; u < FLIGHT; ++u) v[u] = load_word(x, e + 8 * kWarpWords * u, g.width, r >= 0);
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
-            const int e = row.head + 8 * (i + 32 * u);
-            const Piece p = cut(v[u], x + e);
-            if (i + 32 * u < row.body) store_wide(o + e, copied || r < 0 ? p : scaled<BF16>(p, w));
+            const Piece p = join_words(v[u], x, e + 8 * kWarpWords * u);
+            if (lane < kWarpWords) store_word(o, e + 8 * kWarpWords * u, g.width, copied ? p : scaled<BF16>(p, w));
         }
-    }
-    if (lane < row.singles()) {
-        const int e = row.single(lane);
-        o[e] = r < 0 ? uint16_t(0) : (copied ? x[e] : narrow1<BF16>(widen1<BF16>(x[e]) * w));
     }
 }
 
@@ -332,7 +380,7 @@ __global__ void __launch_bounds__(256)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int per_block = 256 / g.lanes, lane = threadIdx.x % g.lanes;
+    const int per_block = static_cast<int>(blockDim.x) / g.lanes, lane = threadIdx.x % g.lanes;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / g.lanes;
     if (t >= g.tokens) return;
     const int32_t *mine = rows + t * g.top_k;
@@ -377,7 +425,8 @@ __global__ void __launch_bounds__(256)
     __shared__ float weight_of[8][kMaxTopK];
     pdl_wait();
     pdl_launch_dependents();
-    const int per_block = 256 / g.lanes, lane = threadIdx.x % g.lanes, slot = threadIdx.x / g.lanes;
+    const int per_block = static_cast<int>(blockDim.x) / g.lanes, lane = threadIdx.x % g.lanes;
+    const int slot = threadIdx.x / g.lanes;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + slot;
     if (t < g.tokens) {
         for (int j = lane; j < g.top_k; j += g.lanes) {
@@ -492,17 +541,18 @@ __global__ void __launch_bounds__(256, 3)
     }
 }
 
-// The same at any alignment, a warp per choice (rows of 3001: 165 us with five
-// blocks an SM, 183 with as many registers as the compiler takes).
+// The same at any alignment, a warp per choice (rows of 3001: 161 us with
+// forty warps an SM, 174 with 32; each word loaded once and passed between
+// lanes, as in dispatch_kernel, 179).
 template <bool BF16>
-__global__ void __launch_bounds__(256, 5)
+__global__ void __launch_bounds__(kSlotThreads, 20)
     combine_grad_kernel(RowShape g, const uint16_t *dY, int64_t lddy, const uint16_t *Ys, int64_t ldys,
                         const int32_t *rows, const float *weights, uint16_t *dYs, int64_t lddys, float *dweights)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * (kSlotThreads / 32) + (threadIdx.x >> 5);
     if (s >= g.rows) return;
     const int32_t r = rows[s];
     const int64_t to = r < 0 ? ~r : r;
@@ -584,9 +634,12 @@ RowShape row_shape(int64_t tokens, int top_k, int64_t width)
     return g;
 }
 
-int64_t row_blocks(const RowShape &g) { return (g.tokens + 256 / g.lanes - 1) / (256 / g.lanes); }
+int64_t row_blocks(const RowShape &g, int threads = 256)
+{
+    return (g.tokens + threads / g.lanes - 1) / (threads / g.lanes);
+}
 
-int64_t slot_blocks(const RowShape &g) { return (g.rows + 7) / 8; }
+int64_t slot_blocks(const RowShape &g) { return (g.rows + kSlotThreads / 32 - 1) / (kSlotThreads / 32); }
 
 }  // namespace
 
@@ -634,19 +687,30 @@ cudaError_t launch_dispatch(bool bf16, int64_t tokens, int top_k, int64_t width,
     const auto k = wide ? (bf16 ? dispatch_wide_kernel<true> : dispatch_wide_kernel<false>)
                         : (bf16 ? dispatch_kernel<true> : dispatch_kernel<false>);
     cudaLaunchAttribute a[1];
-    const cudaLaunchConfig_t c = config(wide ? row_blocks(g) : slot_blocks(g), 256, 0, s, a);
+    const cudaLaunchConfig_t c = wide ? config(row_blocks(g), 256, 0, s, a) : config(slot_blocks(g), kSlotThreads, 0, s, a);
     return cudaLaunchKernelEx(&c, k, g, X, ldx, rows, weights, Xs, ldxs);
 }
+
+constexpr int64_t kManyTokens = 1024;
 
 cudaError_t launch_combine(bool bf16, int64_t tokens, int top_k, int64_t width, const uint16_t *Ys, int64_t ldys,
                            const int32_t *rows, const float *weights, uint16_t *Y, int64_t ldy, cudaStream_t s)
 {
     const bool wide = width % 8 == 0 && wide_rows(Ys, ldys) && wide_rows(Y, ldy);
-    const RowShape g = row_shape(tokens, top_k, width);
+    RowShape g = row_shape(tokens, top_k, width);
+    // Of more tokens than are resident at once, narrower groups in blocks of
+    // 128 threads keep the SMs full to the end; of few, the widest groups are
+    // done first.  Four rows of 2048 (3001) a token, us:
+    //   tokens          256          512        1024        2048         4093
+    //   256 threads  2.4 (4.1)  3.5 (4.8)   5.1 (7.0)   9.3 (15.0)  21.3 (26.8)
+    //   128 threads  2.9 (5.3)  3.5 (5.8)   5.2 (7.4)   8.8 (14.1)  19.0 (25.1)
+    const bool many = tokens > kManyTokens;
+    const int threads = many ? 128 : 256, most = many ? (wide ? 128 : 64) : 256;
+    if (g.lanes > most) g.lanes = most;
     const auto k = wide ? (bf16 ? combine_wide_kernel<true> : combine_wide_kernel<false>)
                         : (bf16 ? combine_kernel<true> : combine_kernel<false>);
     cudaLaunchAttribute a[1];
-    const cudaLaunchConfig_t c = config(row_blocks(g), 256, 0, s, a);
+    const cudaLaunchConfig_t c = config(row_blocks(g, threads), threads, 0, s, a);
     return cudaLaunchKernelEx(&c, k, g, Ys, ldys, rows, weights, Y, ldy);
 }
 
@@ -659,7 +723,7 @@ cudaError_t launch_combine_grad(bool bf16, int64_t tokens, int top_k, int64_t wi
     const auto k = wide ? (bf16 ? combine_grad_wide_kernel<true> : combine_grad_wide_kernel<false>)
                         : (bf16 ? combine_grad_kernel<true> : combine_grad_kernel<false>);
     cudaLaunchAttribute a[1];
-    const cudaLaunchConfig_t c = wide ? config(tokens, g.lanes, 0, s, a) : config(slot_blocks(g), 256, 0, s, a);
+    const cudaLaunchConfig_t c = wide ? config(tokens, g.lanes, 0, s, a) : config(slot_blocks(g), kSlotThreads, 0, s, a);
     return cudaLaunchKernelEx(&c, k, g, dY, lddy, Ys, ldys, rows, weights, dYs, lddys, dweights);
 }
 

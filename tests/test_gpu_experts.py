@@ -416,6 +416,52 @@ def test_rows_with_pitches():
         check_close(dw, grads[1].double(), 2 * (C + 2) * 2.0 ** -23 * terms.abs().sum(2) + 1e-30)
 
 
+@pytest.mark.parametrize("T", [3, 1025])  # few and many tokens
+@pytest.mark.parametrize("C", [1, 7, 8, 9, 247, 248, 249, 255, 743, 744, 745, 1489])
+def test_rows_at_every_alignment(C, T):
+    # Whole numbers: every product and sum is exact.  What lies between the
+    # rows is NaN before and after.
+    k = 2
+    g, rows, _ = routing(T, k, 5, seed=C)
+    place = torch.where(rows >= 0, rows, ~rows).long()
+    X = torch.randint(-8, 9, (T, C), generator=g, device="cuda").half()
+    w = torch.randint(1, 4, (T, k), generator=g, device="cuda").float()
+    kept = (rows >= 0)[:, :, None]
+    out = torch.zeros(T * k, C, device="cuda")
+    out[place.view(-1)] = torch.where(kept, X.float()[:, None, :], 0.0).expand(T, k, C).reshape(-1, C)
+    weighted = torch.zeros_like(out)
+    weighted[place.view(-1)] = (w[:, :, None] * torch.where(kept, X.float()[:, None, :], 0.0)).reshape(-1, C)
+    back = (w[:, :, None] * torch.where(kept, out[place], 0.0)).sum(1)
+    dot = (out[place] * X.float()[:, None, :]).sum(2)
+
+    def buffer(n, ld, shift):
+        buf = torch.full((n * ld + shift + 64,), NAN, dtype=torch.float16, device="cuda")
+        return buf, buf[shift:shift + n * ld].view(n, ld)[:, :C]
+
+    def check(buf, view, want):
+        assert torch.equal(view.float(), want)
+        view.fill_(NAN)
+        assert bool(torch.isnan(buf).all())
+
+    for shift in range(8):
+        ld = C + (shift + 1) % 3
+        x = pitched(X, ld, shift)
+        buf, Xs = buffer(T * k, ld, 7 - shift)
+        gp.gemmpipe_dispatch(gp.F16, T, k, C, x, ld, rows, None, Xs, ld)
+        check(buf, Xs, out)
+        gp.gemmpipe_dispatch(gp.F16, T, k, C, x, ld, rows, w, Xs, ld)
+        check(buf, Xs, weighted)
+        Ys = pitched(out.half(), ld, (3 * shift) % 8)
+        buf, Y = buffer(T, ld, (5 * shift + 1) % 8)
+        gp.gemmpipe_combine(gp.F16, T, k, C, Ys, ld, rows, w, Y, ld)
+        check(buf, Y, back)
+        buf, dYs = buffer(T * k, ld, 7 - shift)
+        dw = torch.empty(T, k, device="cuda")
+        gp.gemmpipe_combine_grad(gp.F16, T, k, C, x, ld, Ys, ld, rows, w, dYs, ld, dw)
+        check(buf, dYs, weighted)
+        assert torch.equal(dw, dot)
+
+
 def test_entries_outside_the_rows_are_passed_over():
     T, k, C = 4, 2, 32
     rows = torch.arange(8, dtype=torch.int32, device="cuda").view(T, k)
