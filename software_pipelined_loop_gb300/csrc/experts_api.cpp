@@ -39,7 +39,7 @@ bool bad_pointer(const void *p, int bytes) { return !p || misaligned(p, bytes); 
 
 constexpr int64_t kMaxWidth = int64_t(1) << 30;  // elements of a row of the rows' operators (32-bit places)
 
-// Rows in 8 bits: a block holds 8192 values, of one row or of all.
+// Rows in 8 bits: a block takes 8192 values of a row of many.
 bool bad_kept(int64_t rows, int64_t width, int64_t ld)
 {
     return width > kMaxWidth || bad_matrix(rows, width, ld) || (rows > 0 && (width + 7) / 8192 + 1 > kMaxDim / rows);

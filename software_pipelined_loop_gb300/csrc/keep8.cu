@@ -19,7 +19,7 @@
 namespace gp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr uint32_t kNanStep = 255;
 
 template <bool BF16>
@@ -193,23 +193,35 @@ __device__ __forceinline__ uint2 load_bytes(const char *p, const char *begin, co
 }
 
 constexpr int kSpan = 256;        // values a warp takes at once
-constexpr int kSpansPerBlock = 32;  // spans of one row that a block takes
 
-// A block's part of a row: `parts` blocks share a row of more than 32 spans.
+// Warps that share a row: a power of two, as many as it has spans for.  (A
+// block for each of 32768 rows of 100 values takes 34 us, a warp 10.)
+__host__ __device__ __forceinline__ int warps_of_row(int spans)
+{
+    int w = 1;
+    while (w < kThreads / 32 && w < spans) w *= 2;
+    return w;
+}
+
+// A warp's part of a row: a block takes one or several short rows, `parts`
+// blocks share a row of more than `take` spans.
 struct RowPart {
     int64_t row;
-    int span;  // the warp's first span; it takes every (kThreads / 32)-th up to `end`
+    int span;  // the warp's first span; it takes every `step`-th up to `end`
+    int step;
     int end;
 };
 
-__device__ __forceinline__ RowPart row_part(int spans, uint32_t parts)
+__device__ __forceinline__ RowPart row_part(int spans, uint32_t parts, int take)
 {
     RowPart p;
-    const uint32_t row = blockIdx.x / parts;
-    const int first = static_cast<int>(blockIdx.x - row * parts) * kSpansPerBlock;
-    p.row = row;
-    p.span = first + static_cast<int>(threadIdx.x / 32);
-    p.end = first + kSpansPerBlock < spans ? first + kSpansPerBlock : spans;
+    p.step = warps_of_row(spans);
+    const uint32_t block = blockIdx.x / parts, warp = threadIdx.x / 32;
+    const int first = static_cast<int>(blockIdx.x - block * parts) * take;
+    const uint32_t shift = static_cast<uint32_t>(__ffs(p.step) - 1);
+    p.row = static_cast<int64_t>(block) * ((kThreads / 32) >> shift) + (warp >> shift);
+    p.span = first + static_cast<int>(warp & (static_cast<uint32_t>(p.step) - 1u));
+    p.end = first + take < spans ? first + take : spans;
     return p;
 }
 
@@ -217,20 +229,22 @@ __device__ __forceinline__ RowPart row_part(int spans, uint32_t parts)
 // own 8-byte words (rows of bytes start anywhere).
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    keep8_kernel(const uint16_t *X, int width, int64_t ldx, uint32_t parts, int8_t *Q, uint8_t *S)
+    keep8_kernel(const uint16_t *X, int64_t rows, int width, int64_t ldx, uint32_t parts, int take,
+                 int8_t *Q, uint8_t *S)
 {
     __shared__ __align__(16) uint8_t stage[kThreads / 32][kSpan + 16];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     uint8_t *mine = stage[threadIdx.x >> 5];
-    const RowPart p = row_part((width + kSpan - 1) / kSpan, parts);
+    const RowPart p = row_part((width + kSpan - 1) / kSpan, parts, take);
+    if (p.row >= rows) return;
     const uint16_t *x = X + p.row * ldx;
     uint8_t *steps = S + p.row * ((width + 31) / 32);
     uint8_t *q = reinterpret_cast<uint8_t *>(Q) + p.row * width;
     // Bytes of a span before the destination's first 8-byte word: the same in every span of a row.
     const int head = static_cast<int>((8 - (reinterpret_cast<uintptr_t>(q) & 7u)) & 7u);
-    for (int sp = p.span; sp < p.end; sp += kThreads / 32) {
+    for (int sp = p.span; sp < p.end; sp += p.step) {
         const int e0 = sp * kSpan, e = e0 + 8 * lane;
         uint32_t w[4] = {0, 0, 0, 0};
         if (e + 8 <= width) {
@@ -264,18 +278,19 @@ __global__ void __launch_bounds__(kThreads)
 // they may lie in two groups.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int width, uint32_t parts, uint16_t *X,
-                    int64_t ldx)
+    restore8_kernel(const int8_t *Q, const uint8_t *S, int64_t rows, int width, uint32_t parts, int take,
+                    uint16_t *X, int64_t ldx)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const RowPart p = row_part((width + 7 + kSpan - 1) / kSpan, parts);
+    const RowPart p = row_part((width + 7 + kSpan - 1) / kSpan, parts, take);
+    if (p.row >= rows) return;
     const char *begin = reinterpret_cast<const char *>(Q), *end = begin + rows * width, *q = begin + p.row * width;
     const uint8_t *s = S + p.row * ((width + 31) / 32);
     uint16_t *x = X + p.row * ldx;
     const int before = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) >> 1);
-    for (int sp = p.span; sp < p.end; sp += kThreads / 32) {
+    for (int sp = p.span; sp < p.end; sp += p.step) {
         const int e = sp * kSpan + 8 * lane - before;
         if (e >= width || e + 8 <= 0) continue;
         const int g0 = e > 0 ? e >> 5 : 0, g1 = (e + 7 < width ? e + 7 : width - 1) >> 5;
@@ -343,18 +358,30 @@ cudaError_t launch(void (*k)(P...), int64_t work, cudaStream_t s, A... args)
     return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
-// Blocks of a row of `values` values (at most 2^30 and a few: places within a row are 32-bit).
-int64_t row_parts(int64_t values)
-{
-    return (values + int64_t(kSpan) * kSpansPerBlock - 1) / (int64_t(kSpan) * kSpansPerBlock);
-}
+// Blocks for rows of `values` values (at most 2^30 and a few: places within a
+// row are 32-bit).  A block takes up to 32 spans of a row; 8 of few rows, which
+// leave SMs free.  Rows of 4001, kept: 64 rows 2.3 us with 8 spans, 3.3 with
+// 32; 32768 rows 117 and 110.  (32768 rows of 4001 and 2001 with 256 threads:
+// 121 and 72 us, 111 and 62 with 128.)
+struct RowBlocks {
+    int take;
+    int64_t parts, all;
+    RowBlocks(int64_t rows, int64_t values)
+    {
+        const int64_t spans = (values + kSpan - 1) / kSpan;
+        const int of_block = kThreads / 32 / warps_of_row(static_cast<int>(spans));
+        take = rows <= 1024 ? 8 : 32;
+        parts = (spans + take - 1) / take;
+        all = (rows + of_block - 1) / of_block * parts;
+    }
+};
 
 // Rows that are one run of whole groups, on the accesses' boundaries, in at
 // most 2^31 - 1 blocks.
 bool dense(const void *X, int64_t ldx, const void *Q, int64_t rows, int64_t width)
 {
     return width % 32 == 0 && ldx == width && reinterpret_cast<uintptr_t>(X) % 16 == 0 &&
-           reinterpret_cast<uintptr_t>(Q) % 8 == 0 && rows * (width / 8) < (int64_t(1) << 40);
+           reinterpret_cast<uintptr_t>(Q) % 8 == 0 && rows * (width / 8) < (int64_t(1) << 39);
 }
 
 }  // namespace
@@ -367,10 +394,9 @@ cudaError_t launch_keep8(bool bf16, int64_t rows, int64_t width, const uint16_t 
         return launch(bf16 ? keep8_dense_kernel<true> : keep8_dense_kernel<false>, (n + kFlight - 1) / kFlight, s, X, n,
                       Q, S);
     }
-    const int64_t parts = row_parts(width);
-    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, rows * parts * kThreads, s, X,
-                  static_cast<int>(width), ldx,
-                  static_cast<uint32_t>(parts), Q, S);
+    const RowBlocks b(rows, width);
+    return launch(bf16 ? keep8_kernel<true> : keep8_kernel<false>, b.all * kThreads, s, X, rows,
+                  static_cast<int>(width), ldx, static_cast<uint32_t>(b.parts), b.take, Q, S);
 }
 
 cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t *Q, const uint8_t *S, uint16_t *X,
@@ -381,10 +407,9 @@ cudaError_t launch_restore8(bool bf16, int64_t rows, int64_t width, const int8_t
         return launch(bf16 ? restore8_dense_kernel<true> : restore8_dense_kernel<false>, (n + kFlight - 1) / kFlight, s,
                       Q, S, n, X);
     }
-    const int64_t parts = row_parts(width + 7);
-    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, rows * parts * kThreads, s, Q, S, rows,
-                  static_cast<int>(width),
-                  static_cast<uint32_t>(parts), X, ldx);
+    const RowBlocks b(rows, width + 7);
+    return launch(bf16 ? restore8_kernel<true> : restore8_kernel<false>, b.all * kThreads, s, Q, S, rows,
+                  static_cast<int>(width), static_cast<uint32_t>(b.parts), b.take, X, ldx);
 }
 
 cudaError_t launch_repitch(const uint16_t *src, int64_t rows, int64_t width, int64_t lds, uint16_t *dst, int64_t ldd,

@@ -535,6 +535,14 @@ def test_keep8(shape, ty):
 
 
 @pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("shape", [(1025, 1), (1030, 100), (1027, 257), (1026, 520), (1031, 777), (1500, 2001),
+                                   (1025, 8300), (5, 257), (6, 513), (3, 2049), (2, 8500)], ids=str)
+def test_keep8_rows_in_blocks(shape, ty):
+    # Few and many rows of one span of 256 values up to more than a block takes.
+    test_keep8(shape, ty)
+
+
+@pytest.mark.parametrize("ty", TYPES)
 def test_keep8_extremes(ty):
     # The type's largest, its smallest, and every power of two between.
     code, dtype, _ = TYPES[ty]
