@@ -517,10 +517,12 @@ __global__ void __launch_bounds__(256, 3)
 #pragma unroll
             for (int j = 0; j < FLIGHT; ++j) {
                 if (r[j] == kNoRow) continue;
-                float fy[8];
-                widen8<BF16>(y[j], fy);
+                if (r[j] >= 0) {  // (a dropped choice's sum stays zero: dY may hold an infinity or NaN)
+                    float fy[8];
+                    widen8<BF16>(y[j], fy);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) dot[j] = fmaf(fd[u], fy[u], dot[j]);
+                    for (int u = 0; u < 8; ++u) dot[j] = fmaf(fd[u], fy[u], dot[j]);
+                }
                 const int64_t to = r[j] < 0 ? ~r[j] : r[j];
                 store_wide(dYs + to * lddys + e, r[j] < 0 ? Piece{{0, 0, 0, 0}} : scaled<BF16>(d, w[j]));
             }
