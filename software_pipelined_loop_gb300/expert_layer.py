@@ -24,6 +24,10 @@ from software_pipelined_loop_gb300 import gemmpipe as gp
 _CODE = {torch.float16: gp.F16, torch.bfloat16: gp.BF16}
 
 
+# The functions below hand their arguments to the library by address: they take
+# dense tensors (expert_layer makes them so) and make their gradients dense.
+
+
 def _empty(like, *shape, dtype=None):
     return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
@@ -110,12 +114,13 @@ class _Combine(torch.autograd.Function):
 
 def expert_layer(x, ids, weights, w1, w2, keep8: bool = False):
     """x: tokens x c; ids: tokens x top_k int32 (outside [0, experts): dropped);
-    weights: tokens x top_k fp32; w1: experts x c x h; w2: experts x h x c."""
+    weights: tokens x top_k fp32; w1: experts x c x h; w2: experts x h x c.
+    Strided tensors are copied to dense ones first."""
     offsets, _, rows = route(ids, w1.shape[0])
     xs = _Dispatch.apply(x.contiguous(), rows, ids.shape[1])
-    hidden = torch.nn.functional.silu(_Product.apply(xs, w1, offsets, keep8))
-    ys = _Product.apply(hidden, w2, offsets, keep8)
-    return _Combine.apply(ys, weights, rows)
+    hidden = torch.nn.functional.silu(_Product.apply(xs, w1.contiguous(), offsets, keep8))
+    ys = _Product.apply(hidden, w2.contiguous(), offsets, keep8)
+    return _Combine.apply(ys, weights.contiguous(), rows)
 
 
 def main() -> None:
