@@ -24,6 +24,36 @@ from software_pipelined_loop_gb300 import gemmpipe as gp
 _CODE = {torch.float16: gp.F16, torch.bfloat16: gp.BF16}
 
 
+def _require(ok: bool, error: type[Exception], message: str) -> None:
+    if not ok:
+        raise error(message)
+
+
+def _check_ids(ids: torch.Tensor) -> None:
+    _require(ids.dtype == torch.int32, TypeError, f"ids: int32 is needed, got {ids.dtype}")
+    _require(ids.dim() == 2, ValueError, f"ids: tokens x top_k is needed, got {tuple(ids.shape)}")
+
+
+def _check_devices(*tensors: torch.Tensor) -> None:
+    # The library launches on the current device's stream.
+    if not all(t.is_cuda for t in tensors) or {t.get_device() for t in tensors} != {torch.cuda.current_device()}:
+        raise ValueError("tensors on the current CUDA device are needed, got " +
+                         ", ".join(str(t.device) for t in tensors))
+
+
+def _check_arguments(x, ids, weights, w1, w2) -> None:
+    _require(x.dtype in _CODE, TypeError, f"x: float16 or bfloat16 is needed, got {x.dtype}")
+    _check_ids(ids)
+    _require(weights.dtype == torch.float32, TypeError, f"weights: float32 is needed, got {weights.dtype}")
+    for name, w in (("w1", w1), ("w2", w2)):
+        _require(w.dtype == x.dtype, TypeError, f"{name}: the type of x, {x.dtype}, is needed, got {w.dtype}")
+        _require(w.dim() == 3, ValueError, f"{name}: one matrix per expert is needed, got {tuple(w.shape)}")
+    tokens, (experts, c, h) = ids.shape[0], w1.shape
+    for name, t, shape in (("x", x, (tokens, c)), ("weights", weights, tuple(ids.shape)), ("w2", w2, (experts, h, c))):
+        _require(tuple(t.shape) == shape, ValueError, f"{name}: {shape} is needed, got {tuple(t.shape)}")
+    _check_devices(x, ids, weights, w1, w2)
+
+
 # The functions below hand their arguments to the library by address: they take
 # dense tensors (expert_layer makes them so) and make their gradients dense.
 
@@ -34,6 +64,8 @@ def _empty(like, *shape, dtype=None):
 
 def route(ids: torch.Tensor, experts: int) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(offsets, slots, rows) of the choices `ids` (tokens x top_k, int32), sorted by expert."""
+    _check_ids(ids)
+    _check_devices(ids)
     t, k = ids.shape
     new = lambda n: torch.empty(n, dtype=torch.int32, device=ids.device)  # noqa: E731
     offsets, slots, rows = new(experts + 1), new(t * k), new(t * k)
@@ -115,7 +147,9 @@ class _Combine(torch.autograd.Function):
 def expert_layer(x, ids, weights, w1, w2, keep8: bool = False):
     """x: tokens x c; ids: tokens x top_k int32 (outside [0, experts): dropped);
     weights: tokens x top_k fp32; w1: experts x c x h; w2: experts x h x c.
-    Strided tensors are copied to dense ones first."""
+    x, w1 and w2 have one 16-bit floating-point type.  Strided tensors are
+    copied to dense ones first; another type, shape or device is refused."""
+    _check_arguments(x, ids, weights, w1, w2)
     offsets, _, rows = route(ids, w1.shape[0])
     xs = _Dispatch.apply(x.contiguous(), rows, ids.shape[1])
     hidden = torch.nn.functional.silu(_Product.apply(xs, w1.contiguous(), offsets, keep8))
