@@ -16,6 +16,7 @@ runs a training step and a one-token step on the GPU and prints their times.
 from __future__ import annotations
 
 import argparse
+import functools
 
 import torch
 
@@ -62,6 +63,32 @@ def _empty(like, *shape, dtype=None):
     return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
+class _Last(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return grads
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the expert layer's gradients cannot be differentiated again")
+
+
+def _once(backward):
+    """For gradients made outside autograd: where a graph of them is asked for
+    (create_graph), they get a node whose differentiation is an error, whatever
+    else requires a gradient -- without one their derivatives would be dropped."""
+    @functools.wraps(backward)
+    def run(ctx, dy):
+        with torch.no_grad():
+            grads = backward(ctx, dy)
+        made = [g for g in grads if g is not None]
+        if not torch.is_grad_enabled() or not made:
+            return grads
+        marked = iter(_Last.apply(torch.empty(0, requires_grad=True), *made))
+        return tuple(g if g is None else next(marked) for g in grads)
+    return run
+
+
 def route(ids: torch.Tensor, experts: int) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(offsets, slots, rows) of the choices `ids` (tokens x top_k, int32), sorted by expert."""
     _check_ids(ids)
@@ -84,6 +111,7 @@ class _Dispatch(torch.autograd.Function):
         return xs
 
     @staticmethod
+    @_once
     def backward(ctx, dxs):
         rows, = ctx.saved_tensors
         dxs = dxs.contiguous()
@@ -109,6 +137,7 @@ class _Product(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         *kept, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
@@ -134,6 +163,7 @@ class _Combine(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         ys, weights, rows = ctx.saved_tensors
         dy = dy.contiguous()
