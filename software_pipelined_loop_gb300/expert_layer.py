@@ -128,27 +128,35 @@ class _Product(torch.autograd.Function):
         e, _, n = w.shape
         y = _empty(x, r, n)
         gp.gemm_grouped(_CODE[x.dtype], r, n, k, e, x, k, offsets, w, y, n)
-        if keep8:
-            q, s = _empty(x, r, k, dtype=torch.int8), _empty(x, r, (k + 31) // 32, dtype=torch.uint8)
-            gp.gemmpipe_keep8(_CODE[x.dtype], r, k, x, k, q, s)
-            ctx.save_for_backward(q, s, w, offsets)
-        else:
-            ctx.save_for_backward(x, w, offsets)
+        # What the gradients that may be asked for need, and no more.
+        x_grad, w_grad = ctx.needs_input_grad[:2]
+        kept = ()
+        if w_grad and keep8:
+            kept = _empty(x, r, k, dtype=torch.int8), _empty(x, r, (k + 31) // 32, dtype=torch.uint8)
+            gp.gemmpipe_keep8(_CODE[x.dtype], r, k, x, k, *kept)
+        elif w_grad:
+            kept = (x,)
+        ctx.save_for_backward(offsets, w if x_grad else None, *kept)
+        ctx.shape = e, k, n
         return y
 
     @staticmethod
     @_once
     def backward(ctx, dy):
-        *kept, w, offsets = ctx.saved_tensors
+        offsets, w, *kept = ctx.saved_tensors
         dy = dy.contiguous()
-        e, k, n = w.shape
+        e, k, n = ctx.shape
         r, ty = dy.shape[0], _CODE[dy.dtype]
-        dx, dw = _empty(dy, r, k), torch.empty_like(w)
-        gp.gemm_grouped_dx(ty, r, n, k, e, dy, n, offsets, w, dx, k)
-        if len(kept) == 2:
-            gp.gemm_grouped_dw8(ty, r, n, k, e, kept[0], kept[1], dy, n, offsets, dw)
-        else:
-            gp.gemm_grouped_dw(ty, r, n, k, e, kept[0], k, dy, n, offsets, dw)
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = _empty(dy, r, k)
+            gp.gemm_grouped_dx(ty, r, n, k, e, dy, n, offsets, w, dx, k)
+        if ctx.needs_input_grad[1]:
+            dw = _empty(dy, e, k, n)
+            if len(kept) == 2:
+                gp.gemm_grouped_dw8(ty, r, n, k, e, *kept, dy, n, offsets, dw)
+            else:
+                gp.gemm_grouped_dw(ty, r, n, k, e, *kept, k, dy, n, offsets, dw)
         return dx, dw, None, None
 
 

@@ -32,3 +32,38 @@ def test_second_derivatives_are_refused(name):
     with pytest.raises(RuntimeError, match="differentiated again"):
         loss.backward()
     assert gp.gemmpipe_get_device_status() == gp.OK
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names of the library calls made, in order."""
+    made = []
+    for name in [n for n in dir(gp) if n.startswith(("gemm_grouped", "gemmpipe_keep8"))]:
+        def counted(*args, _name=name, _call=getattr(gp, name)):
+            made.append(_name)
+            return _call(*args)
+        monkeypatch.setattr(gp, name, counted)
+    return made
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("grad, want", [
+    (("x",), {"gemm_grouped_dx": 2}),                             # frozen experts
+    (("weights",), {}),                                           # the router alone
+    (("w1",), {"gemm_grouped_dx": 1, "gemm_grouped_dw": 1}),
+    (("w2", "weights"), {"gemm_grouped_dw": 1}),
+    (("w1", "w2"), {"gemm_grouped_dx": 1, "gemm_grouped_dw": 2}),  # rows that need no gradient
+    (("x", "weights", "w1", "w2"), {"gemm_grouped_dx": 2, "gemm_grouped_dw": 2})], ids=lambda v: "+".join(v))
+def test_only_the_gradients_asked_for(calls, grad, want, keep8):
+    t, ids, dy = leaves()
+    expert_layer(t["x"], ids, t["weights"], t["w1"], t["w2"], keep8).backward(dy)
+    every = {k: v.grad for k, v in t.items()}
+    t, ids, dy = leaves(grad)
+    y = expert_layer(t["x"], ids, t["weights"], t["w1"], t["w2"], keep8)
+    calls.clear()
+    y.backward(dy)
+    made = [c.replace("dw8", "dw") for c in calls]
+    assert {c: made.count(c) for c in set(made)} == want
+    for name, v in t.items():
+        assert v.grad is None if name not in grad else torch.equal(v.grad, every[name]), name
+    assert gp.gemmpipe_get_device_status() == gp.OK
