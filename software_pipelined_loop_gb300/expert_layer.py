@@ -188,6 +188,7 @@ def expert_layer(x, ids, weights, w1, w2, keep8: bool = False):
     x, w1 and w2 have one 16-bit floating-point type.  Strided tensors are
     copied to dense ones first; another type, shape or device is refused."""
     _check_arguments(x, ids, weights, w1, w2)
+    keep8 = keep8 and torch.is_grad_enabled()  # (needs_input_grad goes by the tensors alone)
     offsets, _, rows = route(ids, w1.shape[0])
     xs = _Dispatch.apply(x.contiguous(), rows, ids.shape[1])
     hidden = torch.nn.functional.silu(_Product.apply(xs, w1.contiguous(), offsets, keep8))

@@ -67,3 +67,12 @@ def test_only_the_gradients_asked_for(calls, grad, want, keep8):
     for name, v in t.items():
         assert v.grad is None if name not in grad else torch.equal(v.grad, every[name]), name
     assert gp.gemmpipe_get_device_status() == gp.OK
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_nothing_is_kept_without_a_backward_pass(calls, mode):
+    t, ids, _ = leaves()
+    with mode():
+        y = expert_layer(t["x"], ids, t["weights"], t["w1"], t["w2"], True)
+    assert calls == ["gemm_grouped"] * 2
+    assert torch.equal(y, expert_layer(t["x"], ids, t["weights"], t["w1"], t["w2"]).detach())
