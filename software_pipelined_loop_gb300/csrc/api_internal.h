@@ -29,9 +29,6 @@ gemmpipe_status_t api_workspace(int dev, cudaStream_t s, int64_t bytes, void **o
 // start as zeros and stay what the kernels make them, then `bytes` of parts.
 gemmpipe_status_t api_parts_workspace(int dev, cudaStream_t s, int64_t counts, int64_t bytes, void **out);
 
-// A number that no other launch of the process has (never 0).
-uint32_t api_epoch();
-
 // Runs fn(ctx), which launches `kernels` kernels on `s`, inside the timing
 // region of the main (gemm) or auxiliary kernels, and counts the launches.
 gemmpipe_status_t api_timed_launch(bool gemm, cudaStream_t s, int kernels, cudaError_t (*fn)(void *), void *ctx);

@@ -810,12 +810,6 @@ gemmpipe_status_t api_parts_workspace(int dev, cudaStream_t s, int64_t counts, i
     return workspace(dev, s, counts + bytes, out, kWsParts, counts);
 }
 
-uint32_t api_epoch()
-{
-    uint32_t e = g_epoch.fetch_add(1) + 1;
-    return e != 0 ? e : g_epoch.fetch_add(1) + 1;
-}
-
 gemmpipe_status_t api_timed_launch(bool gemm, cudaStream_t s, int kernels, cudaError_t (*fn)(void *), void *ctx)
 {
     TimedRegion tr(gemm, s);

@@ -716,18 +716,35 @@ __device__ __forceinline__ float *part_of(const GroupedParams &p, int32_t slot, 
 
 // Counts a finished part; true for the last of `parts`, which leaves the
 // counter at zero for the next launch.  A count is of one launch only (its
-// epoch is beside it), so that a launch that gave up leaves nothing behind.
-__device__ __forceinline__ bool last_part(unsigned long long *count, uint32_t epoch, int parts)
+// number is beside it), so that a launch that gave up leaves nothing behind.
+// The number is in device memory and not an argument: a recorded launch has
+// the same arguments each time.
+__device__ __forceinline__ bool last_part(unsigned long long *count, uint32_t launch, int parts)
 {
     unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(count), want;
     for (;;) {  // at most as often as there are other parts
-        const uint32_t n = (seen >> 32) == epoch ? static_cast<uint32_t>(seen) + 1 : 1u;
+        const uint32_t n = (seen >> 32) == launch ? static_cast<uint32_t>(seen) + 1 : 1u;
         const bool last = n == static_cast<uint32_t>(parts);
-        want = last ? 0ull : (static_cast<unsigned long long>(epoch) << 32) | n;
+        want = last ? 0ull : (static_cast<unsigned long long>(launch) << 32) | n;
         const unsigned long long was = atomicCAS(count, seen, want);
         if (was == seen) return last;
         seen = was;
     }
+}
+
+// The launch's number; each of its `readers` asks once, and the last one moves
+// the number on for the next launch.  (Read by every epilogue warp at its
+// start, while the ring fills.  Moved on at the CTAs' ends instead, behind
+// their stores, it took 1 to 2 us of a call.)
+__device__ __forceinline__ uint32_t launch_number(uint32_t *launch, uint32_t readers)
+{
+    const uint32_t n = __ldcg(launch);
+    __threadfence();
+    if (atomicAdd(launch + 1, 1u) == readers - 1) {
+        launch[1] = 0;
+        launch[0] = n + 1;
+    }
+    return n;
 }
 
 // Accumulator lane l of warp quarter q is feature f0 + 32 q + l, column c the
@@ -750,6 +767,10 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty0 = Cfg::PAIR ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : smem_u32(&ctl->tempty[0]);
     uint16_t *out = static_cast<uint16_t *>(p.out);
+    uint32_t launch = 0;  // (of lane 0)
+    if (Cfg::MODE == kWeights && p.split_rows > 0 && lane == 0)
+        launch = launch_number(p.launch, gridDim.x * Cfg::EPI_WARPS);
+    __syncwarp();
     GroupedIter<Cfg> it(p, tab);
     GroupedTile t;
     while (it.next(p, t)) {
@@ -817,7 +838,7 @@ __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_
                 __syncwarp();
                 bool last = false;
                 if (lane == 0)
-                    last = last_part(&p.part_counts[(t.slot0 * Cfg::CLUSTER + rank) * Cfg::EPI_WARPS + e], p.epoch,
+                    last = last_part(&p.part_counts[(t.slot0 * Cfg::CLUSTER + rank) * Cfg::EPI_WARPS + e], launch,
                                      t.parts);
                 if (__any_sync(0xffffffffu, last)) {
                     __threadfence();

@@ -37,7 +37,7 @@ struct GroupedParams {
     int64_t ldo;             // output row pitch in elements
     float *parts;            // weight gradient: sums of parts of an expert's rows, a slot per tile
     unsigned long long *part_counts;  // ... finished parts, one count per slot and epilogue warp of both CTAs
-    uint32_t epoch;          // ... of this launch
+    uint32_t *launch;        // ... this launch's number, and how many warps have read it
     int32_t split_rows;      // ... an expert of more than 1.5 times as many is summed in parts (0: none is)
     int sorted;              // ... the longest sums go first (up to kMaxSorted experts)
     int bf16;
