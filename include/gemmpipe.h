@@ -45,6 +45,15 @@
  * instead -- same result, no error).  gemm_f16f32 with 16-byte aligned operands and pitches
  * and a tile count that fills whole waves allocates nothing.
  *
+ * CUDA graphs: calls on device buffers may be recorded by stream capture
+ * (each call of a process once before, so that its kernels are loaded).  A
+ * recorded call uses the workspaces of the stream it was recorded on, which
+ * are allocated or grown while recording if need be.  A workspace that a graph
+ * may use is kept when a later call outgrows it;
+ * gemmpipe_release_workspaces() frees it too, and such graphs must not be
+ * launched after that.  Graphs recorded on one stream must not run at the same
+ * time as each other or as other calls on that stream.
+ *
  * Execution: every GEMM call is asynchronous on `stream` (a cudaStream_t;
  * NULL is the legacy default stream) and targets the current CUDA device.
  * A return of GEMMPIPE_OK means "validated and enqueued".  Errors found on

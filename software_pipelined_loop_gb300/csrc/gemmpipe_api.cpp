@@ -514,24 +514,71 @@ struct TimedRegion {
 struct Workspace {
     void *ptr = nullptr;
     int64_t bytes = 0;
+    bool recorded = false;  // a CUDA graph may hold its address
 };
 // Kinds of workspace per (device, stream).
 enum WsKind { kWsOperands = 0, kWsSplit = 1, kWsHost = 2, kWsParts = 3 };
 std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_ws;
+// Workspaces outgrown by their stream that a graph may still use, by device.
+std::vector<std::pair<int, void *>> g_outgrown;
 
-// The (device, stream) workspace of one kind, at least `bytes` long.  A new
-// stream-K workspace has its flags (the first zero_bytes bytes) zeroed on
-// the stream before first use.
+bool is_recording(cudaStream_t s)
+{
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return st != cudaStreamCaptureStatusNone;
+}
+
+// While a stream of the calling thread is being recorded: lets the thread make
+// calls that a recording otherwise forbids because they are not part of it.
+class BesideRecording {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    bool on;
+
+public:
+    explicit BesideRecording(bool on_) : on(on_)
+    {
+        if (on) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+    ~BesideRecording()
+    {
+        if (on) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+};
+
+// Sets memory to zero now, on a stream of its own.
+cudaError_t zero_now(void *p, int64_t bytes)
+{
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), s);
+    const cudaError_t done = cudaStreamSynchronize(s);
+    cudaStreamDestroy(s);
+    return e != cudaSuccess ? e : done;
+}
+
+// The (device, stream) workspace of one kind, at least `bytes` long.  The
+// first zero_bytes bytes of a new one (stream-K flags, counts of parts) are
+// zeroed before first use.  A graph recorded on the stream holds the
+// workspace's address, so what was handed out to one is kept when outgrown.
 gemmpipe_status_t workspace(int dev, cudaStream_t s, int64_t bytes, void **out, int kind = kWsOperands,
                             int64_t zero_bytes = 0)
 {
     std::lock_guard<std::mutex> lk(g_mu);
     Workspace &w = g_ws[std::make_tuple(dev, s, kind)];
+    const bool recording = is_recording(s);
     if (w.bytes < bytes) {
+        const BesideRecording beside(recording);
         if (w.ptr) {
-            cudaFree(w.ptr);  // synchronizes: earlier users of the buffer have finished
-            w.ptr = nullptr;
-            w.bytes = 0;
+            if (recording || w.recorded)
+                g_outgrown.push_back({dev, w.ptr});
+            else
+                cudaFree(w.ptr);  // synchronizes: earlier users of the buffer have finished
+            w = Workspace();
         }
         if (cudaMalloc(&w.ptr, static_cast<size_t>(bytes)) != cudaSuccess) {
             cudaGetLastError();
@@ -539,15 +586,16 @@ gemmpipe_status_t workspace(int dev, cudaStream_t s, int64_t bytes, void **out, 
             return GEMMPIPE_ERR_OUT_OF_MEMORY;
         }
         w.bytes = bytes;
-        if (zero_bytes > 0 && cudaMemsetAsync(w.ptr, 0, static_cast<size_t>(zero_bytes), s) !=
+        if (zero_bytes > 0 && (recording ? zero_now(w.ptr, zero_bytes)
+                                         : cudaMemsetAsync(w.ptr, 0, static_cast<size_t>(zero_bytes), s)) !=
                 cudaSuccess) {
             cudaGetLastError();
             cudaFree(w.ptr);
-            w.ptr = nullptr;
-            w.bytes = 0;
+            w = Workspace();
             return GEMMPIPE_ERR_LAUNCH;
         }
     }
+    w.recorded = w.recorded || recording;
     *out = w.ptr;
     return GEMMPIPE_OK;
 }
@@ -1406,6 +1454,11 @@ gemmpipe_status_t gemmpipe_release_workspaces(void)
         }
     }
     g_ws.clear();
+    for (auto &kv : g_outgrown) {
+        cudaSetDevice(kv.first);
+        cudaFree(kv.second);
+    }
+    g_outgrown.clear();
     for (auto &kv : g_host) {
         cudaSetDevice(kv.first.first);
         if (kv.second.in) cudaStreamDestroy(kv.second.in);
