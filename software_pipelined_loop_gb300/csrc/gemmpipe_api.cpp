@@ -606,7 +606,8 @@ std::atomic<uint32_t> g_epoch{0};
 
 // Fills the stream-K fields of p: the split tiles' partial sums and flags in
 // the stream's split workspace, and a fresh epoch.  Without that workspace
-// the plan falls back to whole tiles.
+// the plan falls back to whole tiles.  A recorded launch has the same epoch at
+// every replay, so the flags are cleared before it, by a node of the graph.
 void set_schedule(Plan &pl, int dev, cudaStream_t s, GemmParams &p)
 {
     p.partials = nullptr;
@@ -615,7 +616,8 @@ void set_schedule(Plan &pl, int dev, cudaStream_t s, GemmParams &p)
     if (pl.sk_tiles > 0) {
         void *ws = nullptr;
         if (pl.split_ctas() <= kMaxSplitCtas &&
-            workspace(dev, s, pl.split_bytes(), &ws, kWsSplit, kSplitFlagBytes) == GEMMPIPE_OK) {
+            workspace(dev, s, pl.split_bytes(), &ws, kWsSplit, kSplitFlagBytes) == GEMMPIPE_OK &&
+            (!is_recording(s) || cudaMemsetAsync(ws, 0, kSplitFlagBytes, s) == cudaSuccess)) {
             p.flags = static_cast<uint32_t *>(ws);
             p.partials = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kSplitFlagBytes);
             uint32_t e = g_epoch.fetch_add(1) + 1;
