@@ -116,9 +116,13 @@ def _ptr(x) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         # The raw handle of torch's current stream; building the Stream object
-        # first costs 3 us a call, as much as the rest of a call.
+        # first costs 3 us a call, as much as the rest of a call, but works on
+        # a torch without this private function.
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return int(torch.cuda.current_stream().cuda_stream)
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
