@@ -14,7 +14,7 @@ struct GroupedVariant {
     int mode;      // GroupedMode
     int bn;        // output rows per tile
     int tile_f;    // features per tile
-    int pair;      // 1: CTA pairs, 256 features per tile; 0: single CTAs, 128
+    int pair;      // 1: CTA pairs, 256 features per tile; 0: single CTAs, 128 or 64
     int cta_bn;    // columns of the row operand per CTA
     int bk;        // products per stage
     int b_part;    // rows of a short copy of the row operand

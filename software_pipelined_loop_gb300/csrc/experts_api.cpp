@@ -158,8 +158,11 @@ bool encode_weight_groups(CUtensorMap *m, bool bf16, const uint16_t *w, int64_t 
     return gp::api_encode_16bit(m, bf16, 4, w, dims, strides, box);
 }
 
-// Rows per tile, by the mean number of rows of an expert.  Measured on 64
-// experts of 4096 x 1536, forward (gradient to the rows), us:
+// Rows per tile, by the mean number of rows of an expert: the bounds are on
+// the device, so rows that no expert has and experts without rows count too,
+// and rows that fall on a few of many experts get smaller tiles than would be
+// best.  Measured on 64 experts of 4096 x 1536 alone, forward (gradient to the
+// rows), us:
 //   mean    32 rows        64             128            256
 //     16    118.6 (122.1)  123.7 (121.5)  122.9 (125.8)  124.8 (128.1)
 //     32    129.6 (133.8)  120.6 (124.7)  130.6 (127.3)  126.8 (129.9)

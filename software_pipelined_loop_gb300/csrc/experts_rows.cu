@@ -543,9 +543,9 @@ __global__ void __launch_bounds__(256, 3)
     }
 }
 
-// The same at any alignment, a warp per choice (rows of 3001: 161 us with
-// forty warps an SM, 174 with 32; each word loaded once and passed between
-// lanes, as in dispatch_kernel, 179).
+// The same at any alignment, a warp per choice (8192 x 8 rows of 3001: 157 us
+// with forty warps an SM in blocks of 64 threads, 174 with 32; each word
+// loaded once and passed between lanes, as in dispatch_kernel, 179).
 template <bool BF16>
 __global__ void __launch_bounds__(kSlotThreads, 20)
     combine_grad_kernel(RowShape g, const uint16_t *dY, int64_t lddy, const uint16_t *Ys, int64_t ldys,
@@ -702,7 +702,8 @@ cudaError_t launch_combine(bool bf16, int64_t tokens, int top_k, int64_t width, 
     RowShape g = row_shape(tokens, top_k, width);
     // Of more tokens than are resident at once, narrower groups in blocks of
     // 128 threads keep the SMs full to the end; of few, the widest groups are
-    // done first.  Four rows of 2048 (3001) a token, us:
+    // done first.  Four rows of 2048 (3001) a token, us (other numbers of rows
+    // were not swept):
     //   tokens          256          512        1024        2048         4093
     //   256 threads  2.4 (4.1)  3.5 (4.8)   5.1 (7.0)   9.3 (15.0)  21.3 (26.8)
     //   128 threads  2.9 (5.3)  3.5 (5.8)   5.2 (7.4)   8.8 (14.1)  19.0 (25.1)

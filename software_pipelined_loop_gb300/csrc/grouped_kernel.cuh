@@ -16,9 +16,11 @@
 // rows may belong to the next expert; they only make columns that are not
 // stored.
 //
-// The ring, barriers, warp roles and bounded waits are those of
-// gemm_kernel.cuh: a producer warp filling stages of 64 products by TMA, an
-// MMA warp, and two epilogue warpgroups on double-buffered accumulators.
+// The ring, barriers and bounded waits are those of gemm_kernel.cuh.  Warps: a
+// producer for each operand, filling stages of 64 products (128 in the tiles
+// of 32 and 64 rows) by TMA, one that issues the MMAs, two epilogue
+// warpgroups on double-buffered accumulators, and for the weight gradient one
+// more producer, below.
 //
 // Weight gradient: the summed dimension is the expert's rows, and the 16 rows
 // of an MMA step must all be its own (the next expert's, or unused ones, may
@@ -752,8 +754,8 @@ __device__ __forceinline__ uint32_t launch_number(uint32_t *launch, uint32_t rea
 // 2 rows, and bulk tensor copies out of the staging tiles measured the same.)
 // An accumulator is handed back with relaxed arrivals: a release at cluster
 // scope waits for the warp's stores of the tile before, and held the MMAs up
-// for it.  Weight gradient of 8192 tokens x 2 on 32 experts, 2048 x 1024:
-// 43 us, 60 with releases, 31 with nothing stored; of 8192 x 4 on 32 experts,
+// for it.  Weight gradient of 8192 rows on 32 experts, 2048 x 1024: 43 us, 60
+// with releases, 31 with nothing stored; of 32768 rows on 32 experts,
 // 4096 x 1536: 250, 261 and 233 us.
 template <class Cfg>
 __device__ void grouped_epilogue(const GroupedParams &p, uint32_t sbase, uint32_t tmem_base,

@@ -5,9 +5,11 @@
 
 `expert_layer` is differentiable in x, the router's weights, W1 and W2; with
 ``keep8=True`` the rows that the weight gradients need (the inputs of both
-products) are kept in 8 bits between the passes.  All products, sorts and sums
-run in the CUDA library; torch supplies memory, autograd's bookkeeping and the
-activation function.
+products) are kept in 8 bits between the passes.  The routing's sort, the rows'
+way to the experts and back, the products and their gradients run in the CUDA
+library.  torch supplies memory, autograd's bookkeeping, the activation between
+the products and its derivative; the choice of the experts and its weights are
+the caller's.  Gradients of the gradients are refused.
 
     python -m software_pipelined_loop_gb300.expert_layer [--tokens N] [--keep8]
 
