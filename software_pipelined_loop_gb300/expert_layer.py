@@ -27,33 +27,37 @@ from software_pipelined_loop_gb300 import gemmpipe as gp
 _CODE = {torch.float16: gp.F16, torch.bfloat16: gp.BF16}
 
 
-def _require(ok: bool, error: type[Exception], message: str) -> None:
-    if not ok:
-        raise error(message)
-
-
 def _check_ids(ids: torch.Tensor) -> None:
-    _require(ids.dtype == torch.int32, TypeError, f"ids: int32 is needed, got {ids.dtype}")
-    _require(ids.dim() == 2, ValueError, f"ids: tokens x top_k is needed, got {tuple(ids.shape)}")
+    if ids.dtype != torch.int32:
+        raise TypeError(f"ids: int32 is needed, got {ids.dtype}")
+    if ids.dim() != 2:
+        raise ValueError(f"ids: tokens x top_k is needed, got {tuple(ids.shape)}")
 
 
-def _check_devices(*tensors: torch.Tensor) -> None:
+def _check_devices(first: torch.Tensor, *others: torch.Tensor) -> None:
     # The library launches on the current device's stream.
-    if not all(t.is_cuda for t in tensors) or {t.get_device() for t in tensors} != {torch.cuda.current_device()}:
-        raise ValueError("tensors on the current CUDA device are needed, got " +
-                         ", ".join(str(t.device) for t in tensors))
+    here = torch.cuda.current_device() if first.is_cuda else -2
+    for t in (first, *others):
+        if t.get_device() != here:
+            raise ValueError("tensors on the current CUDA device are needed, got " +
+                             ", ".join(str(t.device) for t in (first, *others)))
 
 
 def _check_arguments(x, ids, weights, w1, w2) -> None:
-    _require(x.dtype in _CODE, TypeError, f"x: float16 or bfloat16 is needed, got {x.dtype}")
+    ty = x.dtype
+    if ty not in _CODE:
+        raise TypeError(f"x: float16 or bfloat16 is needed, got {ty}")
     _check_ids(ids)
-    _require(weights.dtype == torch.float32, TypeError, f"weights: float32 is needed, got {weights.dtype}")
-    for name, w in (("w1", w1), ("w2", w2)):
-        _require(w.dtype == x.dtype, TypeError, f"{name}: the type of x, {x.dtype}, is needed, got {w.dtype}")
-        _require(w.dim() == 3, ValueError, f"{name}: one matrix per expert is needed, got {tuple(w.shape)}")
-    tokens, (experts, c, h) = ids.shape[0], w1.shape
-    for name, t, shape in (("x", x, (tokens, c)), ("weights", weights, tuple(ids.shape)), ("w2", w2, (experts, h, c))):
-        _require(tuple(t.shape) == shape, ValueError, f"{name}: {shape} is needed, got {tuple(t.shape)}")
+    if weights.dtype != torch.float32:
+        raise TypeError(f"weights: float32 is needed, got {weights.dtype}")
+    if w1.dtype != ty or w2.dtype != ty:
+        raise TypeError(f"w1, w2: the type of x, {ty}, is needed, got {w1.dtype}, {w2.dtype}")
+    if w1.dim() != 3:
+        raise ValueError(f"w1: one matrix per expert is needed, got {tuple(w1.shape)}")
+    choices, (experts, c, h) = ids.shape, w1.shape
+    if x.shape != (choices[0], c) or weights.shape != choices or w2.shape != (experts, h, c):
+        raise ValueError(f"x {(choices[0], c)}, weights {tuple(choices)} and w2 {(experts, h, c)} are needed, "
+                         f"got {tuple(x.shape)}, {tuple(weights.shape)} and {tuple(w2.shape)}")
     _check_devices(x, ids, weights, w1, w2)
 
 
@@ -81,10 +85,12 @@ def _once(backward):
     else requires a gradient -- without one their derivatives would be dropped."""
     @functools.wraps(backward)
     def run(ctx, dy):
+        if not torch.is_grad_enabled():
+            return backward(ctx, dy)
         with torch.no_grad():
             grads = backward(ctx, dy)
         made = [g for g in grads if g is not None]
-        if not torch.is_grad_enabled() or not made:
+        if not made:
             return grads
         marked = iter(_Last.apply(torch.empty(0, requires_grad=True), *made))
         return tuple(g if g is None else next(marked) for g in grads)
@@ -95,6 +101,10 @@ def route(ids: torch.Tensor, experts: int) -> tuple[torch.Tensor, torch.Tensor, 
     """(offsets, slots, rows) of the choices `ids` (tokens x top_k, int32), sorted by expert."""
     _check_ids(ids)
     _check_devices(ids)
+    return _route(ids, experts)
+
+
+def _route(ids, experts):
     t, k = ids.shape
     new = lambda n: torch.empty(n, dtype=torch.int32, device=ids.device)  # noqa: E731
     offsets, slots, rows = new(experts + 1), new(t * k), new(t * k)
@@ -191,7 +201,7 @@ def expert_layer(x, ids, weights, w1, w2, keep8: bool = False):
     copied to dense ones first; another type, shape or device is refused."""
     _check_arguments(x, ids, weights, w1, w2)
     keep8 = keep8 and torch.is_grad_enabled()  # (needs_input_grad goes by the tensors alone)
-    offsets, _, rows = route(ids, w1.shape[0])
+    offsets, _, rows = _route(ids, w1.shape[0])
     xs = _Dispatch.apply(x.contiguous(), rows, ids.shape[1])
     hidden = torch.nn.functional.silu(_Product.apply(xs, w1.contiguous(), offsets, keep8))
     ys = _Product.apply(hidden, w2.contiguous(), offsets, keep8)
