@@ -405,6 +405,85 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, 
                                                 const int32_t *offsets, void *dW, gemmpipe_stream_t stream);
 
 /*
+ * ------------------------------------------------------------- few tokens
+ *
+ * The same layer while tokens are generated one by one: few rows, so that a
+ * pass is the reading of the weights, and weights that may be kept in 4 bits.
+ *
+ *   gemm_rows4             a few rows times a matrix in 4 bits
+ *   gemmpipe_expert_step   the whole expert layer for a few tokens
+ *   gemmpipe_expert_step4  the same with matrices in 4 bits
+ *   gemmpipe_pack4, gemmpipe_unpack4
+ *                          matrices into 4 bits and back (for many rows:
+ *                          unpack, then gemm_grouped)
+ *
+ * As for the operators above: types, sums in fp32, pitches, element
+ * alignment of 16-bit rows and matrices, no overlap, asynchronous on `stream`
+ * on the current device, results that repeat bit for bit, the errors.  They
+ * are inference operators without gradients, use no library workspace and
+ * may be recorded by stream capture.  M and T are at most 64; N, K, C and H
+ * at most 2^31 - 1024.
+ *
+ * A matrix in 4 bits (K x N; E of them densely after one another) is made of
+ *   Q: ceil(K / 8) x N4 words, N4 = N rounded up to a multiple of 4, on a
+ *      16-byte boundary.  Word (b, n) holds rows 8b .. 8b + 7 of column n:
+ *      row 8b + {0, 2, 4, 6, 1, 3, 5, 7}[i] in bits 4i .. 4i + 3, as q;
+ *   S: ceil(K / group) x N4 scales of the 16-bit type, on an 8-byte boundary;
+ *      group is 32, 64 or 128.
+ * Element (k, n) is (q - 8) * S[k / group][n].  Values past K or N are not
+ * used, whatever they are.
+ */
+#define GEMMPIPE_FEW_ROWS 64
+
+/* Y[m] = X[m] . W for a K x N matrix W in 4 bits, whose elements are not
+ * rounded before the product.  X is M x K, Y is M x N.  K == 0 sets Y to zero. */
+GEMMPIPE_API gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t group, const void *X,
+                                          int64_t ldx, const uint32_t *Q, const void *S, void *Y, int64_t ldy,
+                                          gemmpipe_stream_t stream);
+
+/*
+ * Y[t] = sum over the token's choices j of weights[t * top_k + j] *
+ *        (h . W2[e]),  e = experts[t * top_k + j],
+ *   h  = silu(X[t] . W1[e])                    (W3 NULL), or
+ *        silu(X[t] . W1[e]) * (X[t] . W3[e])   (element by element),
+ * silu(a) = a / (1 + exp(-a)).  X and Y are T x C, W1 and W3 are E x C x H, W2
+ * is E x H x C.  A choice outside [0, E) counts for nothing, whatever its
+ * weight; a token without choices gets zeros.  h is rounded to the type, as an
+ * operand of the second product; nothing else is rounded before Y.
+ * hidden: T * top_k rows of H rounded up to a multiple of 8 elements of the
+ * type, on a 16-byte boundary, for the kernels' use (calls that may run at the
+ * same time need one each).  Two launches, the second of which starts while
+ * the first one finishes.
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_expert_step(int type, int64_t T, int64_t top_k, int64_t E, int64_t C,
+                                                    int64_t H, const void *X, int64_t ldx, const int32_t *experts,
+                                                    const float *weights, const void *W1, const void *W2,
+                                                    const void *W3, void *hidden, void *Y, int64_t ldy,
+                                                    gemmpipe_stream_t stream);
+
+/* The same with the matrices in 4 bits (Q3 and S3 both NULL: no W3). */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_expert_step4(int type, int64_t T, int64_t top_k, int64_t E, int64_t C,
+                                                     int64_t H, int64_t group, const void *X, int64_t ldx,
+                                                     const int32_t *experts, const float *weights,
+                                                     const uint32_t *Q1, const void *S1, const uint32_t *Q2,
+                                                     const void *S2, const uint32_t *Q3, const void *S3,
+                                                     void *hidden, void *Y, int64_t ldy, gemmpipe_stream_t stream);
+
+/*
+ * W (E x K x N, dense) into 4 bits.  A group's scale is its largest magnitude
+ * over 7, rounded to the type; q = w / scale, rounded to nearest even and held
+ * between -8 and 7, plus 8 (8 where the scale is zero).  A group that holds an
+ * infinity or a NaN gets the scale NaN and q = 8, and comes back as NaN.
+ * Values past K or N get q = 8, scales past N zero.
+ */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_pack4(int type, int64_t E, int64_t K, int64_t N, int64_t group, const void *W,
+                                              uint32_t *Q, void *S, gemmpipe_stream_t stream);
+
+/* W = (q - 8) * scale, rounded to the type (off by at most half a step of it). */
+GEMMPIPE_API gemmpipe_status_t gemmpipe_unpack4(int type, int64_t E, int64_t K, int64_t N, int64_t group,
+                                                const uint32_t *Q, const void *S, void *W, gemmpipe_stream_t stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the current device's error
  * word.  Returns GEMMPIPE_ERR_TIMEOUT if a kernel of this library gave up on
  * a pipeline wait (every wait is bounded; the kernel then stops issuing

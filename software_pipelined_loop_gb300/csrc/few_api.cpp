@@ -1,0 +1,298 @@
+// few_api.cpp -- the entry points for a few tokens of include/gemmpipe.h:
+// rows times weights in 4 bits, the whole expert layer, and the weights' way
+// into 4 bits and back.  Argument checks and the choice of the launch.
+#include "gemmpipe.h"
+
+#include <cuda_runtime.h>
+
+#include <cstring>
+#include <initializer_list>
+#include <utility>
+
+#include "api_internal.h"
+#include "few.h"
+#include "grouped_params.h"
+
+namespace {
+
+using gp::ApiDevice;
+using gp::FewLaunch;
+using gp::FewParams;
+
+constexpr int64_t kMaxDim = 2147483647 - 1023;  // sizes rounded up to a block stay in 32 bits
+constexpr int64_t kMaxElems = int64_t(1) << 56;
+
+bool misaligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+bool bad_pointer(const void *p, int bytes) { return !p || misaligned(p, bytes); }
+bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
+bool bad_type(int type) { return type != GEMMPIPE_F16 && type != GEMMPIPE_BF16; }
+bool bad_group(int64_t group) { return group != 32 && group != 64 && group != 128; }
+bool bad_pitch(int64_t width, int64_t ld) { return ld < width || ld > 2147483647; }
+bool bad_experts(int64_t E) { return E < 1 || E > gp::kMaxExperts; }
+// Matrices E x K x N.
+bool bad_matrices(int64_t E, int64_t K, int64_t N)
+{
+    return bad_dim(K) || bad_dim(N) || (K > 0 && N > 0 && (K + 127) > kMaxElems / (E * (N + 3)));
+}
+
+gemmpipe_status_t check_all(std::initializer_list<std::pair<const void *, int>> ps)
+{
+    for (const auto &p : ps) {
+        if (!p.first) continue;  // optional
+        const gemmpipe_status_t st = gp::api_check_pointer(p.first, p.second);
+        if (st != GEMMPIPE_OK) return st;
+    }
+    return GEMMPIPE_OK;
+}
+
+cudaStream_t stream_of(gemmpipe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Nothing thrown leaves an entry point.
+template <class F>
+gemmpipe_status_t guarded(F f)
+{
+    try {
+        return f();
+    } catch (...) {
+        return GEMMPIPE_ERR_INTERNAL;
+    }
+}
+
+gemmpipe_status_t zero_rows(void *out, int64_t rows, int64_t width, int64_t ld, cudaStream_t s)
+{
+    const cudaError_t e = cudaMemset2DAsync(out, static_cast<size_t>(ld) * 2, 0, static_cast<size_t>(width) * 2,
+                                            static_cast<size_t>(rows), s);
+    if (e == cudaSuccess) return GEMMPIPE_OK;
+    cudaGetLastError();
+    return GEMMPIPE_ERR_LAUNCH;
+}
+
+int64_t align16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// The launch for `p` (sizes, matrices and ids set): how many blocks share the
+// products of 64 columns, and the shared memory.
+FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, bool down, int sms)
+{
+    FewLaunch l{};
+    l.bf16 = bf16;
+    l.four = four;
+    l.any = any;
+    l.down = down;
+    l.row_blocks = p->tokens <= 8 ? 1 : 4;
+    const int64_t chunk = 8 * l.row_blocks, slots = static_cast<int64_t>(p->tokens) * p->top_k;
+    p->steps = (p->K + gp::kFewStep - 1) / gp::kFewStep;
+    int64_t items = (p->tokens + chunk - 1) / chunk;
+    p->max_items = 0;
+    p->table_bytes = 0;
+    if (p->ids) {
+        // Every expert with rows, and a further item for each full chunk of them.
+        items = (slots < p->experts ? slots : p->experts) + slots / (chunk + 1);
+        p->max_items = static_cast<int>(items);
+        p->table_bytes = static_cast<int>(align16(4 * (3 * static_cast<int64_t>(p->experts) + items + 2 * slots + 1)));
+    }
+    l.grid_y = down ? 1 : static_cast<int>(items);
+    const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols, blocks = columns * l.grid_y;
+    const int64_t steps = p->steps * (down ? items : 1) * (down ? 1 : p->matrices);
+    l.split = 1;
+    while (l.split < 8 && blocks * l.split < 2 * sms && steps >= 2 * gp::kFewWarps * 2 * l.split) l.split *= 2;
+    l.grid_x = static_cast<int>(columns * l.split);
+    l.smem_bytes = p->table_bytes +
+                   4 * gp::kFewWarps * gp::kFewCols * static_cast<int>(down ? p->tokens : chunk);
+    return l;
+}
+
+cudaError_t launch(const FewLaunch &l, const FewParams &p, cudaStream_t s)
+{
+    return l.bf16 ? gp::launch_few_bf16(l, p, s) : gp::launch_few_f16(l, p, s);
+}
+
+struct Matrices {  // W of an expert step: 16 bits, or words with scales
+    const void *W[3];
+    const uint16_t *S[3];
+    int64_t group;  // 0: 16 bits
+};
+
+gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int64_t C, int64_t H, const uint16_t *X,
+                              int64_t ldx, const int32_t *experts, const float *weights, const Matrices &m,
+                              uint16_t *hidden, uint16_t *Y, int64_t ldy, gemmpipe_stream_t stream)
+{
+    const bool four = m.group != 0, gated = m.W[2] != nullptr;
+    if (bad_type(type) || T < 0 || T > gp::kFewRows || top_k < 1 || top_k > gp::kMaxTopK || bad_experts(E) ||
+        bad_matrices(E, C, H) || bad_matrices(E, H, C) || bad_pitch(C, ldx) || bad_pitch(C, ldy) ||
+        (four && bad_group(m.group)))
+        return GEMMPIPE_ERR_INVALID_VALUE;
+    if (T == 0 || C == 0) return GEMMPIPE_OK;
+    if (bad_pointer(Y, 2)) return GEMMPIPE_ERR_INVALID_VALUE;
+    const int wa = four ? 16 : 2, sa = four ? 8 : 1;
+    if (H > 0) {
+        if (bad_pointer(X, 2) || bad_pointer(experts, 4) || bad_pointer(weights, 4) || bad_pointer(hidden, 16))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        for (int i = 0; i < (gated ? 3 : 2); ++i)
+            if (bad_pointer(m.W[i], wa) || (four && bad_pointer(m.S[i], sa))) return GEMMPIPE_ERR_INVALID_VALUE;
+    }
+    if (four && !gated && m.S[2]) return GEMMPIPE_ERR_INVALID_VALUE;  // scales without their words
+    ApiDevice d;
+    gemmpipe_status_t st = gp::api_device(&d);
+    if (st != GEMMPIPE_OK) return st;
+    if ((st = check_all({{Y, 2}})) != GEMMPIPE_OK) return st;
+    cudaStream_t s = stream_of(stream);
+    if (H == 0) return zero_rows(Y, T, C, ldy, s);
+    if ((st = check_all({{X, 2}, {experts, 4}, {weights, 4}, {hidden, 16}})) != GEMMPIPE_OK) return st;
+    for (int i = 0; i < 3; ++i)
+        if ((st = check_all({{m.W[i], wa}, {m.S[i], sa}})) != GEMMPIPE_OK) return st;
+
+    const int64_t ldh = (H + 7) / 8 * 8;
+    FewParams up;
+    std::memset(&up, 0, sizeof(up));
+    up.ids = experts;
+    up.tokens = static_cast<int>(T);
+    up.top_k = static_cast<int>(top_k);
+    up.experts = static_cast<int>(E);
+    up.group_steps = four ? static_cast<int>(m.group / gp::kFewStep) : 1;
+    FewParams down = up;
+    up.X = X;
+    up.ldx = ldx;
+    up.W[0] = m.W[0];
+    up.S[0] = m.S[0];
+    up.W[1] = m.W[2];
+    up.S[1] = m.S[2];
+    up.matrices = gated ? 2 : 1;
+    up.silu = 1;
+    up.K = C;
+    up.N = H;
+    up.out = hidden;
+    up.ldo = up.out_cols = ldh;
+    down.X = hidden;
+    down.ldx = ldh;
+    down.weights = weights;
+    down.W[0] = m.W[1];
+    down.S[0] = m.S[1];
+    down.matrices = 1;
+    down.K = H;
+    down.N = down.out_cols = C;
+    down.out = Y;
+    down.ldo = ldy;
+    const bool rows_off = misaligned(X, 16) || ldx % 8 || C % 8;
+    const bool up_off = rows_off || (!four && (misaligned(m.W[0], 16) || misaligned(m.W[2], 16) || H % 8));
+    const bool down_off = !four && (misaligned(m.W[1], 16) || C % 8);
+    const bool bf16 = type == GEMMPIPE_BF16;
+    const FewLaunch lu = few_launch(&up, bf16, four, up_off, false, d.sms);
+    const FewLaunch ld = few_launch(&down, bf16, four, down_off, true, d.sms);
+    return gp::api_launch(true, s, 2, [&] {
+        const cudaError_t e = launch(lu, up, s);
+        return e != cudaSuccess ? e : launch(ld, down, s);
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t group, const void *X, int64_t ldx,
+                             const uint32_t *Q, const void *S, void *Y, int64_t ldy, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        if (bad_type(type) || M < 0 || M > gp::kFewRows || bad_matrices(1, K, N) || bad_group(group) ||
+            bad_pitch(K, ldx) || bad_pitch(N, ldy))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (M == 0 || N == 0) return GEMMPIPE_OK;
+        if (bad_pointer(Y, 2) || (K > 0 && (bad_pointer(X, 2) || bad_pointer(Q, 16) || bad_pointer(S, 8))))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{Y, 2}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        if (K == 0) return zero_rows(Y, M, N, ldy, s);
+        if ((st = check_all({{X, 2}, {Q, 16}, {S, 8}})) != GEMMPIPE_OK) return st;
+        FewParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.X = static_cast<const uint16_t *>(X);
+        p.ldx = ldx;
+        p.W[0] = Q;
+        p.S[0] = static_cast<const uint16_t *>(S);
+        p.matrices = 1;
+        p.out = static_cast<uint16_t *>(Y);
+        p.ldo = ldy;
+        p.K = K;
+        p.N = p.out_cols = N;
+        p.tokens = static_cast<int>(M);
+        p.top_k = 1;
+        p.experts = 1;
+        p.group_steps = static_cast<int>(group / gp::kFewStep);
+        const bool off = misaligned(X, 16) || ldx % 8 || K % 8;
+        const FewLaunch l = few_launch(&p, type == GEMMPIPE_BF16, true, off, false, d.sms);
+        return gp::api_launch(true, s, 1, [&] { return launch(l, p, s); });
+    });
+}
+
+gemmpipe_status_t gemmpipe_expert_step(int type, int64_t T, int64_t top_k, int64_t E, int64_t C, int64_t H,
+                                       const void *X, int64_t ldx, const int32_t *experts, const float *weights,
+                                       const void *W1, const void *W2, const void *W3, void *hidden, void *Y,
+                                       int64_t ldy, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        const Matrices m{{W1, W2, W3}, {nullptr, nullptr, nullptr}, 0};
+        return expert_step(type, T, top_k, E, C, H, static_cast<const uint16_t *>(X), ldx, experts, weights, m,
+                           static_cast<uint16_t *>(hidden), static_cast<uint16_t *>(Y), ldy, stream);
+    });
+}
+
+gemmpipe_status_t gemmpipe_expert_step4(int type, int64_t T, int64_t top_k, int64_t E, int64_t C, int64_t H,
+                                        int64_t group, const void *X, int64_t ldx, const int32_t *experts,
+                                        const float *weights, const uint32_t *Q1, const void *S1, const uint32_t *Q2,
+                                        const void *S2, const uint32_t *Q3, const void *S3, void *hidden, void *Y,
+                                        int64_t ldy, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        if (bad_group(group)) return GEMMPIPE_ERR_INVALID_VALUE;
+        const Matrices m{{Q1, Q2, Q3},
+                         {static_cast<const uint16_t *>(S1), static_cast<const uint16_t *>(S2),
+                          static_cast<const uint16_t *>(S3)},
+                         group};
+        return expert_step(type, T, top_k, E, C, H, static_cast<const uint16_t *>(X), ldx, experts, weights, m,
+                           static_cast<uint16_t *>(hidden), static_cast<uint16_t *>(Y), ldy, stream);
+    });
+}
+
+gemmpipe_status_t gemmpipe_pack4(int type, int64_t E, int64_t K, int64_t N, int64_t group, const void *W, uint32_t *Q,
+                                 void *S, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        if (bad_type(type) || bad_experts(E) || bad_matrices(E, K, N) || bad_group(group))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (K == 0 || N == 0) return GEMMPIPE_OK;
+        if (bad_pointer(W, 2) || bad_pointer(Q, 16) || bad_pointer(S, 8)) return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{W, 2}, {Q, 16}, {S, 8}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_pack4(type == GEMMPIPE_BF16, E, K, N, static_cast<int>(group),
+                                    static_cast<const uint16_t *>(W), Q, static_cast<uint16_t *>(S), s);
+        });
+    });
+}
+
+gemmpipe_status_t gemmpipe_unpack4(int type, int64_t E, int64_t K, int64_t N, int64_t group, const uint32_t *Q,
+                                   const void *S, void *W, gemmpipe_stream_t stream)
+{
+    return guarded([&] {
+        if (bad_type(type) || bad_experts(E) || bad_matrices(E, K, N) || bad_group(group))
+            return GEMMPIPE_ERR_INVALID_VALUE;
+        if (K == 0 || N == 0) return GEMMPIPE_OK;
+        if (bad_pointer(W, 2) || bad_pointer(Q, 16) || bad_pointer(S, 8)) return GEMMPIPE_ERR_INVALID_VALUE;
+        ApiDevice d;
+        gemmpipe_status_t st = gp::api_device(&d);
+        if (st != GEMMPIPE_OK) return st;
+        if ((st = check_all({{W, 2}, {Q, 16}, {S, 8}})) != GEMMPIPE_OK) return st;
+        cudaStream_t s = stream_of(stream);
+        return gp::api_launch(false, s, 1, [&] {
+            return gp::launch_unpack4(type == GEMMPIPE_BF16, E, K, N, static_cast<int>(group), Q,
+                                      static_cast<const uint16_t *>(S), static_cast<uint16_t *>(W), s);
+        });
+    });
+}
+
+}  // extern "C"

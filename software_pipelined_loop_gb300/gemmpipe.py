@@ -21,6 +21,7 @@ STATUS = {0: "GEMMPIPE_OK", 1: "GEMMPIPE_ERR_INVALID_VALUE", 2: "GEMMPIPE_ERR_UN
           3: "GEMMPIPE_ERR_LAUNCH", 4: "GEMMPIPE_ERR_TIMEOUT", 5: "GEMMPIPE_ERR_INTERNAL",
           6: "GEMMPIPE_ERR_OUT_OF_MEMORY"}
 F16, BF16 = 0, 1  # GEMMPIPE_F16, GEMMPIPE_BF16: the type argument of the expert-layer calls
+FEW_ROWS = 64  # GEMMPIPE_FEW_ROWS: rows or tokens of the few-token calls, at most
 NOALLOC_SCRATCH_BYTES = 16 << 20  # GEMMPIPE_NOALLOC_SCRATCH_BYTES
 OK, ERR_INVALID_VALUE, ERR_UNSUPPORTED_DEVICE, ERR_LAUNCH, ERR_TIMEOUT, ERR_INTERNAL, ERR_OUT_OF_MEMORY = range(7)
 
@@ -70,6 +71,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gemm_grouped_dw8": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
         "gemmpipe_keep8": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
         "gemmpipe_restore8": (_int, [_int, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+        "gemm_rows4": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+        "gemmpipe_expert_step": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _i64, _vp]),
+        "gemmpipe_expert_step4": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+        "gemmpipe_pack4": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+        "gemmpipe_unpack4": (_int, [_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
         "gemmpipe_host_panel_rows": (_i64, [_i64]),
         "gemmpipe_test_trace": (_int, [_vp, _i64]),
         "gemmpipe_get_device_status": (_int, [_vp]),
@@ -224,6 +232,41 @@ def gemmpipe_restore8(type, R, C, Q, S, X, ldx, stream=None) -> None:
     """X = Q * 2**(S - 127), the values that gemmpipe_keep8 kept."""
     _check(load().gemmpipe_restore8(type, R, C, _ptr(Q), _ptr(S), _ptr(X), ldx, _stream(stream)),
            "gemmpipe_restore8")
+
+
+def gemm_rows4(type, M, N, K, group, X, ldx, Q, S, Y, ldy, stream=None) -> None:
+    """Y = X @ W for at most 64 rows X and a K x N matrix in 4 bits (Q, S of gemmpipe_pack4)."""
+    _check(load().gemm_rows4(type, M, N, K, group, _ptr(X), ldx, _ptr(Q), _ptr(S), _ptr(Y), ldy, _stream(stream)),
+           "gemm_rows4")
+
+
+def gemmpipe_expert_step(type, T, top_k, E, C, H, X, ldx, experts, weights, W1, W2, W3, hidden, Y, ldy,
+                         stream=None) -> None:
+    """Y[t] = sum over j of weights[t, j] * (silu(X[t] @ W1[e]) [* (X[t] @ W3[e])]) @ W2[e], e = experts[t, j], for
+    at most 64 tokens (W3 None: ungated); hidden: T * top_k rows of H rounded up to 8, scratch."""
+    _check(load().gemmpipe_expert_step(type, T, top_k, E, C, H, _ptr(X), ldx, _ptr(experts), _ptr(weights), _ptr(W1),
+                                       _ptr(W2), _ptr(W3), _ptr(hidden), _ptr(Y), ldy, _stream(stream)),
+           "gemmpipe_expert_step")
+
+
+def gemmpipe_expert_step4(type, T, top_k, E, C, H, group, X, ldx, experts, weights, Q1, S1, Q2, S2, Q3, S3, hidden, Y,
+                          ldy, stream=None) -> None:
+    """gemmpipe_expert_step with the matrices as gemmpipe_pack4 left them."""
+    _check(load().gemmpipe_expert_step4(type, T, top_k, E, C, H, group, _ptr(X), ldx, _ptr(experts), _ptr(weights),
+                                        _ptr(Q1), _ptr(S1), _ptr(Q2), _ptr(S2), _ptr(Q3), _ptr(S3), _ptr(hidden),
+                                        _ptr(Y), ldy, _stream(stream)), "gemmpipe_expert_step4")
+
+
+def gemmpipe_pack4(type, E, K, N, group, W, Q, S, stream=None) -> None:
+    """W (E x K x N) into 4 bits: Q (E x ceil(K / 8) x N4 words) and S (E x ceil(K / group) x N4 scales), N4 = N
+    rounded up to a multiple of 4."""
+    _check(load().gemmpipe_pack4(type, E, K, N, group, _ptr(W), _ptr(Q), _ptr(S), _stream(stream)), "gemmpipe_pack4")
+
+
+def gemmpipe_unpack4(type, E, K, N, group, Q, S, W, stream=None) -> None:
+    """W = the values that gemmpipe_pack4 kept, rounded to the type."""
+    _check(load().gemmpipe_unpack4(type, E, K, N, group, _ptr(Q), _ptr(S), _ptr(W), _stream(stream)),
+           "gemmpipe_unpack4")
 
 
 def gemmpipe_host_panel_rows(M: int) -> int:
