@@ -85,16 +85,21 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, bool down, in
     p->max_items = 0;
     p->table_bytes = 0;
     if (p->ids) {
-        // Every expert with rows, and a further item for each full chunk of them.
+        // Every expert with rows, and one more for each that more than a chunk
+        // of the tokens (at most two chunks) chose.
         items = (slots < p->experts ? slots : p->experts) + slots / (chunk + 1);
+        if (slots <= 32) items = slots < p->experts ? slots : p->experts;
         p->max_items = static_cast<int>(items);
-        p->table_bytes = static_cast<int>(align16(4 * (3 * static_cast<int64_t>(p->experts) + items + 2 * slots + 1)));
+        const int64_t words = 2 * items + 2 * slots + 3 * static_cast<int64_t>(p->experts) + 1;
+        p->table_bytes = static_cast<int>(slots <= 32 ? 4 * gp::kFewWarps * 128 : align16(4 * words));
     }
     l.grid_y = down ? 1 : static_cast<int>(items);
+    // Blocks of a cluster share the products of 64 columns: as many as still
+    // run all at once, each with two rounds of loads a warp at least.
     const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols, blocks = columns * l.grid_y;
-    const int64_t steps = p->steps * (down ? items : 1) * (down ? 1 : p->matrices);
+    const int64_t steps = p->steps * (down ? items : p->matrices), slots_on_gpu = (l.row_blocks == 1 ? 2 : 1) * sms;
     l.split = 1;
-    while (l.split < 8 && blocks * l.split < 2 * sms && steps >= 2 * gp::kFewWarps * 2 * l.split) l.split *= 2;
+    while (l.split < 8 && blocks * 2 * l.split <= slots_on_gpu && steps >= 2 * gp::kFewWarps * 2 * l.split) l.split *= 2;
     l.grid_x = static_cast<int>(columns * l.split);
     l.smem_bytes = p->table_bytes +
                    4 * gp::kFewWarps * gp::kFewCols * static_cast<int>(down ? p->tokens : chunk);

@@ -86,8 +86,22 @@ __device__ __forceinline__ uint32_t few_pair(uint32_t word, int i)
     }
 }
 
+__device__ __forceinline__ uint4 few_ld_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 few_ld_v2(const void *p)
+{
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
 // 8 bytes at p if `on`, else zeros.
-__device__ __forceinline__ uint2 ld_global_v2_if(const void *p, bool on)
+__device__ __forceinline__ uint2 few_ld_v2_if(const void *p, bool on)
 {
     uint2 v;
     asm volatile(
@@ -138,43 +152,93 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 //
 // An item is an expert and up to CHUNK of the tokens that chose it, in order.
 // A token that chose one expert twice is one row with the sum of both weights.
+// Up to 32 choices are sorted by every warp on its own, in registers, into a
+// table of its own: one load of the ids and no barrier stand before the first
+// load of a weight.
 
 struct FewTables {
-    uint32_t *mask;    // 2 x experts: tokens that chose the expert
-    uint32_t *first;   // experts: its first row
-    uint32_t *expert;  // max_items: expert | chunk << 16
-    uint32_t *row;     // slots: token | slot << 8, sorted by expert and token
-    float *weight;     // slots
-    uint32_t *items;
+    uint32_t *expert;  // items: expert
+    uint32_t *span;    // items: first row | rows << 16
+    uint32_t *row;     // rows: token | slot << 8
+    float *weight;     // rows
 };
 
-__device__ __forceinline__ FewTables few_tables(const FewParams &p, unsigned char *smem)
+__host__ __device__ constexpr int few_own_table_words() { return 4 * 32; }
+
+// At most 32 choices; one table a warp.
+__device__ __forceinline__ int few_build_warp(const FewParams &p, FewTables &t, uint32_t *smem)
 {
-    FewTables t;
-    t.mask = reinterpret_cast<uint32_t *>(smem);
-    t.first = t.mask + 2 * p.experts;
-    t.expert = t.first + p.experts;
-    t.row = t.expert + p.max_items;
-    t.weight = reinterpret_cast<float *>(t.row + p.tokens * p.top_k);
-    t.items = reinterpret_cast<uint32_t *>(t.weight + p.tokens * p.top_k);
-    return t;
+    const int lane = threadIdx.x & 31, k = p.top_k, R = p.tokens * k;
+    t.expert = smem + (threadIdx.x >> 5) * few_own_table_words();
+    t.span = t.expert + 32;
+    t.row = t.span + 32;
+    t.weight = reinterpret_cast<float *>(t.row + 32);
+    uint32_t e = 0xffffffffu;
+    float w = 0.0f;
+    if (lane < R) {
+        e = static_cast<uint32_t>(p.ids[lane]);
+        if (p.weights) w = p.weights[lane];
+    }
+    const bool valid = lane < R && e < static_cast<uint32_t>(p.experts);
+    const int token = lane / k;
+    const uint32_t below = (1u << lane) - 1u, same = __match_any_sync(0xffffffffu, valid ? e : 0xffffffffu);
+    const int from = token * k;
+    const uint32_t mine = same & ((k >= 32 ? 0xffffffffu : (1u << k) - 1u) << (from & 31));  // this token's, same expert
+    const bool again = valid && (mine & below) != 0;
+    const uint32_t rows = __ballot_sync(0xffffffffu, valid && !again);
+    if (__any_sync(0xffffffffu, again)) {
+        float sum = w;
+        for (int j = 1; j < k; ++j) {
+            const float v = __shfl_down_sync(0xffffffffu, w, j);
+            if (lane + j < 32 && (mine >> (lane + j) & 1u)) sum += v;
+        }
+        w = sum;
+    }
+    const uint32_t peers = same & rows;
+    const bool row = valid && !again, leader = row && (peers & below) == 0;
+    const uint32_t items = __ballot_sync(0xffffffffu, leader);
+    const int count = __popc(peers);
+    int first = leader ? count : 0;  // sum of the rows of earlier items
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, first, d);
+        if (lane >= d) first += v;
+    }
+    first -= leader ? count : 0;
+    first = __shfl_sync(0xffffffffu, first, row ? __ffs(peers) - 1 : 0);
+    if (row) {
+        const int at = first + __popc(peers & below);
+        t.row[at] = static_cast<uint32_t>(token) | static_cast<uint32_t>(lane) << 8;
+        t.weight[at] = w;
+    }
+    if (leader) {
+        const int i = __popc(items & below);
+        t.expert[i] = e;
+        t.span[i] = static_cast<uint32_t>(first) | static_cast<uint32_t>(count) << 16;
+    }
+    __syncwarp();
+    return __popc(items);
 }
 
-__device__ __forceinline__ int few_rows_of(const FewTables &t, int e)
-{
-    return __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]);
-}
-
+// Any number of choices; one table a block.
 template <int CHUNK>
-__device__ __forceinline__ int few_build(const FewParams &p, const FewTables &t)
+__device__ __forceinline__ int few_build_block(const FewParams &p, FewTables &t, uint32_t *smem)
 {
     const int tid = threadIdx.x, k = p.top_k, R = p.tokens * k;
-    for (int i = tid; i < 2 * p.experts; i += blockDim.x) t.mask[i] = 0;
+    t.expert = smem;
+    t.span = t.expert + p.max_items;
+    t.row = t.span + p.max_items;
+    t.weight = reinterpret_cast<float *>(t.row + R);
+    uint32_t *mask = reinterpret_cast<uint32_t *>(t.weight + R);  // 2 x experts: tokens that chose the expert
+    uint32_t *start = mask + 2 * p.experts;                        // experts: first row
+    uint32_t *items_out = start + p.experts;
+    const auto rows_of = [&](int e) { return __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); };
+    for (int i = tid; i < 2 * p.experts; i += blockDim.x) mask[i] = 0;
     __syncthreads();
     for (int s = tid; s < R; s += blockDim.x) {
         const uint32_t e = static_cast<uint32_t>(p.ids[s]);
         const int token = s / k;
-        if (e < static_cast<uint32_t>(p.experts)) atomicOr(&t.mask[2 * e + (token >> 5)], 1u << (token & 31));
+        if (e < static_cast<uint32_t>(p.experts)) atomicOr(&mask[2 * e + (token >> 5)], 1u << (token & 31));
     }
     __syncthreads();
     if (tid < 32) {
@@ -182,7 +246,7 @@ __device__ __forceinline__ int few_build(const FewParams &p, const FewTables &t)
         const int lo = min(tid * per, p.experts), hi = min(lo + per, p.experts);
         uint32_t rows = 0, items = 0;
         for (int e = lo; e < hi; ++e) {
-            const int n = few_rows_of(t, e);
+            const int n = rows_of(e);
             rows += n;
             items += (n + CHUNK - 1) / CHUNK;
         }
@@ -194,12 +258,15 @@ __device__ __forceinline__ int few_build(const FewParams &p, const FewTables &t)
         }
         uint32_t row = (both & 0xffffu) - rows, item = (both >> 16) - items;
         for (int e = lo; e < hi; ++e) {
-            const int n = few_rows_of(t, e);
-            t.first[e] = row;
+            const int n = rows_of(e);
+            start[e] = row;
+            for (int c = 0; c < n; c += CHUNK) {
+                t.expert[item] = e;
+                t.span[item++] = (row + c) | static_cast<uint32_t>(min(n - c, CHUNK)) << 16;
+            }
             row += n;
-            for (int c = 0; c * CHUNK < n; ++c) t.expert[item++] = static_cast<uint32_t>(e) | static_cast<uint32_t>(c) << 16;
         }
-        if (tid == 31) *t.items = item;
+        if (tid == 31) *items_out = item;
     }
     __syncthreads();
     for (int s = tid; s < R; s += blockDim.x) {
@@ -216,13 +283,12 @@ __device__ __forceinline__ int few_build(const FewParams &p, const FewTables &t)
                 if (p.ids[i] == e) w += p.weights[i];
         }
         const uint32_t below = (1u << (token & 31)) - 1u;
-        const int at = token < 32 ? __popc(t.mask[2 * e] & below)
-                                  : __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1] & below);
-        t.row[t.first[e] + at] = static_cast<uint32_t>(token) | static_cast<uint32_t>(s) << 8;
-        t.weight[t.first[e] + at] = w;
+        const int at = token < 32 ? __popc(mask[2 * e] & below) : __popc(mask[2 * e]) + __popc(mask[2 * e + 1] & below);
+        t.row[start[e] + at] = static_cast<uint32_t>(token) | static_cast<uint32_t>(s) << 8;
+        t.weight[start[e] + at] = w;
     }
     __syncthreads();
-    return static_cast<int>(*t.items);
+    return static_cast<int>(*items_out);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -237,11 +303,11 @@ struct FewStage {
 // Where a warp's loads are: an item, a step of it, and this lane's places.
 template <int MB>
 struct FewWalk {
-    int item;
-    int64_t step;
+    int item, step, blocks;
+    int group;                  // 4 bits: steps left in the group
     const char *w;              // this lane's piece of the step's first row (4 bits: of its word row)
     const uint16_t *s;          // this lane's scales of the group
-    const uint16_t *x[MB];      // this lane's 8 values of each row (null: no row)
+    const uint16_t *x[MB];      // this lane's 8 values of each row (a place without a row: of the item's first)
 };
 
 template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
@@ -253,19 +319,23 @@ struct FewKernel {
     const FewTables &t;
     const void *W;
     const uint16_t *S;
-    int64_t n0;
-    int g, l4;  // lane / 4, lane % 4
-    int64_t n4;
+    int64_t n0, n4;
+    int g, l4;         // lane / 4, lane % 4
+    int steps;
+    int whole;         // steps whose loads of the warp are all inside the matrix
     int cols;          // 16 bits: this lane's columns inside the matrix (0 .. 8)
     bool on4[2];       // 4 bits: whether each piece is
 
     __device__ __forceinline__ FewKernel(const FewParams &p_, const FewTables &t_, int matrix, int64_t n0_)
-        : p(p_), t(t_), W(p_.W[matrix]), S(p_.S[matrix]), n0(n0_)
+        : p(p_), t(t_), W(matrix ? p_.W[1] : p_.W[0]), S(matrix ? p_.S[1] : p_.S[0]), n0(n0_)
     {
         const int lane = threadIdx.x & 31;
         g = lane >> 2;
         l4 = lane & 3;
         n4 = (p.N + 3) / 4 * 4;
+        steps = static_cast<int>(p.steps);
+        const bool wide = n0 + kFewCols <= (FOUR ? n4 : p.N);
+        whole = wide && !ANY ? static_cast<int>(p.K / kFewStep) : 0;
         if constexpr (FOUR) {
             on4[0] = n0 + 4 * g < n4;
             on4[1] = n0 + 32 + 4 * g < n4;
@@ -275,96 +345,99 @@ struct FewKernel {
         }
     }
 
-    // Row `i` of an item: its place in X, or -1.
-    __device__ __forceinline__ int64_t x_row(int item, int i) const
-    {
-        if (!p.ids) {
-            const int r = item * CHUNK + i;
-            return r < p.tokens ? r : -1;
-        }
-        const uint32_t e = t.expert[item] & 0xffffu, c = t.expert[item] >> 16;
-        const int r = static_cast<int>(c) * CHUNK + i;
-        if (r >= few_rows_of(t, e)) return -1;
-        const uint32_t row = t.row[t.first[e] + r];
-        return DOWN ? row >> 8 : row & 0xffu;
-    }
-
     __device__ __forceinline__ int rows_of(int item) const
     {
-        if (!p.ids) return min(p.tokens - item * CHUNK, CHUNK);
-        const uint32_t e = t.expert[item] & 0xffffu, c = t.expert[item] >> 16;
-        return min(few_rows_of(t, e) - static_cast<int>(c) * CHUNK, CHUNK);
+        return p.ids ? static_cast<int>(t.span[item] >> 16) : min(p.tokens - item * CHUNK, CHUNK);
     }
 
     __device__ __forceinline__ void place(FewWalk<MB> &k) const
     {
-        const int64_t e = p.ids ? t.expert[k.item] & 0xffffu : 0;
+        const int64_t e = p.ids ? t.expert[k.item] : 0;
         if constexpr (FOUR) {
-            const int64_t words = (p.K + 7) / 8, groups = (p.K + 32 * p.group_steps - 1) / (32 * p.group_steps);
-            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 4 * k.step + l4) * n4 + n0 + 4 * g);
-            k.s = S + (e * groups + k.step / p.group_steps) * n4 + n0 + 4 * g;
+            const int group_rows = 32 * p.group_steps, gr = k.step / p.group_steps;
+            const int64_t words = (p.K + 7) / 8, groups = (p.K + group_rows - 1) / group_rows;
+            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 4 * static_cast<int64_t>(k.step) + l4) * n4 + n0 + 4 * g);
+            k.s = S + (e * groups + gr) * n4 + n0 + 4 * g;
+            k.group = (gr + 1) * p.group_steps - k.step;
         } else {
-            k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * k.step + 8 * l4) * p.N + n0 + 8 * g);
-            k.s = nullptr;
+            k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + 8 * l4) * p.N + n0 + 8 * g);
         }
+        const int rows = rows_of(k.item), first = p.ids ? static_cast<int>(t.span[k.item] & 0xffffu) : k.item * CHUNK;
+        k.blocks = (rows + 7) / 8;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            const int64_t r = x_row(k.item, 8 * m + g);
-            k.x[m] = r < 0 ? nullptr : p.X + r * p.ldx + 32 * k.step + 8 * l4;
+            int64_t r = first + (8 * m + g < rows ? 8 * m + g : 0);
+            if (p.ids) r = DOWN ? t.row[r] >> 8 : t.row[r] & 0xffu;
+            k.x[m] = p.X + r * p.ldx + 32 * static_cast<int64_t>(k.step) + 8 * l4;
         }
     }
 
     __device__ __forceinline__ void advance(FewWalk<MB> &k, int items) const
     {
-        if (++k.step == p.steps) {
+        if (++k.step == steps) {
             k.step = 0;
             if (++k.item < items) place(k);
             return;
         }
         if constexpr (FOUR) {
             k.w += 16 * n4;  // 4 rows of words
-            if (k.step % p.group_steps == 0) k.s += n4;
+            if (--k.group == 0) {
+                k.s += n4;
+                k.group = p.group_steps;
+            }
         } else {
             k.w += 64 * p.N;
         }
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-            if (k.x[m]) k.x[m] += 32;
+        for (int m = 0; m < MB; ++m) k.x[m] += 32;
     }
 
-    __device__ __forceinline__ void load_w(FewStage<FOUR, MB> &st, const FewWalk<MB> &k, bool on) const
+    __device__ __forceinline__ void load_w(FewStage<FOUR, MB> &st, const FewWalk<MB> &k) const
     {
-        const int64_t left = p.K - (32 * k.step + 8 * l4);  // rows of the matrix from this lane's first
+        if (k.step < whole) {
+            if constexpr (FOUR) {
+#pragma unroll
+                for (int l = 0; l < 2; ++l) st.w[l] = few_ld_v4(k.w + 128 * l);
+#pragma unroll
+                for (int l = 0; l < 2; ++l) st.s[l] = few_ld_v2(k.s + 32 * l);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) st.w[r] = few_ld_v4(k.w + 2 * r * p.N);
+            }
+            return;
+        }
+        const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + 8 * l4);  // rows from this lane's first
         if constexpr (FOUR) {
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                st.w[l] = ld_global_v4_if(k.w + 128 * l, on && left > 0 && on4[l]);
-                st.s[l] = ld_global_v2_if(k.s + 32 * l, on && on4[l]);
+                st.w[l] = ld_global_v4_if(k.w + 128 * l, left > 0 && on4[l]);
+                st.s[l] = few_ld_v2_if(k.s + 32 * l, on4[l]);
             }
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const char *at = k.w + 2 * r * p.N;
                 if constexpr (ANY)
-                    st.w[r] = few_load8_any(reinterpret_cast<const uint16_t *>(at), on && r < left ? cols : 0);
+                    st.w[r] = few_load8_any(reinterpret_cast<const uint16_t *>(at), r < left ? cols : 0);
                 else
-                    st.w[r] = ld_global_v4_if(at, on && r < left && cols > 0);
+                    st.w[r] = ld_global_v4_if(at, r < left && cols > 0);
             }
         }
     }
 
-    __device__ __forceinline__ void load_x(FewStage<FOUR, MB> &st, const FewWalk<MB> &k, bool on) const
+    __device__ __forceinline__ void load_x(FewStage<FOUR, MB> &st, const FewWalk<MB> &k) const
     {
-        const int64_t left = p.K - (32 * k.step + 8 * l4);
-        const int count = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
+        // Aligned rows hold whole pieces (hidden rows end in zeros).
+        const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + 8 * l4);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            const bool has = on && k.x[m] != nullptr;
-            // Aligned rows hold whole pieces (hidden rows end in zeros).
-            if constexpr (ANY && !DOWN)
-                st.x[m] = few_first(few_load8_any(k.x[m], has ? count : 0), count);
-            else
-                st.x[m] = ld_global_v4_if(k.x[m], has && count > 0);
+            if (MB > 1 && m >= k.blocks) break;
+            if constexpr (ANY && !DOWN) {
+                const int count = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
+                st.x[m] = few_first(few_load8_any(k.x[m], count), count);
+            } else {
+                st.x[m] = ld_global_v4_if(k.x[m], left > 0);
+            }
         }
     }
 
@@ -375,7 +448,7 @@ struct FewKernel {
         if constexpr (FOUR) {
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                const uint32_t *w = &st.w[l].x;
+                const uint32_t w[4] = {st.w[l].x, st.w[l].y, st.w[l].z, st.w[l].w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t u[2][4];
@@ -403,12 +476,14 @@ struct FewKernel {
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                const uint32_t w[4][4] = {{st.w[4 * h].x, st.w[4 * h].y, st.w[4 * h].z, st.w[4 * h].w},
+                                          {st.w[4 * h + 1].x, st.w[4 * h + 1].y, st.w[4 * h + 1].z, st.w[4 * h + 1].w},
+                                          {st.w[4 * h + 2].x, st.w[4 * h + 2].y, st.w[4 * h + 2].z, st.w[4 * h + 2].w},
+                                          {st.w[4 * h + 3].x, st.w[4 * h + 3].y, st.w[4 * h + 3].z, st.w[4 * h + 3].w}};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t r0 = (&st.w[4 * h].x)[j], r1 = (&st.w[4 * h + 1].x)[j], r2 = (&st.w[4 * h + 2].x)[j],
-                                   r3 = (&st.w[4 * h + 3].x)[j];
-                    const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
-                    const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
+                    const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
+                    const uint32_t a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
 #pragma unroll
                     for (int m = 0; m < MB; ++m) {
                         if (MB > 1 && m >= blocks) break;
@@ -428,10 +503,10 @@ struct FewKernel {
     // Adds the sums of an item, weighted, to the warp's sums of the tokens.
     __device__ __forceinline__ void add(float *sums, const float (&acc)[4][MB][4], int item) const
     {
-        const uint32_t e = t.expert[item] & 0xffffu, c = t.expert[item] >> 16;
-        const int rows = rows_of(item), first = static_cast<int>(t.first[e]) + static_cast<int>(c) * CHUNK;
+        const int rows = static_cast<int>(t.span[item] >> 16), first = static_cast<int>(t.span[item] & 0xffffu);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
+            if (MB > 1 && 8 * m >= rows) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 8 * m + 2 * l4 + i;
@@ -450,10 +525,7 @@ struct FewKernel {
         }
     }
 
-    // Products [at, at + count) of the warp, counted over items x steps from
-    // item `base`; down: sums by token in `sums`, else the item's in acc.
-    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, int base, int items, int64_t at,
-                                         int64_t count) const
+    __device__ __forceinline__ static void clear(float (&acc)[4][MB][4])
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -461,49 +533,53 @@ struct FewKernel {
             for (int m = 0; m < MB; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.0f;
+    }
+
+    // The warp's `count` steps from step `step` of item `item` on; down: sums
+    // by token in `sums`, else the item's in acc.
+    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, int item, int step, int items,
+                                         int count) const
+    {
+        clear(acc);
         FewStage<FOUR, MB> st[DEPTH];
         FewWalk<MB> k;
-        k.item = base + static_cast<int>(at / p.steps);
-        k.step = at % p.steps;
-        int item = k.item;
-        int64_t step = k.step;
+        k.item = item;
+        k.step = step;
         if (count > 0) place(k);
         FewWalk<MB> kx = k;
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            load_w(st[d], k, d < count);
-            if (d < count) advance(k, items);
+            if (d >= count) break;
+            load_w(st[d], k);
+            advance(k, items);
         }
         if constexpr (DOWN) pdl_wait();  // hidden rows come from the launch before
+        int blocks = kx.blocks;
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            load_x(st[d], kx, d < count);
-            if (d < count) advance(kx, items);
+            if (d >= count) break;
+            load_x(st[d], kx);
+            if (DOWN || d + 1 < DEPTH) advance(kx, items);
         }
-        int blocks = count > 0 ? (rows_of(item) + 7) / 8 : 0;
-        for (int64_t i = 0; i < count; i += DEPTH) {
+        for (int i = 0; i < count; i += DEPTH) {
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
                 if (i + d >= count) break;
                 multiply(acc, st[d], blocks);
-                const bool more = i + d + DEPTH < count;
-                load_w(st[d], k, more);
-                load_x(st[d], k, more);
-                if (more) advance(k, items);
+                if (i + d + DEPTH < count) {
+                    load_w(st[d], k);
+                    load_x(st[d], k);
+                    advance(k, items);
+                }
                 if constexpr (DOWN) {
-                    if (++step == p.steps || i + d + 1 == count) {
+                    if (++step == steps || i + d + 1 == count) {
                         add(sums, acc, item);
-                        if (step == p.steps && i + d + 1 < count) {
+                        clear(acc);
+                        if (step == steps && i + d + 1 < count) {
                             step = 0;
                             ++item;
                             blocks = (rows_of(item) + 7) / 8;
                         }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) acc[j][m][c] = 0.0f;
                     }
                 }
             }
@@ -513,42 +589,48 @@ struct FewKernel {
 
 // grid: x = column blocks x cluster blocks, y = items (down: 1).
 template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
-__global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const __grid_constant__ FewParams p, int split)
+__global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
+    few_kernel(const __grid_constant__ FewParams p, int split)
 {
     using K = FewKernel<BF16, FOUR, ANY, MB, DOWN>;
     extern __shared__ __align__(16) unsigned char few_smem[];
-    if constexpr (!DOWN) pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5;
+    // The launch that makes hidden rows waits for everything before it and
+    // only then lets the next one start, which may read what was there before
+    // both, weights and choices, right away.
+    if constexpr (!DOWN) pdl_wait();
+    pdl_launch_dependents();
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * kFewCols;
-    const FewTables t = few_tables(p, few_smem);
     float *sums = reinterpret_cast<float *>(few_smem + p.table_bytes);
-
+    FewTables t{};
     int items = static_cast<int>(gridDim.y);
-    if (p.ids) items = few_build<K::CHUNK>(p, t);
+    if (p.ids) {
+        uint32_t *tables = reinterpret_cast<uint32_t *>(few_smem);
+        items = p.tokens * p.top_k <= 32 ? few_build_warp(p, t, tables) : few_build_block<K::CHUNK>(p, t, tables);
+    }
     float acc[4][MB][4];
     int count;  // rows of sums
-    int matrices = p.matrices;
     if constexpr (DOWN) {
-        matrices = 1;
         count = p.tokens;
-        float *own = sums + static_cast<int64_t>(warp) * p.tokens * kFewCols;
+        float *own = sums + warp * (p.tokens * kFewCols);
         for (int i = tid & 31; i < p.tokens * kFewCols; i += 32) own[i] = 0.0f;
         __syncwarp();
-        const int64_t total = static_cast<int64_t>(items) * p.steps, part = rank * kFewWarps + warp,
-                      parts = static_cast<int64_t>(split) * kFewWarps;
+        const int64_t total = static_cast<int64_t>(items) * p.steps;
+        const int part = rank * kFewWarps + warp, parts = split * kFewWarps;
         const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
         const K k(p, t, 0, n0);
-        k.walk(acc, own, 0, items, lo, hi - lo);
+        k.walk(acc, own, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
+               static_cast<int>(hi - lo));
     } else {
         const int item = blockIdx.y;
         if (item >= items) return;  // the whole cluster
-        const int warps = kFewWarps / matrices, matrix = warp / warps;
-        const int64_t part = rank * warps + warp % warps, parts = static_cast<int64_t>(split) * warps;
+        const int warps = kFewWarps / p.matrices, matrix = warp / warps;
+        const int part = rank * warps + warp % warps, parts = split * warps;
         const int64_t lo = p.steps * part / parts, hi = p.steps * (part + 1) / parts;
         const K k(p, t, matrix, n0);
         count = k.rows_of(item);
-        k.walk(acc, nullptr, item, item + 1, lo, hi - lo);
+        k.walk(acc, nullptr, item, static_cast<int>(lo), item + 1, static_cast<int>(hi - lo));
         float *own = sums + warp * (K::CHUNK * kFewCols);
 #pragma unroll
         for (int m = 0; m < MB; ++m)
@@ -562,42 +644,45 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const __grid_consta
     __syncthreads();
 
     // The warps' sums, then the cluster's, in order.
-    const int rows = DOWN ? p.tokens : K::CHUNK, total = count * kFewCols;
-    const int warps = kFewWarps / matrices;
+    const int slab = (DOWN ? p.tokens : K::CHUNK) * kFewCols, total = count * kFewCols;
+    const bool two = !DOWN && p.matrices == 2;
+    const int warps = two ? kFewWarps / 2 : kFewWarps;
     const auto finish = [&](int i, float a, float b) {
         const int r = i / kFewCols;
         const int64_t n = n0 + i % kFewCols;
         if (n >= p.out_cols) return;
-        if (p.silu) a = a / (1.0f + expf(-a));
-        if (matrices == 2) a *= b;
+        if (!DOWN && p.silu) a = a / (1.0f + expf(-a));
+        if (two) a *= b;
         int64_t to = r;
-        if (!DOWN) {
-            if (p.ids) {
-                const uint32_t e = t.expert[blockIdx.y] & 0xffffu, c = t.expert[blockIdx.y] >> 16;
-                to = t.row[t.first[e] + c * K::CHUNK + r] >> 8;
-            } else {
-                to = static_cast<int64_t>(blockIdx.y) * K::CHUNK + r;
-            }
-        }
+        if (!DOWN)
+            to = p.ids ? t.row[(t.span[blockIdx.y] & 0xffffu) + r] >> 8 : static_cast<int64_t>(blockIdx.y) * K::CHUNK + r;
         p.out[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
     };
     for (int i = tid; i < total; i += 32 * kFewWarps) {
-        float s[2] = {0.0f, 0.0f};
-        for (int m = 0; m < matrices; ++m) {
-            for (int w = 0; w < warps; ++w) s[m] += sums[(m * warps + w) * (rows * kFewCols) + i];
-            if (split > 1) sums[m * warps * (rows * kFewCols) + i] = s[m];
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+            const float v = sums[w * slab + i];
+            if (w < warps) a += v;
+            else b += v;
         }
-        if (split == 1) finish(i, s[0], s[1]);
+        if (split == 1) {
+            finish(i, a, b);
+        } else {
+            sums[i] = a;
+            if (two) sums[slab + i] = b;
+        }
     }
     if (split == 1) return;
     cluster_sync();
     const uint32_t base = smem_u32(sums);
     for (int i = rank * (32 * kFewWarps) + tid; i < total; i += split * (32 * kFewWarps)) {
-        float s[2] = {0.0f, 0.0f};
-        for (int m = 0; m < matrices; ++m)
-            for (int r = 0; r < split; ++r)
-                s[m] += ld_cluster_f32(mapa_shared(base + 4 * (m * warps * (rows * kFewCols) + i), r));
-        finish(i, s[0], s[1]);
+        float a = 0.0f, b = 0.0f;
+        for (int r = 0; r < split; ++r) {
+            a += ld_cluster_f32(mapa_shared(base + 4 * i, r));
+            if (two) b += ld_cluster_f32(mapa_shared(base + 4 * (slab + i), r));
+        }
+        finish(i, a, b);
     }
     cluster_sync();  // others may still read this block's sums
 }
@@ -621,10 +706,8 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (DOWN) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
     if (l.split > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = l.split;
