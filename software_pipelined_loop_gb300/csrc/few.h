@@ -10,7 +10,7 @@ namespace gp {
 
 constexpr int kFewRows = 64;       // rows or tokens of a call, at most
 constexpr int kFewCols = 64;       // output columns of a block
-constexpr int kFewWarps = 8;       // warps of a block
+constexpr int kFewWarps = 8;       // warps of a block, at most
 constexpr int kFewStep = 32;       // products of a row per step
 
 // One launch.  Products of rows with one matrix (`ids` null: `tokens` rows of X
@@ -35,12 +35,33 @@ struct FewParams {
     int silu;               // 1: silu of the (first) product
     int max_items;          // entries of the table of (expert, up to 8 * blocks of its rows)
     int table_bytes;        // shared memory before the sums
+    int depth;              // stages of a warp's ring, 1 to 8
 };
+
+// What a warp copies for one step of 32 products: 32 rows of 64 weights (16
+// bits: eight 16-byte pieces a row; off 16-byte boundaries nine, rows 8t .. 8t
+// + 7 shifted by 2t pieces so that the lanes of a load use different banks; 4
+// bits: 4 rows of words, and scales), and 32 values of the rows of X (off
+// boundaries: five pieces a row).
+template <bool FOUR, bool ANY_W, bool ANY_X, int MB>
+struct FewStage {
+    static constexpr int W_PITCH = 144, W_GROUP = 8 * W_PITCH + 32;
+    static constexpr int SCALES = 1024;
+    static constexpr int X = FOUR ? 1024 + 128 : (ANY_W ? 4 * W_GROUP : 4096);
+    static constexpr int X_BLOCK = ANY_X ? 640 : 512;
+    static constexpr int BYTES = X + MB * X_BLOCK;
+};
+
+constexpr int few_stage_bytes(bool four, bool any_w, bool any_x, int blocks)
+{
+    return (four ? 1024 + 128 : (any_w ? FewStage<false, true, true, 1>::X : 4096)) + blocks * (any_x ? 640 : 512);
+}
 
 struct FewLaunch {
     bool bf16, four, any, down;
     int row_blocks;         // 8-row blocks of an item: 1 or 4
     int split;              // blocks of a cluster, sharing the products
+    int warps;              // warps of a block
     int grid_x, grid_y;
     int smem_bytes;
 };

@@ -67,7 +67,7 @@ gemmpipe_status_t zero_rows(void *out, int64_t rows, int64_t width, int64_t ld, 
     return GEMMPIPE_ERR_LAUNCH;
 }
 
-int64_t align16(int64_t x) { return (x + 15) / 16 * 16; }
+int64_t align128(int64_t x) { return (x + 127) / 128 * 128; }
 
 // The launch for `p` (sizes, matrices and ids set): how many blocks share the
 // products of 64 columns, and the shared memory.
@@ -91,18 +91,30 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, bool down, in
         if (slots <= 32) items = slots < p->experts ? slots : p->experts;
         p->max_items = static_cast<int>(items);
         const int64_t words = 2 * items + 2 * slots + 3 * static_cast<int64_t>(p->experts) + 1;
-        p->table_bytes = static_cast<int>(slots <= 32 ? 4 * gp::kFewWarps * 128 : align16(4 * words));
+        p->table_bytes = static_cast<int>(slots <= 32 ? 4 * gp::kFewWarps * 128 : align128(4 * words));
     }
     l.grid_y = down ? 1 : static_cast<int>(items);
     // Blocks of a cluster share the products of 64 columns: as many as still
-    // run all at once, each with two rounds of loads a warp at least.
+    // run all at once, each with two steps a warp at least.
     const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols, blocks = columns * l.grid_y;
-    const int64_t steps = p->steps * (down ? items : p->matrices), slots_on_gpu = (l.row_blocks == 1 ? 2 : 1) * sms;
+    const int64_t steps = p->steps * (down ? items : p->matrices);
+    l.warps = down && p->tokens > 32 ? gp::kFewWarps / 2 : gp::kFewWarps;
     l.split = 1;
-    while (l.split < 8 && blocks * 2 * l.split <= slots_on_gpu && steps >= 2 * gp::kFewWarps * 2 * l.split) l.split *= 2;
+    while (l.split < 8 && blocks * 2 * l.split <= 2 * sms && steps >= 2 * l.warps * 2 * l.split) l.split *= 2;
     l.grid_x = static_cast<int>(columns * l.split);
-    l.smem_bytes = p->table_bytes +
-                   4 * gp::kFewWarps * gp::kFewCols * static_cast<int>(down ? p->tokens : chunk);
+    // Rings as deep as two blocks of an SM can have, else one; no deeper than
+    // the warps' steps.
+    const int stage = gp::few_stage_bytes(four, any && !four, any && !down, l.row_blocks) * l.warps;
+    const int sums = 4 * l.warps * gp::kFewCols * static_cast<int>(down ? p->tokens : chunk);
+    const int fixed = p->table_bytes + (down ? sums : 0);
+    constexpr int kTwo = 228 * 1024 / 2 - 1024, kOne = 227 * 1024;
+    int depth = (kTwo - fixed) / stage;
+    if (depth < 2) depth = (kOne - fixed) / stage;
+    const int64_t most = (steps + l.split * l.warps - 1) / (l.split * l.warps);
+    if (depth > most) depth = static_cast<int>(most);
+    p->depth = depth < 1 ? 1 : (depth > 8 ? 8 : depth);
+    l.smem_bytes = fixed + p->depth * stage;
+    if (!down && l.smem_bytes < p->table_bytes + sums) l.smem_bytes = p->table_bytes + sums;
     return l;
 }
 

@@ -52,6 +52,23 @@ __device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1,
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same without an addend.
+template <bool BF16>
+__device__ __forceinline__ void few_mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%10, %10, %10, %10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%10, %10, %10, %10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 template <bool BF16>
 __device__ __forceinline__ float few_float(uint32_t bits)
 {
@@ -70,63 +87,57 @@ __device__ __forceinline__ uint16_t few_round(float v)
         return __half_as_ushort(__float2half_rn(v));
 }
 
-// Values i and i + 4 of a word of eight 4-bit values: the pair of rows 2i, 2i + 1.
+// Values i and i + 4 of a word of eight 4-bit values: the pair of rows 2i, 2i
+// + 1.  (v & mask) | one is a single operation when both are in registers.
 template <bool BF16>
 __device__ __forceinline__ uint32_t few_pair(uint32_t word, int i)
 {
-    const uint32_t q = (word >> (4 * i)) & 0x000f000fu;
-    if constexpr (BF16) {
-        const uint32_t m = q | 0x43004300u;  // 128 + q
+    uint32_t m;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(BF16 ? 0x43004300u : 0x64006400u));
+    if constexpr (BF16) {  // 128 + q
         const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), __float2bfloat162_rn(136.0f));
         return *reinterpret_cast<const uint32_t *>(&v);
-    } else {
-        const uint32_t m = q | 0x64006400u;  // 1024 + q
+    } else {               // 1024 + q
         const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1032.0f));
         return *reinterpret_cast<const uint32_t *>(&v);
     }
 }
 
-__device__ __forceinline__ uint4 few_ld_v4(const void *p)
+// Asynchronous copies into this CTA's shared memory: `bytes` of 16 or 8 from
+// global memory, zeros behind them (0: nothing is read).
+__device__ __forceinline__ void few_copy16(uint32_t dst, const void *src, uint32_t bytes)
 {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ uint2 few_ld_v2(const void *p)
+__device__ __forceinline__ void few_copy16(uint32_t dst, const void *src)
 {
-    uint2 v;
-    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// 8 bytes at p if `on`, else zeros.
-__device__ __forceinline__ uint2 few_ld_v2_if(const void *p, bool on)
+__device__ __forceinline__ void few_copy8(uint32_t dst, const void *src, uint32_t bytes)
 {
-    uint2 v;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %3, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-        "@p ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y)
-        : "l"(p), "r"(on ? 1u : 0u)
-        : "memory");
-    return v;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Eight 16-bit elements at p, the first `count` of them (others: whatever is
-// there, or zeros); any 2-byte alignment.  Only words that hold one of the
-// first `count` are read.
-__device__ __forceinline__ uint4 few_load8_any(const uint16_t *p, int count)
+__device__ __forceinline__ void few_commit()
 {
-    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-    const char *a = reinterpret_cast<const char *>(p) - s;
-    const uint4 lo = ld_global_v4_if(a, count > 0);
-    const uint4 hi = ld_global_v4_if(a + 16, count > 0 && static_cast<int>(s) + 2 * (count < 8 ? count : 8) > 16);
-    uint32_t o[4];
-    realign16_steps(lo, hi, s, o);
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Waits until at most n - 1 of this thread's groups are incomplete (n: 1 .. 8).
+__device__ __forceinline__ void few_wait(int n)
+{
+    switch (n) {
+    case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 7: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    }
 }
 
 // The first `count` of eight 16-bit elements, zeros behind.
@@ -293,13 +304,6 @@ __device__ __forceinline__ int few_build_block(const FewParams &p, FewTables &t,
 
 // ------------------------------------------------------------------ kernel
 
-template <bool FOUR, int MB>
-struct FewStage {
-    uint4 w[FOUR ? 2 : 8];
-    uint2 s[FOUR ? 2 : 1];
-    uint4 x[MB];
-};
-
 // Where a warp's loads are: an item, a step of it, and this lane's places.
 template <int MB>
 struct FewWalk {
@@ -313,35 +317,37 @@ struct FewWalk {
 template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
 struct FewKernel {
     static constexpr int CHUNK = 8 * MB;
-    static constexpr int DEPTH = FOUR ? 4 : 2;  // steps whose loads are in flight
+    static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && !DOWN;
+    using Stage = FewStage<FOUR, ANY_W, ANY_X, MB>;
 
     const FewParams &p;
     const FewTables &t;
     const void *W;
     const uint16_t *S;
     int64_t n0, n4;
-    int g, l4;         // lane / 4, lane % 4
+    int lane, g, l4;   // lane / 4, lane % 4
     int steps;
     int whole;         // steps whose loads of the warp are all inside the matrix
-    int cols;          // 16 bits: this lane's columns inside the matrix (0 .. 8)
-    bool on4[2];       // 4 bits: whether each piece is
+    bool inside;       // whether this lane's pieces of W are
+    uint32_t put, get; // this lane's first place of W in a stage: to copy to, to read
 
     __device__ __forceinline__ FewKernel(const FewParams &p_, const FewTables &t_, int matrix, int64_t n0_)
         : p(p_), t(t_), W(matrix ? p_.W[1] : p_.W[0]), S(matrix ? p_.S[1] : p_.S[0]), n0(n0_)
     {
-        const int lane = threadIdx.x & 31;
+        lane = threadIdx.x & 31;
         g = lane >> 2;
         l4 = lane & 3;
         n4 = (p.N + 3) / 4 * 4;
         steps = static_cast<int>(p.steps);
         const bool wide = n0 + kFewCols <= (FOUR ? n4 : p.N);
         whole = wide && !ANY ? static_cast<int>(p.K / kFewStep) : 0;
+        inside = FOUR ? n0 + 4 * (lane & 15) < n4 : n0 + 8 * (lane & 7) < p.N;
         if constexpr (FOUR) {
-            on4[0] = n0 + 4 * g < n4;
-            on4[1] = n0 + 32 + 4 * g < n4;
+            put = 256 * (lane >> 4) + 16 * ((lane & 15) ^ (2 * (lane >> 4)));
+            get = 256 * l4 + 16 * (g ^ (2 * l4));
         } else {
-            const int64_t left = p.N - (n0 + 8 * g);
-            cols = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
+            put = 128 * (lane >> 3) + 16 * ((lane & 7) ^ (lane >> 3));
+            get = 1024 * l4 + 16 * (g ^ (2 * l4));
         }
     }
 
@@ -356,11 +362,12 @@ struct FewKernel {
         if constexpr (FOUR) {
             const int group_rows = 32 * p.group_steps, gr = k.step / p.group_steps;
             const int64_t words = (p.K + 7) / 8, groups = (p.K + group_rows - 1) / group_rows;
-            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 4 * static_cast<int64_t>(k.step) + l4) * n4 + n0 + 4 * g);
-            k.s = S + (e * groups + gr) * n4 + n0 + 4 * g;
+            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 4 * static_cast<int64_t>(k.step) + (lane >> 4)) * n4 + n0 + 4 * (lane & 15));
+            k.s = S + (e * groups + gr) * n4 + n0 + 4 * (lane & 15);
             k.group = (gr + 1) * p.group_steps - k.step;
         } else {
-            k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + 8 * l4) * p.N + n0 + 8 * g);
+            // (off 16-byte boundaries: the row, not the lane's piece of it)
+            k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + (lane >> 3)) * p.N + n0 + (ANY_W ? 0 : 8 * (lane & 7)));
         }
         const int rows = rows_of(k.item), first = p.ids ? static_cast<int>(t.span[k.item] & 0xffffu) : k.item * CHUNK;
         k.blocks = (rows + 7) / 8;
@@ -368,13 +375,14 @@ struct FewKernel {
         for (int m = 0; m < MB; ++m) {
             int64_t r = first + (8 * m + g < rows ? 8 * m + g : 0);
             if (p.ids) r = DOWN ? t.row[r] >> 8 : t.row[r] & 0xffu;
-            k.x[m] = p.X + r * p.ldx + 32 * static_cast<int64_t>(k.step) + 8 * l4;
+            k.x[m] = p.X + r * p.ldx + 32 * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
         }
     }
 
     __device__ __forceinline__ void advance(FewWalk<MB> &k, int items) const
     {
-        if (++k.step == steps) {
+        ++k.step;
+        if (DOWN && k.step == steps) {
             k.step = 0;
             if (++k.item < items) place(k);
             return;
@@ -392,63 +400,110 @@ struct FewKernel {
         for (int m = 0; m < MB; ++m) k.x[m] += 32;
     }
 
-    __device__ __forceinline__ void load_w(FewStage<FOUR, MB> &st, const FewWalk<MB> &k) const
+    // Neighbouring lanes copy neighbouring pieces (lanes that share a 32-byte
+    // sector but lie apart cost two requests to the L2 cache).  Pieces of a row
+    // are exchanged so that eight lanes that read together, two columns of rows
+    // 8t + r (4 bits: t), t = 0 .. 3, use all banks: piece c of row i is at
+    // c ^ (i % 8) ^ 2(i / 8), 4 bits: c ^ 2i.
+    __device__ __forceinline__ void load_w(uint32_t st, const FewWalk<MB> &k) const
     {
-        if (k.step < whole) {
-            if constexpr (FOUR) {
-#pragma unroll
-                for (int l = 0; l < 2; ++l) st.w[l] = few_ld_v4(k.w + 128 * l);
-#pragma unroll
-                for (int l = 0; l < 2; ++l) st.s[l] = few_ld_v2(k.s + 32 * l);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) st.w[r] = few_ld_v4(k.w + 2 * r * p.N);
-            }
-            return;
-        }
-        const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + 8 * l4);  // rows from this lane's first
         if constexpr (FOUR) {
+            const uint32_t to = st + put;
+            if (k.step < whole) {
+                few_copy16(to, k.w);
+                few_copy16((to ^ 64u) + 512, k.w + 8 * n4);
+                if (lane < 16) few_copy8(st + Stage::SCALES + 8 * lane, k.s, 8);
+            } else {
+                const int64_t left = (p.K + 7) / 8 - 4 * static_cast<int64_t>(k.step) - (lane >> 4);  // word rows
+                few_copy16(to, k.w, inside && left > 0 ? 16u : 0u);
+                few_copy16((to ^ 64u) + 512, k.w + 8 * n4, inside && left > 2 ? 16u : 0u);
+                if (lane < 16) few_copy8(st + Stage::SCALES + 8 * lane, k.s, inside ? 8u : 0u);
+            }
+        } else if constexpr (!ANY_W) {
+            const uint32_t to = st + put;
+            if (k.step < whole) {
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {
-                st.w[l] = ld_global_v4_if(k.w + 128 * l, left > 0 && on4[l]);
-                st.s[l] = few_ld_v2_if(k.s + 32 * l, on4[l]);
+                for (int i = 0; i < 8; ++i) few_copy16((to ^ (64u * (i & 1)) ^ (32u * (i >> 1))) + 512 * i, k.w + 8 * i * p.N);
+            } else {
+                const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + (lane >> 3));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    few_copy16((to ^ (64u * (i & 1)) ^ (32u * (i >> 1))) + 512 * i, k.w + 8 * i * p.N,
+                               inside && 4 * i < left ? 16u : 0u);
             }
         } else {
+            // A row's 128 bytes lie in up to nine aligned pieces: eight by
+            // neighbouring lanes, then the ninth of row `lane`.
+            const int64_t left = p.K - 32 * static_cast<int64_t>(k.step);
+            const int bytes = static_cast<int>(p.N - n0 < kFewCols ? 2 * (p.N - n0) : 2 * kFewCols);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const char *at = k.w + 2 * r * p.N;
-                if constexpr (ANY)
-                    st.w[r] = few_load8_any(reinterpret_cast<const uint16_t *>(at), r < left ? cols : 0);
-                else
-                    st.w[r] = ld_global_v4_if(at, r < left && cols > 0);
+            for (int i = 0; i < 9; ++i) {
+                const int row = i < 8 ? 4 * i + (lane >> 3) : lane, piece = i < 8 ? lane & 7 : 8;
+                const char *at = k.w + 2 * (row - (lane >> 3)) * p.N;
+                const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u);
+                few_copy16(st + Stage::W_GROUP * (row >> 3) + Stage::W_PITCH * (row & 7) + 16 * piece, at - off + 16 * piece,
+                           row < left && 16 * piece < off + bytes ? 16u : 0u);
             }
         }
     }
 
-    __device__ __forceinline__ void load_x(FewStage<FOUR, MB> &st, const FewWalk<MB> &k) const
+    __device__ __forceinline__ void load_x(uint32_t st, const FewWalk<MB> &k) const
     {
-        // Aligned rows hold whole pieces (hidden rows end in zeros).
-        const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + 8 * l4);
+        const int64_t from = 32 * static_cast<int64_t>(k.step);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             if (MB > 1 && m >= k.blocks) break;
-            if constexpr (ANY && !DOWN) {
-                const int count = left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
-                st.x[m] = few_first(few_load8_any(k.x[m], count), count);
+            const uint32_t to = st + Stage::X + Stage::X_BLOCK * m;
+            if constexpr (ANY_X) {
+                const int64_t left = p.K - from;
+                const int bytes = static_cast<int>(left < 32 ? 2 * left : 64);
+                const char *at = reinterpret_cast<const char *>(k.x[m]);
+                const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u);
+                few_copy16(to + 80 * g + 16 * l4, at - off + 16 * l4, 16 * l4 < off + bytes ? 16u : 0u);
+                if (l4 == 0) few_copy16(to + 80 * g + 64, at - off + 64, 64 < off + bytes ? 16u : 0u);
             } else {
-                st.x[m] = ld_global_v4_if(k.x[m], left > 0);
+                // Aligned rows hold whole pieces (hidden rows end in zeros).
+                if (k.step < whole) few_copy16(to + 16 * lane, k.x[m]);
+                else few_copy16(to + 16 * lane, k.x[m], from + 8 * l4 < p.K ? 16u : 0u);
             }
         }
+    }
+
+    // The eight weights of this lane's row r, whose row begins `off` bytes into its pieces.
+    __device__ __forceinline__ uint4 weights_any(uint32_t st, int r, int off) const
+    {
+        const uint32_t at = st + Stage::W_GROUP * l4 + Stage::W_PITCH * r + 16 * g;
+        uint32_t o[4];
+        realign16_steps(ld_shared_v4(at), ld_shared_v4(at + 16), off, o);
+        return make_uint4(o[0], o[1], o[2], o[3]);
     }
 
     // acc[j][m]: columns pair j of this lane, rows 8m + 2 * l4 and the next:
     // (column, row), (column, row + 1), (column + 1, row), (column + 1, row + 1).
-    __device__ __forceinline__ void multiply(float (&acc)[4][MB][4], const FewStage<FOUR, MB> &st, int blocks) const
+    // w_off, x_off: places of the step's operands off 16-byte boundaries.
+    __device__ __forceinline__ void multiply(float (&acc)[4][MB][4], uint32_t st, int step, int blocks, int w_off,
+                                             const int (&x_off)[MB]) const
     {
+        uint4 x[MB];
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            if (MB > 1 && m >= blocks) break;
+            const uint32_t at = st + Stage::X + Stage::X_BLOCK * m;
+            if constexpr (ANY_X) {
+                uint32_t o[4];
+                realign16_steps(ld_shared_v4(at + 80 * g + 16 * l4), ld_shared_v4(at + 80 * g + 16 * l4 + 16), x_off[m], o);
+                const int64_t left = p.K - (32 * static_cast<int64_t>(step) + 8 * l4);
+                x[m] = few_first(make_uint4(o[0], o[1], o[2], o[3]), left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8));
+            } else {
+                x[m] = ld_shared_v4(at + 16 * lane);
+            }
+        }
         if constexpr (FOUR) {
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                const uint32_t w[4] = {st.w[l].x, st.w[l].y, st.w[l].z, st.w[l].w};
+                const uint4 v = ld_shared_v4(st + get + 128 * l);
+                const uint2 scales = ld_shared_v2(st + Stage::SCALES + 64 * l + 8 * g);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t u[2][4];
@@ -457,14 +512,14 @@ struct FewKernel {
                         u[0][i] = few_pair<BF16>(w[2 * h], i);
                         u[1][i] = few_pair<BF16>(w[2 * h + 1], i);
                     }
-                    const uint32_t sc = h ? st.s[l].y : st.s[l].x;
+                    const uint32_t sc = h ? scales.y : scales.x;
                     const float s0 = few_float<BF16>(sc & 0xffffu), s1 = few_float<BF16>(sc >> 16);
 #pragma unroll
                     for (int m = 0; m < MB; ++m) {
                         if (MB > 1 && m >= blocks) break;
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        few_mma<BF16>(d, u[0][0], u[1][0], u[0][1], u[1][1], st.x[m].x, st.x[m].y);
-                        few_mma<BF16>(d, u[0][2], u[1][2], u[0][3], u[1][3], st.x[m].z, st.x[m].w);
+                        float d[4];
+                        few_mma_first<BF16>(d, u[0][0], u[1][0], u[0][1], u[1][1], x[m].x, x[m].y);
+                        few_mma<BF16>(d, u[0][2], u[1][2], u[0][3], u[1][3], x[m].z, x[m].w);
                         float(&a)[4] = acc[2 * l + h][m];
                         a[0] = fmaf(s0, d[0], a[0]);
                         a[1] = fmaf(s0, d[1], a[1]);
@@ -476,10 +531,19 @@ struct FewKernel {
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t w[4][4] = {{st.w[4 * h].x, st.w[4 * h].y, st.w[4 * h].z, st.w[4 * h].w},
-                                          {st.w[4 * h + 1].x, st.w[4 * h + 1].y, st.w[4 * h + 1].z, st.w[4 * h + 1].w},
-                                          {st.w[4 * h + 2].x, st.w[4 * h + 2].y, st.w[4 * h + 2].z, st.w[4 * h + 2].w},
-                                          {st.w[4 * h + 3].x, st.w[4 * h + 3].y, st.w[4 * h + 3].z, st.w[4 * h + 3].w}};
+                uint32_t w[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    uint4 v;
+                    if constexpr (ANY_W)
+                        v = weights_any(st, 4 * h + r, (w_off + 2 * static_cast<int>(p.N & 7) * (4 * h + r)) & 15);
+                    else
+                        v = ld_shared_v4(((st + get) ^ (16u * (4 * h + r))) + 128 * (4 * h + r));
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    w[r][2] = v.z;
+                    w[r][3] = v.w;
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
@@ -487,7 +551,7 @@ struct FewKernel {
 #pragma unroll
                     for (int m = 0; m < MB; ++m) {
                         if (MB > 1 && m >= blocks) break;
-                        few_mma<BF16>(acc[j][m], a0, a1, a2, a3, h ? st.x[m].z : st.x[m].x, h ? st.x[m].w : st.x[m].y);
+                        few_mma<BF16>(acc[j][m], a0, a1, a2, a3, h ? x[m].z : x[m].x, h ? x[m].w : x[m].y);
                     }
                 }
             }
@@ -535,50 +599,72 @@ struct FewKernel {
                 for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.0f;
     }
 
-    // The warp's `count` steps from step `step` of item `item` on; down: sums
-    // by token in `sums`, else the item's in acc.
-    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, int item, int step, int items,
-                                         int count) const
+    // Bytes from an aligned piece to the first row of W (those of rows 8t are
+    // the same) and to this lane's rows of X.
+    __device__ __forceinline__ void offsets(const FewWalk<MB> &k, int &w_off, int (&x_off)[MB]) const
+    {
+        if constexpr (ANY_W) w_off = static_cast<int>(reinterpret_cast<uintptr_t>(k.w - 2 * (lane >> 3) * p.N) & 15u);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+            if constexpr (ANY_X) x_off[m] = static_cast<int>(reinterpret_cast<uintptr_t>(k.x[m]) & 15u);
+    }
+
+    // The warp's `count` steps from step `step` of item `item` on, through its
+    // ring of `depth` stages; down: sums by token in `sums`, else the item's in
+    // acc.
+    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, uint32_t ring, int depth, int item,
+                                         int step, int items, int count) const
     {
         clear(acc);
-        FewStage<FOUR, MB> st[DEPTH];
         FewWalk<MB> k;
         k.item = item;
         k.step = step;
         if (count > 0) place(k);
         FewWalk<MB> kx = k;
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            if (d >= count) break;
-            load_w(st[d], k);
+        // A step is 64 bytes of X's row, 32 rows of W of any pitch a whole
+        // number of 16-byte pieces: what is off stays off within an item; the
+        // items' matrices and rows differ.
+        int w_off = 0, x_off[MB];
+        if (count > 0) offsets(k, w_off, x_off);
+        for (int d = 0; d < depth && d < count; ++d) {
+            load_w(ring + d * Stage::BYTES, k);
             advance(k, items);
         }
         if constexpr (DOWN) pdl_wait();  // hidden rows come from the launch before
-        int blocks = kx.blocks;
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            if (d >= count) break;
-            load_x(st[d], kx);
-            if (DOWN || d + 1 < DEPTH) advance(kx, items);
+        int blocks = count > 0 ? kx.blocks : 0;
+        for (int d = 0; d < depth; ++d) {
+            if (d < count) {
+                load_x(ring + d * Stage::BYTES, kx);
+                advance(kx, items);
+            }
+            few_commit();
         }
-        for (int i = 0; i < count; i += DEPTH) {
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                if (i + d >= count) break;
-                multiply(acc, st[d], blocks);
-                if (i + d + DEPTH < count) {
-                    load_w(st[d], k);
-                    load_x(st[d], k);
-                    advance(k, items);
-                }
-                if constexpr (DOWN) {
-                    if (++step == steps || i + d + 1 == count) {
-                        add(sums, acc, item);
-                        clear(acc);
-                        if (step == steps && i + d + 1 < count) {
-                            step = 0;
-                            ++item;
-                            blocks = (rows_of(item) + 7) / 8;
+        int slot = 0;
+        for (int i = 0; i < count; ++i) {
+            const uint32_t st = ring + slot * Stage::BYTES;
+            few_wait(depth);
+            __syncwarp();  // a lane's operands are other lanes' copies
+            multiply(acc, st, step, blocks, w_off, x_off);
+            if (i + depth < count) {
+                __syncwarp();
+                load_w(st, k);
+                load_x(st, k);
+                advance(k, items);
+            }
+            few_commit();
+            slot = slot + 1 == depth ? 0 : slot + 1;
+            ++step;
+            if constexpr (DOWN) {
+                if (step == steps || i + 1 == count) {
+                    add(sums, acc, item);
+                    clear(acc);
+                    if (i + 1 < count) {
+                        step = 0;
+                        ++item;
+                        blocks = (rows_of(item) + 7) / 8;
+                        if constexpr (ANY_W) {
+                            const char *at = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + t.expert[item] * p.K * p.N + n0);
+                            w_off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u);
                         }
                     }
                 }
@@ -589,11 +675,10 @@ struct FewKernel {
 
 // grid: x = column blocks x cluster blocks, y = items (down: 1).
 template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
-__global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
-    few_kernel(const __grid_constant__ FewParams p, int split)
+__global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_constant__ FewParams p, int split)
 {
     using K = FewKernel<BF16, FOUR, ANY, MB, DOWN>;
-    extern __shared__ __align__(16) unsigned char few_smem[];
+    extern __shared__ __align__(128) unsigned char few_smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
     // The launch that makes hidden rows waits for everything before it and
     // only then lets the next one start, which may read what was there before
@@ -602,7 +687,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
     pdl_launch_dependents();
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * kFewCols;
+    const int warps_all = static_cast<int>(blockDim.x) >> 5;
+    // Sums of tokens stand beside the rings, those of an item take their place.
     float *sums = reinterpret_cast<float *>(few_smem + p.table_bytes);
+    const uint32_t ring = smem_u32(sums) + (DOWN ? warps_all * p.tokens * kFewCols * 4 : 0) +
+                          warp * (p.depth * K::Stage::BYTES);
     FewTables t{};
     int items = static_cast<int>(gridDim.y);
     if (p.ids) {
@@ -617,20 +706,21 @@ __global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
         for (int i = tid & 31; i < p.tokens * kFewCols; i += 32) own[i] = 0.0f;
         __syncwarp();
         const int64_t total = static_cast<int64_t>(items) * p.steps;
-        const int part = rank * kFewWarps + warp, parts = split * kFewWarps;
+        const int part = rank * warps_all + warp, parts = split * warps_all;
         const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
         const K k(p, t, 0, n0);
-        k.walk(acc, own, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
+        k.walk(acc, own, ring, p.depth, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
                static_cast<int>(hi - lo));
     } else {
         const int item = blockIdx.y;
         if (item >= items) return;  // the whole cluster
-        const int warps = kFewWarps / p.matrices, matrix = warp / warps;
+        const int warps = warps_all / p.matrices, matrix = warp / warps;
         const int part = rank * warps + warp % warps, parts = split * warps;
         const int64_t lo = p.steps * part / parts, hi = p.steps * (part + 1) / parts;
         const K k(p, t, matrix, n0);
         count = k.rows_of(item);
-        k.walk(acc, nullptr, item, static_cast<int>(lo), item + 1, static_cast<int>(hi - lo));
+        k.walk(acc, nullptr, ring, p.depth, item, static_cast<int>(lo), item + 1, static_cast<int>(hi - lo));
+        __syncthreads();
         float *own = sums + warp * (K::CHUNK * kFewCols);
 #pragma unroll
         for (int m = 0; m < MB; ++m)
@@ -646,7 +736,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
     // The warps' sums, then the cluster's, in order.
     const int slab = (DOWN ? p.tokens : K::CHUNK) * kFewCols, total = count * kFewCols;
     const bool two = !DOWN && p.matrices == 2;
-    const int warps = two ? kFewWarps / 2 : kFewWarps;
+    const int warps = two ? warps_all / 2 : warps_all;
     const auto finish = [&](int i, float a, float b) {
         const int r = i / kFewCols;
         const int64_t n = n0 + i % kFewCols;
@@ -658,10 +748,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
             to = p.ids ? t.row[(t.span[blockIdx.y] & 0xffffu) + r] >> 8 : static_cast<int64_t>(blockIdx.y) * K::CHUNK + r;
         p.out[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
     };
-    for (int i = tid; i < total; i += 32 * kFewWarps) {
+    for (int i = tid; i < total; i += blockDim.x) {
         float a = 0.0f, b = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
+#pragma unroll 4
+        for (int w = 0; w < warps_all; ++w) {
             const float v = sums[w * slab + i];
             if (w < warps) a += v;
             else b += v;
@@ -676,7 +766,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, MB == 1 ? 2 : 1)
     if (split == 1) return;
     cluster_sync();
     const uint32_t base = smem_u32(sums);
-    for (int i = rank * (32 * kFewWarps) + tid; i < total; i += split * (32 * kFewWarps)) {
+    for (int i = rank * static_cast<int>(blockDim.x) + tid; i < total; i += split * static_cast<int>(blockDim.x)) {
         float a = 0.0f, b = 0.0f;
         for (int r = 0; r < split; ++r) {
             a += ld_cluster_f32(mapa_shared(base + 4 * i, r));
@@ -701,7 +791,7 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(l.grid_x, l.grid_y, 1);
-    cfg.blockDim = dim3(32 * kFewWarps, 1, 1);
+    cfg.blockDim = dim3(32 * l.warps, 1, 1);
     cfg.dynamicSmemBytes = l.smem_bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
