@@ -10,65 +10,79 @@ namespace gp {
 
 constexpr int kFewRows = 64;       // rows or tokens of a call, at most
 constexpr int kFewCols = 64;       // output columns of a block
-constexpr int kFewWarps = 8;       // warps of a block, at most
-constexpr int kFewStep = 32;       // products of a row per step
+constexpr int kFewWarps = 8;       // warps of a block
 
-// One launch.  Products of rows with one matrix (`ids` null: `tokens` rows of X
-// give `tokens` rows of `out`) or with the matrices of the experts that have
-// rows: upwards from the tokens' rows to one hidden row per choice, or (`down`)
-// from those to the weighted sum of each token.
+// What a launch computes:
+enum FewMode : int {
+    kFewUp = 0,    // rows of X times a matrix, or the tokens' rows times their experts' matrices: hidden rows
+    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (at most 8 tokens)
+    kFewParts = 2, // the same, one fp32 row for each choice: few_combine adds them
+};
+
+// One launch.  An item is an expert and up to 8 * blocks of the tokens that
+// chose it, or (`ids` null) so many of `tokens` rows of X.
 struct FewParams {
-    const uint16_t *X;      // rows by token; down: by slot
+    const uint16_t *X;      // kFewUp: rows by token; else by slot
     int64_t ldx;
     const int32_t *ids;     // tokens x top_k
-    const float *weights;   // tokens x top_k (down)
+    const float *weights;   // tokens x top_k (not kFewUp)
     const void *W[2];       // matrices experts x K x N (16 bits), or words experts x ceil(K / 8) x N4 (4 bits)
     const uint16_t *S[2];   // scales experts x ceil(K / group) x N4 (4 bits)
-    uint16_t *out;
+    void *out;              // 16 bits; kFewParts: fp32
     int64_t ldo;
     int64_t K, N;
     int64_t out_cols;       // columns of out: those past N are set to zero
-    int64_t steps;          // ceil(K / 32)
+    int64_t steps;          // ceil(K / step)
     int tokens, top_k, experts;
     int group_steps;        // group / 32
     int matrices;           // 2: silu(first product) * second product
     int silu;               // 1: silu of the (first) product
-    int max_items;          // entries of the table of (expert, up to 8 * blocks of its rows)
-    int table_bytes;        // shared memory before the sums
-    int depth;              // stages of a warp's ring, 1 to 8
+    int max_items;
+    int table_bytes;        // shared memory of the table of items
 };
 
-// What a warp copies for one step of 32 products: 32 rows of 64 weights (16
-// bits: eight 16-byte pieces a row; off 16-byte boundaries nine, rows 8t .. 8t
-// + 7 shifted by 2t pieces so that the lanes of a load use different banks; 4
-// bits: 4 rows of words, and scales), and 32 values of the rows of X (off
-// boundaries: five pieces a row).
+// What a warp copies for one step of 32 products (4 bits: 64): the rows of 64
+// weights (16 bits: eight 16-byte pieces a row; off 16-byte boundaries nine,
+// rows 8t .. 8t + 7 shifted by 2t pieces so that the lanes of a load use
+// different banks; 4 bits: 8 rows of words, and the scales of both halves),
+// and the values of the rows of X (off boundaries: a piece more).
 template <bool FOUR, bool ANY_W, bool ANY_X, int MB>
 struct FewStage {
+    static constexpr int STEP = FOUR ? 64 : 32;
     static constexpr int W_PITCH = 144, W_GROUP = 8 * W_PITCH + 32;
-    static constexpr int SCALES = 1024;
-    static constexpr int X = FOUR ? 1024 + 128 : (ANY_W ? 4 * W_GROUP : 4096);
-    static constexpr int X_BLOCK = ANY_X ? 640 : 512;
+    static constexpr int SCALES = 2048;
+    static constexpr int X = FOUR ? 2048 + 256 : (ANY_W ? 4 * W_GROUP : 4096);
+    static constexpr int X_PITCH = 2 * STEP + (ANY_X ? 16 : 0);
+    static constexpr int X_BLOCK = 8 * X_PITCH;
     static constexpr int BYTES = X + MB * X_BLOCK;
 };
 
-constexpr int few_stage_bytes(bool four, bool any_w, bool any_x, int blocks)
+// Stages of a warp's ring: as many as let two blocks run on an SM, with the
+// sums of 8 tokens (kFewFlat) or tables of some 500 choices beside them.
+template <bool FOUR, bool ANY, int MB, int MODE>
+constexpr int few_depth()
 {
-    return (four ? 1024 + 128 : (any_w ? FewStage<false, true, true, 1>::X : 4096)) + blocks * (any_x ? 640 : 512);
+    if (MODE == kFewFlat) return FOUR ? 3 : 2;
+    if (FOUR) return MB == 1 ? 4 : (MB == 2 ? 3 : 2);
+    return MB == 1 && !ANY ? 3 : 2;
 }
 
 struct FewLaunch {
-    bool bf16, four, any, down;
-    int row_blocks;         // 8-row blocks of an item: 1 or 4
+    bool bf16, four, any;
+    int mode;
+    int row_blocks;         // 8-row blocks of an item: 1, 2 or 4
     int split;              // blocks of a cluster, sharing the products
-    int warps;              // warps of a block
     int grid_x, grid_y;
-    int smem_bytes;
 };
 
 // four: weights in 4 bits; any: operands off 16-byte boundaries.
 cudaError_t launch_few_f16(const FewLaunch &l, const FewParams &p, cudaStream_t s);
 cudaError_t launch_few_bf16(const FewLaunch &l, const FewParams &p, cudaStream_t s);
+
+// Y[t] = sum of the rows of `parts` (tokens x top_k rows of `width`) that stand
+// for a choice: one inside [0, experts), the token's first of that expert.
+cudaError_t launch_few_combine(bool bf16, int tokens, int top_k, int experts, int64_t width, const int32_t *ids,
+                               const float *parts, uint16_t *Y, int64_t ldy, cudaStream_t s);
 
 cudaError_t launch_pack4(bool bf16, int64_t experts, int64_t K, int64_t N, int group, const uint16_t *W, uint32_t *Q,
                          uint16_t *S, cudaStream_t s);

@@ -69,52 +69,39 @@ gemmpipe_status_t zero_rows(void *out, int64_t rows, int64_t width, int64_t ld, 
 
 int64_t align128(int64_t x) { return (x + 127) / 128 * 128; }
 
-// The launch for `p` (sizes, matrices and ids set): how many blocks share the
-// products of 64 columns, and the shared memory.
-FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, bool down, int sms)
+// The launch for `p` (sizes, matrices and ids set).  Items hold 8 rows of up to
+// 8 tokens; above, 16 rows, or 32 where the experts have more on average.
+FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode, int sms)
 {
     FewLaunch l{};
     l.bf16 = bf16;
     l.four = four;
     l.any = any;
-    l.down = down;
-    l.row_blocks = p->tokens <= 8 ? 1 : 4;
-    const int64_t chunk = 8 * l.row_blocks, slots = static_cast<int64_t>(p->tokens) * p->top_k;
-    p->steps = (p->K + gp::kFewStep - 1) / gp::kFewStep;
+    l.mode = mode;
+    const int64_t slots = static_cast<int64_t>(p->tokens) * p->top_k;
+    const int64_t used = !p->ids ? 1 : (slots < p->experts ? slots : p->experts);  // experts with rows, at most
+    l.row_blocks = p->tokens <= 8 ? 1 : (p->tokens <= 16 || slots <= 16 * used || (any && !four) ? 2 : 4);
+    const int64_t chunk = 8 * l.row_blocks;
+    p->steps = (p->K + (four ? 63 : 31)) / (four ? 64 : 32);
     int64_t items = (p->tokens + chunk - 1) / chunk;
     p->max_items = 0;
     p->table_bytes = 0;
     if (p->ids) {
-        // Every expert with rows, and one more for each that more than a chunk
-        // of the tokens (at most two chunks) chose.
-        items = (slots < p->experts ? slots : p->experts) + slots / (chunk + 1);
-        if (slots <= 32) items = slots < p->experts ? slots : p->experts;
-        p->max_items = static_cast<int>(items);
-        const int64_t words = 2 * items + 2 * slots + 3 * static_cast<int64_t>(p->experts) + 1;
+        // An item for each expert with rows, and one more for each further chunk
+        // of them: taken by the blocks of the first ones.
+        items = used;
+        p->max_items = static_cast<int>(used + (p->tokens > chunk ? slots / chunk : 0));
+        const int64_t words = 2 * static_cast<int64_t>(p->max_items) + 2 * slots + 3 * static_cast<int64_t>(p->experts) + 1;
         p->table_bytes = static_cast<int>(slots <= 32 ? 4 * gp::kFewWarps * 128 : align128(4 * words));
     }
-    l.grid_y = down ? 1 : static_cast<int>(items);
+    l.grid_y = mode == gp::kFewFlat ? 1 : static_cast<int>(items);
     // Blocks of a cluster share the products of 64 columns: as many as still
-    // run all at once, each with two steps a warp at least.
+    // run all at once, each with a step a warp at least.
     const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols, blocks = columns * l.grid_y;
-    const int64_t steps = p->steps * (down ? items : p->matrices);
-    l.warps = down && p->tokens > 32 ? gp::kFewWarps / 2 : gp::kFewWarps;
+    const int64_t steps = p->steps * (mode == gp::kFewFlat ? items : p->matrices);
     l.split = 1;
-    while (l.split < 8 && blocks * 2 * l.split <= 2 * sms && steps >= 2 * l.warps * 2 * l.split) l.split *= 2;
+    while (l.split < 8 && blocks * 2 * l.split <= 2 * sms && steps >= gp::kFewWarps * 2 * l.split) l.split *= 2;
     l.grid_x = static_cast<int>(columns * l.split);
-    // Rings as deep as two blocks of an SM can have, else one; no deeper than
-    // the warps' steps.
-    const int stage = gp::few_stage_bytes(four, any && !four, any && !down, l.row_blocks) * l.warps;
-    const int sums = 4 * l.warps * gp::kFewCols * static_cast<int>(down ? p->tokens : chunk);
-    const int fixed = p->table_bytes + (down ? sums : 0);
-    constexpr int kTwo = 228 * 1024 / 2 - 1024, kOne = 227 * 1024;
-    int depth = (kTwo - fixed) / stage;
-    if (depth < 2) depth = (kOne - fixed) / stage;
-    const int64_t most = (steps + l.split * l.warps - 1) / (l.split * l.warps);
-    if (depth > most) depth = static_cast<int>(most);
-    p->depth = depth < 1 ? 1 : (depth > 8 ? 8 : depth);
-    l.smem_bytes = fixed + p->depth * stage;
-    if (!down && l.smem_bytes < p->table_bytes + sums) l.smem_bytes = p->table_bytes + sums;
     return l;
 }
 
@@ -165,7 +152,7 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     up.tokens = static_cast<int>(T);
     up.top_k = static_cast<int>(top_k);
     up.experts = static_cast<int>(E);
-    up.group_steps = four ? static_cast<int>(m.group / gp::kFewStep) : 1;
+    up.group_steps = four ? static_cast<int>(m.group / 32) : 1;
     FewParams down = up;
     up.X = X;
     up.ldx = ldx;
@@ -193,11 +180,26 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     const bool up_off = rows_off || (!four && (misaligned(m.W[0], 16) || misaligned(m.W[2], 16) || H % 8));
     const bool down_off = !four && (misaligned(m.W[1], 16) || C % 8);
     const bool bf16 = type == GEMMPIPE_BF16;
-    const FewLaunch lu = few_launch(&up, bf16, four, up_off, false, d.sms);
-    const FewLaunch ld = few_launch(&down, bf16, four, down_off, true, d.sms);
-    return gp::api_launch(true, s, 2, [&] {
-        const cudaError_t e = launch(lu, up, s);
-        return e != cudaSuccess ? e : launch(ld, down, s);
+    // The second products of up to 8 tokens are summed where they are made;
+    // those of more go by way of the workspace, a row for each choice.
+    const bool flat = T <= 8;
+    float *parts = nullptr;
+    if (!flat) {
+        void *ws = nullptr;
+        if ((st = gp::api_workspace(d.dev, s, 4 * T * top_k * C, &ws)) != GEMMPIPE_OK) return st;
+        parts = static_cast<float *>(ws);
+        down.out = parts;
+        down.ldo = C;
+    }
+    const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp, d.sms);
+    const FewLaunch ld = few_launch(&down, bf16, four, down_off, flat ? gp::kFewFlat : gp::kFewParts, d.sms);
+    return gp::api_launch(true, s, flat ? 2 : 3, [&] {
+        cudaError_t e = launch(lu, up, s);
+        if (e == cudaSuccess) e = launch(ld, down, s);
+        if (e == cudaSuccess && !flat)
+            e = gp::launch_few_combine(bf16, static_cast<int>(T), static_cast<int>(top_k), static_cast<int>(E), C,
+                                       experts, parts, Y, ldy, s);
+        return e;
     });
 }
 
@@ -236,9 +238,9 @@ gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t 
         p.tokens = static_cast<int>(M);
         p.top_k = 1;
         p.experts = 1;
-        p.group_steps = static_cast<int>(group / gp::kFewStep);
+        p.group_steps = static_cast<int>(group / 32);
         const bool off = misaligned(X, 16) || ldx % 8 || K % 8;
-        const FewLaunch l = few_launch(&p, type == GEMMPIPE_BF16, true, off, false, d.sms);
+        const FewLaunch l = few_launch(&p, type == GEMMPIPE_BF16, true, off, gp::kFewUp, d.sms);
         return gp::api_launch(true, s, 1, [&] { return launch(l, p, s); });
     });
 }

@@ -125,19 +125,11 @@ __device__ __forceinline__ void few_commit()
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Waits until at most n - 1 of this thread's groups are incomplete (n: 1 .. 8).
-__device__ __forceinline__ void few_wait(int n)
+// Waits until at most N of this thread's groups are incomplete.
+template <int N>
+__device__ __forceinline__ void few_wait()
 {
-    switch (n) {
-    case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 7: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The first `count` of eight 16-bit elements, zeros behind.
@@ -177,6 +169,7 @@ struct FewTables {
 __host__ __device__ constexpr int few_own_table_words() { return 4 * 32; }
 
 // At most 32 choices; one table a warp.
+template <int CHUNK>
 __device__ __forceinline__ int few_build_warp(const FewParams &p, FewTables &t, uint32_t *smem)
 {
     const int lane = threadIdx.x & 31, k = p.top_k, R = p.tokens * k;
@@ -207,28 +200,32 @@ __device__ __forceinline__ int few_build_warp(const FewParams &p, FewTables &t, 
     }
     const uint32_t peers = same & rows;
     const bool row = valid && !again, leader = row && (peers & below) == 0;
-    const uint32_t items = __ballot_sync(0xffffffffu, leader);
     const int count = __popc(peers);
-    int first = leader ? count : 0;  // sum of the rows of earlier items
+    // Rows and items of this expert and the ones before it.
+    const uint32_t both = leader ? count | (count + CHUNK - 1) / CHUNK << 16 : 0;
+    uint32_t sum = both;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, first, d);
-        if (lane >= d) first += v;
+        const uint32_t v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += v;
     }
-    first -= leader ? count : 0;
-    first = __shfl_sync(0xffffffffu, first, row ? __ffs(peers) - 1 : 0);
+    const int items = static_cast<int>(__shfl_sync(0xffffffffu, sum, 31) >> 16);
+    const uint32_t before = __shfl_sync(0xffffffffu, sum - both, row ? __ffs(peers) - 1 : 0);
+    const int first = static_cast<int>(before & 0xffffu);
     if (row) {
         const int at = first + __popc(peers & below);
         t.row[at] = static_cast<uint32_t>(token) | static_cast<uint32_t>(lane) << 8;
         t.weight[at] = w;
     }
     if (leader) {
-        const int i = __popc(items & below);
-        t.expert[i] = e;
-        t.span[i] = static_cast<uint32_t>(first) | static_cast<uint32_t>(count) << 16;
+        int i = static_cast<int>(before >> 16);
+        for (int c = 0; c < count; c += CHUNK, ++i) {
+            t.expert[i] = e;
+            t.span[i] = static_cast<uint32_t>(first + c) | static_cast<uint32_t>(min(count - c, CHUNK)) << 16;
+        }
     }
     __syncwarp();
-    return __popc(items);
+    return items;
 }
 
 // Any number of choices; one table a block.
@@ -308,16 +305,16 @@ __device__ __forceinline__ int few_build_block(const FewParams &p, FewTables &t,
 template <int MB>
 struct FewWalk {
     int item, step, blocks;
-    int group;                  // 4 bits: steps left in the group
     const char *w;              // this lane's piece of the step's first row (4 bits: of its word row)
     const uint16_t *s;          // this lane's scales of the group
     const uint16_t *x[MB];      // this lane's 8 values of each row (a place without a row: of the item's first)
 };
 
-template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
+template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 struct FewKernel {
-    static constexpr int CHUNK = 8 * MB;
-    static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && !DOWN;
+    static constexpr int CHUNK = 8 * MB, DEPTH = few_depth<FOUR, ANY, MB, MODE>();
+    static constexpr bool UP = MODE == kFewUp, FLAT = MODE == kFewFlat;
+    static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && UP;
     using Stage = FewStage<FOUR, ANY_W, ANY_X, MB>;
 
     const FewParams &p;
@@ -340,7 +337,7 @@ struct FewKernel {
         n4 = (p.N + 3) / 4 * 4;
         steps = static_cast<int>(p.steps);
         const bool wide = n0 + kFewCols <= (FOUR ? n4 : p.N);
-        whole = wide && !ANY ? static_cast<int>(p.K / kFewStep) : 0;
+        whole = wide && !ANY ? static_cast<int>(p.K / Stage::STEP) : 0;
         inside = FOUR ? n0 + 4 * (lane & 15) < n4 : n0 + 8 * (lane & 7) < p.N;
         if constexpr (FOUR) {
             put = 256 * (lane >> 4) + 16 * ((lane & 15) ^ (2 * (lane >> 4)));
@@ -358,13 +355,12 @@ struct FewKernel {
 
     __device__ __forceinline__ void place(FewWalk<MB> &k) const
     {
-        const int64_t e = p.ids ? t.expert[k.item] : 0;
+        const int64_t e = p.ids ? static_cast<int64_t>(t.expert[k.item]) : 0;
         if constexpr (FOUR) {
-            const int group_rows = 32 * p.group_steps, gr = k.step / p.group_steps;
+            const int group_rows = 32 * p.group_steps;
             const int64_t words = (p.K + 7) / 8, groups = (p.K + group_rows - 1) / group_rows;
-            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 4 * static_cast<int64_t>(k.step) + (lane >> 4)) * n4 + n0 + 4 * (lane & 15));
-            k.s = S + (e * groups + gr) * n4 + n0 + 4 * (lane & 15);
-            k.group = (gr + 1) * p.group_steps - k.step;
+            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 8 * static_cast<int64_t>(k.step) + (lane >> 4)) * n4 + n0 + 4 * (lane & 15));
+            k.s = S + (e * groups + (2 * k.step + (lane >> 4)) / p.group_steps) * n4 + n0 + 4 * (lane & 15);
         } else {
             // (off 16-byte boundaries: the row, not the lane's piece of it)
             k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + (lane >> 3)) * p.N + n0 + (ANY_W ? 0 : 8 * (lane & 7)));
@@ -374,30 +370,28 @@ struct FewKernel {
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             int64_t r = first + (8 * m + g < rows ? 8 * m + g : 0);
-            if (p.ids) r = DOWN ? t.row[r] >> 8 : t.row[r] & 0xffu;
-            k.x[m] = p.X + r * p.ldx + 32 * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
+            if (p.ids) r = UP ? t.row[r] & 0xffu : t.row[r] >> 8;
+            k.x[m] = p.X + r * p.ldx + Stage::STEP * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
         }
     }
 
     __device__ __forceinline__ void advance(FewWalk<MB> &k, int items) const
     {
         ++k.step;
-        if (DOWN && k.step == steps) {
+        if (FLAT && k.step == steps) {
             k.step = 0;
             if (++k.item < items) place(k);
             return;
         }
         if constexpr (FOUR) {
-            k.w += 16 * n4;  // 4 rows of words
-            if (--k.group == 0) {
-                k.s += n4;
-                k.group = p.group_steps;
-            }
+            k.w += 32 * n4;  // 8 rows of words
+            if (p.group_steps == 1) k.s += 2 * n4;
+            else if (p.group_steps == 2 || (k.step & 1) == 0) k.s += n4;
         } else {
             k.w += 64 * p.N;
         }
 #pragma unroll
-        for (int m = 0; m < MB; ++m) k.x[m] += 32;
+        for (int m = 0; m < MB; ++m) k.x[m] += Stage::STEP;
     }
 
     // Neighbouring lanes copy neighbouring pieces (lanes that share a 32-byte
@@ -408,16 +402,18 @@ struct FewKernel {
     __device__ __forceinline__ void load_w(uint32_t st, const FewWalk<MB> &k) const
     {
         if constexpr (FOUR) {
-            const uint32_t to = st + put;
+            const uint32_t to = st + put, scales = st + Stage::SCALES + 8 * lane;
             if (k.step < whole) {
-                few_copy16(to, k.w);
-                few_copy16((to ^ 64u) + 512, k.w + 8 * n4);
-                if (lane < 16) few_copy8(st + Stage::SCALES + 8 * lane, k.s, 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) few_copy16((to ^ (64u * (i & 1))) + 512 * i, k.w + 8 * i * n4);
+                few_copy8(scales, k.s, 8);
             } else {
-                const int64_t left = (p.K + 7) / 8 - 4 * static_cast<int64_t>(k.step) - (lane >> 4);  // word rows
-                few_copy16(to, k.w, inside && left > 0 ? 16u : 0u);
-                few_copy16((to ^ 64u) + 512, k.w + 8 * n4, inside && left > 2 ? 16u : 0u);
-                if (lane < 16) few_copy8(st + Stage::SCALES + 8 * lane, k.s, inside ? 8u : 0u);
+                const int64_t left = p.K - 64 * static_cast<int64_t>(k.step);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    few_copy16((to ^ (64u * (i & 1))) + 512 * i, k.w + 8 * i * n4,
+                               inside && 8 * (2 * i + (lane >> 4)) < left ? 16u : 0u);
+                few_copy8(scales, k.s, inside && 32 * (lane >> 4) < left ? 8u : 0u);
             }
         } else if constexpr (!ANY_W) {
             const uint32_t to = st + put;
@@ -447,25 +443,50 @@ struct FewKernel {
         }
     }
 
+    // Rows of 128 bytes exchange their halves in odd rows, so that eight lanes
+    // that read together, four pieces of two rows, use all banks.
     __device__ __forceinline__ void load_x(uint32_t st, const FewWalk<MB> &k) const
     {
-        const int64_t from = 32 * static_cast<int64_t>(k.step);
+        constexpr int HALVES = Stage::STEP / 32;
+        const int64_t left = p.K - Stage::STEP * static_cast<int64_t>(k.step);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             if (MB > 1 && m >= k.blocks) break;
-            const uint32_t to = st + Stage::X + Stage::X_BLOCK * m;
+            const uint32_t to = st + Stage::X + Stage::X_BLOCK * m + Stage::X_PITCH * g;
             if constexpr (ANY_X) {
-                const int64_t left = p.K - from;
-                const int bytes = static_cast<int>(left < 32 ? 2 * left : 64);
+                const int bytes = static_cast<int>(left < Stage::STEP ? 2 * left : 2 * Stage::STEP);
                 const char *at = reinterpret_cast<const char *>(k.x[m]);
                 const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u);
-                few_copy16(to + 80 * g + 16 * l4, at - off + 16 * l4, 16 * l4 < off + bytes ? 16u : 0u);
-                if (l4 == 0) few_copy16(to + 80 * g + 64, at - off + 64, 64 < off + bytes ? 16u : 0u);
+#pragma unroll
+                for (int i = 0; i <= HALVES; ++i) {
+                    const int piece = 4 * i + l4;
+                    if (i < HALVES || l4 == 0)
+                        few_copy16(to + 16 * piece, at - off + 16 * piece, 16 * piece < off + bytes ? 16u : 0u);
+                }
             } else {
                 // Aligned rows hold whole pieces (hidden rows end in zeros).
-                if (k.step < whole) few_copy16(to + 16 * lane, k.x[m]);
-                else few_copy16(to + 16 * lane, k.x[m], from + 8 * l4 < p.K ? 16u : 0u);
+                const uint32_t at = to + 16 * l4;
+#pragma unroll
+                for (int i = 0; i < HALVES; ++i) {
+                    const uint32_t half = HALVES > 1 ? 64u * (i ^ (g & 1)) : 0u;
+                    if (k.step < whole) few_copy16(at + half, k.x[m] + 32 * i);
+                    else few_copy16(at + half, k.x[m] + 32 * i, 32 * i + 8 * l4 < left ? 16u : 0u);
+                }
             }
+        }
+    }
+
+    // Eight values of this lane's row of block m, from 32 * half + 8 * l4 on.
+    __device__ __forceinline__ uint4 rows_x(uint32_t st, int m, int half, int off, int step) const
+    {
+        const uint32_t at = st + Stage::X + Stage::X_BLOCK * m + Stage::X_PITCH * g + 16 * l4;
+        if constexpr (ANY_X) {
+            uint32_t o[4];
+            realign16_steps(ld_shared_v4(at + 64 * half), ld_shared_v4(at + 64 * half + 16), off, o);
+            const int64_t left = p.K - (Stage::STEP * static_cast<int64_t>(step) + 32 * half + 8 * l4);
+            return few_first(make_uint4(o[0], o[1], o[2], o[3]), left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8));
+        } else {
+            return ld_shared_v4(at + (Stage::STEP > 32 ? 64u * (half ^ (g & 1)) : 0u));
         }
     }
 
@@ -478,48 +499,56 @@ struct FewKernel {
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
 
-    // acc[j][m]: columns pair j of this lane, rows 8m + 2 * l4 and the next:
-    // (column, row), (column, row + 1), (column + 1, row), (column + 1, row + 1).
-    // w_off, x_off: places of the step's operands off 16-byte boundaries.
-    __device__ __forceinline__ void multiply(float (&acc)[4][MB][4], uint32_t st, int step, int blocks, int w_off,
-                                             const int (&x_off)[MB]) const
+    // 4 bits: `SAME` halves of 32 products share their scales; their sums are
+    // multiplied together.
+    template <int SAME>
+    __device__ __forceinline__ void multiply4(float (&acc)[4][MB][4], uint32_t st, int step, int blocks,
+                                              const int (&x_off)[MB]) const
     {
-        uint4 x[MB];
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            if (MB > 1 && m >= blocks) break;
-            const uint32_t at = st + Stage::X + Stage::X_BLOCK * m;
-            if constexpr (ANY_X) {
-                uint32_t o[4];
-                realign16_steps(ld_shared_v4(at + 80 * g + 16 * l4), ld_shared_v4(at + 80 * g + 16 * l4 + 16), x_off[m], o);
-                const int64_t left = p.K - (32 * static_cast<int64_t>(step) + 8 * l4);
-                x[m] = few_first(make_uint4(o[0], o[1], o[2], o[3]), left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8));
-            } else {
-                x[m] = ld_shared_v4(at + 16 * lane);
-            }
-        }
-        if constexpr (FOUR) {
+        for (int q = 0; q < 2; q += SAME) {
+            uint4 x[SAME][MB];
+#pragma unroll
+            for (int i = 0; i < SAME; ++i)
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    if (MB > 1 && m >= blocks) break;
+                    x[i][m] = rows_x(st, m, q + i, x_off[m], step);
+                }
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                const uint4 v = ld_shared_v4(st + get + 128 * l);
-                const uint2 scales = ld_shared_v2(st + Stage::SCALES + 64 * l + 8 * g);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint2 scales = ld_shared_v2(st + Stage::SCALES + 128 * q + 64 * l + 8 * g);
+                uint32_t w[SAME][4];
+#pragma unroll
+                for (int i = 0; i < SAME; ++i) {
+                    const uint4 v = ld_shared_v4(st + get + 1024 * (q + i) + 128 * l);
+                    w[i][0] = v.x;
+                    w[i][1] = v.y;
+                    w[i][2] = v.z;
+                    w[i][3] = v.w;
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t u[2][4];
+                    uint32_t u[SAME][2][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        u[0][i] = few_pair<BF16>(w[2 * h], i);
-                        u[1][i] = few_pair<BF16>(w[2 * h + 1], i);
-                    }
+                    for (int i = 0; i < SAME; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            u[i][0][c] = few_pair<BF16>(w[i][2 * h], c);
+                            u[i][1][c] = few_pair<BF16>(w[i][2 * h + 1], c);
+                        }
                     const uint32_t sc = h ? scales.y : scales.x;
                     const float s0 = few_float<BF16>(sc & 0xffffu), s1 = few_float<BF16>(sc >> 16);
 #pragma unroll
                     for (int m = 0; m < MB; ++m) {
                         if (MB > 1 && m >= blocks) break;
                         float d[4];
-                        few_mma_first<BF16>(d, u[0][0], u[1][0], u[0][1], u[1][1], x[m].x, x[m].y);
-                        few_mma<BF16>(d, u[0][2], u[1][2], u[0][3], u[1][3], x[m].z, x[m].w);
+                        few_mma_first<BF16>(d, u[0][0][0], u[0][1][0], u[0][0][1], u[0][1][1], x[0][m].x, x[0][m].y);
+                        few_mma<BF16>(d, u[0][0][2], u[0][1][2], u[0][0][3], u[0][1][3], x[0][m].z, x[0][m].w);
+                        if constexpr (SAME == 2) {
+                            few_mma<BF16>(d, u[1][0][0], u[1][1][0], u[1][0][1], u[1][1][1], x[1][m].x, x[1][m].y);
+                            few_mma<BF16>(d, u[1][0][2], u[1][1][2], u[1][0][3], u[1][1][3], x[1][m].z, x[1][m].w);
+                        }
                         float(&a)[4] = acc[2 * l + h][m];
                         a[0] = fmaf(s0, d[0], a[0]);
                         a[1] = fmaf(s0, d[1], a[1]);
@@ -528,7 +557,26 @@ struct FewKernel {
                     }
                 }
             }
+        }
+    }
+
+    // acc[j][m]: columns pair j of this lane, rows 8m + 2 * l4 and the next:
+    // (column, row), (column, row + 1), (column + 1, row), (column + 1, row + 1).
+    // w_off, x_off: places of the step's operands off 16-byte boundaries.
+    __device__ __forceinline__ void multiply(float (&acc)[4][MB][4], uint32_t st, int step, int blocks, int w_off,
+                                             const int (&x_off)[MB]) const
+    {
+        if constexpr (FOUR) {
+            // (32 rows: the registers do not hold both halves' operands)
+            if (MB < 4 && p.group_steps > 1) multiply4<MB < 4 ? 2 : 1>(acc, st, step, blocks, x_off);
+            else multiply4<1>(acc, st, step, blocks, x_off);
         } else {
+            uint4 x[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                if (MB > 1 && m >= blocks) break;
+                x[m] = rows_x(st, m, 0, x_off[m], step);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t w[4][4];
@@ -610,10 +658,9 @@ struct FewKernel {
     }
 
     // The warp's `count` steps from step `step` of item `item` on, through its
-    // ring of `depth` stages; down: sums by token in `sums`, else the item's in
-    // acc.
-    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, uint32_t ring, int depth, int item,
-                                         int step, int items, int count) const
+    // ring; kFewFlat: sums by token in `sums`, else the item's in acc.
+    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, uint32_t ring, int item, int step,
+                                         int items, int count) const
     {
         clear(acc);
         FewWalk<MB> k;
@@ -621,40 +668,41 @@ struct FewKernel {
         k.step = step;
         if (count > 0) place(k);
         FewWalk<MB> kx = k;
-        // A step is 64 bytes of X's row, 32 rows of W of any pitch a whole
-        // number of 16-byte pieces: what is off stays off within an item; the
-        // items' matrices and rows differ.
+        // A step is a whole number of 16-byte pieces of X's row, and rows of W of
+        // any pitch: what is off stays off within an item; matrices differ.
         int w_off = 0, x_off[MB];
         if (count > 0) offsets(k, w_off, x_off);
-        for (int d = 0; d < depth && d < count; ++d) {
-            load_w(ring + d * Stage::BYTES, k);
-            advance(k, items);
-        }
-        if constexpr (DOWN) pdl_wait();  // hidden rows come from the launch before
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (d < count) {
+                load_w(ring + d * Stage::BYTES, k);
+                advance(k, items);
+            }
+        if constexpr (!UP) pdl_wait();  // hidden rows come from the launch before
         int blocks = count > 0 ? kx.blocks : 0;
-        for (int d = 0; d < depth; ++d) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
             if (d < count) {
                 load_x(ring + d * Stage::BYTES, kx);
-                advance(kx, items);
+                if (d + 1 < DEPTH) advance(kx, items);
             }
             few_commit();
         }
-        int slot = 0;
+        uint32_t st = ring;
         for (int i = 0; i < count; ++i) {
-            const uint32_t st = ring + slot * Stage::BYTES;
-            few_wait(depth);
+            few_wait<DEPTH - 1>();
             __syncwarp();  // a lane's operands are other lanes' copies
             multiply(acc, st, step, blocks, w_off, x_off);
-            if (i + depth < count) {
-                __syncwarp();
+            __syncwarp();
+            if (i + DEPTH < count) {
                 load_w(st, k);
                 load_x(st, k);
                 advance(k, items);
             }
             few_commit();
-            slot = slot + 1 == depth ? 0 : slot + 1;
+            st = st == ring + (DEPTH - 1) * Stage::BYTES ? ring : st + Stage::BYTES;
             ++step;
-            if constexpr (DOWN) {
+            if constexpr (FLAT) {
                 if (step == steps || i + 1 == count) {
                     add(sums, acc, item);
                     clear(acc);
@@ -673,126 +721,143 @@ struct FewKernel {
     }
 };
 
-// grid: x = column blocks x cluster blocks, y = items (down: 1).
-template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
+// grid: x = column blocks x cluster blocks, y = items (kFewFlat: 1).
+template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 __global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_constant__ FewParams p, int split)
 {
-    using K = FewKernel<BF16, FOUR, ANY, MB, DOWN>;
+    using K = FewKernel<BF16, FOUR, ANY, MB, MODE>;
+    constexpr bool UP = K::UP, FLAT = K::FLAT;
     extern __shared__ __align__(128) unsigned char few_smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
     // The launch that makes hidden rows waits for everything before it and
     // only then lets the next one start, which may read what was there before
     // both, weights and choices, right away.
-    if constexpr (!DOWN) pdl_wait();
+    if constexpr (UP) pdl_wait();
     pdl_launch_dependents();
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * kFewCols;
-    const int warps_all = static_cast<int>(blockDim.x) >> 5;
     // Sums of tokens stand beside the rings, those of an item take their place.
     float *sums = reinterpret_cast<float *>(few_smem + p.table_bytes);
-    const uint32_t ring = smem_u32(sums) + (DOWN ? warps_all * p.tokens * kFewCols * 4 : 0) +
-                          warp * (p.depth * K::Stage::BYTES);
+    const uint32_t ring = smem_u32(sums) + (FLAT ? kFewWarps * p.tokens * kFewCols * 4 : 0) +
+                          warp * (K::DEPTH * K::Stage::BYTES);
     FewTables t{};
     int items = static_cast<int>(gridDim.y);
     if (p.ids) {
         uint32_t *tables = reinterpret_cast<uint32_t *>(few_smem);
-        items = p.tokens * p.top_k <= 32 ? few_build_warp(p, t, tables) : few_build_block<K::CHUNK>(p, t, tables);
+        items = p.tokens * p.top_k <= 32 ? few_build_warp<K::CHUNK>(p, t, tables) : few_build_block<K::CHUNK>(p, t, tables);
     }
     float acc[4][MB][4];
-    int count;  // rows of sums
-    if constexpr (DOWN) {
-        count = p.tokens;
-        float *own = sums + warp * (p.tokens * kFewCols);
-        for (int i = tid & 31; i < p.tokens * kFewCols; i += 32) own[i] = 0.0f;
-        __syncwarp();
-        const int64_t total = static_cast<int64_t>(items) * p.steps;
-        const int part = rank * warps_all + warp, parts = split * warps_all;
-        const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
-        const K k(p, t, 0, n0);
-        k.walk(acc, own, ring, p.depth, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
-               static_cast<int>(hi - lo));
-    } else {
-        const int item = blockIdx.y;
-        if (item >= items) return;  // the whole cluster
-        const int warps = warps_all / p.matrices, matrix = warp / warps;
-        const int part = rank * warps + warp % warps, parts = split * warps;
-        const int64_t lo = p.steps * part / parts, hi = p.steps * (part + 1) / parts;
-        const K k(p, t, matrix, n0);
-        count = k.rows_of(item);
-        k.walk(acc, nullptr, ring, p.depth, item, static_cast<int>(lo), item + 1, static_cast<int>(hi - lo));
-        __syncthreads();
-        float *own = sums + warp * (K::CHUNK * kFewCols);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<float2 *>(own + (8 * m + 2 * k.l4 + i) * kFewCols + k.column(j)) =
-                        make_float2(acc[j][m][i], acc[j][m][2 + i]);
-    }
-    __syncthreads();
+    const int matrices = UP ? p.matrices : 1, warps = kFewWarps / matrices;
+    const int slab = (FLAT ? p.tokens : K::CHUNK) * kFewCols;  // a warp's sums
+    const bool two = matrices == 2;
 
-    // The warps' sums, then the cluster's, in order.
-    const int slab = (DOWN ? p.tokens : K::CHUNK) * kFewCols, total = count * kFewCols;
-    const bool two = !DOWN && p.matrices == 2;
-    const int warps = two ? warps_all / 2 : warps_all;
-    const auto finish = [&](int i, float a, float b) {
+    // Where sum i of an item is stored, and how.
+    const auto finish = [&](int item, int i, float a, float b) {
         const int r = i / kFewCols;
         const int64_t n = n0 + i % kFewCols;
         if (n >= p.out_cols) return;
-        if (!DOWN && p.silu) a = a / (1.0f + expf(-a));
+        if (UP && p.silu) a = a / (1.0f + expf(-a));
         if (two) a *= b;
         int64_t to = r;
-        if (!DOWN)
-            to = p.ids ? t.row[(t.span[blockIdx.y] & 0xffffu) + r] >> 8 : static_cast<int64_t>(blockIdx.y) * K::CHUNK + r;
-        p.out[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
+        if constexpr (!FLAT) {
+            if (p.ids) {
+                const uint32_t row = (t.span[item] & 0xffffu) + r;
+                to = t.row[row] >> 8;
+                if constexpr (!UP) a *= t.weight[row];
+            } else {
+                to = static_cast<int64_t>(item) * K::CHUNK + r;
+            }
+        }
+        if constexpr (MODE == kFewParts)
+            static_cast<float *>(p.out)[to * p.ldo + n] = a;
+        else
+            static_cast<uint16_t *>(p.out)[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
     };
-    for (int i = tid; i < total; i += blockDim.x) {
-        float a = 0.0f, b = 0.0f;
-#pragma unroll 4
-        for (int w = 0; w < warps_all; ++w) {
-            const float v = sums[w * slab + i];
-            if (w < warps) a += v;
-            else b += v;
+    // Adds the warps' `count` rows of sums, then the cluster's, in order.
+    const auto join = [&](int item, int count) {
+        const int total = count * kFewCols;
+        __syncthreads();
+        for (int i = tid; i < total; i += 32 * kFewWarps) {
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) {
+                const float v = sums[w * slab + i];
+                if (w < warps) a += v;
+                else b += v;
+            }
+            if (split == 1) {
+                finish(item, i, a, b);
+            } else {
+                sums[i] = a;
+                if (two) sums[slab + i] = b;
+            }
         }
-        if (split == 1) {
-            finish(i, a, b);
-        } else {
-            sums[i] = a;
-            if (two) sums[slab + i] = b;
+        if (split == 1) return;
+        cluster_sync();
+        const uint32_t base = smem_u32(sums);
+        for (int i = rank * (32 * kFewWarps) + tid; i < total; i += split * (32 * kFewWarps)) {
+            float a = 0.0f, b = 0.0f;
+            for (int r = 0; r < split; ++r) {
+                a += ld_cluster_f32(mapa_shared(base + 4 * i, r));
+                if (two) b += ld_cluster_f32(mapa_shared(base + 4 * (slab + i), r));
+            }
+            finish(item, i, a, b);
+        }
+        cluster_sync();  // others may still read this block's sums
+    };
+
+    if constexpr (FLAT) {
+        float *own = sums + warp * slab;
+        for (int i = tid & 31; i < slab; i += 32) own[i] = 0.0f;
+        __syncwarp();
+        const int64_t total = static_cast<int64_t>(items) * p.steps;
+        const int part = rank * kFewWarps + warp, parts = split * kFewWarps;
+        const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
+        const K k(p, t, 0, n0);
+        k.walk(acc, own, ring, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
+               static_cast<int>(hi - lo));
+        join(0, p.tokens);
+    } else {
+        const int part = rank * warps + warp % warps, parts = split * warps;
+        const int lo = static_cast<int>(p.steps * part / parts), hi = static_cast<int>(p.steps * (part + 1) / parts);
+        const K k(p, t, warp / warps, n0);
+        float *own = sums + warp * slab;
+        if (!UP && static_cast<int>(blockIdx.y) >= items) pdl_wait();  // nothing to do; every launch waits for the last
+        for (int item = blockIdx.y; item < items; item += gridDim.y) {
+            k.walk(acc, nullptr, ring, item, lo, item + 1, hi - lo);
+            __syncthreads();  // the sums take the rings' place
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float2 *>(own + (8 * m + 2 * k.l4 + i) * kFewCols + k.column(j)) =
+                            make_float2(acc[j][m][i], acc[j][m][2 + i]);
+            join(item, k.rows_of(item));
+            __syncthreads();
         }
     }
-    if (split == 1) return;
-    cluster_sync();
-    const uint32_t base = smem_u32(sums);
-    for (int i = rank * static_cast<int>(blockDim.x) + tid; i < total; i += split * static_cast<int>(blockDim.x)) {
-        float a = 0.0f, b = 0.0f;
-        for (int r = 0; r < split; ++r) {
-            a += ld_cluster_f32(mapa_shared(base + 4 * i, r));
-            if (two) b += ld_cluster_f32(mapa_shared(base + 4 * (slab + i), r));
-        }
-        finish(i, a, b);
-    }
-    cluster_sync();  // others may still read this block's sums
 }
 
 // ------------------------------------------------------------------ launch
 
-template <bool BF16, bool FOUR, bool ANY, int MB, bool DOWN>
+template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream_t s)
 {
+    using K = FewKernel<BF16, FOUR, ANY, MB, MODE>;
     constexpr int kMaxSmem = 227 * 1024;
-    if (l.smem_bytes > kMaxSmem) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaSuccess;
-    if (l.smem_bytes > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(few_kernel<BF16, FOUR, ANY, MB, DOWN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  kMaxSmem)) != cudaSuccess)
-        return e;
+    const int sums = 4 * kFewWarps * kFewCols * (K::FLAT ? p.tokens : K::CHUNK);
+    const int rings = kFewWarps * K::DEPTH * K::Stage::BYTES;
+    const int smem = p.table_bytes + (K::FLAT ? sums + rings : (sums > rings ? sums : rings));
+    if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(few_kernel<BF16, FOUR, ANY, MB, MODE>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(l.grid_x, l.grid_y, 1);
-    cfg.blockDim = dim3(32 * l.warps, 1, 1);
-    cfg.dynamicSmemBytes = l.smem_bytes;
+    cfg.blockDim = dim3(32 * kFewWarps, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -806,28 +871,30 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, few_kernel<BF16, FOUR, ANY, MB, DOWN>, p, l.split);
+    e = cudaLaunchKernelEx(&cfg, few_kernel<BF16, FOUR, ANY, MB, MODE>, p, l.split);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool BF16, bool FOUR, bool ANY, int MB>
-cudaError_t launch_few_rows(const FewLaunch &l, const FewParams &p, cudaStream_t s)
+cudaError_t launch_few_mode(const FewLaunch &l, const FewParams &p, cudaStream_t s)
 {
+    if (l.mode == kFewUp) return launch_few_kernel<BF16, FOUR, ANY, MB, kFewUp>(l, p, s);
     // Hidden rows are always aligned: with weights in 4 bits nothing else can be off.
-    if constexpr (FOUR && ANY)
-        return l.down ? launch_few_kernel<BF16, FOUR, false, MB, true>(l, p, s)
-                      : launch_few_kernel<BF16, FOUR, ANY, MB, false>(l, p, s);
+    constexpr bool any = ANY && !FOUR;
+    if constexpr (MB == 1)
+        return launch_few_kernel<BF16, FOUR, any, 1, kFewFlat>(l, p, s);
     else
-        return l.down ? launch_few_kernel<BF16, FOUR, ANY, MB, true>(l, p, s)
-                      : launch_few_kernel<BF16, FOUR, ANY, MB, false>(l, p, s);
+        return launch_few_kernel<BF16, FOUR, any, MB, kFewParts>(l, p, s);
 }
 
 template <bool BF16, bool FOUR>
 cudaError_t launch_few_type(const FewLaunch &l, const FewParams &p, cudaStream_t s)
 {
-    if (l.row_blocks == 1)
-        return l.any ? launch_few_rows<BF16, FOUR, true, 1>(l, p, s) : launch_few_rows<BF16, FOUR, false, 1>(l, p, s);
-    return l.any ? launch_few_rows<BF16, FOUR, true, 4>(l, p, s) : launch_few_rows<BF16, FOUR, false, 4>(l, p, s);
+    if (l.row_blocks == 1) return l.any ? launch_few_mode<BF16, FOUR, true, 1>(l, p, s) : launch_few_mode<BF16, FOUR, false, 1>(l, p, s);
+    if (l.row_blocks == 2) return l.any ? launch_few_mode<BF16, FOUR, true, 2>(l, p, s) : launch_few_mode<BF16, FOUR, false, 2>(l, p, s);
+    if constexpr (FOUR)
+        if (l.any) return launch_few_mode<BF16, FOUR, true, 4>(l, p, s);
+    return l.any ? cudaErrorInvalidConfiguration : launch_few_mode<BF16, FOUR, false, 4>(l, p, s);
 }
 
 }  // namespace gp
