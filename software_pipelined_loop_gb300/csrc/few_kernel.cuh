@@ -36,37 +36,59 @@ namespace gp {
 
 // ------------------------------------------------------------ small pieces
 
-template <bool BF16>
-__device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1)
+// d (+)= a * b.  FIXED: products stay in the order they are written in, where
+// the compiler's own order would keep too many operands in registers.
+template <bool BF16, bool FIXED>
+__device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1)
 {
-    if constexpr (BF16)
+    if constexpr (BF16 && FIXED)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else if constexpr (FIXED)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The same without an addend.
-template <bool BF16>
+template <bool BF16, bool FIXED>
 __device__ __forceinline__ void few_mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1)
+                                        uint32_t b0, uint32_t b1)
 {
-    if constexpr (BF16)
+    if constexpr (BF16 && FIXED)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%10, %10, %10, %10};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-    else
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else if constexpr (FIXED)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%10, %10, %10, %10};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 template <bool BF16>
@@ -142,6 +164,18 @@ __device__ __forceinline__ uint4 few_first(uint4 v, int count)
         else if (count == 2 * i + 1) w[i] &= 0xffffu;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Loads of a stage, FIXED in their order among the products or not.
+template <class T, bool FIXED = false>
+__device__ __forceinline__ T few_ld_shared(uint32_t addr)
+{
+    if constexpr (FIXED && sizeof(T) == 16)
+        return ld_shared_v4(addr);
+    else if constexpr (FIXED)
+        return ld_shared_v2(addr);
+    else
+        return *static_cast<const T *>(__cvta_shared_to_generic(addr));
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
@@ -307,12 +341,14 @@ struct FewWalk {
     int item, step, blocks;
     const char *w;              // this lane's piece of the step's first row (4 bits: of its word row)
     const uint16_t *s;          // this lane's scales of the group
-    const uint16_t *x[MB];      // this lane's 8 values of each row (a place without a row: of the item's first)
+    const uint16_t *x[MB];      // this lane's 8 values of each row
+    uint32_t x_bytes[MB];       // 16, or 0 for a place without a row
 };
 
 template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 struct FewKernel {
     static constexpr int CHUNK = 8 * MB, DEPTH = few_depth<FOUR, ANY, MB, MODE>();
+    static constexpr bool FIXED = MB > 1;
     static constexpr bool UP = MODE == kFewUp, FLAT = MODE == kFewFlat;
     static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && UP;
     using Stage = FewStage<FOUR, ANY_W, ANY_X, MB>;
@@ -371,6 +407,7 @@ struct FewKernel {
         for (int m = 0; m < MB; ++m) {
             int64_t r = first + (8 * m + g < rows ? 8 * m + g : 0);
             if (p.ids) r = UP ? t.row[r] & 0xffu : t.row[r] >> 8;
+            k.x_bytes[m] = 8 * m + g < rows ? 16u : 0u;
             k.x[m] = p.X + r * p.ldx + Stage::STEP * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
         }
     }
@@ -461,7 +498,7 @@ struct FewKernel {
                 for (int i = 0; i <= HALVES; ++i) {
                     const int piece = 4 * i + l4;
                     if (i < HALVES || l4 == 0)
-                        few_copy16(to + 16 * piece, at - off + 16 * piece, 16 * piece < off + bytes ? 16u : 0u);
+                        few_copy16(to + 16 * piece, at - off + 16 * piece, 16 * piece < off + bytes ? k.x_bytes[m] : 0u);
                 }
             } else {
                 // Aligned rows hold whole pieces (hidden rows end in zeros).
@@ -469,8 +506,7 @@ struct FewKernel {
 #pragma unroll
                 for (int i = 0; i < HALVES; ++i) {
                     const uint32_t half = HALVES > 1 ? 64u * (i ^ (g & 1)) : 0u;
-                    if (k.step < whole) few_copy16(at + half, k.x[m] + 32 * i);
-                    else few_copy16(at + half, k.x[m] + 32 * i, 32 * i + 8 * l4 < left ? 16u : 0u);
+                    few_copy16(at + half, k.x[m] + 32 * i, k.step < whole || 32 * i + 8 * l4 < left ? k.x_bytes[m] : 0u);
                 }
             }
         }
@@ -482,11 +518,11 @@ struct FewKernel {
         const uint32_t at = st + Stage::X + Stage::X_BLOCK * m + Stage::X_PITCH * g + 16 * l4;
         if constexpr (ANY_X) {
             uint32_t o[4];
-            realign16_steps(ld_shared_v4(at + 64 * half), ld_shared_v4(at + 64 * half + 16), off, o);
+            realign16_steps(few_ld_shared<uint4, FIXED>(at + 64 * half), few_ld_shared<uint4, FIXED>(at + 64 * half + 16), off, o);
             const int64_t left = p.K - (Stage::STEP * static_cast<int64_t>(step) + 32 * half + 8 * l4);
             return few_first(make_uint4(o[0], o[1], o[2], o[3]), left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8));
         } else {
-            return ld_shared_v4(at + (Stage::STEP > 32 ? 64u * (half ^ (g & 1)) : 0u));
+            return few_ld_shared<uint4, FIXED>(at + (Stage::STEP > 32 ? 64u * (half ^ (g & 1)) : 0u));
         }
     }
 
@@ -495,65 +531,70 @@ struct FewKernel {
     {
         const uint32_t at = st + Stage::W_GROUP * l4 + Stage::W_PITCH * r + 16 * g;
         uint32_t o[4];
-        realign16_steps(ld_shared_v4(at), ld_shared_v4(at + 16), off, o);
+        realign16_steps(few_ld_shared<uint4, FIXED>(at), few_ld_shared<uint4, FIXED>(at + 16), off, o);
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
 
     // 4 bits: `SAME` halves of 32 products share their scales; their sums are
     // multiplied together.
-    template <int SAME>
-    __device__ __forceinline__ void multiply4(float (&acc)[4][MB][4], uint32_t st, int step, int blocks,
+    template <int SAME, int NB>
+    __device__ __forceinline__ void multiply4(float (&acc)[4][MB][4], uint32_t st, int step,
                                               const int (&x_off)[MB]) const
     {
 #pragma unroll
         for (int q = 0; q < 2; q += SAME) {
-            uint4 x[SAME][MB];
+            uint4 x[SAME][NB];
 #pragma unroll
             for (int i = 0; i < SAME; ++i)
 #pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    if (MB > 1 && m >= blocks) break;
-                    x[i][m] = rows_x(st, m, q + i, x_off[m], step);
-                }
+                for (int m = 0; m < NB; ++m) x[i][m] = rows_x(st, m, q + i, x_off[m], step);
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                const uint2 scales = ld_shared_v2(st + Stage::SCALES + 128 * q + 64 * l + 8 * g);
+                const uint2 scales = few_ld_shared<uint2, FIXED>(st + Stage::SCALES + 128 * q + 64 * l + 8 * g);
                 uint32_t w[SAME][4];
 #pragma unroll
                 for (int i = 0; i < SAME; ++i) {
-                    const uint4 v = ld_shared_v4(st + get + 1024 * (q + i) + 128 * l);
+                    const uint4 v = few_ld_shared<uint4, FIXED>(st + get + 1024 * (q + i) + 128 * l);
                     w[i][0] = v.x;
                     w[i][1] = v.y;
                     w[i][2] = v.z;
                     w[i][3] = v.w;
                 }
+                // The sums of different columns and rows in turn, so that none
+                // waits for its own last product: of both pairs of columns for 8
+                // rows, of one for more (both take more registers than there are).
+                constexpr int PAIRS = MB < 4 && NB == 1 ? 2 : 1;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t u[SAME][2][4];
+                for (int h0 = 0; h0 < 2; h0 += PAIRS) {
+                    float d[PAIRS][NB][4];
 #pragma unroll
                     for (int i = 0; i < SAME; ++i)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            u[i][0][c] = few_pair<BF16>(w[i][2 * h], c);
-                            u[i][1][c] = few_pair<BF16>(w[i][2 * h + 1], c);
-                        }
-                    const uint32_t sc = h ? scales.y : scales.x;
-                    const float s0 = few_float<BF16>(sc & 0xffffu), s1 = few_float<BF16>(sc >> 16);
+                        for (int c = 0; c < 4; c += 2)
 #pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        if (MB > 1 && m >= blocks) break;
-                        float d[4];
-                        few_mma_first<BF16>(d, u[0][0][0], u[0][1][0], u[0][0][1], u[0][1][1], x[0][m].x, x[0][m].y);
-                        few_mma<BF16>(d, u[0][0][2], u[0][1][2], u[0][0][3], u[0][1][3], x[0][m].z, x[0][m].w);
-                        if constexpr (SAME == 2) {
-                            few_mma<BF16>(d, u[1][0][0], u[1][1][0], u[1][0][1], u[1][1][1], x[1][m].x, x[1][m].y);
-                            few_mma<BF16>(d, u[1][0][2], u[1][1][2], u[1][0][3], u[1][1][3], x[1][m].z, x[1][m].w);
+                            for (int h = 0; h < PAIRS; ++h) {
+                                const uint32_t v0 = w[i][2 * (h0 + h)], v1 = w[i][2 * (h0 + h) + 1];
+                                const uint32_t a0 = few_pair<BF16>(v0, c), a1 = few_pair<BF16>(v1, c);
+                                const uint32_t a2 = few_pair<BF16>(v0, c + 1), a3 = few_pair<BF16>(v1, c + 1);
+#pragma unroll
+                                for (int m = 0; m < NB; ++m) {
+                                    const uint32_t b0 = c ? x[i][m].z : x[i][m].x, b1 = c ? x[i][m].w : x[i][m].y;
+                                    if (i == 0 && c == 0) few_mma_first<BF16, FIXED>(d[h][m], a0, a1, a2, a3, b0, b1);
+                                    else few_mma<BF16, FIXED>(d[h][m], a0, a1, a2, a3, b0, b1);
+                                }
+                            }
+#pragma unroll
+                    for (int h = 0; h < PAIRS; ++h) {
+                        const uint32_t sc = h0 + h ? scales.y : scales.x;
+                        const float s0 = few_float<BF16>(sc & 0xffffu), s1 = few_float<BF16>(sc >> 16);
+#pragma unroll
+                        for (int m = 0; m < NB; ++m) {
+                            float(&a)[4] = acc[2 * l + h0 + h][m];
+                            a[0] = fmaf(s0, d[h][m][0], a[0]);
+                            a[1] = fmaf(s0, d[h][m][1], a[1]);
+                            a[2] = fmaf(s1, d[h][m][2], a[2]);
+                            a[3] = fmaf(s1, d[h][m][3], a[3]);
                         }
-                        float(&a)[4] = acc[2 * l + h][m];
-                        a[0] = fmaf(s0, d[0], a[0]);
-                        a[1] = fmaf(s0, d[1], a[1]);
-                        a[2] = fmaf(s1, d[2], a[2]);
-                        a[3] = fmaf(s1, d[3], a[3]);
                     }
                 }
             }
@@ -563,20 +604,18 @@ struct FewKernel {
     // acc[j][m]: columns pair j of this lane, rows 8m + 2 * l4 and the next:
     // (column, row), (column, row + 1), (column + 1, row), (column + 1, row + 1).
     // w_off, x_off: places of the step's operands off 16-byte boundaries.
-    __device__ __forceinline__ void multiply(float (&acc)[4][MB][4], uint32_t st, int step, int blocks, int w_off,
+    template <int NB>
+    __device__ __forceinline__ void multiply(float (&acc)[4][MB][4], uint32_t st, int step, int w_off,
                                              const int (&x_off)[MB]) const
     {
         if constexpr (FOUR) {
             // (32 rows: the registers do not hold both halves' operands)
-            if (MB < 4 && p.group_steps > 1) multiply4<MB < 4 ? 2 : 1>(acc, st, step, blocks, x_off);
-            else multiply4<1>(acc, st, step, blocks, x_off);
+            if (MB < 4 && p.group_steps > 1) multiply4<MB < 4 ? 2 : 1, NB>(acc, st, step, x_off);
+            else multiply4<1, NB>(acc, st, step, x_off);
         } else {
-            uint4 x[MB];
+            uint4 x[NB];
 #pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                if (MB > 1 && m >= blocks) break;
-                x[m] = rows_x(st, m, 0, x_off[m], step);
-            }
+            for (int m = 0; m < NB; ++m) x[m] = rows_x(st, m, 0, x_off[m], step);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t w[4][4];
@@ -586,7 +625,7 @@ struct FewKernel {
                     if constexpr (ANY_W)
                         v = weights_any(st, 4 * h + r, (w_off + 2 * static_cast<int>(p.N & 7) * (4 * h + r)) & 15);
                     else
-                        v = ld_shared_v4(((st + get) ^ (16u * (4 * h + r))) + 128 * (4 * h + r));
+                        v = few_ld_shared<uint4, FIXED>(((st + get) ^ (16u * (4 * h + r))) + 128 * (4 * h + r));
                     w[r][0] = v.x;
                     w[r][1] = v.y;
                     w[r][2] = v.z;
@@ -597,10 +636,8 @@ struct FewKernel {
                     const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
                     const uint32_t a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
 #pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        if (MB > 1 && m >= blocks) break;
-                        few_mma<BF16>(acc[j][m], a0, a1, a2, a3, h ? x[m].z : x[m].x, h ? x[m].w : x[m].y);
-                    }
+                    for (int m = 0; m < NB; ++m)
+                        few_mma<BF16, FIXED>(acc[j][m], a0, a1, a2, a3, h ? x[m].z : x[m].x, h ? x[m].w : x[m].y);
                 }
             }
         }
@@ -692,7 +729,10 @@ struct FewKernel {
         for (int i = 0; i < count; ++i) {
             few_wait<DEPTH - 1>();
             __syncwarp();  // a lane's operands are other lanes' copies
-            multiply(acc, st, step, blocks, w_off, x_off);
+            // (blocks without rows give columns that nobody reads)
+            if (MB > 2 && blocks > 2) multiply<MB>(acc, st, step, w_off, x_off);
+            else if (MB > 1 && blocks > 1) multiply<MB < 2 ? 1 : 2>(acc, st, step, w_off, x_off);
+            else multiply<1>(acc, st, step, w_off, x_off);
             __syncwarp();
             if (i + DEPTH < count) {
                 load_w(st, k);

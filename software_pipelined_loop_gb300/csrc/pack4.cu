@@ -1,26 +1,31 @@
 // pack4.cu -- weights into 4 bits with group scales, and back.
 //
-// A group is `group` rows k of one column.  Its scale is the largest magnitude
-// over 7, rounded to the weights' type; a value is w / scale, rounded to the
-// nearest whole number (ties to even), held between -8 and 7, plus 8.  A
-// thread takes a group of one column, neighbours the next columns.
+// A group is `group` rows k of one column.  Its scale s is the largest
+// magnitude over 7, rounded to the weights' type; a value is w / s, rounded to
+// the nearest whole number (ties to even), held between -8 and 7, plus 8.
+//
+// Both directions are bound by memory: 2 bytes of a weight on one side, half a
+// byte and its share of a scale on the other.  A lane takes 8 neighbouring
+// columns of the 8 rows of a word, 16 bytes of each row, and makes or takes
+// apart its 8 words in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "few.h"
+#include "ptx.cuh"
 
 namespace gp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // four warps: 128 rows of 64 columns (pack)
 
 template <bool BF16>
-__device__ __forceinline__ float to_float(uint16_t v)
+__device__ __forceinline__ float to_float(uint32_t bits)
 {
     if constexpr (BF16)
-        return __uint_as_float(static_cast<uint32_t>(v) << 16);
+        return __uint_as_float(bits << 16);
     else
-        return __half2float(__ushort_as_half(v));
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
 }
 
 template <bool BF16>
@@ -32,90 +37,241 @@ __device__ __forceinline__ uint16_t to_bits(float v)
         return __half_as_ushort(__float2half_rn(v));
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) pack4_kernel(int64_t experts, int64_t K, int64_t N, int group,
-                                                         const uint16_t *W, uint32_t *Q, uint16_t *S)
+// Eight 16-bit elements at p, the first `count` of them (others: whatever is
+// there, or zeros).  Only aligned words that hold one of those are read.
+template <bool ANY>
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int count)
 {
+    if constexpr (!ANY) return ld_global_v4_if(p, count > 0);
+    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const char *a = reinterpret_cast<const char *>(p) - s;
+    const uint4 lo = ld_global_v4_if(a, count > 0);
+    const uint4 hi = ld_global_v4_if(a + 16, count > 0 && static_cast<int>(s) + 2 * count > 16);
+    uint32_t o[4];
+    realign16_steps(lo, hi, s, o);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i)
+{
+    return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+}
+
+// The nearest whole number to v / s, ties to even, as a float: the quotient is
+// v * inv corrected by its exact remainder.  Quotients of two 16-bit values are
+// either exactly between two whole numbers, which the correction restores, or
+// further from there than any error here.
+__device__ __forceinline__ float whole(float v, float s, float inv)
+{
+    const float t = v * inv;
+    const float q = fmaf(fmaf(-t, s, v), inv, t);
+    return fminf(fmaxf(rintf(q), -8.0f), 7.0f);
+}
+
+// grid: x = 64 columns, y and z = 128 rows of an expert.
+template <bool BF16, bool ANY>
+__global__ void __launch_bounds__(kThreads) pack4_kernel(int64_t K, int64_t N, int group, int64_t row_tiles,
+                                                         int64_t tiles, const uint16_t *W, uint32_t *Q, uint16_t *S)
+{
+    __shared__ float tops[4][64];
     const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group, words = (K + 7) / 8;
-    const int64_t total = experts * groups * n4;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t n = i % n4, eg = i / n4, gr = eg % groups, e = eg / groups;
-        const int64_t k0 = gr * group;
-        const int rows = static_cast<int>(K - k0 < group ? K - k0 : group);
-        const uint16_t *w = W + (e * K + k0) * N + n;
-        float top = 0.0f;
-        bool finite = true;
-        if (n < N)
-            for (int r = 0; r < rows; ++r) {
-                const float v = fabsf(to_float<BF16>(w[r * N]));
-                finite &= v <= 3.402823466e38f;
-                top = fmaxf(top, v);
-            }
-        // (Past the last column: scale 0, values 0.)
-        const uint16_t bits = finite ? to_bits<BF16>(__fdiv_rn(top, 7.0f)) : to_bits<BF16>(__int_as_float(0x7fffffff));
-        const float scale = to_float<BF16>(bits);
-        S[eg * n4 + n] = bits;
-        for (int b = 0; b < rows; b += 8) {
-            uint32_t word = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = lane >> 3;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + 8 * (lane & 7);
+    const int cols = n >= N ? 0 : (N - n < 8 ? static_cast<int>(N - n) : 8);
+    const int together = group / 32;  // warps that share a group
+    for (int64_t tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+        const int64_t e = tile / row_tiles, k0 = (tile % row_tiles) * 128 + 32 * warp + 8 * block;
+        const int rows = k0 >= K ? 0 : (K - k0 < 8 ? static_cast<int>(K - k0) : 8);
+        uint4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = load8<ANY>(W + (e * K + k0 + r) * N + n, r < rows ? cols : 0);
+        // Largest magnitude of each column; an infinity or NaN makes it infinite.
+        float top[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            // Bits of a magnitude are in the order of its value, those that are not finite above all others.
+            uint32_t most = 0;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                float q = 0.0f;
-                if (b + r < rows && scale > 0.0f)
-                    q = fminf(fmaxf(rintf(__fdiv_rn(to_float<BF16>(w[(b + r) * N]), scale)), -8.0f), 7.0f);
-                word |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * ((r >> 1) + 4 * (r & 1)));
+                const uint32_t b = (word_of(v[r], c >> 1) >> (16 * (c & 1))) & 0x7fffu;
+                most = b > most ? b : most;
             }
-            Q[(e * words + (k0 + b) / 8) * n4 + n] = word;
-        }
-    }
-}
-
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t experts, int64_t K, int64_t N, int group,
-                                                           const uint32_t *Q, const uint16_t *S, uint16_t *W)
-{
-    const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group, words = (K + 7) / 8;
-    const int64_t total = experts * words * N;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t n = i % N, ew = i / N, b = ew % words, e = ew / words;
-        const uint32_t word = Q[ew * n4 + n];
-        const float scale = to_float<BF16>(S[(e * groups + 8 * b / group) * n4 + n]);
+            const uint32_t infinite = BF16 ? 0x7f80u : 0x7c00u;
+            top[c] = most >= infinite ? __int_as_float(0x7f800000) : to_float<BF16>(most);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int q = static_cast<int>(word >> (4 * ((r >> 1) + 4 * (r & 1))) & 15u) - 8;
-            if (8 * b + r < K) W[(e * K + 8 * b + r) * N + n] = to_bits<BF16>(static_cast<float>(q) * scale);
+            for (int d = 8; d < 32; d *= 2) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], d));
+        }
+        if (together > 1) {
+            if (block == 0)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) tops[warp][8 * (lane & 7) + c] = top[c];
+            __syncthreads();
+            const int first = warp / together * together;
+            for (int w = first; w < first + together; ++w)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) top[c] = fmaxf(top[c], tops[w][8 * (lane & 7) + c]);
+            __syncthreads();
+        }
+        uint32_t bits[8], word[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            // (Past the last column: scale 0, values 0.)
+            const bool finite = top[c] <= 3.402823466e38f;
+            if (c >= cols) top[c] = 0.0f;
+            bits[c] = finite || c >= cols ? to_bits<BF16>(__fdiv_rn(top[c], 7.0f)) : (BF16 ? 0x7fffu : 0x7fffu);
+            const float s = to_float<BF16>(bits[c]);
+            word[c] = 0x88888888u;
+            if (!finite || !(s > 0.0f)) continue;
+            // (the reciprocal of a scale below 2^-126 has no fp32 value)
+            const float lift = BF16 && s < 1e-30f ? 0x1p100f : 1.0f, sl = s * lift, inv = __frcp_rn(sl);
+            word[c] = 0;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float x = to_float<BF16>((word_of(v[r], c >> 1) >> (16 * (c & 1))) & 0xffffu);
+                if constexpr (BF16) x *= lift;
+                const int q = static_cast<int>(whole(r < rows ? x : 0.0f, sl, inv)) + 8;
+                word[c] |= static_cast<uint32_t>(q) << (4 * ((r >> 1) + 4 * (r & 1)));
+            }
+        }
+        if (rows > 0) {
+            uint32_t *q = Q + (e * words + k0 / 8) * n4 + n;
+            if (n < n4) *reinterpret_cast<uint4 *>(q) = make_uint4(word[0], word[1], word[2], word[3]);
+            if (n + 4 < n4) *reinterpret_cast<uint4 *>(q + 4) = make_uint4(word[4], word[5], word[6], word[7]);
+            if (k0 % group == 0) {
+                uint16_t *s = S + (e * groups + k0 / group) * n4 + n;
+                if (n < n4) *reinterpret_cast<uint2 *>(s) = make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
+                if (n + 4 < n4) *reinterpret_cast<uint2 *>(s + 4) = make_uint2(bits[4] | bits[5] << 16, bits[6] | bits[7] << 16);
+            }
         }
     }
 }
 
-unsigned blocks_of(int64_t total)
+// The pair of rows 2i, 2i + 1 of a word, as values q - 8, exact (as in few_kernel.cuh).
+template <bool BF16>
+__device__ __forceinline__ uint32_t pair_of(uint32_t word, int i)
 {
-    const int64_t n = (total + kThreads - 1) / kThreads;
-    return static_cast<unsigned>(n < (1 << 20) ? n : (1 << 20));
+    uint32_t m;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(BF16 ? 0x43004300u : 0x64006400u));
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), __float2bfloat162_rn(136.0f));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1032.0f));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 }
+
+// The product of 4 bits and a 16-bit scale, rounded once.
+template <bool BF16>
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// A row of the warp's 256 columns off 16-byte boundaries: lane's 8 elements o,
+// `left` of the row's columns from its first lane's on.  Each lane stores the
+// whole piece that begins among its elements (the next lane has the rest), and
+// single elements what lies before the first piece and after the last.
+__device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4], int lane, int64_t left)
+{
+    const int total = left < 256 ? static_cast<int>(left) : 256;
+    const int skip = static_cast<int>(((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) / 2);  // 0 .. 7
+    uint4 hi;
+    hi.x = __shfl_down_sync(0xffffffffu, o[0], 1);
+    hi.y = __shfl_down_sync(0xffffffffu, o[1], 1);
+    hi.z = __shfl_down_sync(0xffffffffu, o[2], 1);
+    hi.w = __shfl_down_sync(0xffffffffu, o[3], 1);
+    uint32_t v[4];
+    realign16_steps(make_uint4(o[0], o[1], o[2], o[3]), hi, 2 * skip, v);
+    const int at = 8 * lane + skip;
+    if (at + 8 <= total) *reinterpret_cast<uint4 *>(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    // Elements before the first piece, of lane 0, by lanes 0 .. 6; those behind
+    // the last piece, of the last lanes with any, by lanes 8 .. 15.
+    const int end = total < skip ? total : skip + (total - skip) / 8 * 8;  // where the pieces end
+    const int i = lane < 8 ? lane : end + lane - 8;
+    const bool on = lane < 8 ? lane < skip && lane < total : lane < 16 && end >= skip && i < total;
+    const int from = on ? i / 8 : 0;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __shfl_sync(0xffffffffu, o[j], from);
+    const uint32_t x = word_of(make_uint4(w[0], w[1], w[2], w[3]), (i & 7) >> 1);
+    if (on) row[i] = static_cast<uint16_t>(x >> (16 * (i & 1)));
+}
+
+// grid: x = 256 columns; y = rows of words.  A warp takes a row of words.
+template <bool BF16, bool ANY>
+__global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N, int group, int64_t words,
+                                                           int64_t all_words, const uint32_t *Q, const uint16_t *S,
+                                                           uint16_t *W)
+{
+    const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 256, n = first + 8 * lane;
+    for (int64_t ew = blockIdx.y * static_cast<int64_t>(kThreads / 32) + warp; ew < all_words;
+         ew += static_cast<int64_t>(gridDim.y) * (kThreads / 32)) {
+        const int64_t e = ew / words, b = ew % words;
+        const uint32_t *q = Q + ew * n4 + n;
+        const uint16_t *s = S + (e * groups + 8 * b / group) * n4 + n;
+        const uint4 qa = ld_global_v4_if(q, n < n4), qb = ld_global_v4_if(q + 4, n + 4 < n4);
+        uint2 sa = make_uint2(0, 0), sb = sa;
+        if (n < n4) sa = *reinterpret_cast<const uint2 *>(s);
+        if (n + 4 < n4) sb = *reinterpret_cast<const uint2 *>(s + 4);
+        const uint32_t word[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+        const uint32_t scale[4] = {sa.x, sa.y, sb.x, sb.y};
+        const int rows = K - 8 * b < 8 ? static_cast<int>(K - 8 * b) : 8;
+        uint16_t *w = W + (e * K + 8 * b) * N + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t even[4], odd[4];  // rows 2i and 2i + 1, two columns a word
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t a = pair_of<BF16>(word[2 * c], i), b2 = pair_of<BF16>(word[2 * c + 1], i);
+                even[c] = times<BF16>(__byte_perm(a, b2, 0x5410), scale[c]);
+                odd[c] = times<BF16>(__byte_perm(a, b2, 0x7632), scale[c]);
+            }
+            if constexpr (ANY) {
+                uint16_t *row = W + (e * K + 8 * b + 2 * i) * N + first;
+                if (2 * i < rows) store_any(row, even, lane, N - first);
+                if (2 * i + 1 < rows) store_any(row + N, odd, lane, N - first);
+            } else if (n < N) {
+                if (2 * i < rows) *reinterpret_cast<uint4 *>(w + 2 * i * N) = make_uint4(even[0], even[1], even[2], even[3]);
+                if (2 * i + 1 < rows) *reinterpret_cast<uint4 *>(w + (2 * i + 1) * N) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
+            }
+        }
+    }
+}
+
+bool off16(const void *p, int64_t N) { return reinterpret_cast<uintptr_t>(p) % 16 != 0 || N % 8 != 0; }
+
+constexpr int64_t kMaxY = 65535;
 
 }  // namespace
 
 cudaError_t launch_pack4(bool bf16, int64_t experts, int64_t K, int64_t N, int group, const uint16_t *W, uint32_t *Q,
                          uint16_t *S, cudaStream_t s)
 {
-    const unsigned grid = blocks_of(experts * ((K + group - 1) / group) * ((N + 3) / 4 * 4));
-    if (bf16)
-        pack4_kernel<true><<<grid, kThreads, 0, s>>>(experts, K, N, group, W, Q, S);
-    else
-        pack4_kernel<false><<<grid, kThreads, 0, s>>>(experts, K, N, group, W, Q, S);
+    const int64_t row_tiles = (K + 127) / 128, tiles = experts * row_tiles;
+    const dim3 grid(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>(tiles < kMaxY ? tiles : kMaxY));
+    const auto kernel = off16(W, N) ? (bf16 ? pack4_kernel<true, true> : pack4_kernel<false, true>)
+                                    : (bf16 ? pack4_kernel<true, false> : pack4_kernel<false, false>);
+    kernel<<<grid, kThreads, 0, s>>>(K, N, group, row_tiles, tiles, W, Q, S);
     return cudaGetLastError();
 }
 
 cudaError_t launch_unpack4(bool bf16, int64_t experts, int64_t K, int64_t N, int group, const uint32_t *Q,
                            const uint16_t *S, uint16_t *W, cudaStream_t s)
 {
-    const unsigned grid = blocks_of(experts * ((K + 7) / 8) * N);
-    if (bf16)
-        unpack4_kernel<true><<<grid, kThreads, 0, s>>>(experts, K, N, group, Q, S, W);
-    else
-        unpack4_kernel<false><<<grid, kThreads, 0, s>>>(experts, K, N, group, Q, S, W);
+    const int64_t words = (K + 7) / 8, all = experts * words, rows = (all + kThreads / 32 - 1) / (kThreads / 32);
+    const dim3 grid(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(rows < kMaxY ? rows : kMaxY));
+    const auto kernel = off16(W, N) ? (bf16 ? unpack4_kernel<true, true> : unpack4_kernel<false, true>)
+                                    : (bf16 ? unpack4_kernel<true, false> : unpack4_kernel<false, false>);
+    kernel<<<grid, kThreads, 0, s>>>(K, N, group, words, all, Q, S, W);
     return cudaGetLastError();
 }
 
