@@ -57,21 +57,30 @@ struct FewStage {
     static constexpr int BYTES = X + MB * X_BLOCK;
 };
 
+// Blocks of an SM: two, but one where an item's sums take half of the registers
+// of two.
+template <int MB>
+constexpr int few_blocks()
+{
+    return MB < 4 ? 2 : 1;
+}
+
 // Stages of a warp's ring: as many as let two blocks run on an SM, with the
 // sums of 8 tokens (kFewFlat) or tables of some 500 choices beside them.
 template <bool FOUR, bool ANY, int MB, int MODE>
 constexpr int few_depth()
 {
     if (MODE == kFewFlat) return FOUR ? 3 : 2;
-    if (FOUR) return MB == 1 ? 4 : (MB == 2 ? 3 : 2);
-    return MB == 1 && !ANY ? 3 : 2;
+    if (FOUR) return MB == 1 ? 4 : 3;
+    return MB != 2 && !ANY ? 3 : 2;
 }
 
 struct FewLaunch {
     bool bf16, four, any;
     int mode;
     int row_blocks;         // 8-row blocks of an item: 1, 2 or 4
-    int split;              // blocks of a cluster, sharing the products
+    int split;              // blocks of a cluster, sharing the products of 64 columns
+    int wide;               // 64s of columns of a block: 1, 2 or 4 (with split 1)
     int grid_x, grid_y;
 };
 

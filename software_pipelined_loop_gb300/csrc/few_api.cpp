@@ -100,8 +100,14 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode, int
     const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols, blocks = columns * l.grid_y;
     const int64_t steps = p->steps * (mode == gp::kFewFlat ? items : p->matrices);
     l.split = 1;
-    while (l.split < 8 && blocks * 2 * l.split <= 2 * sms && steps >= gp::kFewWarps * 2 * l.split) l.split *= 2;
-    l.grid_x = static_cast<int>(columns * l.split);
+    while (l.split < 8 && blocks * 2 * l.split <= (l.row_blocks < 4 ? 2 : 1) * sms && steps >= gp::kFewWarps * 2 * l.split) l.split *= 2;
+    // Short sums: a warp takes four steps at least where there are blocks
+    // enough, by sharing its columns with fewer others.
+    l.wide = 1;
+    while (mode != gp::kFewFlat && l.split == 1 && l.wide < 4 && blocks >= 2 * 2 * sms * l.wide &&
+           4 * gp::kFewWarps > p->steps * p->matrices * l.wide)
+        l.wide *= 2;
+    l.grid_x = static_cast<int>((columns + l.wide - 1) / l.wide * l.split);
     return l;
 }
 

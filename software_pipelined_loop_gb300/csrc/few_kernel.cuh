@@ -178,11 +178,21 @@ __device__ __forceinline__ T few_ld_shared(uint32_t addr)
         return *static_cast<const T *>(__cvta_shared_to_generic(addr));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+__device__ __forceinline__ void few_st_cluster(uint32_t addr, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// The two halves of a cluster barrier without ordering of memory: nothing but
+// that every block has come so far.
+__device__ __forceinline__ void few_cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void few_cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------- table of items
@@ -761,9 +771,11 @@ struct FewKernel {
     }
 };
 
-// grid: x = column blocks x cluster blocks, y = items (kFewFlat: 1).
+// grid: x = `wide` times 64 columns x blocks of a cluster, y = items (kFewFlat:
+// 1).  The warps of a block share the products of 64 columns, or (wide > 1) so
+// many each of several 64s; `split` blocks share those of the same columns.
 template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
-__global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_constant__ FewParams p, int split)
+__global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(const __grid_constant__ FewParams p, int split, int wide)
 {
     using K = FewKernel<BF16, FOUR, ANY, MB, MODE>;
     constexpr bool UP = K::UP, FLAT = K::FLAT;
@@ -775,11 +787,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_con
     if constexpr (UP) pdl_wait();
     pdl_launch_dependents();
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * kFewCols;
+    const int matrices = UP ? p.matrices : 1;
+    const int warps = kFewWarps / wide, each = warps / matrices;  // of 64 columns, of a matrix of theirs
+    const int64_t n_block = static_cast<int64_t>(blockIdx.x / split) * (wide * kFewCols);
     // Sums of tokens stand beside the rings, those of an item take their place.
-    float *sums = reinterpret_cast<float *>(few_smem + p.table_bytes);
-    const uint32_t ring = smem_u32(sums) + (FLAT ? kFewWarps * p.tokens * kFewCols * 4 : 0) +
-                          warp * (K::DEPTH * K::Stage::BYTES);
+    const int slab = (FLAT ? p.tokens : K::CHUNK) * kFewCols;  // a warp's sums
+    float *from_cluster = reinterpret_cast<float *>(few_smem + p.table_bytes);  // sums of other blocks
+    const int sent = min(p.tokens, FLAT ? p.tokens : K::CHUNK) * kFewCols;      // those of a matrix, at most
+    float *sums = from_cluster + (split > 1 ? matrices * sent : 0);
+    const uint32_t ring = smem_u32(sums) + (FLAT ? kFewWarps * slab * 4 : 0) + warp * (K::DEPTH * K::Stage::BYTES);
     FewTables t{};
     int items = static_cast<int>(gridDim.y);
     if (p.ids) {
@@ -787,17 +803,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_con
         items = p.tokens * p.top_k <= 32 ? few_build_warp<K::CHUNK>(p, t, tables) : few_build_block<K::CHUNK>(p, t, tables);
     }
     float acc[4][MB][4];
-    const int matrices = UP ? p.matrices : 1, warps = kFewWarps / matrices;
-    const int slab = (FLAT ? p.tokens : K::CHUNK) * kFewCols;  // a warp's sums
-    const bool two = matrices == 2;
 
-    // Where sum i of an item is stored, and how.
-    const auto finish = [&](int item, int i, float a, float b) {
+    // Where sum i of 64 columns of an item is stored, and how.
+    const auto finish = [&](int item, int64_t n0, int i, float a, float b) {
         const int r = i / kFewCols;
         const int64_t n = n0 + i % kFewCols;
         if (n >= p.out_cols) return;
         if (UP && p.silu) a = a / (1.0f + expf(-a));
-        if (two) a *= b;
+        if (matrices == 2) a *= b;
         int64_t to = r;
         if constexpr (!FLAT) {
             if (p.ids) {
@@ -813,57 +826,61 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_con
         else
             static_cast<uint16_t *>(p.out)[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
     };
-    // Adds the warps' `count` rows of sums, then the cluster's, in order.
+    // Adds the warps' `count` rows of sums, then the cluster's, in order: every
+    // block sends its sums to the block that will store them.
     const auto join = [&](int item, int count) {
-        const int total = count * kFewCols;
+        const int total = count * kFewCols, share = (total + split - 1) / split;
         __syncthreads();
-        for (int i = tid; i < total; i += 32 * kFewWarps) {
-            float a = 0.0f, b = 0.0f;
+        if (split > 1) few_cluster_wait();  // the others have read what they had here before
+        for (int c = 0; c < wide; ++c)
+            for (int i = tid; i < total; i += 32 * kFewWarps) {
+                float a = 0.0f, b = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) {
-                const float v = sums[w * slab + i];
-                if (w < warps) a += v;
-                else b += v;
+                for (int w = 0; w < kFewWarps; ++w) {
+                    const float v = w < warps ? sums[(c * warps + w) * slab + i] : 0.0f;
+                    if (w < each) a += v;
+                    else b += v;
+                }
+                if (split == 1) {
+                    finish(item, n_block + c * kFewCols, i, a, b);
+                } else {
+                    const uint32_t to = mapa_shared(smem_u32(from_cluster) + 4 * (rank * share + i % share), i / share);
+                    few_st_cluster(to, a);
+                    if (matrices == 2) few_st_cluster(to + 4 * sent, b);
+                }
             }
-            if (split == 1) {
-                finish(item, i, a, b);
-            } else {
-                sums[i] = a;
-                if (two) sums[slab + i] = b;
-            }
-        }
         if (split == 1) return;
         cluster_sync();
-        const uint32_t base = smem_u32(sums);
-        for (int i = rank * (32 * kFewWarps) + tid; i < total; i += split * (32 * kFewWarps)) {
+        for (int i = tid; i < share && rank * share + i < total; i += 32 * kFewWarps) {
             float a = 0.0f, b = 0.0f;
             for (int r = 0; r < split; ++r) {
-                a += ld_cluster_f32(mapa_shared(base + 4 * i, r));
-                if (two) b += ld_cluster_f32(mapa_shared(base + 4 * (slab + i), r));
+                a += from_cluster[r * share + i];
+                if (matrices == 2) b += from_cluster[sent + r * share + i];
             }
-            finish(item, i, a, b);
+            finish(item, n_block, rank * share + i, a, b);
         }
-        cluster_sync();  // others may still read this block's sums
     };
 
     if constexpr (FLAT) {
+        if (split > 1) few_cluster_arrive();
         float *own = sums + warp * slab;
         for (int i = tid & 31; i < slab; i += 32) own[i] = 0.0f;
         __syncwarp();
         const int64_t total = static_cast<int64_t>(items) * p.steps;
         const int part = rank * kFewWarps + warp, parts = split * kFewWarps;
         const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
-        const K k(p, t, 0, n0);
+        const K k(p, t, 0, n_block);
         k.walk(acc, own, ring, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
                static_cast<int>(hi - lo));
         join(0, p.tokens);
     } else {
-        const int part = rank * warps + warp % warps, parts = split * warps;
+        const int part = rank * each + warp % each, parts = split * each;
         const int lo = static_cast<int>(p.steps * part / parts), hi = static_cast<int>(p.steps * (part + 1) / parts);
-        const K k(p, t, warp / warps, n0);
+        const K k(p, t, warp % warps / each, n_block + warp / warps * kFewCols);
         float *own = sums + warp * slab;
         if (!UP && static_cast<int>(blockIdx.y) >= items) pdl_wait();  // nothing to do; every launch waits for the last
         for (int item = blockIdx.y; item < items; item += gridDim.y) {
+            if (split > 1) few_cluster_arrive();
             k.walk(acc, nullptr, ring, item, lo, item + 1, hi - lo);
             __syncthreads();  // the sums take the rings' place
 #pragma unroll
@@ -887,9 +904,10 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
 {
     using K = FewKernel<BF16, FOUR, ANY, MB, MODE>;
     constexpr int kMaxSmem = 227 * 1024;
-    const int sums = 4 * kFewWarps * kFewCols * (K::FLAT ? p.tokens : K::CHUNK);
+    const int slab = 4 * kFewCols * (K::FLAT ? p.tokens : K::CHUNK), sums = kFewWarps * slab;
     const int rings = kFewWarps * K::DEPTH * K::Stage::BYTES;
-    const int smem = p.table_bytes + (K::FLAT ? sums + rings : (sums > rings ? sums : rings));
+    const int smem = p.table_bytes + (l.split > 1 ? p.matrices * 4 * kFewCols * (p.tokens < K::CHUNK ? p.tokens : K::CHUNK) : 0) +
+                     (K::FLAT ? sums + rings : (sums > rings ? sums : rings));
     if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(few_kernel<BF16, FOUR, ANY, MB, MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -911,7 +929,7 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, few_kernel<BF16, FOUR, ANY, MB, MODE>, p, l.split);
+    e = cudaLaunchKernelEx(&cfg, few_kernel<BF16, FOUR, ANY, MB, MODE>, p, l.split, l.wide);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
