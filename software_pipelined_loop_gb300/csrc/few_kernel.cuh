@@ -536,6 +536,41 @@ struct FewKernel {
         }
     }
 
+    // The loads of a step that is whole, and on to the next one of the item.
+    __device__ __forceinline__ void load_whole(uint32_t st, FewWalk<MB> &k, int64_t row) const
+    {
+        const uint32_t to = st + put;
+        if constexpr (FOUR) {
+            const char *w = k.w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i, w += row) few_copy16((to ^ (64u * (i & 1))) + 512 * i, w);
+            k.w = w;
+            few_copy8(st + Stage::SCALES + 8 * lane, k.s, 8);
+            ++k.step;
+            if (p.group_steps == 1) k.s += 2 * n4;
+            else if (p.group_steps == 2 || (k.step & 1) == 0) k.s += n4;
+        } else {
+            const char *w = k.w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i, w += row) few_copy16((to ^ (64u * (i & 1)) ^ (32u * (i >> 1))) + 512 * i, w);
+            k.w = w;
+            ++k.step;
+        }
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            if (m < k.blocks) {
+                const uint32_t at = st + Stage::X + Stage::X_BLOCK * m + Stage::X_PITCH * g + 16 * l4;
+                if constexpr (FOUR) {
+                    few_copy16(at ^ (64u * (g & 1)), k.x[m], k.x_bytes[m]);
+                    few_copy16(at ^ (64u * (g & 1) ^ 64u), k.x[m] + 32, k.x_bytes[m]);
+                } else {
+                    few_copy16(at, k.x[m], k.x_bytes[m]);
+                }
+            }
+            k.x[m] += Stage::STEP;
+        }
+    }
+
     // The eight weights of this lane's row r, whose row begins `off` bytes into its pieces.
     __device__ __forceinline__ uint4 weights_any(uint32_t st, int r, int off) const
     {
@@ -653,6 +688,15 @@ struct FewKernel {
         }
     }
 
+    // (blocks without rows give columns that nobody reads)
+    __device__ __forceinline__ void multiply_rows(float (&acc)[4][MB][4], uint32_t st, int step, int blocks, int w_off,
+                                                  const int (&x_off)[MB]) const
+    {
+        if (MB > 2 && blocks > 2) multiply<MB>(acc, st, step, w_off, x_off);
+        else if (MB > 1 && blocks > 1) multiply<MB < 2 ? 1 : 2>(acc, st, step, w_off, x_off);
+        else multiply<1>(acc, st, step, w_off, x_off);
+    }
+
     // First column of pair j of this lane, from n0.
     __device__ __forceinline__ int column(int j) const
     {
@@ -736,13 +780,25 @@ struct FewKernel {
             few_commit();
         }
         uint32_t st = ring;
-        for (int i = 0; i < count; ++i) {
+        int i = 0;
+        if constexpr (!FLAT && !ANY) {
+            // Whole steps follow one another: nothing to look at in between.
+            const int64_t row = FOUR ? 8 * n4 : 8 * p.N;  // bytes from a lane's piece to its next one
+            for (const int fast = min(count - DEPTH, whole - step - DEPTH); i < fast; ++i) {
+                few_wait<DEPTH - 1>();
+                __syncwarp();
+                multiply_rows(acc, st, step, blocks, w_off, x_off);
+                __syncwarp();
+                load_whole(st, k, row);
+                few_commit();
+                st = st == ring + (DEPTH - 1) * Stage::BYTES ? ring : st + Stage::BYTES;
+            }
+            step += i;
+        }
+        for (; i < count; ++i) {
             few_wait<DEPTH - 1>();
             __syncwarp();  // a lane's operands are other lanes' copies
-            // (blocks without rows give columns that nobody reads)
-            if (MB > 2 && blocks > 2) multiply<MB>(acc, st, step, w_off, x_off);
-            else if (MB > 1 && blocks > 1) multiply<MB < 2 ? 1 : 2>(acc, st, step, w_off, x_off);
-            else multiply<1>(acc, st, step, w_off, x_off);
+            multiply_rows(acc, st, step, blocks, w_off, x_off);
             __syncwarp();
             if (i + DEPTH < count) {
                 load_w(st, k);
