@@ -38,6 +38,9 @@ struct FewParams {
     int matrices;           // 2: silu(first product) * second product
     int silu;               // 1: silu of the (first) product
     int max_items;
+    int columns;            // blocks of columns: ceil(out_cols / (64 * wide))
+    int split;              // blocks of a cluster (1 to 8), sharing the products of 64 columns
+    int wide;               // 64s of columns of a block: 1, 2 or 4 (with split 1)
     int table_bytes;        // shared memory of the table of items
 };
 
@@ -65,28 +68,34 @@ constexpr int few_blocks()
     return MB < 4 ? 2 : 1;
 }
 
-// Stages of a warp's ring: as many as let two blocks run on an SM, with the
-// sums of 8 tokens (kFewFlat) or tables of some 500 choices beside them.
-template <bool FOUR, bool ANY, int MB, int MODE>
+// Stages of a warp's ring: what lets two blocks run on an SM beside their sums
+// and tables.  (A stage more made short calls slower by up to 5%: the first
+// products wait for more copies of others.)
+template <bool FOUR, int MB>
 constexpr int few_depth()
 {
-    if (MODE == kFewFlat) return FOUR ? 3 : 2;
-    if (FOUR) return MB == 1 ? 4 : 3;
-    return MB != 2 && !ANY ? 3 : 2;
+    return (FOUR && MB == 1) || MB == 4 ? 3 : 2;
 }
+
+// Floats of a block's room for the cluster's sums of `rows` rows of a matrix (a
+// multiple of 128 bytes: the rings follow).
+__host__ __device__ constexpr int few_sent(int rows) { return rows * kFewCols + 32; }
 
 struct FewLaunch {
     bool bf16, four, any;
     int mode;
     int row_blocks;         // 8-row blocks of an item: 1, 2 or 4
-    int split;              // blocks of a cluster, sharing the products of 64 columns
-    int wide;               // 64s of columns of a block: 1, 2 or 4 (with split 1)
-    int grid_x, grid_y;
+    int grid;               // blocks
+    bool ok;                // sizes that the kernel can count
 };
 
 // four: weights in 4 bits; any: operands off 16-byte boundaries.
 cudaError_t launch_few_f16(const FewLaunch &l, const FewParams &p, cudaStream_t s);
 cudaError_t launch_few_bf16(const FewLaunch &l, const FewParams &p, cudaStream_t s);
+
+// Clusters of `split` (1 to 8) blocks that run at once on the current device:
+// [0] of kernels with two blocks an SM, [1] with one.  0 on an error.
+int few_room(int one, int split);
 
 // Y[t] = sum of the rows of `parts` (tokens x top_k rows of `width`) that stand
 // for a choice: one inside [0, experts), the token's first of that expert.

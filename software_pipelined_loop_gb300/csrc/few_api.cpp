@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 #include <utility>
@@ -71,7 +72,7 @@ int64_t align128(int64_t x) { return (x + 127) / 128 * 128; }
 
 // The launch for `p` (sizes, matrices and ids set).  Items hold 8 rows of up to
 // 8 tokens; above, 16 rows, or 32 where the experts have more on average.
-FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode, int sms)
+FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
 {
     FewLaunch l{};
     l.bf16 = bf16;
@@ -84,7 +85,7 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode, int
     const int64_t chunk = 8 * l.row_blocks;
     p->steps = (p->K + (four ? 63 : 31)) / (four ? 64 : 32);
     int64_t items = (p->tokens + chunk - 1) / chunk;
-    p->max_items = 0;
+    p->max_items = static_cast<int>(items);
     p->table_bytes = 0;
     if (p->ids) {
         // An item for each expert with rows, and one more for each further chunk
@@ -94,20 +95,49 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode, int
         const int64_t words = 2 * static_cast<int64_t>(p->max_items) + 2 * slots + 3 * static_cast<int64_t>(p->experts) + 1;
         p->table_bytes = static_cast<int>(slots <= 32 ? 4 * gp::kFewWarps * 128 : align128(4 * words));
     }
-    l.grid_y = mode == gp::kFewFlat ? 1 : static_cast<int>(items);
-    // Blocks of a cluster share the products of 64 columns: as many as still
-    // run all at once, each with a step a warp at least.
-    const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols, blocks = columns * l.grid_y;
-    const int64_t steps = p->steps * (mode == gp::kFewFlat ? items : p->matrices);
-    l.split = 1;
-    while (l.split < 8 && blocks * 2 * l.split <= (l.row_blocks < 4 ? 2 : 1) * sms && steps >= gp::kFewWarps * 2 * l.split) l.split *= 2;
-    // Short sums: a warp takes four steps at least where there are blocks
+    // Units of work: 64 columns of an item each (kFewFlat: of all items).  The
+    // experts that have rows are not known here: as many as tokens that choose
+    // any of them alike would reach.
+    const bool all = mode == gp::kFewFlat;
+    const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols;
+    double reached = static_cast<double>(items);
+    if (p->ids && p->top_k < p->experts)
+        reached = p->experts * (1.0 - std::pow(1.0 - static_cast<double>(p->top_k) / p->experts, p->tokens));
+    const double units = static_cast<double>(columns) * (all ? 1.0 : reached);
+    const double steps = static_cast<double>(p->steps) * (all ? reached : p->matrices);
+    // Blocks of a cluster share a unit's products.  Time in us: rounds of units
+    // over the clusters that run at once, each the steps of a warp (measured
+    // with all warps of an SM at work) and the end of a unit.
+    const int one = l.row_blocks == 4;
+    const double step_us = four ? 1.0 : 1.45;
+    double best = 0.0;
+    int64_t room = 0;
+    p->split = 0;
+    for (int split = 1; split <= 8; ++split) {
+        const int64_t at_once = gp::few_room(one, split);
+        if (at_once < 1 || (split > 1 && units > at_once)) continue;
+        const double warp_steps = std::ceil(steps / (gp::kFewWarps * split));
+        const double us = std::ceil(units / at_once) * (warp_steps * step_us + (split == 1 ? 1.0 : 1.7));
+        if (p->split == 0 || us < best) {
+            best = us;
+            p->split = split;
+            room = at_once;
+        }
+    }
+    if (p->split == 0) {
+        l.ok = false;
+        return l;
+    }
+    // Short sums: a warp takes four steps at least where there are units
     // enough, by sharing its columns with fewer others.
-    l.wide = 1;
-    while (mode != gp::kFewFlat && l.split == 1 && l.wide < 4 && blocks >= 2 * 2 * sms * l.wide &&
-           4 * gp::kFewWarps > p->steps * p->matrices * l.wide)
-        l.wide *= 2;
-    l.grid_x = static_cast<int>((columns + l.wide - 1) / l.wide * l.split);
+    p->wide = 1;
+    while (!all && p->split == 1 && p->wide < 4 && units >= 2.0 * room * p->wide &&
+           4 * gp::kFewWarps > steps * p->wide)
+        p->wide *= 2;
+    p->columns = static_cast<int>((columns + p->wide - 1) / p->wide);
+    l.ok = static_cast<int64_t>(p->columns) * p->max_items < int64_t(1) << 30;  // (units are counted in 32 bits)
+    const int64_t clusters = static_cast<int64_t>(p->columns) * (all ? 1 : items);
+    l.grid = static_cast<int>((all || clusters <= 4 * room ? clusters : room) * p->split);
     return l;
 }
 
@@ -197,8 +227,9 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
         down.out = parts;
         down.ldo = C;
     }
-    const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp, d.sms);
-    const FewLaunch ld = few_launch(&down, bf16, four, down_off, flat ? gp::kFewFlat : gp::kFewParts, d.sms);
+    const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp);
+    const FewLaunch ld = few_launch(&down, bf16, four, down_off, flat ? gp::kFewFlat : gp::kFewParts);
+    if (!lu.ok || !ld.ok) return GEMMPIPE_ERR_INVALID_VALUE;
     return gp::api_launch(true, s, flat ? 2 : 3, [&] {
         cudaError_t e = launch(lu, up, s);
         if (e == cudaSuccess) e = launch(ld, down, s);
@@ -246,7 +277,8 @@ gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t 
         p.experts = 1;
         p.group_steps = static_cast<int>(group / 32);
         const bool off = misaligned(X, 16) || ldx % 8 || K % 8;
-        const FewLaunch l = few_launch(&p, type == GEMMPIPE_BF16, true, off, gp::kFewUp, d.sms);
+        const FewLaunch l = few_launch(&p, type == GEMMPIPE_BF16, true, off, gp::kFewUp);
+        if (!l.ok) return GEMMPIPE_ERR_INVALID_VALUE;
         return gp::api_launch(true, s, 1, [&] { return launch(l, p, s); });
     });
 }

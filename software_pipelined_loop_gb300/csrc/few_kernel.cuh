@@ -345,10 +345,19 @@ __device__ __forceinline__ int few_build_block(const FewParams &p, FewTables &t,
 
 // ------------------------------------------------------------------ kernel
 
-// Where a warp's loads are: an item, a step of it, and this lane's places.
+// A unit of work: 64 columns of an item (kFewFlat: an item).  A warp takes the
+// steps [lo, hi) of the units `first`, `first` + `stride`, ...; its loads run
+// ahead of its products into the next unit.
+struct FewShare {
+    int first, stride, units;  // units: the number of all
+    int lo, hi;
+};
+
+// Where a warp's loads are, with this lane's places.
 template <int MB>
 struct FewWalk {
-    int item, step, blocks;
+    int unit, step, blocks;
+    int whole;                  // steps of the unit whose loads of the warp are all inside the matrix
     const char *w;              // this lane's piece of the step's first row (4 bits: of its word row)
     const uint16_t *s;          // this lane's scales of the group
     const uint16_t *x[MB];      // this lane's 8 values of each row
@@ -357,7 +366,7 @@ struct FewWalk {
 
 template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 struct FewKernel {
-    static constexpr int CHUNK = 8 * MB, DEPTH = few_depth<FOUR, ANY, MB, MODE>();
+    static constexpr int CHUNK = 8 * MB, DEPTH = few_depth<FOUR, MB>();
     static constexpr bool FIXED = MB > 1;
     static constexpr bool UP = MODE == kFewUp, FLAT = MODE == kFewFlat;
     static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && UP;
@@ -367,24 +376,20 @@ struct FewKernel {
     const FewTables &t;
     const void *W;
     const uint16_t *S;
-    int64_t n0, n4;
+    int64_t n_first;   // the warp's columns in the first block of columns (kFewFlat: in this one)
+    int64_t n4;
+    FewShare share;
     int lane, g, l4;   // lane / 4, lane % 4
-    int steps;
-    int whole;         // steps whose loads of the warp are all inside the matrix
-    bool inside;       // whether this lane's pieces of W are
     uint32_t put, get; // this lane's first place of W in a stage: to copy to, to read
 
-    __device__ __forceinline__ FewKernel(const FewParams &p_, const FewTables &t_, int matrix, int64_t n0_)
-        : p(p_), t(t_), W(matrix ? p_.W[1] : p_.W[0]), S(matrix ? p_.S[1] : p_.S[0]), n0(n0_)
+    __device__ __forceinline__ FewKernel(const FewParams &p_, const FewTables &t_, int matrix, int64_t n_first_,
+                                         const FewShare &share_)
+        : p(p_), t(t_), W(matrix ? p_.W[1] : p_.W[0]), S(matrix ? p_.S[1] : p_.S[0]), n_first(n_first_), share(share_)
     {
         lane = threadIdx.x & 31;
         g = lane >> 2;
         l4 = lane & 3;
         n4 = (p.N + 3) / 4 * 4;
-        steps = static_cast<int>(p.steps);
-        const bool wide = n0 + kFewCols <= (FOUR ? n4 : p.N);
-        whole = wide && !ANY ? static_cast<int>(p.K / Stage::STEP) : 0;
-        inside = FOUR ? n0 + 4 * (lane & 15) < n4 : n0 + 8 * (lane & 7) < p.N;
         if constexpr (FOUR) {
             put = 256 * (lane >> 4) + 16 * ((lane & 15) ^ (2 * (lane >> 4)));
             get = 256 * l4 + 16 * (g ^ (2 * l4));
@@ -394,14 +399,32 @@ struct FewKernel {
         }
     }
 
+    __device__ __forceinline__ int item_of(int unit) const { return FLAT ? unit : unit / p.columns; }
+
+    // The warp's first column in a unit.
+    __device__ __forceinline__ int64_t column_of(int unit) const
+    {
+        return FLAT ? n_first : n_first + static_cast<int64_t>(unit % p.columns) * (p.wide * kFewCols);
+    }
+
     __device__ __forceinline__ int rows_of(int item) const
     {
         return p.ids ? static_cast<int>(t.span[item] >> 16) : min(p.tokens - item * CHUNK, CHUNK);
     }
 
+    // Element 0 of row i of an item, or of its first row where it has no such row.
+    __device__ __forceinline__ const uint16_t *row_of(int item, int rows, int i) const
+    {
+        const int first = p.ids ? static_cast<int>(t.span[item] & 0xffffu) : item * CHUNK;
+        int64_t r = first + (i < rows ? i : 0);
+        if (p.ids) r = UP ? t.row[r] & 0xffu : t.row[r] >> 8;
+        return p.X + r * p.ldx;
+    }
+
     __device__ __forceinline__ void place(FewWalk<MB> &k) const
     {
-        const int64_t e = p.ids ? static_cast<int64_t>(t.expert[k.item]) : 0;
+        const int item = item_of(k.unit);
+        const int64_t e = p.ids ? static_cast<int64_t>(t.expert[item]) : 0, n0 = column_of(k.unit);
         if constexpr (FOUR) {
             const int group_rows = 32 * p.group_steps;
             const int64_t words = (p.K + 7) / 8, groups = (p.K + group_rows - 1) / group_rows;
@@ -411,25 +434,20 @@ struct FewKernel {
             // (off 16-byte boundaries: the row, not the lane's piece of it)
             k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + (lane >> 3)) * p.N + n0 + (ANY_W ? 0 : 8 * (lane & 7)));
         }
-        const int rows = rows_of(k.item), first = p.ids ? static_cast<int>(t.span[k.item] & 0xffffu) : k.item * CHUNK;
+        k.whole = !ANY && n0 + kFewCols <= (FOUR ? n4 : p.N) ? static_cast<int>(p.K / Stage::STEP) : 0;
+        const int rows = rows_of(item);
         k.blocks = (rows + 7) / 8;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            int64_t r = first + (8 * m + g < rows ? 8 * m + g : 0);
-            if (p.ids) r = UP ? t.row[r] & 0xffu : t.row[r] >> 8;
             k.x_bytes[m] = 8 * m + g < rows ? 16u : 0u;
-            k.x[m] = p.X + r * p.ldx + Stage::STEP * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
+            k.x[m] = row_of(item, rows, 8 * m + g) + Stage::STEP * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
         }
     }
 
-    __device__ __forceinline__ void advance(FewWalk<MB> &k, int items) const
+    // On to the pointers of the step after this one, of the same unit.
+    __device__ __forceinline__ void next_step(FewWalk<MB> &k) const
     {
         ++k.step;
-        if (FLAT && k.step == steps) {
-            k.step = 0;
-            if (++k.item < items) place(k);
-            return;
-        }
         if constexpr (FOUR) {
             k.w += 32 * n4;  // 8 rows of words
             if (p.group_steps == 1) k.s += 2 * n4;
@@ -441,6 +459,17 @@ struct FewKernel {
         for (int m = 0; m < MB; ++m) k.x[m] += Stage::STEP;
     }
 
+    __device__ __forceinline__ void advance(FewWalk<MB> &k) const
+    {
+        if (k.step + 1 < share.hi) {
+            next_step(k);
+            return;
+        }
+        k.step = share.lo;
+        k.unit += share.stride;
+        if (k.unit < share.units) place(k);
+    }
+
     // Neighbouring lanes copy neighbouring pieces (lanes that share a 32-byte
     // sector but lie apart cost two requests to the L2 cache).  Pieces of a row
     // are exchanged so that eight lanes that read together, two columns of rows
@@ -450,11 +479,12 @@ struct FewKernel {
     {
         if constexpr (FOUR) {
             const uint32_t to = st + put, scales = st + Stage::SCALES + 8 * lane;
-            if (k.step < whole) {
+            if (k.step < k.whole) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) few_copy16((to ^ (64u * (i & 1))) + 512 * i, k.w + 8 * i * n4);
                 few_copy8(scales, k.s, 8);
             } else {
+                const bool inside = column_of(k.unit) + 4 * (lane & 15) < n4;
                 const int64_t left = p.K - 64 * static_cast<int64_t>(k.step);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -464,10 +494,11 @@ struct FewKernel {
             }
         } else if constexpr (!ANY_W) {
             const uint32_t to = st + put;
-            if (k.step < whole) {
+            if (k.step < k.whole) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) few_copy16((to ^ (64u * (i & 1)) ^ (32u * (i >> 1))) + 512 * i, k.w + 8 * i * p.N);
             } else {
+                const bool inside = column_of(k.unit) + 8 * (lane & 7) < p.N;
                 const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + (lane >> 3));
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -477,8 +508,8 @@ struct FewKernel {
         } else {
             // A row's 128 bytes lie in up to nine aligned pieces: eight by
             // neighbouring lanes, then the ninth of row `lane`.
-            const int64_t left = p.K - 32 * static_cast<int64_t>(k.step);
-            const int bytes = static_cast<int>(p.N - n0 < kFewCols ? 2 * (p.N - n0) : 2 * kFewCols);
+            const int64_t left = p.K - 32 * static_cast<int64_t>(k.step), n_left = p.N - column_of(k.unit);
+            const int bytes = static_cast<int>(n_left < kFewCols ? (n_left > 0 ? 2 * n_left : -16) : 2 * kFewCols);
 #pragma unroll
             for (int i = 0; i < 9; ++i) {
                 const int row = i < 8 ? 4 * i + (lane >> 3) : lane, piece = i < 8 ? lane & 7 : 8;
@@ -516,7 +547,7 @@ struct FewKernel {
 #pragma unroll
                 for (int i = 0; i < HALVES; ++i) {
                     const uint32_t half = HALVES > 1 ? 64u * (i ^ (g & 1)) : 0u;
-                    few_copy16(at + half, k.x[m] + 32 * i, k.step < whole || 32 * i + 8 * l4 < left ? k.x_bytes[m] : 0u);
+                    few_copy16(at + half, k.x[m] + 32 * i, k.step < k.whole || 32 * i + 8 * l4 < left ? k.x_bytes[m] : 0u);
                 }
             }
         }
@@ -536,7 +567,7 @@ struct FewKernel {
         }
     }
 
-    // The loads of a step that is whole, and on to the next one of the item.
+    // The loads of a step that is whole, and on to the next one of the unit.
     __device__ __forceinline__ void load_whole(uint32_t st, FewWalk<MB> &k, int64_t row) const
     {
         const uint32_t to = st + put;
@@ -739,104 +770,109 @@ struct FewKernel {
     }
 
     // Bytes from an aligned piece to the first row of W (those of rows 8t are
-    // the same) and to this lane's rows of X.
-    __device__ __forceinline__ void offsets(const FewWalk<MB> &k, int &w_off, int (&x_off)[MB]) const
+    // the same) and to this lane's rows of X.  A step is a whole number of
+    // pieces of X's row, and rows of W of any pitch: they stay within a unit.
+    __device__ __forceinline__ void offsets(int unit, int &w_off, int (&x_off)[MB]) const
     {
-        if constexpr (ANY_W) w_off = static_cast<int>(reinterpret_cast<uintptr_t>(k.w - 2 * (lane >> 3) * p.N) & 15u);
+        const int item = item_of(unit);
+        if constexpr (ANY_W) {
+            const int64_t e = p.ids ? static_cast<int64_t>(t.expert[item]) : 0;
+            w_off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const uint16_t *>(W) + e * p.K * p.N + column_of(unit)) & 15u);
+        }
+        if constexpr (ANY_X) {
+            const int rows = rows_of(item);
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-            if constexpr (ANY_X) x_off[m] = static_cast<int>(reinterpret_cast<uintptr_t>(k.x[m]) & 15u);
+            for (int m = 0; m < MB; ++m) x_off[m] = static_cast<int>(reinterpret_cast<uintptr_t>(row_of(item, rows, 8 * m + g)) & 15u);
+        }
     }
 
-    // The warp's `count` steps from step `step` of item `item` on, through its
-    // ring; kFewFlat: sums by token in `sums`, else the item's in acc.
-    __device__ __forceinline__ void walk(float (&acc)[4][MB][4], float *sums, uint32_t ring, int item, int step,
-                                         int items, int count) const
+    // All products of the warp, from step `step` of its first unit on, `count`
+    // steps, through its ring.  After a unit's last step here `done(unit, acc)`
+    // takes the sums.
+    template <class Done>
+    __device__ __forceinline__ void walk(uint32_t ring, int step, int64_t count, Done done) const
     {
-        clear(acc);
+        float acc[4][MB][4];
         FewWalk<MB> k;
-        k.item = item;
+        k.unit = share.first;
         k.step = step;
         if (count > 0) place(k);
         FewWalk<MB> kx = k;
-        // A step is a whole number of 16-byte pieces of X's row, and rows of W of
-        // any pitch: what is off stays off within an item; matrices differ.
-        int w_off = 0, x_off[MB];
-        if (count > 0) offsets(k, w_off, x_off);
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d)
             if (d < count) {
                 load_w(ring + d * Stage::BYTES, k);
-                advance(k, items);
+                advance(k);
             }
         if constexpr (!UP) pdl_wait();  // hidden rows come from the launch before
-        int blocks = count > 0 ? kx.blocks : 0;
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
             if (d < count) {
                 load_x(ring + d * Stage::BYTES, kx);
-                if (d + 1 < DEPTH) advance(kx, items);
+                if (d + 1 < DEPTH) advance(kx);
             }
             few_commit();
         }
+        if (FLAT && count == 0) return;
+        const int64_t row = FOUR ? 8 * n4 : 8 * p.N;  // bytes from a lane's piece to its next one
         uint32_t st = ring;
-        int i = 0;
-        if constexpr (!FLAT && !ANY) {
-            // Whole steps follow one another: nothing to look at in between.
-            const int64_t row = FOUR ? 8 * n4 : 8 * p.N;  // bytes from a lane's piece to its next one
-            for (const int fast = min(count - DEPTH, whole - step - DEPTH); i < fast; ++i) {
+        int64_t left = count;  // steps to go
+        for (int unit = share.first; unit < share.units; unit += share.stride) {
+            clear(acc);
+            const int blocks = (rows_of(item_of(unit)) + 7) / 8;
+            int w_off = 0, x_off[MB];
+            offsets(unit, w_off, x_off);
+            const int last = left < share.hi - step ? step + static_cast<int>(left) : share.hi;
+            const auto work = [&](auto load) {
                 few_wait<DEPTH - 1>();
-                __syncwarp();
+                __syncwarp();  // a lane's operands are other lanes' copies
                 multiply_rows(acc, st, step, blocks, w_off, x_off);
                 __syncwarp();
-                load_whole(st, k, row);
+                load();
                 few_commit();
                 st = st == ring + (DEPTH - 1) * Stage::BYTES ? ring : st + Stage::BYTES;
-            }
-            step += i;
-        }
-        for (; i < count; ++i) {
-            few_wait<DEPTH - 1>();
-            __syncwarp();  // a lane's operands are other lanes' copies
-            multiply_rows(acc, st, step, blocks, w_off, x_off);
-            __syncwarp();
-            if (i + DEPTH < count) {
-                load_w(st, k);
-                load_x(st, k);
-                advance(k, items);
-            }
-            few_commit();
-            st = st == ring + (DEPTH - 1) * Stage::BYTES ? ring : st + Stage::BYTES;
-            ++step;
-            if constexpr (FLAT) {
-                if (step == steps || i + 1 == count) {
-                    add(sums, acc, item);
-                    clear(acc);
-                    if (i + 1 < count) {
-                        step = 0;
-                        ++item;
-                        blocks = (rows_of(item) + 7) / 8;
-                        if constexpr (ANY_W) {
-                            const char *at = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + t.expert[item] * p.K * p.N + n0);
-                            w_off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u);
-                        }
-                    }
+            };
+            while (step < last) {
+                // Runs of steps whose loads are whole and lead on to the same unit: nothing else to look at.
+                int run = 0;
+                if (!ANY && left > DEPTH) {
+                    run = min(last - step, min(k.whole, share.hi - 1) - k.step);
+                    if (left - DEPTH < run) run = static_cast<int>(left - DEPTH);
                 }
+                if (run > 0) {
+                    for (int i = 0; i < run; ++i) work([&] { load_whole(st, k, row); });
+                    step += run;
+                    left -= run;
+                    continue;
+                }
+                work([&] {
+                    if (left > DEPTH) {
+                        load_w(st, k);
+                        load_x(st, k);
+                        advance(k);
+                    }
+                });
+                ++step;
+                --left;
             }
+            done(unit, acc);
+            if (FLAT && left == 0) break;
+            step = share.lo;
         }
     }
 };
 
-// grid: x = `wide` times 64 columns x blocks of a cluster, y = items (kFewFlat:
-// 1).  The warps of a block share the products of 64 columns, or (wide > 1) so
-// many each of several 64s; `split` blocks share those of the same columns.
+// A block (of a cluster of `split`) takes units in turn: `wide` times 64 columns
+// of an item (kFewFlat: the items, of its own columns).  Its warps share the
+// products of 64 columns, or (wide > 1) so many each of several 64s; the blocks
+// of a cluster share those of the same columns.
 template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
-__global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(const __grid_constant__ FewParams p, int split, int wide)
+__global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(const __grid_constant__ FewParams p)
 {
     using K = FewKernel<BF16, FOUR, ANY, MB, MODE>;
     constexpr bool UP = K::UP, FLAT = K::FLAT;
     extern __shared__ __align__(128) unsigned char few_smem[];
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, split = p.split;
     // The launch that makes hidden rows waits for everything before it and
     // only then lets the next one start, which may read what was there before
     // both, weights and choices, right away.
@@ -844,26 +880,21 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
     pdl_launch_dependents();
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int matrices = UP ? p.matrices : 1;
-    const int warps = kFewWarps / wide, each = warps / matrices;  // of 64 columns, of a matrix of theirs
-    const int64_t n_block = static_cast<int64_t>(blockIdx.x / split) * (wide * kFewCols);
-    // Sums of tokens stand beside the rings, those of an item take their place.
-    const int slab = (FLAT ? p.tokens : K::CHUNK) * kFewCols;  // a warp's sums
+    const int warps = kFewWarps / p.wide, each = warps / matrices;  // of 64 columns, of a matrix of theirs
+    const int slab_rows = FLAT ? p.tokens : 8, slab = slab_rows * kFewCols;  // a warp's sums
+    const int sent = few_sent(min(p.tokens, slab_rows));                     // those of a matrix that count, at most
     float *from_cluster = reinterpret_cast<float *>(few_smem + p.table_bytes);  // sums of other blocks
-    const int sent = min(p.tokens, FLAT ? p.tokens : K::CHUNK) * kFewCols;      // those of a matrix, at most
     float *sums = from_cluster + (split > 1 ? matrices * sent : 0);
-    const uint32_t ring = smem_u32(sums) + (FLAT ? kFewWarps * slab * 4 : 0) + warp * (K::DEPTH * K::Stage::BYTES);
+    const uint32_t ring = smem_u32(sums) + kFewWarps * slab * 4 + warp * (K::DEPTH * K::Stage::BYTES);
     FewTables t{};
-    int items = static_cast<int>(gridDim.y);
+    int items = p.max_items;
     if (p.ids) {
         uint32_t *tables = reinterpret_cast<uint32_t *>(few_smem);
         items = p.tokens * p.top_k <= 32 ? few_build_warp<K::CHUNK>(p, t, tables) : few_build_block<K::CHUNK>(p, t, tables);
     }
-    float acc[4][MB][4];
 
-    // Where sum i of 64 columns of an item is stored, and how.
-    const auto finish = [&](int item, int64_t n0, int i, float a, float b) {
-        const int r = i / kFewCols;
-        const int64_t n = n0 + i % kFewCols;
+    // Where the sum of row r and column n of an item is stored, and how.
+    const auto finish = [&](int item, int r, int64_t n, float a, float b) {
         if (n >= p.out_cols) return;
         if (UP && p.silu) a = a / (1.0f + expf(-a));
         if (matrices == 2) a *= b;
@@ -882,13 +913,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
         else
             static_cast<uint16_t *>(p.out)[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
     };
-    // Adds the warps' `count` rows of sums, then the cluster's, in order: every
-    // block sends its sums to the block that will store them.
-    const auto join = [&](int item, int count) {
-        const int total = count * kFewCols, share = (total + split - 1) / split;
+    // Adds the warps' sums of `rows` rows, the first of them row r0 of the item,
+    // then the cluster's, in order: every block sends its sums to the block
+    // that will store them.  (more: this is not the last time.)
+    const auto join = [&](int item, int64_t n0, int r0, int rows, bool more) {
+        const int total = rows * kFewCols, part = (total + split - 1) / split;
         __syncthreads();
         if (split > 1) few_cluster_wait();  // the others have read what they had here before
-        for (int c = 0; c < wide; ++c)
+        for (int c = 0; c < p.wide; ++c)
             for (int i = tid; i < total; i += 32 * kFewWarps) {
                 float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -898,58 +930,65 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
                     else b += v;
                 }
                 if (split == 1) {
-                    finish(item, n_block + c * kFewCols, i, a, b);
+                    finish(item, r0 + i / kFewCols, n0 + c * kFewCols + i % kFewCols, a, b);
                 } else {
-                    const uint32_t to = mapa_shared(smem_u32(from_cluster) + 4 * (rank * share + i % share), i / share);
+                    const uint32_t to = mapa_shared(smem_u32(from_cluster) + 4 * (rank * part + i % part), i / part);
                     few_st_cluster(to, a);
                     if (matrices == 2) few_st_cluster(to + 4 * sent, b);
                 }
             }
-        if (split == 1) return;
-        cluster_sync();
-        for (int i = tid; i < share && rank * share + i < total; i += 32 * kFewWarps) {
-            float a = 0.0f, b = 0.0f;
-            for (int r = 0; r < split; ++r) {
-                a += from_cluster[r * share + i];
-                if (matrices == 2) b += from_cluster[sent + r * share + i];
+        if (split > 1) {
+            cluster_sync();
+            for (int i = tid; i < part && rank * part + i < total; i += 32 * kFewWarps) {
+                float a = 0.0f, b = 0.0f;
+                for (int r = 0; r < split; ++r) {
+                    a += from_cluster[r * part + i];
+                    if (matrices == 2) b += from_cluster[sent + r * part + i];
+                }
+                const int at = rank * part + i;
+                finish(item, r0 + at / kFewCols, n0 + at % kFewCols, a, b);
             }
-            finish(item, n_block, rank * share + i, a, b);
+            if (more) few_cluster_arrive();
         }
+        __syncthreads();
     };
 
+    const int cluster = static_cast<int>(blockIdx.x) / split, clusters = static_cast<int>(gridDim.x) / split;
+    if (split > 1 && (FLAT || cluster < items * p.columns)) few_cluster_arrive();
     if constexpr (FLAT) {
-        if (split > 1) few_cluster_arrive();
+        const int64_t n0 = static_cast<int64_t>(cluster) * kFewCols;
         float *own = sums + warp * slab;
         for (int i = tid & 31; i < slab; i += 32) own[i] = 0.0f;
         __syncwarp();
         const int64_t total = static_cast<int64_t>(items) * p.steps;
         const int part = rank * kFewWarps + warp, parts = split * kFewWarps;
         const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
-        const K k(p, t, 0, n_block);
-        k.walk(acc, own, ring, static_cast<int>(lo / p.steps), static_cast<int>(lo % p.steps), items,
-               static_cast<int>(hi - lo));
-        join(0, p.tokens);
+        const K k(p, t, 0, n0, FewShare{static_cast<int>(lo / p.steps), 1, items, 0, static_cast<int>(p.steps)});
+        k.walk(ring, static_cast<int>(lo % p.steps), hi - lo,
+               [&](int item, const float(&acc)[4][MB][4]) { k.add(own, acc, item); });
+        join(0, n0, 0, p.tokens, false);
     } else {
         const int part = rank * each + warp % each, parts = split * each;
         const int lo = static_cast<int>(p.steps * part / parts), hi = static_cast<int>(p.steps * (part + 1) / parts);
-        const K k(p, t, warp % warps / each, n_block + warp / warps * kFewCols);
+        const int units = items * p.columns;
+        const K k(p, t, warp % warps / each, warp / warps * kFewCols, FewShare{cluster, clusters, units, lo, hi});
+        const int mine = cluster < units ? (units - cluster + clusters - 1) / clusters : 0;
         float *own = sums + warp * slab;
-        if (!UP && static_cast<int>(blockIdx.y) >= items) pdl_wait();  // nothing to do; every launch waits for the last
-        for (int item = blockIdx.y; item < items; item += gridDim.y) {
-            if (split > 1) few_cluster_arrive();
-            k.walk(acc, nullptr, ring, item, lo, item + 1, hi - lo);
-            __syncthreads();  // the sums take the rings' place
+        k.walk(ring, lo, static_cast<int64_t>(mine) * (hi - lo), [&](int unit, const float(&acc)[4][MB][4]) {
+            const int item = unit / p.columns, rows = k.rows_of(item);
+            const int64_t n0 = static_cast<int64_t>(unit % p.columns) * (p.wide * kFewCols);
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
+            for (int m = 0; m < MB; ++m) {
+                if (MB > 1 && 8 * m >= rows) break;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float2 *>(own + (8 * m + 2 * k.l4 + i) * kFewCols + k.column(j)) =
+                        *reinterpret_cast<float2 *>(own + (2 * k.l4 + i) * kFewCols + k.column(j)) =
                             make_float2(acc[j][m][i], acc[j][m][2 + i]);
-            join(item, k.rows_of(item));
-            __syncthreads();
-        }
+                join(item, n0, 8 * m, min(rows - 8 * m, 8), 8 * (m + 1) < rows || unit + clusters < units);
+            }
+        });
     }
 }
 
@@ -960,16 +999,15 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
 {
     using K = FewKernel<BF16, FOUR, ANY, MB, MODE>;
     constexpr int kMaxSmem = 227 * 1024;
-    const int slab = 4 * kFewCols * (K::FLAT ? p.tokens : K::CHUNK), sums = kFewWarps * slab;
-    const int rings = kFewWarps * K::DEPTH * K::Stage::BYTES;
-    const int smem = p.table_bytes + (l.split > 1 ? p.matrices * 4 * kFewCols * (p.tokens < K::CHUNK ? p.tokens : K::CHUNK) : 0) +
-                     (K::FLAT ? sums + rings : (sums > rings ? sums : rings));
+    const int rows = K::FLAT ? p.tokens : 8, sent = p.tokens < rows ? p.tokens : rows;
+    const int smem = p.table_bytes + 4 * ((p.split > 1 ? p.matrices * few_sent(sent) : 0) + kFewWarps * rows * kFewCols) +
+                     kFewWarps * K::DEPTH * K::Stage::BYTES;
     if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(few_kernel<BF16, FOUR, ANY, MB, MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(l.grid_x, l.grid_y, 1);
+    cfg.gridDim = dim3(l.grid, 1, 1);
     cfg.blockDim = dim3(32 * kFewWarps, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -977,16 +1015,43 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
     int n = 0;
     attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    if (l.split > 1) {
+    if (p.split > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = l.split;
+        attr[n].val.clusterDim.x = p.split;
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, few_kernel<BF16, FOUR, ANY, MB, MODE>, p, l.split, l.wide);
+    e = cudaLaunchKernelEx(&cfg, few_kernel<BF16, FOUR, ANY, MB, MODE>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Clusters of `split` blocks that run at once on the current device, for the
+// kernels of two blocks an SM (MB 1) or of one (MB 4); 0 on an error.
+template <int MB>
+int few_room_of(int split)
+{
+    const auto kernel = few_kernel<true, false, false, MB, kFewUp>;
+    constexpr int smem = MB < 4 ? 100 * 1024 : 200 * 1024;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split * 64, 1, 1);
+    cfg.blockDim = dim3(32 * kFewWarps, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
 template <bool BF16, bool FOUR, bool ANY, int MB>
