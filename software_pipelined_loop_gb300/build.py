@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libgemmpipe.so")
 
 SOURCES = ["gemm_f16.cu", "gemm_s8.cu", "aux_kernels.cu", "gemmpipe_api.cpp", "gemm_noalloc.cu", "gemm_imma.cu",
            "grouped.cu", "experts_rows.cu", "keep8.cu", "experts_api.cpp",
-           "few_f16.cu", "few_bf16.cu", "few_combine.cu", "pack4.cu", "few_api.cpp"]
+           "few_f16.cu", "few_bf16.cu", "few_combine.cu", "rows4_wide.cu", "pack4.cu", "few_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
           "-I" + INCLUDE, "-I" + CSRC]

@@ -2,6 +2,7 @@
 // weights' way into 4 bits and back (pack4.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -101,6 +102,29 @@ int few_room(int one, int split);
 // for a choice: one inside [0, experts), the token's first of that expert.
 cudaError_t launch_few_combine(bool bf16, int tokens, int top_k, int experts, int64_t width, const int32_t *ids,
                                const float *parts, uint16_t *Y, int64_t ldy, cudaStream_t s);
+
+// ---- more than 16 rows times weights in 4 bits (rows4_wide.cu)
+
+struct WideParams {
+    const uint16_t *S;
+    uint16_t *Y;
+    int64_t ldy, N, n4, K;
+    int M, group;
+    int stages;            // ceil(K / 128)
+    int split;             // CTAs of a cluster, sharing a tile's k
+    int64_t stall_stage;   // test hook: the stage that CTA 0 leaves unfilled (-1: none)
+    int *status;
+    uint64_t timeout_ns;
+};
+
+constexpr int kWideCols = 128;  // columns of a tile
+
+// words: rows of 16-bit halves of the words, boxes of 64 x 16; rows: X, boxes of
+// 64 x 64 (more than 32 rows) or 64 x 32.
+cudaError_t launch_rows4_wide(bool bf16, const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p,
+                              int grid, cudaStream_t s);
+
+// ---- weights into 4 bits and back (pack4.cu)
 
 cudaError_t launch_pack4(bool bf16, int64_t experts, int64_t K, int64_t N, int group, const uint16_t *W, uint32_t *Q,
                          uint16_t *S, cudaStream_t s);

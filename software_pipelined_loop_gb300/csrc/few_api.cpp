@@ -13,6 +13,7 @@
 #include "api_internal.h"
 #include "few.h"
 #include "grouped_params.h"
+#include "variants.h"
 
 namespace {
 
@@ -146,6 +147,50 @@ cudaError_t launch(const FewLaunch &l, const FewParams &p, cudaStream_t s)
     return l.bf16 ? gp::launch_few_bf16(l, p, s) : gp::launch_few_f16(l, p, s);
 }
 
+// More than 16 aligned rows times 4 bits: tiles of 128 columns on tcgen05.
+bool wide_rows4(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx)
+{
+    return M > 16 && N <= (int64_t(1) << 29) && K <= (int64_t(1) << 30) && !misaligned(X, 16) && ldx % 8 == 0;
+}
+
+gemmpipe_status_t rows4_wide(bool bf16, int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *X, int64_t ldx,
+                             const uint32_t *Q, const uint16_t *S, uint16_t *Y, int64_t ldy, cudaStream_t s)
+{
+    gp::WideParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.S = S;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.N = N;
+    p.n4 = (N + 3) / 4 * 4;
+    p.K = K;
+    p.M = static_cast<int>(M);
+    p.group = static_cast<int>(group);
+    p.stages = static_cast<int>((K + 127) / 128);
+    const int64_t tiles = (N + gp::kWideCols - 1) / gp::kWideCols;
+    // As many CTAs a tile as run at once, of two stages at least.
+    p.split = 1;
+    for (int split = 2; split <= 8; ++split)
+        if (tiles <= gp::few_room(1, split) && 2 * split <= p.stages) p.split = split;
+    CUtensorMap words, rows;
+    const uint64_t wd[2] = {static_cast<uint64_t>(2 * p.n4), static_cast<uint64_t>((K + 7) / 8)};
+    const uint64_t ws[1] = {static_cast<uint64_t>(4 * p.n4)};
+    const uint64_t xd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
+    const uint64_t xs[1] = {static_cast<uint64_t>(2 * ldx)};
+    const uint32_t wb[2] = {64, 16}, xb[2] = {64, M > 32 ? 64u : 32u};
+    if (!gp::api_encode_16bit(&words, bf16, 2, Q, wd, ws, wb) || !gp::api_encode_16bit(&rows, bf16, 2, X, xd, xs, xb))
+        return GEMMPIPE_ERR_INTERNAL;
+    p.timeout_ns = 2000000000ull + static_cast<uint64_t>(p.stages) * 10000ull;
+    p.stall_stage = gp::api_take_stall(&p.timeout_ns);
+    if (gp::status_word(&p.status) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMMPIPE_ERR_LAUNCH;
+    }
+    return gp::api_launch(true, s, 1, [&] {
+        return gp::launch_rows4_wide(bf16, words, rows, p, static_cast<int>(tiles * p.split), s);
+    });
+}
+
 struct Matrices {  // W of an expert step: 16 bits, or words with scales
     const void *W[3];
     const uint16_t *S[3];
@@ -261,6 +306,10 @@ gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t 
         cudaStream_t s = stream_of(stream);
         if (K == 0) return zero_rows(Y, M, N, ldy, s);
         if ((st = check_all({{X, 2}, {Q, 16}, {S, 8}})) != GEMMPIPE_OK) return st;
+        const bool bf16 = type == GEMMPIPE_BF16;
+        if (wide_rows4(M, N, K, X, ldx))
+            return rows4_wide(bf16, M, N, K, group, static_cast<const uint16_t *>(X), ldx, Q,
+                              static_cast<const uint16_t *>(S), static_cast<uint16_t *>(Y), ldy, s);
         FewParams p;
         std::memset(&p, 0, sizeof(p));
         p.X = static_cast<const uint16_t *>(X);
@@ -277,7 +326,7 @@ gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t 
         p.experts = 1;
         p.group_steps = static_cast<int>(group / 32);
         const bool off = misaligned(X, 16) || ldx % 8 || K % 8;
-        const FewLaunch l = few_launch(&p, type == GEMMPIPE_BF16, true, off, gp::kFewUp);
+        const FewLaunch l = few_launch(&p, bf16, true, off, gp::kFewUp);
         if (!l.ok) return GEMMPIPE_ERR_INVALID_VALUE;
         return gp::api_launch(true, s, 1, [&] { return launch(l, p, s); });
     });

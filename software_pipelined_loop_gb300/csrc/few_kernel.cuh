@@ -110,17 +110,27 @@ __device__ __forceinline__ uint16_t few_round(float v)
 }
 
 // Values i and i + 4 of a word of eight 4-bit values: the pair of rows 2i, 2i
-// + 1.  (v & mask) | one is a single operation when both are in registers.
+// + 1.  (v & mask) | one is a single operation when both are in registers.  The
+// fp16 mantissa holds the upper of two neighbouring values in its place, 16
+// times as large, so that one shift serves two pairs; that of bf16 is too short.
 template <bool BF16>
 __device__ __forceinline__ uint32_t few_pair(uint32_t word, int i)
 {
     uint32_t m;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(BF16 ? 0x43004300u : 0x64006400u));
-    if constexpr (BF16) {  // 128 + q
-        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), __float2bfloat162_rn(136.0f));
+    if constexpr (BF16) {
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), __float2bfloat162_rn(136.0f));  // 128 + q
         return *reinterpret_cast<const uint32_t *>(&v);
-    } else {               // 1024 + q
-        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1032.0f));
+    } else {
+        const uint32_t w = word >> (8 * (i >> 1));
+        __half2 v;
+        if (i & 1) {
+            asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(w), "r"(0x00f000f0u), "r"(0x64006400u));
+            v = __hfma2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));  // 1024 + 16 q
+        } else {
+            asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(w), "r"(0x000f000fu), "r"(0x64006400u));
+            v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1032.0f));  // 1024 + q
+        }
         return *reinterpret_cast<const uint32_t *>(&v);
     }
 }
@@ -164,18 +174,6 @@ __device__ __forceinline__ uint4 few_first(uint4 v, int count)
         else if (count == 2 * i + 1) w[i] &= 0xffffu;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Loads of a stage, FIXED in their order among the products or not.
-template <class T, bool FIXED = false>
-__device__ __forceinline__ T few_ld_shared(uint32_t addr)
-{
-    if constexpr (FIXED && sizeof(T) == 16)
-        return ld_shared_v4(addr);
-    else if constexpr (FIXED)
-        return ld_shared_v2(addr);
-    else
-        return *static_cast<const T *>(__cvta_shared_to_generic(addr));
 }
 
 __device__ __forceinline__ void few_st_cluster(uint32_t addr, float v)
@@ -559,11 +557,11 @@ struct FewKernel {
         const uint32_t at = st + Stage::X + Stage::X_BLOCK * m + Stage::X_PITCH * g + 16 * l4;
         if constexpr (ANY_X) {
             uint32_t o[4];
-            realign16_steps(few_ld_shared<uint4, FIXED>(at + 64 * half), few_ld_shared<uint4, FIXED>(at + 64 * half + 16), off, o);
+            realign16_steps(ld_shared_v4(at + 64 * half), ld_shared_v4(at + 64 * half + 16), off, o);
             const int64_t left = p.K - (Stage::STEP * static_cast<int64_t>(step) + 32 * half + 8 * l4);
             return few_first(make_uint4(o[0], o[1], o[2], o[3]), left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8));
         } else {
-            return few_ld_shared<uint4, FIXED>(at + (Stage::STEP > 32 ? 64u * (half ^ (g & 1)) : 0u));
+            return ld_shared_v4(at + (Stage::STEP > 32 ? 64u * (half ^ (g & 1)) : 0u));
         }
     }
 
@@ -607,7 +605,7 @@ struct FewKernel {
     {
         const uint32_t at = st + Stage::W_GROUP * l4 + Stage::W_PITCH * r + 16 * g;
         uint32_t o[4];
-        realign16_steps(few_ld_shared<uint4, FIXED>(at), few_ld_shared<uint4, FIXED>(at + 16), off, o);
+        realign16_steps(ld_shared_v4(at), ld_shared_v4(at + 16), off, o);
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
 
@@ -626,11 +624,11 @@ struct FewKernel {
                 for (int m = 0; m < NB; ++m) x[i][m] = rows_x(st, m, q + i, x_off[m], step);
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                const uint2 scales = few_ld_shared<uint2, FIXED>(st + Stage::SCALES + 128 * q + 64 * l + 8 * g);
+                const uint2 scales = ld_shared_v2(st + Stage::SCALES + 128 * q + 64 * l + 8 * g);
                 uint32_t w[SAME][4];
 #pragma unroll
                 for (int i = 0; i < SAME; ++i) {
-                    const uint4 v = few_ld_shared<uint4, FIXED>(st + get + 1024 * (q + i) + 128 * l);
+                    const uint4 v = ld_shared_v4(st + get + 1024 * (q + i) + 128 * l);
                     w[i][0] = v.x;
                     w[i][1] = v.y;
                     w[i][2] = v.z;
@@ -701,7 +699,7 @@ struct FewKernel {
                     if constexpr (ANY_W)
                         v = weights_any(st, 4 * h + r, (w_off + 2 * static_cast<int>(p.N & 7) * (4 * h + r)) & 15);
                     else
-                        v = few_ld_shared<uint4, FIXED>(((st + get) ^ (16u * (4 * h + r))) + 128 * (4 * h + r));
+                        v = ld_shared_v4(((st + get) ^ (16u * (4 * h + r))) + 128 * (4 * h + r));
                     w[r][0] = v.x;
                     w[r][1] = v.y;
                     w[r][2] = v.z;

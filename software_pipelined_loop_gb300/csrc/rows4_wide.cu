@@ -1,0 +1,469 @@
+// rows4_wide.cu -- more than 16 rows times weights in 4 bits, on the tensor
+// cores' tensor memory.
+//
+// Y[m][n] = sum over groups g of s[g][n] * (sum over k of the group of
+// X[m][k] * (q[k][n] - 8)).  With some tens of rows the warp-level matrix
+// instructions of few_kernel.cuh are the bound (1024 products a cycle and SM;
+// 64 rows x 16384 x 4096: 38 us, 28 of them products alone).  Here a CTA takes
+// 128 columns and a range of k:
+//   - a producer warp fills a ring of stages of 128 k with TMA copies of the
+//     words (16 rows of 128) and of X's rows (128-byte swizzle);
+//   - two warpgroups take stages in turn: a thread has one column, turns its
+//     sixteen words into 128 exact 16-bit values and stores them to tensor memory
+//     -- as operand A of the MMA, whose 128 rows are the columns; so weights
+//     pass neither back through shared memory nor through a rounding;
+//   - an MMA warp issues tcgen05.mma (128 x rows x 16) with X from shared
+//     memory, into one accumulator per group of k;
+//   - a fourth warpgroup reads a group's accumulator, a column a thread, and
+//     adds it to the column's sums in registers, times the group's scale: fp32
+//     throughout, one rounding at the end.
+// The CTAs of a cluster share a tile's k; their sums meet in shared memory, in
+// a fixed order.  Every wait is bounded (Waiter).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "few.h"
+#include "gemm_kernel.cuh"
+
+namespace gp {
+namespace {
+
+constexpr int kStageK = 128;  // products of a row in a stage: a whole number of groups, or one
+
+template <int MP_>
+struct WideCfg {
+    static constexpr int MP = MP_;                          // rows of X, rounded up: the MMA's columns
+    static constexpr int SUBS = kStageK / 64;               // tiles of 64 products
+    static constexpr int X_BYTES = SUBS * MP * 128, WORD_BOX = kStageK / 8 * 128, WORD_BYTES = 4 * WORD_BOX;
+    static constexpr int STAGE_BYTES = X_BYTES + WORD_BYTES;
+    static constexpr int STAGES = MP == 64 ? 7 : 8;
+    static constexpr int A_BUFS = 3, A_COLS = kStageK / 2;  // tensor memory: a stage's values of 128 columns
+    static constexpr int D_BUFS = MP == 64 ? 5 : 7;         // accumulators of MP columns
+    static constexpr int D_COL0 = A_BUFS * A_COLS;
+    static constexpr int CTL_OFF = STAGES * STAGE_BYTES;
+    static constexpr int SMEM_BYTES = 1024 + CTL_OFF + 512;
+    static constexpr int PRODUCER_WARP = 0, MMA_WARP = 1, SUM_WARP0 = 4, UNPACK_WARP0 = 8, THREADS = 16 * 32;
+
+    static_assert(D_COL0 + D_BUFS * MP <= 512, "tensor memory");
+    static_assert(D_BUFS + 1 < STAGES + 1 && A_BUFS < STAGES, "a stage's barrier outlasts its readers");
+    static_assert(STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448 && SMEM_BYTES > 116 * 1024, "one CTA an SM");
+    static_assert(MP * 128 * 4 <= CTL_OFF, "sums of the cluster in the ring's place");
+};
+
+template <class Cfg>
+struct WideCtl {
+    uint64_t full[Cfg::STAGES];    // copies of a stage have landed
+    uint64_t a_full[Cfg::A_BUFS];  // its values are in tensor memory
+    // Its products are done: the stage may be filled again, the values' buffer
+    // too, and accumulators that end here be read.
+    uint64_t done[Cfg::STAGES];
+    uint64_t d_empty[Cfg::D_BUFS];  // an accumulator has been read
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// A place in a ring of N, and the parity of its barrier's phase.
+template <int N>
+struct Ring {
+    int at = 0;
+    uint32_t parity = 0;
+
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// A whole warp's bounded wait, without branches by lane.
+__device__ __forceinline__ bool wait_for(const Waiter &w, const uint64_t *bar, uint32_t parity)
+{
+    const uint32_t at = smem_u32(bar);
+    for (int i = 0; i < 16; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    return __all_sync(0xffffffffu, w.wait(at, parity));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float scale_of(uint16_t bits)
+{
+    if constexpr (BF16)
+        return __uint_as_float(static_cast<uint32_t>(bits) << 16);
+    else
+        return __half2float(__ushort_as_half(bits));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t round_of(float v)
+{
+    if constexpr (BF16)
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else
+        return __half_as_ushort(__float2half_rn(v));
+}
+
+// Values i and i + 4 of a word as 16-bit numbers q - 8: rows 2i, 2i + 1.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pair_of(uint32_t word, int i)
+{
+    uint32_t m;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(m) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(BF16 ? 0x43004300u : 0x64006400u));
+    if constexpr (BF16) {  // 128 + q
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), __float2bfloat162_rn(136.0f));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {               // 1024 + q
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1032.0f));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// 32 columns of this thread's lane of tensor memory.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc].
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// The CTA's stages [lo, hi).
+struct WideRange {
+    int lo, hi;
+};
+
+__device__ __forceinline__ WideRange wide_range(const WideParams &p, int rank)
+{
+    return WideRange{static_cast<int>(static_cast<int64_t>(p.stages) * rank / p.split),
+                     static_cast<int>(static_cast<int64_t>(p.stages) * (rank + 1) / p.split)};
+}
+
+template <class Cfg>
+__device__ void wide_producer(const WideParams &p, const CUtensorMap *words, const CUtensorMap *rows, uint32_t sbase,
+                              WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r, int col0)
+{
+    Ring<Cfg::STAGES> slot;
+    for (int i = r.lo; i < r.hi; ++i, slot.next()) {
+        if (!wait_for(w, &ctl->done[slot.at], slot.parity ^ 1u)) {
+            // Copies in flight land before the CTA's shared memory goes.
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000ull) {
+            }
+            return;
+        }
+        if (static_cast<int64_t>(i - r.lo) == p.stall_stage && blockIdx.x == 0) continue;  // (test hook)
+        if (elect_one_sync()) {
+            const uint32_t bar = smem_u32(&ctl->full[slot.at]), at = sbase + slot.at * Cfg::STAGE_BYTES;
+            mbar_arrive_expect_tx(bar, Cfg::STAGE_BYTES);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)  // 32 columns of words: 64 16-bit elements
+                tma_load_2d(at + Cfg::X_BYTES + Cfg::WORD_BOX * c, words, bar, 2 * (col0 + 32 * c), kStageK / 8 * i);
+#pragma unroll
+            for (int t = 0; t < Cfg::SUBS; ++t)
+                tma_load_2d(at + Cfg::MP * 128 * t, rows, bar, kStageK * i + 64 * t, 0);
+        }
+        __syncwarp();
+    }
+}
+
+template <class Cfg, bool BF16>
+__device__ void wide_unpack(uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r,
+                            int warp, int lane)
+{
+    const int q = warp & 3, mine = (warp - Cfg::UNPACK_WARP0) >> 2;  // quarter of the columns, which stages
+    const uint32_t at0 = sbase + Cfg::X_BYTES + Cfg::WORD_BOX * q + 4u * (lane & 3);
+    uint32_t piece[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) piece[b] = 128u * b + (static_cast<uint32_t>((lane >> 2) ^ b) << 4);
+    Ring<Cfg::STAGES> slot, before;  // this stage, and the last one that used its buffer
+    Ring<Cfg::A_BUFS> a;
+    for (int i = 0; i < r.hi - r.lo; ++i, slot.next(), a.next()) {
+        const bool used = i >= Cfg::A_BUFS;
+        if ((i & 1) == mine) {
+            if (!wait_for(w, &ctl->full[slot.at], slot.parity)) return;
+            const uint32_t at = at0 + slot.at * Cfg::STAGE_BYTES;
+            const uint32_t to = tmem + (static_cast<uint32_t>(32 * q) << 16) + Cfg::A_COLS * a.at;
+#pragma unroll
+            for (int t = 0; t < Cfg::SUBS; ++t) {
+                uint32_t v[32];
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const uint32_t word = ld_shared_b32(at + 1024 * t + piece[b]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * b + j] = pair_of<BF16>(word, j);
+                }
+                if (t == 0 && used) {
+                    // (the products before in this buffer; their barrier is not filled again before this stage is done)
+                    if (!wait_for(w, &ctl->done[before.at], before.parity)) return;
+                    tc_fence_after_sync();
+                }
+                tmem_st_32x32b_x32(to + 32 * t, v);
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->a_full[a.at]));
+        }
+        if (used) before.next();
+    }
+}
+
+// BLOCK: MMAs of a group, all in one stage.  The warp that everything waits
+// for: what it takes to issue a block's MMAs and to find the next one's barriers
+// ready is most of a stage's time, so those are looked at while the MMAs go out.
+template <class Cfg, bool BF16, int BLOCK>
+__device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w,
+                         const WideRange &r)
+{
+    constexpr int STEPS = kStageK / 16;
+    const uint32_t idesc = umma_idesc_16bit_f32(128, Cfg::MP, BF16, false, false);
+    const uint64_t b0 = umma_desc_sw128(sbase, 16, 1024);
+    Ring<Cfg::STAGES> slot;
+    Ring<Cfg::A_BUFS> a;
+    Ring<Cfg::D_BUFS> d;
+    const int64_t rows = p.K - kStageK * static_cast<int64_t>(r.lo);
+    bool ok = true, ready = false, free = true;
+    int i = 0;
+    for (const int stages = r.hi - r.lo; i < stages && ok; ++i) {
+        const int64_t left = rows - kStageK * static_cast<int64_t>(i);
+        const int steps = left >= kStageK ? STEPS : static_cast<int>((left + 15) / 16);
+        const uint32_t b_lo = static_cast<uint32_t>(b0) + ((slot.at * Cfg::STAGE_BYTES) >> 4);
+        const uint32_t a_at = tmem + Cfg::A_COLS * a.at;
+        uint64_t *const done = &ctl->done[slot.at];
+        if (!ready) ok = wait_for(w, &ctl->a_full[a.at], a.parity) && wait_for(w, &ctl->full[slot.at], slot.parity);
+        slot.next();
+        a.next();
+        const uint32_t next_a = smem_u32(&ctl->a_full[a.at]), next_full = smem_u32(&ctl->full[slot.at]);
+#pragma unroll
+        for (int j0 = 0; j0 < STEPS; j0 += BLOCK) {
+            if (j0 >= steps || !ok) break;
+            if (!free) ok = wait_for(w, &ctl->d_empty[d.at], d.parity ^ 1u);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d_at = tmem + Cfg::D_COL0 + Cfg::MP * d.at;
+            d.next();
+            const bool is_free = mbar_test_wait(smem_u32(&ctl->d_empty[d.at]), d.parity ^ 1u);
+            bool a_in = true, x_in = true;
+            if (j0 + BLOCK >= STEPS) {
+                a_in = mbar_test_wait(next_a, a.parity);
+                x_in = mbar_test_wait(next_full, slot.parity);
+            }
+            if (elect_one_sync()) {
+#pragma unroll
+                for (int j = j0; j < j0 + BLOCK; ++j)  // (16 products on: 8 columns of A, 32 bytes of B, tiles of 64)
+                    if (j < steps)
+                        umma_f16_ta(d_at, a_at + 8 * j,
+                                    (b0 & 0xffffffff00000000ull) | (b_lo + (j >> 2) * (Cfg::MP * 128 >> 4) + 2 * (j & 3)),
+                                    idesc, j > j0 ? 1u : 0u);
+                if (j0 + BLOCK >= steps) umma_commit(smem_u32(done));
+            }
+            free = __all_sync(0xffffffffu, is_free);
+            if (j0 + BLOCK >= STEPS) ready = __all_sync(0xffffffffu, a_in && x_in);
+        }
+    }
+    if (!ok && i > 1) {
+        if (elect_one_sync()) umma_commit(smem_u32(&ctl->drain));
+        __syncwarp();
+        w.wait_drain(smem_u32(&ctl->drain), 0, kDrainNs);
+    }
+}
+
+// This thread's column's sums over the CTA's groups.
+template <class Cfg, bool BF16>
+__device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r,
+                          int64_t n, int warp, int lane, float (&sum)[Cfg::MP])
+{
+#pragma unroll
+    for (int m = 0; m < Cfg::MP; ++m) sum[m] = 0.0f;
+    const int64_t k0 = kStageK * static_cast<int64_t>(r.lo), k1 = kStageK * static_cast<int64_t>(r.hi);
+    const int64_t rows = (k1 < p.K ? k1 : p.K) - k0;
+    const int groups = rows > 0 ? static_cast<int>((rows + p.group - 1) / p.group) : 0;
+    const int each = kStageK / p.group;  // groups of a stage
+    const uint16_t *scale = p.S + k0 / p.group * p.n4 + (n < p.n4 ? n : 0);
+    Ring<Cfg::STAGES> slot;
+    Ring<Cfg::D_BUFS> d;
+    // A stage's scales are loaded while the stage before is summed, and waited
+    // for before the next ones are asked for: a load in flight would hold up the
+    // use of the ones before it.
+    uint16_t next[kStageK / 32];
+    const auto fetch = [&](int g0) {
+#pragma unroll
+        for (int u = 0; u < kStageK / 32; ++u) next[u] = u < each && g0 + u < groups ? scale[(g0 + u) * p.n4] : 0;
+    };
+    fetch(0);
+    for (int g0 = 0; g0 < groups; g0 += each, slot.next()) {
+        float s[kStageK / 32];
+#pragma unroll
+        for (int u = 0; u < kStageK / 32; ++u) s[u] = scale_of<BF16>(next[u]);
+        fetch(g0 + each);
+        // (not filled again before STAGES more, and accumulators do not reach that far)
+        if (!wait_for(w, &ctl->done[slot.at], slot.parity)) return;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int u = 0; u < kStageK / 32; ++u) {
+            if (u >= each || g0 + u >= groups) break;
+            const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + Cfg::D_COL0 + Cfg::MP * d.at;
+            uint32_t v[2][32];
+            tmem_ld_32x32b_x32(at, v[0]);
+            if constexpr (Cfg::MP == 64) tmem_ld_32x32b_x32(at + 32, v[1]);
+            tmem_wait_ld();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->d_empty[d.at]));
+            d.next();
+#pragma unroll
+            for (int m = 0; m < Cfg::MP; ++m) sum[m] = fmaf(s[u], __uint_as_float(v[m / 32][m % 32]), sum[m]);
+        }
+    }
+}
+
+template <class Cfg, bool BF16>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    rows4_wide_kernel(const __grid_constant__ CUtensorMap words, const __grid_constant__ CUtensorMap rows,
+                      const __grid_constant__ WideParams p)
+{
+    extern __shared__ __align__(1024) uint8_t wide_smem[];
+    const uint32_t raw = smem_u32(wide_smem), pad = (1024u - (raw & 1023u)) & 1023u, sbase = raw + pad;
+    auto *ctl = reinterpret_cast<WideCtl<Cfg> *>(wide_smem + pad + Cfg::CTL_OFF);
+    static_assert(sizeof(WideCtl<Cfg>) <= 512, "control block");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->done[s]), 1);
+        }
+        for (int a = 0; a < Cfg::A_BUFS; ++a) mbar_init(smem_u32(&ctl->a_full[a]), 4);
+        for (int d = 0; d < Cfg::D_BUFS; ++d) mbar_init(smem_u32(&ctl->d_empty[d]), 4);
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&words);
+        tma_prefetch_desc(&rows);
+    }
+    if (warp == Cfg::MMA_WARP) {
+        tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = ctl->tmem_base;
+    const Waiter w{&ctl->abort, p.status, p.timeout_ns};
+    const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x / p.split) * 128;
+    const WideRange r = wide_range(p, rank);
+    const int column = static_cast<int>(threadIdx.x) - 32 * Cfg::SUM_WARP0;  // (of the sums' threads)
+    const bool sums = warp >= Cfg::SUM_WARP0 && warp < Cfg::UNPACK_WARP0;
+    const int64_t n = col0 + column;
+    float sum[Cfg::MP];
+    if (warp == Cfg::PRODUCER_WARP) {
+        wide_producer<Cfg>(p, &words, &rows, sbase, ctl, w, r, static_cast<int>(col0));
+    } else if (warp == Cfg::MMA_WARP) {
+        if (p.group == 32) wide_mma<Cfg, BF16, 2>(p, sbase, tmem, ctl, w, r);
+        else if (p.group == 64) wide_mma<Cfg, BF16, 4>(p, sbase, tmem, ctl, w, r);
+        else wide_mma<Cfg, BF16, 8>(p, sbase, tmem, ctl, w, r);
+    } else if (warp >= Cfg::UNPACK_WARP0) {
+        wide_unpack<Cfg, BF16>(sbase, tmem, ctl, w, r, warp, lane);
+    } else if (sums) {
+        wide_sums<Cfg, BF16>(p, tmem, ctl, w, r, n, warp, lane, sum);
+        if (p.split == 1) {
+            if (n < p.N)
+#pragma unroll
+                for (int m = 0; m < Cfg::MP; ++m)
+                    if (m < p.M) p.Y[m * p.ldy + n] = round_of<BF16>(sum[m]);
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == Cfg::MMA_WARP) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+    if (p.split == 1) return;
+    // The ring is idle: the CTAs' sums, rows of 128 columns, take its place.
+    float *mine = reinterpret_cast<float *>(wide_smem + pad);
+    if (sums)
+#pragma unroll
+        for (int m = 0; m < Cfg::MP; ++m)
+            if (m < p.M) mine[m * 128 + column] = sum[m];
+    cluster_sync();
+    if (sums && n < p.N)
+        for (int m = rank; m < p.M; m += p.split) {
+            float v = 0.0f;
+            for (int c = 0; c < p.split; ++c) v += ld_cluster_f32(mapa_shared(sbase + 4 * (m * 128 + column), c));
+            p.Y[m * p.ldy + n] = round_of<BF16>(v);
+        }
+    cluster_sync();  // others may still read this CTA's sums
+}
+
+template <class Cfg, bool BF16>
+cudaError_t launch(const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p, int grid, cudaStream_t s)
+{
+    const auto kernel = rows4_wide_kernel<Cfg, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, words, rows, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rows4_wide(bool bf16, const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p,
+                              int grid, cudaStream_t s)
+{
+    if (p.M > 32)
+        return bf16 ? launch<WideCfg<64>, true>(words, rows, p, grid, s) : launch<WideCfg<64>, false>(words, rows, p, grid, s);
+    return bf16 ? launch<WideCfg<32>, true>(words, rows, p, grid, s) : launch<WideCfg<32>, false>(words, rows, p, grid, s);
+}
+
+}  // namespace gp
