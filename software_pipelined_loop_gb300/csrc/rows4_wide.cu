@@ -14,9 +14,9 @@
 //     pass neither back through shared memory nor through a rounding;
 //   - an MMA warp issues tcgen05.mma (128 x rows x 16) with X from shared
 //     memory, into one accumulator per group of k;
-//   - a fourth warpgroup reads a group's accumulator, a column a thread, and
-//     adds it to the column's sums in registers, times the group's scale: fp32
-//     throughout, one rounding at the end.
+//   - one or two more warpgroups read a group's accumulator, a column and 32
+//     rows a thread, and add it to the column's sums in registers, times the
+//     group's scale: fp32 throughout, one rounding at the end.
 // The CTAs of a cluster share a tile's k; their sums meet in shared memory, in
 // a fixed order.  Every wait is bounded (Waiter).
 #include <cuda_bf16.h>
@@ -42,14 +42,21 @@ struct WideCfg {
     static constexpr int A_BUFS = 3, A_COLS = kStageK / 2;  // tensor memory: a stage's values of 128 columns
     static constexpr int D_BUFS = MP == 64 ? 5 : 7;         // accumulators of MP columns
     static constexpr int D_COL0 = A_BUFS * A_COLS;
-    static constexpr int CTL_OFF = STAGES * STAGE_BYTES;
+    static constexpr int SCALE_STAGES = 8, SCALE_AHEAD = 5;  // ring of scales, of each warpgroup of sums
+    static constexpr int SCALE_STAGE_BYTES = kStageK / 32 * 128 * 2, SCALE_OFF = STAGES * STAGE_BYTES;
+    static constexpr int CTL_OFF = SCALE_OFF + MP / 32 * SCALE_STAGES * SCALE_STAGE_BYTES;
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + 512;
-    static constexpr int PRODUCER_WARP = 0, MMA_WARP = 1, SUM_WARP0 = 4, UNPACK_WARP0 = 8, THREADS = 16 * 32;
+    // Warps: the producer, two that issue MMAs, one idle; four or eight of sums;
+    // eight that unpack.
+    static constexpr int PRODUCER_WARP = 0, MMA_WARP0 = 1, MMA_WARPS = 2, SUM_WARP0 = 4;
+    static constexpr int SUMS = 32, SUM_WARPS = 4 * (MP / SUMS);  // rows that a thread of sums has
+    static constexpr int UNPACK_WARP0 = SUM_WARP0 + SUM_WARPS, THREADS = 32 * (UNPACK_WARP0 + 8);
 
     static_assert(D_COL0 + D_BUFS * MP <= 512, "tensor memory");
+    static_assert(SCALE_AHEAD + 2 <= SCALE_STAGES, "scales are read before their place is filled again");
     static_assert(D_BUFS + 1 < STAGES + 1 && A_BUFS < STAGES, "a stage's barrier outlasts its readers");
     static_assert(STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448 && SMEM_BYTES > 116 * 1024, "one CTA an SM");
-    static_assert(MP * 128 * 4 <= CTL_OFF, "sums of the cluster in the ring's place");
+    static_assert(MP * 128 * 4 <= SCALE_OFF, "sums of the cluster in the ring's place");
 };
 
 template <class Cfg>
@@ -60,7 +67,7 @@ struct WideCtl {
     // too, and accumulators that end here be read.
     uint64_t done[Cfg::STAGES];
     uint64_t d_empty[Cfg::D_BUFS];  // an accumulator has been read
-    uint64_t drain;
+    uint64_t drain[Cfg::MMA_WARPS];
     uint32_t tmem_base;
     int abort;
 };
@@ -241,12 +248,13 @@ __device__ void wide_unpack(uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, co
     }
 }
 
-// BLOCK: MMAs of a group, all in one stage.  The warp that everything waits
-// for: what it takes to issue a block's MMAs and to find the next one's barriers
-// ready is most of a stage's time, so those are looked at while the MMAs go out.
+// BLOCK: MMAs of a group, all in one stage.  Issuing a stage's MMAs and finding
+// the next barriers ready takes a warp longer than anything else takes (8 MMAs
+// 500 to 600 cycles, the rest as much again), so two warps take stages in turn,
+// and the next barriers are looked at while the MMAs go out.
 template <class Cfg, bool BF16, int BLOCK>
 __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w,
-                         const WideRange &r)
+                         const WideRange &r, int mine)
 {
     constexpr int STEPS = kStageK / 16;
     const uint32_t idesc = umma_idesc_16bit_f32(128, Cfg::MP, BF16, false, false);
@@ -254,19 +262,24 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
     Ring<Cfg::STAGES> slot;
     Ring<Cfg::A_BUFS> a;
     Ring<Cfg::D_BUFS> d;
+    const auto skip = [&](int stages) {
+        for (int s = 0; s < stages; ++s) {
+            slot.next();
+            a.next();
+#pragma unroll
+            for (int j = 0; j < STEPS; j += BLOCK) d.next();
+        }
+    };
+    skip(mine);
     const int64_t rows = p.K - kStageK * static_cast<int64_t>(r.lo);
-    bool ok = true, ready = false, free = true;
-    int i = 0;
-    for (const int stages = r.hi - r.lo; i < stages && ok; ++i) {
+    bool ok = true, ready = false, free = false, issued = false;
+    for (int i = mine; i < r.hi - r.lo && ok; i += Cfg::MMA_WARPS) {
         const int64_t left = rows - kStageK * static_cast<int64_t>(i);
         const int steps = left >= kStageK ? STEPS : static_cast<int>((left + 15) / 16);
         const uint32_t b_lo = static_cast<uint32_t>(b0) + ((slot.at * Cfg::STAGE_BYTES) >> 4);
         const uint32_t a_at = tmem + Cfg::A_COLS * a.at;
         uint64_t *const done = &ctl->done[slot.at];
         if (!ready) ok = wait_for(w, &ctl->a_full[a.at], a.parity) && wait_for(w, &ctl->full[slot.at], slot.parity);
-        slot.next();
-        a.next();
-        const uint32_t next_a = smem_u32(&ctl->a_full[a.at]), next_full = smem_u32(&ctl->full[slot.at]);
 #pragma unroll
         for (int j0 = 0; j0 < STEPS; j0 += BLOCK) {
             if (j0 >= steps || !ok) break;
@@ -275,12 +288,15 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
             tc_fence_after_sync();
             const uint32_t d_at = tmem + Cfg::D_COL0 + Cfg::MP * d.at;
             d.next();
-            const bool is_free = mbar_test_wait(smem_u32(&ctl->d_empty[d.at]), d.parity ^ 1u);
             bool a_in = true, x_in = true;
             if (j0 + BLOCK >= STEPS) {
-                a_in = mbar_test_wait(next_a, a.parity);
-                x_in = mbar_test_wait(next_full, slot.parity);
+                slot.next();
+                a.next();
+                skip(Cfg::MMA_WARPS - 1);
+                a_in = mbar_test_wait(smem_u32(&ctl->a_full[a.at]), a.parity);
+                x_in = mbar_test_wait(smem_u32(&ctl->full[slot.at]), slot.parity);
             }
+            const bool is_free = mbar_test_wait(smem_u32(&ctl->d_empty[d.at]), d.parity ^ 1u);
             if (elect_one_sync()) {
 #pragma unroll
                 for (int j = j0; j < j0 + BLOCK; ++j)  // (16 products on: 8 columns of A, 32 bytes of B, tiles of 64)
@@ -290,64 +306,79 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
                                     idesc, j > j0 ? 1u : 0u);
                 if (j0 + BLOCK >= steps) umma_commit(smem_u32(done));
             }
+            issued = true;
             free = __all_sync(0xffffffffu, is_free);
             if (j0 + BLOCK >= STEPS) ready = __all_sync(0xffffffffu, a_in && x_in);
         }
     }
-    if (!ok && i > 1) {
-        if (elect_one_sync()) umma_commit(smem_u32(&ctl->drain));
+    if (!ok && issued) {
+        if (elect_one_sync()) umma_commit(smem_u32(&ctl->drain[mine]));
         __syncwarp();
-        w.wait_drain(smem_u32(&ctl->drain), 0, kDrainNs);
+        w.wait_drain(smem_u32(&ctl->drain[mine]), 0, kDrainNs);
     }
 }
 
-// This thread's column's sums over the CTA's groups.
+// This thread's column's sums over the CTA's groups, of 32 of the rows.
 template <class Cfg, bool BF16>
-__device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r,
-                          int64_t n, int warp, int lane, float (&sum)[Cfg::MP])
+__device__ void wide_sums(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r,
+                          int64_t n, int warp, int lane, float (&sum)[Cfg::SUMS])
 {
 #pragma unroll
-    for (int m = 0; m < Cfg::MP; ++m) sum[m] = 0.0f;
+    for (int m = 0; m < Cfg::SUMS; ++m) sum[m] = 0.0f;
     const int64_t k0 = kStageK * static_cast<int64_t>(r.lo), k1 = kStageK * static_cast<int64_t>(r.hi);
     const int64_t rows = (k1 < p.K ? k1 : p.K) - k0;
     const int groups = rows > 0 ? static_cast<int>((rows + p.group - 1) / p.group) : 0;
     const int each = kStageK / p.group;  // groups of a stage
-    const uint16_t *scale = p.S + k0 / p.group * p.n4 + (n < p.n4 ? n : 0);
     Ring<Cfg::STAGES> slot;
     Ring<Cfg::D_BUFS> d;
-    // A stage's scales are loaded while the stage before is summed, and waited
-    // for before the next ones are asked for: a load in flight would hold up the
-    // use of the ones before it.
-    uint16_t next[kStageK / 32];
-    const auto fetch = [&](int g0) {
-#pragma unroll
-        for (int u = 0; u < kStageK / 32; ++u) next[u] = u < each && g0 + u < groups ? scale[(g0 + u) * p.n4] : 0;
+    const int part = (warp - Cfg::SUM_WARP0) >> 2;
+    const uint32_t at0 = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + Cfg::D_COL0 + Cfg::SUMS * part;
+    // Scales come by a ring of the warpgroup's own, some stages ahead: a warp
+    // copies a group's, four columns a lane.  (Loaded into registers a stage
+    // ahead they were the bound: a load takes about two stages.)
+    const uint32_t ring = sbase + Cfg::SCALE_OFF + part * (Cfg::SCALE_STAGES * Cfg::SCALE_STAGE_BYTES);
+    const int64_t col = n - (threadIdx.x & 127) + 4 * lane;
+    const int mine = warp & 3;
+    const uint16_t *scale = p.S + (k0 / p.group + mine) * p.n4 + (col < p.n4 ? col : 0);
+    const auto fetch = [&](int stage) {
+        const bool on = mine < each && stage * each + mine < groups && col < p.n4;
+        const uint32_t to = ring + stage % Cfg::SCALE_STAGES * Cfg::SCALE_STAGE_BYTES + 256 * mine + 8 * lane;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to),
+                     "l"(on ? scale + static_cast<int64_t>(stage) * each * p.n4 : p.S), "r"(on ? 8u : 0u)
+                     : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(0);
-    for (int g0 = 0; g0 < groups; g0 += each, slot.next()) {
+    for (int g = 0; g < Cfg::SCALE_AHEAD; ++g) fetch(g);
+    int stage = 0;
+    bool ok = true;
+    for (int g0 = 0; g0 < groups; g0 += each, ++stage, slot.next()) {
+        fetch(stage + Cfg::SCALE_AHEAD);
+        asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::SCALE_AHEAD) : "memory");
+        named_barrier_sync(1 + part, 128);
+        const uint32_t from = ring + stage % Cfg::SCALE_STAGES * Cfg::SCALE_STAGE_BYTES + 2 * (threadIdx.x & 127);
         float s[kStageK / 32];
 #pragma unroll
-        for (int u = 0; u < kStageK / 32; ++u) s[u] = scale_of<BF16>(next[u]);
-        fetch(g0 + each);
-        // (not filled again before STAGES more, and accumulators do not reach that far)
-        if (!wait_for(w, &ctl->done[slot.at], slot.parity)) return;
+        for (int u = 0; u < kStageK / 32; ++u) s[u] = scale_of<BF16>(ld_shared_u16(from + 256 * u));
+        // (not filled again before STAGES more, and accumulators do not reach that far; a warp that gives up
+        // still comes to the barriers that it shares with others)
+        ok = ok && wait_for(w, &ctl->done[slot.at], slot.parity);
+        if (!ok) continue;
         tc_fence_after_sync();
 #pragma unroll
         for (int u = 0; u < kStageK / 32; ++u) {
             if (u >= each || g0 + u >= groups) break;
-            const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + Cfg::D_COL0 + Cfg::MP * d.at;
-            uint32_t v[2][32];
-            tmem_ld_32x32b_x32(at, v[0]);
-            if constexpr (Cfg::MP == 64) tmem_ld_32x32b_x32(at + 32, v[1]);
+            uint32_t v[Cfg::SUMS];
+            tmem_ld_32x32b_x32(at0 + Cfg::MP * d.at, v);
             tmem_wait_ld();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl->d_empty[d.at]));
             d.next();
 #pragma unroll
-            for (int m = 0; m < Cfg::MP; ++m) sum[m] = fmaf(s[u], __uint_as_float(v[m / 32][m % 32]), sum[m]);
+            for (int m = 0; m < Cfg::SUMS; ++m) sum[m] = fmaf(s[u], __uint_as_float(v[m]), sum[m]);
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <class Cfg, bool BF16>
@@ -366,14 +397,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             mbar_init(smem_u32(&ctl->done[s]), 1);
         }
         for (int a = 0; a < Cfg::A_BUFS; ++a) mbar_init(smem_u32(&ctl->a_full[a]), 4);
-        for (int d = 0; d < Cfg::D_BUFS; ++d) mbar_init(smem_u32(&ctl->d_empty[d]), 4);
-        mbar_init(smem_u32(&ctl->drain), 1);
+        for (int d = 0; d < Cfg::D_BUFS; ++d) mbar_init(smem_u32(&ctl->d_empty[d]), Cfg::SUM_WARPS);
+        for (int i = 0; i < Cfg::MMA_WARPS; ++i) mbar_init(smem_u32(&ctl->drain[i]), 1);
         ctl->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&words);
         tma_prefetch_desc(&rows);
     }
-    if (warp == Cfg::MMA_WARP) {
+    if (warp == Cfg::MMA_WARP0) {
         tmem_alloc(smem_u32(&ctl->tmem_base), 512);
         tmem_relinquish();
     }
@@ -387,31 +418,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x / p.split) * 128;
     const WideRange r = wide_range(p, rank);
-    const int column = static_cast<int>(threadIdx.x) - 32 * Cfg::SUM_WARP0;  // (of the sums' threads)
+    const int column = static_cast<int>(threadIdx.x) & 127;  // of the sums' threads, and the first row of theirs
+    const int row0 = Cfg::SUMS * ((warp - Cfg::SUM_WARP0) >> 2);
     const bool sums = warp >= Cfg::SUM_WARP0 && warp < Cfg::UNPACK_WARP0;
     const int64_t n = col0 + column;
-    float sum[Cfg::MP];
+    float sum[Cfg::SUMS];
     if (warp == Cfg::PRODUCER_WARP) {
         wide_producer<Cfg>(p, &words, &rows, sbase, ctl, w, r, static_cast<int>(col0));
-    } else if (warp == Cfg::MMA_WARP) {
-        if (p.group == 32) wide_mma<Cfg, BF16, 2>(p, sbase, tmem, ctl, w, r);
-        else if (p.group == 64) wide_mma<Cfg, BF16, 4>(p, sbase, tmem, ctl, w, r);
-        else wide_mma<Cfg, BF16, 8>(p, sbase, tmem, ctl, w, r);
+    } else if (warp < Cfg::SUM_WARP0) {
+        const int mine = warp - Cfg::MMA_WARP0;
+        if (mine >= Cfg::MMA_WARPS) {
+        } else if (p.group == 32) wide_mma<Cfg, BF16, 2>(p, sbase, tmem, ctl, w, r, mine);
+        else if (p.group == 64) wide_mma<Cfg, BF16, 4>(p, sbase, tmem, ctl, w, r, mine);
+        else wide_mma<Cfg, BF16, 8>(p, sbase, tmem, ctl, w, r, mine);
     } else if (warp >= Cfg::UNPACK_WARP0) {
         wide_unpack<Cfg, BF16>(sbase, tmem, ctl, w, r, warp, lane);
     } else if (sums) {
-        wide_sums<Cfg, BF16>(p, tmem, ctl, w, r, n, warp, lane, sum);
+        wide_sums<Cfg, BF16>(p, sbase, tmem, ctl, w, r, n, warp, lane, sum);
         if (p.split == 1) {
             if (n < p.N)
 #pragma unroll
-                for (int m = 0; m < Cfg::MP; ++m)
-                    if (m < p.M) p.Y[m * p.ldy + n] = round_of<BF16>(sum[m]);
+                for (int m = 0; m < Cfg::SUMS; ++m)
+                    if (row0 + m < p.M) p.Y[(row0 + m) * p.ldy + n] = round_of<BF16>(sum[m]);
         }
     }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == Cfg::MMA_WARP) {
+    if (warp == Cfg::MMA_WARP0) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
@@ -420,11 +454,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     float *mine = reinterpret_cast<float *>(wide_smem + pad);
     if (sums)
 #pragma unroll
-        for (int m = 0; m < Cfg::MP; ++m)
-            if (m < p.M) mine[m * 128 + column] = sum[m];
+        for (int m = 0; m < Cfg::SUMS; ++m)
+            if (row0 + m < p.M) mine[(row0 + m) * 128 + column] = sum[m];
     cluster_sync();
     if (sums && n < p.N)
-        for (int m = rank; m < p.M; m += p.split) {
+        for (int m = row0 + rank; m < p.M && m < row0 + Cfg::SUMS; m += p.split) {
             float v = 0.0f;
             for (int c = 0; c < p.split; ++c) v += ld_cluster_f32(mapa_shared(sbase + 4 * (m * 128 + column), c));
             p.Y[m * p.ldy + n] = round_of<BF16>(v);
