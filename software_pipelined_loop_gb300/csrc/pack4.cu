@@ -57,23 +57,44 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i)
     return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
-// The nearest whole number to v / s, ties to even, as a float: the quotient is
-// v * inv corrected by its exact remainder.  Quotients of two 16-bit values are
-// either exactly between two whole numbers, which the correction restores, or
-// further from there than any error here.
-__device__ __forceinline__ float whole(float v, float s, float inv)
+// Larger of two pairs of 16-bit numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
-    const float t = v * inv;
-    const float q = fmaf(fmaf(-t, s, v), inv, t);
-    return fminf(fmaxf(rintf(q), -8.0f), 7.0f);
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-// grid: x = 64 columns, y and z = 128 rows of an expert.
+constexpr float kRound = 12582912.0f;            // 1.5 * 2^23: a sum with it ends in the nearest whole number
+constexpr uint32_t kRoundBits = 0x4b400000u;
+
+// The word of a column's eight values x (scale s > 0, inv = 1 / s): whole
+// numbers nearest to x / s, ties to even, plus 8.  The quotient is x * inv,
+// corrected by its exact remainder: quotients of two 16-bit values are either
+// exactly between two whole numbers, which the correction restores, or further
+// from there than any error here.  They lie within 7.02 unless the scale has
+// lost bits (CLAMP).  The whole number comes out of the last bits of a sum with
+// kRound, and the eight are put together modulo 2^32, constants and all.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t word_from(const float (&x)[8], float s, float inv)
+{
+    uint32_t word = 0u - (kRoundBits - 8u) * 0x11111111u;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const float t = x[r] * inv;
+        float q = fmaf(fmaf(-t, s, x[r]), inv, t);
+        if (CLAMP) q = fminf(fmaxf(q, -8.0f), 7.0f);
+        word += __float_as_uint(q + kRound) << (4 * ((r >> 1) + 4 * (r & 1)));
+    }
+    return word;
+}
+
+// grid: x = 64 columns, y = 128 rows of an expert.
 template <bool BF16, bool ANY>
 __global__ void __launch_bounds__(kThreads) pack4_kernel(int64_t K, int64_t N, int group, int64_t row_tiles,
                                                          int64_t tiles, const uint16_t *W, uint32_t *Q, uint16_t *S)
 {
-    __shared__ float tops[4][64];
+    __shared__ uint32_t tops[4][32];
     const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group, words = (K + 7) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = lane >> 3;
     const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + 8 * (lane & 7);
@@ -85,53 +106,62 @@ __global__ void __launch_bounds__(kThreads) pack4_kernel(int64_t K, int64_t N, i
         uint4 v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) v[r] = load8<ANY>(W + (e * K + k0 + r) * N + n, r < rows ? cols : 0);
-        // Largest magnitude of each column; an infinity or NaN makes it infinite.
-        float top[8];
+        // Largest magnitude of each column, by its bits: they are in the order
+        // of the values, those that are not finite above all others.
+        uint32_t top[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            // Bits of a magnitude are in the order of its value, those that are not finite above all others.
-            uint32_t most = 0;
+        for (int c = 0; c < 4; ++c) {
+            top[c] = word_of(v[0], c) & 0x7fff7fffu;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const uint32_t b = (word_of(v[r], c >> 1) >> (16 * (c & 1))) & 0x7fffu;
-                most = b > most ? b : most;
-            }
-            const uint32_t infinite = BF16 ? 0x7f80u : 0x7c00u;
-            top[c] = most >= infinite ? __int_as_float(0x7f800000) : to_float<BF16>(most);
+            for (int r = 1; r < 8; ++r) top[c] = max_u16x2(top[c], word_of(v[r], c) & 0x7fff7fffu);
 #pragma unroll
-            for (int d = 8; d < 32; d *= 2) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], d));
+            for (int d = 8; d < 32; d *= 2) top[c] = max_u16x2(top[c], __shfl_xor_sync(0xffffffffu, top[c], d));
         }
         if (together > 1) {
             if (block == 0)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) tops[warp][8 * (lane & 7) + c] = top[c];
+                for (int c = 0; c < 4; ++c) tops[warp][4 * (lane & 7) + c] = top[c];
             __syncthreads();
             const int first = warp / together * together;
             for (int w = first; w < first + together; ++w)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) top[c] = fmaxf(top[c], tops[w][8 * (lane & 7) + c]);
+                for (int c = 0; c < 4; ++c) top[c] = max_u16x2(top[c], tops[w][4 * (lane & 7) + c]);
             __syncthreads();
         }
+        constexpr uint32_t kInfinite = BF16 ? 0x7f80u : 0x7c00u, kNan = 0x7fffu, kNormal = BF16 ? 0x0080u : 0x0400u;
         uint32_t bits[8], word[8];
+        bool lost = false;  // scales that are subnormal numbers
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
+            const uint32_t most = c < cols ? (c & 1 ? top[c >> 1] >> 16 : top[c >> 1] & 0xffffu) : 0u;
             // (Past the last column: scale 0, values 0.)
-            const bool finite = top[c] <= 3.402823466e38f;
-            if (c >= cols) top[c] = 0.0f;
-            bits[c] = finite || c >= cols ? to_bits<BF16>(__fdiv_rn(top[c], 7.0f)) : (BF16 ? 0x7fffu : 0x7fffu);
-            const float s = to_float<BF16>(bits[c]);
-            word[c] = 0x88888888u;
-            if (!finite || !(s > 0.0f)) continue;
-            // (the reciprocal of a scale below 2^-126 has no fp32 value)
-            const float lift = BF16 && s < 1e-30f ? 0x1p100f : 1.0f, sl = s * lift, inv = __frcp_rn(sl);
-            word[c] = 0;
+            bits[c] = most >= kInfinite ? kNan : to_bits<BF16>(__fdiv_rn(to_float<BF16>(most), 7.0f));
+            lost |= bits[c] != 0 && bits[c] < kNormal;
+        }
+        lost = __any_sync(0xffffffffu, lost);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            float s = to_float<BF16>(bits[c]), x[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                float x = to_float<BF16>((word_of(v[r], c >> 1) >> (16 * (c & 1))) & 0xffffu);
-                if constexpr (BF16) x *= lift;
-                const int q = static_cast<int>(whole(r < rows ? x : 0.0f, sl, inv)) + 8;
-                word[c] |= static_cast<uint32_t>(q) << (4 * ((r >> 1) + 4 * (r & 1)));
+                const uint32_t two = word_of(v[r], c >> 1);
+                x[r] = BF16 ? __uint_as_float(c & 1 ? two & 0xffff0000u : two << 16) : to_float<BF16>(c & 1 ? two >> 16 : two & 0xffffu);
             }
+            if (rows < 8)  // (off boundaries a row's piece holds other things behind the last one)
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r >= rows) x[r] = 0.0f;
+            if (!lost) {
+                word[c] = word_from<false>(x, s, __frcp_rn(s));
+            } else {
+                // (the reciprocal of a scale below 2^-126 has no fp32 value)
+                const float lift = BF16 && s < 1e-30f ? 0x1p100f : 1.0f;
+                s *= lift;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) x[r] *= lift;
+                word[c] = word_from<true>(x, s, __frcp_rn(s));
+            }
+            if (bits[c] == 0 || bits[c] == kNan) word[c] = 0x88888888u;
         }
         if (rows > 0) {
             uint32_t *q = Q + (e * words + k0 / 8) * n4 + n;
@@ -174,13 +204,14 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
     }
 }
 
-// A row of the warp's 256 columns off 16-byte boundaries: lane's 8 elements o,
-// `left` of the row's columns from its first lane's on.  Each lane stores the
-// whole piece that begins among its elements (the next lane has the rest), and
-// single elements what lies before the first piece and after the last.
-__device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4], int lane, int64_t left)
+// Off 16-byte boundaries a warp has 256 columns of a row and stores the whole
+// aligned pieces that begin in the first 248 of them, each put together from
+// two lanes' elements; the next warp begins with the last eight.  Single
+// elements are stored only at a row's two ends.
+constexpr int kAnyCols = 248;
+
+__device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4], int lane, int64_t first, int64_t N)
 {
-    const int total = left < 256 ? static_cast<int>(left) : 256;
     const int skip = static_cast<int>(((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) / 2);  // 0 .. 7
     uint4 hi;
     hi.x = __shfl_down_sync(0xffffffffu, o[0], 1);
@@ -190,21 +221,19 @@ __device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4],
     uint32_t v[4];
     realign16_steps(make_uint4(o[0], o[1], o[2], o[3]), hi, 2 * skip, v);
     const int at = 8 * lane + skip;
-    if (at + 8 <= total) *reinterpret_cast<uint4 *>(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
-    // Elements before the first piece, of lane 0, by lanes 0 .. 6; those behind
-    // the last piece, of the last lanes with any, by lanes 8 .. 15.
-    const int end = total < skip ? total : skip + (total - skip) / 8 * 8;  // where the pieces end
-    const int i = lane < 8 ? lane : end + lane - 8;
-    const bool on = lane < 8 ? lane < skip && lane < total : lane < 16 && end >= skip && i < total;
-    const int from = on ? i / 8 : 0;
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __shfl_sync(0xffffffffu, o[j], from);
-    const uint32_t x = word_of(make_uint4(w[0], w[1], w[2], w[3]), (i & 7) >> 1);
-    if (on) row[i] = static_cast<uint16_t>(x >> (16 * (i & 1)));
+    const int64_t left = N - first - at;  // columns from this lane's piece on
+    if (lane < 31) {
+        if (left >= 8) {
+            *reinterpret_cast<uint4 *>(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        } else if (left > 0) {
+            for (int i = 0; i < left; ++i) row[at + i] = static_cast<uint16_t>(word_of(make_uint4(v[0], v[1], v[2], v[3]), i >> 1) >> (16 * (i & 1)));
+        }
+    }
+    if (first == 0 && lane == 0)
+        for (int i = 0; i < skip && i < N; ++i) row[i] = static_cast<uint16_t>(word_of(make_uint4(o[0], o[1], o[2], o[3]), i >> 1) >> (16 * (i & 1)));
 }
 
-// grid: x = 256 columns; y = rows of words.  A warp takes a row of words.
+// grid: x = columns of a warp; y = rows of words.  A warp takes a row of words.
 template <bool BF16, bool ANY>
 __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N, int group, int64_t words,
                                                            int64_t all_words, const uint32_t *Q, const uint16_t *S,
@@ -212,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N,
 {
     const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * 256, n = first + 8 * lane;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (ANY ? kAnyCols : 256), n = first + 8 * lane;
     for (int64_t ew = blockIdx.y * static_cast<int64_t>(kThreads / 32) + warp; ew < all_words;
          ew += static_cast<int64_t>(gridDim.y) * (kThreads / 32)) {
         const int64_t e = ew / words, b = ew % words;
@@ -237,8 +266,8 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N,
             }
             if constexpr (ANY) {
                 uint16_t *row = W + (e * K + 8 * b + 2 * i) * N + first;
-                if (2 * i < rows) store_any(row, even, lane, N - first);
-                if (2 * i + 1 < rows) store_any(row + N, odd, lane, N - first);
+                if (2 * i < rows) store_any(row, even, lane, first, N);
+                if (2 * i + 1 < rows) store_any(row + N, odd, lane, first, N);
             } else if (n < N) {
                 if (2 * i < rows) *reinterpret_cast<uint4 *>(w + 2 * i * N) = make_uint4(even[0], even[1], even[2], even[3]);
                 if (2 * i + 1 < rows) *reinterpret_cast<uint4 *>(w + (2 * i + 1) * N) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
@@ -268,8 +297,10 @@ cudaError_t launch_unpack4(bool bf16, int64_t experts, int64_t K, int64_t N, int
                            const uint16_t *S, uint16_t *W, cudaStream_t s)
 {
     const int64_t words = (K + 7) / 8, all = experts * words, rows = (all + kThreads / 32 - 1) / (kThreads / 32);
-    const dim3 grid(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(rows < kMaxY ? rows : kMaxY));
-    const auto kernel = off16(W, N) ? (bf16 ? unpack4_kernel<true, true> : unpack4_kernel<false, true>)
+    const bool any = off16(W, N);
+    const dim3 grid(static_cast<unsigned>(any ? N / 8 / (kAnyCols / 8) + 1 : (N + 255) / 256),
+                    static_cast<unsigned>(rows < kMaxY ? rows : kMaxY));
+    const auto kernel = any ? (bf16 ? unpack4_kernel<true, true> : unpack4_kernel<false, true>)
                                     : (bf16 ? unpack4_kernel<true, false> : unpack4_kernel<false, false>);
     kernel<<<grid, kThreads, 0, s>>>(K, N, group, words, all, Q, S, W);
     return cudaGetLastError();
