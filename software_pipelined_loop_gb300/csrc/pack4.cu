@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t word_from(const float (&x)[8], float s, floa
 
 // grid: x = 64 columns, y = 128 rows of an expert.
 template <bool BF16, bool ANY>
-__global__ void __launch_bounds__(kThreads) pack4_kernel(int64_t K, int64_t N, int group, int64_t row_tiles,
+__global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N, int group, int64_t row_tiles,
                                                          int64_t tiles, const uint16_t *W, uint32_t *Q, uint16_t *S)
 {
     __shared__ uint32_t tops[4][32];
@@ -141,28 +141,35 @@ __global__ void __launch_bounds__(kThreads) pack4_kernel(int64_t K, int64_t N, i
         lost = __any_sync(0xffffffffu, lost);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            float s = to_float<BF16>(bits[c]), x[8];
+            const float s = to_float<BF16>(bits[c]);
+            float x[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const uint32_t two = word_of(v[r], c >> 1);
                 x[r] = BF16 ? __uint_as_float(c & 1 ? two & 0xffff0000u : two << 16) : to_float<BF16>(c & 1 ? two >> 16 : two & 0xffffu);
             }
-            if (rows < 8)  // (off boundaries a row's piece holds other things behind the last one)
+            word[c] = word_from<false>(x, s, __frcp_rn(s));
+        }
+        if (lost) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t b = 0;
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r >= rows) x[r] = 0.0f;
-            if (!lost) {
-                word[c] = word_from<false>(x, s, __frcp_rn(s));
-            } else {
+                for (int i = 0; i < 8; ++i) b = i == c ? bits[i] : b;
                 // (the reciprocal of a scale below 2^-126 has no fp32 value)
-                const float lift = BF16 && s < 1e-30f ? 0x1p100f : 1.0f;
+                float s = to_float<BF16>(b), x[8];
+                const float lift = s < 1e-30f ? 0x1p100f : 1.0f;
                 s *= lift;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) x[r] *= lift;
-                word[c] = word_from<true>(x, s, __frcp_rn(s));
+                for (int r = 0; r < 8; ++r) x[r] = to_float<BF16>((word_of(v[r], c >> 1) >> (16 * (c & 1))) & 0xffffu) * lift;
+                const uint32_t w = word_from<true>(x, s, __frcp_rn(s));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) word[i] = i == c ? w : word[i];
             }
-            if (bits[c] == 0 || bits[c] == kNan) word[c] = 0x88888888u;
         }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (bits[c] == 0 || bits[c] == kNan) word[c] = 0x88888888u;
         if (rows > 0) {
             uint32_t *q = Q + (e * words + k0 / 8) * n4 + n;
             if (n < n4) *reinterpret_cast<uint4 *>(q) = make_uint4(word[0], word[1], word[2], word[3]);
@@ -204,14 +211,13 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
     }
 }
 
-// Off 16-byte boundaries a warp has 256 columns of a row and stores the whole
-// aligned pieces that begin in the first 248 of them, each put together from
-// two lanes' elements; the next warp begins with the last eight.  Single
-// elements are stored only at a row's two ends.
-constexpr int kAnyCols = 248;
-
-__device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4], int lane, int64_t first, int64_t N)
+// A row of the warp's 256 columns off 16-byte boundaries: lane's 8 elements o,
+// `left` of the row's columns from its first lane's on.  Each lane stores the
+// whole piece that begins among its elements (the next lane has the rest), and
+// single elements what lies before the first piece and after the last.
+__device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4], int lane, int64_t left)
 {
+    const int total = left < 256 ? static_cast<int>(left) : 256;
     const int skip = static_cast<int>(((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) / 2);  // 0 .. 7
     uint4 hi;
     hi.x = __shfl_down_sync(0xffffffffu, o[0], 1);
@@ -221,19 +227,21 @@ __device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4],
     uint32_t v[4];
     realign16_steps(make_uint4(o[0], o[1], o[2], o[3]), hi, 2 * skip, v);
     const int at = 8 * lane + skip;
-    const int64_t left = N - first - at;  // columns from this lane's piece on
-    if (lane < 31) {
-        if (left >= 8) {
-            *reinterpret_cast<uint4 *>(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
-        } else if (left > 0) {
-            for (int i = 0; i < left; ++i) row[at + i] = static_cast<uint16_t>(word_of(make_uint4(v[0], v[1], v[2], v[3]), i >> 1) >> (16 * (i & 1)));
-        }
-    }
-    if (first == 0 && lane == 0)
-        for (int i = 0; i < skip && i < N; ++i) row[i] = static_cast<uint16_t>(word_of(make_uint4(o[0], o[1], o[2], o[3]), i >> 1) >> (16 * (i & 1)));
+    if (at + 8 <= total) *reinterpret_cast<uint4 *>(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    // Elements before the first piece, of lane 0, by lanes 0 .. 6; those behind
+    // the last piece, of the last lanes with any, by lanes 8 .. 15.
+    const int end = total < skip ? total : skip + (total - skip) / 8 * 8;  // where the pieces end
+    const int i = lane < 8 ? lane : end + lane - 8;
+    const bool on = lane < 8 ? lane < skip && lane < total : lane < 16 && end >= skip && i < total;
+    const int from = on ? i / 8 : 0;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __shfl_sync(0xffffffffu, o[j], from);
+    const uint32_t x = word_of(make_uint4(w[0], w[1], w[2], w[3]), (i & 7) >> 1);
+    if (on) row[i] = static_cast<uint16_t>(x >> (16 * (i & 1)));
 }
 
-// grid: x = columns of a warp; y = rows of words.  A warp takes a row of words.
+// grid: x = 256 columns; y = rows of words.  A warp takes a row of words.
 template <bool BF16, bool ANY>
 __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N, int group, int64_t words,
                                                            int64_t all_words, const uint32_t *Q, const uint16_t *S,
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N,
 {
     const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (ANY ? kAnyCols : 256), n = first + 8 * lane;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 256, n = first + 8 * lane;
     for (int64_t ew = blockIdx.y * static_cast<int64_t>(kThreads / 32) + warp; ew < all_words;
          ew += static_cast<int64_t>(gridDim.y) * (kThreads / 32)) {
         const int64_t e = ew / words, b = ew % words;
@@ -266,8 +274,8 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N,
             }
             if constexpr (ANY) {
                 uint16_t *row = W + (e * K + 8 * b + 2 * i) * N + first;
-                if (2 * i < rows) store_any(row, even, lane, first, N);
-                if (2 * i + 1 < rows) store_any(row + N, odd, lane, first, N);
+                if (2 * i < rows) store_any(row, even, lane, N - first);
+                if (2 * i + 1 < rows) store_any(row + N, odd, lane, N - first);
             } else if (n < N) {
                 if (2 * i < rows) *reinterpret_cast<uint4 *>(w + 2 * i * N) = make_uint4(even[0], even[1], even[2], even[3]);
                 if (2 * i + 1 < rows) *reinterpret_cast<uint4 *>(w + (2 * i + 1) * N) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
@@ -298,8 +306,7 @@ cudaError_t launch_unpack4(bool bf16, int64_t experts, int64_t K, int64_t N, int
 {
     const int64_t words = (K + 7) / 8, all = experts * words, rows = (all + kThreads / 32 - 1) / (kThreads / 32);
     const bool any = off16(W, N);
-    const dim3 grid(static_cast<unsigned>(any ? N / 8 / (kAnyCols / 8) + 1 : (N + 255) / 256),
-                    static_cast<unsigned>(rows < kMaxY ? rows : kMaxY));
+    const dim3 grid(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(rows < kMaxY ? rows : kMaxY));
     const auto kernel = any ? (bf16 ? unpack4_kernel<true, true> : unpack4_kernel<false, true>)
                                     : (bf16 ? unpack4_kernel<true, false> : unpack4_kernel<false, false>);
     kernel<<<grid, kThreads, 0, s>>>(K, N, group, words, all, Q, S, W);
