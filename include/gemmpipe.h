@@ -420,9 +420,14 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, 
  * As for the operators above: types, sums in fp32, pitches, element
  * alignment of 16-bit rows and matrices, no overlap, asynchronous on `stream`
  * on the current device, results that repeat bit for bit, the errors.  They
- * are inference operators without gradients, use no library workspace and
- * may be recorded by stream capture.  M and T are at most 64; N, K, C and H
- * at most 2^31 - 1024.
+ * are inference operators without gradients and may be recorded by stream
+ * capture.  The expert layer of more than 8 tokens uses the library workspace
+ * (T * top_k rows of C fp32 values), the others do not.  M and T are at most
+ * 64; N, K, C and H at most 2^31 - 1024; an expert layer whose experts with
+ * rows, at most, times its 64-column blocks reach 2^30 is
+ * GEMMPIPE_ERR_INVALID_VALUE.  gemm_rows4 on more than 16 rows of X on 16-byte
+ * boundaries waits for pipeline stages as the products above do
+ * (GEMMPIPE_ERR_TIMEOUT from gemmpipe_get_device_status).
  *
  * A matrix in 4 bits (K x N; E of them densely after one another) is made of
  *   Q: ceil(K / 8) x N4 words, N4 = N rounded up to a multiple of 4, on a
@@ -479,7 +484,9 @@ GEMMPIPE_API gemmpipe_status_t gemmpipe_expert_step4(int type, int64_t T, int64_
 GEMMPIPE_API gemmpipe_status_t gemmpipe_pack4(int type, int64_t E, int64_t K, int64_t N, int64_t group, const void *W,
                                               uint32_t *Q, void *S, gemmpipe_stream_t stream);
 
-/* W = (q - 8) * scale, rounded to the type (off by at most half a step of it). */
+/* W = (q - 8) * scale, rounded to the type (off by at most half a step of it;
+ * infinity where that is past the type's largest value, which 7 times a scale
+ * that was rounded up may be). */
 GEMMPIPE_API gemmpipe_status_t gemmpipe_unpack4(int type, int64_t E, int64_t K, int64_t N, int64_t group,
                                                 const uint32_t *Q, const void *S, void *W, gemmpipe_stream_t stream);
 

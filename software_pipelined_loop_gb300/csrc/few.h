@@ -1,11 +1,13 @@
-// few.h -- launchers of the kernels for a few rows (few_kernel.cuh) and of the
-// weights' way into 4 bits and back (pack4.cu).
+// few.h -- launchers of the kernels for a few rows (few_kernel.cuh,
+// rows4_wide.cu) and of the weights' way into 4 bits and back (pack4.cu).
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+
+#include "gemmpipe.h"
 
 namespace gp {
 
@@ -87,7 +89,7 @@ struct FewLaunch {
     int mode;
     int row_blocks;         // 8-row blocks of an item: 1, 2 or 4
     int grid;               // blocks
-    bool ok;                // sizes that the kernel can count
+    gemmpipe_status_t status;
 };
 
 // four: weights in 4 bits; any: operands off 16-byte boundaries.

@@ -125,10 +125,8 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
             room = at_once;
         }
     }
-    if (p->split == 0) {
-        l.ok = false;
-        return l;
-    }
+    l.status = GEMMPIPE_ERR_LAUNCH;
+    if (p->split == 0) return l;  // (the device did not say)
     // Short sums: a warp takes four steps at least where there are units
     // enough, by sharing its columns with fewer others.
     p->wide = 1;
@@ -136,7 +134,9 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
            4 * gp::kFewWarps > steps * p->wide)
         p->wide *= 2;
     p->columns = static_cast<int>((columns + p->wide - 1) / p->wide);
-    l.ok = static_cast<int64_t>(p->columns) * p->max_items < int64_t(1) << 30;  // (units are counted in 32 bits)
+    // (units are counted in 32 bits)
+    const bool counted = static_cast<int64_t>(p->columns) * p->max_items < int64_t(1) << 30;
+    l.status = counted ? GEMMPIPE_OK : GEMMPIPE_ERR_INVALID_VALUE;
     const int64_t clusters = static_cast<int64_t>(p->columns) * (all ? 1 : items);
     l.grid = static_cast<int>((all || clusters <= 4 * room ? clusters : room) * p->split);
     return l;
@@ -274,7 +274,7 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     }
     const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp);
     const FewLaunch ld = few_launch(&down, bf16, four, down_off, flat ? gp::kFewFlat : gp::kFewParts);
-    if (!lu.ok || !ld.ok) return GEMMPIPE_ERR_INVALID_VALUE;
+    if (lu.status != GEMMPIPE_OK || ld.status != GEMMPIPE_OK) return lu.status != GEMMPIPE_OK ? lu.status : ld.status;
     return gp::api_launch(true, s, flat ? 2 : 3, [&] {
         cudaError_t e = launch(lu, up, s);
         if (e == cudaSuccess) e = launch(ld, down, s);
@@ -327,7 +327,7 @@ gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t 
         p.group_steps = static_cast<int>(group / 32);
         const bool off = misaligned(X, 16) || ldx % 8 || K % 8;
         const FewLaunch l = few_launch(&p, bf16, true, off, gp::kFewUp);
-        if (!l.ok) return GEMMPIPE_ERR_INVALID_VALUE;
+        if (l.status != GEMMPIPE_OK) return l.status;
         return gp::api_launch(true, s, 1, [&] { return launch(l, p, s); });
     });
 }

@@ -1,6 +1,4 @@
 // few_bf16.cu -- the kernels for a few rows, bf16.
-#include <atomic>
-
 #include "few_kernel.cuh"
 
 namespace gp {

@@ -3,31 +3,44 @@
 //
 // out[r][n] = sum over k of X[r][k] * W[k][n], for at most 64 rows.  Every
 // weight is read once and used for few rows, so the kernel is bound by the
-// rate at which weights come from memory; everything else is arranged around
-// loads that never wait for one another:
-//   - a warp takes 64 columns and walks over k in steps of 32.  Its lanes load
-//     16-byte pieces of the matrix straight into registers, a few steps ahead
-//     of the products, without shared memory or barriers in between;
+// rate at which weights come from memory (in 4 bits, by what it takes to make
+// 16-bit values of them); everything else is arranged around that:
+//   - a warp takes 64 columns and walks over k in steps of 32 (4 bits: 64).  It
+//     copies the weights, scales and rows of X of the next steps into a ring of
+//     its own in shared memory, asynchronously, so that no block-wide barrier
+//     stands between loads and products.  (Straight into registers the same
+//     loads allowed half of the bytes in flight: 4 tokens x 8 of 64 experts of
+//     4096 x 1536 took 154 us, 139 with the ring.)  Its loads run ahead into
+//     its next unit of work;
 //   - the products run on warp-level matrix instructions (m16n8k16) with the
 //     weights as the 16-row operand and 8 rows of X as the 8-column operand.
 //     The places of n and k in that operand are free as long as X has the same
-//     order, so a lane's own loads are its operand: with g = lane / 4 and
-//     t = lane % 4 it has rows k = 8t .. 8t + 7 of a step and
+//     order: with g = lane / 4 and t = lane % 4 a lane takes rows k = 8t .. 8t
+//     + 7 of 32 and
 //       16 bits: columns 8g .. 8g + 7 (one 16-byte load a row),
 //       4 bits:  columns 4g .. 4g + 3 and 32 + 4g .. (a word of 8 rows each);
 //     in 16 bits two rows' words are woven into (k, k + 1) pairs by byte
 //     permutes, in 4 bits a word's pairs lie as the instruction wants them;
 //   - X's operand is the 8 values k = 8t .. 8t + 7 of row g: one 16-byte load;
-//   - 4-bit values become v + 1024 (fp16) or v + 128 (bf16) by one mask and or,
-//     exact, then the constant and the 8 are taken off, exact; a step's sum is
-//     multiplied by the columns' scales in fp32, so nothing is rounded before
-//     the end but hidden rows, which are operands of the next product;
+//   - 4-bit values become 1024 + q (fp16) or 128 + q (bf16) by a mask and an or,
+//     exact, then the constant and the 8 are taken off, exact; the sum over a
+//     group's products of a step is multiplied by the columns' scales in fp32,
+//     so nothing is rounded before the end but hidden rows, which are operands
+//     of the next product;
 //   - the 8 warps of a block and the blocks of a cluster share the products;
 //     their sums meet in shared memory, in a fixed order.
+//
+// Measured (GB300, back to back, SM clock about 1.95 GHz): weights in 16 bits
+// 6.0 to 6.6 TB/s where there are some 0.3 ms of them or more, in 4 bits 4.9
+// (bf16) and 5.3 (fp16) TB/s: 165 and 150 instructions of a warp for 32 x 64
+// weights, of which the logic operations that take words apart (7 or 5 for 8
+// weights, at half rate) keep their pipe 62% busy.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "few.h"
 #include "ptx.cuh"
@@ -1001,9 +1014,17 @@ cudaError_t launch_few_kernel(const FewLaunch &l, const FewParams &p, cudaStream
     const int smem = p.table_bytes + 4 * ((p.split > 1 ? p.matrices * few_sent(sent) : 0) + kFewWarps * rows * kFewCols) +
                      kFewWarps * K::DEPTH * K::Stage::BYTES;
     if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(few_kernel<BF16, FOUR, ANY, MB, MODE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    static std::atomic<int> done[128];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    if (!done[dev].load()) {
+        e = cudaFuncSetAttribute(few_kernel<BF16, FOUR, ANY, MB, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxSmem);
+        if (e != cudaSuccess) return e;
+        done[dev].store(1);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(l.grid, 1, 1);
     cfg.blockDim = dim3(32 * kFewWarps, 1, 1);

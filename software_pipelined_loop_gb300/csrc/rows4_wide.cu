@@ -4,7 +4,8 @@
 // Y[m][n] = sum over groups g of s[g][n] * (sum over k of the group of
 // X[m][k] * (q[k][n] - 8)).  With some tens of rows the warp-level matrix
 // instructions of few_kernel.cuh are the bound (1024 products a cycle and SM;
-// 64 rows x 16384 x 4096: 38 us, 28 of them products alone).  Here a CTA takes
+// 64 rows x 16384 x 4096 in groups of 32: 38 us there, 32 here; 64 rows x 4096
+// x 16384 in groups of 128: 54 and 20).  Here a CTA takes
 // 128 columns and a range of k:
 //   - a producer warp fills a ring of stages of 128 k with TMA copies of the
 //     words (16 rows of 128) and of X's rows (128-byte swizzle);
@@ -19,6 +20,13 @@
 //     group's scale: fp32 throughout, one rounding at the end.
 // The CTAs of a cluster share a tile's k; their sums meet in shared memory, in
 // a fixed order.  Every wait is bounded (Waiter).
+//
+// What bounds it: not the products (half of the MMAs left out changes nothing)
+// but what a warp takes to pass a stage on: about 900 cycles a stage of 128 k,
+// 1500 in groups of 32, where four accumulators a stage are handed back and
+// forth.  The same with two warps of MMAs or one (35.9 us in groups of 32), with
+// three warpgroups that unpack (slower by a quarter) or with a barrier for half
+// a stage.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -470,8 +478,16 @@ template <class Cfg, bool BF16>
 cudaError_t launch(const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p, int grid, cudaStream_t s)
 {
     const auto kernel = rows4_wide_kernel<Cfg, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    static std::atomic<int> done[128];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    if (!done[dev].load()) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        done[dev].store(1);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);

@@ -13,7 +13,8 @@ the caller's.  Gradients of the gradients are refused.
 
     python -m software_pipelined_loop_gb300.expert_layer [--tokens N] [--keep8]
 
-runs a training step and a one-token step on the GPU and prints their times.
+runs a training step and one-token steps on the GPU and prints their times; few
+tokens without gradients have calls of their own (few_tokens).
 """
 from __future__ import annotations
 
@@ -209,6 +210,8 @@ def expert_layer(x, ids, weights, w1, w2, keep8: bool = False):
 
 
 def main() -> None:
+    from software_pipelined_loop_gb300.few_tokens import expert_step, pack4
+
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--keep8", action="store_true", help="keep the saved rows in 8 bits")
@@ -248,6 +251,9 @@ def main() -> None:
     one = inputs(1)
     with torch.no_grad():
         print(f"one token: {timed(lambda: expert_layer(*one, w1, w2), 100) * 1e3:.1f} us")
+        print(f"one token, few-token call: {timed(lambda: expert_step(*one, w1, w2), 100) * 1e3:.1f} us")
+        m1, m2 = pack4(w1), pack4(w2)
+        print(f"one token, weights in 4 bits: {timed(lambda: expert_step(*one, m1, m2), 100) * 1e3:.1f} us")
     status = gp.gemmpipe_get_device_status()
     if status != gp.OK:
         raise SystemExit(f"device status {gp.STATUS.get(status, status)}")

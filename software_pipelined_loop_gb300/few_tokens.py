@@ -8,6 +8,9 @@ the whole expert layer for a few tokens with weights in 16 or in 4 bits.
 For generating token by token: at most 64 rows or tokens a call, no gradients
 (expert_layer has them).  Everything is computed in the CUDA library; torch
 supplies memory.  A matrix for many rows is brought back with unpack4.
+
+    m = pack4(w1)                  # once, when the weights are loaded
+    y = expert_step(x, ids, weights, m, pack4(w2))
 """
 from __future__ import annotations
 
