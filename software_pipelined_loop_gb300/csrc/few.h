@@ -9,6 +9,9 @@
 
 #include "gemmpipe.h"
 
+#ifndef W_S64
+#define W_S64 0
+#endif
 namespace gp {
 
 constexpr int kFewRows = 64;       // rows or tokens of a call, at most
@@ -112,7 +115,7 @@ struct WideParams {
     uint16_t *Y;
     int64_t ldy, N, n4, K;
     int M, group;
-    int stages;            // ceil(K / 128)
+    int stages;            // ceil(K / wide_stage_k)
     int split;             // CTAs of a cluster, sharing a tile's k
     int64_t stall_stage;   // test hook: the stage that CTA 0 leaves unfilled (-1: none)
     int *status;
@@ -121,8 +124,11 @@ struct WideParams {
 
 constexpr int kWideCols = 128;  // columns of a tile
 
-// words: rows of 16-bit halves of the words, boxes of 64 x 16; rows: X, boxes of
-// 64 x 64 (more than 32 rows) or 64 x 32.
+// Products of a row in a stage of the ring.
+constexpr int wide_stage_k(int group) { return group <= W_S64 ? 64 : 128; }
+
+// words: rows of 16-bit halves of the words, boxes of 64 x (stage / 8); rows: X,
+// boxes of 64 x 64 (more than 32 rows) or 64 x 32.
 cudaError_t launch_rows4_wide(bool bf16, const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p,
                               int grid, cudaStream_t s);
 

@@ -166,18 +166,19 @@ gemmpipe_status_t rows4_wide(bool bf16, int64_t M, int64_t N, int64_t K, int64_t
     p.K = K;
     p.M = static_cast<int>(M);
     p.group = static_cast<int>(group);
-    p.stages = static_cast<int>((K + 127) / 128);
+    const int stage_k = gp::wide_stage_k(p.group);
+    p.stages = static_cast<int>((K + stage_k - 1) / stage_k);
     const int64_t tiles = (N + gp::kWideCols - 1) / gp::kWideCols;
-    // As many CTAs a tile as run at once, of two stages at least.
+    // As many CTAs a tile as run at once, of 256 products at least.
     p.split = 1;
     for (int split = 2; split <= 8; ++split)
-        if (tiles <= gp::few_room(1, split) && 2 * split <= p.stages) p.split = split;
+        if (tiles <= gp::few_room(1, split) && 256 * (split - 1) < K) p.split = split;
     CUtensorMap words, rows;
     const uint64_t wd[2] = {static_cast<uint64_t>(2 * p.n4), static_cast<uint64_t>((K + 7) / 8)};
     const uint64_t ws[1] = {static_cast<uint64_t>(4 * p.n4)};
     const uint64_t xd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
     const uint64_t xs[1] = {static_cast<uint64_t>(2 * ldx)};
-    const uint32_t wb[2] = {64, 16}, xb[2] = {64, M > 32 ? 64u : 32u};
+    const uint32_t wb[2] = {64, static_cast<uint32_t>(stage_k / 8)}, xb[2] = {64, M > 32 ? 64u : 32u};
     if (!gp::api_encode_16bit(&words, bf16, 2, Q, wd, ws, wb) || !gp::api_encode_16bit(&rows, bf16, 2, X, xd, xs, xb))
         return GEMMPIPE_ERR_INTERNAL;
     p.timeout_ns = 2000000000ull + static_cast<uint64_t>(p.stages) * 10000ull;

@@ -31,28 +31,34 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "few.h"
 #include "gemm_kernel.cuh"
 
+#ifndef W_A32
+#define W_A32 3
+#define W_A64 4
+#define W_A128 5
+#endif
 namespace gp {
 namespace {
 
-constexpr int kStageK = 128;  // products of a row in a stage: a whole number of groups, or one
-
-template <int MP_>
+template <int MP_, int GROUP_>
 struct WideCfg {
-    static constexpr int MP = MP_;                          // rows of X, rounded up: the MMA's columns
-    static constexpr int SUBS = kStageK / 64;               // tiles of 64 products
-    static constexpr int X_BYTES = SUBS * MP * 128, WORD_BOX = kStageK / 8 * 128, WORD_BYTES = 4 * WORD_BOX;
+    static constexpr int MP = MP_, GROUP = GROUP_;          // rows of X, rounded up: the MMA's columns
+    static constexpr int STAGE_K = wide_stage_k(GROUP);     // products of a row in a stage: whole groups
+    static constexpr int EACH = STAGE_K / GROUP;            // accumulators of a stage
+    static constexpr int SUBS = STAGE_K / 64;               // tiles of 64 products
+    static constexpr int X_BYTES = SUBS * MP * 128, WORD_BOX = STAGE_K / 8 * 128, WORD_BYTES = 4 * WORD_BOX;
     static constexpr int STAGE_BYTES = X_BYTES + WORD_BYTES;
-    static constexpr int STAGES = MP == 64 ? 7 : 8;
-    static constexpr int A_BUFS = 3, A_COLS = kStageK / 2;  // tensor memory: a stage's values of 128 columns
-    static constexpr int D_BUFS = MP == 64 ? 5 : 7;         // accumulators of MP columns
+    static constexpr int STAGES = (MP == 64 ? 7 : 8) * 128 / STAGE_K;
+    // Tensor memory: a stage's values of 128 columns, and accumulators of MP columns.
+    static constexpr int A_BUFS = GROUP == 32 ? W_A32 : GROUP == 64 ? W_A64 : W_A128, A_COLS = STAGE_K / 2;
     static constexpr int D_COL0 = A_BUFS * A_COLS;
-    static constexpr int SCALE_STAGES = 8, SCALE_AHEAD = 5;  // ring of scales, of each warpgroup of sums
-    static constexpr int SCALE_STAGE_BYTES = kStageK / 32 * 128 * 2, SCALE_OFF = STAGES * STAGE_BYTES;
-    static constexpr int CTL_OFF = SCALE_OFF + MP / 32 * SCALE_STAGES * SCALE_STAGE_BYTES;
+    static constexpr int D_ROOM = (512 - D_COL0) / MP, D_MOST = EACH * (STAGES - 2), D_BUFS = D_ROOM < D_MOST ? D_ROOM : D_MOST;
+    static constexpr int SCALE_AHEAD = EACH == 4 ? 2 : EACH == 2 ? 3 : 4;  // stages
+    static constexpr int CTL_OFF = STAGES * STAGE_BYTES;
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + 512;
     // Warps: the producer, two that issue MMAs, one idle; four or eight of sums;
     // eight that unpack.
@@ -61,10 +67,9 @@ struct WideCfg {
     static constexpr int UNPACK_WARP0 = SUM_WARP0 + SUM_WARPS, THREADS = 32 * (UNPACK_WARP0 + 8);
 
     static_assert(D_COL0 + D_BUFS * MP <= 512, "tensor memory");
-    static_assert(SCALE_AHEAD + 2 <= SCALE_STAGES, "scales are read before their place is filled again");
-    static_assert(D_BUFS + 1 < STAGES + 1 && A_BUFS < STAGES, "a stage's barrier outlasts its readers");
+    static_assert(D_BUFS / EACH + 1 < STAGES && A_BUFS < STAGES, "a stage's barrier outlasts its readers");
     static_assert(STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448 && SMEM_BYTES > 116 * 1024, "one CTA an SM");
-    static_assert(MP * 128 * 4 <= SCALE_OFF, "sums of the cluster in the ring's place");
+    static_assert(MP * 128 * 4 <= CTL_OFF, "sums of the cluster in the ring's place");
 };
 
 template <class Cfg>
@@ -205,10 +210,10 @@ __device__ void wide_producer(const WideParams &p, const CUtensorMap *words, con
             mbar_arrive_expect_tx(bar, Cfg::STAGE_BYTES);
 #pragma unroll
             for (int c = 0; c < 4; ++c)  // 32 columns of words: 64 16-bit elements
-                tma_load_2d(at + Cfg::X_BYTES + Cfg::WORD_BOX * c, words, bar, 2 * (col0 + 32 * c), kStageK / 8 * i);
+                tma_load_2d(at + Cfg::X_BYTES + Cfg::WORD_BOX * c, words, bar, 2 * (col0 + 32 * c), Cfg::STAGE_K / 8 * i);
 #pragma unroll
             for (int t = 0; t < Cfg::SUBS; ++t)
-                tma_load_2d(at + Cfg::MP * 128 * t, rows, bar, kStageK * i + 64 * t, 0);
+                tma_load_2d(at + Cfg::MP * 128 * t, rows, bar, Cfg::STAGE_K * i + 64 * t, 0);
         }
         __syncwarp();
     }
@@ -256,15 +261,15 @@ __device__ void wide_unpack(uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, co
     }
 }
 
-// BLOCK: MMAs of a group, all in one stage.  Issuing a stage's MMAs and finding
+// Issuing a stage's MMAs and finding
 // the next barriers ready takes a warp longer than anything else takes (8 MMAs
 // 500 to 600 cycles, the rest as much again), so two warps take stages in turn,
 // and the next barriers are looked at while the MMAs go out.
-template <class Cfg, bool BF16, int BLOCK>
+template <class Cfg, bool BF16>
 __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w,
                          const WideRange &r, int mine)
 {
-    constexpr int STEPS = kStageK / 16;
+    constexpr int STEPS = Cfg::STAGE_K / 16, BLOCK = Cfg::GROUP / 16;
     const uint32_t idesc = umma_idesc_16bit_f32(128, Cfg::MP, BF16, false, false);
     const uint64_t b0 = umma_desc_sw128(sbase, 16, 1024);
     Ring<Cfg::STAGES> slot;
@@ -279,11 +284,11 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
         }
     };
     skip(mine);
-    const int64_t rows = p.K - kStageK * static_cast<int64_t>(r.lo);
+    const int64_t rows = p.K - Cfg::STAGE_K * static_cast<int64_t>(r.lo);
     bool ok = true, ready = false, free = false, issued = false;
     for (int i = mine; i < r.hi - r.lo && ok; i += Cfg::MMA_WARPS) {
-        const int64_t left = rows - kStageK * static_cast<int64_t>(i);
-        const int steps = left >= kStageK ? STEPS : static_cast<int>((left + 15) / 16);
+        const int64_t left = rows - Cfg::STAGE_K * static_cast<int64_t>(i);
+        const int steps = left >= Cfg::STAGE_K ? STEPS : static_cast<int>((left + 15) / 16);
         const uint32_t b_lo = static_cast<uint32_t>(b0) + ((slot.at * Cfg::STAGE_BYTES) >> 4);
         const uint32_t a_at = tmem + Cfg::A_COLS * a.at;
         uint64_t *const done = &ctl->done[slot.at];
@@ -328,65 +333,59 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
 
 // This thread's column's sums over the CTA's groups, of 32 of the rows.
 template <class Cfg, bool BF16>
-__device__ void wide_sums(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r,
-                          int64_t n, int warp, int lane, float (&sum)[Cfg::SUMS])
+__device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r, int64_t n,
+                          int warp, int lane, float (&sum)[Cfg::SUMS])
 {
 #pragma unroll
     for (int m = 0; m < Cfg::SUMS; ++m) sum[m] = 0.0f;
-    const int64_t k0 = kStageK * static_cast<int64_t>(r.lo), k1 = kStageK * static_cast<int64_t>(r.hi);
+    const int64_t k0 = Cfg::STAGE_K * static_cast<int64_t>(r.lo), k1 = Cfg::STAGE_K * static_cast<int64_t>(r.hi);
     const int64_t rows = (k1 < p.K ? k1 : p.K) - k0;
-    const int groups = rows > 0 ? static_cast<int>((rows + p.group - 1) / p.group) : 0;
-    const int each = kStageK / p.group;  // groups of a stage
+    const int groups = rows > 0 ? static_cast<int>((rows + Cfg::GROUP - 1) / Cfg::GROUP) : 0;
+    constexpr int EACH = Cfg::EACH;
     Ring<Cfg::STAGES> slot;
     Ring<Cfg::D_BUFS> d;
     const int part = (warp - Cfg::SUM_WARP0) >> 2;
     const uint32_t at0 = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + Cfg::D_COL0 + Cfg::SUMS * part;
-    // Scales come by a ring of the warpgroup's own, some stages ahead: a warp
-    // copies a group's, four columns a lane.  (Loaded into registers a stage
-    // ahead they were the bound: a load takes about two stages.)
-    const uint32_t ring = sbase + Cfg::SCALE_OFF + part * (Cfg::SCALE_STAGES * Cfg::SCALE_STAGE_BYTES);
-    const int64_t col = n - (threadIdx.x & 127) + 4 * lane;
-    const int mine = warp & 3;
-    const uint16_t *scale = p.S + (k0 / p.group + mine) * p.n4 + (col < p.n4 ? col : 0);
-    const auto fetch = [&](int stage) {
-        const bool on = mine < each && stage * each + mine < groups && col < p.n4;
-        const uint32_t to = ring + stage % Cfg::SCALE_STAGES * Cfg::SCALE_STAGE_BYTES + 256 * mine + 8 * lane;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to),
-                     "l"(on ? scale + static_cast<int64_t>(stage) * each * p.n4 : p.S), "r"(on ? 8u : 0u)
-                     : "memory");
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    // This column's scales, AHEAD stages ahead in registers: a load takes a
+    // stage or two, and the loop is short.
+    constexpr int AHEAD = Cfg::SCALE_AHEAD;
+    const uint16_t *scale = p.S + k0 / Cfg::GROUP * p.n4 + (n < p.n4 ? n : 0);
+    uint16_t next[AHEAD][EACH];
+    int loaded = 0;  // groups
+    const auto fetch = [&](uint16_t(&s)[EACH]) {
+#pragma unroll
+        for (int u = 0; u < EACH; ++u, ++loaded, scale += p.n4) s[u] = loaded < groups ? __ldg(scale) : uint16_t(0);
     };
-    for (int g = 0; g < Cfg::SCALE_AHEAD; ++g) fetch(g);
-    int stage = 0;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) fetch(next[a]);
     bool ok = true;
-    for (int g0 = 0; g0 < groups; g0 += each, ++stage, slot.next()) {
-        fetch(stage + Cfg::SCALE_AHEAD);
-        asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::SCALE_AHEAD) : "memory");
-        named_barrier_sync(1 + part, 128);
-        const uint32_t from = ring + stage % Cfg::SCALE_STAGES * Cfg::SCALE_STAGE_BYTES + 2 * (threadIdx.x & 127);
-        float s[kStageK / 32];
+    for (int g0 = 0; ok && g0 < groups;) {
 #pragma unroll
-        for (int u = 0; u < kStageK / 32; ++u) s[u] = scale_of<BF16>(ld_shared_u16(from + 256 * u));
-        // (not filled again before STAGES more, and accumulators do not reach that far; a warp that gives up
-        // still comes to the barriers that it shares with others)
-        ok = ok && wait_for(w, &ctl->done[slot.at], slot.parity);
-        if (!ok) continue;
-        tc_fence_after_sync();
+        for (int a = 0; a < AHEAD; ++a, g0 += EACH, slot.next()) {
+            if (g0 >= groups) break;
+            float s[EACH];
 #pragma unroll
-        for (int u = 0; u < kStageK / 32; ++u) {
-            if (u >= each || g0 + u >= groups) break;
-            uint32_t v[Cfg::SUMS];
-            tmem_ld_32x32b_x32(at0 + Cfg::MP * d.at, v);
-            tmem_wait_ld();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->d_empty[d.at]));
-            d.next();
+            for (int u = 0; u < EACH; ++u) s[u] = scale_of<BF16>(next[a][u]);
+            fetch(next[a]);
+            // (not filled again before STAGES more, and accumulators do not reach that far)
+            ok = wait_for(w, &ctl->done[slot.at], slot.parity);
+            if (!ok) break;
+            tc_fence_after_sync();
 #pragma unroll
-            for (int m = 0; m < Cfg::SUMS; ++m) sum[m] = fmaf(s[u], __uint_as_float(v[m]), sum[m]);
+            for (int u = 0; u < EACH; ++u) {
+                if (g0 + u >= groups) break;
+                uint32_t v[Cfg::SUMS];
+                tmem_ld_32x32b_x32(at0 + Cfg::MP * d.at, v);
+                tmem_wait_ld();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->d_empty[d.at]));
+                d.next();
+#pragma unroll
+                for (int m = 0; m < Cfg::SUMS; ++m) sum[m] = fmaf(s[u], __uint_as_float(v[m]), sum[m]);
+            }
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <class Cfg, bool BF16>
@@ -435,14 +434,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         wide_producer<Cfg>(p, &words, &rows, sbase, ctl, w, r, static_cast<int>(col0));
     } else if (warp < Cfg::SUM_WARP0) {
         const int mine = warp - Cfg::MMA_WARP0;
-        if (mine >= Cfg::MMA_WARPS) {
-        } else if (p.group == 32) wide_mma<Cfg, BF16, 2>(p, sbase, tmem, ctl, w, r, mine);
-        else if (p.group == 64) wide_mma<Cfg, BF16, 4>(p, sbase, tmem, ctl, w, r, mine);
-        else wide_mma<Cfg, BF16, 8>(p, sbase, tmem, ctl, w, r, mine);
+        if (mine < Cfg::MMA_WARPS) wide_mma<Cfg, BF16>(p, sbase, tmem, ctl, w, r, mine);
     } else if (warp >= Cfg::UNPACK_WARP0) {
         wide_unpack<Cfg, BF16>(sbase, tmem, ctl, w, r, warp, lane);
     } else if (sums) {
-        wide_sums<Cfg, BF16>(p, sbase, tmem, ctl, w, r, n, warp, lane, sum);
+        wide_sums<Cfg, BF16>(p, tmem, ctl, w, r, n, warp, lane, sum);
         if (p.split == 1) {
             if (n < p.N)
 #pragma unroll
@@ -511,9 +507,17 @@ cudaError_t launch(const CUtensorMap &words, const CUtensorMap &rows, const Wide
 cudaError_t launch_rows4_wide(bool bf16, const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p,
                               int grid, cudaStream_t s)
 {
-    if (p.M > 32)
-        return bf16 ? launch<WideCfg<64>, true>(words, rows, p, grid, s) : launch<WideCfg<64>, false>(words, rows, p, grid, s);
-    return bf16 ? launch<WideCfg<32>, true>(words, rows, p, grid, s) : launch<WideCfg<32>, false>(words, rows, p, grid, s);
+    const auto of_group = [&](auto group) {
+        constexpr int GROUP = decltype(group)::value;
+        if (p.M > 32)
+            return bf16 ? launch<WideCfg<64, GROUP>, true>(words, rows, p, grid, s)
+                        : launch<WideCfg<64, GROUP>, false>(words, rows, p, grid, s);
+        return bf16 ? launch<WideCfg<32, GROUP>, true>(words, rows, p, grid, s)
+                    : launch<WideCfg<32, GROUP>, false>(words, rows, p, grid, s);
+    };
+    if (p.group == 32) return of_group(std::integral_constant<int, 32>());
+    if (p.group == 64) return of_group(std::integral_constant<int, 64>());
+    return of_group(std::integral_constant<int, 128>());
 }
 
 }  // namespace gp
