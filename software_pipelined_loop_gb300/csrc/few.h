@@ -9,9 +9,6 @@
 
 #include "gemmpipe.h"
 
-#ifndef W_S64
-#define W_S64 0
-#endif
 namespace gp {
 
 constexpr int kFewRows = 64;       // rows or tokens of a call, at most
@@ -111,6 +108,9 @@ cudaError_t launch_few_combine(bool bf16, int tokens, int top_k, int experts, in
 // ---- more than 16 rows times weights in 4 bits (rows4_wide.cu)
 
 struct WideParams {
+    const uint16_t *X;
+    int64_t ldx;
+    const uint32_t *Q;
     const uint16_t *S;
     uint16_t *Y;
     int64_t ldy, N, n4, K;
@@ -125,10 +125,10 @@ struct WideParams {
 constexpr int kWideCols = 128;  // columns of a tile
 
 // Products of a row in a stage of the ring.
-constexpr int wide_stage_k(int group) { return group <= W_S64 ? 64 : 128; }
+constexpr int wide_stage_k(int group) { return group == 32 ? 64 : 128; }
 
-// words: rows of 16-bit halves of the words, boxes of 64 x (stage / 8); rows: X,
-// boxes of 64 x 64 (more than 32 rows) or 64 x 32.
+// words: boxes of 128 x (stage / 8), not swizzled; rows: X, boxes of 64 x 64 (more than 32
+// rows) or 64 x 32.
 cudaError_t launch_rows4_wide(bool bf16, const CUtensorMap &words, const CUtensorMap &rows, const WideParams &p,
                               int grid, cudaStream_t s);
 

@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
@@ -147,6 +148,34 @@ cudaError_t launch(const FewLaunch &l, const FewParams &p, cudaStream_t s)
     return l.bf16 ? gp::launch_few_bf16(l, p, s) : gp::launch_few_f16(l, p, s);
 }
 
+// Tensor map of rows x n4 words, boxes of a stage of 128 columns (one copy: the
+// 128-byte swizzle would take four, and a copy costs its warp 100 cycles).
+bool encode_words(CUtensorMap *m, const uint32_t *Q, int64_t rows, int64_t n4, int group)
+{
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<void *> encode{nullptr};
+    void *f = encode.load();
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess || !f) {
+            cudaGetLastError();
+            return false;
+        }
+        encode.store(f);
+    }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n4), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t pitch[1] = {static_cast<cuuint64_t>(4 * n4)};
+    const cuuint32_t box[2] = {gp::kWideCols, static_cast<cuuint32_t>(gp::wide_stage_k(group) / 8)}, each[2] = {1, 1};
+    return reinterpret_cast<Encode>(f)(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t *>(Q), dims, pitch, box,
+                                       each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // More than 16 aligned rows times 4 bits: tiles of 128 columns on tcgen05.
 bool wide_rows4(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx)
 {
@@ -158,6 +187,9 @@ gemmpipe_status_t rows4_wide(bool bf16, int64_t M, int64_t N, int64_t K, int64_t
 {
     gp::WideParams p;
     std::memset(&p, 0, sizeof(p));
+    p.X = X;
+    p.ldx = ldx;
+    p.Q = Q;
     p.S = S;
     p.Y = Y;
     p.ldy = ldy;
@@ -174,12 +206,10 @@ gemmpipe_status_t rows4_wide(bool bf16, int64_t M, int64_t N, int64_t K, int64_t
     for (int split = 2; split <= 8; ++split)
         if (tiles <= gp::few_room(1, split) && 256 * (split - 1) < K) p.split = split;
     CUtensorMap words, rows;
-    const uint64_t wd[2] = {static_cast<uint64_t>(2 * p.n4), static_cast<uint64_t>((K + 7) / 8)};
-    const uint64_t ws[1] = {static_cast<uint64_t>(4 * p.n4)};
     const uint64_t xd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
     const uint64_t xs[1] = {static_cast<uint64_t>(2 * ldx)};
-    const uint32_t wb[2] = {64, static_cast<uint32_t>(stage_k / 8)}, xb[2] = {64, M > 32 ? 64u : 32u};
-    if (!gp::api_encode_16bit(&words, bf16, 2, Q, wd, ws, wb) || !gp::api_encode_16bit(&rows, bf16, 2, X, xd, xs, xb))
+    const uint32_t xb[2] = {64, M > 32 ? 64u : 32u};
+    if (!encode_words(&words, Q, (K + 7) / 8, p.n4, p.group) || !gp::api_encode_16bit(&rows, bf16, 2, X, xd, xs, xb))
         return GEMMPIPE_ERR_INTERNAL;
     p.timeout_ns = 2000000000ull + static_cast<uint64_t>(p.stages) * 10000ull;
     p.stall_stage = gp::api_take_stall(&p.timeout_ns);

@@ -1,32 +1,38 @@
 // rows4_wide.cu -- more than 16 rows times weights in 4 bits, on the tensor
 // cores' tensor memory.
 //
-// Y[m][n] = sum over groups g of s[g][n] * (sum over k of the group of
-// X[m][k] * (q[k][n] - 8)).  With some tens of rows the warp-level matrix
-// instructions of few_kernel.cuh are the bound (1024 products a cycle and SM;
-// 64 rows x 16384 x 4096 in groups of 32: 38 us there, 32 here; 64 rows x 4096
-// x 16384 in groups of 128: 54 and 20).  Here a CTA takes
+// Y[m][n] = sum over k of X[m][k] * (q[k][n] - 8) * s[k / group][n].  With some
+// tens of rows the warp-level matrix instructions of few_kernel.cuh are the
+// bound (1024 products a cycle and SM; 64 rows x 16384 x 4096 in groups of 32:
+// 38 us there; 64 rows x 4096 x 16384 in groups of 128: 54).  Here a CTA takes
 // 128 columns and a range of k:
-//   - a producer warp fills a ring of stages of 128 k with TMA copies of the
-//     words (16 rows of 128) and of X's rows (128-byte swizzle);
-//   - two warpgroups take stages in turn: a thread has one column, turns its
-//     sixteen words into 128 exact 16-bit values and stores them to tensor memory
-//     -- as operand A of the MMA, whose 128 rows are the columns; so weights
-//     pass neither back through shared memory nor through a rounding;
-//   - an MMA warp issues tcgen05.mma (128 x rows x 16) with X from shared
-//     memory, into one accumulator per group of k;
-//   - one or two more warpgroups read a group's accumulator, a column and 32
-//     rows a thread, and add it to the column's sums in registers, times the
-//     group's scale: fp32 throughout, one rounding at the end.
-// The CTAs of a cluster share a tile's k; their sums meet in shared memory, in
-// a fixed order.  Every wait is bounded (Waiter).
+//   - producer warps fill a ring of stages with TMA copies of the words (rows
+//     of 128) and of X's rows (128-byte swizzle);
+//   - warpgroups take stages in turn: a thread has one column, turns its words
+//     into 16-bit values and stores them to tensor memory -- as operand A of
+//     the MMA, whose 128 rows are the columns; so weights pass not back through
+//     shared memory;
+//   - two MMA warps issue tcgen05.mma (128 x rows x 16) with X from shared
+//     memory, every other stage each.
+// Scales, by size of group:
+//   - 64 and 128: the values are q - 8, exact, and each group of k has an
+//     accumulator; one or two more warpgroups read it, a column and 32 rows a
+//     thread, and add it to sums in registers, times the scale;
+//   - 32: an accumulator handed over costs some 300 cycles, and there would be
+//     four for 128 k.  The values are w = (q - 8) * s, which has at most 4 bits
+//     more than the type holds: it is split into its rounding and the rest,
+//     exactly, and both are multiplied, into one accumulator for all groups.
+//     Infinities, and scales so large that w is past the type's largest value,
+//     do not survive that: a sum that is not finite is made again plainly.
+// fp32 throughout, one rounding at the end.  The CTAs of a cluster share a
+// tile's k; their sums meet in shared memory, in a fixed order.  Every wait is
+// bounded (Waiter).
 //
-// What bounds it: not the products (half of the MMAs left out changes nothing)
-// but what a warp takes to pass a stage on: about 900 cycles a stage of 128 k,
-// 1500 in groups of 32, where four accumulators a stage are handed back and
-// forth.  The same with two warps of MMAs or one (35.9 us in groups of 32), with
-// three warpgroups that unpack (slower by a quarter) or with a barrier for half
-// a stage.
+// What bounds it: tensor memory.  Storing 16 KB of values costs about 100
+// cycles and the MMAs' reading them 128, and a stage passes through four or five
+// kinds of warps in 450 cycles at least, whatever its size.  Split values are
+// twice the bytes: 64 rows x 4096 x 16384 take 17 us in groups of 128, 19 of 64,
+// 22 of 32 (as the others do: 30; the others as this one does: 22).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,50 +42,54 @@
 #include "few.h"
 #include "gemm_kernel.cuh"
 
-#ifndef W_A32
-#define W_A32 3
-#define W_A64 4
-#define W_A128 5
-#endif
 namespace gp {
 namespace {
 
 template <int MP_, int GROUP_>
 struct WideCfg {
     static constexpr int MP = MP_, GROUP = GROUP_;          // rows of X, rounded up: the MMA's columns
-    static constexpr int STAGE_K = wide_stage_k(GROUP);     // products of a row in a stage: whole groups
-    static constexpr int EACH = STAGE_K / GROUP;            // accumulators of a stage
-    static constexpr int SUBS = STAGE_K / 64;               // tiles of 64 products
-    static constexpr int X_BYTES = SUBS * MP * 128, WORD_BOX = STAGE_K / 8 * 128, WORD_BYTES = 4 * WORD_BOX;
+    static constexpr bool SPLIT = GROUP == 32;              // values times scales, in two parts
+    static constexpr int STAGE_K = wide_stage_k(GROUP), SUBS = STAGE_K / 64;
+    static constexpr int EACH = SPLIT ? 0 : STAGE_K / GROUP;  // accumulators of a stage
+    static constexpr int X_BYTES = SUBS * MP * 128, WORD_PITCH = 4 * kWideCols, WORD_BYTES = STAGE_K / 8 * WORD_PITCH;
     static constexpr int STAGE_BYTES = X_BYTES + WORD_BYTES;
-    static constexpr int STAGES = (MP == 64 ? 7 : 8) * 128 / STAGE_K;
-    // Tensor memory: a stage's values of 128 columns, and accumulators of MP columns.
-    static constexpr int A_BUFS = GROUP == 32 ? W_A32 : GROUP == 64 ? W_A64 : W_A128, A_COLS = STAGE_K / 2;
-    static constexpr int D_COL0 = A_BUFS * A_COLS;
-    static constexpr int D_ROOM = (512 - D_COL0) / MP, D_MOST = EACH * (STAGES - 2), D_BUFS = D_ROOM < D_MOST ? D_ROOM : D_MOST;
-    static constexpr int SCALE_AHEAD = EACH == 4 ? 2 : EACH == 2 ? 3 : 4;  // stages
+    static constexpr int STAGES = (MP == 64 ? 6 : 8) * 128 / STAGE_K;
+    // Warps: two producers, two that issue MMAs, warpgroups of sums (without SPLIT), warpgroups that unpack.
+    static constexpr int PRODUCERS = 2, MMA_WARP0 = 2, MMA_WARPS = 2, END_WARP0 = 4;
+    static constexpr int SUMS = 32, END_WARPS = 4 * (MP / SUMS);  // rows that a thread has at the end; warps that have some
+    static constexpr int UNPACK_WARP0 = SPLIT ? END_WARP0 : END_WARP0 + END_WARPS, UNPACK_GROUPS = SPLIT ? 4 : 2;
+    static constexpr int THREADS = 32 * UNPACK_WARP0 + 128 * UNPACK_GROUPS;
+    // Tensor memory: a stage's values (SPLIT: and their rests) of 128 columns, accumulators of MP columns.
+    static constexpr int PART_COLS = STAGE_K / 2, A_COLS = SPLIT ? 2 * PART_COLS : PART_COLS;
+    static constexpr int A_BUFS = SPLIT ? 6 : 4, D_COL0 = A_BUFS * A_COLS;
+    static constexpr int D_ROOM = (512 - D_COL0) / MP, D_MOST = SPLIT ? MMA_WARPS : EACH * (STAGES - 2);
+    static constexpr int D_BUFS = D_ROOM < D_MOST ? D_ROOM : D_MOST;
     static constexpr int CTL_OFF = STAGES * STAGE_BYTES;
     static constexpr int SMEM_BYTES = 1024 + CTL_OFF + 512;
-    // Warps: the producer, two that issue MMAs, one idle; four or eight of sums;
-    // eight that unpack.
-    static constexpr int PRODUCER_WARP = 0, MMA_WARP0 = 1, MMA_WARPS = 2, SUM_WARP0 = 4;
-    static constexpr int SUMS = 32, SUM_WARPS = 4 * (MP / SUMS);  // rows that a thread of sums has
-    static constexpr int UNPACK_WARP0 = SUM_WARP0 + SUM_WARPS, THREADS = 32 * (UNPACK_WARP0 + 8);
 
-    static_assert(D_COL0 + D_BUFS * MP <= 512, "tensor memory");
-    static_assert(D_BUFS / EACH + 1 < STAGES && A_BUFS < STAGES, "a stage's barrier outlasts its readers");
+    static_assert(SPLIT ? D_BUFS == MMA_WARPS : D_BUFS >= 3 && D_BUFS >= EACH, "tensor memory");
+    static_assert(A_BUFS < STAGES && D_BUFS < (SPLIT ? 512 : EACH * STAGES), "a stage's barrier outlasts its readers");
+    // A barrier's phases are told apart by one bit: who waits for a phase has to
+    // know that the one before is over.  So the users of a place in a ring are
+    // the same warps each time round, and the producer of a stage has been
+    // that of the one whose buffer of values it takes.  (Accumulators go round
+    // in the order of the sums, and a warp's last use of one tells enough of
+    // the uses before if there are three.)
+    static_assert(STAGES % PRODUCERS == 0 && STAGES % UNPACK_GROUPS == 0 && STAGES % MMA_WARPS == 0, "phases");
+    static_assert(A_BUFS % MMA_WARPS == 0 && A_BUFS % PRODUCERS == 0, "phases");
     static_assert(STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448 && SMEM_BYTES > 116 * 1024, "one CTA an SM");
-    static_assert(MP * 128 * 4 <= CTL_OFF, "sums of the cluster in the ring's place");
+    static_assert(MP * kWideCols * 4 <= CTL_OFF, "sums of the cluster in the ring's place");
 };
 
 template <class Cfg>
 struct WideCtl {
-    uint64_t full[Cfg::STAGES];    // copies of a stage have landed
-    uint64_t a_full[Cfg::A_BUFS];  // its values are in tensor memory
+    uint64_t full[Cfg::STAGES];     // copies of a stage have landed
+    uint64_t a_full[Cfg::A_BUFS];   // its values are in tensor memory
     // Its products are done: the stage may be filled again, the values' buffer
     // too, and accumulators that end here be read.
     uint64_t done[Cfg::STAGES];
-    uint64_t d_empty[Cfg::D_BUFS];  // an accumulator has been read
+    uint64_t d_empty[Cfg::D_BUFS];  // an accumulator has been read (without SPLIT)
+    uint64_t all_done;              // all products are done (SPLIT)
     uint64_t drain[Cfg::MMA_WARPS];
     uint32_t tmem_base;
     int abort;
@@ -91,12 +101,23 @@ struct Ring {
     int at = 0;
     uint32_t parity = 0;
 
-    __device__ __forceinline__ void next()
+    __device__ __forceinline__ void skip(int n)  // n at most N
     {
-        if (++at == N) {
-            at = 0;
+        at += n;
+        if (at >= N) {
+            at -= N;
             parity ^= 1u;
         }
+    }
+
+    __device__ __forceinline__ Ring back(int n) const  // n below N
+    {
+        Ring r{at - n, parity};
+        if (r.at < 0) {
+            r.at += N;
+            r.parity ^= 1u;
+        }
+        return r;
     }
 };
 
@@ -127,7 +148,7 @@ __device__ __forceinline__ uint16_t round_of(float v)
         return __half_as_ushort(__float2half_rn(v));
 }
 
-// Values i and i + 4 of a word as 16-bit numbers q - 8: rows 2i, 2i + 1.
+// Values i and i + 4 of a word as 16-bit numbers q - 8: rows 2i and 2i + 1.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pair_of(uint32_t word, int i)
 {
@@ -140,6 +161,23 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t word, int i)
         const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1032.0f));
         return *reinterpret_cast<const uint32_t *>(&v);
     }
+}
+
+// A pair times the scale in both halves of `scale`: rounded, and what that is
+// too large by, exactly.
+template <bool BF16>
+__device__ __forceinline__ void split_of(uint32_t pair, uint32_t scale, uint32_t &rounded, uint32_t &over)
+{
+    const uint32_t minus = scale ^ 0x80008000u;
+    const auto split = [&](auto zero) {
+        using T = decltype(zero);
+        const T q = *reinterpret_cast<const T *>(&pair), s = *reinterpret_cast<const T *>(&scale);
+        const T h = __hmul2_rn(q, s), o = __hfma2(q, *reinterpret_cast<const T *>(&minus), h);
+        rounded = *reinterpret_cast<const uint32_t *>(&h);
+        over = *reinterpret_cast<const uint32_t *>(&o);
+    };
+    if constexpr (BF16) split(__nv_bfloat162());
+    else split(__half2());
 }
 
 // 32 columns of this thread's lane of tensor memory.
@@ -193,10 +231,11 @@ __device__ __forceinline__ WideRange wide_range(const WideParams &p, int rank)
 
 template <class Cfg>
 __device__ void wide_producer(const WideParams &p, const CUtensorMap *words, const CUtensorMap *rows, uint32_t sbase,
-                              WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r, int col0)
+                              WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r, int col0, int mine)
 {
     Ring<Cfg::STAGES> slot;
-    for (int i = r.lo; i < r.hi; ++i, slot.next()) {
+    slot.skip(mine);
+    for (int i = r.lo + mine; i < r.hi; i += Cfg::PRODUCERS, slot.skip(Cfg::PRODUCERS)) {
         if (!wait_for(w, &ctl->done[slot.at], slot.parity ^ 1u)) {
             // Copies in flight land before the CTA's shared memory goes.
             const uint64_t t0 = globaltimer_ns();
@@ -208,9 +247,7 @@ __device__ void wide_producer(const WideParams &p, const CUtensorMap *words, con
         if (elect_one_sync()) {
             const uint32_t bar = smem_u32(&ctl->full[slot.at]), at = sbase + slot.at * Cfg::STAGE_BYTES;
             mbar_arrive_expect_tx(bar, Cfg::STAGE_BYTES);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)  // 32 columns of words: 64 16-bit elements
-                tma_load_2d(at + Cfg::X_BYTES + Cfg::WORD_BOX * c, words, bar, 2 * (col0 + 32 * c), Cfg::STAGE_K / 8 * i);
+            tma_load_2d(at + Cfg::X_BYTES, words, bar, col0, Cfg::STAGE_K / 8 * i);
 #pragma unroll
             for (int t = 0; t < Cfg::SUBS; ++t)
                 tma_load_2d(at + Cfg::MP * 128 * t, rows, bar, Cfg::STAGE_K * i + 64 * t, 0);
@@ -219,46 +256,77 @@ __device__ void wide_producer(const WideParams &p, const CUtensorMap *words, con
     }
 }
 
+// The warpgroup's stages of this thread's column.  False: a wait ran out.
 template <class Cfg, bool BF16>
-__device__ void wide_unpack(uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r,
-                            int warp, int lane)
+__device__ bool wide_unpack(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w,
+                            const WideRange &r, int64_t n, int warp, int lane)
 {
+    constexpr int TURNS = Cfg::UNPACK_GROUPS;
     const int q = warp & 3, mine = (warp - Cfg::UNPACK_WARP0) >> 2;  // quarter of the columns, which stages
-    const uint32_t at0 = sbase + Cfg::X_BYTES + Cfg::WORD_BOX * q + 4u * (lane & 3);
-    uint32_t piece[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) piece[b] = 128u * b + (static_cast<uint32_t>((lane >> 2) ^ b) << 4);
-    Ring<Cfg::STAGES> slot, before;  // this stage, and the last one that used its buffer
-    Ring<Cfg::A_BUFS> a;
-    for (int i = 0; i < r.hi - r.lo; ++i, slot.next(), a.next()) {
-        const bool used = i >= Cfg::A_BUFS;
-        if ((i & 1) == mine) {
-            if (!wait_for(w, &ctl->full[slot.at], slot.parity)) return;
-            const uint32_t at = at0 + slot.at * Cfg::STAGE_BYTES;
-            const uint32_t to = tmem + (static_cast<uint32_t>(32 * q) << 16) + Cfg::A_COLS * a.at;
-#pragma unroll
-            for (int t = 0; t < Cfg::SUBS; ++t) {
-                uint32_t v[32];
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    const uint32_t word = ld_shared_b32(at + 1024 * t + piece[b]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[4 * b + j] = pair_of<BF16>(word, j);
-                }
-                if (t == 0 && used) {
-                    // (the products before in this buffer; their barrier is not filled again before this stage is done)
-                    if (!wait_for(w, &ctl->done[before.at], before.parity)) return;
-                    tc_fence_after_sync();
-                }
-                tmem_st_32x32b_x32(to + 32 * t, v);
-            }
-            tmem_wait_st();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->a_full[a.at]));
+    const uint32_t at0 = sbase + Cfg::X_BYTES + 4u * (32 * q + lane);
+    // SPLIT: scales of a stage's first and last 32 rows, loaded a turn ahead, into
+    // two pairs of registers by turns (a move would wait for the load).  Past K
+    // the last one again: x is zero there.
+    const uint16_t *const column = p.S + (n < p.n4 ? n : 0);
+    const int last = static_cast<int>((p.K - 1) / 32);
+    int group = 2 * (r.lo + mine);
+    uint32_t scales[2][2] = {};
+    const auto fetch = [&](uint32_t(&s)[2]) {
+        if constexpr (Cfg::SPLIT) {
+            s[0] = __ldg(column + min(group, last) * p.n4);
+            s[1] = __ldg(column + min(group + 1, last) * p.n4);
+            group += 2 * TURNS;
         }
-        if (used) before.next();
+    };
+    fetch(scales[0]);
+    Ring<Cfg::STAGES> slot;
+    Ring<Cfg::A_BUFS> a;
+    slot.skip(mine);
+    a.skip(mine);
+    const auto unpack = [&](int i, const uint32_t(&scale)[2]) {
+        if (!wait_for(w, &ctl->full[slot.at], slot.parity)) return false;
+        const uint32_t at = at0 + slot.at * Cfg::STAGE_BYTES;
+        const uint32_t to = tmem + (static_cast<uint32_t>(32 * q) << 16) + Cfg::A_COLS * a.at;
+        const uint32_t s0 = scale[0] * 0x10001u, s1 = scale[1] * 0x10001u;
+#pragma unroll
+        for (int t = 0; t < Cfg::SUBS; ++t) {
+            uint32_t v[32], over[32];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const uint32_t word = ld_shared_b32(at + Cfg::WORD_PITCH * (8 * t + b));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t pair = pair_of<BF16>(word, j);
+                    if constexpr (Cfg::SPLIT) split_of<BF16>(pair, b < 4 ? s0 : s1, v[4 * b + j], over[4 * b + j]);
+                    else v[4 * b + j] = pair;
+                }
+            }
+            if (t == 0 && i >= Cfg::A_BUFS) {
+                // (the products before in this buffer; their barrier is not filled again before this stage is done)
+                const Ring<Cfg::STAGES> before = slot.back(Cfg::A_BUFS);
+                if (!wait_for(w, &ctl->done[before.at], before.parity)) return false;
+                tc_fence_after_sync();
+            }
+            tmem_st_32x32b_x32(to + 32 * t, v);
+            if constexpr (Cfg::SPLIT) tmem_st_32x32b_x32(to + Cfg::PART_COLS + 32 * t, over);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->a_full[a.at]));
+        slot.skip(TURNS);
+        a.skip(TURNS);
+        return true;
+    };
+    const int stages = r.hi - r.lo;
+    for (int i = mine; i < stages; i += 2 * TURNS) {
+        fetch(scales[1]);
+        if (!unpack(i, scales[0])) return false;
+        if (i + TURNS >= stages) break;
+        fetch(scales[0]);
+        if (!unpack(i + TURNS, scales[1])) return false;
     }
+    return true;
 }
 
 // Issuing a stage's MMAs and finding
@@ -276,12 +344,9 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
     Ring<Cfg::A_BUFS> a;
     Ring<Cfg::D_BUFS> d;
     const auto skip = [&](int stages) {
-        for (int s = 0; s < stages; ++s) {
-            slot.next();
-            a.next();
-#pragma unroll
-            for (int j = 0; j < STEPS; j += BLOCK) d.next();
-        }
+        slot.skip(stages);
+        a.skip(stages);
+        for (int j = 0; j < stages * Cfg::EACH; ++j) d.skip(1);
     };
     skip(mine);
     const int64_t rows = p.K - Cfg::STAGE_K * static_cast<int64_t>(r.lo);
@@ -300,11 +365,11 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d_at = tmem + Cfg::D_COL0 + Cfg::MP * d.at;
-            d.next();
+            d.skip(1);
             bool a_in = true, x_in = true;
             if (j0 + BLOCK >= STEPS) {
-                slot.next();
-                a.next();
+                slot.skip(1);
+                a.skip(1);
                 skip(Cfg::MMA_WARPS - 1);
                 a_in = mbar_test_wait(smem_u32(&ctl->a_full[a.at]), a.parity);
                 x_in = mbar_test_wait(smem_u32(&ctl->full[slot.at]), slot.parity);
@@ -331,6 +396,52 @@ __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, Wid
     }
 }
 
+// SPLIT: values and rests of all groups into one accumulator of the warp's own
+// (MMAs of different warps are not ordered).  X has landed where the words have,
+// which the warps that unpacked them saw.
+template <class Cfg, bool BF16>
+__device__ void wide_mma_split(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w,
+                         const WideRange &r, int mine)
+{
+    constexpr int STEPS = Cfg::STAGE_K / 16;
+    const uint32_t idesc = umma_idesc_16bit_f32(128, Cfg::MP, BF16, false, false), minus = idesc | 1u << 13;  // A negated
+    const uint64_t b0 = umma_desc_sw128(sbase, 16, 1024);
+    const uint32_t d_at = tmem + Cfg::D_COL0 + Cfg::MP * mine;
+    Ring<Cfg::STAGES> slot;
+    Ring<Cfg::A_BUFS> a;
+    slot.skip(mine);
+    a.skip(mine);
+    const int stages = r.hi - r.lo;
+    bool ok = true, issued = false;
+    for (int i = mine; i < stages; i += Cfg::MMA_WARPS) {
+        const int64_t left = p.K - Cfg::STAGE_K * static_cast<int64_t>(r.lo + i);
+        const int steps = left >= Cfg::STAGE_K ? STEPS : static_cast<int>((left + 15) / 16);
+        const uint32_t b_lo = static_cast<uint32_t>(b0) + ((slot.at * Cfg::STAGE_BYTES) >> 4);
+        const uint32_t a_at = tmem + Cfg::A_COLS * a.at;
+        if (!(ok = wait_for(w, &ctl->a_full[a.at], a.parity))) break;
+        tc_fence_after_sync();
+        if (elect_one_sync()) {
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j)  // (16 products on: 8 columns of A, 32 bytes of B)
+                if (j < steps) {
+                    const uint64_t b = (b0 & 0xffffffff00000000ull) | (b_lo + 2 * j);
+                    umma_f16_ta(d_at, a_at + 8 * j, b, idesc, issued || j > 0 ? 1u : 0u);
+                    umma_f16_ta(d_at, a_at + Cfg::PART_COLS + 8 * j, b, minus, 1u);
+                }
+            umma_commit(smem_u32(&ctl->done[slot.at]));
+            if (i + Cfg::MMA_WARPS >= stages) umma_commit(smem_u32(&ctl->all_done));
+        }
+        issued = true;
+        slot.skip(Cfg::MMA_WARPS);
+        a.skip(Cfg::MMA_WARPS);
+    }
+    if (!ok && issued) {
+        if (elect_one_sync()) umma_commit(smem_u32(&ctl->drain[mine]));
+        __syncwarp();
+        w.wait_drain(smem_u32(&ctl->drain[mine]), 0, kDrainNs);
+    }
+}
+
 // This thread's column's sums over the CTA's groups, of 32 of the rows.
 template <class Cfg, bool BF16>
 __device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w, const WideRange &r, int64_t n,
@@ -344,11 +455,11 @@ __device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl,
     constexpr int EACH = Cfg::EACH;
     Ring<Cfg::STAGES> slot;
     Ring<Cfg::D_BUFS> d;
-    const int part = (warp - Cfg::SUM_WARP0) >> 2;
+    const int part = (warp - Cfg::END_WARP0) >> 2;
     const uint32_t at0 = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + Cfg::D_COL0 + Cfg::SUMS * part;
     // This column's scales, AHEAD stages ahead in registers: a load takes a
     // stage or two, and the loop is short.
-    constexpr int AHEAD = Cfg::SCALE_AHEAD;
+    constexpr int AHEAD = 3;
     const uint16_t *scale = p.S + k0 / Cfg::GROUP * p.n4 + (n < p.n4 ? n : 0);
     uint16_t next[AHEAD][EACH];
     int loaded = 0;  // groups
@@ -361,7 +472,7 @@ __device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl,
     bool ok = true;
     for (int g0 = 0; ok && g0 < groups;) {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a, g0 += EACH, slot.next()) {
+        for (int a = 0; a < AHEAD; ++a, g0 += EACH, slot.skip(1)) {
             if (g0 >= groups) break;
             float s[EACH];
 #pragma unroll
@@ -380,12 +491,30 @@ __device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl,
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctl->d_empty[d.at]));
-                d.next();
+                d.skip(1);
 #pragma unroll
                 for (int m = 0; m < Cfg::SUMS; ++m) sum[m] = fmaf(s[u], __uint_as_float(v[m]), sum[m]);
             }
         }
     }
+}
+
+// Y[m][n], group by group as it is written down.
+template <bool BF16>
+__device__ __noinline__ float wide_plain(const WideParams &p, int m, int64_t n)
+{
+    const uint16_t *x = p.X + m * p.ldx;
+    float sum = 0.0f;
+    for (int64_t k0 = 0; k0 < p.K && !isnan(sum); k0 += p.group) {
+        float part = 0.0f;
+        for (int64_t k = k0; k < k0 + p.group && k < p.K; ++k) {
+            const int row = static_cast<int>(k & 7), place = (row & 1 ? 4 : 0) + (row >> 1);
+            const int q = static_cast<int>(p.Q[(k >> 3) * p.n4 + n] >> (4 * place) & 15u);
+            part = fmaf(scale_of<BF16>(x[k]), static_cast<float>(q - 8), part);
+        }
+        sum = fmaf(scale_of<BF16>(p.S[k0 / p.group * p.n4 + n]), part, sum);
+    }
+    return sum;
 }
 
 template <class Cfg, bool BF16>
@@ -398,13 +527,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     auto *ctl = reinterpret_cast<WideCtl<Cfg> *>(wide_smem + pad + Cfg::CTL_OFF);
     static_assert(sizeof(WideCtl<Cfg>) <= 512, "control block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const WideRange r = wide_range(p, rank);
+    const int stages = r.hi - r.lo, accumulators = stages < Cfg::MMA_WARPS ? stages : Cfg::MMA_WARPS;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::STAGES; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->done[s]), 1);
         }
         for (int a = 0; a < Cfg::A_BUFS; ++a) mbar_init(smem_u32(&ctl->a_full[a]), 4);
-        for (int d = 0; d < Cfg::D_BUFS; ++d) mbar_init(smem_u32(&ctl->d_empty[d]), Cfg::SUM_WARPS);
+        for (int d = 0; d < Cfg::D_BUFS; ++d) mbar_init(smem_u32(&ctl->d_empty[d]), Cfg::END_WARPS);
+        mbar_init(smem_u32(&ctl->all_done), accumulators);
         for (int i = 0; i < Cfg::MMA_WARPS; ++i) mbar_init(smem_u32(&ctl->drain[i]), 1);
         ctl->abort = 0;
         fence_mbar_init();
@@ -422,28 +555,46 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_fence_after_sync();
     const uint32_t tmem = ctl->tmem_base;
     const Waiter w{&ctl->abort, p.status, p.timeout_ns};
-    const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int64_t col0 = static_cast<int64_t>(blockIdx.x / p.split) * 128;
-    const WideRange r = wide_range(p, rank);
-    const int column = static_cast<int>(threadIdx.x) & 127;  // of the sums' threads, and the first row of theirs
-    const int row0 = Cfg::SUMS * ((warp - Cfg::SUM_WARP0) >> 2);
-    const bool sums = warp >= Cfg::SUM_WARP0 && warp < Cfg::UNPACK_WARP0;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x / p.split) * kWideCols;
+    // At the end a warpgroup has SUMS rows, a thread a column of them.
+    const int column = static_cast<int>(threadIdx.x) & 127, row0 = Cfg::SUMS * ((warp - Cfg::END_WARP0) >> 2);
+    const bool ends = warp >= Cfg::END_WARP0 && warp < Cfg::END_WARP0 + Cfg::END_WARPS;
     const int64_t n = col0 + column;
-    float sum[Cfg::SUMS];
-    if (warp == Cfg::PRODUCER_WARP) {
-        wide_producer<Cfg>(p, &words, &rows, sbase, ctl, w, r, static_cast<int>(col0));
-    } else if (warp < Cfg::SUM_WARP0) {
-        const int mine = warp - Cfg::MMA_WARP0;
-        if (mine < Cfg::MMA_WARPS) wide_mma<Cfg, BF16>(p, sbase, tmem, ctl, w, r, mine);
-    } else if (warp >= Cfg::UNPACK_WARP0) {
-        wide_unpack<Cfg, BF16>(sbase, tmem, ctl, w, r, warp, lane);
-    } else if (sums) {
-        wide_sums<Cfg, BF16>(p, tmem, ctl, w, r, n, warp, lane, sum);
-        if (p.split == 1) {
-            if (n < p.N)
+    const auto store = [&](int m, float v) {
+        // (a wait that ran out leaves anything)
+        if (Cfg::SPLIT && !isfinite(v) && ctl->abort == 0) v = wide_plain<BF16>(p, m, n);
+        p.Y[m * p.ldy + n] = round_of<BF16>(v);
+    };
+    float *sums = reinterpret_cast<float *>(wide_smem + pad);  // in the ring's place, once every stage is done
+    if (warp < Cfg::PRODUCERS) {
+        wide_producer<Cfg>(p, &words, &rows, sbase, ctl, w, r, static_cast<int>(col0), warp);
+    } else if (warp < Cfg::END_WARP0) {
+        if constexpr (Cfg::SPLIT) wide_mma_split<Cfg, BF16>(p, sbase, tmem, ctl, w, r, warp - Cfg::MMA_WARP0);
+        else wide_mma<Cfg, BF16>(p, sbase, tmem, ctl, w, r, warp - Cfg::MMA_WARP0);
+    } else {
+        bool ok = true;
+        if (warp >= Cfg::UNPACK_WARP0) ok = wide_unpack<Cfg, BF16>(p, sbase, tmem, ctl, w, r, n, warp, lane);
+        if (ends) {
+            float sum[Cfg::SUMS] = {};
+            if constexpr (!Cfg::SPLIT) {
+                wide_sums<Cfg, BF16>(p, tmem, ctl, w, r, n, warp, lane, sum);
+            } else if (ok && wait_for(w, &ctl->all_done, 0)) {
+                tc_fence_after_sync();
+                const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + Cfg::D_COL0 + row0;
+                for (int d = 0; d < accumulators; ++d) {
+                    uint32_t v[Cfg::SUMS];
+                    tmem_ld_32x32b_x32(at + Cfg::MP * d, v);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int m = 0; m < Cfg::SUMS; ++m)
-                    if (row0 + m < p.M) p.Y[(row0 + m) * p.ldy + n] = round_of<BF16>(sum[m]);
+                    for (int m = 0; m < Cfg::SUMS; ++m) sum[m] += __uint_as_float(v[m]);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < Cfg::SUMS; ++m) {
+                if (row0 + m >= p.M) break;
+                if (p.split > 1) sums[(row0 + m) * kWideCols + column] = sum[m];
+                else if (n < p.N) store(row0 + m, sum[m]);
+            }
         }
     }
     __syncwarp();
@@ -454,18 +605,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         tmem_dealloc(tmem, 512);
     }
     if (p.split == 1) return;
-    // The ring is idle: the CTAs' sums, rows of 128 columns, take its place.
-    float *mine = reinterpret_cast<float *>(wide_smem + pad);
-    if (sums)
-#pragma unroll
-        for (int m = 0; m < Cfg::SUMS; ++m)
-            if (row0 + m < p.M) mine[(row0 + m) * 128 + column] = sum[m];
     cluster_sync();
-    if (sums && n < p.N)
+    if (ends && n < p.N)
         for (int m = row0 + rank; m < p.M && m < row0 + Cfg::SUMS; m += p.split) {
             float v = 0.0f;
-            for (int c = 0; c < p.split; ++c) v += ld_cluster_f32(mapa_shared(sbase + 4 * (m * 128 + column), c));
-            p.Y[m * p.ldy + n] = round_of<BF16>(v);
+            for (int c = 0; c < p.split; ++c) v += ld_cluster_f32(mapa_shared(sbase + 4 * (m * kWideCols + column), c));
+            store(m, v);
         }
     cluster_sync();  // others may still read this CTA's sums
 }
