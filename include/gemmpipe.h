@@ -425,7 +425,7 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, 
  * (T * top_k rows of C fp32 values), the others do not.  M and T are at most
  * 64; N, K, C and H at most 2^31 - 1024; an expert layer whose experts with
  * rows, at most, times its 64-column blocks reach 2^30 is
- * GEMMPIPE_ERR_INVALID_VALUE.  gemm_rows4 on more than 16 rows of X on 16-byte
+ * GEMMPIPE_ERR_INVALID_VALUE.  gemm_rows4 on more than 8 rows of X on 16-byte
  * boundaries waits for pipeline stages as the products above do
  * (GEMMPIPE_ERR_TIMEOUT from gemmpipe_get_device_status).
  *

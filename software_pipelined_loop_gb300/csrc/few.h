@@ -105,7 +105,7 @@ int few_room(int one, int split);
 cudaError_t launch_few_combine(bool bf16, int tokens, int top_k, int experts, int64_t width, const int32_t *ids,
                                const float *parts, uint16_t *Y, int64_t ldy, cudaStream_t s);
 
-// ---- more than 16 rows times weights in 4 bits (rows4_wide.cu)
+// ---- some rows times weights in 4 bits (rows4_wide.cu)
 
 struct WideParams {
     const uint16_t *X;

@@ -176,10 +176,15 @@ bool encode_words(CUtensorMap *m, const uint32_t *Q, int64_t rows, int64_t n4, i
                                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// More than 16 aligned rows times 4 bits: tiles of 128 columns on tcgen05.
-bool wide_rows4(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx)
+// Some aligned rows times 4 bits: tiles of 128 columns on tcgen05.  16 rows in
+// groups of 128 (64, 32): 4096 x 16384 13.8 (15.8, 19.6) us there and 16.6 (16.6,
+// 17.2) as few rows, 16384 x 4096 15.4 (17.3, 20.7) and 18.1 (18.1, 18.9), 2048 x
+// 2048 6.3 (6.7, 6.5) and 7.2 (7.2, 7.4); 8 rows x 4096 x 16384 in groups of 128
+// 13.5 and 12.6; 32 rows in groups of 32 22 and 31.
+bool wide_rows4(int64_t M, int64_t N, int64_t K, int64_t group, const void *X, int64_t ldx)
 {
-    return M > 16 && N <= (int64_t(1) << 29) && K <= (int64_t(1) << 30) && !misaligned(X, 16) && ldx % 8 == 0;
+    return M > (group == 32 ? 16 : 8) && N <= (int64_t(1) << 29) && K <= (int64_t(1) << 30) && !misaligned(X, 16) &&
+           ldx % 8 == 0;
 }
 
 gemmpipe_status_t rows4_wide(bool bf16, int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *X, int64_t ldx,
@@ -338,7 +343,7 @@ gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_t K, int64_t 
         if (K == 0) return zero_rows(Y, M, N, ldy, s);
         if ((st = check_all({{X, 2}, {Q, 16}, {S, 8}})) != GEMMPIPE_OK) return st;
         const bool bf16 = type == GEMMPIPE_BF16;
-        if (wide_rows4(M, N, K, X, ldx))
+        if (wide_rows4(M, N, K, group, X, ldx))
             return rows4_wide(bf16, M, N, K, group, static_cast<const uint16_t *>(X), ldx, Q,
                               static_cast<const uint16_t *>(S), static_cast<uint16_t *>(Y), ldy, s);
         FewParams p;

@@ -1,5 +1,5 @@
-// rows4_wide.cu -- more than 16 rows times weights in 4 bits, on the tensor
-// cores' tensor memory.
+// rows4_wide.cu -- some rows times weights in 4 bits (more than 8, in groups of
+// 32 more than 16), on the tensor cores' tensor memory.
 //
 // Y[m][n] = sum over k of X[m][k] * (q[k][n] - 8) * s[k / group][n].  With some
 // tens of rows the warp-level matrix instructions of few_kernel.cuh are the

@@ -2,6 +2,8 @@
 stages and clusters against exact results, graphs, and its bounded waits."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -112,3 +114,45 @@ def test_a_stage_that_never_comes(k, n, stage):
     gp.gemm_rows4(gp.BF16, 64, n, k, 32, x, k, q, s, y, n)
     assert gp.gemmpipe_get_device_status() == gp.OK
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("m, k, n", [(9, 4096, 300), (16, 136, 130), (12, 2048, 1024), (10, 64, 40), (9, 8, 5)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("type_", TYPES)
+def test_nine_rows_and_more(type_, group, m, k, n):
+    run(type_, m, k, n, group)
+
+
+@pytest.mark.parametrize("m", [20, 64])
+@pytest.mark.parametrize("k", [160, 4096])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("type_", TYPES)
+def test_infinities_and_large_scales(type_, group, k, m):
+    """What is not finite, and scales whose weights are past the type's largest value, give what the formula
+    gives."""
+    n = 200
+    g = generator("large", type_, group, k, m)
+    dtype = TYPES[type_][1]
+    x, steps = ints(g, -2, 2, m, k), ints(g, -8, 7, 1, k, n)
+    scale = torch.exp2(ints(g, -2, 1, 1, -(-k // group), n))
+    top = torch.finfo(dtype).max
+    x[3, 5], x[4, 6], x[5, k - 1], x[5, 0] = math.inf, -math.inf, math.inf, math.inf
+    x[6, 70], x[7] = math.nan, math.nan
+    x[8, 2:] = 0
+    scale[0, 1, 11], scale[0, 0, 12], scale[0, -1, 13] = math.inf, math.nan, -math.inf
+    scale[0, :, 14] = top / 4              # times 7: past the largest value, times 2 ^ -13: not
+    scale[0, :, 15] = -top
+    x[9] *= 2.0 ** -13
+    scale, x = scale.to(dtype).double(), x.to(dtype).double()
+    parts = torch.stack([x[:, a:a + group] @ steps[0, a:a + group] for a in range(0, k, group)])
+    want = (parts.float() * scale[0][:, None].float()).double().sum(0).float().to(dtype)
+    y = torch.empty(m, n, dtype=dtype, device="cuda")
+    gp.gemm_rows4(TYPES[type_][0], m, n, k, group, x.to(dtype), k, words_of(steps), scales_of(scale, n, dtype), y, n)
+    assert gp.gemmpipe_get_device_status() == gp.OK
+    # (whole numbers, in row 9 times 2^-13, with sums below 2^24 of the scales' last bits: exact in fp32; sums of
+    # infinities do not depend on the order)
+    same = (y == want) | (y.isnan() & want.isnan())
+    plain = torch.ones(n, dtype=torch.bool, device="cuda")
+    plain[14:16] = False
+    assert bool(same[:, plain].all())
+    assert bool(same[9].all()) and bool(y[9, 14:16].isfinite().all())
