@@ -421,8 +421,8 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, 
  * alignment of 16-bit rows and matrices, no overlap, asynchronous on `stream`
  * on the current device, results that repeat bit for bit, the errors.  They
  * are inference operators without gradients and may be recorded by stream
- * capture.  The expert layer of more than 8 tokens uses the library workspace
- * (T * top_k rows of C fp32 values), the others do not.  M and T are at most
+ * capture.  The expert layer of more than 12 tokens (in 4 bits: 16) uses the
+ * library workspace (T * top_k rows of C fp32 values), the others do not.  M and T are at most
  * 64; N, K, C and H at most 2^31 - 1024; an expert layer whose experts with
  * rows, at most, times its 64-column blocks reach 2^30 is
  * GEMMPIPE_ERR_INVALID_VALUE.  gemm_rows4 on more than 8 rows of X on 16-byte
@@ -457,8 +457,8 @@ GEMMPIPE_API gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_
  * operand of the second product; nothing else is rounded before Y.
  * hidden: T * top_k rows of H rounded up to a multiple of 8 elements of the
  * type, on a 16-byte boundary, for the kernels' use (calls that may run at the
- * same time need one each).  Two launches, the second of which starts while
- * the first one finishes.
+ * same time need one each).  Two launches, for more than 12 tokens (in 4 bits:
+ * 16) three, each of which starts while the one before it finishes.
  */
 GEMMPIPE_API gemmpipe_status_t gemmpipe_expert_step(int type, int64_t T, int64_t top_k, int64_t E, int64_t C,
                                                     int64_t H, const void *X, int64_t ldx, const int32_t *experts,

@@ -18,7 +18,7 @@ constexpr int kFewWarps = 8;       // warps of a block
 // What a launch computes:
 enum FewMode : int {
     kFewUp = 0,    // rows of X times a matrix, or the tokens' rows times their experts' matrices: hidden rows
-    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (at most 8 tokens)
+    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (at most 16 tokens)
     kFewParts = 2, // the same, one fp32 row for each choice: few_combine adds them
 };
 

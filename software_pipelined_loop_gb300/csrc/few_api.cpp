@@ -297,9 +297,12 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     const bool up_off = rows_off || (!four && (misaligned(m.W[0], 16) || misaligned(m.W[2], 16) || H % 8));
     const bool down_off = !four && (misaligned(m.W[1], 16) || C % 8);
     const bool bf16 = type == GEMMPIPE_BF16;
-    // The second products of up to 8 tokens are summed where they are made;
-    // those of more go by way of the workspace, a row for each choice.
-    const bool flat = T <= 8;
+    // The second products of a few tokens are summed where they are made, as many
+    // as leave room for two blocks on an SM; those of more go by way of the
+    // workspace, a row for each choice.  12 tokens x 4 of 32 experts of 2048 x 1024
+    // 59 us and 67 that way (4 bits: 40 and 47), x 8 of 64 of 4096 x 1536 262 and 268
+    // (134 and 138); 16 tokens 79 and 70 (44 and 50), 296 and 292 (144 and 146).
+    const bool flat = T <= (four ? 16 : 12);
     float *parts = nullptr;
     if (!flat) {
         void *ws = nullptr;

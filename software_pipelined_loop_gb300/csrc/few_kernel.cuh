@@ -1079,6 +1079,8 @@ cudaError_t launch_few_mode(const FewLaunch &l, const FewParams &p, cudaStream_t
     if (l.mode == kFewUp) return launch_few_kernel<BF16, FOUR, ANY, MB, kFewUp>(l, p, s);
     // Hidden rows are always aligned: with weights in 4 bits nothing else can be off.
     constexpr bool any = ANY && !FOUR;
+    if constexpr (MB == 2)
+        if (l.mode == kFewFlat) return launch_few_kernel<BF16, FOUR, any, 2, kFewFlat>(l, p, s);
     if constexpr (MB == 1)
         return launch_few_kernel<BF16, FOUR, any, 1, kFewFlat>(l, p, s);
     else

@@ -143,3 +143,14 @@ def test_choices_written_just_before():
         for y, case in zip(got, cases * 5):
             assert torch.equal(y, case["want"])
     status_ok()
+
+
+@pytest.mark.parametrize("t", [12, 13, 16, 17])
+@pytest.mark.parametrize("k, e, c, h", [(8, 5, 320, 200), (3, 40, 65, 264), (64, 3, 40, 24)])
+@pytest.mark.parametrize("four", [0, 32, 128])
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+def test_tokens_around_the_ways_of_summing(type_, four, k, e, c, h, t):
+    args = step_case(type_, t, k, e, c, h, True, four)
+    y = run_step(type_, args, e, h, four)
+    status_ok()
+    assert torch.equal(y, args["want"])
