@@ -4,10 +4,12 @@
 // magnitude over 7, rounded to the weights' type; a value is w / s, rounded to
 // the nearest whole number (ties to even), held between -8 and 7, plus 8.
 //
-// Both directions are bound by memory: 2 bytes of a weight on one side, half a
-// byte and its share of a scale on the other.  A lane takes 8 neighbouring
-// columns of the 8 rows of a word, 16 bytes of each row, and makes or takes
-// apart its 8 words in registers.
+// A lane takes 8 neighbouring columns of the 8 rows of a word, 16 bytes of each
+// row, and makes or takes apart its 8 words in registers.  Memory (2 bytes of a
+// weight on one side, half a byte and its share of a scale on the other) bounds
+// unpacking; packing and rows off 16-byte boundaries are bound by instructions:
+// places come by shifts and grid dimensions, as a lane has 64 weights only and a
+// division is as long as the work on ten.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,10 +67,26 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
     return d;
 }
 
+// About 1 / s, off by an ulp or two.
+__device__ __forceinline__ float about_inverse(float s)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+
+// m / 7 for a 16-bit value m: the product with about 1 / 7, corrected by its exact
+// remainder.  Rounded to 16 bits it is what the quotient gives (checked for all values).
+__device__ __forceinline__ float seventh(float m)
+{
+    const float t = m * (1.0f / 7.0f);
+    return fmaf(fmaf(-7.0f, t, m), 1.0f / 7.0f, t);
+}
+
 constexpr float kRound = 12582912.0f;            // 1.5 * 2^23: a sum with it ends in the nearest whole number
 constexpr uint32_t kRoundBits = 0x4b400000u;
 
-// The word of a column's eight values x (scale s > 0, inv = 1 / s): whole
+// The word of a column's eight values x (scale s > 0, inv about 1 / s): whole
 // numbers nearest to x / s, ties to even, plus 8.  The quotient is x * inv,
 // corrected by its exact remainder: quotients of two 16-bit values are either
 // exactly between two whole numbers, which the correction restores, or further
@@ -89,19 +107,20 @@ __device__ __forceinline__ uint32_t word_from(const float (&x)[8], float s, floa
     return word;
 }
 
-// grid: x = 64 columns, y = 128 rows of an expert.
+// grid: x = 64 columns, y = 128 rows, z = experts.  Groups of 1 << shift.
 template <bool BF16, bool ANY>
-__global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N, int group, int64_t row_tiles,
-                                                         int64_t tiles, const uint16_t *W, uint32_t *Q, uint16_t *S)
+__global__ void __launch_bounds__(kThreads, 7) pack4_kernel(int64_t K, int64_t N, int shift, int64_t tiles,
+                                                            const uint16_t *W, uint32_t *Q, uint16_t *S)
 {
     __shared__ uint32_t tops[4][32];
-    const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group, words = (K + 7) / 8;
+    const int64_t n4 = (N + 3) / 4 * 4, words = (K + 7) / 8;
+    const int64_t groups = (K + (1 << shift) - 1) >> shift, e = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = lane >> 3;
     const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + 8 * (lane & 7);
     const int cols = n >= N ? 0 : (N - n < 8 ? static_cast<int>(N - n) : 8);
-    const int together = group / 32;  // warps that share a group
+    const int together = 1 << (shift - 5);  // warps that share a group
     for (int64_t tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
-        const int64_t e = tile / row_tiles, k0 = (tile % row_tiles) * 128 + 32 * warp + 8 * block;
+        const int64_t k0 = tile * 128 + 32 * warp + 8 * block;
         const int rows = k0 >= K ? 0 : (K - k0 < 8 ? static_cast<int>(K - k0) : 8);
         uint4 v[8];
 #pragma unroll
@@ -122,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tops[warp][4 * (lane & 7) + c] = top[c];
             __syncthreads();
-            const int first = warp / together * together;
+            const int first = warp & -together;
             for (int w = first; w < first + together; ++w)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) top[c] = max_u16x2(top[c], tops[w][4 * (lane & 7) + c]);
@@ -135,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N
         for (int c = 0; c < 8; ++c) {
             const uint32_t most = c < cols ? (c & 1 ? top[c >> 1] >> 16 : top[c >> 1] & 0xffffu) : 0u;
             // (Past the last column: scale 0, values 0.)
-            bits[c] = most >= kInfinite ? kNan : to_bits<BF16>(__fdiv_rn(to_float<BF16>(most), 7.0f));
+            bits[c] = most >= kInfinite ? kNan : to_bits<BF16>(seventh(to_float<BF16>(most)));
             lost |= bits[c] != 0 && bits[c] < kNormal;
         }
         lost = __any_sync(0xffffffffu, lost);
@@ -148,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N
                 const uint32_t two = word_of(v[r], c >> 1);
                 x[r] = BF16 ? __uint_as_float(c & 1 ? two & 0xffff0000u : two << 16) : to_float<BF16>(c & 1 ? two >> 16 : two & 0xffffu);
             }
-            word[c] = word_from<false>(x, s, __frcp_rn(s));
+            word[c] = word_from<false>(x, s, about_inverse(s));
         }
         if (lost) {
 #pragma unroll 1
@@ -162,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N
                 s *= lift;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) x[r] = to_float<BF16>((word_of(v[r], c >> 1) >> (16 * (c & 1))) & 0xffffu) * lift;
-                const uint32_t w = word_from<true>(x, s, __frcp_rn(s));
+                const uint32_t w = word_from<true>(x, s, about_inverse(s));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) word[i] = i == c ? w : word[i];
             }
@@ -174,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 8) pack4_kernel(int64_t K, int64_t N
             uint32_t *q = Q + (e * words + k0 / 8) * n4 + n;
             if (n < n4) *reinterpret_cast<uint4 *>(q) = make_uint4(word[0], word[1], word[2], word[3]);
             if (n + 4 < n4) *reinterpret_cast<uint4 *>(q + 4) = make_uint4(word[4], word[5], word[6], word[7]);
-            if (k0 % group == 0) {
-                uint16_t *s = S + (e * groups + k0 / group) * n4 + n;
+            if ((k0 & ((1 << shift) - 1)) == 0) {
+                uint16_t *s = S + (e * groups + (k0 >> shift)) * n4 + n;
                 if (n < n4) *reinterpret_cast<uint2 *>(s) = make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
                 if (n + 4 < n4) *reinterpret_cast<uint2 *>(s + 4) = make_uint2(bits[4] | bits[5] << 16, bits[6] | bits[7] << 16);
             }
@@ -241,20 +260,18 @@ __device__ __forceinline__ void store_any(uint16_t *row, const uint32_t (&o)[4],
     if (on) row[i] = static_cast<uint16_t>(x >> (16 * (i & 1)));
 }
 
-// grid: x = 256 columns; y = rows of words.  A warp takes a row of words.
+// grid: x = 256 columns; y = rows of words; z = experts.  A warp takes a row of words.
 template <bool BF16, bool ANY>
-__global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N, int group, int64_t words,
-                                                           int64_t all_words, const uint32_t *Q, const uint16_t *S,
-                                                           uint16_t *W)
+__global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N, int shift, int64_t words,
+                                                           const uint32_t *Q, const uint16_t *S, uint16_t *W)
 {
-    const int64_t n4 = (N + 3) / 4 * 4, groups = (K + group - 1) / group;
+    const int64_t n4 = (N + 3) / 4 * 4, groups = (K + (1 << shift) - 1) >> shift, e = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * 256, n = first + 8 * lane;
-    for (int64_t ew = blockIdx.y * static_cast<int64_t>(kThreads / 32) + warp; ew < all_words;
-         ew += static_cast<int64_t>(gridDim.y) * (kThreads / 32)) {
-        const int64_t e = ew / words, b = ew % words;
-        const uint32_t *q = Q + ew * n4 + n;
-        const uint16_t *s = S + (e * groups + 8 * b / group) * n4 + n;
+    for (int64_t b = blockIdx.y * static_cast<int64_t>(kThreads / 32) + warp; b < words;
+         b += static_cast<int64_t>(gridDim.y) * (kThreads / 32)) {
+        const uint32_t *q = Q + (e * words + b) * n4 + n;
+        const uint16_t *s = S + (e * groups + (8 * b >> shift)) * n4 + n;
         const uint4 qa = ld_global_v4_if(q, n < n4), qb = ld_global_v4_if(q + 4, n + 4 < n4);
         uint2 sa = make_uint2(0, 0), sb = sa;
         if (n < n4) sa = *reinterpret_cast<const uint2 *>(s);
@@ -286,30 +303,35 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(int64_t K, int64_t N,
 
 bool off16(const void *p, int64_t N) { return reinterpret_cast<uintptr_t>(p) % 16 != 0 || N % 8 != 0; }
 
-constexpr int64_t kMaxY = 65535;
+dim3 grid_of(int64_t x, int64_t y, int64_t z)
+{
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y < 65535 ? y : 65535), static_cast<unsigned>(z));
+}
+
+int shift_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 
 }  // namespace
 
 cudaError_t launch_pack4(bool bf16, int64_t experts, int64_t K, int64_t N, int group, const uint16_t *W, uint32_t *Q,
                          uint16_t *S, cudaStream_t s)
 {
-    const int64_t row_tiles = (K + 127) / 128, tiles = experts * row_tiles;
-    const dim3 grid(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>(tiles < kMaxY ? tiles : kMaxY));
+    const int64_t tiles = (K + 127) / 128;
+    const dim3 grid = grid_of((N + 63) / 64, tiles, experts);
     const auto kernel = off16(W, N) ? (bf16 ? pack4_kernel<true, true> : pack4_kernel<false, true>)
                                     : (bf16 ? pack4_kernel<true, false> : pack4_kernel<false, false>);
-    kernel<<<grid, kThreads, 0, s>>>(K, N, group, row_tiles, tiles, W, Q, S);
+    kernel<<<grid, kThreads, 0, s>>>(K, N, shift_of(group), tiles, W, Q, S);
     return cudaGetLastError();
 }
 
 cudaError_t launch_unpack4(bool bf16, int64_t experts, int64_t K, int64_t N, int group, const uint32_t *Q,
                            const uint16_t *S, uint16_t *W, cudaStream_t s)
 {
-    const int64_t words = (K + 7) / 8, all = experts * words, rows = (all + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t words = (K + 7) / 8;
     const bool any = off16(W, N);
-    const dim3 grid(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(rows < kMaxY ? rows : kMaxY));
+    const dim3 grid = grid_of((N + 255) / 256, (words + kThreads / 32 - 1) / (kThreads / 32), experts);
     const auto kernel = any ? (bf16 ? unpack4_kernel<true, true> : unpack4_kernel<false, true>)
                                     : (bf16 ? unpack4_kernel<true, false> : unpack4_kernel<false, false>);
-    kernel<<<grid, kThreads, 0, s>>>(K, N, group, words, all, Q, S, W);
+    kernel<<<grid, kThreads, 0, s>>>(K, N, shift_of(group), words, Q, S, W);
     return cudaGetLastError();
 }
 
