@@ -35,9 +35,11 @@ struct FewParams {
     int64_t ldo;
     int64_t K, N;
     int64_t out_cols;       // columns of out: those past N are set to zero
-    int64_t steps;          // ceil(K / step)
+    int64_t words, groups;  // ceil(K / 8), ceil(K / group) (4 bits)
+    uint32_t steps;         // ceil(K / step): below 2^26
     int tokens, top_k, experts;
     int group_steps;        // group / 32
+    int group_shift;        // log2 of it
     int matrices;           // 2: silu(first product) * second product
     int silu;               // 1: silu of the (first) product
     int max_items;

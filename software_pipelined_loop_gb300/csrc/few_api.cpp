@@ -85,7 +85,10 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
     const int64_t used = !p->ids ? 1 : (slots < p->experts ? slots : p->experts);  // experts with rows, at most
     l.row_blocks = p->tokens <= 8 ? 1 : (p->tokens <= 16 || slots <= 16 * used || (any && !four) ? 2 : 4);
     const int64_t chunk = 8 * l.row_blocks;
-    p->steps = (p->K + (four ? 63 : 31)) / (four ? 64 : 32);
+    p->steps = static_cast<uint32_t>((p->K + (four ? 63 : 31)) / (four ? 64 : 32));
+    p->group_shift = p->group_steps == 4 ? 2 : p->group_steps == 2 ? 1 : 0;
+    p->words = (p->K + 7) / 8;
+    p->groups = (p->K + 32 * p->group_steps - 1) / (32 * p->group_steps);
     int64_t items = (p->tokens + chunk - 1) / chunk;
     p->max_items = static_cast<int>(items);
     p->table_bytes = 0;

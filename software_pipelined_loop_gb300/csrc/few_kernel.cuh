@@ -437,10 +437,8 @@ struct FewKernel {
         const int item = item_of(k.unit);
         const int64_t e = p.ids ? static_cast<int64_t>(t.expert[item]) : 0, n0 = column_of(k.unit);
         if constexpr (FOUR) {
-            const int group_rows = 32 * p.group_steps;
-            const int64_t words = (p.K + 7) / 8, groups = (p.K + group_rows - 1) / group_rows;
-            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * words + 8 * static_cast<int64_t>(k.step) + (lane >> 4)) * n4 + n0 + 4 * (lane & 15));
-            k.s = S + (e * groups + (2 * k.step + (lane >> 4)) / p.group_steps) * n4 + n0 + 4 * (lane & 15);
+            k.w = reinterpret_cast<const char *>(static_cast<const uint32_t *>(W) + (e * p.words + 8 * static_cast<int64_t>(k.step) + (lane >> 4)) * n4 + n0 + 4 * (lane & 15));
+            k.s = S + (e * p.groups + ((2 * k.step + (lane >> 4)) >> p.group_shift)) * n4 + n0 + 4 * (lane & 15);
         } else {
             // (off 16-byte boundaries: the row, not the lane's piece of it)
             k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + (lane >> 3)) * p.N + n0 + (ANY_W ? 0 : 8 * (lane & 7)));
@@ -972,14 +970,20 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
         for (int i = tid & 31; i < slab; i += 32) own[i] = 0.0f;
         __syncwarp();
         const int64_t total = static_cast<int64_t>(items) * p.steps;
-        const int part = rank * kFewWarps + warp, parts = split * kFewWarps;
-        const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
-        const K k(p, t, 0, n0, FewShare{static_cast<int>(lo / p.steps), 1, items, 0, static_cast<int>(p.steps)});
-        k.walk(ring, static_cast<int>(lo % p.steps), hi - lo,
+        const uint32_t part = rank * kFewWarps + warp, parts = split * kFewWarps;
+        // (a 64-bit division is some 200 cycles)
+        const bool small = total < int64_t(1) << 26;
+        const uint32_t total32 = static_cast<uint32_t>(total);
+        const int64_t lo = small ? total32 * part / parts : total * part / parts;
+        const int64_t hi = small ? total32 * (part + 1) / parts : total * (part + 1) / parts;
+        const uint32_t first = small ? static_cast<uint32_t>(lo) / p.steps : static_cast<uint32_t>(lo / p.steps);
+        const uint32_t ahead = static_cast<uint32_t>(lo - static_cast<int64_t>(first) * p.steps);
+        const K k(p, t, 0, n0, FewShare{static_cast<int>(first), 1, items, 0, static_cast<int>(p.steps)});
+        k.walk(ring, static_cast<int>(ahead), hi - lo,
                [&](int item, const float(&acc)[4][MB][4]) { k.add(own, acc, item); });
         join(0, n0, 0, p.tokens, false);
     } else {
-        const int part = rank * each + warp % each, parts = split * each;
+        const uint32_t part = rank * each + warp % each, parts = split * each;  // at most 64
         const int lo = static_cast<int>(p.steps * part / parts), hi = static_cast<int>(p.steps * (part + 1) / parts);
         const int units = items * p.columns;
         const K k(p, t, warp % warps / each, warp / warps * kFewCols, FewShare{cluster, clusters, units, lo, hi});
