@@ -154,3 +154,35 @@ def test_tokens_around_the_ways_of_summing(type_, four, k, e, c, h, t):
     y = run_step(type_, args, e, h, four)
     status_ok()
     assert torch.equal(y, args["want"])
+
+
+@pytest.mark.parametrize("m", [1, 9, 12, 20, 64])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+def test_subnormal_scales(type_, group, m):
+    """Scales below the type's normal numbers are taken as they are, and weights made of them."""
+    k, n = 520, 136
+    g = generator("subnormal", type_, group, m)
+    dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[type_]
+    code = {"f16": gp.F16, "bf16": gp.BF16}[type_]
+    least, lift = (2.0 ** -24, 1.0) if type_ == "f16" else (2.0 ** -133, 2.0 ** 100)
+    x, steps = ints(g, -2, 2, m, k) * lift, ints(g, -8, 7, 1, k, n)
+    scale = ints(g, 0, 100, 1, -(-k // group), n) * least
+    want = (x @ (steps * scale.repeat_interleave(group, 1)[:, :k])[0]).to(dtype)  # exact sums, one rounding
+    y = torch.empty(m, n, dtype=dtype, device="cuda")
+    gp.gemm_rows4(code, m, n, k, group, x.to(dtype), k, words_of(steps), scales_of(scale, n, dtype), y, n)
+    status_ok()
+    assert torch.equal(y, want)
+
+
+def test_subnormal_scales_of_the_step():
+    """The same through the whole layer: fp16 scales of 2^-24 to 2^-18 in the second product."""
+    t, k, e, c, h = 9, 2, 4, 96, 64
+    args = step_case("f16", t, k, e, c, h, True, 32)
+    q2, s2 = args["w2"]
+    args["w2"] = q2, s2 * 2.0 ** -20
+    y = run_step("f16", args, e, h, 32)
+    status_ok()
+    want = args["want"].double() * 2.0 ** -20
+    # (want is rounded once to 11 bits, the result again, to multiples of 2^-24)
+    assert bool(((y.double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -25).all())
