@@ -368,7 +368,7 @@ struct FewShare {
 template <int MB>
 struct FewWalk {
     int unit, step, blocks;
-    int whole;                  // steps of the unit whose loads of the warp are all inside the matrix
+    int whole;                  // steps of the unit whose loads of weights are all inside the matrix
     const char *w;              // this lane's piece of the step's first row (4 bits: of its word row)
     const uint16_t *s;          // this lane's scales of the group
     const uint16_t *x[MB];      // this lane's 8 values of each row
@@ -410,6 +410,9 @@ struct FewKernel {
         }
     }
 
+    // (K, and columns, are below 2^31 - 1023)
+    __device__ __forceinline__ int K32() const { return static_cast<int>(p.K); }
+
     __device__ __forceinline__ int item_of(int unit) const { return FLAT ? unit : unit / p.columns; }
 
     // The warp's first column in a unit.
@@ -443,7 +446,7 @@ struct FewKernel {
             // (off 16-byte boundaries: the row, not the lane's piece of it)
             k.w = reinterpret_cast<const char *>(static_cast<const uint16_t *>(W) + (e * p.K + 32 * static_cast<int64_t>(k.step) + (lane >> 3)) * p.N + n0 + (ANY_W ? 0 : 8 * (lane & 7)));
         }
-        k.whole = !ANY && n0 + kFewCols <= (FOUR ? n4 : p.N) ? static_cast<int>(p.K / Stage::STEP) : 0;
+        k.whole = !ANY_W && n0 + kFewCols <= (FOUR ? n4 : p.N) ? static_cast<int>(p.K / Stage::STEP) : 0;
         const int rows = rows_of(item);
         k.blocks = (rows + 7) / 8;
 #pragma unroll
@@ -494,7 +497,7 @@ struct FewKernel {
                 few_copy8(scales, k.s, 8);
             } else {
                 const bool inside = column_of(k.unit) + 4 * (lane & 15) < n4;
-                const int64_t left = p.K - 64 * static_cast<int64_t>(k.step);
+                const int left = K32() - 64 * k.step;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     few_copy16((to ^ (64u * (i & 1))) + 512 * i, k.w + 8 * i * n4,
@@ -508,7 +511,7 @@ struct FewKernel {
                 for (int i = 0; i < 8; ++i) few_copy16((to ^ (64u * (i & 1)) ^ (32u * (i >> 1))) + 512 * i, k.w + 8 * i * p.N);
             } else {
                 const bool inside = column_of(k.unit) + 8 * (lane & 7) < p.N;
-                const int64_t left = p.K - (32 * static_cast<int64_t>(k.step) + (lane >> 3));
+                const int left = K32() - (32 * k.step + (lane >> 3));
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     few_copy16((to ^ (64u * (i & 1)) ^ (32u * (i >> 1))) + 512 * i, k.w + 8 * i * p.N,
@@ -517,8 +520,8 @@ struct FewKernel {
         } else {
             // A row's 128 bytes lie in up to nine aligned pieces: eight by
             // neighbouring lanes, then the ninth of row `lane`.
-            const int64_t left = p.K - 32 * static_cast<int64_t>(k.step), n_left = p.N - column_of(k.unit);
-            const int bytes = static_cast<int>(n_left < kFewCols ? (n_left > 0 ? 2 * n_left : -16) : 2 * kFewCols);
+            const int left = K32() - 32 * k.step, n_left = static_cast<int>(p.N) - static_cast<int>(column_of(k.unit));
+            const int bytes = n_left < kFewCols ? (n_left > 0 ? 2 * n_left : -16) : 2 * kFewCols;
 #pragma unroll
             for (int i = 0; i < 9; ++i) {
                 const int row = i < 8 ? 4 * i + (lane >> 3) : lane, piece = i < 8 ? lane & 7 : 8;
@@ -535,13 +538,13 @@ struct FewKernel {
     __device__ __forceinline__ void load_x(uint32_t st, const FewWalk<MB> &k) const
     {
         constexpr int HALVES = Stage::STEP / 32;
-        const int64_t left = p.K - Stage::STEP * static_cast<int64_t>(k.step);
+        const int left = K32() - Stage::STEP * k.step;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             if (MB > 1 && m >= k.blocks) break;
             const uint32_t to = st + Stage::X + Stage::X_BLOCK * m + Stage::X_PITCH * g;
             if constexpr (ANY_X) {
-                const int bytes = static_cast<int>(left < Stage::STEP ? 2 * left : 2 * Stage::STEP);
+                const int bytes = left < Stage::STEP ? 2 * left : 2 * Stage::STEP;
                 const char *at = reinterpret_cast<const char *>(k.x[m]);
                 const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u);
 #pragma unroll
@@ -569,8 +572,10 @@ struct FewKernel {
         if constexpr (ANY_X) {
             uint32_t o[4];
             realign16_steps(ld_shared_v4(at + 64 * half), ld_shared_v4(at + 64 * half + 16), off, o);
-            const int64_t left = p.K - (Stage::STEP * static_cast<int64_t>(step) + 32 * half + 8 * l4);
-            return few_first(make_uint4(o[0], o[1], o[2], o[3]), left < 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8));
+            const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+            if (step + 1 < static_cast<int>(p.steps)) return v;
+            const int left = K32() - (Stage::STEP * step + 32 * half + 8 * l4);
+            return few_first(v, left < 0 ? 0 : (left < 8 ? left : 8));
         } else {
             return ld_shared_v4(at + (Stage::STEP > 32 ? 64u * (half ^ (g & 1)) : 0u));
         }
