@@ -522,6 +522,19 @@ struct FewKernel {
             // neighbouring lanes, then the ninth of row `lane`.
             const int left = K32() - 32 * k.step, n_left = static_cast<int>(p.N) - static_cast<int>(column_of(k.unit));
             const int bytes = n_left < kFewCols ? (n_left > 0 ? 2 * n_left : -16) : 2 * kFewCols;
+            if (left > 32 && n_left >= kFewCols) {
+                // Whole rows, and others behind them: all nine pieces may be read.
+                const uint32_t n32 = static_cast<uint32_t>(p.N), to = st + Stage::W_PITCH * (lane >> 3) + 16 * (lane & 7);
+                const uint64_t row = reinterpret_cast<uint64_t>(k.w), piece = row + 16 * (lane & 7);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    few_copy16(to + Stage::W_GROUP * (i >> 1) + 4 * Stage::W_PITCH * (i & 1),
+                               reinterpret_cast<const void *>((piece + static_cast<uint64_t>(n32) * (8u * i)) & ~uint64_t(15)));
+                const uint64_t last = row + static_cast<uint64_t>(n32) * (2u * (lane - (lane >> 3)));
+                few_copy16(st + Stage::W_GROUP * (lane >> 3) + Stage::W_PITCH * (lane & 7) + 128,
+                           reinterpret_cast<const void *>((last & ~uint64_t(15)) + 128));
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < 9; ++i) {
                 const int row = i < 8 ? 4 * i + (lane >> 3) : lane, piece = i < 8 ? lane & 7 : 8;
