@@ -18,20 +18,23 @@ constexpr int kFewWarps = 8;       // warps of a block
 // What a launch computes:
 enum FewMode : int {
     kFewUp = 0,    // rows of X times a matrix, or the tokens' rows times their experts' matrices: hidden rows
-    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (at most 16 tokens)
+    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (9 to 16 tokens)
     kFewParts = 2, // the same, one fp32 row for each choice: few_combine adds them
+    kFewTwo = 3,   // as kFewFlat, hidden rows in two parts (at most 8 tokens)
 };
 
 // One launch.  An item is an expert and up to 8 * blocks of the tokens that
 // chose it, or (`ids` null) so many of `tokens` rows of X.
 struct FewParams {
     const uint16_t *X;      // kFewUp: rows by token; else by slot
+    const uint16_t *X2;     // kFewTwo: what their rounding left
     int64_t ldx;
     const int32_t *ids;     // tokens x top_k
     const float *weights;   // tokens x top_k (not kFewUp)
     const void *W[2];       // matrices experts x K x N (16 bits), or words experts x ceil(K / 8) x N4 (4 bits)
     const uint16_t *S[2];   // scales experts x ceil(K / group) x N4 (4 bits)
     void *out;              // 16 bits; kFewParts: fp32
+    uint16_t *rest;         // kFewUp: what the rounding of out leaves (may be null)
     int64_t ldo;
     int64_t K, N;
     int64_t out_cols;       // columns of out: those past N are set to zero

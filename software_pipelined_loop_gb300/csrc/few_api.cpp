@@ -84,6 +84,7 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
     const int64_t slots = static_cast<int64_t>(p->tokens) * p->top_k;
     const int64_t used = !p->ids ? 1 : (slots < p->experts ? slots : p->experts);  // experts with rows, at most
     l.row_blocks = p->tokens <= 8 ? 1 : (p->tokens <= 16 || slots <= 16 * used || (any && !four) ? 2 : 4);
+    if (mode == gp::kFewTwo) l.row_blocks = p->tokens <= 4 ? 1 : 2;
     const int64_t chunk = 8 * l.row_blocks;
     p->steps = static_cast<uint32_t>((p->K + (four ? 63 : 31)) / (four ? 64 : 32));
     p->group_shift = p->group_steps == 4 ? 2 : p->group_steps == 2 ? 1 : 0;
@@ -103,7 +104,7 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
     // Units of work: 64 columns of an item each (kFewFlat: of all items).  The
     // experts that have rows are not known here: as many as tokens that choose
     // any of them alike would reach.
-    const bool all = mode == gp::kFewFlat;
+    const bool all = mode == gp::kFewFlat || mode == gp::kFewTwo;
     const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols;
     double reached = static_cast<double>(items);
     if (p->ids && p->top_k < p->experts)
@@ -306,16 +307,25 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     // 59 us and 67 that way (4 bits: 40 and 47), x 8 of 64 of 4096 x 1536 262 and 268
     // (134 and 138); 16 tokens 79 and 70 (44 and 50), 296 and 292 (144 and 146).
     const bool flat = T <= (four ? 16 : 12);
-    float *parts = nullptr;
-    if (!flat) {
-        void *ws = nullptr;
-        if ((st = gp::api_workspace(d.dev, s, 4 * T * top_k * C, &ws)) != GEMMPIPE_OK) return st;
-        parts = static_cast<float *>(ws);
+    // Hidden rows of up to 8 tokens keep what their rounding leaves, beside them
+    // in the workspace: it takes rows of the matrix instructions that are empty,
+    // and the error is that of the last rounding (with rounded rows 1.4 times it).
+    const bool two = T <= 8;
+    void *ws = nullptr;
+    if (two || !flat) {
+        const int64_t bytes = two ? 2 * T * top_k * ldh : 4 * T * top_k * C;
+        if ((st = gp::api_workspace(d.dev, s, bytes, &ws)) != GEMMPIPE_OK) return st;
+    }
+    float *parts = static_cast<float *>(ws);
+    if (two) {
+        up.rest = static_cast<uint16_t *>(ws);
+        down.X2 = up.rest;
+    } else if (!flat) {
         down.out = parts;
         down.ldo = C;
     }
     const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp);
-    const FewLaunch ld = few_launch(&down, bf16, four, down_off, flat ? gp::kFewFlat : gp::kFewParts);
+    const FewLaunch ld = few_launch(&down, bf16, four, down_off, two ? gp::kFewTwo : flat ? gp::kFewFlat : gp::kFewParts);
     if (lu.status != GEMMPIPE_OK || ld.status != GEMMPIPE_OK) return lu.status != GEMMPIPE_OK ? lu.status : ld.status;
     return gp::api_launch(true, s, flat ? 2 : 3, [&] {
         cudaError_t e = launch(lu, up, s);

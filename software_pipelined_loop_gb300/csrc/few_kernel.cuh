@@ -25,8 +25,8 @@
 //   - 4-bit values become 1024 + q (fp16) or 128 + q (bf16) by a mask and an or,
 //     exact, then the constant and the 8 are taken off, exact; the sum over a
 //     group's products of a step is multiplied by the columns' scales in fp32,
-//     so nothing is rounded before the end but hidden rows, which are operands
-//     of the next product;
+//     so nothing is rounded before the end but the hidden rows of more than 8
+//     tokens, operands of the next product (of up to 8 the rest is kept, too);
 //   - the 8 warps of a block and the blocks of a cluster share the products;
 //     their sums meet in shared memory, in a fixed order.
 //
@@ -379,7 +379,7 @@ template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 struct FewKernel {
     static constexpr int CHUNK = 8 * MB, DEPTH = few_depth<FOUR, MB>();
     static constexpr bool FIXED = MB > 1;
-    static constexpr bool UP = MODE == kFewUp, FLAT = MODE == kFewFlat;
+    static constexpr bool UP = MODE == kFewUp, TWO = MODE == kFewTwo, FLAT = MODE == kFewFlat || TWO;
     static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && UP;
     using Stage = FewStage<FOUR, ANY_W, ANY_X, MB>;
 
@@ -426,13 +426,19 @@ struct FewKernel {
         return p.ids ? static_cast<int>(t.span[item] >> 16) : min(p.tokens - item * CHUNK, CHUNK);
     }
 
-    // Element 0 of row i of an item, or of its first row where it has no such row.
+    // TWO: an item's row is two of the products', its rounded values and their
+    // rest, which take places that few tokens leave empty.
+    __device__ __forceinline__ static int blocks_of(int rows) { return ((TWO ? 2 * rows : rows) + 7) / 8; }
+
+    // Element 0 of row i of an item's products, or of its first row where it has no such row.
     __device__ __forceinline__ const uint16_t *row_of(int item, int rows, int i) const
     {
+        const uint16_t *X = TWO && (i & 1) ? p.X2 : p.X;
+        if (TWO) i >>= 1;
         const int first = p.ids ? static_cast<int>(t.span[item] & 0xffffu) : item * CHUNK;
         int64_t r = first + (i < rows ? i : 0);
         if (p.ids) r = UP ? t.row[r] & 0xffu : t.row[r] >> 8;
-        return p.X + r * p.ldx;
+        return X + r * p.ldx;
     }
 
     __device__ __forceinline__ void place(FewWalk<MB> &k) const
@@ -448,10 +454,10 @@ struct FewKernel {
         }
         k.whole = !ANY_W && n0 + kFewCols <= (FOUR ? n4 : p.N) ? static_cast<int>(p.K / Stage::STEP) : 0;
         const int rows = rows_of(item);
-        k.blocks = (rows + 7) / 8;
+        k.blocks = blocks_of(rows);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            k.x_bytes[m] = 8 * m + g < rows ? 16u : 0u;
+            k.x_bytes[m] = 8 * m + g < (TWO ? 2 * rows : rows) ? 16u : 0u;
             k.x[m] = row_of(item, rows, 8 * m + g) + Stage::STEP * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
         }
     }
@@ -767,19 +773,20 @@ struct FewKernel {
         const int rows = static_cast<int>(t.span[item] >> 16), first = static_cast<int>(t.span[item] & 0xffffu);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            if (MB > 1 && 8 * m >= rows) break;
+            if (MB > 1 && m >= blocks_of(rows)) break;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * m + 2 * l4 + i;
+            for (int i = 0; i < (TWO ? 1 : 2); ++i) {
+                const int r = TWO ? 4 * m + l4 : 8 * m + 2 * l4 + i;
                 if (r >= rows) continue;
                 const float w = t.weight[first + r];
                 float *to = sums + (t.row[first + r] & 0xffu) * kFewCols;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    const float(&a)[4] = acc[j][m];
                     float2 *v = reinterpret_cast<float2 *>(to + column(j));
                     float2 old = *v;
-                    old.x = fmaf(w, acc[j][m][i], old.x);
-                    old.y = fmaf(w, acc[j][m][2 + i], old.y);
+                    old.x = fmaf(w, TWO ? a[0] + a[1] : a[i], old.x);
+                    old.y = fmaf(w, TWO ? a[2] + a[3] : a[2 + i], old.y);
                     *v = old;
                 }
             }
@@ -846,7 +853,7 @@ struct FewKernel {
         int64_t left = count;  // steps to go
         for (int unit = share.first; unit < share.units; unit += share.stride) {
             clear(acc);
-            const int blocks = (rows_of(item_of(unit)) + 7) / 8;
+            const int blocks = blocks_of(rows_of(item_of(unit)));
             int w_off = 0, x_off[MB];
             offsets(unit, w_off, x_off);
             const int last = left < share.hi - step ? step + static_cast<int>(left) : share.hi;
@@ -937,8 +944,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
         }
         if constexpr (MODE == kFewParts)
             static_cast<float *>(p.out)[to * p.ldo + n] = a;
-        else
-            static_cast<uint16_t *>(p.out)[to * p.ldo + n] = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
+        else {
+            const uint16_t rounded = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
+            static_cast<uint16_t *>(p.out)[to * p.ldo + n] = rounded;
+            if (UP && p.rest) {  // (nothing is left of what is not finite)
+                const float left = n < p.N ? a - few_float<BF16>(rounded) : 0.0f;
+                p.rest[to * p.ldo + n] = fabsf(left) < INFINITY ? few_round<BF16>(left) : static_cast<uint16_t>(0);
+            }
+        }
     };
     // Adds the warps' sums of `rows` rows, the first of them row r0 of the item,
     // then the cluster's, in order: every block sends its sums to the block
@@ -1101,10 +1114,12 @@ cudaError_t launch_few_mode(const FewLaunch &l, const FewParams &p, cudaStream_t
     if (l.mode == kFewUp) return launch_few_kernel<BF16, FOUR, ANY, MB, kFewUp>(l, p, s);
     // Hidden rows are always aligned: with weights in 4 bits nothing else can be off.
     constexpr bool any = ANY && !FOUR;
+    if constexpr (MB < 4)
+        if (l.mode == kFewTwo) return launch_few_kernel<BF16, FOUR, any, MB, kFewTwo>(l, p, s);
     if constexpr (MB == 2)
         if (l.mode == kFewFlat) return launch_few_kernel<BF16, FOUR, any, 2, kFewFlat>(l, p, s);
     if constexpr (MB == 1)
-        return launch_few_kernel<BF16, FOUR, any, 1, kFewFlat>(l, p, s);
+        return cudaErrorInvalidConfiguration;
     else
         return launch_few_kernel<BF16, FOUR, any, MB, kFewParts>(l, p, s);
 }

@@ -186,3 +186,37 @@ def test_subnormal_scales_of_the_step():
     want = args["want"].double() * 2.0 ** -20
     # (want is rounded once to 11 bits, the result again, to multiples of 2^-24)
     assert bool(((y.double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("t", [1, 3, 4, 5, 8])
+@pytest.mark.parametrize("four", [0, 64])
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+def test_few_tokens_are_rounded_once(type_, four, t):
+    """Up to 8 tokens: the distance from the exact result is that of its rounding."""
+    e, c, h, k = 6, 520, 264, 3
+    g = generator("once", type_, four, t)
+    dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[type_]
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, weights = rand(t, c).to(dtype), torch.rand(t, k, generator=g, device="cuda")
+    ids = torch.randint(0, e, (t, k), generator=g, device="cuda").int()
+    ws = [(rand(e, a, b) * a ** -0.5).to(dtype) for a, b in ((c, h), (h, c), (c, h))]
+    if four:
+        ws = [few.pack4(w, four) for w in ws]
+        exact = []
+        for m in ws:
+            q = torch.stack([(m.words >> (4 * [0, 2, 4, 6, 1, 3, 5, 7].index(r))) & 15 for r in range(8)], 2).flatten(1, 2)
+            s = m.scales.double().repeat_interleave(four, 1)[:, :m.inner, :m.outer]
+            exact.append((q[:, :m.inner, :m.outer].double() - 8) * s)
+    else:
+        exact = [w.double() for w in ws]
+    want = torch.zeros(t, c, dtype=torch.float64, device="cuda")
+    for i in range(t):
+        for j in range(k):
+            e1, e2, e3 = (w[int(ids[i, j])] for w in exact)
+            hidden = torch.nn.functional.silu(x[i].double() @ e1) * (x[i].double() @ e3)
+            want[i] += weights[i, j].double() * (hidden @ e2)
+    y = few.expert_step(x, ids, weights, *ws)
+    status_ok()
+    once = float((want.to(dtype).double() - want).norm())
+    # (besides: fp32 sums and the activation, some 2^-20 of the values, next to 2^-9 or 2^-12)
+    assert float((y.double() - want).norm()) <= 1.05 * once
