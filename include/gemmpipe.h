@@ -59,8 +59,9 @@
  * A return of GEMMPIPE_OK means "validated and enqueued".  Errors found on
  * the device (a pipeline wait that ran out of time) are reported later by
  * gemmpipe_get_device_status().  No C++ exception crosses this interface.
- * Calls may come from several host threads; the library's own state is
- * guarded by a mutex.
+ * Calls may come from several host threads, on one stream too: the library's
+ * own state is guarded by a mutex, and a call that uses a workspace of the
+ * stream enqueues all of its kernels before another one may take it.
  *
  * Error behaviour common to the GEMM entry points:
  *   - M, N or K negative, any of them above 2^31 - 1, a matrix of 2^56

@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "gemmpipe.h"
 
 namespace gp {
@@ -22,11 +24,25 @@ gemmpipe_status_t api_device(ApiDevice *out);
 // A non-null device or managed pointer aligned to `align` bytes.
 gemmpipe_status_t api_check_pointer(const void *p, int align);
 
-// The operand workspace of (device, stream), at least `bytes` long.
+// Held from before a workspace of (device, stream) is taken until the last
+// launch that uses it is enqueued: calls that several host threads make on one
+// stream would otherwise write one's operands or sums between another's
+// launches, or free the memory that the other has taken and not used yet.  The
+// holder's own calls may take it again.
+class ApiOrder {
+    std::unique_lock<std::recursive_mutex> held;
+
+public:
+    ApiOrder(int dev, cudaStream_t s);
+};
+
+// The operand workspace of (device, stream), at least `bytes` long; to be taken
+// and used under ApiOrder.
 gemmpipe_status_t api_workspace(int dev, cudaStream_t s, int64_t bytes, void **out);
 
 // The workspace of (device, stream) for sums in parts: `counts` bytes that
-// start as zeros and stay what the kernels make them, then `bytes` of parts.
+// start as zeros and stay what the kernels make them, then `bytes` of parts;
+// to be taken and used under ApiOrder.
 gemmpipe_status_t api_parts_workspace(int dev, cudaStream_t s, int64_t counts, int64_t bytes, void **out);
 
 // Runs fn(ctx), which launches `kernels` kernels on `s`, inside the timing

@@ -241,6 +241,7 @@ gemmpipe_status_t run_product(Product q, const ApiDevice &d, cudaStream_t s)
         slots = (2 * q.R / split_rows + 1) * matrix_tiles;
         if (split_rows + split_rows / 2 >= q.R || slots > gp::kMaxPartSlots) split_rows = slots = 0;
     }
+    const gp::ApiOrder order(d.dev, s);
     gemmpipe_status_t st = GEMMPIPE_OK;
     const uint16_t *W = q.W;
     void *ws = nullptr;
@@ -433,6 +434,7 @@ gemmpipe_status_t gemmpipe_route(int64_t T, int64_t top_k, int64_t E, const int3
         cudaStream_t s = stream_of(stream);
         if (t.R == 0) return zero_rows(reinterpret_cast<uint16_t *>(offsets), 1, 2 * (E + 1), 2 * (E + 1), s);
         if ((st = check_all({{experts, 4}, {slots, 4}, {rows, 4}})) != GEMMPIPE_OK) return st;
+        const gp::ApiOrder order(d.dev, s);
         void *ws = nullptr;
         const int64_t bytes = gp::route_scratch_bytes(t.R, static_cast<int>(E));
         if (bytes > 0 && (st = gp::api_workspace(d.dev, s, bytes, &ws)) != GEMMPIPE_OK) return st;

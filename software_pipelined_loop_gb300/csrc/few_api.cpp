@@ -311,6 +311,7 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     // in the workspace: it takes rows of the matrix instructions that are empty,
     // and the error is that of the last rounding (with rounded rows 1.4 times it).
     const bool two = T <= 8;
+    const gp::ApiOrder order(d.dev, s);
     void *ws = nullptr;
     if (two || !flat) {
         const int64_t bytes = two ? 2 * T * top_k * ldh : 4 * T * top_k * C;

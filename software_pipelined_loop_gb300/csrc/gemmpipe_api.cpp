@@ -565,6 +565,7 @@ cudaError_t zero_now(void *p, int64_t bytes)
 // first zero_bytes bytes of a new one (stream-K flags, counts of parts) are
 // zeroed before first use.  A graph recorded on the stream holds the
 // workspace's address, so what was handed out to one is kept when outgrown.
+// Taken and used under ApiOrder.
 gemmpipe_status_t workspace(int dev, cudaStream_t s, int64_t bytes, void **out, int kind = kWsOperands,
                             int64_t zero_bytes = 0)
 {
@@ -848,6 +849,15 @@ gemmpipe_status_t api_device(ApiDevice *out)
     return GEMMPIPE_OK;
 }
 
+// (Streams share the locks of a fixed table, which needs no memory of its own;
+// a thread holds one at a time, so two streams of one lock only take turns.)
+ApiOrder::ApiOrder(int dev, cudaStream_t s)
+{
+    static std::recursive_mutex locks[61];
+    held = std::unique_lock<std::recursive_mutex>(
+        locks[(reinterpret_cast<uintptr_t>(s) / 16 + static_cast<uintptr_t>(dev)) % 61]);
+}
+
 gemmpipe_status_t api_check_pointer(const void *p, int align) { return check_pointer(p, align); }
 
 gemmpipe_status_t api_workspace(int dev, cudaStream_t s, int64_t bytes, void **out)
@@ -1096,6 +1106,7 @@ gemmpipe_status_t gemm_s8s8s32_host(int64_t M, int64_t N, int64_t K, const int8_
     DeviceInfo d;
     if ((st = device_info(&d, &dev)) != GEMMPIPE_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const gp::ApiOrder order(dev, s);
     void *dA = nullptr, *dB = nullptr, *dC = nullptr;
     if ((st = host_buffers(dev, s, M, N, K, 1, 4, &dA, &dB, &dC)) != GEMMPIPE_OK) return st;
     const int8_t *A8 = static_cast<const int8_t *>(dA), *B8 = static_cast<const int8_t *>(dB);
@@ -1157,6 +1168,7 @@ gemmpipe_status_t gemm_f16f32_host(int64_t M, int64_t N, int64_t K, const gemmpi
     DeviceInfo d;
     if ((st = device_info(&d, &dev)) != GEMMPIPE_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const gp::ApiOrder order(dev, s);
     void *dA = nullptr, *dB = nullptr, *dC = nullptr;
     if ((st = host_buffers(dev, s, M, N, K, 2, 4, &dA, &dB, &dC)) != GEMMPIPE_OK) return st;
     const gemmpipe_half_t *A16 = static_cast<const gemmpipe_half_t *>(dA);
@@ -1189,6 +1201,7 @@ gemmpipe_status_t gemm_f16f32(int64_t M, int64_t N, int64_t K, const gemmpipe_ha
     if ((st = check_device_pointers(K, A, B, C, 2, 4)) != GEMMPIPE_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (K == 0) return zero_c(C, M * N * 4, d, s);
+    const gp::ApiOrder order(dev, s);
     const uint16_t *Ause = A, *Buse = B;
     int64_t lda = K, ldb = N;
     if (pad_wanted(A, K, B, N)) {
@@ -1236,6 +1249,7 @@ gemmpipe_status_t gemm_s8s8s32(int64_t M, int64_t N, int64_t K, const int8_t *A,
     if ((st = check_device_pointers(K, A, B, C, 1, 4)) != GEMMPIPE_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (K == 0) return zero_c(C, M * N * 4, d, s);
+    const gp::ApiOrder order(dev, s);
     if (imma_wanted(A, K)) {
         // Comparison path: B transposed, then warp-level integer MMA.
         const int64_t ldbt = gp::imma_bt_pitch(K);
