@@ -767,6 +767,14 @@ struct FewKernel {
         return FOUR ? 32 * (j >> 1) + 4 * g + 2 * (j & 1) : 8 * g + 2 * j;
     }
 
+    // TWO: a row's sum from those of its rounded values and of their rest.  An
+    // infinite weight makes infinities of both, of either sign, and NaN of a
+    // rest of zero: there the sum is that of the rounded values.
+    __device__ __forceinline__ static float both(float rounded, float rest)
+    {
+        return fabsf(rest) < INFINITY ? rounded + rest : rounded;
+    }
+
     // Adds the sums of an item, weighted, to the warp's sums of the tokens.
     __device__ __forceinline__ void add(float *sums, const float (&acc)[4][MB][4], int item) const
     {
@@ -785,8 +793,8 @@ struct FewKernel {
                     const float(&a)[4] = acc[j][m];
                     float2 *v = reinterpret_cast<float2 *>(to + column(j));
                     float2 old = *v;
-                    old.x = fmaf(w, TWO ? a[0] + a[1] : a[i], old.x);
-                    old.y = fmaf(w, TWO ? a[2] + a[3] : a[2 + i], old.y);
+                    old.x = fmaf(w, TWO ? both(a[0], a[1]) : a[i], old.x);
+                    old.y = fmaf(w, TWO ? both(a[2], a[3]) : a[2 + i], old.y);
                     *v = old;
                 }
             }
