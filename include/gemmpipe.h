@@ -456,8 +456,10 @@ GEMMPIPE_API gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_
  * silu(a) = a / (1 + exp(-a)).  X and Y are T x C, W1 and W3 are E x C x H, W2
  * is E x H x C.  A choice outside [0, E) counts for nothing, whatever its
  * weight; a token without choices gets zeros.  Of more than 8 tokens h is rounded
- * to the type, as an operand of the second product (of up to 8 it has twice the
- * type's bits); nothing else is rounded before Y.
+ * to the type, as an operand of the second product (of up to 8 it is kept in two
+ * values of the type, its rounding and what that leaves: fp16 22 bits, down to
+ * 2^-35; bf16 16 bits); a value of h past the type's largest one becomes infinite;
+ * nothing else is rounded before Y.
  * hidden: T * top_k rows of H rounded up to a multiple of 8 elements of the
  * type, on a 16-byte boundary, for the kernels' use (calls that may run at the
  * same time need one each).  Two launches, for more than 12 tokens (in 4 bits:

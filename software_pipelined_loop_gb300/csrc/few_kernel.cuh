@@ -122,6 +122,12 @@ __device__ __forceinline__ uint16_t few_round(float v)
         return __half_as_ushort(__float2half_rn(v));
 }
 
+// What the rounding of a hidden value leaves is kept times this: of fp16 values it
+// would mostly be below the normal numbers (it is 2^-12 of the value at most,
+// and 16 at most), where bits are lost.
+template <bool BF16>
+constexpr float kFewLift = BF16 ? 1.0f : 2048.0f;
+
 // Values i and i + 4 of a word of eight 4-bit values: the pair of rows 2i, 2i
 // + 1.  (v & mask) | one is a single operation when both are in registers.  The
 // fp16 mantissa holds the upper of two neighbouring values in its place, 16
@@ -772,7 +778,7 @@ struct FewKernel {
     // rest of zero: there the sum is that of the rounded values.
     __device__ __forceinline__ static float both(float rounded, float rest)
     {
-        return fabsf(rest) < INFINITY ? rounded + rest : rounded;
+        return fabsf(rest) < INFINITY ? fmaf(rest, 1.0f / kFewLift<BF16>, rounded) : rounded;
     }
 
     // Adds the sums of an item, weighted, to the warp's sums of the tokens.
@@ -956,7 +962,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
             const uint16_t rounded = n < p.N ? few_round<BF16>(a) : static_cast<uint16_t>(0);
             static_cast<uint16_t *>(p.out)[to * p.ldo + n] = rounded;
             if (UP && p.rest) {  // (nothing is left of what is not finite)
-                const float left = n < p.N ? a - few_float<BF16>(rounded) : 0.0f;
+                const float left = n < p.N ? (a - few_float<BF16>(rounded)) * kFewLift<BF16> : 0.0f;
                 p.rest[to * p.ldo + n] = fabsf(left) < INFINITY ? few_round<BF16>(left) : static_cast<uint16_t>(0);
             }
         }
