@@ -499,22 +499,67 @@ __device__ void wide_sums(const WideParams &p, uint32_t tmem, WideCtl<Cfg> *ctl,
     }
 }
 
-// Y[m][n], group by group as it is written down.
-template <bool BF16>
-__device__ __noinline__ float wide_plain(const WideParams &p, int m, int64_t n)
+// SPLIT: the sums of the CTA's k that are not finite, again, group by group as
+// they are written down: 8 rows at a time, a thread a column of them, and the
+// warpgroups that unpack take groups in turn.  All threads of the CTA come here,
+// with its sums in `sums` (MP x 128).  64 rows x 2^18 x 128, every sum infinite:
+// 8.4 ms, one row of them 1.2 (all finite 0.13; by one thread a sum of all the
+// cluster's k: 104).
+template <class Cfg, bool BF16>
+__device__ __noinline__ void wide_again(const WideParams &p, WideRange r, int64_t n, int warp, float *sums)
 {
-    const uint16_t *x = p.X + m * p.ldx;
-    float sum = 0.0f;
-    for (int64_t k0 = 0; k0 < p.K && !isnan(sum); k0 += p.group) {
-        float part = 0.0f;
-        for (int64_t k = k0; k < k0 + p.group && k < p.K; ++k) {
-            const int row = static_cast<int>(k & 7), place = (row & 1 ? 4 : 0) + (row >> 1);
-            const int q = static_cast<int>(p.Q[(k >> 3) * p.n4 + n] >> (4 * place) & 15u);
-            part = fmaf(scale_of<BF16>(x[k]), static_cast<float>(q - 8), part);
+    constexpr int ROWS = 8, TEAMS = Cfg::UNPACK_GROUPS, EACH = Cfg::STAGE_K / Cfg::GROUP;
+    static_assert((Cfg::MP + TEAMS * ROWS) * kWideCols * 4 <= Cfg::CTL_OFF, "sums and parts in the ring's place");
+    float *const parts = sums + Cfg::MP * kWideCols;  // TEAMS x ROWS x 128
+    const int column = static_cast<int>(threadIdx.x) & 127, team = (warp - Cfg::UNPACK_WARP0) >> 2;
+    const bool on = warp >= Cfg::UNPACK_WARP0 && n < p.N;
+    const int64_t groups = (p.K + Cfg::GROUP - 1) / Cfg::GROUP, first = static_cast<int64_t>(r.lo) * EACH;
+    const int64_t last = static_cast<int64_t>(r.hi) * EACH < groups ? static_cast<int64_t>(r.hi) * EACH : groups;
+    for (int m0 = 0; m0 < p.M; m0 += ROWS) {
+        bool bad = false;
+        if (on)
+            for (int i = 0; i < ROWS && m0 + i < p.M; ++i) bad |= !isfinite(sums[(m0 + i) * kWideCols + column]);
+        if (!__syncthreads_or(bad)) continue;
+        float sum[ROWS] = {};
+        for (int64_t g = first + team; bad && g < last; g += TEAMS) {
+            float part[ROWS] = {};
+#pragma unroll
+            for (int b = 0; b < Cfg::GROUP / 8; ++b) {
+                const int64_t k = Cfg::GROUP * g + 8 * b;
+                if (k >= p.K) break;
+                const int count = p.K - k < 8 ? static_cast<int>(p.K - k) : 8;
+                const uint32_t word = p.Q[(k >> 3) * p.n4 + n];
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                    // (a whole piece of 16 bytes, of which the first is inside the row)
+                    const uint4 v = *reinterpret_cast<const uint4 *>(p.X + (m0 + i < p.M ? m0 + i : m0) * p.ldx + k);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int q = static_cast<int>(word >> (4 * ((j & 1 ? 4 : 0) + (j >> 1))) & 15u);
+                        const uint16_t bits = static_cast<uint16_t>(x[j >> 1] >> (16 * (j & 1)));
+                        if (j < count) part[i] = fmaf(scale_of<BF16>(bits), static_cast<float>(q - 8), part[i]);
+                    }
+                }
+            }
+            const float s = scale_of<BF16>(p.S[g * p.n4 + n]);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) sum[i] = fmaf(s, part[i], sum[i]);
         }
-        sum = fmaf(scale_of<BF16>(p.S[k0 / p.group * p.n4 + n]), part, sum);
+        if (on)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) parts[(team * ROWS + i) * kWideCols + column] = sum[i];
+        __syncthreads();
+        if (on)
+            for (int i = team; i < ROWS && m0 + i < p.M; i += TEAMS) {
+                float &to = sums[(m0 + i) * kWideCols + column];
+                if (isfinite(to)) continue;
+                float all = 0.0f;
+                for (int t = 0; t < TEAMS; ++t) all += parts[(t * ROWS + i) * kWideCols + column];
+                to = all;
+            }
+        __syncthreads();
     }
-    return sum;
 }
 
 template <class Cfg, bool BF16>
@@ -560,12 +605,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int column = static_cast<int>(threadIdx.x) & 127, row0 = Cfg::SUMS * ((warp - Cfg::END_WARP0) >> 2);
     const bool ends = warp >= Cfg::END_WARP0 && warp < Cfg::END_WARP0 + Cfg::END_WARPS;
     const int64_t n = col0 + column;
-    const auto store = [&](int m, float v) {
-        // (a wait that ran out leaves anything)
-        if (Cfg::SPLIT && !isfinite(v) && ctl->abort == 0) v = wide_plain<BF16>(p, m, n);
-        p.Y[m * p.ldy + n] = round_of<BF16>(v);
-    };
+    const auto store = [&](int m, float v) { p.Y[m * p.ldy + n] = round_of<BF16>(v); };
     float *sums = reinterpret_cast<float *>(wide_smem + pad);  // in the ring's place, once every stage is done
+    bool bad = false;  // a sum that is not finite
     if (warp < Cfg::PRODUCERS) {
         wide_producer<Cfg>(p, &words, &rows, sbase, ctl, w, r, static_cast<int>(col0), warp);
     } else if (warp < Cfg::END_WARP0) {
@@ -592,10 +634,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
             for (int m = 0; m < Cfg::SUMS; ++m) {
                 if (row0 + m >= p.M) break;
-                if (p.split > 1) sums[(row0 + m) * kWideCols + column] = sum[m];
+                if (Cfg::SPLIT || p.split > 1) sums[(row0 + m) * kWideCols + column] = sum[m];
                 else if (n < p.N) store(row0 + m, sum[m]);
+                bad |= Cfg::SPLIT && n < p.N && !isfinite(sum[m]);
             }
         }
+    }
+    __syncwarp();
+    if constexpr (Cfg::SPLIT) {
+        if (__syncthreads_or(bad) && ctl->abort == 0) wide_again<Cfg, BF16>(p, r, n, warp, sums);  // (a wait that ran out leaves anything)
+        if (p.split == 1 && ends && n < p.N)
+            for (int m = row0; m < row0 + Cfg::SUMS && m < p.M; ++m) store(m, sums[m * kWideCols + column]);
     }
     __syncwarp();
     tc_fence_before_sync();

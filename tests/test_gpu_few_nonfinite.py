@@ -1,4 +1,5 @@
-"""Infinities and NaN in the operands of the few-token operators: the results that the formulas give."""
+"""Infinities and NaN in the operands of the few-token operators: the results that the formulas give, and in a time
+that is of the order of the finite ones'."""
 from __future__ import annotations
 
 import math
@@ -6,6 +7,7 @@ import math
 import pytest
 import torch
 
+from software_pipelined_loop_gb300 import gemmpipe as gp
 from test_gpu_few import TYPES, generator, ints, run_step, scales_of, status_ok, words_of
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +72,42 @@ def test_infinities_of_the_second_matrix(type_, four, t):
     rest = want.isfinite()
     error = (y[rest].double() - want[rest]).norm() / want[rest].norm()
     assert float(error) <= 3 * torch.finfo(dtype).eps / 2  # (hidden rows and y: a rounding each, at most)
+
+
+@pytest.mark.parametrize("what", ["rows", "scales", "large scales"])
+@pytest.mark.parametrize("type_", TYPES)
+def test_time_of_sums_that_are_not_finite(type_, what):
+    """64 rows x 2^18 x 128 in groups of 32: every sum infinite, or its weights past the type's largest value."""
+    m, k, n, group = 64, 1 << 18, 128, 32
+    code, dtype = TYPES[type_]
+    g = generator("slow", type_, what)
+    x = ints(g, 0, 1, m, k).to(dtype)
+    steps = ints(g, 1, 7, 1, k, n)
+    scale = torch.full((1, k // group, n), 2.0 ** -6, dtype=torch.float64, device="cuda")
+    if what == "rows":
+        x[:, 1000] = math.inf
+        want = torch.full((m, n), math.inf, dtype=dtype, device="cuda")
+    elif what == "scales":
+        scale[0, 77] = math.inf
+        x[:, 77 * group] = 1
+        want = torch.full((m, n), math.inf, dtype=dtype, device="cuda")
+    else:
+        # One group's weights are past the largest value; its rows of X bring them back to 7 * 2^-9.
+        top = torch.finfo(dtype).max
+        scale[0, 55] = 2.0 ** math.floor(math.log2(top))
+        steps[0, 55 * group:56 * group] = 7
+        x *= 0
+        x[:, 55 * group] = 2.0 ** -24 if type_ == "f16" else 2.0 ** -130
+        want = (x[:, 55 * group, None].double() * 7 * scale[:, 55]).to(dtype).expand(m, n)
+    q, s = words_of(steps), scales_of(scale, n, dtype)
+    y = torch.empty(m, n, dtype=dtype, device="cuda")
+    call = lambda: gp.gemm_rows4(code, m, n, k, group, x, k, q, s, y, n)  # noqa: E731
+    call()
+    start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    call()
+    stop.record()
+    status_ok()
+    assert torch.equal(y, want)
+    # The finite sums take some 0.1 ms; one thread's whole sum after another, hundreds of ms.
+    assert start.elapsed_time(stop) < 40
