@@ -200,16 +200,22 @@ __device__ __forceinline__ void few_st_cluster(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// The two halves of a cluster barrier without ordering of memory: nothing but
-// that every block has come so far.
-__device__ __forceinline__ void few_cluster_arrive()
+// The two halves of a cluster barrier.  The first arrival says nothing but that
+// the block is there; a later one, that what the block has read may be written
+// over by the others after their wait.
+__device__ __forceinline__ void few_cluster_arrive_first()
 {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void few_cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void few_cluster_wait()
 {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------- table of items
@@ -319,7 +325,7 @@ __device__ __forceinline__ int few_build_block(const FewParams &p, FewTables &t,
             rows += n;
             items += (n + CHUNK - 1) / CHUNK;
         }
-        uint32_t both = rows | items << 16;  // at most 4096 and 1148
+        uint32_t both = rows | items << 16;  // at most 4096 and (1024 experts, 4096 rows in 16s) 1216
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, both, d);
@@ -992,6 +998,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
                 }
             }
         if (split > 1) {
+            __syncwarp();
             cluster_sync();
             for (int i = tid; i < part && rank * part + i < total; i += 32 * kFewWarps) {
                 float a = 0.0f, b = 0.0f;
@@ -1002,13 +1009,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
                 const int at = rank * part + i;
                 finish(item, r0 + at / kFewCols, n0 + at % kFewCols, a, b);
             }
+            __syncwarp();
             if (more) few_cluster_arrive();
         }
         __syncthreads();
     };
 
     const int cluster = static_cast<int>(blockIdx.x) / split, clusters = static_cast<int>(gridDim.x) / split;
-    if (split > 1 && (FLAT || cluster < items * p.columns)) few_cluster_arrive();
+    if (split > 1 && (FLAT || cluster < items * p.columns)) few_cluster_arrive_first();
     if constexpr (FLAT) {
         const int64_t n0 = static_cast<int64_t>(cluster) * kFewCols;
         float *own = sums + warp * slab;
