@@ -6,7 +6,7 @@ the whole expert layer for a few tokens with weights in 16 or in 4 bits.
         weight * ((silu(x @ w1[e]) * (x @ w3[e])) @ w2[e]), without w3 ungated
 
 For generating token by token: at most 64 rows or tokens a call, no gradients
-(expert_layer has them).  Everything is computed in the CUDA library; torch
+(expert_layer has them): asking for them is an error.  Everything is computed in the CUDA library; torch
 supplies memory.  A matrix for many rows is brought back with unpack4.
 
     m = pack4(w1)                  # once, when the weights are loaded
@@ -42,7 +42,7 @@ class Packed4(NamedTuple):
 
 
 def _no_gradients(*tensors) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
         raise RuntimeError("the few-token operators have no gradients: use expert_layer, or torch.no_grad()")
 
 
@@ -94,6 +94,7 @@ def unpack4(m: Packed4) -> torch.Tensor:
     """The matrices (experts x inner x outer), each value rounded to the scales' type."""
     _check_type(m.scales)
     _check_packed("m", m, m.scales.dtype)
+    _no_gradients(m.scales)
     _check_devices(m.words, m.scales)
     w = torch.empty(m.experts, m.inner, m.outer, dtype=m.scales.dtype, device=m.words.device)
     gp.gemmpipe_unpack4(_CODE[w.dtype], m.experts, m.inner, m.outer, m.group, m.words.contiguous(),
@@ -108,7 +109,7 @@ def rows4(x: torch.Tensor, m: Packed4) -> torch.Tensor:
     if x.dim() != 2 or x.shape[0] > gp.FEW_ROWS or x.shape[1] != m.inner or m.experts != 1:
         raise ValueError(f"at most {gp.FEW_ROWS} rows of {m.inner} values and one matrix are needed, "
                          f"got {tuple(x.shape)} and {m.experts}")
-    _no_gradients(x)
+    _no_gradients(x, m.scales)
     _check_devices(x, m.words, m.scales)
     x, ldx = _rows(x)
     y = torch.empty(x.shape[0], m.outer, dtype=x.dtype, device=x.device)
