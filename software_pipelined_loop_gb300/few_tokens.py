@@ -6,7 +6,7 @@ the whole expert layer for a few tokens with weights in 16 or in 4 bits.
         weight * ((silu(x @ w1[e]) * (x @ w3[e])) @ w2[e]), without w3 ungated
 
 For generating token by token: at most 64 rows or tokens a call, no gradients
-(expert_layer has them): asking for them is an error.  Everything is computed in the CUDA library; torch
+(expert_layer has them): asking for them, in forward mode too, is an error.  Everything is computed in the CUDA library; torch
 supplies memory.  A matrix for many rows is brought back with unpack4.
 
     m = pack4(w1)                  # once, when the weights are loaded
@@ -17,6 +17,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from software_pipelined_loop_gb300 import gemmpipe as gp
 from software_pipelined_loop_gb300.expert_layer import _CODE, _check_devices, _check_ids
@@ -44,6 +45,11 @@ class Packed4(NamedTuple):
 def _no_gradients(*tensors) -> None:
     if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
         raise RuntimeError("the few-token operators have no gradients: use expert_layer, or torch.no_grad()")
+    # Forward mode goes by tangents, under no_grad too.  (Outside a dual level there
+    # are none; looking at each tensor costs a microsecond.)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and not torch.is_inference_mode_enabled() and \
+            any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError("the few-token operators have no gradients, forward-mode ones neither")
 
 
 def _check_type(x) -> None:

@@ -1,8 +1,10 @@
-"""The few-token operators have no gradients: whoever asks for them, of any argument, gets an error instead of a result without them (all before any device call, no GPU needed)."""
+"""The few-token operators have no gradients: whoever asks for them, in reverse or in forward mode and of any argument,
+gets an error instead of a result without them (all before any device call, no GPU needed)."""
 from __future__ import annotations
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from software_pipelined_loop_gb300 import few_tokens as few
 from test_few_tokens_arguments import C, H, T, arguments, packed
@@ -33,8 +35,22 @@ def test_reverse_mode(name):
         dict(calls(lambda t: t.clone().requires_grad_()))[name]()
 
 
+@pytest.mark.parametrize("no_grad", [False, True])
+@pytest.mark.parametrize("name", NAMES)
+def test_forward_mode(name, no_grad):
+    with forward_ad.dual_level(), torch.set_grad_enabled(not no_grad):
+        with pytest.raises(RuntimeError, match="gradients"):
+            dict(calls(lambda t: forward_ad.make_dual(t, torch.ones_like(t))))[name]()
+
+
 @pytest.mark.parametrize("name", NAMES)
 def test_without_gradients_the_call_goes_on(name):
     # (to the next check, which finds no GPU tensors)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         dict(calls(lambda t: t.clone().requires_grad_()))[name]()
+    with forward_ad.dual_level(), pytest.raises(ValueError, match="CUDA"):
+        dict(calls(lambda t: t))[name]()
+    with forward_ad.dual_level():
+        dual = dict(calls(lambda t: forward_ad.make_dual(t, torch.ones_like(t))))[name]
+        with torch.inference_mode(), pytest.raises(ValueError, match="CUDA"):
+            dual()
