@@ -423,8 +423,8 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, 
  * on the current device, results that repeat bit for bit, the errors.  They
  * are inference operators without gradients and may be recorded by stream
  * capture.  The expert layer uses the library workspace: T * top_k rows of H
- * 16-bit values for up to 8 tokens, of C fp32 values for more than 12 (in 4
- * bits: 16).  M and T are at most
+ * 16-bit values, and of C fp32 values for more than 12 tokens (in 4 bits: 16).
+ * M and T are at most
  * 64; N, K, C and H at most 2^31 - 1024; an expert layer whose experts with
  * rows, at most, times its 64-column blocks reach 2^30 is
  * GEMMPIPE_ERR_INVALID_VALUE.  gemm_rows4 on more than 8 rows of X on 16-byte
@@ -455,11 +455,10 @@ GEMMPIPE_API gemmpipe_status_t gemm_rows4(int type, int64_t M, int64_t N, int64_
  *        silu(X[t] . W1[e]) * (X[t] . W3[e])   (element by element),
  * silu(a) = a / (1 + exp(-a)).  X and Y are T x C, W1 and W3 are E x C x H, W2
  * is E x H x C.  A choice outside [0, E) counts for nothing, whatever its
- * weight; a token without choices gets zeros.  Of more than 8 tokens h is rounded
- * to the type, as an operand of the second product (of up to 8 it is kept in two
- * values of the type, its rounding and what that leaves: fp16 22 bits, down to
- * 2^-35; bf16 16 bits); a value of h past the type's largest one becomes infinite;
- * nothing else is rounded before Y.
+ * weight; a token without choices gets zeros.  h is kept in two values of the
+ * type, its rounding and what that leaves (fp16 22 bits, down to 2^-35; bf16 16
+ * bits); a value of h past the type's largest one becomes infinite; nothing else
+ * is rounded before Y.
  * hidden: T * top_k rows of H rounded up to a multiple of 8 elements of the
  * type, on a 16-byte boundary, for the kernels' use (calls that may run at the
  * same time need one each).  Two launches, for more than 12 tokens (in 4 bits:

@@ -18,16 +18,20 @@ constexpr int kFewWarps = 8;       // warps of a block
 // What a launch computes:
 enum FewMode : int {
     kFewUp = 0,    // rows of X times a matrix, or the tokens' rows times their experts' matrices: hidden rows
-    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (9 to 16 tokens)
+    kFewFlat = 1,  // hidden rows times the experts' second matrices, summed by token in the block (few tokens)
     kFewParts = 2, // the same, one fp32 row for each choice: few_combine adds them
-    kFewTwo = 3,   // as kFewFlat, hidden rows in two parts (at most 8 tokens)
 };
 
-// One launch.  An item is an expert and up to 8 * blocks of the tokens that
-// chose it, or (`ids` null) so many of `tokens` rows of X.
+// Rows of an item: what `blocks` 8-row blocks of the products hold.  Hidden rows
+// are in two parts, their rounding to the type and what that leaves, so that
+// nothing is lost between the products, and take two rows each.
+__host__ __device__ constexpr int few_chunk(int blocks, bool up) { return (up ? 8 : 4) * blocks; }
+
+// One launch.  An item is an expert and up to few_chunk of the tokens that chose
+// it, or (`ids` null) so many of `tokens` rows of X.
 struct FewParams {
     const uint16_t *X;      // kFewUp: rows by token; else by slot
-    const uint16_t *X2;     // kFewTwo: what their rounding left
+    const uint16_t *X2;     // not kFewUp: what their rounding left
     int64_t ldx;
     const int32_t *ids;     // tokens x top_k
     const float *weights;   // tokens x top_k (not kFewUp)

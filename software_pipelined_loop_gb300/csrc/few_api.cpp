@@ -72,8 +72,12 @@ gemmpipe_status_t zero_rows(void *out, int64_t rows, int64_t width, int64_t ld, 
 
 int64_t align128(int64_t x) { return (x + 127) / 128 * 128; }
 
-// The launch for `p` (sizes, matrices and ids set).  Items hold 8 rows of up to
-// 8 tokens; above, 16 rows, or 32 where the experts have more on average.
+// The launch for `p` (sizes, matrices and ids set).  Items of the first product
+// hold 8 rows of up to 8 tokens; above, 16 rows, or 32 where the experts have more
+// on average.  Those of the second product, whose rows are two each, hold 4 rows
+// of up to 4 tokens; above, 8, or, of weights in 16 bits, 16 where the experts have
+// more on average (64 tokens x 8 of 16 experts of 4096 x 1536 181 us, 199 in 8s; of 64
+// experts 415 and 408; in 4 bits 203 and 187, 237 and 224).
 FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
 {
     FewLaunch l{};
@@ -83,9 +87,10 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
     l.mode = mode;
     const int64_t slots = static_cast<int64_t>(p->tokens) * p->top_k;
     const int64_t used = !p->ids ? 1 : (slots < p->experts ? slots : p->experts);  // experts with rows, at most
-    l.row_blocks = p->tokens <= 8 ? 1 : (p->tokens <= 16 || slots <= 16 * used || (any && !four) ? 2 : 4);
-    if (mode == gp::kFewTwo) l.row_blocks = p->tokens <= 4 ? 1 : 2;
-    const int64_t chunk = 8 * l.row_blocks;
+    const bool up = mode == gp::kFewUp;
+    const bool many = p->tokens > 16 && slots > 16 * used && !(any && !four);
+    l.row_blocks = p->tokens <= (up ? 8 : 4) ? 1 : (many && (up || (mode == gp::kFewParts && !four)) ? 4 : 2);
+    const int64_t chunk = gp::few_chunk(l.row_blocks, up);
     p->steps = static_cast<uint32_t>((p->K + (four ? 63 : 31)) / (four ? 64 : 32));
     p->group_shift = p->group_steps == 4 ? 2 : p->group_steps == 2 ? 1 : 0;
     p->words = (p->K + 7) / 8;
@@ -104,7 +109,7 @@ FewLaunch few_launch(FewParams *p, bool bf16, bool four, bool any, int mode)
     // Units of work: 64 columns of an item each (kFewFlat: of all items).  The
     // experts that have rows are not known here: as many as tokens that choose
     // any of them alike would reach.
-    const bool all = mode == gp::kFewFlat || mode == gp::kFewTwo;
+    const bool all = mode == gp::kFewFlat;
     const int64_t columns = (p->out_cols + gp::kFewCols - 1) / gp::kFewCols;
     double reached = static_cast<double>(items);
     if (p->ids && p->top_k < p->experts)
@@ -304,30 +309,25 @@ gemmpipe_status_t expert_step(int type, int64_t T, int64_t top_k, int64_t E, int
     // The second products of a few tokens are summed where they are made, as many
     // as leave room for two blocks on an SM; those of more go by way of the
     // workspace, a row for each choice.  12 tokens x 4 of 32 experts of 2048 x 1024
-    // 59 us and 67 that way (4 bits: 40 and 47), x 8 of 64 of 4096 x 1536 262 and 268
-    // (134 and 138); 16 tokens 79 and 70 (44 and 50), 296 and 292 (144 and 146).
+    // 59 us and 65 that way (4 bits: 36 and 42), x 8 of 64 of 4096 x 1536 218 and 221
+    // (107 and 106); 16 tokens 77 and 68 (42 and 45), 251 and 244 (124 and 126).
     const bool flat = T <= (four ? 16 : 12);
-    // Hidden rows of up to 8 tokens keep what their rounding leaves, beside them
-    // in the workspace: it takes rows of the matrix instructions that are empty,
-    // and the error is that of the last rounding (with rounded rows 1.4 times it).
-    const bool two = T <= 8;
+    const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp);
+    const FewLaunch ld = few_launch(&down, bf16, four, down_off, flat ? gp::kFewFlat : gp::kFewParts);
+    if (lu.status != GEMMPIPE_OK || ld.status != GEMMPIPE_OK) return lu.status != GEMMPIPE_OK ? lu.status : ld.status;
+    // What the rounding of hidden rows leaves is in the workspace, and before the
+    // sums the rows for each choice.
     const gp::ApiOrder order(d.dev, s);
+    const int64_t rest_bytes = align128(2 * T * top_k * ldh);
     void *ws = nullptr;
-    if (two || !flat) {
-        const int64_t bytes = two ? 2 * T * top_k * ldh : 4 * T * top_k * C;
-        if ((st = gp::api_workspace(d.dev, s, bytes, &ws)) != GEMMPIPE_OK) return st;
-    }
-    float *parts = static_cast<float *>(ws);
-    if (two) {
-        up.rest = static_cast<uint16_t *>(ws);
-        down.X2 = up.rest;
-    } else if (!flat) {
+    if ((st = gp::api_workspace(d.dev, s, rest_bytes + (flat ? 0 : 4 * T * top_k * C), &ws)) != GEMMPIPE_OK) return st;
+    float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + rest_bytes);
+    up.rest = static_cast<uint16_t *>(ws);
+    down.X2 = up.rest;
+    if (!flat) {
         down.out = parts;
         down.ldo = C;
     }
-    const FewLaunch lu = few_launch(&up, bf16, four, up_off, gp::kFewUp);
-    const FewLaunch ld = few_launch(&down, bf16, four, down_off, two ? gp::kFewTwo : flat ? gp::kFewFlat : gp::kFewParts);
-    if (lu.status != GEMMPIPE_OK || ld.status != GEMMPIPE_OK) return lu.status != GEMMPIPE_OK ? lu.status : ld.status;
     return gp::api_launch(true, s, flat ? 2 : 3, [&] {
         cudaError_t e = launch(lu, up, s);
         if (e == cudaSuccess) e = launch(ld, down, s);

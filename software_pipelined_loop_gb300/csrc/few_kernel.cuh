@@ -25,8 +25,8 @@
 //   - 4-bit values become 1024 + q (fp16) or 128 + q (bf16) by a mask and an or,
 //     exact, then the constant and the 8 are taken off, exact; the sum over a
 //     group's products of a step is multiplied by the columns' scales in fp32,
-//     so nothing is rounded before the end but the hidden rows of more than 8
-//     tokens, operands of the next product (of up to 8 the rest is kept, too);
+//     so nothing is rounded before the end; hidden rows, operands of the next
+//     product, are two rows there: their rounding and what that leaves;
 //   - the 8 warps of a block and the blocks of a cluster share the products;
 //     their sums meet in shared memory, in a fixed order.
 //
@@ -389,9 +389,10 @@ struct FewWalk {
 
 template <bool BF16, bool FOUR, bool ANY, int MB, int MODE>
 struct FewKernel {
-    static constexpr int CHUNK = 8 * MB, DEPTH = few_depth<FOUR, MB>();
+    static constexpr int DEPTH = few_depth<FOUR, MB>();
     static constexpr bool FIXED = MB > 1;
-    static constexpr bool UP = MODE == kFewUp, TWO = MODE == kFewTwo, FLAT = MODE == kFewFlat || TWO;
+    static constexpr bool UP = MODE == kFewUp, FLAT = MODE == kFewFlat;
+    static constexpr int PARTS = UP ? 1 : 2, CHUNK = few_chunk(MB, UP);  // rows of the products for a row of an item
     static constexpr bool ANY_W = ANY && !FOUR, ANY_X = ANY && UP;
     using Stage = FewStage<FOUR, ANY_W, ANY_X, MB>;
 
@@ -438,15 +439,14 @@ struct FewKernel {
         return p.ids ? static_cast<int>(t.span[item] >> 16) : min(p.tokens - item * CHUNK, CHUNK);
     }
 
-    // TWO: an item's row is two of the products', its rounded values and their
-    // rest, which take places that few tokens leave empty.
-    __device__ __forceinline__ static int blocks_of(int rows) { return ((TWO ? 2 * rows : rows) + 7) / 8; }
+    // A hidden row is two of the products' rows, its rounded values and their rest.
+    __device__ __forceinline__ static int blocks_of(int rows) { return (PARTS * rows + 7) / 8; }
 
     // Element 0 of row i of an item's products, or of its first row where it has no such row.
     __device__ __forceinline__ const uint16_t *row_of(int item, int rows, int i) const
     {
-        const uint16_t *X = TWO && (i & 1) ? p.X2 : p.X;
-        if (TWO) i >>= 1;
+        const uint16_t *X = !UP && (i & 1) ? p.X2 : p.X;
+        if (!UP) i >>= 1;
         const int first = p.ids ? static_cast<int>(t.span[item] & 0xffffu) : item * CHUNK;
         int64_t r = first + (i < rows ? i : 0);
         if (p.ids) r = UP ? t.row[r] & 0xffu : t.row[r] >> 8;
@@ -469,7 +469,7 @@ struct FewKernel {
         k.blocks = blocks_of(rows);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            k.x_bytes[m] = 8 * m + g < (TWO ? 2 * rows : rows) ? 16u : 0u;
+            k.x_bytes[m] = 8 * m + g < PARTS * rows ? 16u : 0u;
             k.x[m] = row_of(item, rows, 8 * m + g) + Stage::STEP * static_cast<int64_t>(k.step) + (ANY_X ? 0 : 8 * l4);
         }
     }
@@ -779,7 +779,7 @@ struct FewKernel {
         return FOUR ? 32 * (j >> 1) + 4 * g + 2 * (j & 1) : 8 * g + 2 * j;
     }
 
-    // TWO: a row's sum from those of its rounded values and of their rest.  An
+    // A hidden row's sum from those of its rounded values and of their rest.  An
     // infinite weight makes infinities of both, of either sign, and NaN of a
     // rest of zero: there the sum is that of the rounded values.
     __device__ __forceinline__ static float both(float rounded, float rest)
@@ -793,22 +793,18 @@ struct FewKernel {
         const int rows = static_cast<int>(t.span[item] >> 16), first = static_cast<int>(t.span[item] & 0xffffu);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            if (MB > 1 && m >= blocks_of(rows)) break;
+            const int r = 4 * m + l4;
+            if (r >= rows) break;
+            const float w = t.weight[first + r];
+            float *to = sums + (t.row[first + r] & 0xffu) * kFewCols;
 #pragma unroll
-            for (int i = 0; i < (TWO ? 1 : 2); ++i) {
-                const int r = TWO ? 4 * m + l4 : 8 * m + 2 * l4 + i;
-                if (r >= rows) continue;
-                const float w = t.weight[first + r];
-                float *to = sums + (t.row[first + r] & 0xffu) * kFewCols;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float(&a)[4] = acc[j][m];
-                    float2 *v = reinterpret_cast<float2 *>(to + column(j));
-                    float2 old = *v;
-                    old.x = fmaf(w, TWO ? both(a[0], a[1]) : a[i], old.x);
-                    old.y = fmaf(w, TWO ? both(a[2], a[3]) : a[2 + i], old.y);
-                    *v = old;
-                }
+            for (int j = 0; j < 4; ++j) {
+                const float(&a)[4] = acc[j][m];
+                float2 *v = reinterpret_cast<float2 *>(to + column(j));
+                float2 old = *v;
+                old.x = fmaf(w, both(a[0], a[1]), old.x);
+                old.y = fmaf(w, both(a[2], a[3]), old.y);
+                *v = old;
             }
         }
     }
@@ -1045,16 +1041,25 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_blocks<MB>()) few_kernel(c
         k.walk(ring, lo, static_cast<int64_t>(mine) * (hi - lo), [&](int unit, const float(&acc)[4][MB][4]) {
             const int item = unit / p.columns, rows = k.rows_of(item);
             const int64_t n0 = static_cast<int64_t>(unit % p.columns) * (p.wide * kFewCols);
+            // 8 rows at a time: of a block of the products, or of two where a row is two of theirs.
 #pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                if (MB > 1 && 8 * m >= rows) break;
+            for (int m0 = 0; m0 < MB; m0 += K::PARTS) {
+                const int r0 = 8 / K::PARTS * m0;
+                if (MB > K::PARTS && r0 >= rows) break;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int m = m0; m < m0 + K::PARTS && m < MB; ++m)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float2 *>(own + (2 * k.l4 + i) * kFewCols + k.column(j)) =
-                            make_float2(acc[j][m][i], acc[j][m][2 + i]);
-                join(item, n0, 8 * m, min(rows - 8 * m, 8), 8 * (m + 1) < rows || unit + clusters < units);
+                    for (int j = 0; j < 4; ++j) {
+                        const float(&a)[4] = acc[j][m];
+                        if constexpr (UP) {
+                            *reinterpret_cast<float2 *>(own + 2 * k.l4 * kFewCols + k.column(j)) = make_float2(a[0], a[2]);
+                            *reinterpret_cast<float2 *>(own + (2 * k.l4 + 1) * kFewCols + k.column(j)) = make_float2(a[1], a[3]);
+                        } else {
+                            *reinterpret_cast<float2 *>(own + (4 * (m - m0) + k.l4) * kFewCols + k.column(j)) =
+                                make_float2(k.both(a[0], a[1]), k.both(a[2], a[3]));
+                        }
+                    }
+                join(item, n0, r0, min(rows - r0, 8), r0 + 8 < rows || unit + clusters < units);
             }
         });
     }
@@ -1137,13 +1142,11 @@ cudaError_t launch_few_mode(const FewLaunch &l, const FewParams &p, cudaStream_t
     // Hidden rows are always aligned: with weights in 4 bits nothing else can be off.
     constexpr bool any = ANY && !FOUR;
     if constexpr (MB < 4)
-        if (l.mode == kFewTwo) return launch_few_kernel<BF16, FOUR, any, MB, kFewTwo>(l, p, s);
-    if constexpr (MB == 2)
-        if (l.mode == kFewFlat) return launch_few_kernel<BF16, FOUR, any, 2, kFewFlat>(l, p, s);
-    if constexpr (MB == 1)
+        if (l.mode == kFewFlat) return launch_few_kernel<BF16, FOUR, any, MB, kFewFlat>(l, p, s);
+    if constexpr (MB == 1 || (FOUR && MB == 4))
         return cudaErrorInvalidConfiguration;
     else
-        return launch_few_kernel<BF16, FOUR, any, MB, kFewParts>(l, p, s);
+        return l.mode == kFewParts ? launch_few_kernel<BF16, FOUR, any, MB, kFewParts>(l, p, s) : cudaErrorInvalidConfiguration;
 }
 
 template <bool BF16, bool FOUR>

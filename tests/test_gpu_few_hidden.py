@@ -51,3 +51,19 @@ def test_small_hidden_values(type_, four, t, small):
     error, once = error_and_rounding(type_, four, t, 3, 6, 520, 264, small, "small")
     # (besides: fp32 sums and the activation, some 2^-20 of the values, next to 2^-9 or 2^-12)
     assert error <= 1.05 * once
+
+
+@pytest.mark.parametrize("t, k, e", [(9, 3, 6), (12, 2, 3), (13, 3, 6), (16, 8, 24), (17, 2, 3), (40, 2, 8), (64, 8, 24),
+                                     (64, 4, 4)])
+@pytest.mark.parametrize("four", [0, 32, 128])
+@pytest.mark.parametrize("type_", TYPES)
+def test_many_tokens(type_, four, t, k, e):
+    """More than 8 tokens, few and many rows of an expert: the same as for one."""
+    error, once = error_and_rounding(type_, four, t, k, e, 520, 264, 4, "many")
+    assert error <= 1.05 * once
+
+
+@pytest.mark.parametrize("t", [11, 50])
+def test_many_tokens_off_boundaries(t):
+    error, once = error_and_rounding("f16", 0, t, 4, 12, 411, 101, 4, "odd")
+    assert error <= 1.05 * once
