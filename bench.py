@@ -255,7 +255,26 @@ def time_steps(call, steps: int, flush=None, stream=None) -> list[float]:
     return [a.elapsed_time(b) for a, b in evs]
 
 
-def measure_gemm(wl, steps: int, warmup: int, dev, flush, peaks, peak_src):
+AUTOMATIC = (-1, 0, 0, -1, -1)  # gemmpipe_set_plan_override's arguments: nothing overridden
+
+
+def rank_override(world: int, cta_pair: int, force: tuple = AUTOMATIC) -> tuple:
+    """Plan override for a workload planned with `cta_pair` on `world` ranks.
+
+    Quads (2) share A by TMA multicast loads, which are for runs on one GPU
+    alone: several ranks take CTA pairs instead."""
+    return (*force[:3], 1, force[4]) if world > 1 and cta_pair == 2 else force
+
+
+def parse_force(text: str, world: int) -> tuple:
+    force = tuple(int(x) for x in text.split(","))
+    force += AUTOMATIC[len(force):]
+    if world > 1 and force[3] == 2:
+        raise ValueError("--force: quads (cta_pair 2) are for runs on one GPU")
+    return force
+
+
+def measure_gemm(wl, steps: int, warmup: int, dev, flush, peaks, peak_src, world: int = 1, force: tuple = AUTOMATIC):
     """Device-resident timing of one workload (name, dtype, M, N, K, A, B)."""
     import torch
 
@@ -264,6 +283,10 @@ def measure_gemm(wl, steps: int, warmup: int, dev, flush, peaks, peak_src):
     Ad = torch.from_numpy(A).to(dev)
     Bd = torch.from_numpy(B).to(dev)
     C = torch.empty((M, N), dtype=torch.int32 if dtype == "s8" else torch.float32, device=dev)
+    gemmpipe.gemmpipe_set_plan_override(*force)
+    override = rank_override(world, gemmpipe.gemmpipe_plan(0 if dtype == "s8" else 1, M, N, K, Ad, Bd, C)["cta_pair"],
+                             force)
+    gemmpipe.gemmpipe_set_plan_override(*override)  # (of this workload, in measure_e2e too)
     stream = torch.cuda.current_stream(dev)
     fn = gemmpipe.gemm_s8s8s32 if dtype == "s8" else gemmpipe.gemm_f16f32
     call = lambda: fn(M, N, K, Ad, Bd, C, stream)
@@ -315,7 +338,7 @@ def measure_gemm(wl, steps: int, warmup: int, dev, flush, peaks, peak_src):
         "ops_per_s": flops / ms / 1e9, "bytes_per_s": alg_bytes / ms / 1e6, "kernel_ms": kernel_ms,
         "aux_ms": aux_ms / max(1, aux_n) if aux_n else 0.0, "launches": launches, "flops": flops,
         "alg_bytes": alg_bytes, "roofline": roof, "plan": plan, "l2": "flushed" if needs_flush else "inputs > L2",
-        "window": (t0, t1), "A": A, "B": B, "C": C,
+        "window": (t0, t1), "A": A, "B": B, "C": C, "override": override,
     }
 
 
@@ -330,6 +353,7 @@ def measure_e2e(res: dict, steps: int, dev) -> dict:
 
     from software_pipelined_loop_gb300 import gemmpipe
     A, B, M, N, K = res["A"], res["B"], res["M"], res["N"], res["K"]
+    gemmpipe.gemmpipe_set_plan_override(*res["override"])
     Ah = torch.from_numpy(A).pin_memory()
     Bh = torch.from_numpy(B).pin_memory()
     out_dtype = torch.int32 if res["dtype"] == "s8" else torch.float32
@@ -529,7 +553,8 @@ def run_gpu(args) -> int:
         if dist:
             dist.barrier()
         torch.cuda.synchronize()
-        head = measure_gemm(workload(HEADLINE), args.steps, args.warmup, dev, flush, peaks, peak_src)
+        force = parse_force(args.force, world) if args.force else AUTOMATIC
+        head = measure_gemm(workload(HEADLINE), args.steps, args.warmup, dev, flush, peaks, peak_src, world, force)
         torch.cuda.synchronize()
         if dist:
             dist.barrier()
@@ -541,7 +566,7 @@ def run_gpu(args) -> int:
             # Small cases first, the metric's FP16 4096^3 and skinny last.
             for wl in (workload(0), workload(1), workload(4), workload(3), fp16_4096()):
                 secondary.append(measure_gemm(wl, max(10, args.steps // 4), args.warmup, dev, flush, peaks,
-                                              peak_src))
+                                              peak_src, world, force))
         e2e = measure_e2e(head, max(5, args.steps // 4), dev)
         copy_ref = measure_copy_ref(dev, peaks)
         context = None
@@ -764,10 +789,14 @@ def main() -> int:
         if dt not in ("s8", "f16"):
             ap.error("--shape dtype must be s8 or f16")
         SHAPE = (dt, int(M), int(N), int(K))
+    world = int(os.environ.get("WORLD_SIZE", "1"))
     if args.force:
-        from software_pipelined_loop_gb300 import build, gemmpipe
-        build.build()
-        gemmpipe.gemmpipe_set_plan_override(*[int(x) for x in args.force.split(",")])
+        try:
+            parse_force(args.force, world)
+        except ValueError as error:
+            ap.error(str(error))
+    if args.ablation and world > 1:
+        ap.error("--ablation is for one GPU (it times quads, among others)")
     if args.impl == "reference":
         return run_reference(args)
     if args.ablation:
