@@ -61,7 +61,9 @@
  * gemmpipe_get_device_status().  No C++ exception crosses this interface.
  * Calls may come from several host threads, on one stream too: the library's
  * own state is guarded by a mutex, and a call that uses a workspace of the
- * stream enqueues all of its kernels before another one may take it.
+ * stream enqueues all of its kernels before another one may take it.  (A
+ * stream is told by its handle: cudaStreamPerThread, one handle for a stream
+ * of each thread, is for calls of one thread at a time.)
  *
  * Error behaviour common to the GEMM entry points:
  *   - M, N or K negative, any of them above 2^31 - 1, a matrix of 2^56
@@ -438,7 +440,10 @@ GEMMPIPE_API gemmpipe_status_t gemm_grouped_dw8(int type, int64_t R, int64_t N, 
  *   S: ceil(K / group) x N4 scales of the 16-bit type, on an 8-byte boundary;
  *      group is 32, 64 or 128.
  * Element (k, n) is (q - 8) * S[k / group][n].  Values past K or N are not
- * used, whatever they are.
+ * used, whatever they are.  The products x * (q - 8) of a group, or of half or a
+ * quarter of it, may be summed before they are scaled: values of X past 2^117
+ * (bf16) may make that sum infinite, and an infinite scale makes infinity or NaN
+ * of it as a whole.
  */
 #define GEMMPIPE_FEW_ROWS 64
 

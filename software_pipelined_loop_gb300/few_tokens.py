@@ -7,7 +7,10 @@ the whole expert layer for a few tokens with weights in 16 or in 4 bits.
 
 For generating token by token: at most 64 rows or tokens a call, no gradients
 (expert_layer has them): asking for them, in forward mode too, is an error.  Everything is computed in the CUDA library; torch
-supplies memory.  A matrix for many rows is brought back with unpack4.
+supplies memory.  A matrix for many rows is brought back with unpack4.  Graphs
+recorded on one stream (torch records all of a process on the same one unless it
+is given another) share the library's workspace of that stream where expert_step
+uses it: they must not run at the same time.
 
     m = pack4(w1)                  # once, when the weights are loaded
     y = expert_step(x, ids, weights, m, pack4(w2))
