@@ -186,10 +186,11 @@ bool encode_words(CUtensorMap *m, const uint32_t *Q, int64_t rows, int64_t n4, i
 }
 
 // Some aligned rows times 4 bits: tiles of 128 columns on tcgen05.  16 rows in
-// groups of 128 (64, 32): 4096 x 16384 13.8 (15.8, 19.6) us there and 16.6 (16.6,
-// 17.2) as few rows, 16384 x 4096 15.4 (17.3, 20.7) and 18.1 (18.1, 18.9), 2048 x
-// 2048 6.3 (6.7, 6.5) and 7.2 (7.2, 7.4); 8 rows x 4096 x 16384 in groups of 128
-// 13.5 and 12.6; 32 rows in groups of 32 22 and 31.
+// groups of 128 (64): 4096 x 16384 13.8 (15.8) us there and 16.6 (16.6) as few
+// rows, 16384 x 4096 15.4 (17.3) and 18.1 (18.1), 2048 x 2048 6.3 (6.7) and 7.2
+// (7.2); 8 rows x 4096 x 16384 in groups of 128 13.5 and 12.6.  In groups of 32, 17
+// rows there and 16 as few rows: 19.3 and 17.5, 21.1 and 18.9, 6.8 and 7.0; 32 rows
+// x 4096 x 16384 19.5 and 31.
 bool wide_rows4(int64_t M, int64_t N, int64_t K, int64_t group, const void *X, int64_t ldx)
 {
     return M > (group == 32 ? 16 : 8) && N <= (int64_t(1) << 29) && K <= (int64_t(1) << 30) && !misaligned(X, 16) &&

@@ -31,10 +31,11 @@
 //     their sums meet in shared memory, in a fixed order.
 //
 // Measured (GB300, back to back, SM clock about 1.95 GHz): weights in 16 bits
-// 6.0 to 6.6 TB/s where there are some 0.3 ms of them or more, in 4 bits 4.9
-// (bf16) and 5.3 (fp16) TB/s: 165 and 150 instructions of a warp for 32 x 64
-// weights, of which the logic operations that take words apart (7 or 5 for 8
-// weights, at half rate) keep their pipe 62% busy.
+// 6.0 to 6.6 TB/s where there are some 0.3 ms of them or more.  In 4 bits, one row
+// x 16384 x 19456, whose 304 units fill all places, 4.8 (bf16) and 5.3 (fp16) TB/s;
+// x 16384 x 16384, 256 units, 4.1 in the same time: 165 and 150 instructions of a
+// warp for 32 x 64 weights, of which the logic operations that take words apart (7
+// or 5 for 8 weights, at half rate) keep their pipe 62% busy.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -23,7 +23,7 @@
 //     more than the type holds: it is split into its rounding and the rest,
 //     exactly, and both are multiplied, into one accumulator for all groups.
 //     Infinities, and scales so large that w is past the type's largest value,
-//     do not survive that: a sum that is not finite is made again plainly.
+//     do not survive that: sums that are not finite are made again (wide_again).
 // fp32 throughout, one rounding at the end.  The CTAs of a cluster share a
 // tile's k; their sums meet in shared memory, in a fixed order.  Every wait is
 // bounded (Waiter).
@@ -32,7 +32,7 @@
 // cycles and the MMAs' reading them 128, and a stage passes through four or five
 // kinds of warps in 450 cycles at least, whatever its size.  Split values are
 // twice the bytes: 64 rows x 4096 x 16384 take 17 us in groups of 128, 19 of 64,
-// 22 of 32 (as the others do: 30; the others as this one does: 22).
+// 21 of 32 (as the others do: 30; the others as this one does: 22).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -329,10 +329,10 @@ __device__ bool wide_unpack(const WideParams &p, uint32_t sbase, uint32_t tmem, 
     return true;
 }
 
-// Issuing a stage's MMAs and finding
-// the next barriers ready takes a warp longer than anything else takes (8 MMAs
-// 500 to 600 cycles, the rest as much again), so two warps take stages in turn,
-// and the next barriers are looked at while the MMAs go out.
+// Issuing a stage's MMAs and finding the next barriers ready takes a warp longer
+// than anything else takes (8 MMAs 500 to 600 cycles, the rest as much again), so
+// two warps take stages in turn, and the next barriers are looked at while the
+// MMAs go out.
 template <class Cfg, bool BF16>
 __device__ void wide_mma(const WideParams &p, uint32_t sbase, uint32_t tmem, WideCtl<Cfg> *ctl, const Waiter &w,
                          const WideRange &r, int mine)
