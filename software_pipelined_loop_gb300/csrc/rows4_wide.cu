@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
     __syncwarp();
     if constexpr (Cfg::SPLIT) {
-        if (__syncthreads_or(bad) && ctl->abort == 0) wide_again<Cfg, BF16>(p, r, n, warp, sums);  // (a wait that ran out leaves anything)
+        // (a wait that ran out leaves anything)
+        if (__syncthreads_or(bad) && ctl->abort == 0) wide_again<Cfg, BF16>(p, r, n, warp, sums);
         if (p.split == 1 && ends && n < p.N)
             for (int m = row0; m < row0 + Cfg::SUMS && m < p.M; ++m) store(m, sums[m * kWideCols + column]);
     }
